@@ -34,6 +34,9 @@ NOALLOC_SCRATCH_BYTES = 64 << 20   # GDN_NOALLOC_SCRATCH_BYTES
 EXPORTS = ("gdn_chunk_fwd", "gdn_chunk_fwd_noalloc", "gdn_chunk_fwd_workspace_bytes", "gdn_workspace_status",
            "gdn_state_qdq",
            "gdn_state_qdq_int8", "gdn_decode_step", "gdn_chunk_bwd_dh", "gdn_chunk_bwd_workspace_bytes",
+           "gdn_lin_attn_fwd", "gdn_lin_attn_fwd_workspace_bytes", "gdn_lin_attn_bwd",
+           "gdn_lin_attn_bwd_workspace_bytes", "gdn_lin_attn_step", "gdn_block_norm_fwd", "gdn_block_norm_bwd",
+           "gdn_block_norm_bwd_workspace_bytes", "gdn_act_pack", "gdn_act_unpack",
            "gdn_status_string", "gdn_last_error")
 
 
@@ -67,6 +70,35 @@ class GdnDebug(ctypes.Structure):
         ("suffix_pre", ctypes.c_void_p),
         ("suffix_post", ctypes.c_void_p),
         ("status", ctypes.c_void_p),
+    ]
+
+
+GDN_ACT_SILU = 0
+GDN_ACT_SIGMOID = 1
+
+
+class GdnLin(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32),
+        ("n_heads", ctypes.c_int32),
+        ("qk_heads", ctypes.c_int32),
+        ("dk", ctypes.c_int32),
+        ("dv", ctypes.c_int32),
+        ("io_dtype", ctypes.c_int32),
+        ("gate_per_token", ctypes.c_int32),
+        ("total_tokens", ctypes.c_int64),
+    ]
+
+
+class GdnNorm(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int32),
+        ("io_dtype", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("act", ctypes.c_int32),
+        ("res_scale", ctypes.c_float),
+        ("eps", ctypes.c_float),
     ]
 
 
@@ -111,6 +143,20 @@ def lib():
     L.gdn_workspace_status.argtypes = [_vp, _vp]
     L.gdn_workspace_status.restype = ctypes.c_int
     L.gdn_decode_step.restype = ctypes.c_int
+    lin, norm, size, i32 = ctypes.POINTER(GdnLin), ctypes.POINTER(GdnNorm), ctypes.c_size_t, ctypes.c_int32
+    L.gdn_lin_attn_fwd.argtypes = [lin] + [_vp] * 9 + [size, _vp]
+    L.gdn_lin_attn_bwd.argtypes = [lin] + [_vp] * 14 + [size, _vp]
+    L.gdn_lin_attn_step.argtypes = [lin] + [_vp] * 7
+    L.gdn_block_norm_fwd.argtypes = [norm] + [_vp] * 12
+    L.gdn_block_norm_bwd.argtypes = [norm] + [_vp] * 15 + [size, _vp]
+    L.gdn_act_pack.argtypes = [_vp, i32, _vp, _vp, ctypes.c_int64, i32, _vp]
+    L.gdn_act_unpack.argtypes = [_vp, _vp, _vp, i32, ctypes.c_int64, i32, _vp]
+    for name in ("lin_attn_fwd", "lin_attn_bwd", "lin_attn_step", "block_norm_fwd", "block_norm_bwd", "act_pack",
+                 "act_unpack"):
+        getattr(L, "gdn_" + name).restype = ctypes.c_int
+    for name, p in (("lin_attn_fwd", lin), ("lin_attn_bwd", lin), ("block_norm_bwd", norm)):
+        f = getattr(L, f"gdn_{name}_workspace_bytes")
+        f.argtypes, f.restype = [p], size
     L.gdn_status_string.argtypes = [ctypes.c_int]
     L.gdn_status_string.restype = ctypes.c_char_p
     L.gdn_last_error.argtypes = []

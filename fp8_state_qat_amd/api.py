@@ -14,7 +14,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import GDN_BF16, GDN_F32, GDN_QDQ_CHUNK, GDN_QDQ_WRITE, GdnDebug, GdnShape
+from ._lib import GDN_BF16, GDN_F32, GDN_QDQ_CHUNK, GDN_QDQ_WRITE, GdnDebug, GdnLin, GdnNorm, GdnShape
 
 _DT = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
 
@@ -368,3 +368,292 @@ def decode_step(q, k, v, beta, g, state, *, qdq=True, o=None, o_dtype=None, stat
                                     _ptr(scales), _stream())
     _lib.check(st)
     return o
+
+
+# ---------------------------------------------------------------------------
+# Linear attention with a decay for each head, block norms, 8-bit activations
+# ---------------------------------------------------------------------------
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _scratch(workspace, need, like):
+    """The caller's workspace (checked by the library for its size), or one of `need` bytes."""
+    if need == 0:
+        _lib.check(_lib.GDN_ERR_INVALID_ARG)
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+    _dev(workspace, "workspace", torch.uint8)
+    _on_device(k=like, workspace=workspace)
+    if workspace.dim() != 1:
+        raise ValueError("workspace must be a 1-D uint8 tensor")
+    return workspace
+
+
+def _lin_inputs(q, k, v, g):
+    """Checks of q, k, v, g; (T, H, Hk, dk, dv)."""
+    _dev(k, "k")
+    if k.dim() != 3:
+        raise ValueError(f"k must be [T, Hk, dk], got shape {tuple(k.shape)}")
+    T, Hk, dk = k.shape
+    if k.dtype not in _DT:
+        raise ValueError("q, k, v must share one dtype: float32 or bfloat16")
+    _dev(q, "q", k.dtype, (T, Hk, dk))
+    _dev(v, "v", k.dtype)
+    if v.dim() != 3 or v.shape[0] != T:
+        raise ValueError(f"v must be [{T}, H, dv], got shape {tuple(v.shape)}")
+    H, dv = v.shape[1], v.shape[2]
+    _dev(g, "g", torch.float32, (H,) if isinstance(g, torch.Tensor) and g.dim() == 1 else (T, H))
+    return T, H, Hk, dk, dv
+
+
+def _lin_seqs(cu_seqlens):
+    _dev(cu_seqlens, "cu_seqlens", torch.int32)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be [N + 1] with N >= 1")
+    return cu_seqlens.numel() - 1
+
+
+def lin_attn_workspace_bytes(N, H, Hk, dk, dv, T, io_dtype=torch.bfloat16, gate_per_token=True, backward=False):
+    """Device workspace lin_attn_fwd (or lin_attn_bwd) needs for this shape (bytes)."""
+    shape = GdnLin(N, H, Hk, dk, dv, _DT[io_dtype], 1 if gate_per_token else 0, T)
+    L = _lib.lib()
+    n = (L.gdn_lin_attn_bwd_workspace_bytes if backward else L.gdn_lin_attn_fwd_workspace_bytes)(ctypes.byref(shape))
+    if n == 0:
+        _lib.check(_lib.GDN_ERR_INVALID_ARG)
+    return n
+
+
+def lin_attn_fwd(q, k, v, g, cu_seqlens, *, initial_state=None, out=None, final_state=None, workspace=None,
+                 check_status=False):
+    """gdn_lin_attn_fwd: S_t = e^{g_t} S_{t-1} + v_t k_t^T, o_t = S_t q_t over
+    packed sequences.  q, k: [T, Hk, dk]; v: [T, H, dv] (fp32 or bf16; value
+    head h uses query/key head h // (H / Hk)); g: [T, H], or [H] for one decay
+    a head, fp32 natural log; cu_seqlens: [N + 1] int32; initial_state:
+    [N, H, dv, dk] fp32 or None.  Rows outside every sequence are not written.
+    check_status: read the workspace's status word after the call
+    (synchronizes; raises GdnError when cu_seqlens is out of contract).
+    Returns (o, final_state)."""
+    T, H, Hk, dk, dv = _lin_inputs(q, k, v, g)
+    N = _lin_seqs(cu_seqlens)
+    _dev(initial_state, "initial_state", torch.float32, (N, H, dv, dk))
+    _dev(out, "out", k.dtype, (T, H, dv))
+    _dev(final_state, "final_state", torch.float32, (N, H, dv, dk))
+    _on_device(q=q, k=k, v=v, g=g, cu_seqlens=cu_seqlens, initial_state=initial_state, out=out,
+               final_state=final_state)
+    if out is None:
+        out = torch.empty_like(v)
+    if final_state is None:
+        final_state = torch.empty((N, H, dv, dk), dtype=torch.float32, device=k.device)
+    shape = ctypes.byref(GdnLin(N, H, Hk, dk, dv, _DT[k.dtype], 1 if g.dim() == 2 else 0, T))
+    L = _lib.lib()
+    workspace = _scratch(workspace, L.gdn_lin_attn_fwd_workspace_bytes(shape), k)
+    _lib.check(L.gdn_lin_attn_fwd(shape, _addr(q), _addr(k), _addr(v), _addr(g), _addr(cu_seqlens),
+                                  _addr(initial_state), _addr(out), _addr(final_state), _addr(workspace),
+                                  workspace.numel(), _stream()))
+    if check_status:
+        workspace_status(workspace)
+    return out, final_state
+
+
+def lin_attn_bwd(q, k, v, g, cu_seqlens, d_o, *, initial_state=None, d_final_state=None, dq=None, dk=None, d_v=None,
+                 dg=None, d_initial_state=None, workspace=None, check_status=False):
+    """gdn_lin_attn_bwd: gradients of L = sum o . d_o + <S_final, d_final_state>
+    for lin_attn_fwd's inputs.  d_o: as v; d_final_state: [N, H, dv, dk] fp32
+    or None (zero).  Returns (dq, dk, dv, dg, d_initial_state): dq, dk, dv in
+    the inputs' dtype (dq and dk summed over the heads that share them), dg
+    fp32 of g's shape, d_initial_state [N, H, dv, dk] fp32."""
+    T, H, Hk, dk_, dv_ = _lin_inputs(q, k, v, g)
+    N = _lin_seqs(cu_seqlens)
+    st = (N, H, dv_, dk_)
+    for name, t, dt, shp in (("d_o", d_o, k.dtype, v.shape), ("initial_state", initial_state, torch.float32, st),
+                             ("d_final_state", d_final_state, torch.float32, st), ("dq", dq, k.dtype, k.shape),
+                             ("dk", dk, k.dtype, k.shape), ("d_v", d_v, k.dtype, v.shape),
+                             ("dg", dg, torch.float32, g.shape),
+                             ("d_initial_state", d_initial_state, torch.float32, st)):
+        _dev(t, name, dt, shp)
+    if d_o is None:
+        raise ValueError("d_o is required")
+    _on_device(q=q, k=k, v=v, g=g, cu_seqlens=cu_seqlens, d_o=d_o, initial_state=initial_state,
+               d_final_state=d_final_state, dq=dq, dk=dk, d_v=d_v, dg=dg, d_initial_state=d_initial_state)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    d_v = torch.empty_like(v) if d_v is None else d_v
+    dg = torch.empty_like(g) if dg is None else dg
+    if d_initial_state is None:
+        d_initial_state = torch.empty(st, dtype=torch.float32, device=k.device)
+    shape = ctypes.byref(GdnLin(N, H, Hk, dk_, dv_, _DT[k.dtype], 1 if g.dim() == 2 else 0, T))
+    L = _lib.lib()
+    workspace = _scratch(workspace, L.gdn_lin_attn_bwd_workspace_bytes(shape), k)
+    _lib.check(L.gdn_lin_attn_bwd(shape, _addr(q), _addr(k), _addr(v), _addr(g), _addr(cu_seqlens), _addr(d_o),
+                                  _addr(initial_state), _addr(d_final_state), _addr(dq), _addr(dk), _addr(d_v),
+                                  _addr(dg), _addr(d_initial_state), _addr(workspace), workspace.numel(),
+                                  _stream()))
+    if check_status:
+        workspace_status(workspace)
+    return dq, dk, d_v, dg, d_initial_state
+
+
+def lin_attn_step(q, k, v, g, state, *, o=None):
+    """gdn_lin_attn_step: one token for each sequence.  q, k: [N, Hk, dk]; v:
+    [N, H, dv]; g: [N, H] or [H]; state [N, H, dv, dk] fp32 updated in place.
+    Returns o [N, H, dv]."""
+    N, H, Hk, dk, dv = _lin_inputs(q, k, v, g)
+    if state is None:
+        raise ValueError("state is required")
+    _dev(state, "state", torch.float32, (N, H, dv, dk))
+    _dev(o, "o", k.dtype, (N, H, dv))
+    _on_device(q=q, k=k, v=v, g=g, state=state, o=o)
+    if o is None:
+        o = torch.empty_like(v)
+    shape = GdnLin(N, H, Hk, dk, dv, _DT[k.dtype], 1 if g.dim() == 2 else 0, N)
+    _lib.check(_lib.lib().gdn_lin_attn_step(ctypes.byref(shape), _addr(q), _addr(k), _addr(v), _addr(g),
+                                            _addr(state), _addr(o), _stream()))
+    return o
+
+
+_ACT = {"silu": _lib.GDN_ACT_SILU, "sigmoid": _lib.GDN_ACT_SIGMOID}
+
+
+def _rows(t, name):
+    _dev(t, name)
+    if t is None or t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name} must be [..., cols] with cols >= 1")
+    return t.shape[-1], t.numel() // t.shape[-1]
+
+
+def _norm_shape(rows, cols, io_dtype, x_dtype, act, res_scale, eps):
+    if io_dtype not in _DT or x_dtype not in _DT:
+        raise ValueError("dtypes must be float32 or bfloat16")
+    if act not in _ACT:
+        raise ValueError(f"act must be one of {sorted(_ACT)}, got {act!r}")
+    return GdnNorm(rows, cols, _DT[io_dtype], _DT[x_dtype], _ACT[act], float(res_scale), float(eps))
+
+
+def block_norm_fwd(f, w_post, *, gate=None, act="silu", residual=None, res_scale=1.0, w_pre=None, eps=1e-6,
+                   x_dtype=None, checkpoint=False):
+    """gdn_block_norm_fwd: the norm after a block, its gate, the scaled residual
+    and the norm before the next block:
+        x = res_scale * (f / rms(f) * w_post * a(gate)) + residual
+        h = x / rms(x) * w_pre
+    f, gate: [..., cols] fp32 or bf16; act: "silu" or "sigmoid"; residual: as f
+    in x_dtype (default: the residual's dtype, else f's); w_post, w_pre: [cols]
+    fp32.  Without w_pre h is None.  Returns (x, h); with checkpoint also f and
+    the gate as (codes, scales) of act_pack (None without a gate)."""
+    cols, rows = _rows(f, "f")
+    if x_dtype is None:
+        x_dtype = residual.dtype if isinstance(residual, torch.Tensor) else f.dtype
+    shape = _norm_shape(rows, cols, f.dtype, x_dtype, act, res_scale, eps)
+    for name, t, dt, shp in (("gate", gate, f.dtype, f.shape), ("residual", residual, x_dtype, f.shape),
+                             ("w_post", w_post, torch.float32, (cols,)), ("w_pre", w_pre, torch.float32, (cols,))):
+        _dev(t, name, dt, shp)
+    if w_post is None:
+        raise ValueError("w_post is required")
+    _on_device(f=f, gate=gate, residual=residual, w_post=w_post, w_pre=w_pre)
+    x = torch.empty_like(f, dtype=x_dtype)
+    h = torch.empty_like(f) if w_pre is not None else None
+    fc = zc = (None, None)
+    if checkpoint:
+        fc = _code_buffers(f)
+        zc = _code_buffers(f) if gate is not None else zc
+    _lib.check(_lib.lib().gdn_block_norm_fwd(ctypes.byref(shape), _addr(f), _addr(gate), _addr(residual),
+                                             _addr(w_post), _addr(w_pre), _addr(x), _addr(h), _addr(fc[0]),
+                                             _addr(fc[1]), _addr(zc[0]), _addr(zc[1]), _stream()))
+    if checkpoint:
+        return x, h, fc, (zc if gate is not None else None)
+    return x, h
+
+
+def _values_or_codes(t, name, dtype):
+    """(values or codes, scales or None) of an argument that may be act_pack's pair."""
+    if not isinstance(t, tuple):
+        _dev(t, name, dtype)
+        return t, None
+    if len(t) != 2:
+        raise ValueError(f"{name} must be a tensor or (codes, scales)")
+    codes, scales = t
+    _dev(codes, f"{name} codes", torch.float8_e4m3fn)
+    cols, _ = _rows(codes, f"{name} codes")
+    if scales is None:
+        raise ValueError(f"{name} scales are required")
+    _dev(scales, f"{name} scales", torch.float32, codes.shape[:-1] + (-(-cols // 64),))
+    return codes, scales
+
+
+def block_norm_bwd(f, w_post, d_x, *, d_h=None, x=None, w_pre=None, gate=None, act="silu", res_scale=1.0, eps=1e-6,
+                   want_residual=True, io_dtype=None, workspace=None):
+    """gdn_block_norm_bwd: gradients of block_norm_fwd's inputs from d_x and,
+    with w_pre, d_h (x is the forward's x).  f and gate are the forward's
+    tensors or both its (codes, scales) checkpoints; io_dtype: the dtype of f
+    (needed with checkpoints and no d_h).
+    Returns (d_f, d_gate, d_residual, d_w_post, d_w_pre), None where the
+    forward had no such input (d_residual also without want_residual)."""
+    if io_dtype is None:
+        io_dtype = d_h.dtype if isinstance(d_h, torch.Tensor) else None if isinstance(f, tuple) else f.dtype
+        if io_dtype is None:
+            raise ValueError("io_dtype is needed with checkpoints and no d_h")
+    f, f_scales = _values_or_codes(f, "f", io_dtype)
+    cols, rows = _rows(f, "f")
+    z_scales = None
+    if gate is not None:
+        gate, z_scales = _values_or_codes(gate, "gate", io_dtype)
+        if (z_scales is None) != (f_scales is None):
+            raise ValueError("f and gate must both be tensors or both checkpoints")
+    _dev(d_x, "d_x")
+    if d_x is None:
+        raise ValueError("d_x is required")
+    shape = _norm_shape(rows, cols, io_dtype, d_x.dtype, act, res_scale, eps)
+    for name, t, dt, shp in (("gate", gate, f.dtype, f.shape), ("d_x", d_x, None, f.shape),
+                             ("d_h", d_h, io_dtype, f.shape), ("x", x, d_x.dtype, f.shape),
+                             ("w_post", w_post, torch.float32, (cols,)), ("w_pre", w_pre, torch.float32, (cols,))):
+        _dev(t, name, dt, shp)
+    if w_post is None:
+        raise ValueError("w_post is required")
+    if w_pre is not None and (x is None or d_h is None):
+        raise ValueError("w_pre needs x and d_h")
+    if w_pre is None:
+        x = d_h = None
+    _on_device(f=f, gate=gate, f_scales=f_scales, gate_scales=z_scales, d_x=d_x, d_h=d_h, x=x, w_post=w_post,
+               w_pre=w_pre)
+    d_f = torch.empty_like(f, dtype=io_dtype)
+    d_z = torch.empty_like(d_f) if gate is not None else None
+    d_res = torch.empty_like(d_x) if want_residual else None
+    dw_post = torch.empty_like(w_post)
+    dw_pre = torch.empty_like(w_pre) if w_pre is not None else None
+    L = _lib.lib()
+    workspace = _scratch(workspace, L.gdn_block_norm_bwd_workspace_bytes(ctypes.byref(shape)), f)
+    _lib.check(L.gdn_block_norm_bwd(ctypes.byref(shape), _addr(f), _addr(f_scales), _addr(gate), _addr(z_scales),
+                                    _addr(w_post), _addr(w_pre), _addr(x), _addr(d_x), _addr(d_h), _addr(d_f),
+                                    _addr(d_z), _addr(d_res), _addr(dw_post), _addr(dw_pre), _addr(workspace),
+                                    workspace.numel(), _stream()))
+    return d_f, d_z, d_res, dw_post, dw_pre
+
+
+def _code_buffers(x):
+    return (torch.empty_like(x, dtype=torch.float8_e4m3fn),
+            torch.empty(x.shape[:-1] + (-(-x.shape[-1] // 64),), dtype=torch.float32, device=x.device))
+
+
+def act_pack(x):
+    """gdn_act_pack: x [..., cols] (fp32 or bf16) as E4M3 codes with one fp32
+    scale for each 64 columns.  Returns (codes float8_e4m3fn [..., cols],
+    scales [..., ceil(cols / 64)])."""
+    cols, rows = _rows(x, "x")
+    if x.dtype not in _DT:
+        raise ValueError("x must be float32 or bfloat16")
+    _on_device(x=x)
+    codes, scales = _code_buffers(x)
+    _lib.check(_lib.lib().gdn_act_pack(_addr(x), _DT[x.dtype], _addr(codes), _addr(scales), rows, cols, _stream()))
+    return codes, scales
+
+
+def act_unpack(codes, scales, *, dtype=torch.bfloat16):
+    """gdn_act_unpack: the values code * scale of act_pack's result, in dtype."""
+    codes, scales = _values_or_codes((codes, scales), "act", None)
+    cols, rows = _rows(codes, "codes")
+    if dtype not in _DT:
+        raise ValueError("dtype must be float32 or bfloat16")
+    _on_device(codes=codes, scales=scales)
+    x = torch.empty_like(codes, dtype=dtype)
+    _lib.check(_lib.lib().gdn_act_unpack(_addr(codes), _addr(scales), _addr(x), _DT[dtype], rows, cols, _stream()))
+    return x

@@ -336,3 +336,242 @@ gdn_status_t gdn_chunk_bwd_dh(const gdn_shape_t* shape, const void* q, const voi
 }
 
 }  // extern "C"
+
+namespace {
+
+gdn_status_t check_lin(const gdn_lin_t* s, bool step) {
+  if (s == nullptr) return fail(GDN_ERR_INVALID_ARG, "shape is NULL");
+  if (s->n_seqs < 1) return fail(GDN_ERR_INVALID_ARG, "n_seqs must be >= 1 (got %d)", s->n_seqs);
+  if (s->n_heads < 1) return fail(GDN_ERR_INVALID_ARG, "n_heads must be >= 1 (got %d)", s->n_heads);
+  if (s->qk_heads < 1 || s->n_heads % s->qk_heads != 0)
+    return fail(GDN_ERR_INVALID_ARG, "qk_heads must divide n_heads (got %d, %d)", s->qk_heads, s->n_heads);
+  if (s->dv < 1 || s->dv % 64 != 0)
+    return fail(GDN_ERR_INVALID_ARG, "dv must be a positive multiple of 64 (got %d)", s->dv);
+  if (s->dk != 64 && s->dk != 128) return fail(GDN_ERR_UNSUPPORTED, "dk must be 64 or 128 (got %d)", s->dk);
+  if (s->dv > 256) return fail(GDN_ERR_UNSUPPORTED, "dv above 256 is not supported (got %d)", s->dv);
+  if (s->io_dtype != GDN_F32 && s->io_dtype != GDN_BF16)
+    return fail(GDN_ERR_INVALID_ARG, "io_dtype must be GDN_F32 or GDN_BF16");
+  if (s->gate_per_token != 0 && s->gate_per_token != 1)
+    return fail(GDN_ERR_INVALID_ARG, "gate_per_token must be 0 or 1");
+  if (s->total_tokens < 0) return fail(GDN_ERR_INVALID_ARG, "total_tokens must be >= 0");
+  if (step && s->total_tokens != s->n_seqs)
+    return fail(GDN_ERR_INVALID_ARG, "step: total_tokens must equal n_seqs");
+  // row strides and the workgroups of a launch are 32-bit, sequences a grid's second dimension
+  if (s->total_tokens >= (int64_t)1 << 31) return fail(GDN_ERR_UNSUPPORTED, "total_tokens must be below 2^31");
+  if ((int64_t)s->n_heads * s->dv >= (int64_t)1 << 28 || (int64_t)s->n_heads * s->dk >= (int64_t)1 << 28)
+    return fail(GDN_ERR_UNSUPPORTED, "n_heads too large");
+  if (!step && s->n_seqs > 65535) return fail(GDN_ERR_UNSUPPORTED, "more than 65535 sequences");
+  const int64_t units = (int64_t)s->n_heads * (s->dv / 16) *
+                        (step ? (int64_t)s->n_seqs : s->total_tokens / 64 + s->n_seqs);
+  if (units >= (int64_t)1 << 31) return fail(GDN_ERR_UNSUPPORTED, "too many (segment, head, tile) units");
+  return GDN_OK;
+}
+
+gdn_status_t check_workspace(const void* workspace, size_t bytes, size_t need, uintptr_t align) {
+  if (workspace == nullptr || bytes < need)
+    return fail(GDN_ERR_INVALID_ARG, "workspace needs %zu bytes (got %zu%s)", need, bytes, workspace ? "" : ", NULL");
+  if (!aligned(workspace, align))
+    return fail(GDN_ERR_INVALID_ARG, "workspace must be %d-byte aligned", (int)align);
+  return GDN_OK;
+}
+
+gdn_status_t check_norm(const gdn_norm_t* s) {
+  if (s == nullptr) return fail(GDN_ERR_INVALID_ARG, "shape is NULL");
+  if (s->rows < 0) return fail(GDN_ERR_INVALID_ARG, "rows must be >= 0");
+  if (s->cols < 1) return fail(GDN_ERR_INVALID_ARG, "cols must be >= 1 (got %d)", s->cols);
+  if (s->cols > 16384) return fail(GDN_ERR_UNSUPPORTED, "cols above 16384 is not supported (got %d)", s->cols);
+  if (s->rows >= (int64_t)1 << 31) return fail(GDN_ERR_UNSUPPORTED, "too many rows");
+  if ((s->io_dtype != GDN_F32 && s->io_dtype != GDN_BF16) || (s->x_dtype != GDN_F32 && s->x_dtype != GDN_BF16))
+    return fail(GDN_ERR_INVALID_ARG, "io_dtype and x_dtype must be GDN_F32 or GDN_BF16");
+  if (s->io_dtype == GDN_F32 && s->x_dtype != GDN_F32)
+    return fail(GDN_ERR_UNSUPPORTED, "io_dtype GDN_F32 takes x_dtype GDN_F32");
+  if (s->act != GDN_ACT_SILU && s->act != GDN_ACT_SIGMOID)
+    return fail(GDN_ERR_INVALID_ARG, "act must be GDN_ACT_SILU or GDN_ACT_SIGMOID");
+  if (!(s->eps > 0.0f)) return fail(GDN_ERR_INVALID_ARG, "eps must be positive");
+  return GDN_OK;
+}
+
+// Element alignment of the row-wise buffers (wider accesses are chosen by the pointers).
+uintptr_t elem(int dtype) { return dtype == GDN_BF16 ? 2 : 4; }
+
+gdn_status_t check_act(const void* x, int32_t dtype, const void* codes, const void* scales, int64_t rows,
+                       int32_t cols) {
+  if (rows < 0 || cols < 1) return fail(GDN_ERR_INVALID_ARG, "rows must be >= 0 and cols >= 1");
+  if (dtype != GDN_F32 && dtype != GDN_BF16)
+    return fail(GDN_ERR_INVALID_ARG, "dtype must be GDN_F32 or GDN_BF16");
+  const int64_t groups = ((int64_t)cols + 63) / 64;
+  if (rows >= ((int64_t)1 << 31) / groups) return fail(GDN_ERR_UNSUPPORTED, "too many (row, group) pairs");
+  if (rows > 0 && (!x || !codes || !scales))
+    return fail(GDN_ERR_INVALID_ARG, "x, codes and scales must be non-NULL");
+  if (!aligned(x, elem(dtype)) || !aligned(scales, 4)) return fail(GDN_ERR_INVALID_ARG, "misaligned buffer");
+  return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gdn_lin_attn_fwd_workspace_bytes(const gdn_lin_t* shape) {
+  g_err[0] = 0;
+  return check_lin(shape, false) == GDN_OK ? gdn::lin_fwd_workspace_bytes(*shape) : 0;
+}
+
+size_t gdn_lin_attn_bwd_workspace_bytes(const gdn_lin_t* shape) {
+  g_err[0] = 0;
+  return check_lin(shape, false) == GDN_OK ? gdn::lin_bwd_workspace_bytes(*shape) : 0;
+}
+
+gdn_status_t gdn_lin_attn_fwd(const gdn_lin_t* shape, const void* q, const void* k, const void* v, const float* g,
+                              const int32_t* cu_seqlens, const float* initial_state, void* o, float* final_state,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  g_err[0] = 0;
+  gdn_status_t st = check_lin(shape, false);
+  if (st != GDN_OK) return st;
+  if (!cu_seqlens || !final_state || !g)
+    return fail(GDN_ERR_INVALID_ARG, "cu_seqlens, g and final_state must be non-NULL");
+  if (shape->total_tokens > 0 && (!q || !k || !v || !o))
+    return fail(GDN_ERR_INVALID_ARG, "q, k, v and o must be non-NULL");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(initial_state, 16) ||
+      !aligned(final_state, 16) || !aligned(g, 4) || !aligned(cu_seqlens, 4))
+    return fail(GDN_ERR_INVALID_ARG, "misaligned buffer (q, k, v, o and states need 16 bytes)");
+  if (initial_state == final_state)
+    return fail(GDN_ERR_INVALID_ARG, "final_state may not alias initial_state");
+  st = check_workspace(workspace, workspace_bytes, gdn::lin_fwd_workspace_bytes(*shape), 256);
+  if (st == GDN_OK) st = check_device();
+  if (st != GDN_OK) return st;
+  hipError_t e = gdn::launch_lin_fwd(*shape, q, k, v, g, cu_seqlens, initial_state, o, final_state, workspace,
+                                     (hipStream_t)stream);
+  if (e != hipSuccess) return fail(GDN_ERR_DEVICE, "launch failed: %s", hipGetErrorString(e));
+  return GDN_OK;
+}
+
+gdn_status_t gdn_lin_attn_bwd(const gdn_lin_t* shape, const void* q, const void* k, const void* v, const float* g,
+                              const int32_t* cu_seqlens, const void* d_o, const float* initial_state,
+                              const float* d_final_state, void* dq, void* dk, void* d_v, float* dg,
+                              float* d_initial_state, void* workspace, size_t workspace_bytes, void* stream) {
+  g_err[0] = 0;
+  gdn_status_t st = check_lin(shape, false);
+  if (st != GDN_OK) return st;
+  if (!cu_seqlens || !g || !d_initial_state)
+    return fail(GDN_ERR_INVALID_ARG, "cu_seqlens, g and d_initial_state must be non-NULL");
+  if (shape->total_tokens > 0 && (!q || !k || !v || !d_o || !dq || !dk || !d_v))
+    return fail(GDN_ERR_INVALID_ARG, "q, k, v, d_o, dq, dk and d_v must be non-NULL");
+  if (!dg && (shape->total_tokens > 0 || !shape->gate_per_token))
+    return fail(GDN_ERR_INVALID_ARG, "dg must be non-NULL");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(d_o, 16) || !aligned(dq, 16) ||
+      !aligned(dk, 16) || !aligned(d_v, 16) || !aligned(initial_state, 16) || !aligned(d_final_state, 16) ||
+      !aligned(d_initial_state, 16) || !aligned(g, 4) || !aligned(dg, 4) || !aligned(cu_seqlens, 4))
+    return fail(GDN_ERR_INVALID_ARG, "misaligned buffer (q, k, v, their gradients and states need 16 bytes)");
+  if (d_initial_state == initial_state || d_initial_state == d_final_state)
+    return fail(GDN_ERR_INVALID_ARG, "d_initial_state may not alias initial_state or d_final_state");
+  st = check_workspace(workspace, workspace_bytes, gdn::lin_bwd_workspace_bytes(*shape), 256);
+  if (st == GDN_OK) st = check_device();
+  if (st != GDN_OK) return st;
+  hipError_t e = gdn::launch_lin_bwd(*shape, q, k, v, g, cu_seqlens, d_o, initial_state, d_final_state, dq, dk, d_v,
+                                     dg, d_initial_state, workspace, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(GDN_ERR_DEVICE, "launch failed: %s", hipGetErrorString(e));
+  return GDN_OK;
+}
+
+gdn_status_t gdn_lin_attn_step(const gdn_lin_t* shape, const void* q, const void* k, const void* v, const float* g,
+                               float* state, void* o, void* stream) {
+  g_err[0] = 0;
+  gdn_status_t st = check_lin(shape, true);
+  if (st != GDN_OK) return st;
+  if (!q || !k || !v || !g || !state || !o)
+    return fail(GDN_ERR_INVALID_ARG, "q, k, v, g, state and o must be non-NULL");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(state, 16) || !aligned(o, 16) ||
+      !aligned(g, 4))
+    return fail(GDN_ERR_INVALID_ARG, "misaligned buffer (q, k, v, o and the state need 16 bytes)");
+  st = check_device();
+  if (st != GDN_OK) return st;
+  hipError_t e = gdn::launch_lin_step(*shape, q, k, v, g, state, o, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(GDN_ERR_DEVICE, "launch failed: %s", hipGetErrorString(e));
+  return GDN_OK;
+}
+
+gdn_status_t gdn_block_norm_fwd(const gdn_norm_t* shape, const void* f, const void* gate, const void* residual,
+                                const float* w_post, const float* w_pre, void* x, void* h, uint8_t* f_codes,
+                                float* f_scales, uint8_t* gate_codes, float* gate_scales, void* stream) {
+  g_err[0] = 0;
+  gdn_status_t st = check_norm(shape);
+  if (st != GDN_OK) return st;
+  if (!w_post || (w_pre != nullptr) != (h != nullptr))
+    if (shape->rows > 0) return fail(GDN_ERR_INVALID_ARG, "w_post must be non-NULL, w_pre and h given together");
+  if (shape->rows > 0 && (!f || !x)) return fail(GDN_ERR_INVALID_ARG, "f and x must be non-NULL");
+  if ((f_codes != nullptr) != (f_scales != nullptr) || (gate_codes != nullptr) != (gate_scales != nullptr) ||
+      (gate_codes != nullptr) != (f_codes != nullptr && gate != nullptr))
+    return fail(GDN_ERR_INVALID_ARG, "checkpoint codes and scales are given together, for f and for the gate");
+  const uintptr_t a = elem(shape->io_dtype), b = elem(shape->x_dtype);
+  if (!aligned(f, a) || !aligned(gate, a) || !aligned(h, a) || !aligned(residual, b) || !aligned(x, b) ||
+      !aligned(w_post, 4) || !aligned(w_pre, 4) || !aligned(f_scales, 4) || !aligned(gate_scales, 4))
+    return fail(GDN_ERR_INVALID_ARG, "misaligned buffer");
+  st = check_device();
+  if (st != GDN_OK || shape->rows == 0) return st;
+  hipError_t e = gdn::launch_block_norm_fwd(*shape, f, gate, residual, w_post, w_pre, x, h, f_codes, f_scales,
+                                            gate_codes, gate_scales, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(GDN_ERR_DEVICE, "launch failed: %s", hipGetErrorString(e));
+  return GDN_OK;
+}
+
+size_t gdn_block_norm_bwd_workspace_bytes(const gdn_norm_t* shape) {
+  g_err[0] = 0;
+  return check_norm(shape) == GDN_OK ? gdn::block_norm_bwd_workspace_bytes(*shape) : 0;
+}
+
+gdn_status_t gdn_block_norm_bwd(const gdn_norm_t* shape, const void* f, const float* f_scales, const void* gate,
+                                const float* gate_scales, const float* w_post, const float* w_pre, const void* x,
+                                const void* d_x, const void* d_h, void* d_f, void* d_z, void* d_residual,
+                                float* dw_post, float* dw_pre, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  g_err[0] = 0;
+  gdn_status_t st = check_norm(shape);
+  if (st != GDN_OK) return st;
+  if (!w_post || !dw_post || (w_pre != nullptr) != (dw_pre != nullptr))
+    return fail(GDN_ERR_INVALID_ARG, "w_post and dw_post must be non-NULL, w_pre and dw_pre given together");
+  if (shape->rows > 0) {
+    if (!f || !d_x || !d_f) return fail(GDN_ERR_INVALID_ARG, "f, d_x and d_f must be non-NULL");
+    if (w_pre != nullptr && (!x || !d_h)) return fail(GDN_ERR_INVALID_ARG, "with w_pre, x and d_h must be non-NULL");
+    if ((gate != nullptr) != (d_z != nullptr)) return fail(GDN_ERR_INVALID_ARG, "the gate and d_z are given together");
+    if ((gate_scales != nullptr) != (f_scales != nullptr && gate != nullptr))
+      return fail(GDN_ERR_INVALID_ARG, "f and the gate are both codes, with scales, or both values");
+  }
+  const bool codes = f_scales != nullptr;
+  const uintptr_t a = elem(shape->io_dtype), b = elem(shape->x_dtype);
+  if ((!codes && (!aligned(f, a) || !aligned(gate, a))) || !aligned(d_h, a) || !aligned(d_f, a) ||
+      !aligned(d_z, a) || !aligned(x, b) || !aligned(d_x, b) || !aligned(d_residual, b) || !aligned(w_post, 4) ||
+      !aligned(w_pre, 4) || !aligned(dw_post, 4) || !aligned(dw_pre, 4) || !aligned(f_scales, 4) ||
+      !aligned(gate_scales, 4))
+    return fail(GDN_ERR_INVALID_ARG, "misaligned buffer");
+  st = check_workspace(workspace, workspace_bytes, gdn::block_norm_bwd_workspace_bytes(*shape), 16);
+  if (st == GDN_OK) st = check_device();
+  if (st != GDN_OK) return st;
+  hipError_t e = gdn::launch_block_norm_bwd(*shape, f, f_scales, gate, gate_scales, w_post, w_pre, x, d_x, d_h, d_f,
+                                            d_z, d_residual, dw_post, dw_pre, workspace, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(GDN_ERR_DEVICE, "launch failed: %s", hipGetErrorString(e));
+  return GDN_OK;
+}
+
+gdn_status_t gdn_act_pack(const void* x, int32_t dtype, uint8_t* codes, float* scales, int64_t rows, int32_t cols,
+                          void* stream) {
+  g_err[0] = 0;
+  gdn_status_t st = check_act(x, dtype, codes, scales, rows, cols);
+  if (st == GDN_OK) st = check_device();
+  if (st != GDN_OK || rows == 0) return st;
+  hipError_t e = gdn::launch_act_pack(x, dtype, codes, scales, rows, cols, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(GDN_ERR_DEVICE, "launch failed: %s", hipGetErrorString(e));
+  return GDN_OK;
+}
+
+gdn_status_t gdn_act_unpack(const uint8_t* codes, const float* scales, void* x, int32_t dtype, int64_t rows,
+                            int32_t cols, void* stream) {
+  g_err[0] = 0;
+  gdn_status_t st = check_act(x, dtype, codes, scales, rows, cols);
+  if (st == GDN_OK) st = check_device();
+  if (st != GDN_OK || rows == 0) return st;
+  hipError_t e = gdn::launch_act_unpack(codes, scales, x, dtype, rows, cols, (hipStream_t)stream);
+  if (e != hipSuccess) return fail(GDN_ERR_DEVICE, "launch failed: %s", hipGetErrorString(e));
+  return GDN_OK;
+}
+
+}  // extern "C"

@@ -109,4 +109,34 @@ hipError_t launch_chunk_bwd_dh(const gdn_shape_t& s, const void* q, const void* 
                                const void* dout, const float* dfin, float* dh, float* dinit, float* dvals,
                                void* workspace, hipStream_t stream);
 
+// Linear attention (gdn_lin_step.hip, gdn_lin.hip).
+hipError_t launch_lin_step(const gdn_lin_t& s, const void* q, const void* k, const void* v, const float* g,
+                           float* state, void* o, hipStream_t stream);
+size_t lin_fwd_workspace_bytes(const gdn_lin_t& s);
+hipError_t launch_lin_fwd(const gdn_lin_t& s, const void* q, const void* k, const void* v, const float* g,
+                          const int32_t* cu_seqlens, const float* initial_state, void* o, float* final_state,
+                          void* workspace, hipStream_t stream);
+size_t lin_bwd_workspace_bytes(const gdn_lin_t& s);
+hipError_t launch_lin_bwd(const gdn_lin_t& s, const void* q, const void* k, const void* v, const float* g,
+                          const int32_t* cu_seqlens, const void* d_o, const float* initial_state,
+                          const float* d_final_state, void* dq, void* dk, void* d_v, float* dg,
+                          float* d_initial_state, void* workspace, hipStream_t stream);
+
+// Block norms (gdn_block_norm.hip); f and the gate are E4M3 codes in the
+// backward where f_scales is given.
+hipError_t launch_block_norm_fwd(const gdn_norm_t& s, const void* f, const void* gate, const void* residual,
+                                 const float* w_post, const float* w_pre, void* x, void* h, uint8_t* f_codes,
+                                 float* f_scales, uint8_t* z_codes, float* z_scales, hipStream_t stream);
+size_t block_norm_bwd_workspace_bytes(const gdn_norm_t& s);
+hipError_t launch_block_norm_bwd(const gdn_norm_t& s, const void* f, const float* f_scales, const void* gate,
+                                 const float* gate_scales, const float* w_post, const float* w_pre, const void* x,
+                                 const void* d_x, const void* d_h, void* d_f, void* d_z, void* d_residual,
+                                 float* dw_post, float* dw_pre, void* workspace, hipStream_t stream);
+
+// Activations as E4M3 codes (gdn_act8.hip).
+hipError_t launch_act_pack(const void* x, int dtype, uint8_t* codes, float* scales, int64_t rows, int cols,
+                           hipStream_t stream);
+hipError_t launch_act_unpack(const uint8_t* codes, const float* scales, void* x, int dtype, int64_t rows, int cols,
+                             hipStream_t stream);
+
 }  // namespace gdn

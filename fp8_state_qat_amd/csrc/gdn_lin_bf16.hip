@@ -1,0 +1,15 @@
+// gdn_lin_bf16.hip -- the linear-attention scan kernels for bf16 inputs.
+#include "gdn_lin_scan.hpp"
+
+namespace gdn {
+hipError_t launch_lin_scan_bf16(const LinScan& A, LinMode mode, int64_t slots, hipStream_t stream) {
+  switch (mode) {
+    case kLinO: return lin_scan_mode<EngBF16, kLinO>(A, slots, stream);
+    case kLinStF: return lin_scan_mode<EngBF16, kLinStF>(A, slots, stream);
+    case kLinDQ: return lin_scan_mode<EngBF16, kLinDQ>(A, slots, stream);
+    case kLinStR: return lin_scan_mode<EngBF16, kLinStR>(A, slots, stream);
+    case kLinDV: return lin_scan_mode<EngBF16, kLinDV>(A, slots, stream);
+    default: return lin_scan_mode<EngBF16, kLinDK>(A, slots, stream);
+  }
+}
+}  // namespace gdn

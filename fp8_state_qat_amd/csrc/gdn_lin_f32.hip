@@ -1,0 +1,15 @@
+// gdn_lin_f32.hip -- the linear-attention scan kernels for fp32 inputs.
+#include "gdn_lin_scan.hpp"
+
+namespace gdn {
+hipError_t launch_lin_scan_f32(const LinScan& A, LinMode mode, int64_t slots, hipStream_t stream) {
+  switch (mode) {
+    case kLinO: return lin_scan_mode<EngF32, kLinO>(A, slots, stream);
+    case kLinStF: return lin_scan_mode<EngF32, kLinStF>(A, slots, stream);
+    case kLinDQ: return lin_scan_mode<EngF32, kLinDQ>(A, slots, stream);
+    case kLinStR: return lin_scan_mode<EngF32, kLinStR>(A, slots, stream);
+    case kLinDV: return lin_scan_mode<EngF32, kLinDV>(A, slots, stream);
+    default: return lin_scan_mode<EngF32, kLinDK>(A, slots, stream);
+  }
+}
+}  // namespace gdn

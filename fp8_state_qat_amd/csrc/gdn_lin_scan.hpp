@@ -1,0 +1,712 @@
+// gdn_lin_scan.hpp -- the scan kernel of linear attention with a decay for
+// each head, forward and backward.
+//
+// Mathematics.  With G_i the sum of the log decays of a 64-token chunk up to
+// token i, D_ij = e^(G_i - G_j) and S the state entering the chunk,
+//     o_i  = sum_{j<=i} D_ij (q_i.k_j) v_j      + e^(G_i) S q_i
+//     S   <- e^(G_C) S + sum_j e^(G_C - G_j) v_j k_j^T
+// The gradients are three more sums of the same form (dS: gradient of the
+// state at the chunk's end, which runs backwards in time):
+//     dq_i = sum_{j<=i} D_ij (do_i.v_j) k_j     + e^(G_i) S^T do_i
+//     dk_j = sum_{i>=j} D_ij (v_j.do_i) q_i     + e^(G_C - G_j) dS^T v_j
+//     dv_j = sum_{i>=j} D_ij (k_j.q_i) do_i     + e^(G_C - G_j) dS k_j
+//     dS  <- e^(G_C) dS + sum_i e^(G_i) do_i q_i^T
+// so one kernel serves all of them: out_a = sum_b w_ab (Q_a.K_b) V_b + in_a X^T Q_a,
+// X <- e^(G_C) X + sum_b out_b K_b V_b^T, with the operands' roles and the
+// direction set by the mode.
+//
+// Gradient of the log decays.  g_t scales every product that lies across it:
+// in a chunk, with M_ij = D_ij (q_i.k_j)(do_i.v_j) for i > j, r_i = q_i.(state
+// part of dq_i), c_j = k_j.(state part of dk_j) and X = e^(G_C) <S, dS>,
+//     dg_t = sum_{i>=t} (sum_j M_ij + r_i) - sum_{j>=t} sum_i M_ij + sum_{j<t} c_j + X.
+// X = Y - sum_j c_j with Y = <S, dS> at the chunk's end; before it (the next
+// chunk of the reversed walk) Y is X + sum_i r_i.  That recursion is started
+// anew every kAnchor chunks from the product of the two states, the forward
+// one stored there by the dq pass: its rounding errors never run far.
+//
+// Work split.  A workgroup owns one segment (a run of whole chunks of one
+// sequence) of one virtual head (a value head, or a 64- or 128-row tile of
+// one) and walks its chunks with X in fp32 accumulators: wave w holds the
+// columns 32 w .. 32 w + 31 of X for all CK rows.  Segments of a sequence run
+// at once: state passes first form every segment's own sum and decay, a small
+// kernel turns them into the state at each segment's start.  The segment
+// length is set by the host so that the card is full; with enough (sequence,
+// head) pairs there is one segment a sequence and the state passes vanish.
+//
+// Products (bf16 inputs: v_mfma_f32_16x16x32_bf16; fp32 inputs: fp32 MFMA).
+// Inputs enter as they are.  fp32 operands are split into bf16 planes: the
+// pair weights (24 bits of them would not show in a bf16 output) into two, X
+// into two where it only reaches a bf16 output and three where its product
+// enters dg, the weighted V rows of the state update into three, so that the
+// states and dg keep fp32 accuracy.  (Two planes leave 2e-6 of a value.)
+// The row relabelling dkmap makes the accumulators of X, in place, the A
+// operand of X^T Q, and the eight channels of a lane contiguous in memory;
+// P^T = K Q^T comes out as the B operand of the product with V.
+//
+// LDS: Q, K, V tiles of the chunk (64 rows, 16-byte units XOR-swizzled so
+// that row fragments, transpose reads and stores spread over the banks), the
+// fragments of P, gate vectors of this and the next chunk.  The next chunk's
+// rows are loaded into registers while this one computes (bf16).
+#pragma once
+
+#include <type_traits>
+
+#include "gdn_chunk_common.hpp"
+#include "gdn_lin.hpp"
+
+namespace gdn {
+
+// ---------------------------------------------------------------------------
+// Segments.  Sequence n has max(1, ceil(L_n / seglen)) of them, numbered
+// through the batch; every wave finds its own by scanning cu_seqlens.
+// ---------------------------------------------------------------------------
+struct LinSeg {
+  int n;        // sequence, -1: the slot is unused
+  int s, nseg;  // this segment of the sequence, their number
+  int t0, len;  // first row and rows
+  int slot0;    // slot of the sequence's first segment
+  bool bad;     // cu_seqlens out of contract
+};
+
+// want_seq: `at` is a sequence instead of a slot.
+__device__ __forceinline__ LinSeg lin_find(const int32_t* __restrict__ cu, int N, int64_t T, int seglen, int at,
+                                           bool want_seq) {
+  LinSeg r;
+  r.n = -1;
+  r.s = r.nseg = r.t0 = r.len = r.slot0 = 0;
+  r.bad = false;
+  const int ln = threadIdx.x & 63;
+  int base = 0;
+  for (int n0 = 0; n0 < N; n0 += 64) {
+    const int n = n0 + ln;
+    const bool in = n < N;
+    const int a = in ? cu[n] : 0, b = in ? cu[n + 1] : 0;
+    const bool wrong = in && (a < 0 || b < a || b > T);
+    if (__ballot(wrong) != 0) {
+      r.bad = true;
+      return r;
+    }
+    const int L = b - a;
+    const int cnt = in ? (L > 0 ? (L - 1) / seglen + 1 : 1) : 0;
+    int sum = cnt;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int v = __shfl_up(sum, off, 64);
+      if (ln >= off) sum += v;
+    }
+    const int lo = base + sum - cnt;
+    const bool mine = in && (want_seq ? n == at : (at >= lo && at < lo + cnt));
+    const unsigned long long m = __ballot(mine);
+    if (m != 0) {
+      const int src = __ffsll((unsigned long long)m) - 1;
+      r.n = n0 + src;
+      r.nseg = uniform(__shfl(cnt, src, 64));
+      r.slot0 = uniform(__shfl(lo, src, 64));
+      r.s = want_seq ? 0 : at - r.slot0;
+      const int rows = uniform(__shfl(L, src, 64)) - r.s * seglen;
+      r.t0 = uniform(__shfl(a, src, 64)) + r.s * seglen;
+      r.len = want_seq ? rows : (rows < seglen ? rows : seglen);
+    }
+    base += __shfl(sum, 63, 64);
+  }
+  return r;
+}
+
+// Swizzled 16-byte unit u of a tile row of U units: the rows of a fragment
+// (16 of them, one unit) and of a transpose read (4 rows, 4 units) both land
+// in distinct banks.
+template <int U>
+__device__ __forceinline__ int lin_unit(int row, int u) {
+  if constexpr (U >= 16) return u ^ (((row & 3) << 2) | ((row >> 2) & 3));
+  else return u ^ ((((row >> 1) & 1) << 2) | ((row >> 2) & 3));
+}
+
+template <typename E, int D>
+struct LinTile {
+  static constexpr int kUnits = D * (int)sizeof(E) / 16;
+  static constexpr int kBytes = kChunk * D * (int)sizeof(E);
+  // eight consecutive columns from c0 of a row, as a fragment
+  template <class Eng>
+  static __device__ __forceinline__ typename Eng::Fr row8(const char* t, int row, int c0) {
+    if constexpr (sizeof(E) == 2) {
+      return Eng::ld((const E*)(t + row * D * 2 + 16 * lin_unit<kUnits>(row, c0 / 8)));
+    } else {
+      return Eng::ld2((const E*)(t + row * D * 4 + 16 * lin_unit<kUnits>(row, c0 / 4)),
+                      (const E*)(t + row * D * 4 + 16 * lin_unit<kUnits>(row, c0 / 4 + 1)));
+    }
+  }
+  // column c0 + 8 (ln / 4) + ln % 4 of the rows kperm of k-block kb: the
+  // transposed fragment whose 16 columns are relabelled by dkmap
+  template <class Eng>
+  static __device__ __forceinline__ typename Eng::Fr cols8(const char* t, int kb, int c0, int ln, int gq) {
+    if constexpr (sizeof(E) == 2) {
+      const int r0 = 32 * kb + 4 * gq + (ln >> 2), r1 = r0 + 16, c = c0 + 8 * (ln & 3);
+      const uint2 a = lds_read_tr16(t + r0 * D * 2 + 16 * lin_unit<kUnits>(r0, c / 8) + (c & 4) * 2);
+      const uint2 b = lds_read_tr16(t + r1 * D * 2 + 16 * lin_unit<kUnits>(r1, c / 8) + (c & 4) * 2);
+      return __builtin_bit_cast(typename Eng::Fr, make_uint4(a.x, a.y, b.x, b.y));
+    } else {
+      typename Eng::Fr f;
+      const int c = c0 + 8 * (ln >> 2) + (ln & 3);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int r = 32 * kb + 4 * gq + (j & 3) + 16 * (j >> 2);
+        f.v[j] = *(const float*)(t + r * D * 4 + 16 * lin_unit<kUnits>(r, c / 4) + (c & 3) * 4);
+      }
+      return f;
+    }
+  }
+};
+
+// Rows of a chunk (n valid, the rest 0) from memory into registers and from
+// registers into a tile; NT threads.
+template <typename E, int D, int NT>
+struct LinRows {
+  static constexpr int kUnits = D * (int)sizeof(E) / 16;
+  static constexpr int kPer = kChunk * kUnits / NT;
+  static __device__ __forceinline__ uint4 ld1(const E* p, int64_t stride, int n, int i) {
+    const int idx = threadIdx.x + NT * i, row = idx / kUnits, u = idx % kUnits;
+    return row < n ? *reinterpret_cast<const uint4*>(p + row * stride + u * (16 / sizeof(E)))
+                   : make_uint4(0, 0, 0, 0);
+  }
+  static __device__ __forceinline__ void st1(char* t, int i, uint4 x) {
+    const int idx = threadIdx.x + NT * i, row = idx / kUnits, u = idx % kUnits;
+    *reinterpret_cast<uint4*>(t + row * D * sizeof(E) + 16 * lin_unit<kUnits>(row, u)) = x;
+  }
+  uint4 r[kPer];
+  __device__ __forceinline__ void load(const E* p, int64_t stride, int n) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) r[i] = ld1(p, stride, n, i);
+  }
+  __device__ __forceinline__ void store(char* t) const {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) st1(t, i, r[i]);
+  }
+  static __device__ __forceinline__ void copy(char* t, const E* p, int64_t stride, int n) {
+    constexpr int kStep = kPer < 8 ? kPer : 8;
+#pragma unroll 1
+    for (int i0 = 0; i0 < kPer; i0 += kStep) {
+      uint4 x[kStep];
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) x[i] = ld1(p, stride, n, i0 + i);
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) st1(t, i0 + i, x[i]);
+    }
+  }
+};
+
+struct LinGates {
+  float hi[kChunk], lo[kChunk];  // G_i = hi + lo
+  float in[kChunk];              // weight of X^T Q_a
+  float out[kChunk];             // weight of K_b V_b^T in the state
+  float decay;                   // e^(G_C)
+  float pad[3];
+};
+
+// One wave: the chunk's gate vectors.  The sums run in fp64 (far tokens of a
+// strongly decaying chunk differ by large G); a log decay below -1e4 has the
+// weight 0 and is held there, so that -inf leaves no NaN.
+template <bool kRev>
+__device__ __forceinline__ double lin_gates(LinGates& s, float g) {
+  const int ln = threadIdx.x & 63;
+  double G = (double)(g < -1e4f ? -1e4f : g);
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const double v = __shfl_up(G, off, 64);
+    if (ln >= off) G += v;
+  }
+  const double C = __shfl(G, 63, 64);
+  const float hi = (float)G;
+  s.hi[ln] = hi;
+  s.lo[ln] = (float)(G - (double)hi);
+  const float a = expf(hi), b = expf((float)(C - G));
+  s.in[ln] = kRev ? b : a;
+  s.out[ln] = kRev ? a : b;
+  if (ln == 63) s.decay = a;
+  return C;
+}
+
+__device__ __forceinline__ void ld8(const uint16_t* p, float (&x)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[2 * j] = bf16_lo(w[j]);
+    x[2 * j + 1] = bf16_hi(w[j]);
+  }
+}
+__device__ __forceinline__ void ld8(const float* p, float (&x)[8]) {
+  const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[j] = a[j];
+    x[4 + j] = b[j];
+  }
+}
+
+template <class Eng, int CK, int CV, int MODE>
+struct LinLds {
+  using E = typename Eng::E;
+  static constexpr bool kOut = MODE != kLinStF && MODE != kLinStR;
+  static constexpr bool kDots = MODE == kLinDQ || MODE == kLinDK;
+  static constexpr int kFrag = 64 * (sizeof(E) == 2 ? 16 : 32);
+  static constexpr int K = 0;
+  static constexpr int V = K + LinTile<E, CK>::kBytes;
+  static constexpr int Q = V + LinTile<E, CV>::kBytes;
+  static constexpr int P = Q + (kOut ? LinTile<E, CK>::kBytes : 0);
+  static constexpr int G = P + (kOut ? 8 * Eng::kPlanes * kFrag : 0);
+  static constexpr int R = G + 2 * (int)sizeof(LinGates);
+  static constexpr int M = R + (kDots ? (CV / 32) * kChunk * 4 : 0);
+  static constexpr int Y = M + (MODE == kLinDK ? 5 * kChunk * 4 : 0);
+  static constexpr int kBytes = Y + (MODE == kLinDK ? 32 : 0);
+};
+
+__device__ __forceinline__ double wave_sum_f64(double v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+
+template <class Eng, int CK, int CV, int MODE>
+__global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(LinScan A) {
+  using E = typename Eng::E;
+  using Fr = typename Eng::Fr;
+  using Lds = LinLds<Eng, CK, CV, MODE>;
+  using TK = LinTile<E, CK>;
+  using TV = LinTile<E, CV>;
+  constexpr bool kOut = Lds::kOut, kDots = Lds::kDots;
+  constexpr bool kRev = MODE == kLinStR || MODE == kLinDV || MODE == kLinDK;
+  constexpr bool kXT = !kDots;             // X rows are key channels (else value rows)
+  constexpr bool kThree = kDots;           // X in three planes: its product enters dg
+  constexpr int NT = 2 * CV, NW = NT / 64;
+  constexpr int RT = CK / 16;              // row tiles of X
+
+  extern __shared__ char smem[];
+  LinGates* sG = reinterpret_cast<LinGates*>(smem + Lds::G);
+
+  const int slot = blockIdx.x / A.VH, vh = blockIdx.x % A.VH;
+  const LinSeg sg = lin_find(A.cu, A.N, A.T, A.seglen, slot, false);
+  if (A.status != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *A.status = sg.bad ? kStatusBadIndex : 0;
+  if (sg.bad) return;
+  const int tid = threadIdx.x, w = tid >> 6, ln = tid & 15, gq = (tid >> 4) & 3;
+  const int64_t sv = (int64_t)slot * A.VH + vh;
+  if (sg.n < 0) {
+    if (MODE == kLinDK && A.dg_part != nullptr && tid == 0) A.dg_part[sv] = 0.0;
+    return;
+  }
+  // the state pass leaves out the segment whose sum nothing reads
+  if (MODE == kLinStF && sg.s == sg.nseg - 1) return;
+  if (MODE == kLinStR && sg.s == 0) return;
+
+  const int64_t t0 = sg.t0;
+  // stored states: a segment's groups from t0 / (rows of a group) + slot on, which no two segments share
+  const int64_t dump0 = (t0 / (kAnchor * kChunk) + slot) * A.VH + vh;
+  const E* pK = (const E*)A.K + t0 * A.ks + (int64_t)(vh / A.kd) * CK;
+  const E* pV = (const E*)A.V + t0 * A.vs + (int64_t)(vh / A.vd) * CV;
+  const E* pQ = kOut ? (const E*)A.Q + t0 * A.qs + (int64_t)(vh / A.qd) * CK : nullptr;
+  const E* pE = kDots ? (const E*)A.E + t0 * A.es + (int64_t)(vh / A.ed) * CV : nullptr;
+  const float* pg = A.g + t0 * A.g_row + vh / A.tiles;
+
+  // X: tile tr holds rows dkmap(16 tr + 4 gq + r), column tile t the column
+  // 32 w + 8 (ln / 4) + 4 t + ln % 4
+  f32x4 X[RT][2];
+  const int64_t st_size = (int64_t)A.tw * A.dk;
+  auto st_at = [&](int tr, int t, int r) -> int64_t {
+    const int row = 32 * (tr / 2) + 8 * gq + 4 * (tr & 1) + r, colx = 32 * w + 8 * (ln >> 2) + 4 * t + (ln & 3);
+    return kXT ? (int64_t)colx * CK + row : (int64_t)row * CV + colx;
+  };
+  {
+    const float* p = nullptr;
+    if (kOut) {
+      if (A.seg != nullptr) p = A.seg + sv * st_size;
+      else if (A.first != nullptr) p = A.first + ((int64_t)sg.n * A.VH + vh) * st_size;
+    }
+#pragma unroll
+    for (int tr = 0; tr < RT; ++tr)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (p != nullptr) {
+          if constexpr (kXT) x = *reinterpret_cast<const f32x4*>(p + st_at(tr, t, 0));
+          else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = p[st_at(tr, t, r)];
+          }
+        }
+        X[tr][t] = x;
+      }
+  }
+
+  const int nch = (sg.len + kChunk - 1) / kChunk;
+  auto rows_of = [&](int c) { const int n = sg.len - kChunk * c; return n < kChunk ? n : kChunk; };
+  constexpr bool kPre = sizeof(E) == 2;
+  LinRows<E, CK, NT> rK;
+  LinRows<E, CV, NT> rV;
+  LinRows<E, CK, NT> rQ;
+  float rg = 0.0f;
+  auto fetch = [&](int c) {
+    const int n = rows_of(c);
+    const int64_t r0 = (int64_t)kChunk * c;
+    if constexpr (kPre) {
+      rK.load(pK + r0 * A.ks, A.ks, n);
+      rV.load(pV + r0 * A.vs, A.vs, n);
+      if constexpr (kOut) rQ.load(pQ + r0 * A.qs, A.qs, n);
+    }
+    if (w == 0) rg = (tid & 63) < n ? pg[(r0 + (tid & 63)) * A.g_row] : 0.0f;
+  };
+
+  double Gsum = 0.0;                       // wave 0: sum of the segment's log decays
+  double Y = 0.0, dg_sum = 0.0;            // DK, wave 0
+  if (nch > 0) {
+    fetch(kRev ? nch - 1 : 0);
+    if (w == 0) Gsum += lin_gates<kRev>(sG[0], rg);
+  }
+#pragma unroll 1
+  for (int it = 0; it < nch; ++it) {
+    const int c = kRev ? nch - 1 - it : it, n = rows_of(c);
+    const int64_t r0 = (int64_t)kChunk * c;
+    const LinGates& g = sG[it & 1];
+    if constexpr (kPre) {
+      rK.store(smem + Lds::K);
+      rV.store(smem + Lds::V);
+      if constexpr (kOut) rQ.store(smem + Lds::Q);
+    } else {
+      LinRows<E, CK, NT>::copy(smem + Lds::K, pK + r0 * A.ks, A.ks, n);
+      LinRows<E, CV, NT>::copy(smem + Lds::V, pV + r0 * A.vs, A.vs, n);
+      if constexpr (kOut) LinRows<E, CK, NT>::copy(smem + Lds::Q, pQ + r0 * A.qs, A.qs, n);
+    }
+    __syncthreads();
+    if (it + 1 < nch) fetch(kRev ? c - 1 : c + 1);
+
+    // DK: Y = <S, dS> at the chunk's end, anew from the stored state of its group
+    if constexpr (MODE == kLinDK) {
+      if (c % kAnchor == kAnchor - 1 || c == nch - 1) {
+        const f32x4* d = reinterpret_cast<const f32x4*>(A.dump) +
+                         (dump0 + (c / kAnchor) * (int64_t)A.VH) * (CK * CV / 4) + tid;
+        double y = 0.0;
+#pragma unroll
+        for (int tr = 0; tr < RT; ++tr)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const f32x4 s = d[(2 * tr + t) * NT];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) y = fma((double)s[r], (double)X[tr][t][r], y);
+          }
+        y = wave_sum_f64(y);
+        if ((tid & 63) == 0) reinterpret_cast<double*>(smem + Lds::Y)[w] = y;
+      }
+    }
+
+    f32x4 O[4][2];
+    if constexpr (kOut) {
+      // ---- pair products of row blocks a (this wave's) and b, weighted
+#pragma unroll
+      for (int half = 0; half < 4 / NW; ++half) {
+        const int a = NW == 4 ? w : (half == 0 ? w : 3 - w);
+        const float ah = g.hi[16 * a + ln], al = g.lo[16 * a + ln];
+        Fr qf[CK / 32];
+#pragma unroll
+        for (int p = 0; p < CK / 32; ++p) qf[p] = TK::template row8<Eng>(smem + Lds::Q, 16 * a + ln, 32 * p + 8 * gq);
+        Fr ef[MODE == kLinDK ? CV / 32 : 1];
+        float cm = 0.0f;                   // DK: column sums of M
+        if constexpr (MODE == kLinDK) {
+          const int row = 16 * a + ln;
+#pragma unroll
+          for (int p = 0; p < CV / 32; ++p) {
+            const E* e = pE + (r0 + (row < n ? row : 0)) * A.es + 32 * p + 8 * gq;
+            ef[p] = Eng::ld(e);
+          }
+        }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          if (kRev ? 2 * kb + 1 < a : 2 * kb > a) {
+            if constexpr (MODE == kLinDK) {
+              if (ln == 0) {
+#pragma unroll
+                for (int bb = 0; bb < 2; ++bb)
+#pragma unroll
+                  for (int r = 0; r < 4; ++r)
+                    reinterpret_cast<float*>(smem + Lds::M)[64 * a + 16 * (2 * kb + bb) + 4 * gq + r] = 0.0f;
+              }
+            }
+            continue;
+          }
+          float pw[8];
+#pragma unroll
+          for (int bb = 0; bb < 2; ++bb) {
+            const int b = 2 * kb + bb;
+            f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f}, acc2 = acc;
+            if (kRev ? b >= a : b <= a) {
+#pragma unroll
+              for (int p = 0; p < CK / 32; ++p)
+                Eng::mma(acc, TK::template row8<Eng>(smem + Lds::K, 16 * b + ln, 32 * p + 8 * gq), qf[p]);
+              if constexpr (MODE == kLinDK) {
+#pragma unroll
+                for (int p = 0; p < CV / 32; ++p)
+                  Eng::mma(acc2, TV::template row8<Eng>(smem + Lds::V, 16 * b + ln, 32 * p + 8 * gq), ef[p]);
+              }
+            }
+            const f32x4 bh = *reinterpret_cast<const f32x4*>(&g.hi[16 * b + 4 * gq]);
+            const f32x4 bl = *reinterpret_cast<const f32x4*>(&g.lo[16 * b + 4 * gq]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int ia = 16 * a + ln, ib = 16 * b + 4 * gq + r;
+              const float d = kRev ? (bh[r] - ah) + (bl[r] - al) : (ah - bh[r]) + (al - bl[r]);
+              const float wt = (kRev ? ib >= ia : ib <= ia) ? expf(d) : 0.0f;
+              pw[4 * bb + r] = acc[r] * wt;
+              if constexpr (MODE == kLinDK) {
+                const float m = ib > ia ? acc2[r] * pw[4 * bb + r] : 0.0f;
+                cm += m;
+                const float rm = group_sum<16>(m);
+                if (ln == 0) reinterpret_cast<float*>(smem + Lds::M)[64 * a + ib] = rm;
+              }
+            }
+          }
+          Fr hi, lo;
+          Eng::split(pw, hi, lo);
+          char* dst = smem + Lds::P + (2 * a + kb) * Eng::kPlanes * Lds::kFrag + (tid & 63) * (Lds::kFrag / 64);
+          Eng::st((E*)dst, hi);
+          if constexpr (Eng::kPlanes == 2) Eng::st((E*)(dst + Lds::kFrag), lo);
+        }
+        if constexpr (MODE == kLinDK) {
+          cm += __shfl_xor(cm, 16, 64);
+          cm += __shfl_xor(cm, 32, 64);
+          if (gq == 0) reinterpret_cast<float*>(smem + Lds::M)[256 + 16 * a + ln] = cm;
+        }
+      }
+    }
+    if (it + 1 < nch && w == 0) Gsum += lin_gates<kRev>(sG[(it + 1) & 1], rg);
+
+    Fr vf[2][2];                           // V^T fragments of this wave's columns
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+        vf[t][kb] = TV::template cols8<Eng>(smem + Lds::V, kb, 32 * w + 4 * t, ln, gq);
+
+    if constexpr (kOut) {
+      // ---- state part: O^T = X^T Q^T, scaled by the rows' weights
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) O[rt][0] = O[rt][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int p = 0; p < CK / 32; ++p) {
+        Fr xh[2], xm[2], xl[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float x8[8] = {X[2 * p][t][0], X[2 * p][t][1], X[2 * p][t][2], X[2 * p][t][3],
+                               X[2 * p + 1][t][0], X[2 * p + 1][t][1], X[2 * p + 1][t][2], X[2 * p + 1][t][3]};
+          if constexpr (kThree) Eng::split3(x8, xh[t], xm[t], xl[t]);
+          else Eng::split(x8, xh[t], xm[t]);
+        }
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+          const Fr qf = TK::template row8<Eng>(smem + Lds::Q, 16 * rt + ln, 32 * p + 8 * gq);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            Eng::mma(O[rt][t], xh[t], qf);
+            if constexpr (Eng::kSplit) {
+              Eng::mma(O[rt][t], xm[t], qf);
+              if constexpr (kThree) Eng::mma(O[rt][t], xl[t], qf);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) {
+        const float s = g.in[16 * rt + ln];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) O[rt][t][r] *= s;
+      }
+      if constexpr (kDots) {               // r_i, c_j: the wave's columns of the dots
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+          const int row = 16 * rt + ln;
+          const E* e = pE + (r0 + (row < n ? row : 0)) * A.es + 32 * w + 8 * gq;
+          float d = 0.0f, ev[8];
+          ld8(e, ev);
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) d = fmaf(O[rt][t][r], ev[4 * t + r], d);
+          d += __shfl_xor(d, 16, 64);
+          d += __shfl_xor(d, 32, 64);
+          if (gq == 0) reinterpret_cast<float*>(smem + Lds::R)[kChunk * w + row] = row < n ? d : 0.0f;
+        }
+      }
+      __syncthreads();
+      // ---- pair part: O^T += V^T P^T
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          if (kRev ? 2 * kb + 1 < rt : 2 * kb > rt) continue;
+          const char* src = smem + Lds::P + (2 * rt + kb) * Eng::kPlanes * Lds::kFrag + (tid & 63) * (Lds::kFrag / 64);
+          const Fr ph = Eng::ld((const E*)src);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) Eng::mma(O[rt][t], vf[t][kb], ph);
+          if constexpr (Eng::kPlanes == 2) {
+            const Fr pl = Eng::ld((const E*)(src + Lds::kFrag));
+#pragma unroll
+            for (int t = 0; t < 2; ++t) Eng::mma(O[rt][t], vf[t][kb], pl);
+          }
+        }
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) {
+        const int row = 16 * rt + ln;
+        if (row < n) {
+          const int64_t at = (t0 + r0 + row) * A.os + (int64_t)(vh / A.od) * CV + 32 * w + 8 * gq;
+          if (sizeof(E) == 4 || A.out_f32) {
+            float* o = (float*)A.out + at;
+            *reinterpret_cast<f32x4*>(o) = O[rt][0];
+            *reinterpret_cast<f32x4*>(o + 4) = O[rt][1];
+          } else {
+            *reinterpret_cast<uint4*>((uint16_t*)A.out + at) =
+                make_uint4(pack_bf16x2(O[rt][0][0], O[rt][0][1]), pack_bf16x2(O[rt][0][2], O[rt][0][3]),
+                           pack_bf16x2(O[rt][1][0], O[rt][1][1]), pack_bf16x2(O[rt][1][2], O[rt][1][3]));
+          }
+        }
+      }
+      if constexpr (kDots) {
+        if (w == 0) {
+          const int t = tid & 63;
+          float d = 0.0f;
+#pragma unroll
+          for (int k = 0; k < NW; ++k) d += reinterpret_cast<const float*>(smem + Lds::R)[kChunk * k + t];
+          const int64_t at = (t0 + r0 + t) * A.VH + vh;
+          if constexpr (MODE == kLinDQ) {
+            if (t < n) A.rdot[at] = d;
+          } else {
+            const float* sM = reinterpret_cast<const float*>(smem + Lds::M);
+            if (c % kAnchor == kAnchor - 1 || c == nch - 1) {
+              const double* sY = reinterpret_cast<const double*>(smem + Lds::Y);
+              Y = sY[0];
+#pragma unroll
+              for (int k = 1; k < NW; ++k) Y += sY[k];
+            }
+            const double r = t < n ? (double)A.rdot[at] : 0.0;
+            double rm = 0.0;               // row sum of M, over the column blocks
+#pragma unroll
+            for (int a = 0; a < 4; ++a) rm += (double)sM[64 * a + t];
+            double suf = rm + r - (double)sM[256 + t], pre = (double)d;
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+              const double u = __shfl_down(suf, off, 64), v = __shfl_up(pre, off, 64);
+              if (t + off < 64) suf += u;
+              if (t >= off) pre += v;
+            }
+            const double csum = __shfl(pre, 63, 64);
+            const double Xc = Y - csum;
+            const double dg = suf + (pre - (double)d) + Xc;
+            Y = Xc + wave_sum_f64(r);
+            if (t < n) {
+              if (A.dg_tok != nullptr) A.dg_tok[at] = (float)dg;
+              dg_sum += dg;
+            }
+          }
+        }
+      }
+    }
+
+    // ---- X <- e^(G_C) X + sum_b out_b K_b V_b^T
+    const float dec = g.decay;
+#pragma unroll
+    for (int tr = 0; tr < RT; ++tr)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) X[tr][t][r] *= dec;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      const f32x4 w0 = *reinterpret_cast<const f32x4*>(&g.out[32 * kb + 4 * gq]);
+      const f32x4 w1 = *reinterpret_cast<const f32x4*>(&g.out[32 * kb + 16 + 4 * gq]);
+      Fr vh_[2], vm[2], vl[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        float x8[8];
+        if constexpr (Eng::kSplit) {
+          const uint4 u = __builtin_bit_cast(uint4, vf[t][kb]);
+          x8[0] = bf16_lo(u.x) * w0[0]; x8[1] = bf16_hi(u.x) * w0[1];
+          x8[2] = bf16_lo(u.y) * w0[2]; x8[3] = bf16_hi(u.y) * w0[3];
+          x8[4] = bf16_lo(u.z) * w1[0]; x8[5] = bf16_hi(u.z) * w1[1];
+          x8[6] = bf16_lo(u.w) * w1[2]; x8[7] = bf16_hi(u.w) * w1[3];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x8[j] = vf[t][kb].v[j] * (j < 4 ? w0[j] : w1[j & 3]);
+        }
+        Eng::split3(x8, vh_[t], vm[t], vl[t]);
+      }
+#pragma unroll
+      for (int tr = 0; tr < RT; ++tr) {
+        const Fr kf = TK::template cols8<Eng>(smem + Lds::K, kb, 32 * (tr / 2) + 4 * (tr & 1), ln, gq);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          Eng::mma(X[tr][t], kf, vh_[t]);
+          if constexpr (Eng::kSplit) {
+            Eng::mma(X[tr][t], kf, vm[t]);
+            Eng::mma(X[tr][t], kf, vl[t]);
+          }
+        }
+      }
+    }
+    if constexpr (MODE == kLinDQ) {
+      if (c % kAnchor == kAnchor - 1 || c == nch - 1) {
+        f32x4* d = reinterpret_cast<f32x4*>(A.dump) + (dump0 + (c / kAnchor) * (int64_t)A.VH) * (CK * CV / 4) + tid;
+#pragma unroll
+        for (int tr = 0; tr < RT; ++tr)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) d[(2 * tr + t) * NT] = X[tr][t];
+      }
+    }
+    __syncthreads();
+  }
+
+  // ---- the state after the walk
+  float* p = nullptr;
+  if (!kOut) p = A.seg + sv * st_size;
+  else if (A.last != nullptr && sg.s == (kRev ? 0 : sg.nseg - 1)) p = A.last + ((int64_t)sg.n * A.VH + vh) * st_size;
+  if (p != nullptr) {
+#pragma unroll
+    for (int tr = 0; tr < RT; ++tr)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if constexpr (kXT) *reinterpret_cast<f32x4*>(p + st_at(tr, t, 0)) = X[tr][t];
+        else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) p[st_at(tr, t, r)] = X[tr][t][r];
+        }
+      }
+  }
+  if (!kOut && tid == 0) A.seg_decay[sv] = expf((float)Gsum);
+  if constexpr (MODE == kLinDK) {
+    if (A.dg_part != nullptr && w == 0) {
+      const double s = wave_sum_f64(dg_sum);
+      if (tid == 0) A.dg_part[sv] = s;
+    }
+  }
+}
+
+template <class Eng, int CK, int CV, int MODE>
+static hipError_t lin_scan_go(const LinScan& A, int64_t slots, hipStream_t stream) {
+  static PerDeviceOnce once;
+  constexpr int lds = LinLds<Eng, CK, CV, MODE>::kBytes;
+  const auto kern = lin_scan_kernel<Eng, CK, CV, MODE>;
+  const hipError_t e = set_dyn_lds_once(once, (const void*)kern, lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(slots * A.VH)), dim3(2 * CV), lds, stream, A);
+  return hipGetLastError();
+}
+
+// CK, CV: the key channels and the value rows of a virtual head, in the order
+// the mode takes them.
+template <class Eng, int MODE>
+static hipError_t lin_scan_mode(const LinScan& A, int64_t slots, hipStream_t stream) {
+  const bool swap = MODE == kLinDQ || MODE == kLinDK;
+  const int ck = swap ? A.tw : A.dk, cv = swap ? A.dk : A.tw;
+  if (ck == 64) return cv == 64 ? lin_scan_go<Eng, 64, 64, MODE>(A, slots, stream)
+                                : lin_scan_go<Eng, 64, 128, MODE>(A, slots, stream);
+  return cv == 64 ? lin_scan_go<Eng, 128, 64, MODE>(A, slots, stream)
+                  : lin_scan_go<Eng, 128, 128, MODE>(A, slots, stream);
+}
+
+}  // namespace gdn

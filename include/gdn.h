@@ -352,6 +352,140 @@ gdn_status_t gdn_chunk_bwd_dh(const gdn_shape_t* shape,
  * of gdn_chunk_fwd's workspace.  0 for an invalid shape. */
 size_t gdn_chunk_bwd_workspace_bytes(const gdn_shape_t* shape);
 
+/*
+ * Linear attention with a decay for each head:
+ *   S_t = e^{g_t} S_{t-1} + v_t k_t^T,   o_t = S_t q_t      (S: dv x dk, fp32)
+ * over packed sequences, its gradients, and its single-token form.
+ *
+ *   q, k   [total_tokens, qk_heads, dk] io_dtype; value head h uses query/key
+ *          head h / (n_heads / qk_heads)
+ *   v      [total_tokens, n_heads, dv] io_dtype
+ *   g      natural-log decay, <= 0 expected: [total_tokens, n_heads] fp32 with
+ *          gate_per_token, else [n_heads], one decay a head for all tokens.
+ *          -inf (the token starts from an empty state) is allowed.
+ * A state is [n_seqs, n_heads, dv, dk] fp32.  Buffers are 16-byte aligned (g
+ * and dg 4), row-major.
+ */
+typedef struct {
+    int32_t n_seqs;            /* N >= 1 */
+    int32_t n_heads;           /* H >= 1, value heads */
+    int32_t qk_heads;          /* divides n_heads */
+    int32_t dk;                /* 64 or 128 */
+    int32_t dv;                /* a multiple of 64, at most 256 */
+    int32_t io_dtype;          /* gdn_dtype_t of q, k, v, o and of the gradients dq, dk, dv */
+    int32_t gate_per_token;    /* 0: g is [H]; 1: g is [T, H] */
+    int64_t total_tokens;      /* T >= 0, below 2^31 (step: must equal n_seqs) */
+} gdn_lin_t;
+
+/*
+ * gdn_lin_attn_fwd -- outputs and final states of packed sequences.
+ *   cu_seqlens  [N + 1] int32: sequence n is rows [cu_seqlens[n], cu_seqlens[n + 1]);
+ *               rows outside every sequence are not written.  Entries that
+ *               decrease or leave [0, total_tokens] are found on the device:
+ *               nothing is written then and gdn_workspace_status reports it.
+ *   initial_state  NULL: zero.
+ *   o           [total_tokens, n_heads, dv] io_dtype
+ *   final_state the state after each sequence (the initial state where it is
+ *               empty); may not alias initial_state.
+ *   workspace   gdn_lin_attn_fwd_workspace_bytes(shape) bytes, 256-byte aligned.
+ */
+gdn_status_t gdn_lin_attn_fwd(const gdn_lin_t* shape, const void* q, const void* k, const void* v,
+                              const float* g, const int32_t* cu_seqlens, const float* initial_state,
+                              void* o, float* final_state, void* workspace, size_t workspace_bytes,
+                              void* stream);
+/* Workspace bytes of gdn_lin_attn_fwd; 0 for an invalid shape. */
+size_t gdn_lin_attn_fwd_workspace_bytes(const gdn_lin_t* shape);
+
+/*
+ * gdn_lin_attn_bwd -- gradients of L = sum o . d_o + <S_final, d_final_state>.
+ *   d_o            [total_tokens, n_heads, dv] io_dtype
+ *   initial_state  that of the forward, or NULL;  d_final_state: NULL: zero
+ *   dq, dk         [total_tokens, qk_heads, dk] io_dtype (summed over the value
+ *                  heads that share a query/key head);  d_v as v
+ *   dg             fp32, shape of g (summed over all tokens for [H])
+ *   d_initial_state  a state (written also without an initial state)
+ * cu_seqlens and the workspace as for gdn_lin_attn_fwd.
+ */
+gdn_status_t gdn_lin_attn_bwd(const gdn_lin_t* shape, const void* q, const void* k, const void* v,
+                              const float* g, const int32_t* cu_seqlens, const void* d_o,
+                              const float* initial_state, const float* d_final_state,
+                              void* dq, void* dk, void* d_v, float* dg, float* d_initial_state,
+                              void* workspace, size_t workspace_bytes, void* stream);
+/* Workspace bytes of gdn_lin_attn_bwd; 0 for an invalid shape. */
+size_t gdn_lin_attn_bwd_workspace_bytes(const gdn_lin_t* shape);
+
+/*
+ * gdn_lin_attn_step -- one token for each sequence (total_tokens == n_seqs;
+ * q, k [N, qk_heads, dk], v and o [N, n_heads, dv], g [N, n_heads] or [n_heads]):
+ * the state is updated in place and o is taken from the updated state.
+ */
+gdn_status_t gdn_lin_attn_step(const gdn_lin_t* shape, const void* q, const void* k, const void* v,
+                               const float* g, float* state, void* o, void* stream);
+
+/* The gate's form in the block norms: a(z) = z / (1 + e^-z), or 1 / (1 + e^-z). */
+typedef enum {
+    GDN_ACT_SILU = 0,
+    GDN_ACT_SIGMOID = 1
+} gdn_act_t;
+
+/*
+ * The norm after a block, its gate, the scaled residual and the norm before
+ * the next block, row by row ([rows, cols], row-major; 1 <= cols <= 16384):
+ *   x = res_scale * (f / rms(f) * w_post * a(gate)) + residual
+ *   h = x / rms(x) * w_pre              rms(u) = sqrt(mean u^2 + eps)
+ * h is formed from x before x is rounded to x_dtype.
+ */
+typedef struct {
+    int64_t rows;              /* >= 0 */
+    int32_t cols;
+    int32_t io_dtype;          /* gdn_dtype_t of f, gate, h and their gradients */
+    int32_t x_dtype;           /* gdn_dtype_t of x and the residual; GDN_F32 with io_dtype GDN_F32 */
+    int32_t act;               /* gdn_act_t (read only with a gate) */
+    float res_scale;
+    float eps;                 /* > 0 */
+} gdn_norm_t;
+
+/*
+ * gdn_block_norm_fwd
+ *   gate, residual  NULL: none;  w_post, w_pre  [cols] fp32;  w_pre NULL: no h
+ *   f_codes, f_scales (and gate_codes, gate_scales with a gate)  outputs, given
+ *               together or NULL: f and the gate as gdn_act_pack stores them.
+ */
+gdn_status_t gdn_block_norm_fwd(const gdn_norm_t* shape, const void* f, const void* gate,
+                                const void* residual, const float* w_post, const float* w_pre,
+                                void* x, void* h, uint8_t* f_codes, float* f_scales,
+                                uint8_t* gate_codes, float* gate_scales, void* stream);
+
+/*
+ * gdn_block_norm_bwd -- gradients from those of x (d_x) and h (d_h).
+ *   f, gate     the forward's inputs; with f_scales (and gate_scales) given they
+ *               are E4M3 codes, and the gradients those at the coded values
+ *   x           the forward's x and d_h: needed with w_pre, else NULL
+ *   d_z         with a gate;  d_residual  NULL: not wanted
+ *   dw_post, dw_pre  [cols] fp32, sums over the rows (dw_pre with w_pre)
+ *   workspace   gdn_block_norm_bwd_workspace_bytes(shape) bytes, 16-byte aligned
+ */
+gdn_status_t gdn_block_norm_bwd(const gdn_norm_t* shape, const void* f, const float* f_scales,
+                                const void* gate, const float* gate_scales, const float* w_post,
+                                const float* w_pre, const void* x, const void* d_x, const void* d_h,
+                                void* d_f, void* d_z, void* d_residual, float* dw_post, float* dw_pre,
+                                void* workspace, size_t workspace_bytes, void* stream);
+/* Workspace bytes of gdn_block_norm_bwd; 0 for an invalid shape. */
+size_t gdn_block_norm_bwd_workspace_bytes(const gdn_norm_t* shape);
+
+/*
+ * gdn_act_pack, gdn_act_unpack -- activations [rows, cols] as E4M3 codes.
+ * Each 64 consecutive columns of a row (fewer at a row's end) share the scale
+ * s = RN(amax / 448), 1 where that is not positive; code = the E4M3 value
+ * nearest to RN(x / s), ties to even; the value a code stands for is
+ * RN(code * s).  codes [rows, cols] bytes (OCP E4M3FN), scales [rows,
+ * ceil(cols / 64)] fp32.  rows * ceil(cols / 64) < 2^31.
+ */
+gdn_status_t gdn_act_pack(const void* x, int32_t dtype, uint8_t* codes, float* scales,
+                          int64_t rows, int32_t cols, void* stream);
+gdn_status_t gdn_act_unpack(const uint8_t* codes, const float* scales, void* x, int32_t dtype,
+                            int64_t rows, int32_t cols, void* stream);
+
 /* Static description of a status code. */
 const char* gdn_status_string(gdn_status_t status);
 
