@@ -427,8 +427,10 @@ gdn_status_t gdn_lin_attn_fwd(const gdn_lin_t* shape, const void* q, const void*
   g_err[0] = 0;
   gdn_status_t st = check_lin(shape, false);
   if (st != GDN_OK) return st;
-  if (!cu_seqlens || !final_state || !g)
-    return fail(GDN_ERR_INVALID_ARG, "cu_seqlens, g and final_state must be non-NULL");
+  if (!cu_seqlens || !final_state)
+    return fail(GDN_ERR_INVALID_ARG, "cu_seqlens and final_state must be non-NULL");
+  if (!g && (shape->total_tokens > 0 || !shape->gate_per_token))
+    return fail(GDN_ERR_INVALID_ARG, "g must be non-NULL");
   if (shape->total_tokens > 0 && (!q || !k || !v || !o))
     return fail(GDN_ERR_INVALID_ARG, "q, k, v and o must be non-NULL");
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(initial_state, 16) ||
@@ -452,12 +454,12 @@ gdn_status_t gdn_lin_attn_bwd(const gdn_lin_t* shape, const void* q, const void*
   g_err[0] = 0;
   gdn_status_t st = check_lin(shape, false);
   if (st != GDN_OK) return st;
-  if (!cu_seqlens || !g || !d_initial_state)
-    return fail(GDN_ERR_INVALID_ARG, "cu_seqlens, g and d_initial_state must be non-NULL");
+  if (!cu_seqlens || !d_initial_state)
+    return fail(GDN_ERR_INVALID_ARG, "cu_seqlens and d_initial_state must be non-NULL");
   if (shape->total_tokens > 0 && (!q || !k || !v || !d_o || !dq || !dk || !d_v))
     return fail(GDN_ERR_INVALID_ARG, "q, k, v, d_o, dq, dk and d_v must be non-NULL");
-  if (!dg && (shape->total_tokens > 0 || !shape->gate_per_token))
-    return fail(GDN_ERR_INVALID_ARG, "dg must be non-NULL");
+  if ((!g || !dg) && (shape->total_tokens > 0 || !shape->gate_per_token))
+    return fail(GDN_ERR_INVALID_ARG, "g and dg must be non-NULL");
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(d_o, 16) || !aligned(dq, 16) ||
       !aligned(dk, 16) || !aligned(d_v, 16) || !aligned(initial_state, 16) || !aligned(d_final_state, 16) ||
       !aligned(d_initial_state, 16) || !aligned(g, 4) || !aligned(dg, 4) || !aligned(cu_seqlens, 4))
