@@ -356,10 +356,12 @@ gdn_status_t check_lin(const gdn_lin_t* s, bool step) {
   if (s->total_tokens < 0) return fail(GDN_ERR_INVALID_ARG, "total_tokens must be >= 0");
   if (step && s->total_tokens != s->n_seqs)
     return fail(GDN_ERR_INVALID_ARG, "step: total_tokens must equal n_seqs");
-  // row strides and the workgroups of a launch are 32-bit, sequences a grid's second dimension
+  // the workgroups of a launch are 32-bit, sequences a grid's second dimension
   if (s->total_tokens >= (int64_t)1 << 31) return fail(GDN_ERR_UNSUPPORTED, "total_tokens must be below 2^31");
-  if ((int64_t)s->n_heads * s->dv >= (int64_t)1 << 28 || (int64_t)s->n_heads * s->dk >= (int64_t)1 << 28)
-    return fail(GDN_ERR_UNSUPPORTED, "n_heads too large");
+  // a chunk of 64 rows is addressed with 32-bit byte offsets, partial gradients (fp32) included
+  if ((int64_t)64 * s->n_heads * s->dv * 4 >= (int64_t)1 << 31 ||
+      (int64_t)64 * s->n_heads * (s->dv / 64) * s->dk * 4 >= (int64_t)1 << 31)
+    return fail(GDN_ERR_UNSUPPORTED, "n_heads too large (64 rows of fp32 must be below 2^31 bytes)");
   if (!step && s->n_seqs > 65535) return fail(GDN_ERR_UNSUPPORTED, "more than 65535 sequences");
   const int64_t units = (int64_t)s->n_heads * (s->dv / 16) *
                         (step ? (int64_t)s->n_seqs : s->total_tokens / 64 + s->n_seqs);

@@ -45,8 +45,11 @@
 //
 // LDS: Q, K, V tiles of the chunk (64 rows, 16-byte units XOR-swizzled so
 // that row fragments, transpose reads and stores spread over the banks), the
-// fragments of P, gate vectors of this and the next chunk.  The next chunk's
-// rows are loaded into registers while this one computes (bf16).
+// fragments of P, gate vectors of this and the next chunk.  bf16 rows go from
+// memory straight into LDS: Q and V are free after the state part, K has a
+// second tile, so the next chunk's rows are asked for in the middle of this
+// one and a chunk needs two barriers (a state pass one).  At 128 x 128 the
+// tiles take 80 KB: two workgroups a compute unit.
 #pragma once
 
 #include <type_traits>
@@ -157,42 +160,67 @@ struct LinTile {
   }
 };
 
-// Rows of a chunk (n valid, the rest 0) from memory into registers and from
-// registers into a tile; NT threads.
+// Rows of a chunk into a tile; NT threads.
 template <typename E, int D, int NT>
 struct LinRows {
   static constexpr int kUnits = D * (int)sizeof(E) / 16;
   static constexpr int kPer = kChunk * kUnits / NT;
-  static __device__ __forceinline__ uint4 ld1(const E* p, int64_t stride, int n, int i) {
-    const int idx = threadIdx.x + NT * i, row = idx / kUnits, u = idx % kUnits;
-    return row < n ? *reinterpret_cast<const uint4*>(p + row * stride + u * (16 / sizeof(E)))
-                   : make_uint4(0, 0, 0, 0);
-  }
-  static __device__ __forceinline__ void st1(char* t, int i, uint4 x) {
-    const int idx = threadIdx.x + NT * i, row = idx / kUnits, u = idx % kUnits;
-    *reinterpret_cast<uint4*>(t + row * D * sizeof(E) + 16 * lin_unit<kUnits>(row, u)) = x;
-  }
-  uint4 r[kPer];
-  __device__ __forceinline__ void load(const E* p, int64_t stride, int n) {
+  // Asked for and on the way (wait_vmem, then a barrier): rows from n on are
+  // copies of the last valid one, which no result takes in.
+  static __device__ __forceinline__ void ask(uint32_t lds, const E* p, int stride, int n) {
+    const uint32_t at = lds + 16 * 64 * (threadIdx.x >> 6);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) r[i] = ld1(p, stride, n, i);
+    for (int i = 0; i < kPer; ++i) {
+      const int idx = (int)threadIdx.x + NT * i, row = idx / kUnits, u = lin_unit<kUnits>(row, idx % kUnits);
+      const int r = row < n ? row : n - 1;
+      lds_load16(p, (uint32_t)(r * stride + u * (16 / (int)sizeof(E))) * (uint32_t)sizeof(E), at + 16 * NT * i);
+    }
   }
-  __device__ __forceinline__ void store(char* t) const {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) st1(t, i, r[i]);
-  }
-  static __device__ __forceinline__ void copy(char* t, const E* p, int64_t stride, int n) {
+  // Through registers; rows from n on are 0.
+  static __device__ __forceinline__ void copy(char* t, const E* p, int stride, int n) {
     constexpr int kStep = kPer < 8 ? kPer : 8;
 #pragma unroll 1
     for (int i0 = 0; i0 < kPer; i0 += kStep) {
       uint4 x[kStep];
 #pragma unroll
-      for (int i = 0; i < kStep; ++i) x[i] = ld1(p, stride, n, i0 + i);
+      for (int i = 0; i < kStep; ++i) {
+        const int idx = (int)threadIdx.x + NT * (i0 + i), row = idx / kUnits, u = idx % kUnits;
+        x[i] = row < n ? *reinterpret_cast<const uint4*>(p + (int64_t)row * stride + u * (16 / sizeof(E)))
+                       : make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
-      for (int i = 0; i < kStep; ++i) st1(t, i0 + i, x[i]);
+      for (int i = 0; i < kStep; ++i) {
+        const int idx = (int)threadIdx.x + NT * (i0 + i), row = idx / kUnits, u = idx % kUnits;
+        *reinterpret_cast<uint4*>(t + row * D * sizeof(E) + 16 * lin_unit<kUnits>(row, u)) = x[i];
+      }
     }
   }
 };
+
+// Inclusive prefix sum of fp64 over the lanes of a wave by DPP moves (the
+// steps of wave_prefix_sum), and a lane's value in every lane.
+template <int kCtrl, int kRowMask>
+__device__ __forceinline__ double dpp_add_f64(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, kCtrl, kRowMask, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), kCtrl, kRowMask, 0xF, false);
+  return v + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double wave_prefix_f64(double v) {
+  v = dpp_add_f64<0x111, 0xF>(v);
+  v = dpp_add_f64<0x112, 0xF>(v);
+  v = dpp_add_f64<0x114, 0xF>(v);
+  v = dpp_add_f64<0x118, 0xF>(v);
+  v = dpp_add_f64<0x142, 0xA>(v);
+  return dpp_add_f64<0x143, 0xC>(v);
+}
+__device__ __forceinline__ double last_lane(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ float lin_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 struct LinGates {
   float hi[kChunk], lo[kChunk];  // G_i = hi + lo
@@ -202,25 +230,21 @@ struct LinGates {
   float pad[3];
 };
 
-// One wave: the chunk's gate vectors.  The sums run in fp64 (far tokens of a
-// strongly decaying chunk differ by large G); a log decay below -1e4 has the
-// weight 0 and is held there, so that -inf leaves no NaN.
+// One wave: the chunk's gate vectors; rows from n on have no weight in the
+// state.  The sums run in fp64 (far tokens of a strongly decaying chunk differ
+// by large G); a log decay below -1e4 has the weight 0 and is held there, so
+// that -inf leaves no NaN.  Returns the chunk's sum.
 template <bool kRev>
-__device__ __forceinline__ double lin_gates(LinGates& s, float g) {
+__device__ __forceinline__ double lin_gates(LinGates& s, float g, int n) {
   const int ln = threadIdx.x & 63;
-  double G = (double)(g < -1e4f ? -1e4f : g);
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const double v = __shfl_up(G, off, 64);
-    if (ln >= off) G += v;
-  }
-  const double C = __shfl(G, 63, 64);
+  const double G = wave_prefix_f64((double)(g < -1e4f ? -1e4f : g));
+  const double C = last_lane(G);
   const float hi = (float)G;
   s.hi[ln] = hi;
   s.lo[ln] = (float)(G - (double)hi);
   const float a = expf(hi), b = expf((float)(C - G));
   s.in[ln] = kRev ? b : a;
-  s.out[ln] = kRev ? a : b;
+  s.out[ln] = ln < n ? (kRev ? a : b) : 0.0f;
   if (ln == 63) s.decay = a;
   return C;
 }
@@ -248,23 +272,29 @@ struct LinLds {
   using E = typename Eng::E;
   static constexpr bool kOut = MODE != kLinStF && MODE != kLinStR;
   static constexpr bool kDots = MODE == kLinDQ || MODE == kLinDK;
+  static constexpr bool kDirect = sizeof(E) == 2;
   static constexpr int kFrag = 64 * (sizeof(E) == 2 ? 16 : 32);
+  static constexpr int kVTiles = kDirect && !kOut ? 2 : 1;
   static constexpr int K = 0;
-  static constexpr int V = K + LinTile<E, CK>::kBytes;
-  static constexpr int Q = V + LinTile<E, CV>::kBytes;
+  static constexpr int V = K + (kDirect ? 2 : 1) * LinTile<E, CK>::kBytes;
+  static constexpr int Q = V + kVTiles * LinTile<E, CV>::kBytes;
   static constexpr int P = Q + (kOut ? LinTile<E, CK>::kBytes : 0);
-  static constexpr int G = P + (kOut ? 8 * Eng::kPlanes * kFrag : 0);
+  static constexpr int G = P + (kOut ? 6 * Eng::kPlanes * kFrag : 0);
   static constexpr int R = G + 2 * (int)sizeof(LinGates);
   static constexpr int M = R + (kDots ? (CV / 32) * kChunk * 4 : 0);
-  static constexpr int Y = M + (MODE == kLinDK ? 5 * kChunk * 4 : 0);
+  static constexpr int Y = M + (MODE == kLinDK ? (10 * 16 + kChunk) * 4 : 0);
   static constexpr int kBytes = Y + (MODE == kLinDK ? 32 : 0);
 };
 
-__device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+// The six 16 x 32 blocks of P (row tile rt, k-block kb) inside the triangle,
+// and the ten 16 x 16 tiles (a, b >= a) of the reverse one.
+template <bool kRev>
+__host__ __device__ constexpr bool lin_has(int rt, int kb) { return kRev ? 2 * kb + 1 >= rt : 2 * kb <= rt; }
+template <bool kRev>
+__host__ __device__ constexpr int lin_block(int rt, int kb) {
+  return kRev ? (rt < 2 ? 2 * rt + kb : 2 + rt) : (rt < 2 ? rt : 2 * rt - 2 + kb);
 }
+__host__ __device__ constexpr int lin_tri(int a, int b) { return 4 * a - a * (a - 1) / 2 + b - a; }
 
 template <class Eng, int CK, int CV, int MODE>
 __global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(LinScan A) {
@@ -273,21 +303,30 @@ __global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(L
   using Lds = LinLds<Eng, CK, CV, MODE>;
   using TK = LinTile<E, CK>;
   using TV = LinTile<E, CV>;
-  constexpr bool kOut = Lds::kOut, kDots = Lds::kDots;
+  constexpr bool kOut = Lds::kOut, kDots = Lds::kDots, kDirect = Lds::kDirect;
   constexpr bool kRev = MODE == kLinStR || MODE == kLinDV || MODE == kLinDK;
   constexpr bool kXT = !kDots;             // X rows are key channels (else value rows)
-  constexpr bool kThree = kDots;           // X in three planes: its product enters dg
+  constexpr int kXPlanes = Eng::kSplit ? (kDots ? 3 : 2) : 1;   // three where X's product enters dg
+  constexpr int kVPlanes = Eng::kSplit ? 3 : 1;
   constexpr int NT = 2 * CV, NW = NT / 64;
   constexpr int RT = CK / 16;              // row tiles of X
+  // the wave with the fewest pair tiles forms the next gates, and dg
+  constexpr int kGateWave = kRev ? NW - 1 : 0;
+  using RowsK = LinRows<E, CK, NT>;
+  using RowsV = LinRows<E, CV, NT>;
 
   extern __shared__ char smem[];
   LinGates* sG = reinterpret_cast<LinGates*>(smem + Lds::G);
+  float* sR = reinterpret_cast<float*>(smem + Lds::R);
+  float* sM = reinterpret_cast<float*>(smem + Lds::M);
+  double* sY = reinterpret_cast<double*>(smem + Lds::Y);
+  const uint32_t lds0 = lds_base_u32(smem);
 
   const int slot = blockIdx.x / A.VH, vh = blockIdx.x % A.VH;
   const LinSeg sg = lin_find(A.cu, A.N, A.T, A.seglen, slot, false);
   if (A.status != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *A.status = sg.bad ? kStatusBadIndex : 0;
   if (sg.bad) return;
-  const int tid = threadIdx.x, w = tid >> 6, ln = tid & 15, gq = (tid >> 4) & 3;
+  const int tid = threadIdx.x, w = uniform(tid >> 6), l64 = tid & 63, ln = tid & 15, gq = (tid >> 4) & 3;
   const int64_t sv = (int64_t)slot * A.VH + vh;
   if (sg.n < 0) {
     if (MODE == kLinDK && A.dg_part != nullptr && tid == 0) A.dg_part[sv] = 0.0;
@@ -306,6 +345,22 @@ __global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(L
   const E* pE = kDots ? (const E*)A.E + t0 * A.es + (int64_t)(vh / A.ed) * CV : nullptr;
   const float* pg = A.g + t0 * A.g_row + vh / A.tiles;
 
+  const int nch = (sg.len + kChunk - 1) / kChunk;
+  auto chunk_of = [&](int it) { return kRev ? nch - 1 - it : it; };
+  auto rows_of = [&](int c) { const int n = sg.len - kChunk * c; return n < kChunk ? n : kChunk; };
+  auto gate_of = [&](int it) -> float {
+    const int c = chunk_of(it);
+    return it < nch && l64 < rows_of(c) ? pg[((int64_t)kChunk * c + l64) * A.g_row] : 0.0f;
+  };
+  // the rows of walk step it: K into its tile, V and Q into theirs
+  auto ask = [&](int it) {
+    const int c = chunk_of(it), n = rows_of(c);
+    const int64_t r0 = (int64_t)kChunk * c;
+    RowsK::ask(lds0 + Lds::K + (it & 1) * TK::kBytes, pK + r0 * A.ks, A.ks, n);
+    RowsV::ask(lds0 + Lds::V + (kOut ? 0 : (it & 1) * TV::kBytes), pV + r0 * A.vs, A.vs, n);
+    if constexpr (kOut) RowsK::ask(lds0 + Lds::Q, pQ + r0 * A.qs, A.qs, n);
+  };
+
   // X: tile tr holds rows dkmap(16 tr + 4 gq + r), column tile t the column
   // 32 w + 8 (ln / 4) + 4 t + ln % 4
   f32x4 X[RT][2];
@@ -314,6 +369,13 @@ __global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(L
     const int row = 32 * (tr / 2) + 8 * gq + 4 * (tr & 1) + r, colx = 32 * w + 8 * (ln >> 2) + 4 * t + (ln & 3);
     return kXT ? (int64_t)colx * CK + row : (int64_t)row * CV + colx;
   };
+  float rg = 0.0f;                         // gate wave: the next step's log decays
+  double Gsum = 0.0;                       // and the segment's sum
+  if (w == kGateWave && nch > 0) {
+    Gsum += lin_gates<kRev>(sG[0], gate_of(0), rows_of(chunk_of(0)));
+    rg = gate_of(1);
+  }
+  if (kDirect && nch > 0) ask(0);
   {
     const float* p = nullptr;
     if (kOut) {
@@ -335,51 +397,32 @@ __global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(L
         X[tr][t] = x;
       }
   }
+  double Y = 0.0, dg_sum = 0.0;            // DK, gate wave
 
-  const int nch = (sg.len + kChunk - 1) / kChunk;
-  auto rows_of = [&](int c) { const int n = sg.len - kChunk * c; return n < kChunk ? n : kChunk; };
-  constexpr bool kPre = sizeof(E) == 2;
-  LinRows<E, CK, NT> rK;
-  LinRows<E, CV, NT> rV;
-  LinRows<E, CK, NT> rQ;
-  float rg = 0.0f;
-  auto fetch = [&](int c) {
-    const int n = rows_of(c);
-    const int64_t r0 = (int64_t)kChunk * c;
-    if constexpr (kPre) {
-      rK.load(pK + r0 * A.ks, A.ks, n);
-      rV.load(pV + r0 * A.vs, A.vs, n);
-      if constexpr (kOut) rQ.load(pQ + r0 * A.qs, A.qs, n);
-    }
-    if (w == 0) rg = (tid & 63) < n ? pg[(r0 + (tid & 63)) * A.g_row] : 0.0f;
-  };
-
-  double Gsum = 0.0;                       // wave 0: sum of the segment's log decays
-  double Y = 0.0, dg_sum = 0.0;            // DK, wave 0
-  if (nch > 0) {
-    fetch(kRev ? nch - 1 : 0);
-    if (w == 0) Gsum += lin_gates<kRev>(sG[0], rg);
-  }
 #pragma unroll 1
   for (int it = 0; it < nch; ++it) {
-    const int c = kRev ? nch - 1 - it : it, n = rows_of(c);
+    const int c = chunk_of(it), n = rows_of(c);
     const int64_t r0 = (int64_t)kChunk * c;
     const LinGates& g = sG[it & 1];
-    if constexpr (kPre) {
-      rK.store(smem + Lds::K);
-      rV.store(smem + Lds::V);
-      if constexpr (kOut) rQ.store(smem + Lds::Q);
+    const bool anchor = c % kAnchor == kAnchor - 1 || c == nch - 1;
+    const char* sK = smem + Lds::K + (kDirect ? (it & 1) * TK::kBytes : 0);
+    const char* sV = smem + Lds::V + (kDirect && !kOut ? (it & 1) * TV::kBytes : 0);
+    const char* sQ = smem + Lds::Q;
+    if constexpr (kDirect) {
+      wait_vmem();
+      barrier_lds();
+      if (!kOut && it + 1 < nch) ask(it + 1);
     } else {
-      LinRows<E, CK, NT>::copy(smem + Lds::K, pK + r0 * A.ks, A.ks, n);
-      LinRows<E, CV, NT>::copy(smem + Lds::V, pV + r0 * A.vs, A.vs, n);
-      if constexpr (kOut) LinRows<E, CK, NT>::copy(smem + Lds::Q, pQ + r0 * A.qs, A.qs, n);
+      RowsK::copy(smem + Lds::K, pK + r0 * A.ks, A.ks, n);
+      RowsV::copy(smem + Lds::V, pV + r0 * A.vs, A.vs, n);
+      if constexpr (kOut) RowsK::copy(smem + Lds::Q, pQ + r0 * A.qs, A.qs, n);
+      __syncthreads();
     }
-    __syncthreads();
-    if (it + 1 < nch) fetch(kRev ? c - 1 : c + 1);
-
-    // DK: Y = <S, dS> at the chunk's end, anew from the stored state of its group
+    float rdot = 0.0f;
     if constexpr (MODE == kLinDK) {
-      if (c % kAnchor == kAnchor - 1 || c == nch - 1) {
+      if (w == kGateWave && l64 < n) rdot = A.rdot[(t0 + r0 + l64) * A.VH + vh];
+      // Y = <S, dS> at the chunk's end, anew from the stored state of its group
+      if (anchor) {
         const f32x4* d = reinterpret_cast<const f32x4*>(A.dump) +
                          (dump0 + (c / kAnchor) * (int64_t)A.VH) * (CK * CV / 4) + tid;
         double y = 0.0;
@@ -391,12 +434,11 @@ __global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(L
 #pragma unroll
             for (int r = 0; r < 4; ++r) y = fma((double)s[r], (double)X[tr][t][r], y);
           }
-        y = wave_sum_f64(y);
-        if ((tid & 63) == 0) reinterpret_cast<double*>(smem + Lds::Y)[w] = y;
+        y = last_lane(wave_prefix_f64(y));
+        if (l64 == 0) sY[w] = y;
       }
     }
 
-    f32x4 O[4][2];
     if constexpr (kOut) {
       // ---- pair products of row blocks a (this wave's) and b, weighted
 #pragma unroll
@@ -405,44 +447,32 @@ __global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(L
         const float ah = g.hi[16 * a + ln], al = g.lo[16 * a + ln];
         Fr qf[CK / 32];
 #pragma unroll
-        for (int p = 0; p < CK / 32; ++p) qf[p] = TK::template row8<Eng>(smem + Lds::Q, 16 * a + ln, 32 * p + 8 * gq);
+        for (int p = 0; p < CK / 32; ++p) qf[p] = TK::template row8<Eng>(sQ, 16 * a + ln, 32 * p + 8 * gq);
         Fr ef[MODE == kLinDK ? CV / 32 : 1];
         float cm = 0.0f;                   // DK: column sums of M
         if constexpr (MODE == kLinDK) {
           const int row = 16 * a + ln;
+          const E* e = pE + (r0 + (row < n ? row : n - 1)) * A.es + 8 * gq;
 #pragma unroll
-          for (int p = 0; p < CV / 32; ++p) {
-            const E* e = pE + (r0 + (row < n ? row : 0)) * A.es + 32 * p + 8 * gq;
-            ef[p] = Eng::ld(e);
-          }
+          for (int p = 0; p < CV / 32; ++p) ef[p] = Eng::ld(e + 32 * p);
         }
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-          if (kRev ? 2 * kb + 1 < a : 2 * kb > a) {
-            if constexpr (MODE == kLinDK) {
-              if (ln == 0) {
-#pragma unroll
-                for (int bb = 0; bb < 2; ++bb)
-#pragma unroll
-                  for (int r = 0; r < 4; ++r)
-                    reinterpret_cast<float*>(smem + Lds::M)[64 * a + 16 * (2 * kb + bb) + 4 * gq + r] = 0.0f;
-              }
-            }
-            continue;
-          }
+          if (!lin_has<kRev>(a, kb)) continue;
           float pw[8];
 #pragma unroll
           for (int bb = 0; bb < 2; ++bb) {
             const int b = 2 * kb + bb;
             f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f}, acc2 = acc;
-            if (kRev ? b >= a : b <= a) {
+            const bool in = kRev ? b >= a : b <= a;
+            if (in) {
 #pragma unroll
               for (int p = 0; p < CK / 32; ++p)
-                Eng::mma(acc, TK::template row8<Eng>(smem + Lds::K, 16 * b + ln, 32 * p + 8 * gq), qf[p]);
+                Eng::mma(acc, TK::template row8<Eng>(sK, 16 * b + ln, 32 * p + 8 * gq), qf[p]);
               if constexpr (MODE == kLinDK) {
 #pragma unroll
                 for (int p = 0; p < CV / 32; ++p)
-                  Eng::mma(acc2, TV::template row8<Eng>(smem + Lds::V, 16 * b + ln, 32 * p + 8 * gq), ef[p]);
+                  Eng::mma(acc2, TV::template row8<Eng>(sV, 16 * b + ln, 32 * p + 8 * gq), ef[p]);
               }
             }
             const f32x4 bh = *reinterpret_cast<const f32x4*>(&g.hi[16 * b + 4 * gq]);
@@ -451,64 +481,62 @@ __global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(L
             for (int r = 0; r < 4; ++r) {
               const int ia = 16 * a + ln, ib = 16 * b + 4 * gq + r;
               const float d = kRev ? (bh[r] - ah) + (bl[r] - al) : (ah - bh[r]) + (al - bl[r]);
-              const float wt = (kRev ? ib >= ia : ib <= ia) ? expf(d) : 0.0f;
-              pw[4 * bb + r] = acc[r] * wt;
+              pw[4 * bb + r] = (kRev ? ib >= ia && ib < n : ib <= ia) ? acc[r] * lin_exp(d) : 0.0f;
               if constexpr (MODE == kLinDK) {
                 const float m = ib > ia ? acc2[r] * pw[4 * bb + r] : 0.0f;
                 cm += m;
                 const float rm = group_sum<16>(m);
-                if (ln == 0) reinterpret_cast<float*>(smem + Lds::M)[64 * a + ib] = rm;
+                if (in && ln == 0) sM[16 * lin_tri(a, b) + 4 * gq + r] = rm;
               }
             }
           }
-          Fr hi, lo;
-          Eng::split(pw, hi, lo);
-          char* dst = smem + Lds::P + (2 * a + kb) * Eng::kPlanes * Lds::kFrag + (tid & 63) * (Lds::kFrag / 64);
-          Eng::st((E*)dst, hi);
-          if constexpr (Eng::kPlanes == 2) Eng::st((E*)(dst + Lds::kFrag), lo);
+          Fr pl[2];
+          Eng::split(pw, pl[0], pl[1]);
+          char* dst = smem + Lds::P + lin_block<kRev>(a, kb) * Eng::kPlanes * Lds::kFrag + l64 * (Lds::kFrag / 64);
+#pragma unroll
+          for (int k = 0; k < Eng::kPlanes; ++k) Eng::st((E*)(dst + k * Lds::kFrag), pl[k]);
         }
         if constexpr (MODE == kLinDK) {
           cm += __shfl_xor(cm, 16, 64);
           cm += __shfl_xor(cm, 32, 64);
-          if (gq == 0) reinterpret_cast<float*>(smem + Lds::M)[256 + 16 * a + ln] = cm;
+          if (gq == 0) sM[160 + 16 * a + ln] = cm;
         }
       }
     }
-    if (it + 1 < nch && w == 0) Gsum += lin_gates<kRev>(sG[(it + 1) & 1], rg);
+    if (w == kGateWave && it + 1 < nch) {
+      Gsum += lin_gates<kRev>(sG[(it + 1) & 1], rg, rows_of(chunk_of(it + 1)));
+      rg = gate_of(it + 2);
+    }
 
     Fr vf[2][2];                           // V^T fragments of this wave's columns
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-        vf[t][kb] = TV::template cols8<Eng>(smem + Lds::V, kb, 32 * w + 4 * t, ln, gq);
+      for (int kb = 0; kb < 2; ++kb) vf[t][kb] = TV::template cols8<Eng>(sV, kb, 32 * w + 4 * t, ln, gq);
 
     if constexpr (kOut) {
       // ---- state part: O^T = X^T Q^T, scaled by the rows' weights
+      f32x4 O[4][2];
 #pragma unroll
       for (int rt = 0; rt < 4; ++rt) O[rt][0] = O[rt][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int p = 0; p < CK / 32; ++p) {
-        Fr xh[2], xm[2], xl[2];
+        Fr xf[2][3], qf[4];
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) qf[rt] = TK::template row8<Eng>(sQ, 16 * rt + ln, 32 * p + 8 * gq);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const float x8[8] = {X[2 * p][t][0], X[2 * p][t][1], X[2 * p][t][2], X[2 * p][t][3],
                                X[2 * p + 1][t][0], X[2 * p + 1][t][1], X[2 * p + 1][t][2], X[2 * p + 1][t][3]};
-          if constexpr (kThree) Eng::split3(x8, xh[t], xm[t], xl[t]);
-          else Eng::split(x8, xh[t], xm[t]);
+          if constexpr (kXPlanes == 3) Eng::split3(x8, xf[t][0], xf[t][1], xf[t][2]);
+          else Eng::split(x8, xf[t][0], xf[t][1]);
         }
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          const Fr qf = TK::template row8<Eng>(smem + Lds::Q, 16 * rt + ln, 32 * p + 8 * gq);
+        for (int k = 0; k < kXPlanes; ++k)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            Eng::mma(O[rt][t], xh[t], qf);
-            if constexpr (Eng::kSplit) {
-              Eng::mma(O[rt][t], xm[t], qf);
-              if constexpr (kThree) Eng::mma(O[rt][t], xl[t], qf);
-            }
-          }
-        }
+          for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) Eng::mma(O[rt][t], xf[t][k], qf[rt]);
       }
 #pragma unroll
       for (int rt = 0; rt < 4; ++rt) {
@@ -522,35 +550,33 @@ __global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(L
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
           const int row = 16 * rt + ln;
-          const E* e = pE + (r0 + (row < n ? row : 0)) * A.es + 32 * w + 8 * gq;
           float d = 0.0f, ev[8];
-          ld8(e, ev);
+          ld8(pE + (r0 + (row < n ? row : n - 1)) * A.es + 32 * w + 8 * gq, ev);
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) d = fmaf(O[rt][t][r], ev[4 * t + r], d);
           d += __shfl_xor(d, 16, 64);
           d += __shfl_xor(d, 32, 64);
-          if (gq == 0) reinterpret_cast<float*>(smem + Lds::R)[kChunk * w + row] = row < n ? d : 0.0f;
+          if (gq == 0) sR[kChunk * w + row] = row < n ? d : 0.0f;
         }
+        asm volatile("" ::"v"(rdot));      // its load ends before the next chunk's are asked for
       }
-      __syncthreads();
+      barrier_lds();
+      if (kDirect && it + 1 < nch) ask(it + 1);
       // ---- pair part: O^T += V^T P^T
 #pragma unroll
-      for (int rt = 0; rt < 4; ++rt)
+      for (int k = 0; k < Eng::kPlanes; ++k)
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          if (kRev ? 2 * kb + 1 < rt : 2 * kb > rt) continue;
-          const char* src = smem + Lds::P + (2 * rt + kb) * Eng::kPlanes * Lds::kFrag + (tid & 63) * (Lds::kFrag / 64);
-          const Fr ph = Eng::ld((const E*)src);
+        for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) Eng::mma(O[rt][t], vf[t][kb], ph);
-          if constexpr (Eng::kPlanes == 2) {
-            const Fr pl = Eng::ld((const E*)(src + Lds::kFrag));
+          for (int rt = 0; rt < 4; ++rt) {
+            if (!lin_has<kRev>(rt, kb)) continue;
+            const Fr pf = Eng::ld((const E*)(smem + Lds::P + (lin_block<kRev>(rt, kb) * Eng::kPlanes + k) * Lds::kFrag +
+                                             l64 * (Lds::kFrag / 64)));
 #pragma unroll
-            for (int t = 0; t < 2; ++t) Eng::mma(O[rt][t], vf[t][kb], pl);
+            for (int t = 0; t < 2; ++t) Eng::mma(O[rt][t], vf[t][kb], pf);
           }
-        }
 #pragma unroll
       for (int rt = 0; rt < 4; ++rt) {
         const int row = 16 * rt + ln;
@@ -568,38 +594,29 @@ __global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(L
         }
       }
       if constexpr (kDots) {
-        if (w == 0) {
-          const int t = tid & 63;
+        if (w == kGateWave) {
           float d = 0.0f;
 #pragma unroll
-          for (int k = 0; k < NW; ++k) d += reinterpret_cast<const float*>(smem + Lds::R)[kChunk * k + t];
-          const int64_t at = (t0 + r0 + t) * A.VH + vh;
+          for (int k = 0; k < NW; ++k) d += sR[kChunk * k + l64];
+          const int64_t at = (t0 + r0 + l64) * A.VH + vh;
           if constexpr (MODE == kLinDQ) {
-            if (t < n) A.rdot[at] = d;
+            if (l64 < n) A.rdot[at] = d;
           } else {
-            const float* sM = reinterpret_cast<const float*>(smem + Lds::M);
-            if (c % kAnchor == kAnchor - 1 || c == nch - 1) {
-              const double* sY = reinterpret_cast<const double*>(smem + Lds::Y);
+            if (anchor) {
               Y = sY[0];
 #pragma unroll
               for (int k = 1; k < NW; ++k) Y += sY[k];
             }
-            const double r = t < n ? (double)A.rdot[at] : 0.0;
             double rm = 0.0;               // row sum of M, over the column blocks
 #pragma unroll
-            for (int a = 0; a < 4; ++a) rm += (double)sM[64 * a + t];
-            double suf = rm + r - (double)sM[256 + t], pre = (double)d;
-#pragma unroll
-            for (int off = 1; off < 64; off <<= 1) {
-              const double u = __shfl_down(suf, off, 64), v = __shfl_up(pre, off, 64);
-              if (t + off < 64) suf += u;
-              if (t >= off) pre += v;
-            }
-            const double csum = __shfl(pre, 63, 64);
-            const double Xc = Y - csum;
-            const double dg = suf + (pre - (double)d) + Xc;
-            Y = Xc + wave_sum_f64(r);
-            if (t < n) {
+            for (int a = 0; a < 4; ++a)
+              if (a <= (l64 >> 4)) rm += (double)sM[16 * lin_tri(a, l64 >> 4) + (l64 & 15)];
+            const double own = rm + (double)rdot - (double)sM[160 + l64];
+            const double head = wave_prefix_f64(own), pre = wave_prefix_f64((double)d);
+            const double Xc = Y - last_lane(pre);
+            const double dg = (last_lane(head) - head + own) + (pre - (double)d) + Xc;
+            Y = Xc + last_lane(wave_prefix_f64((double)rdot));
+            if (l64 < n) {
               if (A.dg_tok != nullptr) A.dg_tok[at] = (float)dg;
               dg_sum += dg;
             }
@@ -620,7 +637,7 @@ __global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(L
     for (int kb = 0; kb < 2; ++kb) {
       const f32x4 w0 = *reinterpret_cast<const f32x4*>(&g.out[32 * kb + 4 * gq]);
       const f32x4 w1 = *reinterpret_cast<const f32x4*>(&g.out[32 * kb + 16 + 4 * gq]);
-      Fr vh_[2], vm[2], vl[2];
+      Fr wv[2][3];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         float x8[8];
@@ -634,23 +651,25 @@ __global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(L
 #pragma unroll
           for (int j = 0; j < 8; ++j) x8[j] = vf[t][kb].v[j] * (j < 4 ? w0[j] : w1[j & 3]);
         }
-        Eng::split3(x8, vh_[t], vm[t], vl[t]);
+        Eng::split3(x8, wv[t][0], wv[t][1], wv[t][2]);
       }
+      constexpr int kStep = 4;             // row tiles whose products alternate
 #pragma unroll
-      for (int tr = 0; tr < RT; ++tr) {
-        const Fr kf = TK::template cols8<Eng>(smem + Lds::K, kb, 32 * (tr / 2) + 4 * (tr & 1), ln, gq);
+      for (int tr0 = 0; tr0 < RT; tr0 += kStep) {
+        Fr kf[kStep];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          Eng::mma(X[tr][t], kf, vh_[t]);
-          if constexpr (Eng::kSplit) {
-            Eng::mma(X[tr][t], kf, vm[t]);
-            Eng::mma(X[tr][t], kf, vl[t]);
-          }
-        }
+        for (int i = 0; i < kStep; ++i)
+          kf[i] = TK::template cols8<Eng>(sK, kb, 32 * ((tr0 + i) / 2) + 4 * (i & 1), ln, gq);
+#pragma unroll
+        for (int k = 0; k < kVPlanes; ++k)
+#pragma unroll
+          for (int i = 0; i < kStep; ++i)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) Eng::mma(X[tr0 + i][t], kf[i], wv[t][k]);
       }
     }
     if constexpr (MODE == kLinDQ) {
-      if (c % kAnchor == kAnchor - 1 || c == nch - 1) {
+      if (anchor) {
         f32x4* d = reinterpret_cast<f32x4*>(A.dump) + (dump0 + (c / kAnchor) * (int64_t)A.VH) * (CK * CV / 4) + tid;
 #pragma unroll
         for (int tr = 0; tr < RT; ++tr)
@@ -658,7 +677,7 @@ __global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(L
           for (int t = 0; t < 2; ++t) d[(2 * tr + t) * NT] = X[tr][t];
       }
     }
-    __syncthreads();
+    if constexpr (!kDirect) __syncthreads();
   }
 
   // ---- the state after the walk
@@ -677,11 +696,11 @@ __global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(L
         }
       }
   }
-  if (!kOut && tid == 0) A.seg_decay[sv] = expf((float)Gsum);
+  if (!kOut && w == kGateWave && l64 == 0) A.seg_decay[sv] = expf((float)Gsum);
   if constexpr (MODE == kLinDK) {
-    if (A.dg_part != nullptr && w == 0) {
-      const double s = wave_sum_f64(dg_sum);
-      if (tid == 0) A.dg_part[sv] = s;
+    if (A.dg_part != nullptr && w == kGateWave) {
+      const double s = last_lane(wave_prefix_f64(dg_sum));
+      if (l64 == 0) A.dg_part[sv] = s;
     }
   }
 }
