@@ -259,7 +259,6 @@ hipError_t launch_lin_fwd(const gdn_lin_t& s, const void* q, const void* k, cons
   A.last = final_state;
   A.out = o;
   A.os = vv;
-  A.od = 1;
   return run_scan(s, A, kLinO, L, stream);
 }
 
@@ -302,42 +301,35 @@ hipError_t launch_lin_bwd(const gdn_lin_t& s, const void* q, const void* k, cons
     A.rdot = L.rdot;
     A.out = sum ? (void*)L.part_q : dq;
     A.os = qrow;
-    A.od = 1;
     A.out_f32 = sum;
     GDN_TRY(run_scan(s, A, kLinDQ, L, stream));
     B.status = nullptr;
   }
-  {
-    LinScan A = B;   // dv = reverse pass of (k, q, do)
-    set_q(A, ok);
-    set_k(A, oq);
-    set_v(A, od);
-    A.seg = L.segR;
-    A.first = d_final_state;
-    A.last = d_initial_state;
-    A.out = d_v;
-    A.os = vv;
-    A.od = 1;
-    GDN_TRY(run_scan(s, A, kLinDV, L, stream));
-  }
-  {
-    LinScan A = B;   // dk = reverse pass of (v, do, q)
-    set_q(A, ov);
-    set_k(A, od);
-    set_v(A, oq);
-    set_e(A, ok);
-    A.seg = L.segR;
-    A.first = d_final_state;
-    A.dump = L.dump;
-    A.rdot = L.rdot;
-    A.out = sum ? (void*)L.part_k : dk;
-    A.os = qrow;
-    A.od = 1;
-    A.out_f32 = sum;
-    if (s.gate_per_token) A.dg_tok = L.tiles > 1 ? L.dgt : dg;
-    else A.dg_part = L.dgp;
-    GDN_TRY(run_scan(s, A, kLinDK, L, stream));
-  }
+  LinScan V = B;     // dv = reverse pass of (k, q, do)
+  set_q(V, ok);
+  set_k(V, oq);
+  set_v(V, od);
+  V.seg = L.segR;
+  V.first = d_final_state;
+  V.last = d_initial_state;
+  V.out = d_v;
+  V.os = vv;
+  LinScan K = B;     // dk = reverse pass of (v, do, q)
+  set_q(K, ov);
+  set_k(K, od);
+  set_v(K, oq);
+  set_e(K, ok);
+  K.seg = L.segR;
+  K.first = d_final_state;
+  K.dump = L.dump;
+  K.rdot = L.rdot;
+  K.out = sum ? (void*)L.part_k : dk;
+  K.os = qrow;
+  K.out_f32 = sum;
+  if (s.gate_per_token) K.dg_tok = L.tiles > 1 ? L.dgt : dg;
+  else K.dg_part = L.dgp;
+  GDN_TRY(s.io_dtype == GDN_BF16 ? launch_lin_rev_bf16(K, V, L.slots, stream)
+                                 : launch_lin_rev_f32(K, V, L.slots, stream));
   if (sum && s.total_tokens > 0) {
     const int d4 = s.dk / 4;
     const int64_t row4 = (int64_t)s.qk_heads * d4;

@@ -5,7 +5,7 @@
 
 namespace gdn {
 
-// The passes of the scan kernel (see gdn_lin_scan.hpp).
+// The passes of the scan (see gdn_lin_scan.hpp); kLinDV and kLinDK run together.
 enum LinMode : int { kLinO = 0, kLinStF = 1, kLinDQ = 2, kLinStR = 3, kLinDV = 4, kLinDK = 5 };
 
 constexpr int kAnchor = 4;  // chunks between two stored states of the backward
@@ -29,7 +29,7 @@ struct LinScan {
   double* dg_part;        // DK: [slot][VH] sums over the segment's tokens, or null
   int32_t* status;        // written by the first kernel of a call, read by its reduction
   int qs, ks, vs, es, os; // row strides (elements)
-  int qd, kd, vd, ed, od; // head of operand X = virtual head / xd
+  int qd, kd, vd, ed;     // head of operand X = virtual head / xd
   int64_t g_row;          // gate row stride: n_heads, or 0
   int VH, tiles, dk, tw;
   int N, seglen;
@@ -39,5 +39,8 @@ struct LinScan {
 
 hipError_t launch_lin_scan_bf16(const LinScan& A, LinMode mode, int64_t slots, hipStream_t stream);
 hipError_t launch_lin_scan_f32(const LinScan& A, LinMode mode, int64_t slots, hipStream_t stream);
+// The reverse passes together: A the dk pass, B the dv pass.
+hipError_t launch_lin_rev_bf16(const LinScan& A, const LinScan& B, int64_t slots, hipStream_t stream);
+hipError_t launch_lin_rev_f32(const LinScan& A, const LinScan& B, int64_t slots, hipStream_t stream);
 
 }  // namespace gdn

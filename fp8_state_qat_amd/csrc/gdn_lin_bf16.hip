@@ -7,9 +7,10 @@ hipError_t launch_lin_scan_bf16(const LinScan& A, LinMode mode, int64_t slots, h
     case kLinO: return lin_scan_mode<EngBF16, kLinO>(A, slots, stream);
     case kLinStF: return lin_scan_mode<EngBF16, kLinStF>(A, slots, stream);
     case kLinDQ: return lin_scan_mode<EngBF16, kLinDQ>(A, slots, stream);
-    case kLinStR: return lin_scan_mode<EngBF16, kLinStR>(A, slots, stream);
-    case kLinDV: return lin_scan_mode<EngBF16, kLinDV>(A, slots, stream);
-    default: return lin_scan_mode<EngBF16, kLinDK>(A, slots, stream);
+    default: return lin_scan_mode<EngBF16, kLinStR>(A, slots, stream);
   }
+}
+hipError_t launch_lin_rev_bf16(const LinScan& A, const LinScan& B, int64_t slots, hipStream_t stream) {
+  return lin_rev<EngBF16>(A, B, slots, stream);
 }
 }  // namespace gdn

@@ -160,11 +160,14 @@ struct LinTile {
   }
 };
 
-// Rows of a chunk into a tile; NT threads.
+// Rows of a chunk into a tile; NT threads (whole waves drop out of the last
+// step where the units do not divide).
 template <typename E, int D, int NT>
 struct LinRows {
   static constexpr int kUnits = D * (int)sizeof(E) / 16;
-  static constexpr int kPer = kChunk * kUnits / NT;
+  static constexpr int kAll = kChunk * kUnits;
+  static constexpr int kPer = (kAll + NT - 1) / NT;
+  static_assert(kAll % 64 == 0, "whole waves");
   // Asked for and on the way (wait_vmem, then a barrier): rows from n on are
   // copies of the last valid one, which no result takes in.
   static __device__ __forceinline__ void ask(uint32_t lds, const E* p, int stride, int n) {
@@ -172,6 +175,7 @@ struct LinRows {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int idx = (int)threadIdx.x + NT * i, row = idx / kUnits, u = lin_unit<kUnits>(row, idx % kUnits);
+      if (kAll % NT != 0 && uniform(idx) >= kAll) break;
       const int r = row < n ? row : n - 1;
       lds_load16(p, (uint32_t)(r * stride + u * (16 / (int)sizeof(E))) * (uint32_t)sizeof(E), at + 16 * NT * i);
     }
@@ -179,6 +183,7 @@ struct LinRows {
   // Through registers; rows from n on are 0.
   static __device__ __forceinline__ void copy(char* t, const E* p, int stride, int n) {
     constexpr int kStep = kPer < 8 ? kPer : 8;
+    static_assert(kPer % kStep == 0, "whole steps");
 #pragma unroll 1
     for (int i0 = 0; i0 < kPer; i0 += kStep) {
       uint4 x[kStep];
@@ -191,6 +196,7 @@ struct LinRows {
 #pragma unroll
       for (int i = 0; i < kStep; ++i) {
         const int idx = (int)threadIdx.x + NT * (i0 + i), row = idx / kUnits, u = idx % kUnits;
+        if (kAll % NT != 0 && idx >= kAll) break;
         *reinterpret_cast<uint4*>(t + row * D * sizeof(E) + 16 * lin_unit<kUnits>(row, u)) = x[i];
       }
     }
@@ -267,25 +273,6 @@ __device__ __forceinline__ void ld8(const float* p, float (&x)[8]) {
   }
 }
 
-template <class Eng, int CK, int CV, int MODE>
-struct LinLds {
-  using E = typename Eng::E;
-  static constexpr bool kOut = MODE != kLinStF && MODE != kLinStR;
-  static constexpr bool kDots = MODE == kLinDQ || MODE == kLinDK;
-  static constexpr bool kDirect = sizeof(E) == 2;
-  static constexpr int kFrag = 64 * (sizeof(E) == 2 ? 16 : 32);
-  static constexpr int kVTiles = kDirect && !kOut ? 2 : 1;
-  static constexpr int K = 0;
-  static constexpr int V = K + (kDirect ? 2 : 1) * LinTile<E, CK>::kBytes;
-  static constexpr int Q = V + kVTiles * LinTile<E, CV>::kBytes;
-  static constexpr int P = Q + (kOut ? LinTile<E, CK>::kBytes : 0);
-  static constexpr int G = P + (kOut ? 6 * Eng::kPlanes * kFrag : 0);
-  static constexpr int R = G + 2 * (int)sizeof(LinGates);
-  static constexpr int M = R + (kDots ? (CV / 32) * kChunk * 4 : 0);
-  static constexpr int Y = M + (MODE == kLinDK ? (10 * 16 + kChunk) * 4 : 0);
-  static constexpr int kBytes = Y + (MODE == kLinDK ? 32 : 0);
-};
-
 // The six 16 x 32 blocks of P (row tile rt, k-block kb) inside the triangle,
 // and the ten 16 x 16 tiles (a, b >= a) of the reverse one.
 template <bool kRev>
@@ -296,91 +283,86 @@ __host__ __device__ constexpr int lin_block(int rt, int kb) {
 }
 __host__ __device__ constexpr int lin_tri(int a, int b) { return 4 * a - a * (a - 1) / 2 + b - a; }
 
+// One workgroup's place in the batch, the same for all its waves.
+struct LinPlace {
+  LinSeg sg;
+  int slot, vh, nch;
+  int64_t sv, dump0;
+  const float* pg;
+  // false: nothing to do (unused slot, bad index arrays)
+  __device__ __forceinline__ bool find(const LinScan& A) {
+    slot = blockIdx.x / A.VH;
+    vh = blockIdx.x % A.VH;
+    sg = lin_find(A.cu, A.N, A.T, A.seglen, slot, false);
+    if (A.status != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *A.status = sg.bad ? kStatusBadIndex : 0;
+    if (sg.bad) return false;
+    sv = (int64_t)slot * A.VH + vh;
+    if (sg.n < 0) return false;
+    // stored states: a segment's groups from t0 / (rows of a group) + slot on, which no two segments share
+    dump0 = ((int64_t)sg.t0 / (kAnchor * kChunk) + slot) * A.VH + vh;
+    nch = (sg.len + kChunk - 1) / kChunk;
+    pg = A.g + sg.t0 * A.g_row + vh / A.tiles;
+    return true;
+  }
+  template <bool kRev>
+  __device__ __forceinline__ int chunk(int it) const { return kRev ? nch - 1 - it : it; }
+  __device__ __forceinline__ int rows(int c) const {
+    const int n = sg.len - kChunk * c;
+    return n < kChunk ? n : kChunk;
+  }
+  // this lane's log decay of walk step it
+  template <bool kRev>
+  __device__ __forceinline__ float gate(int it, int64_t g_row) const {
+    const int c = chunk<kRev>(it), l = threadIdx.x & 63;
+    return it < nch && l < rows(c) ? pg[((int64_t)kChunk * c + l) * g_row] : 0.0f;
+  }
+};
+
+// The walk of one role (mode) by its CV / 32 waves: X and the pieces of a
+// chunk's work.  w: the wave's index in the role.
 template <class Eng, int CK, int CV, int MODE>
-__global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(LinScan A) {
+struct LinWalk {
   using E = typename Eng::E;
   using Fr = typename Eng::Fr;
-  using Lds = LinLds<Eng, CK, CV, MODE>;
   using TK = LinTile<E, CK>;
   using TV = LinTile<E, CV>;
-  constexpr bool kOut = Lds::kOut, kDots = Lds::kDots, kDirect = Lds::kDirect;
-  constexpr bool kRev = MODE == kLinStR || MODE == kLinDV || MODE == kLinDK;
-  constexpr bool kXT = !kDots;             // X rows are key channels (else value rows)
-  constexpr int kXPlanes = Eng::kSplit ? (kDots ? 3 : 2) : 1;   // three where X's product enters dg
-  constexpr int kVPlanes = Eng::kSplit ? 3 : 1;
-  constexpr int NT = 2 * CV, NW = NT / 64;
-  constexpr int RT = CK / 16;              // row tiles of X
-  // the wave with the fewest pair tiles forms the next gates, and dg
-  constexpr int kGateWave = kRev ? NW - 1 : 0;
-  using RowsK = LinRows<E, CK, NT>;
-  using RowsV = LinRows<E, CV, NT>;
+  static constexpr bool kOut = MODE != kLinStF && MODE != kLinStR;
+  static constexpr bool kDots = MODE == kLinDQ || MODE == kLinDK;
+  static constexpr bool kRev = MODE == kLinStR || MODE == kLinDV || MODE == kLinDK;
+  static constexpr bool kXT = !kDots;      // X rows are key channels (else value rows)
+  static constexpr int kXPlanes = Eng::kSplit ? (kDots ? 3 : 2) : 1;   // three where X's product enters dg
+  static constexpr int kVPlanes = Eng::kSplit ? 3 : 1;
+  static constexpr int NW = CV / 32, NT = 64 * NW;
+  static constexpr int RT = CK / 16;       // row tiles of X
+  static constexpr int kFrag = 64 * (sizeof(E) == 2 ? 16 : 32);
+  static constexpr int kPBytes = 6 * Eng::kPlanes * kFrag;
+  // the wave with the fewest pair tiles: it forms the next gates, and dg
+  static constexpr int kLight = kRev ? NW - 1 : 0;
 
-  extern __shared__ char smem[];
-  LinGates* sG = reinterpret_cast<LinGates*>(smem + Lds::G);
-  float* sR = reinterpret_cast<float*>(smem + Lds::R);
-  float* sM = reinterpret_cast<float*>(smem + Lds::M);
-  double* sY = reinterpret_cast<double*>(smem + Lds::Y);
-  const uint32_t lds0 = lds_base_u32(smem);
-
-  const int slot = blockIdx.x / A.VH, vh = blockIdx.x % A.VH;
-  const LinSeg sg = lin_find(A.cu, A.N, A.T, A.seglen, slot, false);
-  if (A.status != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *A.status = sg.bad ? kStatusBadIndex : 0;
-  if (sg.bad) return;
-  const int tid = threadIdx.x, w = uniform(tid >> 6), l64 = tid & 63, ln = tid & 15, gq = (tid >> 4) & 3;
-  const int64_t sv = (int64_t)slot * A.VH + vh;
-  if (sg.n < 0) {
-    if (MODE == kLinDK && A.dg_part != nullptr && tid == 0) A.dg_part[sv] = 0.0;
-    return;
-  }
-  // the state pass leaves out the segment whose sum nothing reads
-  if (MODE == kLinStF && sg.s == sg.nseg - 1) return;
-  if (MODE == kLinStR && sg.s == 0) return;
-
-  const int64_t t0 = sg.t0;
-  // stored states: a segment's groups from t0 / (rows of a group) + slot on, which no two segments share
-  const int64_t dump0 = (t0 / (kAnchor * kChunk) + slot) * A.VH + vh;
-  const E* pK = (const E*)A.K + t0 * A.ks + (int64_t)(vh / A.kd) * CK;
-  const E* pV = (const E*)A.V + t0 * A.vs + (int64_t)(vh / A.vd) * CV;
-  const E* pQ = kOut ? (const E*)A.Q + t0 * A.qs + (int64_t)(vh / A.qd) * CK : nullptr;
-  const E* pE = kDots ? (const E*)A.E + t0 * A.es + (int64_t)(vh / A.ed) * CV : nullptr;
-  const float* pg = A.g + t0 * A.g_row + vh / A.tiles;
-
-  const int nch = (sg.len + kChunk - 1) / kChunk;
-  auto chunk_of = [&](int it) { return kRev ? nch - 1 - it : it; };
-  auto rows_of = [&](int c) { const int n = sg.len - kChunk * c; return n < kChunk ? n : kChunk; };
-  auto gate_of = [&](int it) -> float {
-    const int c = chunk_of(it);
-    return it < nch && l64 < rows_of(c) ? pg[((int64_t)kChunk * c + l64) * A.g_row] : 0.0f;
-  };
-  // the rows of walk step it: K into its tile, V and Q into theirs
-  auto ask = [&](int it) {
-    const int c = chunk_of(it), n = rows_of(c);
-    const int64_t r0 = (int64_t)kChunk * c;
-    RowsK::ask(lds0 + Lds::K + (it & 1) * TK::kBytes, pK + r0 * A.ks, A.ks, n);
-    RowsV::ask(lds0 + Lds::V + (kOut ? 0 : (it & 1) * TV::kBytes), pV + r0 * A.vs, A.vs, n);
-    if constexpr (kOut) RowsK::ask(lds0 + Lds::Q, pQ + r0 * A.qs, A.qs, n);
-  };
-
+  const LinScan& A;
+  const LinPlace& L;
+  const int w, l64, ln, gq;
   // X: tile tr holds rows dkmap(16 tr + 4 gq + r), column tile t the column
   // 32 w + 8 (ln / 4) + 4 t + ln % 4
-  f32x4 X[RT][2];
-  const int64_t st_size = (int64_t)A.tw * A.dk;
-  auto st_at = [&](int tr, int t, int r) -> int64_t {
+  f32x4 X[RT][2], O[4][2];
+  Fr vf[2][2];                             // V^T fragments of this wave's columns
+  float rdot;                              // DK, light wave: this lane's r_i
+  double Y, dg_sum;
+
+  __device__ __forceinline__ LinWalk(const LinScan& a, const LinPlace& l, int wave)
+      : A(a), L(l), w(wave), l64(threadIdx.x & 63), ln(threadIdx.x & 15), gq((threadIdx.x >> 4) & 3), rdot(0.0f),
+        Y(0.0), dg_sum(0.0) {}
+
+  __device__ __forceinline__ int64_t st_at(int tr, int t, int r) const {
     const int row = 32 * (tr / 2) + 8 * gq + 4 * (tr & 1) + r, colx = 32 * w + 8 * (ln >> 2) + 4 * t + (ln & 3);
     return kXT ? (int64_t)colx * CK + row : (int64_t)row * CV + colx;
-  };
-  float rg = 0.0f;                         // gate wave: the next step's log decays
-  double Gsum = 0.0;                       // and the segment's sum
-  if (w == kGateWave && nch > 0) {
-    Gsum += lin_gates<kRev>(sG[0], gate_of(0), rows_of(chunk_of(0)));
-    rg = gate_of(1);
   }
-  if (kDirect && nch > 0) ask(0);
-  {
+  __device__ __forceinline__ void load_state() {
+    const int64_t size = (int64_t)A.tw * A.dk;
     const float* p = nullptr;
     if (kOut) {
-      if (A.seg != nullptr) p = A.seg + sv * st_size;
-      else if (A.first != nullptr) p = A.first + ((int64_t)sg.n * A.VH + vh) * st_size;
+      if (A.seg != nullptr) p = A.seg + L.sv * size;
+      else if (A.first != nullptr) p = A.first + ((int64_t)L.sg.n * A.VH + L.vh) * size;
     }
 #pragma unroll
     for (int tr = 0; tr < RT; ++tr)
@@ -397,235 +379,242 @@ __global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(L
         X[tr][t] = x;
       }
   }
-  double Y = 0.0, dg_sum = 0.0;            // DK, gate wave
-
-#pragma unroll 1
-  for (int it = 0; it < nch; ++it) {
-    const int c = chunk_of(it), n = rows_of(c);
-    const int64_t r0 = (int64_t)kChunk * c;
-    const LinGates& g = sG[it & 1];
-    const bool anchor = c % kAnchor == kAnchor - 1 || c == nch - 1;
-    const char* sK = smem + Lds::K + (kDirect ? (it & 1) * TK::kBytes : 0);
-    const char* sV = smem + Lds::V + (kDirect && !kOut ? (it & 1) * TV::kBytes : 0);
-    const char* sQ = smem + Lds::Q;
-    if constexpr (kDirect) {
-      wait_vmem();
-      barrier_lds();
-      if (!kOut && it + 1 < nch) ask(it + 1);
-    } else {
-      RowsK::copy(smem + Lds::K, pK + r0 * A.ks, A.ks, n);
-      RowsV::copy(smem + Lds::V, pV + r0 * A.vs, A.vs, n);
-      if constexpr (kOut) RowsK::copy(smem + Lds::Q, pQ + r0 * A.qs, A.qs, n);
-      __syncthreads();
-    }
-    float rdot = 0.0f;
-    if constexpr (MODE == kLinDK) {
-      if (w == kGateWave && l64 < n) rdot = A.rdot[(t0 + r0 + l64) * A.VH + vh];
-      // Y = <S, dS> at the chunk's end, anew from the stored state of its group
-      if (anchor) {
-        const f32x4* d = reinterpret_cast<const f32x4*>(A.dump) +
-                         (dump0 + (c / kAnchor) * (int64_t)A.VH) * (CK * CV / 4) + tid;
-        double y = 0.0;
+  // the state after the walk: a segment's sum, or the sequence's last state
+  __device__ __forceinline__ void store_state() const {
+    const int64_t size = (int64_t)A.tw * A.dk;
+    float* p = nullptr;
+    if (!kOut) p = A.seg + L.sv * size;
+    else if (A.last != nullptr && L.sg.s == (kRev ? 0 : L.sg.nseg - 1))
+      p = A.last + ((int64_t)L.sg.n * A.VH + L.vh) * size;
+    if (p == nullptr) return;
 #pragma unroll
-        for (int tr = 0; tr < RT; ++tr)
+    for (int tr = 0; tr < RT; ++tr)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const f32x4 s = d[(2 * tr + t) * NT];
+      for (int t = 0; t < 2; ++t) {
+        if constexpr (kXT) *reinterpret_cast<f32x4*>(p + st_at(tr, t, 0)) = X[tr][t];
+        else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) y = fma((double)s[r], (double)X[tr][t][r], y);
-          }
-        y = last_lane(wave_prefix_f64(y));
-        if (l64 == 0) sY[w] = y;
-      }
-    }
-
-    if constexpr (kOut) {
-      // ---- pair products of row blocks a (this wave's) and b, weighted
-#pragma unroll
-      for (int half = 0; half < 4 / NW; ++half) {
-        const int a = NW == 4 ? w : (half == 0 ? w : 3 - w);
-        const float ah = g.hi[16 * a + ln], al = g.lo[16 * a + ln];
-        Fr qf[CK / 32];
-#pragma unroll
-        for (int p = 0; p < CK / 32; ++p) qf[p] = TK::template row8<Eng>(sQ, 16 * a + ln, 32 * p + 8 * gq);
-        Fr ef[MODE == kLinDK ? CV / 32 : 1];
-        float cm = 0.0f;                   // DK: column sums of M
-        if constexpr (MODE == kLinDK) {
-          const int row = 16 * a + ln;
-          const E* e = pE + (r0 + (row < n ? row : n - 1)) * A.es + 8 * gq;
-#pragma unroll
-          for (int p = 0; p < CV / 32; ++p) ef[p] = Eng::ld(e + 32 * p);
-        }
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          if (!lin_has<kRev>(a, kb)) continue;
-          float pw[8];
-#pragma unroll
-          for (int bb = 0; bb < 2; ++bb) {
-            const int b = 2 * kb + bb;
-            f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f}, acc2 = acc;
-            const bool in = kRev ? b >= a : b <= a;
-            if (in) {
-#pragma unroll
-              for (int p = 0; p < CK / 32; ++p)
-                Eng::mma(acc, TK::template row8<Eng>(sK, 16 * b + ln, 32 * p + 8 * gq), qf[p]);
-              if constexpr (MODE == kLinDK) {
-#pragma unroll
-                for (int p = 0; p < CV / 32; ++p)
-                  Eng::mma(acc2, TV::template row8<Eng>(sV, 16 * b + ln, 32 * p + 8 * gq), ef[p]);
-              }
-            }
-            const f32x4 bh = *reinterpret_cast<const f32x4*>(&g.hi[16 * b + 4 * gq]);
-            const f32x4 bl = *reinterpret_cast<const f32x4*>(&g.lo[16 * b + 4 * gq]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int ia = 16 * a + ln, ib = 16 * b + 4 * gq + r;
-              const float d = kRev ? (bh[r] - ah) + (bl[r] - al) : (ah - bh[r]) + (al - bl[r]);
-              pw[4 * bb + r] = (kRev ? ib >= ia && ib < n : ib <= ia) ? acc[r] * lin_exp(d) : 0.0f;
-              if constexpr (MODE == kLinDK) {
-                const float m = ib > ia ? acc2[r] * pw[4 * bb + r] : 0.0f;
-                cm += m;
-                const float rm = group_sum<16>(m);
-                if (in && ln == 0) sM[16 * lin_tri(a, b) + 4 * gq + r] = rm;
-              }
-            }
-          }
-          Fr pl[2];
-          Eng::split(pw, pl[0], pl[1]);
-          char* dst = smem + Lds::P + lin_block<kRev>(a, kb) * Eng::kPlanes * Lds::kFrag + l64 * (Lds::kFrag / 64);
-#pragma unroll
-          for (int k = 0; k < Eng::kPlanes; ++k) Eng::st((E*)(dst + k * Lds::kFrag), pl[k]);
-        }
-        if constexpr (MODE == kLinDK) {
-          cm += __shfl_xor(cm, 16, 64);
-          cm += __shfl_xor(cm, 32, 64);
-          if (gq == 0) sM[160 + 16 * a + ln] = cm;
+          for (int r = 0; r < 4; ++r) p[st_at(tr, t, r)] = X[tr][t][r];
         }
       }
-    }
-    if (w == kGateWave && it + 1 < nch) {
-      Gsum += lin_gates<kRev>(sG[(it + 1) & 1], rg, rows_of(chunk_of(it + 1)));
-      rg = gate_of(it + 2);
-    }
+  }
+  __device__ __forceinline__ bool anchor(int c) const { return c % kAnchor == kAnchor - 1 || c == L.nch - 1; }
+  __device__ __forceinline__ f32x4* dumped(int c) const {
+    return reinterpret_cast<f32x4*>(A.dump) + (L.dump0 + (c / kAnchor) * (int64_t)A.VH) * (CK * CV / 4) + 64 * w + l64;
+  }
+  __device__ __forceinline__ void store_anchor(int c) const {
+    f32x4* d = dumped(c);
+#pragma unroll
+    for (int tr = 0; tr < RT; ++tr)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) d[(2 * tr + t) * NT] = X[tr][t];
+  }
+  // DK: Y = <S, dS> at the chunk's end, anew from the stored state of its
+  // group; and the light wave's r_i
+  __device__ __forceinline__ void begin_dg(int c, int n, double* sY) {
+    if (w == kLight)
+      rdot = l64 < n ? A.rdot[((int64_t)L.sg.t0 + kChunk * c + l64) * A.VH + L.vh] : 0.0f;
+    if (!anchor(c)) return;
+    const f32x4* d = dumped(c);
+    double y = 0.0;
+#pragma unroll
+    for (int tr = 0; tr < RT; ++tr)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const f32x4 s = d[(2 * tr + t) * NT];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y = fma((double)s[r], (double)X[tr][t][r], y);
+      }
+    y = last_lane(wave_prefix_f64(y));
+    if (l64 == 0) sY[w] = y;
+  }
 
-    Fr vf[2][2];                           // V^T fragments of this wave's columns
+  // Pair products of row blocks a (this wave's) and b, weighted, into sP.
+  // sE: DK's tile of k.
+  __device__ __forceinline__ void pairs(const char* sQ, const char* sK, const char* sV, const char* sE,
+                                        const LinGates& g, int n, char* sP, float* sM) {
+#pragma unroll
+    for (int half = 0; half < 4 / NW; ++half) {
+      const int a = NW == 4 ? w : (half == 0 ? w : 3 - w);
+      const float ah = g.hi[16 * a + ln], al = g.lo[16 * a + ln];
+      Fr qf[CK / 32];
+#pragma unroll
+      for (int p = 0; p < CK / 32; ++p) qf[p] = TK::template row8<Eng>(sQ, 16 * a + ln, 32 * p + 8 * gq);
+      Fr ef[MODE == kLinDK ? CV / 32 : 1];
+      float cm = 0.0f;                     // DK: column sums of M
+      if constexpr (MODE == kLinDK) {
+#pragma unroll
+        for (int p = 0; p < CV / 32; ++p) ef[p] = TV::template row8<Eng>(sE, 16 * a + ln, 32 * p + 8 * gq);
+      }
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        if (!lin_has<kRev>(a, kb)) continue;
+        float pw[8];
+#pragma unroll
+        for (int bb = 0; bb < 2; ++bb) {
+          const int b = 2 * kb + bb;
+          f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f}, acc2 = acc;
+          const bool in = kRev ? b >= a : b <= a;
+          if (in) {
+#pragma unroll
+            for (int p = 0; p < CK / 32; ++p)
+              Eng::mma(acc, TK::template row8<Eng>(sK, 16 * b + ln, 32 * p + 8 * gq), qf[p]);
+            if constexpr (MODE == kLinDK) {
+#pragma unroll
+              for (int p = 0; p < CV / 32; ++p)
+                Eng::mma(acc2, TV::template row8<Eng>(sV, 16 * b + ln, 32 * p + 8 * gq), ef[p]);
+            }
+          }
+          const f32x4 bh = *reinterpret_cast<const f32x4*>(&g.hi[16 * b + 4 * gq]);
+          const f32x4 bl = *reinterpret_cast<const f32x4*>(&g.lo[16 * b + 4 * gq]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int ia = 16 * a + ln, ib = 16 * b + 4 * gq + r;
+            const float d = kRev ? (bh[r] - ah) + (bl[r] - al) : (ah - bh[r]) + (al - bl[r]);
+            pw[4 * bb + r] = (kRev ? ib >= ia && ib < n : ib <= ia) ? acc[r] * lin_exp(d) : 0.0f;
+            if constexpr (MODE == kLinDK) {
+              const float m = ib > ia ? acc2[r] * pw[4 * bb + r] : 0.0f;
+              cm += m;
+              const float rm = group_sum<16>(m);
+              if (in && ln == 0) sM[16 * lin_tri(a, b) + 4 * gq + r] = rm;
+            }
+          }
+        }
+        Fr pl[2];
+        Eng::split(pw, pl[0], pl[1]);
+        char* dst = sP + lin_block<kRev>(a, kb) * Eng::kPlanes * kFrag + l64 * (kFrag / 64);
+#pragma unroll
+        for (int k = 0; k < Eng::kPlanes; ++k) Eng::st((E*)(dst + k * kFrag), pl[k]);
+      }
+      if constexpr (MODE == kLinDK) {
+        cm += __shfl_xor(cm, 16, 64);
+        cm += __shfl_xor(cm, 32, 64);
+        if (gq == 0) sM[160 + 16 * a + ln] = cm;
+      }
+    }
+  }
+
+  __device__ __forceinline__ void take_v(const char* sV) {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) vf[t][kb] = TV::template cols8<Eng>(sV, kb, 32 * w + 4 * t, ln, gq);
+  }
 
-    if constexpr (kOut) {
-      // ---- state part: O^T = X^T Q^T, scaled by the rows' weights
-      f32x4 O[4][2];
+  // State part: O^T = X^T Q^T, scaled by the rows' weights.
+  __device__ __forceinline__ void state_part(const char* sQ, const LinGates& g) {
 #pragma unroll
-      for (int rt = 0; rt < 4; ++rt) O[rt][0] = O[rt][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int rt = 0; rt < 4; ++rt) O[rt][0] = O[rt][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int p = 0; p < CK / 32; ++p) {
-        Fr xf[2][3], qf[4];
+    for (int p = 0; p < CK / 32; ++p) {
+      Fr xf[2][3], qf[4];
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) qf[rt] = TK::template row8<Eng>(sQ, 16 * rt + ln, 32 * p + 8 * gq);
+      for (int rt = 0; rt < 4; ++rt) qf[rt] = TK::template row8<Eng>(sQ, 16 * rt + ln, 32 * p + 8 * gq);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const float x8[8] = {X[2 * p][t][0], X[2 * p][t][1], X[2 * p][t][2], X[2 * p][t][3],
-                               X[2 * p + 1][t][0], X[2 * p + 1][t][1], X[2 * p + 1][t][2], X[2 * p + 1][t][3]};
-          if constexpr (kXPlanes == 3) Eng::split3(x8, xf[t][0], xf[t][1], xf[t][2]);
-          else Eng::split(x8, xf[t][0], xf[t][1]);
-        }
-#pragma unroll
-        for (int k = 0; k < kXPlanes; ++k)
-#pragma unroll
-          for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) Eng::mma(O[rt][t], xf[t][k], qf[rt]);
+      for (int t = 0; t < 2; ++t) {
+        const float x8[8] = {X[2 * p][t][0], X[2 * p][t][1], X[2 * p][t][2], X[2 * p][t][3],
+                             X[2 * p + 1][t][0], X[2 * p + 1][t][1], X[2 * p + 1][t][2], X[2 * p + 1][t][3]};
+        if constexpr (kXPlanes == 3) Eng::split3(x8, xf[t][0], xf[t][1], xf[t][2]);
+        else Eng::split(x8, xf[t][0], xf[t][1]);
       }
 #pragma unroll
-      for (int rt = 0; rt < 4; ++rt) {
-        const float s = g.in[16 * rt + ln];
+      for (int k = 0; k < kXPlanes; ++k)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) O[rt][t][r] *= s;
-      }
-      if constexpr (kDots) {               // r_i, c_j: the wave's columns of the dots
+          for (int t = 0; t < 2; ++t) Eng::mma(O[rt][t], xf[t][k], qf[rt]);
+    }
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) {
+      const float s = g.in[16 * rt + ln];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) O[rt][t][r] *= s;
+    }
+  }
+  // DQ, DK: the wave's columns of r_i, c_j; e(row, x): eight columns of E.
+  template <class F>
+  __device__ __forceinline__ void dots(int n, float* sR, F e) const {
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) {
+      const int row = 16 * rt + ln;
+      float d = 0.0f, ev[8];
+      e(row, ev);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) d = fmaf(O[rt][t][r], ev[4 * t + r], d);
+      d += __shfl_xor(d, 16, 64);
+      d += __shfl_xor(d, 32, 64);
+      if (gq == 0) sR[kChunk * w + row] = row < n ? d : 0.0f;
+    }
+  }
+
+  // Pair part: O^T += V^T P^T.
+  __device__ __forceinline__ void pair_part(const char* sP) {
+#pragma unroll
+    for (int k = 0; k < Eng::kPlanes; ++k)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
-          const int row = 16 * rt + ln;
-          float d = 0.0f, ev[8];
-          ld8(pE + (r0 + (row < n ? row : n - 1)) * A.es + 32 * w + 8 * gq, ev);
+          if (!lin_has<kRev>(rt, kb)) continue;
+          const Fr pf = Eng::ld((const E*)(sP + (lin_block<kRev>(rt, kb) * Eng::kPlanes + k) * kFrag +
+                                           l64 * (kFrag / 64)));
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) d = fmaf(O[rt][t][r], ev[4 * t + r], d);
-          d += __shfl_xor(d, 16, 64);
-          d += __shfl_xor(d, 32, 64);
-          if (gq == 0) sR[kChunk * w + row] = row < n ? d : 0.0f;
+          for (int t = 0; t < 2; ++t) Eng::mma(O[rt][t], vf[t][kb], pf);
         }
-        asm volatile("" ::"v"(rdot));      // its load ends before the next chunk's are asked for
-      }
-      barrier_lds();
-      if (kDirect && it + 1 < nch) ask(it + 1);
-      // ---- pair part: O^T += V^T P^T
+  }
+  __device__ __forceinline__ void store_out(int c, int n) const {
 #pragma unroll
-      for (int k = 0; k < Eng::kPlanes; ++k)
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-          for (int rt = 0; rt < 4; ++rt) {
-            if (!lin_has<kRev>(rt, kb)) continue;
-            const Fr pf = Eng::ld((const E*)(smem + Lds::P + (lin_block<kRev>(rt, kb) * Eng::kPlanes + k) * Lds::kFrag +
-                                             l64 * (Lds::kFrag / 64)));
-#pragma unroll
-            for (int t = 0; t < 2; ++t) Eng::mma(O[rt][t], vf[t][kb], pf);
-          }
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt) {
-        const int row = 16 * rt + ln;
-        if (row < n) {
-          const int64_t at = (t0 + r0 + row) * A.os + (int64_t)(vh / A.od) * CV + 32 * w + 8 * gq;
-          if (sizeof(E) == 4 || A.out_f32) {
-            float* o = (float*)A.out + at;
-            *reinterpret_cast<f32x4*>(o) = O[rt][0];
-            *reinterpret_cast<f32x4*>(o + 4) = O[rt][1];
-          } else {
-            *reinterpret_cast<uint4*>((uint16_t*)A.out + at) =
-                make_uint4(pack_bf16x2(O[rt][0][0], O[rt][0][1]), pack_bf16x2(O[rt][0][2], O[rt][0][3]),
-                           pack_bf16x2(O[rt][1][0], O[rt][1][1]), pack_bf16x2(O[rt][1][2], O[rt][1][3]));
-          }
-        }
-      }
-      if constexpr (kDots) {
-        if (w == kGateWave) {
-          float d = 0.0f;
-#pragma unroll
-          for (int k = 0; k < NW; ++k) d += sR[kChunk * k + l64];
-          const int64_t at = (t0 + r0 + l64) * A.VH + vh;
-          if constexpr (MODE == kLinDQ) {
-            if (l64 < n) A.rdot[at] = d;
-          } else {
-            if (anchor) {
-              Y = sY[0];
-#pragma unroll
-              for (int k = 1; k < NW; ++k) Y += sY[k];
-            }
-            double rm = 0.0;               // row sum of M, over the column blocks
-#pragma unroll
-            for (int a = 0; a < 4; ++a)
-              if (a <= (l64 >> 4)) rm += (double)sM[16 * lin_tri(a, l64 >> 4) + (l64 & 15)];
-            const double own = rm + (double)rdot - (double)sM[160 + l64];
-            const double head = wave_prefix_f64(own), pre = wave_prefix_f64((double)d);
-            const double Xc = Y - last_lane(pre);
-            const double dg = (last_lane(head) - head + own) + (pre - (double)d) + Xc;
-            Y = Xc + last_lane(wave_prefix_f64((double)rdot));
-            if (l64 < n) {
-              if (A.dg_tok != nullptr) A.dg_tok[at] = (float)dg;
-              dg_sum += dg;
-            }
-          }
-        }
+    for (int rt = 0; rt < 4; ++rt) {
+      const int row = 16 * rt + ln;
+      if (row >= n) continue;
+      const int64_t at = ((int64_t)L.sg.t0 + kChunk * c + row) * A.os + (int64_t)L.vh * CV + 32 * w + 8 * gq;
+      if (sizeof(E) == 4 || A.out_f32) {
+        float* o = (float*)A.out + at;
+        *reinterpret_cast<f32x4*>(o) = O[rt][0];
+        *reinterpret_cast<f32x4*>(o + 4) = O[rt][1];
+      } else {
+        *reinterpret_cast<uint4*>((uint16_t*)A.out + at) =
+            make_uint4(pack_bf16x2(O[rt][0][0], O[rt][0][1]), pack_bf16x2(O[rt][0][2], O[rt][0][3]),
+                       pack_bf16x2(O[rt][1][0], O[rt][1][1]), pack_bf16x2(O[rt][1][2], O[rt][1][3]));
       }
     }
+  }
+  // DQ's light wave: r_i; DK's: dg of the chunk's tokens.
+  __device__ __forceinline__ void end_dots(int c, int n, const float* sR, const float* sM, const double* sY) {
+    float d = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) d += sR[kChunk * k + l64];
+    const int64_t at = ((int64_t)L.sg.t0 + kChunk * c + l64) * A.VH + L.vh;
+    if constexpr (MODE == kLinDQ) {
+      if (l64 < n) A.rdot[at] = d;
+    } else if constexpr (MODE == kLinDK) {
+      if (anchor(c)) {
+        Y = sY[0];
+#pragma unroll
+        for (int k = 1; k < NW; ++k) Y += sY[k];
+      }
+      double rm = 0.0;                     // row sum of M, over the column blocks
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+        if (a <= (l64 >> 4)) rm += (double)sM[16 * lin_tri(a, l64 >> 4) + (l64 & 15)];
+      const double own = rm + (double)rdot - (double)sM[160 + l64];
+      const double head = wave_prefix_f64(own), pre = wave_prefix_f64((double)d);
+      const double Xc = Y - last_lane(pre);
+      const double dg = (last_lane(head) - head + own) + (pre - (double)d) + Xc;
+      Y = Xc + last_lane(wave_prefix_f64((double)rdot));
+      if (l64 < n) {
+        if (A.dg_tok != nullptr) A.dg_tok[at] = (float)dg;
+        dg_sum += dg;
+      }
+    }
+  }
 
-    // ---- X <- e^(G_C) X + sum_b out_b K_b V_b^T
+  // X <- e^(G_C) X + sum_b out_b K_b V_b^T
+  __device__ __forceinline__ void update(const char* sK, const LinGates& g) {
     const float dec = g.decay;
 #pragma unroll
     for (int tr = 0; tr < RT; ++tr)
@@ -668,40 +657,263 @@ __global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(L
             for (int t = 0; t < 2; ++t) Eng::mma(X[tr0 + i][t], kf[i], wv[t][k]);
       }
     }
+  }
+};
+
+// Forward passes and state passes: one role, CV / 32 waves.
+template <class Eng, int CK, int CV, int MODE>
+struct LinLds {
+  using E = typename Eng::E;
+  using W = LinWalk<Eng, CK, CV, MODE>;
+  static constexpr bool kDirect = sizeof(E) == 2;
+  static constexpr int kVTiles = kDirect && !W::kOut ? 2 : 1;
+  static constexpr int K = 0;
+  static constexpr int V = K + (kDirect ? 2 : 1) * W::TK::kBytes;
+  static constexpr int Q = V + kVTiles * W::TV::kBytes;
+  static constexpr int P = Q + (W::kOut ? W::TK::kBytes : 0);
+  static constexpr int G = P + (W::kOut ? W::kPBytes : 0);
+  static constexpr int R = G + 2 * (int)sizeof(LinGates);
+  static constexpr int kBytes = R + (W::kDots ? W::NW * kChunk * 4 : 0);
+};
+
+template <class Eng, int CK, int CV, int MODE>
+__global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(LinScan A) {
+  using E = typename Eng::E;
+  using Lds = LinLds<Eng, CK, CV, MODE>;
+  using W = LinWalk<Eng, CK, CV, MODE>;
+  using RowsK = LinRows<E, CK, W::NT>;
+  using RowsV = LinRows<E, CV, W::NT>;
+  constexpr bool kOut = W::kOut, kDots = W::kDots, kDirect = Lds::kDirect, kRev = W::kRev;
+
+  extern __shared__ char smem[];
+  LinGates* sG = reinterpret_cast<LinGates*>(smem + Lds::G);
+  float* sR = reinterpret_cast<float*>(smem + Lds::R);
+  const uint32_t lds0 = lds_base_u32(smem);
+
+  LinPlace L;
+  if (!L.find(A)) return;
+  // the state pass leaves out the segment whose sum nothing reads
+  if (MODE == kLinStF && L.sg.s == L.sg.nseg - 1) return;
+  if (MODE == kLinStR && L.sg.s == 0) return;
+  const int w = uniform(threadIdx.x >> 6);
+  W S(A, L, w);
+
+  const int64_t t0 = L.sg.t0;
+  const E* pK = (const E*)A.K + t0 * A.ks + (int64_t)(L.vh / A.kd) * CK;
+  const E* pV = (const E*)A.V + t0 * A.vs + (int64_t)(L.vh / A.vd) * CV;
+  const E* pQ = kOut ? (const E*)A.Q + t0 * A.qs + (int64_t)(L.vh / A.qd) * CK : nullptr;
+  const E* pE = kDots ? (const E*)A.E + t0 * A.es + (int64_t)(L.vh / A.ed) * CV : nullptr;
+  // the rows of walk step it: K into its tile, V and Q into theirs
+  auto ask = [&](int it) {
+    const int c = L.chunk<kRev>(it), n = L.rows(c);
+    const int64_t r0 = (int64_t)kChunk * c;
+    RowsK::ask(lds0 + Lds::K + (it & 1) * W::TK::kBytes, pK + r0 * A.ks, A.ks, n);
+    RowsV::ask(lds0 + Lds::V + (kOut ? 0 : (it & 1) * W::TV::kBytes), pV + r0 * A.vs, A.vs, n);
+    if constexpr (kOut) RowsK::ask(lds0 + Lds::Q, pQ + r0 * A.qs, A.qs, n);
+  };
+
+  const int nch = L.nch;
+  float rg = 0.0f;                         // light wave: the next step's log decays
+  double Gsum = 0.0;                       // and the segment's sum
+  if (w == W::kLight && nch > 0) {
+    Gsum += lin_gates<kRev>(sG[0], L.gate<kRev>(0, A.g_row), L.rows(L.chunk<kRev>(0)));
+    rg = L.gate<kRev>(1, A.g_row);
+  }
+  if (kDirect && nch > 0) ask(0);
+  S.load_state();
+
+#pragma unroll 1
+  for (int it = 0; it < nch; ++it) {
+    const int c = L.chunk<kRev>(it), n = L.rows(c);
+    const int64_t r0 = (int64_t)kChunk * c;
+    const LinGates& g = sG[it & 1];
+    const char* sK = smem + Lds::K + (kDirect ? (it & 1) * W::TK::kBytes : 0);
+    const char* sV = smem + Lds::V + (kDirect && !kOut ? (it & 1) * W::TV::kBytes : 0);
+    if constexpr (kDirect) {
+      wait_vmem();
+      barrier_lds();
+      if (!kOut && it + 1 < nch) ask(it + 1);
+    } else {
+      RowsK::copy(smem + Lds::K, pK + r0 * A.ks, A.ks, n);
+      RowsV::copy(smem + Lds::V, pV + r0 * A.vs, A.vs, n);
+      if constexpr (kOut) RowsK::copy(smem + Lds::Q, pQ + r0 * A.qs, A.qs, n);
+      __syncthreads();
+    }
+    if constexpr (kOut) S.pairs(smem + Lds::Q, sK, sV, nullptr, g, n, smem + Lds::P, nullptr);
+    if (w == W::kLight && it + 1 < nch) {
+      Gsum += lin_gates<kRev>(sG[(it + 1) & 1], rg, L.rows(L.chunk<kRev>(it + 1)));
+      rg = L.gate<kRev>(it + 2, A.g_row);
+    }
+    S.take_v(sV);
+    if constexpr (kOut) {
+      S.state_part(smem + Lds::Q, g);
+      if constexpr (kDots)
+        S.dots(n, sR, [&](int row, float(&x)[8]) {
+          ld8(pE + (r0 + (row < n ? row : n - 1)) * A.es + 32 * w + 8 * S.gq, x);
+        });
+      barrier_lds();
+      if (kDirect && it + 1 < nch) ask(it + 1);
+      S.pair_part(smem + Lds::P);
+      S.store_out(c, n);
+      if (kDots && w == W::kLight) S.end_dots(c, n, sR, nullptr, nullptr);
+    }
+    S.update(sK, g);
     if constexpr (MODE == kLinDQ) {
-      if (anchor) {
-        f32x4* d = reinterpret_cast<f32x4*>(A.dump) + (dump0 + (c / kAnchor) * (int64_t)A.VH) * (CK * CV / 4) + tid;
-#pragma unroll
-        for (int tr = 0; tr < RT; ++tr)
-#pragma unroll
-          for (int t = 0; t < 2; ++t) d[(2 * tr + t) * NT] = X[tr][t];
-      }
+      if (S.anchor(c)) S.store_anchor(c);
     }
     if constexpr (!kDirect) __syncthreads();
   }
+  S.store_state();
+  if (!kOut && w == W::kLight && S.l64 == 0) A.seg_decay[L.sv] = expf((float)Gsum);
+}
 
-  // ---- the state after the walk
-  float* p = nullptr;
-  if (!kOut) p = A.seg + sv * st_size;
-  else if (A.last != nullptr && sg.s == (kRev ? 0 : sg.nseg - 1)) p = A.last + ((int64_t)sg.n * A.VH + vh) * st_size;
-  if (p != nullptr) {
-#pragma unroll
-    for (int tr = 0; tr < RT; ++tr)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if constexpr (kXT) *reinterpret_cast<f32x4*>(p + st_at(tr, t, 0)) = X[tr][t];
-        else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) p[st_at(tr, t, r)] = X[tr][t][r];
-        }
-      }
+// The reverse passes of the backward, dk (with dg) and dv, as two roles of
+// one workgroup: the first DK / 32 waves walk X = dS [TW, DK] for dk, the next
+// TW / 32 waves X = dS^T [DK, TW] for dv.  They share the chunk's rows of q, k,
+// v and d_o in LDS (q and d_o, which both still read after the second
+// barrier, have two tiles), so each is read once.
+template <class Eng, int DK, int TW>
+struct LinRevLds {
+  using E = typename Eng::E;
+  using WK = LinWalk<Eng, TW, DK, kLinDK>;
+  using WV = LinWalk<Eng, DK, TW, kLinDV>;
+  static constexpr bool kDirect = sizeof(E) == 2;
+  static constexpr int kTiles = kDirect ? 2 : 1;
+  static constexpr int TD = LinTile<E, DK>::kBytes, TV = LinTile<E, TW>::kBytes;
+  static constexpr int Q = 0;
+  static constexpr int O = Q + kTiles * TD;
+  static constexpr int K = O + kTiles * TV;
+  static constexpr int V = K + TD;
+  static constexpr int PK = V + TV;
+  static constexpr int PV = PK + WK::kPBytes;
+  static constexpr int G = PV + WV::kPBytes;
+  static constexpr int R = G + 2 * (int)sizeof(LinGates);
+  static constexpr int M = R + WK::NW * kChunk * 4;
+  static constexpr int Y = M + (10 * 16 + kChunk) * 4;
+  static constexpr int kBytes = Y + 32;
+};
+
+// A: the dk pass (Q = v, K = d_o, V = q, E = k); B: the dv pass.
+template <class Eng, int DK, int TW>
+__global__ __launch_bounds__(2 * (DK + TW), Eng::kSplit ? 2 : 1) void lin_rev_kernel(LinScan A, LinScan B) {
+  using E = typename Eng::E;
+  using Lds = LinRevLds<Eng, DK, TW>;
+  using WK = typename Lds::WK;
+  using WV = typename Lds::WV;
+  constexpr int NT = 2 * (DK + TW);
+  constexpr bool kDirect = Lds::kDirect;
+  using RowsD = LinRows<E, DK, NT>;
+  using RowsT = LinRows<E, TW, NT>;
+
+  extern __shared__ char smem[];
+  LinGates* sG = reinterpret_cast<LinGates*>(smem + Lds::G);
+  float* sR = reinterpret_cast<float*>(smem + Lds::R);
+  float* sM = reinterpret_cast<float*>(smem + Lds::M);
+  double* sY = reinterpret_cast<double*>(smem + Lds::Y);
+  const uint32_t lds0 = lds_base_u32(smem);
+
+  LinPlace L;
+  if (!L.find(A)) {
+    // an unused slot's part of dg (a bad index array leaves it unread)
+    if (A.dg_part != nullptr && threadIdx.x == 0) A.dg_part[(int64_t)blockIdx.x] = 0.0;
+    return;
   }
-  if (!kOut && w == kGateWave && l64 == 0) A.seg_decay[sv] = expf((float)Gsum);
-  if constexpr (MODE == kLinDK) {
-    if (A.dg_part != nullptr && w == kGateWave) {
-      const double s = last_lane(wave_prefix_f64(dg_sum));
-      if (l64 == 0) A.dg_part[sv] = s;
+  const int w = uniform(threadIdx.x >> 6);
+  const int64_t t0 = L.sg.t0;
+  const E* pQ = (const E*)A.V + t0 * A.vs + (int64_t)(L.vh / A.vd) * DK;
+  const E* pK = (const E*)A.E + t0 * A.es + (int64_t)(L.vh / A.ed) * DK;
+  const E* pV = (const E*)A.Q + t0 * A.qs + (int64_t)(L.vh / A.qd) * TW;
+  const E* pO = (const E*)A.K + t0 * A.ks + (int64_t)(L.vh / A.kd) * TW;
+  const int nch = L.nch;
+  auto ask = [&](int it) {
+    const int c = L.chunk<true>(it), n = L.rows(c);
+    const int64_t r0 = (int64_t)kChunk * c;
+    RowsD::ask(lds0 + Lds::Q + (it & 1) * Lds::TD, pQ + r0 * A.vs, A.vs, n);
+    RowsT::ask(lds0 + Lds::O + (it & 1) * Lds::TV, pO + r0 * A.ks, A.ks, n);
+    RowsD::ask(lds0 + Lds::K, pK + r0 * A.es, A.es, n);
+    RowsT::ask(lds0 + Lds::V, pV + r0 * A.qs, A.qs, n);
+  };
+  auto begin = [&](int it) {               // the chunk's tiles and gates are there
+    if constexpr (kDirect) {
+      wait_vmem();
+      barrier_lds();
+    } else {
+      const int c = L.chunk<true>(it), n = L.rows(c);
+      const int64_t r0 = (int64_t)kChunk * c;
+      RowsD::copy(smem + Lds::Q, pQ + r0 * A.vs, A.vs, n);
+      RowsT::copy(smem + Lds::O, pO + r0 * A.ks, A.ks, n);
+      RowsD::copy(smem + Lds::K, pK + r0 * A.es, A.es, n);
+      RowsT::copy(smem + Lds::V, pV + r0 * A.qs, A.qs, n);
+      __syncthreads();
     }
+  };
+  auto middle = [&](int it) {              // P, the dots and the next gates are there; k and v are free
+    barrier_lds();
+    if (kDirect && it + 1 < nch) ask(it + 1);
+  };
+
+  if (w < WK::NW) {
+    if (kDirect && nch > 0) ask(0);
+    WK S(A, L, w);
+    S.load_state();
+#pragma unroll 1
+    for (int it = 0; it < nch; ++it) {
+      const int c = L.chunk<true>(it), n = L.rows(c);
+      const LinGates& g = sG[it & 1];
+      const char* sQ = smem + Lds::Q + (kDirect ? (it & 1) * Lds::TD : 0);
+      const char* sO = smem + Lds::O + (kDirect ? (it & 1) * Lds::TV : 0);
+      begin(it);
+      S.begin_dg(c, n, sY);
+      S.pairs(smem + Lds::V, sO, sQ, smem + Lds::K, g, n, smem + Lds::PK, sM);
+      S.take_v(sQ);
+      S.state_part(smem + Lds::V, g);
+      S.dots(n, sR, [&](int row, float(&x)[8]) {
+        const auto f = WK::TV::template row8<Eng>(smem + Lds::K, row, 32 * w + 8 * S.gq);
+        ld8((const E*)&f, x);
+      });
+      asm volatile("" ::"v"(S.rdot));      // its load ends before the next chunk's are asked for
+      middle(it);
+      S.pair_part(smem + Lds::PK);
+      S.store_out(c, n);
+      if (w == WK::kLight) S.end_dots(c, n, sR, sM, sY);
+      S.update(sO, g);
+      if constexpr (!kDirect) __syncthreads();
+    }
+    if (A.dg_part != nullptr && w == WK::kLight) {
+      const double s = last_lane(wave_prefix_f64(S.dg_sum));
+      if (S.l64 == 0) A.dg_part[L.sv] = s;
+    }
+  } else {
+    const int wv = w - WK::NW;
+    float rg = 0.0f;
+    if (wv == WV::kLight && nch > 0) {
+      lin_gates<true>(sG[0], L.gate<true>(0, A.g_row), L.rows(L.chunk<true>(0)));
+      rg = L.gate<true>(1, A.g_row);
+    }
+    if (kDirect && nch > 0) ask(0);
+    WV S(B, L, wv);
+    S.load_state();
+#pragma unroll 1
+    for (int it = 0; it < nch; ++it) {
+      const int c = L.chunk<true>(it), n = L.rows(c);
+      const LinGates& g = sG[it & 1];
+      const char* sQ = smem + Lds::Q + (kDirect ? (it & 1) * Lds::TD : 0);
+      const char* sO = smem + Lds::O + (kDirect ? (it & 1) * Lds::TV : 0);
+      begin(it);
+      S.pairs(smem + Lds::K, sQ, sO, nullptr, g, n, smem + Lds::PV, nullptr);
+      if (wv == WV::kLight && it + 1 < nch) {
+        lin_gates<true>(sG[(it + 1) & 1], rg, L.rows(L.chunk<true>(it + 1)));
+        rg = L.gate<true>(it + 2, A.g_row);
+      }
+      S.take_v(sO);
+      S.state_part(smem + Lds::K, g);
+      middle(it);
+      S.pair_part(smem + Lds::PV);
+      S.store_out(c, n);
+      S.update(sQ, g);
+      if constexpr (!kDirect) __syncthreads();
+    }
+    S.store_state();
   }
 }
 
@@ -720,12 +932,31 @@ static hipError_t lin_scan_go(const LinScan& A, int64_t slots, hipStream_t strea
 // the mode takes them.
 template <class Eng, int MODE>
 static hipError_t lin_scan_mode(const LinScan& A, int64_t slots, hipStream_t stream) {
-  const bool swap = MODE == kLinDQ || MODE == kLinDK;
+  constexpr bool swap = MODE == kLinDQ;
   const int ck = swap ? A.tw : A.dk, cv = swap ? A.dk : A.tw;
   if (ck == 64) return cv == 64 ? lin_scan_go<Eng, 64, 64, MODE>(A, slots, stream)
                                 : lin_scan_go<Eng, 64, 128, MODE>(A, slots, stream);
   return cv == 64 ? lin_scan_go<Eng, 128, 64, MODE>(A, slots, stream)
                   : lin_scan_go<Eng, 128, 128, MODE>(A, slots, stream);
+}
+
+// The dk and dv passes in one launch.
+template <class Eng, int DK, int TW>
+static hipError_t lin_rev_go(const LinScan& A, const LinScan& B, int64_t slots, hipStream_t stream) {
+  static PerDeviceOnce once;
+  constexpr int lds = LinRevLds<Eng, DK, TW>::kBytes;
+  const auto kern = lin_rev_kernel<Eng, DK, TW>;
+  const hipError_t e = set_dyn_lds_once(once, (const void*)kern, lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(slots * A.VH)), dim3(2 * (DK + TW)), lds, stream, A, B);
+  return hipGetLastError();
+}
+template <class Eng>
+static hipError_t lin_rev(const LinScan& A, const LinScan& B, int64_t slots, hipStream_t stream) {
+  if (A.dk == 64) return A.tw == 64 ? lin_rev_go<Eng, 64, 64>(A, B, slots, stream)
+                                    : lin_rev_go<Eng, 64, 128>(A, B, slots, stream);
+  return A.tw == 64 ? lin_rev_go<Eng, 128, 64>(A, B, slots, stream)
+                    : lin_rev_go<Eng, 128, 128>(A, B, slots, stream);
 }
 
 }  // namespace gdn
