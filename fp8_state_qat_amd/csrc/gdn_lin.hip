@@ -117,14 +117,19 @@ __global__ __launch_bounds__(kThreads) void lin_reduce_dg_head_kernel(const doub
 int lin_tile(int dv) { return dv % 128 == 0 ? 128 : 64; }
 
 // Rows of a segment: whole sequences when the (sequence, head) pairs alone
-// fill the card twice, else enough segments for that, of at least 128 rows.
-constexpr int64_t kLinUnits = 512;
+// fill the card, else enough segments for that, of at least 128 rows.  The
+// scan's workgroups fit a compute unit twice, with fp32 tiles of 128 key
+// channels once (8 heads of 128 x 128, 6000 fp32 tokens: 106 us forward and
+// 328 backward with 256 units, 119 and 374 with 512; 16 bf16 heads, 32k
+// tokens: 239 with 256, 231 with 512).
+int64_t lin_units(const gdn_lin_t& s) { return s.io_dtype == GDN_F32 && s.dk == 128 ? 256 : 512; }
 constexpr int64_t kLinMinSeg = 128;
 int lin_seglen(const gdn_lin_t& s) {
   const int64_t VH = (int64_t)s.n_heads * (s.dv / lin_tile(s.dv));
+  const int64_t units = lin_units(s);
   const int64_t whole = (s.total_tokens / kChunk + 1) * kChunk;
-  if ((int64_t)s.n_seqs * VH >= kLinUnits) return (int)whole;
-  int64_t len = (s.total_tokens * VH + kLinUnits - 1) / kLinUnits;
+  if ((int64_t)s.n_seqs * VH >= units) return (int)whole;
+  int64_t len = (s.total_tokens * VH + units - 1) / units;
   if (len < kLinMinSeg) len = kLinMinSeg;
   len = (len + kChunk - 1) / kChunk * kChunk;
   return (int)(len < whole ? len : whole);

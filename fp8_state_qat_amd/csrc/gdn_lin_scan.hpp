@@ -27,7 +27,9 @@
 // Work split.  A workgroup owns one segment (a run of whole chunks of one
 // sequence) of one virtual head (a value head, or a 64- or 128-row tile of
 // one) and walks its chunks with X in fp32 accumulators: wave w holds the
-// columns 32 w .. 32 w + 31 of X for all CK rows.  Segments of a sequence run
+// columns 16 w .. 16 w + 15 of X for all CK rows (eight waves at 128 columns;
+// four with 32 columns each left the same time at 128 x 128 bf16 and 13 to
+// 30% more on smaller tiles and fp32).  Segments of a sequence run
 // at once: state passes first form every segment's own sum and decay, a small
 // kernel turns them into the state at each segment's start.  The segment
 // length is set by the host so that the card is full; with enough (sequence,
@@ -40,7 +42,7 @@
 // enters dg, the weighted V rows of the state update into three, so that the
 // states and dg keep fp32 accuracy.  (Two planes leave 2e-6 of a value.)
 // The row relabelling dkmap makes the accumulators of X, in place, the A
-// operand of X^T Q, and the eight channels of a lane contiguous in memory;
+// operand of X^T Q;
 // P^T = K Q^T comes out as the B operand of the product with V.
 //
 // LDS: Q, K, V tiles of the chunk (64 rows, 16-byte units XOR-swizzled so
@@ -124,6 +126,12 @@ __device__ __forceinline__ int lin_unit(int row, int u) {
   else return u ^ ((((row >> 1) & 1) << 2) | ((row >> 2) & 3));
 }
 
+__device__ __forceinline__ f32x4 ld4(const uint16_t* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return f32x4{bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y)};
+}
+__device__ __forceinline__ f32x4 ld4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+
 template <typename E, int D>
 struct LinTile {
   static constexpr int kUnits = D * (int)sizeof(E) / 16;
@@ -138,18 +146,25 @@ struct LinTile {
                       (const E*)(t + row * D * 4 + 16 * lin_unit<kUnits>(row, c0 / 4 + 1)));
     }
   }
-  // column c0 + 8 (ln / 4) + ln % 4 of the rows kperm of k-block kb: the
-  // transposed fragment whose 16 columns are relabelled by dkmap
-  template <class Eng>
+  // four consecutive columns from c0 of a row, as fp32
+  static __device__ __forceinline__ f32x4 row4(const char* t, int row, int c0) {
+    constexpr int kPer = 16 / (int)sizeof(E);
+    return ld4((const E*)(t + row * D * sizeof(E) + 16 * lin_unit<kUnits>(row, c0 / kPer) +
+                          (c0 % kPer) * sizeof(E)));
+  }
+  // column c0 + kStep (ln / 4) + ln % 4 of the rows kperm of k-block kb: a
+  // transposed fragment of 16 columns, in order (kStep 4) or as dkmap
+  // relabels them (kStep 8)
+  template <class Eng, int kStep>
   static __device__ __forceinline__ typename Eng::Fr cols8(const char* t, int kb, int c0, int ln, int gq) {
     if constexpr (sizeof(E) == 2) {
-      const int r0 = 32 * kb + 4 * gq + (ln >> 2), r1 = r0 + 16, c = c0 + 8 * (ln & 3);
+      const int r0 = 32 * kb + 4 * gq + (ln >> 2), r1 = r0 + 16, c = c0 + kStep * (ln & 3);
       const uint2 a = lds_read_tr16(t + r0 * D * 2 + 16 * lin_unit<kUnits>(r0, c / 8) + (c & 4) * 2);
       const uint2 b = lds_read_tr16(t + r1 * D * 2 + 16 * lin_unit<kUnits>(r1, c / 8) + (c & 4) * 2);
       return __builtin_bit_cast(typename Eng::Fr, make_uint4(a.x, a.y, b.x, b.y));
     } else {
       typename Eng::Fr f;
-      const int c = c0 + 8 * (ln >> 2) + (ln & 3);
+      const int c = c0 + kStep * (ln >> 2) + (ln & 3);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int r = 32 * kb + 4 * gq + (j & 3) + 16 * (j >> 2);
@@ -232,46 +247,39 @@ struct LinGates {
   float hi[kChunk], lo[kChunk];  // G_i = hi + lo
   float in[kChunk];              // weight of X^T Q_a
   float out[kChunk];             // weight of K_b V_b^T in the state
+};
+// of the reverse passes: in[63] is not e^(G_C) there
+struct LinGatesRev : LinGates {
   float decay;                   // e^(G_C)
   float pad[3];
 };
+template <bool kRev>
+using LinGatesOf = std::conditional_t<kRev, LinGatesRev, LinGates>;
+__device__ __forceinline__ float lin_decay(const LinGates& g) { return g.in[kChunk - 1]; }
+__device__ __forceinline__ float lin_decay(const LinGatesRev& g) { return g.decay; }
 
 // One wave: the chunk's gate vectors; rows from n on have no weight in the
 // state.  The sums run in fp64 (far tokens of a strongly decaying chunk differ
 // by large G); a log decay below -1e4 has the weight 0 and is held there, so
-// that -inf leaves no NaN.  Returns the chunk's sum.
+// that -inf leaves no NaN.  later: log decays between the chunk and the end
+// that its state weights refer to.  Returns the chunk's sum.
 template <bool kRev>
-__device__ __forceinline__ double lin_gates(LinGates& s, float g, int n) {
+__device__ __forceinline__ double lin_gates(LinGatesOf<kRev>& s, float g, int n, double later = 0.0) {
   const int ln = threadIdx.x & 63;
   const double G = wave_prefix_f64((double)(g < -1e4f ? -1e4f : g));
   const double C = last_lane(G);
   const float hi = (float)G;
   s.hi[ln] = hi;
   s.lo[ln] = (float)(G - (double)hi);
-  const float a = expf(hi), b = expf((float)(C - G));
+  const float a = expf(hi), b = expf((float)(C - G + later));
   s.in[ln] = kRev ? b : a;
   s.out[ln] = ln < n ? (kRev ? a : b) : 0.0f;
-  if (ln == 63) s.decay = a;
+  if constexpr (kRev) {
+    if (ln == kChunk - 1) s.decay = a;
+  }
   return C;
 }
 
-__device__ __forceinline__ void ld8(const uint16_t* p, float (&x)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    x[2 * j] = bf16_lo(w[j]);
-    x[2 * j + 1] = bf16_hi(w[j]);
-  }
-}
-__device__ __forceinline__ void ld8(const float* p, float (&x)[8]) {
-  const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    x[j] = a[j];
-    x[4 + j] = b[j];
-  }
-}
 
 // The six 16 x 32 blocks of P (row tile rt, k-block kb) inside the triangle,
 // and the ten 16 x 16 tiles (a, b >= a) of the reverse one.
@@ -280,6 +288,11 @@ __host__ __device__ constexpr bool lin_has(int rt, int kb) { return kRev ? 2 * k
 template <bool kRev>
 __host__ __device__ constexpr int lin_block(int rt, int kb) {
   return kRev ? (rt < 2 ? 2 * rt + kb : 2 + rt) : (rt < 2 ? rt : 2 * rt - 2 + kb);
+}
+template <bool kRev>
+__device__ __forceinline__ void lin_block_at(int blk, int& rt, int& kb) {   // its inverse
+  rt = kRev ? (blk < 4 ? blk >> 1 : blk - 2) : (blk < 2 ? blk : 1 + (blk >> 1));
+  kb = kRev ? (blk < 4 ? blk & 1 : 1) : (blk < 2 ? 0 : blk & 1);
 }
 __host__ __device__ constexpr int lin_tri(int a, int b) { return 4 * a - a * (a - 1) / 2 + b - a; }
 
@@ -318,7 +331,7 @@ struct LinPlace {
   }
 };
 
-// The walk of one role (mode) by its CV / 32 waves: X and the pieces of a
+// The walk of one role (mode) by its CV / 16 waves: X and the pieces of a
 // chunk's work.  w: the wave's index in the role.
 template <class Eng, int CK, int CV, int MODE>
 struct LinWalk {
@@ -329,23 +342,29 @@ struct LinWalk {
   static constexpr bool kOut = MODE != kLinStF && MODE != kLinStR;
   static constexpr bool kDots = MODE == kLinDQ || MODE == kLinDK;
   static constexpr bool kRev = MODE == kLinStR || MODE == kLinDV || MODE == kLinDK;
+  // The forward state pass also walks from the last chunk to the first: its
+  // weights hold the decays up to the segment's end, X needs none of its own,
+  // and the chunks it read last are those that the output pass reads first.
+  static constexpr bool kBack = kRev || MODE == kLinStF;
+  using Gates = LinGatesOf<kRev>;
   static constexpr bool kXT = !kDots;      // X rows are key channels (else value rows)
   static constexpr int kXPlanes = Eng::kSplit ? (kDots ? 3 : 2) : 1;   // three where X's product enters dg
   static constexpr int kVPlanes = Eng::kSplit ? 3 : 1;
-  static constexpr int NW = CV / 32, NT = 64 * NW;
+  static constexpr int NW = CV / 16, NT = 64 * NW;
   static constexpr int RT = CK / 16;       // row tiles of X
   static constexpr int kFrag = 64 * (sizeof(E) == 2 ? 16 : 32);
   static constexpr int kPBytes = 6 * Eng::kPlanes * kFrag;
-  // the wave with the fewest pair tiles: it forms the next gates, and dg
-  static constexpr int kLight = kRev ? NW - 1 : 0;
+  // the wave with the fewest pair tiles (they are dealt block by block): it
+  // forms the next gates, and dg
+  static constexpr int kLight = kRev && NW == 4 ? 2 : NW - 1;
 
   const LinScan& A;
   const LinPlace& L;
   const int w, l64, ln, gq;
-  // X: tile tr holds rows dkmap(16 tr + 4 gq + r), column tile t the column
-  // 32 w + 8 (ln / 4) + 4 t + ln % 4
-  f32x4 X[RT][2], O[4][2];
-  Fr vf[2][2];                             // V^T fragments of this wave's columns
+  // X: tile tr holds rows dkmap(16 tr + 4 gq + r), column 16 w + ln; O: row
+  // tile rt the row 16 rt + ln, columns 16 w + 4 gq + r
+  f32x4 X[RT], O[4];
+  Fr vf[2];                                // V^T fragments of this wave's columns
   float rdot;                              // DK, light wave: this lane's r_i
   double Y, dg_sum;
 
@@ -353,8 +372,8 @@ struct LinWalk {
       : A(a), L(l), w(wave), l64(threadIdx.x & 63), ln(threadIdx.x & 15), gq((threadIdx.x >> 4) & 3), rdot(0.0f),
         Y(0.0), dg_sum(0.0) {}
 
-  __device__ __forceinline__ int64_t st_at(int tr, int t, int r) const {
-    const int row = 32 * (tr / 2) + 8 * gq + 4 * (tr & 1) + r, colx = 32 * w + 8 * (ln >> 2) + 4 * t + (ln & 3);
+  __device__ __forceinline__ int64_t st_at(int tr, int r) const {
+    const int row = 32 * (tr / 2) + 8 * gq + 4 * (tr & 1) + r, colx = 16 * w + ln;
     return kXT ? (int64_t)colx * CK + row : (int64_t)row * CV + colx;
   }
   __device__ __forceinline__ void load_state() {
@@ -365,19 +384,17 @@ struct LinWalk {
       else if (A.first != nullptr) p = A.first + ((int64_t)L.sg.n * A.VH + L.vh) * size;
     }
 #pragma unroll
-    for (int tr = 0; tr < RT; ++tr)
+    for (int tr = 0; tr < RT; ++tr) {
+      f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (p != nullptr) {
+        if constexpr (kXT) x = *reinterpret_cast<const f32x4*>(p + st_at(tr, 0));
+        else {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (p != nullptr) {
-          if constexpr (kXT) x = *reinterpret_cast<const f32x4*>(p + st_at(tr, t, 0));
-          else {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = p[st_at(tr, t, r)];
-          }
+          for (int r = 0; r < 4; ++r) x[r] = p[st_at(tr, r)];
         }
-        X[tr][t] = x;
       }
+      X[tr] = x;
+    }
   }
   // the state after the walk: a segment's sum, or the sequence's last state
   __device__ __forceinline__ void store_state() const {
@@ -388,15 +405,13 @@ struct LinWalk {
       p = A.last + ((int64_t)L.sg.n * A.VH + L.vh) * size;
     if (p == nullptr) return;
 #pragma unroll
-    for (int tr = 0; tr < RT; ++tr)
+    for (int tr = 0; tr < RT; ++tr) {
+      if constexpr (kXT) *reinterpret_cast<f32x4*>(p + st_at(tr, 0)) = X[tr];
+      else {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if constexpr (kXT) *reinterpret_cast<f32x4*>(p + st_at(tr, t, 0)) = X[tr][t];
-        else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) p[st_at(tr, t, r)] = X[tr][t][r];
-        }
+        for (int r = 0; r < 4; ++r) p[st_at(tr, r)] = X[tr][r];
       }
+    }
   }
   __device__ __forceinline__ bool anchor(int c) const { return c % kAnchor == kAnchor - 1 || c == L.nch - 1; }
   __device__ __forceinline__ f32x4* dumped(int c) const {
@@ -405,9 +420,7 @@ struct LinWalk {
   __device__ __forceinline__ void store_anchor(int c) const {
     f32x4* d = dumped(c);
 #pragma unroll
-    for (int tr = 0; tr < RT; ++tr)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) d[(2 * tr + t) * NT] = X[tr][t];
+    for (int tr = 0; tr < RT; ++tr) d[tr * NT] = X[tr];
   }
   // DK: Y = <S, dS> at the chunk's end, anew from the stored state of its
   // group; and the light wave's r_i
@@ -418,133 +431,117 @@ struct LinWalk {
     const f32x4* d = dumped(c);
     double y = 0.0;
 #pragma unroll
-    for (int tr = 0; tr < RT; ++tr)
+    for (int tr = 0; tr < RT; ++tr) {
+      const f32x4 s = d[tr * NT];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const f32x4 s = d[(2 * tr + t) * NT];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) y = fma((double)s[r], (double)X[tr][t][r], y);
-      }
+      for (int r = 0; r < 4; ++r) y = fma((double)s[r], (double)X[tr][r], y);
+    }
     y = last_lane(wave_prefix_f64(y));
     if (l64 == 0) sY[w] = y;
   }
 
-  // Pair products of row blocks a (this wave's) and b, weighted, into sP.
-  // sE: DK's tile of k.
+  // Pair products of this wave's 16 x 32 blocks, weighted, into sP.  sE: DK's
+  // tile of k; sM: its sums of M over the rows of a tile (ten of 16) and over
+  // the columns of a block (six of 16).
   __device__ __forceinline__ void pairs(const char* sQ, const char* sK, const char* sV, const char* sE,
-                                        const LinGates& g, int n, char* sP, float* sM) {
-#pragma unroll
-    for (int half = 0; half < 4 / NW; ++half) {
-      const int a = NW == 4 ? w : (half == 0 ? w : 3 - w);
+                                        const Gates& g, int n, char* sP, float* sM) {
+#pragma unroll 1
+    for (int blk = w; blk < 6; blk += NW) {
+      int a, kb;
+      lin_block_at<kRev>(blk, a, kb);
       const float ah = g.hi[16 * a + ln], al = g.lo[16 * a + ln];
-      Fr qf[CK / 32];
-#pragma unroll
-      for (int p = 0; p < CK / 32; ++p) qf[p] = TK::template row8<Eng>(sQ, 16 * a + ln, 32 * p + 8 * gq);
-      Fr ef[MODE == kLinDK ? CV / 32 : 1];
+      // both tiles of the block, also where the triangle leaves one out (2 of 6)
+      f32x4 acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+      f32x4 acc2[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
       float cm = 0.0f;                     // DK: column sums of M
+#pragma unroll
+      for (int p = 0; p < CK / 32; ++p) {
+        const Fr qf = TK::template row8<Eng>(sQ, 16 * a + ln, 32 * p + 8 * gq);
+#pragma unroll
+        for (int bb = 0; bb < 2; ++bb)
+          Eng::mma(acc[bb], TK::template row8<Eng>(sK, 32 * kb + 16 * bb + ln, 32 * p + 8 * gq), qf);
+      }
       if constexpr (MODE == kLinDK) {
 #pragma unroll
-        for (int p = 0; p < CV / 32; ++p) ef[p] = TV::template row8<Eng>(sE, 16 * a + ln, 32 * p + 8 * gq);
+        for (int p = 0; p < CV / 32; ++p) {
+          const Fr ef = TV::template row8<Eng>(sE, 16 * a + ln, 32 * p + 8 * gq);
+#pragma unroll
+          for (int bb = 0; bb < 2; ++bb)
+            Eng::mma(acc2[bb], TV::template row8<Eng>(sV, 32 * kb + 16 * bb + ln, 32 * p + 8 * gq), ef);
+        }
       }
+      float pw[8];
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        if (!lin_has<kRev>(a, kb)) continue;
-        float pw[8];
+      for (int bb = 0; bb < 2; ++bb) {
+        const int b = 2 * kb + bb;
+        const f32x4 bh = *reinterpret_cast<const f32x4*>(&g.hi[16 * b + 4 * gq]);
+        const f32x4 bl = *reinterpret_cast<const f32x4*>(&g.lo[16 * b + 4 * gq]);
 #pragma unroll
-        for (int bb = 0; bb < 2; ++bb) {
-          const int b = 2 * kb + bb;
-          f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f}, acc2 = acc;
-          const bool in = kRev ? b >= a : b <= a;
-          if (in) {
-#pragma unroll
-            for (int p = 0; p < CK / 32; ++p)
-              Eng::mma(acc, TK::template row8<Eng>(sK, 16 * b + ln, 32 * p + 8 * gq), qf[p]);
-            if constexpr (MODE == kLinDK) {
-#pragma unroll
-              for (int p = 0; p < CV / 32; ++p)
-                Eng::mma(acc2, TV::template row8<Eng>(sV, 16 * b + ln, 32 * p + 8 * gq), ef[p]);
-            }
-          }
-          const f32x4 bh = *reinterpret_cast<const f32x4*>(&g.hi[16 * b + 4 * gq]);
-          const f32x4 bl = *reinterpret_cast<const f32x4*>(&g.lo[16 * b + 4 * gq]);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int ia = 16 * a + ln, ib = 16 * b + 4 * gq + r;
-            const float d = kRev ? (bh[r] - ah) + (bl[r] - al) : (ah - bh[r]) + (al - bl[r]);
-            pw[4 * bb + r] = (kRev ? ib >= ia && ib < n : ib <= ia) ? acc[r] * lin_exp(d) : 0.0f;
-            if constexpr (MODE == kLinDK) {
-              const float m = ib > ia ? acc2[r] * pw[4 * bb + r] : 0.0f;
-              cm += m;
-              const float rm = group_sum<16>(m);
-              if (in && ln == 0) sM[16 * lin_tri(a, b) + 4 * gq + r] = rm;
-            }
+        for (int r = 0; r < 4; ++r) {
+          const int ia = 16 * a + ln, ib = 16 * b + 4 * gq + r;
+          const float d = kRev ? (bh[r] - ah) + (bl[r] - al) : (ah - bh[r]) + (al - bl[r]);
+          pw[4 * bb + r] = (kRev ? ib >= ia && ib < n : ib <= ia) ? acc[bb][r] * lin_exp(d) : 0.0f;
+          if constexpr (MODE == kLinDK) {
+            const float m = ib > ia ? acc2[bb][r] * pw[4 * bb + r] : 0.0f;
+            cm += m;
+            const float rm = group_sum<16>(m);
+            if (b >= a && ln == 0) sM[16 * lin_tri(a, b) + 4 * gq + r] = rm;
           }
         }
-        Fr pl[2];
-        Eng::split(pw, pl[0], pl[1]);
-        char* dst = sP + lin_block<kRev>(a, kb) * Eng::kPlanes * kFrag + l64 * (kFrag / 64);
-#pragma unroll
-        for (int k = 0; k < Eng::kPlanes; ++k) Eng::st((E*)(dst + k * kFrag), pl[k]);
       }
+      Fr pl[2];
+      Eng::split(pw, pl[0], pl[1]);
+      char* dst = sP + blk * Eng::kPlanes * kFrag + l64 * (kFrag / 64);
+#pragma unroll
+      for (int k = 0; k < Eng::kPlanes; ++k) Eng::st((E*)(dst + k * kFrag), pl[k]);
       if constexpr (MODE == kLinDK) {
         cm += __shfl_xor(cm, 16, 64);
         cm += __shfl_xor(cm, 32, 64);
-        if (gq == 0) sM[160 + 16 * a + ln] = cm;
+        if (gq == 0) sM[160 + 16 * blk + ln] = cm;
       }
     }
   }
 
   __device__ __forceinline__ void take_v(const char* sV) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) vf[t][kb] = TV::template cols8<Eng>(sV, kb, 32 * w + 4 * t, ln, gq);
+    for (int kb = 0; kb < 2; ++kb) vf[kb] = TV::template cols8<Eng, 4>(sV, kb, 16 * w, ln, gq);
   }
 
   // State part: O^T = X^T Q^T, scaled by the rows' weights.
-  __device__ __forceinline__ void state_part(const char* sQ, const LinGates& g) {
+  __device__ __forceinline__ void state_part(const char* sQ, const Gates& g) {
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt) O[rt][0] = O[rt][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int rt = 0; rt < 4; ++rt) O[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int p = 0; p < CK / 32; ++p) {
-      Fr xf[2][3], qf[4];
+      Fr xf[3], qf[4];
 #pragma unroll
       for (int rt = 0; rt < 4; ++rt) qf[rt] = TK::template row8<Eng>(sQ, 16 * rt + ln, 32 * p + 8 * gq);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const float x8[8] = {X[2 * p][t][0], X[2 * p][t][1], X[2 * p][t][2], X[2 * p][t][3],
-                             X[2 * p + 1][t][0], X[2 * p + 1][t][1], X[2 * p + 1][t][2], X[2 * p + 1][t][3]};
-        if constexpr (kXPlanes == 3) Eng::split3(x8, xf[t][0], xf[t][1], xf[t][2]);
-        else Eng::split(x8, xf[t][0], xf[t][1]);
-      }
+      const float x8[8] = {X[2 * p][0], X[2 * p][1], X[2 * p][2], X[2 * p][3],
+                           X[2 * p + 1][0], X[2 * p + 1][1], X[2 * p + 1][2], X[2 * p + 1][3]};
+      if constexpr (kXPlanes == 3) Eng::split3(x8, xf[0], xf[1], xf[2]);
+      else Eng::split(x8, xf[0], xf[1]);
 #pragma unroll
       for (int k = 0; k < kXPlanes; ++k)
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-          for (int t = 0; t < 2; ++t) Eng::mma(O[rt][t], xf[t][k], qf[rt]);
+        for (int rt = 0; rt < 4; ++rt) Eng::mma(O[rt], xf[k], qf[rt]);
     }
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
       const float s = g.in[16 * rt + ln];
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) O[rt][t][r] *= s;
+      for (int r = 0; r < 4; ++r) O[rt][r] *= s;
     }
   }
-  // DQ, DK: the wave's columns of r_i, c_j; e(row, x): eight columns of E.
+  // DQ, DK: the wave's columns of r_i, c_j; e(row): its four columns of E.
   template <class F>
   __device__ __forceinline__ void dots(int n, float* sR, F e) const {
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
       const int row = 16 * rt + ln;
-      float d = 0.0f, ev[8];
-      e(row, ev);
+      const f32x4 ev = e(row);
+      float d = 0.0f;
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) d = fmaf(O[rt][t][r], ev[4 * t + r], d);
+      for (int r = 0; r < 4; ++r) d = fmaf(O[rt][r], ev[r], d);
       d += __shfl_xor(d, 16, 64);
       d += __shfl_xor(d, 32, 64);
       if (gq == 0) sR[kChunk * w + row] = row < n ? d : 0.0f;
@@ -562,25 +559,23 @@ struct LinWalk {
           if (!lin_has<kRev>(rt, kb)) continue;
           const Fr pf = Eng::ld((const E*)(sP + (lin_block<kRev>(rt, kb) * Eng::kPlanes + k) * kFrag +
                                            l64 * (kFrag / 64)));
-#pragma unroll
-          for (int t = 0; t < 2; ++t) Eng::mma(O[rt][t], vf[t][kb], pf);
+          Eng::mma(O[rt], vf[kb], pf);
         }
   }
   __device__ __forceinline__ void store_out(int c, int n) const {
+    const bool wide = sizeof(E) == 4 || A.out_f32;
+    // a chunk's rows lie within 2^31 bytes of its first: 32-bit offsets from there
+    char* base = (char*)A.out + (((int64_t)L.sg.t0 + kChunk * c) * A.os + (int64_t)L.vh * CV) * (wide ? 4 : 2);
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
       const int row = 16 * rt + ln;
       if (row >= n) continue;
-      const int64_t at = ((int64_t)L.sg.t0 + kChunk * c + row) * A.os + (int64_t)L.vh * CV + 32 * w + 8 * gq;
-      if (sizeof(E) == 4 || A.out_f32) {
-        float* o = (float*)A.out + at;
-        *reinterpret_cast<f32x4*>(o) = O[rt][0];
-        *reinterpret_cast<f32x4*>(o + 4) = O[rt][1];
-      } else {
-        *reinterpret_cast<uint4*>((uint16_t*)A.out + at) =
-            make_uint4(pack_bf16x2(O[rt][0][0], O[rt][0][1]), pack_bf16x2(O[rt][0][2], O[rt][0][3]),
-                       pack_bf16x2(O[rt][1][0], O[rt][1][1]), pack_bf16x2(O[rt][1][2], O[rt][1][3]));
-      }
+      const uint32_t at = (uint32_t)(row * A.os + 16 * w + 4 * gq);
+      if (wide)
+        *reinterpret_cast<f32x4*>(base + 4 * at) = O[rt];
+      else
+        *reinterpret_cast<uint2*>(base + 2 * at) =
+            make_uint2(pack_bf16x2(O[rt][0], O[rt][1]), pack_bf16x2(O[rt][2], O[rt][3]));
     }
   }
   // DQ's light wave: r_i; DK's: dg of the chunk's tokens.
@@ -601,7 +596,11 @@ struct LinWalk {
 #pragma unroll
       for (int a = 0; a < 4; ++a)
         if (a <= (l64 >> 4)) rm += (double)sM[16 * lin_tri(a, l64 >> 4) + (l64 & 15)];
-      const double own = rm + (double)rdot - (double)sM[160 + l64];
+      double cm = 0.0;                     // column sum, over the row blocks
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+        if (lin_has<true>(l64 >> 4, kb)) cm += (double)sM[160 + 16 * lin_block<true>(l64 >> 4, kb) + (l64 & 15)];
+      const double own = rm + (double)rdot - cm;
       const double head = wave_prefix_f64(own), pre = wave_prefix_f64((double)d);
       const double Xc = Y - last_lane(pre);
       const double dg = (last_lane(head) - head + own) + (pre - (double)d) + Xc;
@@ -614,53 +613,48 @@ struct LinWalk {
   }
 
   // X <- e^(G_C) X + sum_b out_b K_b V_b^T
-  __device__ __forceinline__ void update(const char* sK, const LinGates& g) {
-    const float dec = g.decay;
+  __device__ __forceinline__ void update(const char* sK, const Gates& g) {
+    if constexpr (MODE != kLinStF) {
+      const float dec = lin_decay(g);
 #pragma unroll
-    for (int tr = 0; tr < RT; ++tr)
+      for (int tr = 0; tr < RT; ++tr)
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) X[tr][t][r] *= dec;
+        for (int r = 0; r < 4; ++r) X[tr][r] *= dec;
+    }
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       const f32x4 w0 = *reinterpret_cast<const f32x4*>(&g.out[32 * kb + 4 * gq]);
       const f32x4 w1 = *reinterpret_cast<const f32x4*>(&g.out[32 * kb + 16 + 4 * gq]);
-      Fr wv[2][3];
+      Fr wv[3];
+      float x8[8];
+      if constexpr (Eng::kSplit) {
+        const uint4 u = __builtin_bit_cast(uint4, vf[kb]);
+        x8[0] = bf16_lo(u.x) * w0[0]; x8[1] = bf16_hi(u.x) * w0[1];
+        x8[2] = bf16_lo(u.y) * w0[2]; x8[3] = bf16_hi(u.y) * w0[3];
+        x8[4] = bf16_lo(u.z) * w1[0]; x8[5] = bf16_hi(u.z) * w1[1];
+        x8[6] = bf16_lo(u.w) * w1[2]; x8[7] = bf16_hi(u.w) * w1[3];
+      } else {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        float x8[8];
-        if constexpr (Eng::kSplit) {
-          const uint4 u = __builtin_bit_cast(uint4, vf[t][kb]);
-          x8[0] = bf16_lo(u.x) * w0[0]; x8[1] = bf16_hi(u.x) * w0[1];
-          x8[2] = bf16_lo(u.y) * w0[2]; x8[3] = bf16_hi(u.y) * w0[3];
-          x8[4] = bf16_lo(u.z) * w1[0]; x8[5] = bf16_hi(u.z) * w1[1];
-          x8[6] = bf16_lo(u.w) * w1[2]; x8[7] = bf16_hi(u.w) * w1[3];
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x8[j] = vf[t][kb].v[j] * (j < 4 ? w0[j] : w1[j & 3]);
-        }
-        Eng::split3(x8, wv[t][0], wv[t][1], wv[t][2]);
+        for (int j = 0; j < 8; ++j) x8[j] = vf[kb].v[j] * (j < 4 ? w0[j] : w1[j & 3]);
       }
-      constexpr int kStep = 4;             // row tiles whose products alternate
+      Eng::split3(x8, wv[0], wv[1], wv[2]);
+      constexpr int kStep = Eng::kSplit ? 4 : 2;   // row tiles whose products alternate
 #pragma unroll
       for (int tr0 = 0; tr0 < RT; tr0 += kStep) {
         Fr kf[kStep];
 #pragma unroll
         for (int i = 0; i < kStep; ++i)
-          kf[i] = TK::template cols8<Eng>(sK, kb, 32 * ((tr0 + i) / 2) + 4 * (i & 1), ln, gq);
+          kf[i] = TK::template cols8<Eng, 8>(sK, kb, 32 * ((tr0 + i) / 2) + 4 * (i & 1), ln, gq);
 #pragma unroll
         for (int k = 0; k < kVPlanes; ++k)
 #pragma unroll
-          for (int i = 0; i < kStep; ++i)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) Eng::mma(X[tr0 + i][t], kf[i], wv[t][k]);
+          for (int i = 0; i < kStep; ++i) Eng::mma(X[tr0 + i], kf[i], wv[k]);
       }
     }
   }
 };
 
-// Forward passes and state passes: one role, CV / 32 waves.
+// Forward passes and state passes: one role, CV / 16 waves.
 template <class Eng, int CK, int CV, int MODE>
 struct LinLds {
   using E = typename Eng::E;
@@ -672,21 +666,21 @@ struct LinLds {
   static constexpr int Q = V + kVTiles * W::TV::kBytes;
   static constexpr int P = Q + (W::kOut ? W::TK::kBytes : 0);
   static constexpr int G = P + (W::kOut ? W::kPBytes : 0);
-  static constexpr int R = G + 2 * (int)sizeof(LinGates);
+  static constexpr int R = G + 2 * (int)sizeof(typename W::Gates);
   static constexpr int kBytes = R + (W::kDots ? W::NW * kChunk * 4 : 0);
 };
 
 template <class Eng, int CK, int CV, int MODE>
-__global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(LinScan A) {
+__global__ __launch_bounds__(4 * CV, Eng::kSplit ? CV / 32 : CV / 64) void lin_scan_kernel(LinScan A) {
   using E = typename Eng::E;
   using Lds = LinLds<Eng, CK, CV, MODE>;
   using W = LinWalk<Eng, CK, CV, MODE>;
   using RowsK = LinRows<E, CK, W::NT>;
   using RowsV = LinRows<E, CV, W::NT>;
-  constexpr bool kOut = W::kOut, kDots = W::kDots, kDirect = Lds::kDirect, kRev = W::kRev;
+  constexpr bool kOut = W::kOut, kDots = W::kDots, kDirect = Lds::kDirect, kRev = W::kRev, kBack = W::kBack;
 
   extern __shared__ char smem[];
-  LinGates* sG = reinterpret_cast<LinGates*>(smem + Lds::G);
+  auto* sG = reinterpret_cast<typename W::Gates*>(smem + Lds::G);
   float* sR = reinterpret_cast<float*>(smem + Lds::R);
   const uint32_t lds0 = lds_base_u32(smem);
 
@@ -705,7 +699,7 @@ __global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(L
   const E* pE = kDots ? (const E*)A.E + t0 * A.es + (int64_t)(L.vh / A.ed) * CV : nullptr;
   // the rows of walk step it: K into its tile, V and Q into theirs
   auto ask = [&](int it) {
-    const int c = L.chunk<kRev>(it), n = L.rows(c);
+    const int c = L.chunk<kBack>(it), n = L.rows(c);
     const int64_t r0 = (int64_t)kChunk * c;
     RowsK::ask(lds0 + Lds::K + (it & 1) * W::TK::kBytes, pK + r0 * A.ks, A.ks, n);
     RowsV::ask(lds0 + Lds::V + (kOut ? 0 : (it & 1) * W::TV::kBytes), pV + r0 * A.vs, A.vs, n);
@@ -716,17 +710,17 @@ __global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(L
   float rg = 0.0f;                         // light wave: the next step's log decays
   double Gsum = 0.0;                       // and the segment's sum
   if (w == W::kLight && nch > 0) {
-    Gsum += lin_gates<kRev>(sG[0], L.gate<kRev>(0, A.g_row), L.rows(L.chunk<kRev>(0)));
-    rg = L.gate<kRev>(1, A.g_row);
+    Gsum += lin_gates<kRev>(sG[0], L.gate<kBack>(0, A.g_row), L.rows(L.chunk<kBack>(0)));
+    rg = L.gate<kBack>(1, A.g_row);
   }
   if (kDirect && nch > 0) ask(0);
   S.load_state();
 
 #pragma unroll 1
   for (int it = 0; it < nch; ++it) {
-    const int c = L.chunk<kRev>(it), n = L.rows(c);
+    const int c = L.chunk<kBack>(it), n = L.rows(c);
     const int64_t r0 = (int64_t)kChunk * c;
-    const LinGates& g = sG[it & 1];
+    const auto& g = sG[it & 1];
     const char* sK = smem + Lds::K + (kDirect ? (it & 1) * W::TK::kBytes : 0);
     const char* sV = smem + Lds::V + (kDirect && !kOut ? (it & 1) * W::TV::kBytes : 0);
     if constexpr (kDirect) {
@@ -741,15 +735,15 @@ __global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(L
     }
     if constexpr (kOut) S.pairs(smem + Lds::Q, sK, sV, nullptr, g, n, smem + Lds::P, nullptr);
     if (w == W::kLight && it + 1 < nch) {
-      Gsum += lin_gates<kRev>(sG[(it + 1) & 1], rg, L.rows(L.chunk<kRev>(it + 1)));
-      rg = L.gate<kRev>(it + 2, A.g_row);
+      Gsum += lin_gates<kRev>(sG[(it + 1) & 1], rg, L.rows(L.chunk<kBack>(it + 1)), MODE == kLinStF ? Gsum : 0.0);
+      rg = L.gate<kBack>(it + 2, A.g_row);
     }
     S.take_v(sV);
     if constexpr (kOut) {
       S.state_part(smem + Lds::Q, g);
       if constexpr (kDots)
-        S.dots(n, sR, [&](int row, float(&x)[8]) {
-          ld8(pE + (r0 + (row < n ? row : n - 1)) * A.es + 32 * w + 8 * S.gq, x);
+        S.dots(n, sR, [&](int row) {
+          return ld4(pE + (r0 + (row < n ? row : n - 1)) * A.es + 16 * w + 4 * S.gq);
         });
       barrier_lds();
       if (kDirect && it + 1 < nch) ask(it + 1);
@@ -768,8 +762,8 @@ __global__ __launch_bounds__(2 * CV, Eng::kSplit ? 2 : 1) void lin_scan_kernel(L
 }
 
 // The reverse passes of the backward, dk (with dg) and dv, as two roles of
-// one workgroup: the first DK / 32 waves walk X = dS [TW, DK] for dk, the next
-// TW / 32 waves X = dS^T [DK, TW] for dv.  They share the chunk's rows of q, k,
+// one workgroup: the first DK / 16 waves walk X = dS [TW, DK] for dk, the next
+// TW / 16 waves X = dS^T [DK, TW] for dv.  They share the chunk's rows of q, k,
 // v and d_o in LDS (q and d_o, which both still read after the second
 // barrier, have two tiles), so each is read once.
 template <class Eng, int DK, int TW>
@@ -787,26 +781,27 @@ struct LinRevLds {
   static constexpr int PK = V + TV;
   static constexpr int PV = PK + WK::kPBytes;
   static constexpr int G = PV + WV::kPBytes;
-  static constexpr int R = G + 2 * (int)sizeof(LinGates);
+  static constexpr int R = G + 2 * (int)sizeof(LinGatesRev);
   static constexpr int M = R + WK::NW * kChunk * 4;
-  static constexpr int Y = M + (10 * 16 + kChunk) * 4;
-  static constexpr int kBytes = Y + 32;
+  static constexpr int Y = M + (10 + 6) * 16 * 4;
+  static constexpr int kBytes = Y + WK::NW * 8;
 };
 
 // A: the dk pass (Q = v, K = d_o, V = q, E = k); B: the dv pass.
 template <class Eng, int DK, int TW>
-__global__ __launch_bounds__(2 * (DK + TW), Eng::kSplit ? 2 : 1) void lin_rev_kernel(LinScan A, LinScan B) {
+__global__ __launch_bounds__(4 * (DK + TW), (DK + TW) / 64 * (sizeof(typename Eng::E) == 2 && DK + TW == 128 ? 2 : 1))
+void lin_rev_kernel(LinScan A, LinScan B) {
   using E = typename Eng::E;
   using Lds = LinRevLds<Eng, DK, TW>;
   using WK = typename Lds::WK;
   using WV = typename Lds::WV;
-  constexpr int NT = 2 * (DK + TW);
+  constexpr int NT = 4 * (DK + TW);
   constexpr bool kDirect = Lds::kDirect;
   using RowsD = LinRows<E, DK, NT>;
   using RowsT = LinRows<E, TW, NT>;
 
   extern __shared__ char smem[];
-  LinGates* sG = reinterpret_cast<LinGates*>(smem + Lds::G);
+  LinGatesRev* sG = reinterpret_cast<LinGatesRev*>(smem + Lds::G);
   float* sR = reinterpret_cast<float*>(smem + Lds::R);
   float* sM = reinterpret_cast<float*>(smem + Lds::M);
   double* sY = reinterpret_cast<double*>(smem + Lds::Y);
@@ -859,7 +854,7 @@ __global__ __launch_bounds__(2 * (DK + TW), Eng::kSplit ? 2 : 1) void lin_rev_ke
 #pragma unroll 1
     for (int it = 0; it < nch; ++it) {
       const int c = L.chunk<true>(it), n = L.rows(c);
-      const LinGates& g = sG[it & 1];
+      const LinGatesRev& g = sG[it & 1];
       const char* sQ = smem + Lds::Q + (kDirect ? (it & 1) * Lds::TD : 0);
       const char* sO = smem + Lds::O + (kDirect ? (it & 1) * Lds::TV : 0);
       begin(it);
@@ -867,10 +862,7 @@ __global__ __launch_bounds__(2 * (DK + TW), Eng::kSplit ? 2 : 1) void lin_rev_ke
       S.pairs(smem + Lds::V, sO, sQ, smem + Lds::K, g, n, smem + Lds::PK, sM);
       S.take_v(sQ);
       S.state_part(smem + Lds::V, g);
-      S.dots(n, sR, [&](int row, float(&x)[8]) {
-        const auto f = WK::TV::template row8<Eng>(smem + Lds::K, row, 32 * w + 8 * S.gq);
-        ld8((const E*)&f, x);
-      });
+      S.dots(n, sR, [&](int row) { return WK::TV::row4(smem + Lds::K, row, 16 * w + 4 * S.gq); });
       asm volatile("" ::"v"(S.rdot));      // its load ends before the next chunk's are asked for
       middle(it);
       S.pair_part(smem + Lds::PK);
@@ -896,7 +888,7 @@ __global__ __launch_bounds__(2 * (DK + TW), Eng::kSplit ? 2 : 1) void lin_rev_ke
 #pragma unroll 1
     for (int it = 0; it < nch; ++it) {
       const int c = L.chunk<true>(it), n = L.rows(c);
-      const LinGates& g = sG[it & 1];
+      const LinGatesRev& g = sG[it & 1];
       const char* sQ = smem + Lds::Q + (kDirect ? (it & 1) * Lds::TD : 0);
       const char* sO = smem + Lds::O + (kDirect ? (it & 1) * Lds::TV : 0);
       begin(it);
@@ -924,7 +916,7 @@ static hipError_t lin_scan_go(const LinScan& A, int64_t slots, hipStream_t strea
   const auto kern = lin_scan_kernel<Eng, CK, CV, MODE>;
   const hipError_t e = set_dyn_lds_once(once, (const void*)kern, lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(slots * A.VH)), dim3(2 * CV), lds, stream, A);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(slots * A.VH)), dim3(4 * CV), lds, stream, A);
   return hipGetLastError();
 }
 
@@ -948,7 +940,7 @@ static hipError_t lin_rev_go(const LinScan& A, const LinScan& B, int64_t slots, 
   const auto kern = lin_rev_kernel<Eng, DK, TW>;
   const hipError_t e = set_dyn_lds_once(once, (const void*)kern, lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)(slots * A.VH)), dim3(2 * (DK + TW)), lds, stream, A, B);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(slots * A.VH)), dim3(4 * (DK + TW)), lds, stream, A, B);
   return hipGetLastError();
 }
 template <class Eng>
