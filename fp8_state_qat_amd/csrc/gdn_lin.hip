@@ -9,23 +9,22 @@ namespace {
 // Segment sums to segment starts: seg[s] holds the segment's own sum and
 // becomes the state at its start (forward: before the first token; reverse:
 // after the last), cur <- e^(its decays) cur + sum.  One thread per four
-// state values, blockIdx.y: sequence.
+// state values, blockIdx.y: sequence, blockIdx.z: direction.
+struct LinStarts {
+  float* seg;
+  const float* decay;
+  const float* first;
+};
 template <bool kRev>
-__global__ __launch_bounds__(kThreads) void lin_starts_kernel(float* __restrict__ seg,
-                                                              const float* __restrict__ decay,
-                                                              const float* __restrict__ first,
-                                                              const int32_t* __restrict__ cu, int N, int64_t T,
-                                                              int seglen, int VH, int st4) {
-  const LinSeg q = lin_find(cu, N, T, seglen, blockIdx.y, true);
-  if (q.bad) return;
+__device__ __forceinline__ void lin_starts(const LinStarts& P, const LinSeg& q, int VH, int st4) {
   const int i = blockIdx.x * kThreads + threadIdx.x;
   const int vh = i / st4, e = i % st4;
   if (vh >= VH) return;
-  float4* S = reinterpret_cast<float4*>(seg);
+  float4* S = reinterpret_cast<float4*>(P.seg);
   float4 cur = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (first != nullptr) cur = reinterpret_cast<const float4*>(first)[((int64_t)q.n * VH + vh) * st4 + e];
+  if (P.first != nullptr) cur = reinterpret_cast<const float4*>(P.first)[((int64_t)q.n * VH + vh) * st4 + e];
   auto at = [&](int j) { return (int64_t)(q.slot0 + (kRev ? q.nseg - 1 - j : j)) * VH + vh; };
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 8;
   float4 own[kAhead];
   float dec[kAhead];
   for (int j0 = 0; j0 < q.nseg; j0 += kAhead) {
@@ -33,7 +32,7 @@ __global__ __launch_bounds__(kThreads) void lin_starts_kernel(float* __restrict_
     for (int k = 0; k < kAhead; ++k)
       if (j0 + k < q.nseg - 1) {   // the last segment of the walk has no sum
         own[k] = S[at(j0 + k) * st4 + e];
-        dec[k] = decay[at(j0 + k)];
+        dec[k] = P.decay[at(j0 + k)];
       }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
@@ -49,89 +48,107 @@ __global__ __launch_bounds__(kThreads) void lin_starts_kernel(float* __restrict_
     }
   }
 }
+__global__ __launch_bounds__(kThreads) void lin_starts_kernel(LinStarts F, LinStarts R,
+                                                              const int32_t* __restrict__ cu, int N, int64_t T,
+                                                              int seglen, int VH, int st4) {
+  const LinSeg q = lin_find(cu, N, T, seglen, blockIdx.y, true);
+  if (q.bad) return;
+  if (blockIdx.z == 0) lin_starts<false>(F, q, VH, st4);
+  else lin_starts<true>(R, q, VH, st4);
+}
 
-// Sums of the R virtual heads that share a query/key head, in fp32 and in
-// order, for dq (blockIdx.y 0) and dk (1): four values a thread, rows
-// [cu[0], cu[N]) only.
+// The sums that end a backward, one launch.  blockIdx.y 0, 1: dq and dk, where
+// R virtual heads share a query/key head, in fp32 and in order, four values a
+// thread, rows [cu[0], cu[N]) only.  blockIdx.y 2: dg, from the tiles of a
+// token's value rows, or for fixed decays from the segments' sums in fp64, one
+// workgroup a head.  The caller leaves out what it does not need.
+struct LinReduce {
+  const float* part_q;
+  const float* part_k;
+  void* dq;
+  void* dk;
+  const float* dg_tok;
+  const double* dg_part;
+  float* dg;
+  const int32_t* cu;
+  const int32_t* status;
+  int64_t slots, row4;
+  int N, R, d4, H, VH, tiles;
+  int y0;               // blockIdx.y of the launch's first part
+};
+
 template <typename T>
-__global__ __launch_bounds__(kThreads) void lin_reduce_qk_kernel(const float* __restrict__ part_q,
-                                                                 const float* __restrict__ part_k,
-                                                                 T* __restrict__ dq, T* __restrict__ dk,
-                                                                 const int32_t* __restrict__ cu,
-                                                                 const int32_t* __restrict__ status, int N, int R,
-                                                                 int d4, int64_t row4) {
-  if (*status != 0) return;
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x + (int64_t)cu[0] * row4;
-  if (i >= (int64_t)cu[N] * row4) return;
-  const int64_t head = i / d4;             // row * qk_heads + head
-  const float4* p = reinterpret_cast<const float4*>(blockIdx.y ? part_k : part_q) + head * R * d4 + i % d4;
+__device__ __forceinline__ void lin_reduce_qk(const LinReduce& A, const float* part, T* out0) {
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x + (int64_t)A.cu[0] * A.row4;
+  if (i >= (int64_t)A.cu[A.N] * A.row4) return;
+  const int64_t head = i / A.d4;           // row * qk_heads + head
+  const float4* p = reinterpret_cast<const float4*>(part) + head * A.R * A.d4 + i % A.d4;
   float4 s = p[0];
-  for (int r = 1; r < R; ++r) {
-    const float4 x = p[(int64_t)r * d4];
+  for (int r = 1; r < A.R; ++r) {
+    const float4 x = p[(int64_t)r * A.d4];
     s.x += x.x;
     s.y += x.y;
     s.z += x.z;
     s.w += x.w;
   }
-  T* out = (blockIdx.y ? dk : dq) + 4 * i;
+  T* out = out0 + 4 * i;
   if constexpr (sizeof(T) == 2)
     *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
   else
     *reinterpret_cast<float4*>(out) = s;
 }
 
-// dg of a token's head from the tiles of its value rows.
-__global__ __launch_bounds__(kThreads) void lin_reduce_dg_kernel(const float* __restrict__ part,
-                                                                 float* __restrict__ dg,
-                                                                 const int32_t* __restrict__ cu,
-                                                                 const int32_t* __restrict__ status, int N, int H,
-                                                                 int tiles) {
-  if (*status != 0) return;
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x + (int64_t)cu[0] * H;
-  if (i >= (int64_t)cu[N] * H) return;
-  float s = part[i * tiles];
-  for (int t = 1; t < tiles; ++t) s += part[i * tiles + t];
-  dg[i] = s;
-}
-
-// dg of a head's fixed decay: the segments' sums in fp64, one workgroup a head.
-__global__ __launch_bounds__(kThreads) void lin_reduce_dg_head_kernel(const double* __restrict__ part,
-                                                                      float* __restrict__ dg,
-                                                                      const int32_t* __restrict__ status,
-                                                                      int64_t slots, int VH, int tiles) {
-  __shared__ double s[kThreads];
-  if (*status != 0) return;
-  double a = 0.0;
-  for (int64_t i = threadIdx.x; i < slots * tiles; i += kThreads)
-    a += part[(i / tiles) * VH + (int64_t)blockIdx.x * tiles + i % tiles];
-  s[threadIdx.x] = a;
-  __syncthreads();
-  for (int off = kThreads / 2; off >= 1; off >>= 1) {
-    if ((int)threadIdx.x < off) s[threadIdx.x] += s[threadIdx.x + off];
+template <typename T>
+__global__ __launch_bounds__(kThreads) void lin_reduce_kernel(LinReduce A) {
+  __shared__ double sum[kThreads];
+  if (*A.status != 0) return;
+  const int y = blockIdx.y + A.y0;
+  if (y < 2) {
+    lin_reduce_qk<T>(A, y ? A.part_k : A.part_q, (T*)(y ? A.dk : A.dq));
+  } else if (A.dg_tok != nullptr) {
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x + (int64_t)A.cu[0] * A.H;
+    if (i >= (int64_t)A.cu[A.N] * A.H) return;
+    float s = A.dg_tok[i * A.tiles];
+    for (int t = 1; t < A.tiles; ++t) s += A.dg_tok[i * A.tiles + t];
+    A.dg[i] = s;
+  } else if ((int)blockIdx.x < A.H) {
+    double a = 0.0;
+    for (int64_t i = threadIdx.x; i < A.slots * A.tiles; i += kThreads)
+      a += A.dg_part[(i / A.tiles) * A.VH + (int64_t)blockIdx.x * A.tiles + i % A.tiles];
+    sum[threadIdx.x] = a;
     __syncthreads();
+    for (int off = kThreads / 2; off >= 1; off >>= 1) {
+      if ((int)threadIdx.x < off) sum[threadIdx.x] += sum[threadIdx.x + off];
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) A.dg[blockIdx.x] = (float)sum[0];
   }
-  if (threadIdx.x == 0) dg[blockIdx.x] = (float)s[0];
 }
 
 // Value rows are taken in tiles of 128 where they divide into them, else 64.
 int lin_tile(int dv) { return dv % 128 == 0 ? 128 : 64; }
 
 // Rows of a segment: whole sequences when the (sequence, head) pairs alone
-// fill the card, else enough segments for that, of at least 128 rows.  The
+// fill the card, else enough segments for that, down to single chunks (with
+// two chunks at least, 4 heads of 512 tokens took 25 us forward and 53 backward
+// instead of 21 and 40, ragged fp32 prompts 64 instead of 53).  The
 // scan's workgroups fit a compute unit twice, with fp32 tiles of 128 key
 // channels once (8 heads of 128 x 128, 6000 fp32 tokens: 106 us forward and
 // 328 backward with 256 units, 119 and 374 with 512; 16 bf16 heads, 32k
 // tokens: 239 with 256, 231 with 512).
 int64_t lin_units(const gdn_lin_t& s) { return s.io_dtype == GDN_F32 && s.dk == 128 ? 256 : 512; }
-constexpr int64_t kLinMinSeg = 128;
-int lin_seglen(const gdn_lin_t& s) {
+// Forward calls of up to four chunks stay whole: one kernel instead of three
+// (130 tokens 12 us instead of 17, 192: 16 and 23, 256: 20 and 24; 384 tokens
+// the same either way).  The backward's chain a chunk is longer: 256 tokens
+// take 65 us whole and 53 in segments.
+constexpr int64_t kLinWhole = 256;
+int lin_seglen(const gdn_lin_t& s, bool bwd) {
   const int64_t VH = (int64_t)s.n_heads * (s.dv / lin_tile(s.dv));
   const int64_t units = lin_units(s);
   const int64_t whole = (s.total_tokens / kChunk + 1) * kChunk;
-  if ((int64_t)s.n_seqs * VH >= units) return (int)whole;
+  if ((int64_t)s.n_seqs * VH >= units || (!bwd && s.total_tokens <= kLinWhole)) return (int)whole;
   int64_t len = (s.total_tokens * VH + units - 1) / units;
-  if (len < kLinMinSeg) len = kLinMinSeg;
-  len = (len + kChunk - 1) / kChunk * kChunk;
+  len = len < kChunk ? kChunk : (len + kChunk - 1) / kChunk * kChunk;
   return (int)(len < whole ? len : whole);
 }
 
@@ -159,7 +176,7 @@ LinLayout lin_layout(const gdn_lin_t& s, void* ws, bool bwd) {
   L.tiles = s.dv / L.tw;
   L.VH = s.n_heads * L.tiles;
   L.R = L.VH / s.qk_heads;
-  L.seglen = lin_seglen(s);
+  L.seglen = lin_seglen(s, bwd);
   L.slots = s.total_tokens / L.seglen + s.n_seqs;
   L.split = s.total_tokens > L.seglen;
   size_t at = 0;
@@ -223,12 +240,13 @@ void set_k(LinScan& A, const Operand& o) { A.K = o.p; A.ks = o.stride; A.kd = o.
 void set_v(LinScan& A, const Operand& o) { A.V = o.p; A.vs = o.stride; A.vd = o.div; }
 void set_e(LinScan& A, const Operand& o) { A.E = o.p; A.es = o.stride; A.ed = o.div; }
 
-void starts(const gdn_lin_t& s, const LinLayout& L, float* seg, const float* dec, const float* first,
-            const int32_t* cu, bool rev, hipStream_t stream) {
+// dirs: forward alone, or both
+void starts(const gdn_lin_t& s, const LinLayout& L, const LinStarts& F, const LinStarts& R, int dirs,
+            const int32_t* cu, hipStream_t stream) {
   const int st4 = L.tw * s.dk / 4;
-  const dim3 grid((unsigned)(((int64_t)L.VH * st4 + kThreads - 1) / kThreads), s.n_seqs);
-  hipLaunchKernelGGL(rev ? lin_starts_kernel<true> : lin_starts_kernel<false>, grid, dim3(kThreads), 0, stream, seg,
-                     dec, first, cu, s.n_seqs, s.total_tokens, L.seglen, L.VH, st4);
+  const dim3 grid((unsigned)(((int64_t)L.VH * st4 + kThreads - 1) / kThreads), s.n_seqs, dirs);
+  hipLaunchKernelGGL(lin_starts_kernel, grid, dim3(kThreads), 0, stream, F, R, cu, s.n_seqs, s.total_tokens,
+                     L.seglen, L.VH, st4);
 }
 
 }  // namespace
@@ -256,7 +274,7 @@ hipError_t launch_lin_fwd(const gdn_lin_t& s, const void* q, const void* k, cons
     A.seg = L.segF;
     A.seg_decay = L.decF;
     GDN_TRY(run_scan(s, A, kLinStF, L, stream));
-    starts(s, L, L.segF, L.decF, initial_state, cu_seqlens, false, stream);
+    starts(s, L, {L.segF, L.decF, initial_state}, {}, 1, cu_seqlens, stream);
     A.status = nullptr;
   }
   set_q(A, oq);
@@ -277,20 +295,20 @@ hipError_t launch_lin_bwd(const gdn_lin_t& s, const void* q, const void* k, cons
   LinScan B = lin_base(s, L, g, cu_seqlens);
   B.status = L.status;
   if (L.split) {
-    LinScan A = B;
+    LinScan A = B, R = B;
     set_k(A, ok);
     set_v(A, ov);
     A.seg = L.segF;
     A.seg_decay = L.decF;
-    GDN_TRY(run_scan(s, A, kLinStF, L, stream));
-    A.status = B.status = nullptr;
-    set_k(A, oq);
-    set_v(A, od);
-    A.seg = L.segR;
-    A.seg_decay = L.decR;
-    GDN_TRY(run_scan(s, A, kLinStR, L, stream));
-    starts(s, L, L.segF, L.decF, initial_state, cu_seqlens, false, stream);
-    starts(s, L, L.segR, L.decR, d_final_state, cu_seqlens, true, stream);
+    set_k(R, oq);
+    set_v(R, od);
+    R.status = nullptr;
+    R.seg = L.segR;
+    R.seg_decay = L.decR;
+    GDN_TRY(s.io_dtype == GDN_BF16 ? launch_lin_sums_bf16(A, R, L.slots, stream)
+                                   : launch_lin_sums_f32(A, R, L.slots, stream));
+    B.status = nullptr;
+    starts(s, L, {L.segF, L.decF, initial_state}, {L.segR, L.decR, d_final_state}, 2, cu_seqlens, stream);
   }
   const bool sum = L.R > 1;
   const int qrow = sum ? L.VH * s.dk : qk;
@@ -335,23 +353,24 @@ hipError_t launch_lin_bwd(const gdn_lin_t& s, const void* q, const void* k, cons
   else K.dg_part = L.dgp;
   GDN_TRY(s.io_dtype == GDN_BF16 ? launch_lin_rev_bf16(K, V, L.slots, stream)
                                  : launch_lin_rev_f32(K, V, L.slots, stream));
-  if (sum && s.total_tokens > 0) {
-    const int d4 = s.dk / 4;
-    const int64_t row4 = (int64_t)s.qk_heads * d4;
-    const dim3 grid((unsigned)((s.total_tokens * row4 + kThreads - 1) / kThreads), 2);
-    if (s.io_dtype == GDN_BF16)
-      hipLaunchKernelGGL(lin_reduce_qk_kernel<uint16_t>, grid, dim3(kThreads), 0, stream, L.part_q, L.part_k,
-                         (uint16_t*)dq, (uint16_t*)dk, cu_seqlens, L.status, s.n_seqs, L.R, d4, row4);
-    else
-      hipLaunchKernelGGL(lin_reduce_qk_kernel<float>, grid, dim3(kThreads), 0, stream, L.part_q, L.part_k,
-                         (float*)dq, (float*)dk, cu_seqlens, L.status, s.n_seqs, L.R, d4, row4);
+  const bool qk_sum = sum && s.total_tokens > 0;
+  const bool dg_sum = !s.gate_per_token || (L.tiles > 1 && s.total_tokens > 0);
+  if (qk_sum || dg_sum) {
+    LinReduce A{};
+    A.part_q = L.part_q; A.part_k = L.part_k; A.dq = dq; A.dk = dk;
+    A.dg_tok = L.dgt; A.dg_part = L.dgp; A.dg = dg;
+    A.cu = cu_seqlens; A.status = L.status;
+    A.slots = L.slots;
+    A.N = s.n_seqs; A.R = L.R; A.d4 = s.dk / 4; A.row4 = (int64_t)s.qk_heads * A.d4;
+    A.H = s.n_heads; A.VH = L.VH; A.tiles = L.tiles;
+    A.y0 = qk_sum ? 0 : 2;
+    auto blocks = [](int64_t n) { return (n + kThreads - 1) / kThreads; };
+    const int64_t bq = qk_sum ? blocks(s.total_tokens * A.row4) : 0;
+    const int64_t bg = !dg_sum ? 0 : s.gate_per_token ? blocks(s.total_tokens * s.n_heads) : s.n_heads;
+    const dim3 grid((unsigned)(bq > bg ? bq : bg), (qk_sum ? 2 : 0) + (dg_sum ? 1 : 0));
+    hipLaunchKernelGGL(s.io_dtype == GDN_BF16 ? lin_reduce_kernel<uint16_t> : lin_reduce_kernel<float>, grid,
+                       dim3(kThreads), 0, stream, A);
   }
-  if (!s.gate_per_token)
-    hipLaunchKernelGGL(lin_reduce_dg_head_kernel, dim3(s.n_heads), dim3(kThreads), 0, stream, L.dgp, dg, L.status,
-                       L.slots, L.VH, L.tiles);
-  else if (L.tiles > 1 && s.total_tokens > 0)
-    hipLaunchKernelGGL(lin_reduce_dg_kernel, dim3((unsigned)((s.total_tokens * s.n_heads + kThreads - 1) / kThreads)),
-                       dim3(kThreads), 0, stream, L.dgt, dg, cu_seqlens, L.status, s.n_seqs, s.n_heads, L.tiles);
   return hipGetLastError();
 }
 

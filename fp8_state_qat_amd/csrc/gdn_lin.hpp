@@ -5,7 +5,7 @@
 
 namespace gdn {
 
-// The passes of the scan (see gdn_lin_scan.hpp); kLinDV and kLinDK run together.
+// The passes of the scan (see gdn_lin_scan.hpp); kLinStR runs with kLinStF, kLinDV with kLinDK.
 enum LinMode : int { kLinO = 0, kLinStF = 1, kLinDQ = 2, kLinStR = 3, kLinDV = 4, kLinDK = 5 };
 
 constexpr int kAnchor = 4;  // chunks between two stored states of the backward
@@ -39,6 +39,9 @@ struct LinScan {
 
 hipError_t launch_lin_scan_bf16(const LinScan& A, LinMode mode, int64_t slots, hipStream_t stream);
 hipError_t launch_lin_scan_f32(const LinScan& A, LinMode mode, int64_t slots, hipStream_t stream);
+// The state passes of the backward together: A forward, B reverse.
+hipError_t launch_lin_sums_bf16(const LinScan& A, const LinScan& B, int64_t slots, hipStream_t stream);
+hipError_t launch_lin_sums_f32(const LinScan& A, const LinScan& B, int64_t slots, hipStream_t stream);
 // The reverse passes together: A the dk pass, B the dv pass.
 hipError_t launch_lin_rev_bf16(const LinScan& A, const LinScan& B, int64_t slots, hipStream_t stream);
 hipError_t launch_lin_rev_f32(const LinScan& A, const LinScan& B, int64_t slots, hipStream_t stream);

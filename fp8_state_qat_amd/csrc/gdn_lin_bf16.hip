@@ -6,9 +6,11 @@ hipError_t launch_lin_scan_bf16(const LinScan& A, LinMode mode, int64_t slots, h
   switch (mode) {
     case kLinO: return lin_scan_mode<EngBF16, kLinO>(A, slots, stream);
     case kLinStF: return lin_scan_mode<EngBF16, kLinStF>(A, slots, stream);
-    case kLinDQ: return lin_scan_mode<EngBF16, kLinDQ>(A, slots, stream);
-    default: return lin_scan_mode<EngBF16, kLinStR>(A, slots, stream);
+    default: return lin_scan_mode<EngBF16, kLinDQ>(A, slots, stream);
   }
+}
+hipError_t launch_lin_sums_bf16(const LinScan& A, const LinScan& B, int64_t slots, hipStream_t stream) {
+  return lin_sums<EngBF16>(A, B, slots, stream);
 }
 hipError_t launch_lin_rev_bf16(const LinScan& A, const LinScan& B, int64_t slots, hipStream_t stream) {
   return lin_rev<EngBF16>(A, B, slots, stream);

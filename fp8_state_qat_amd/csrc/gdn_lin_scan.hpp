@@ -195,25 +195,21 @@ struct LinRows {
       lds_load16(p, (uint32_t)(r * stride + u * (16 / (int)sizeof(E))) * (uint32_t)sizeof(E), at + 16 * NT * i);
     }
   }
-  // Through registers; rows from n on are 0.
-  static __device__ __forceinline__ void copy(char* t, const E* p, int stride, int n) {
-    constexpr int kStep = kPer < 8 ? kPer : 8;
-    static_assert(kPer % kStep == 0, "whole steps");
-#pragma unroll 1
-    for (int i0 = 0; i0 < kPer; i0 += kStep) {
-      uint4 x[kStep];
+  // Through registers, in two halves; rows from n on are 0.
+  static __device__ __forceinline__ void fetch(uint4 (&x)[kPer], const E* p, int stride, int n) {
 #pragma unroll
-      for (int i = 0; i < kStep; ++i) {
-        const int idx = (int)threadIdx.x + NT * (i0 + i), row = idx / kUnits, u = idx % kUnits;
-        x[i] = row < n ? *reinterpret_cast<const uint4*>(p + (int64_t)row * stride + u * (16 / sizeof(E)))
-                       : make_uint4(0, 0, 0, 0);
-      }
+    for (int i = 0; i < kPer; ++i) {
+      const int idx = (int)threadIdx.x + NT * i, row = idx / kUnits, u = idx % kUnits;
+      x[i] = row < n ? *reinterpret_cast<const uint4*>(p + (uint32_t)(row * stride + u * (16 / (int)sizeof(E))))
+                     : make_uint4(0, 0, 0, 0);
+    }
+  }
+  static __device__ __forceinline__ void put(char* t, const uint4 (&x)[kPer]) {
 #pragma unroll
-      for (int i = 0; i < kStep; ++i) {
-        const int idx = (int)threadIdx.x + NT * (i0 + i), row = idx / kUnits, u = idx % kUnits;
-        if (kAll % NT != 0 && idx >= kAll) break;
-        *reinterpret_cast<uint4*>(t + row * D * sizeof(E) + 16 * lin_unit<kUnits>(row, u)) = x[i];
-      }
+    for (int i = 0; i < kPer; ++i) {
+      const int idx = (int)threadIdx.x + NT * i, row = idx / kUnits, u = idx % kUnits;
+      if (kAll % NT != 0 && idx >= kAll) break;
+      *reinterpret_cast<uint4*>(t + row * D * sizeof(E) + 16 * lin_unit<kUnits>(row, u)) = x[i];
     }
   }
 };
@@ -671,7 +667,7 @@ struct LinLds {
 };
 
 template <class Eng, int CK, int CV, int MODE>
-__global__ __launch_bounds__(4 * CV, Eng::kSplit ? CV / 32 : CV / 64) void lin_scan_kernel(LinScan A) {
+__device__ __forceinline__ void lin_scan_walk(const LinScan& A) {
   using E = typename Eng::E;
   using Lds = LinLds<Eng, CK, CV, MODE>;
   using W = LinWalk<Eng, CK, CV, MODE>;
@@ -713,7 +709,19 @@ __global__ __launch_bounds__(4 * CV, Eng::kSplit ? CV / 32 : CV / 64) void lin_s
     Gsum += lin_gates<kRev>(sG[0], L.gate<kBack>(0, A.g_row), L.rows(L.chunk<kBack>(0)));
     rg = L.gate<kBack>(1, A.g_row);
   }
-  if (kDirect && nch > 0) ask(0);
+  // fp32 rows, which do not fit twice, wait for their tiles in registers
+  uint4 xk[RowsK::kPer], xv[RowsV::kPer], xq[RowsK::kPer];
+  auto fetch = [&](int it) {
+    const int c = L.chunk<kBack>(it), n = L.rows(c);
+    const int64_t r0 = (int64_t)kChunk * c;
+    RowsK::fetch(xk, pK + r0 * A.ks, A.ks, n);
+    RowsV::fetch(xv, pV + r0 * A.vs, A.vs, n);
+    if constexpr (kOut) RowsK::fetch(xq, pQ + r0 * A.qs, A.qs, n);
+  };
+  if (nch > 0) {
+    if constexpr (kDirect) ask(0);
+    else fetch(0);
+  }
   S.load_state();
 
 #pragma unroll 1
@@ -728,10 +736,11 @@ __global__ __launch_bounds__(4 * CV, Eng::kSplit ? CV / 32 : CV / 64) void lin_s
       barrier_lds();
       if (!kOut && it + 1 < nch) ask(it + 1);
     } else {
-      RowsK::copy(smem + Lds::K, pK + r0 * A.ks, A.ks, n);
-      RowsV::copy(smem + Lds::V, pV + r0 * A.vs, A.vs, n);
-      if constexpr (kOut) RowsK::copy(smem + Lds::Q, pQ + r0 * A.qs, A.qs, n);
-      __syncthreads();
+      RowsK::put(smem + Lds::K, xk);
+      RowsV::put(smem + Lds::V, xv);
+      if constexpr (kOut) RowsK::put(smem + Lds::Q, xq);
+      barrier_lds();
+      if (it + 1 < nch) fetch(it + 1);
     }
     if constexpr (kOut) S.pairs(smem + Lds::Q, sK, sV, nullptr, g, n, smem + Lds::P, nullptr);
     if (w == W::kLight && it + 1 < nch) {
@@ -755,10 +764,23 @@ __global__ __launch_bounds__(4 * CV, Eng::kSplit ? CV / 32 : CV / 64) void lin_s
     if constexpr (MODE == kLinDQ) {
       if (S.anchor(c)) S.store_anchor(c);
     }
-    if constexpr (!kDirect) __syncthreads();
+    if constexpr (!kDirect) barrier_lds();
   }
   S.store_state();
   if (!kOut && w == W::kLight && S.l64 == 0) A.seg_decay[L.sv] = expf((float)Gsum);
+}
+
+template <class Eng, int CK, int CV, int MODE>
+__global__ __launch_bounds__(4 * CV, Eng::kSplit ? CV / 32 : CV / 64) void lin_scan_kernel(LinScan A) {
+  lin_scan_walk<Eng, CK, CV, MODE>(A);
+}
+
+// Both state passes of the backward at once: the forward states' sums A and
+// those of the states' gradients B (blockIdx.y).
+template <class Eng, int CK, int CV>
+__global__ __launch_bounds__(4 * CV, Eng::kSplit ? CV / 32 : CV / 64) void lin_sums_kernel(LinScan A, LinScan B) {
+  if (blockIdx.y == 0) lin_scan_walk<Eng, CK, CV, kLinStF>(A);
+  else lin_scan_walk<Eng, CK, CV, kLinStR>(B);
 }
 
 // The reverse passes of the backward, dk (with dg) and dv, as two roles of
@@ -835,10 +857,15 @@ void lin_rev_kernel(LinScan A, LinScan B) {
     } else {
       const int c = L.chunk<true>(it), n = L.rows(c);
       const int64_t r0 = (int64_t)kChunk * c;
-      RowsD::copy(smem + Lds::Q, pQ + r0 * A.vs, A.vs, n);
-      RowsT::copy(smem + Lds::O, pO + r0 * A.ks, A.ks, n);
-      RowsD::copy(smem + Lds::K, pK + r0 * A.es, A.es, n);
-      RowsT::copy(smem + Lds::V, pV + r0 * A.qs, A.qs, n);
+      auto copy = [&](auto rows, char* t, const E* p, int stride) {
+        uint4 x[decltype(rows)::kPer];
+        rows.fetch(x, p + r0 * stride, stride, n);
+        rows.put(t, x);
+      };
+      copy(RowsD(), smem + Lds::Q, pQ, A.vs);
+      copy(RowsT(), smem + Lds::O, pO, A.ks);
+      copy(RowsD(), smem + Lds::K, pK, A.es);
+      copy(RowsT(), smem + Lds::V, pV, A.qs);
       __syncthreads();
     }
   };
@@ -918,6 +945,24 @@ static hipError_t lin_scan_go(const LinScan& A, int64_t slots, hipStream_t strea
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3((unsigned)(slots * A.VH)), dim3(4 * CV), lds, stream, A);
   return hipGetLastError();
+}
+
+template <class Eng, int CK, int CV>
+static hipError_t lin_sums_go(const LinScan& A, const LinScan& B, int64_t slots, hipStream_t stream) {
+  static PerDeviceOnce once;
+  constexpr int lds = LinLds<Eng, CK, CV, kLinStF>::kBytes, ldsR = LinLds<Eng, CK, CV, kLinStR>::kBytes;
+  const auto kern = lin_sums_kernel<Eng, CK, CV>;
+  const hipError_t e = set_dyn_lds_once(once, (const void*)kern, lds > ldsR ? lds : ldsR);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(slots * A.VH), 2), dim3(4 * CV), lds > ldsR ? lds : ldsR, stream, A, B);
+  return hipGetLastError();
+}
+template <class Eng>
+static hipError_t lin_sums(const LinScan& A, const LinScan& B, int64_t slots, hipStream_t stream) {
+  if (A.dk == 64) return A.tw == 64 ? lin_sums_go<Eng, 64, 64>(A, B, slots, stream)
+                                    : lin_sums_go<Eng, 64, 128>(A, B, slots, stream);
+  return A.tw == 64 ? lin_sums_go<Eng, 128, 64>(A, B, slots, stream)
+                    : lin_sums_go<Eng, 128, 128>(A, B, slots, stream);
 }
 
 // CK, CV: the key channels and the value rows of a virtual head, in the order
