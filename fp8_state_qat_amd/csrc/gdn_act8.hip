@@ -4,21 +4,22 @@
 //
 // Memory bound: 2 or 4 bytes read and 1 + 4/64 written a value (the reverse
 // for the way back).  A lane takes eight consecutive columns, the eight lanes
-// of a group find its amax by DPP moves, and a thread works on kUnroll groups
-// at a stride of the whole grid, all loads of them in flight at once.
+// of a group find its amax by DPP moves, and a workgroup takes kUnroll
+// neighbouring runs of 32 groups, all its loads in flight at once (16384 x
+// 4096 bf16 there and back: 73 us, 5.6 TB/s; 75 with one run, 76 with four).
 #include "gdn_rows.hpp"
 
 namespace gdn {
 
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 2;
 
 template <typename T, bool kVec>
 __global__ __launch_bounds__(kThreads) void act_pack_kernel(const T* __restrict__ x, uint8_t* __restrict__ codes,
                                                             float* __restrict__ scales, uint32_t n_groups,
                                                             uint32_t groups, int cols) {
   const int l8 = threadIdx.x & 7;
-  const uint32_t stride = gridDim.x * (kThreads / 8);
-  const uint32_t g0 = blockIdx.x * (kThreads / 8) + (threadIdx.x >> 3);
+  constexpr uint32_t stride = kThreads / 8;
+  const uint32_t g0 = blockIdx.x * (kUnroll * stride) + (threadIdx.x >> 3);
   float v[kUnroll][8];
   int64_t at[kUnroll];
   int n[kUnroll];
@@ -45,8 +46,8 @@ __global__ __launch_bounds__(kThreads) void act_unpack_kernel(const uint8_t* __r
                                                               const float* __restrict__ scales, T* __restrict__ x,
                                                               uint32_t n_groups, uint32_t groups, int cols) {
   const int l8 = threadIdx.x & 7;
-  const uint32_t stride = gridDim.x * (kThreads / 8);
-  const uint32_t g0 = blockIdx.x * (kThreads / 8) + (threadIdx.x >> 3);
+  constexpr uint32_t stride = kThreads / 8;
+  const uint32_t g0 = blockIdx.x * (kUnroll * stride) + (threadIdx.x >> 3);
   uint2 c[kUnroll];
   float s[kUnroll];
   int64_t at[kUnroll];

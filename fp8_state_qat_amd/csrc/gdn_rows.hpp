@@ -70,15 +70,17 @@ __device__ __forceinline__ float group_scale(const float (&x)[8]) {
 
 // E4M3 codes of an octet at scale s: RN(x / s) in fp32 (through the fp64
 // quotient), then the nearest E4M3 value, ties to even.  Where s is
-// subnormal x / s can exceed 448 by its rounding, and the conversion would
-// make that NaN: it is held at 448.  A NaN stays a NaN.
+// subnormal x / s can exceed 448 by s's rounding, and the conversion would
+// make that NaN: it is held at 448 (a normal s leaves at most 448 (1 + 2^-23),
+// which converts to 448).  A NaN stays a NaN.
 __device__ __forceinline__ uint2 e4m3_oct(const float (&x)[8], float s) {
   const double r = rcp_f64(s);
   float y[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    y[j] = div_rn_f64(x[j], r);
-    y[j] = y[j] > 448.0f ? 448.0f : (y[j] < -448.0f ? -448.0f : y[j]);
+  for (int j = 0; j < 8; ++j) y[j] = div_rn_f64(x[j], r);
+  if (__ballot(s < 0x1p-126f) != 0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = y[j] > 448.0f ? 448.0f : (y[j] < -448.0f ? -448.0f : y[j]);
   }
   int a = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
   a = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], a, true);
