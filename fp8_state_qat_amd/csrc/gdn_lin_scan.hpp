@@ -350,9 +350,8 @@ struct LinWalk {
   static constexpr int RT = CK / 16;       // row tiles of X
   static constexpr int kFrag = 64 * (sizeof(E) == 2 ? 16 : 32);
   static constexpr int kPBytes = 6 * Eng::kPlanes * kFrag;
-  // the wave with the fewest pair tiles (they are dealt block by block): it
-  // forms the next gates, and dg
-  static constexpr int kLight = kRev && NW == 4 ? 2 : NW - 1;
+  // the wave with the fewest pair blocks: it forms the next gates, and dg
+  static constexpr int kLight = NW - 1;
 
   const LinScan& A;
   const LinPlace& L;
@@ -436,13 +435,14 @@ struct LinWalk {
     if (l64 == 0) sY[w] = y;
   }
 
-  // Pair products of this wave's 16 x 32 blocks, weighted, into sP.  sE: DK's
-  // tile of k; sM: its sums of M over the rows of a tile (ten of 16) and over
-  // the columns of a block (six of 16).
-  __device__ __forceinline__ void pairs(const char* sQ, const char* sK, const char* sV, const char* sE,
-                                        const Gates& g, int n, char* sP, float* sM) {
+  // Pair products of the 16 x 32 blocks first, first + step, .., weighted, into
+  // sP.  sE: DK's tile of k; sM: its sums of M over the rows of a tile (ten of
+  // 16) and over the columns of a block (six of 16).
+  static __device__ __forceinline__ void pairs(int first, int step, const char* sQ, const char* sK, const char* sV,
+                                               const char* sE, const Gates& g, int n, char* sP, float* sM) {
+    const int l64 = threadIdx.x & 63, ln = l64 & 15, gq = l64 >> 4;
 #pragma unroll 1
-    for (int blk = w; blk < 6; blk += NW) {
+    for (int blk = first; blk < 6; blk += step) {
       int a, kb;
       lin_block_at<kRev>(blk, a, kb);
       const float ah = g.hi[16 * a + ln], al = g.lo[16 * a + ln];
@@ -742,7 +742,7 @@ __device__ __forceinline__ void lin_scan_walk(const LinScan& A) {
       barrier_lds();
       if (it + 1 < nch) fetch(it + 1);
     }
-    if constexpr (kOut) S.pairs(smem + Lds::Q, sK, sV, nullptr, g, n, smem + Lds::P, nullptr);
+    if constexpr (kOut) W::pairs(w, W::NW, smem + Lds::Q, sK, sV, nullptr, g, n, smem + Lds::P, nullptr);
     if (w == W::kLight && it + 1 < nch) {
       Gsum += lin_gates<kRev>(sG[(it + 1) & 1], rg, L.rows(L.chunk<kBack>(it + 1)), MODE == kLinStF ? Gsum : 0.0);
       rg = L.gate<kBack>(it + 2, A.g_row);
@@ -787,7 +787,9 @@ __global__ __launch_bounds__(4 * CV, Eng::kSplit ? CV / 32 : CV / 64) void lin_s
 // one workgroup: the first DK / 16 waves walk X = dS [TW, DK] for dk, the next
 // TW / 16 waves X = dS^T [DK, TW] for dv.  They share the chunk's rows of q, k,
 // v and d_o in LDS (q and d_o, which both still read after the second
-// barrier, have two tiles), so each is read once.
+// barrier, have two tiles), so each is read once.  Each role forms the other's
+// pair products: dk's are two products and the sums of M, and its waves have
+// the longer state part (11 ragged sequences, 8 heads of 64 x 128: 43 us for 47).
 template <class Eng, int DK, int TW>
 struct LinRevLds {
   using E = typename Eng::E;
@@ -886,7 +888,7 @@ void lin_rev_kernel(LinScan A, LinScan B) {
       const char* sO = smem + Lds::O + (kDirect ? (it & 1) * Lds::TV : 0);
       begin(it);
       S.begin_dg(c, n, sY);
-      S.pairs(smem + Lds::V, sO, sQ, smem + Lds::K, g, n, smem + Lds::PK, sM);
+      WV::pairs(w, WK::NW, smem + Lds::K, sQ, sO, nullptr, g, n, smem + Lds::PV, nullptr);
       S.take_v(sQ);
       S.state_part(smem + Lds::V, g);
       S.dots(n, sR, [&](int row) { return WK::TV::row4(smem + Lds::K, row, 16 * w + 4 * S.gq); });
@@ -919,7 +921,7 @@ void lin_rev_kernel(LinScan A, LinScan B) {
       const char* sQ = smem + Lds::Q + (kDirect ? (it & 1) * Lds::TD : 0);
       const char* sO = smem + Lds::O + (kDirect ? (it & 1) * Lds::TV : 0);
       begin(it);
-      S.pairs(smem + Lds::K, sQ, sO, nullptr, g, n, smem + Lds::PV, nullptr);
+      WK::pairs(wv, WV::NW, smem + Lds::V, sO, sQ, smem + Lds::K, g, n, smem + Lds::PK, sM);
       if (wv == WV::kLight && it + 1 < nch) {
         lin_gates<true>(sG[(it + 1) & 1], rg, L.rows(L.chunk<true>(it + 1)));
         rg = L.gate<true>(it + 2, A.g_row);
