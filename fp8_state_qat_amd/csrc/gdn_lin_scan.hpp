@@ -503,6 +503,69 @@ struct LinWalk {
     for (int kb = 0; kb < 2; ++kb) vf[kb] = TV::template cols8<Eng, 4>(sV, kb, 16 * w, ln, gq);
   }
 
+  // O: a weight of 0 times an infinity or a NaN of V would reach the tokens
+  // before it.  Such values are taken out of the fragments; bad_from is the
+  // first token of this lane's column with one (kChunk: none).  True where
+  // the wave has any (rare: O and X are then put right by taint).
+  __device__ __forceinline__ bool clear_v(int& bad_from) {
+    constexpr int kWords = sizeof(Fr) / 4;
+    struct Words {
+      uint32_t u[kWords];
+    };
+    bool any;
+    if constexpr (Eng::kSplit) {           // 0 times the columns on the matrix unit: NaN where one holds any
+      f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+      const Fr zero = __builtin_bit_cast(Fr, make_uint4(0, 0, 0, 0));
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) Eng::mma(z, vf[kb], zero);
+      any = !((z[0] + z[1]) + (z[2] + z[3]) == 0.0f);
+    } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        const Words x = __builtin_bit_cast(Words, vf[kb]);
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) m = max(m, x.u[j] & 0x7fffffffu);
+      }
+      any = m >= 0x7f800000u;
+    }
+    if (__ballot(any) == 0) return false;
+    int first = kChunk;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      Words x = __builtin_bit_cast(Words, vf[kb]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t& u = x.u[j * kWords / 8];
+        const uint32_t inf = !Eng::kSplit ? 0x7f800000u : (j & 1) ? 0x7f800000u : 0x7f80u;
+        const uint32_t all = !Eng::kSplit ? 0xffffffffu : (j & 1) ? 0xffff0000u : 0xffffu;
+        if ((u & inf) != inf) continue;
+        u &= ~all;
+        first = min(first, 32 * kb + 4 * gq + (j & 3) + 16 * (j >> 2));
+      }
+      vf[kb] = __builtin_bit_cast(Fr, x);
+    }
+    first = min(first, __shfl_xor(first, 16, 64));
+    bad_from = min(first, __shfl_xor(first, 32, 64));
+    return true;
+  }
+  __device__ __forceinline__ void taint_out(int bad_from) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int from = __shfl(bad_from, 4 * gq + r, 64);
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt)
+        if (16 * rt + ln >= from) O[rt][r] = __builtin_nanf("");
+    }
+  }
+  __device__ __forceinline__ void taint_state(int bad_from) {
+#pragma unroll
+    for (int tr = 0; tr < RT; ++tr)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (bad_from < kChunk) X[tr][r] = __builtin_nanf("");
+  }
+
   // State part: O^T = X^T Q^T, scaled by the rows' weights.
   __device__ __forceinline__ void state_part(const char* sQ, const Gates& g) {
 #pragma unroll
@@ -748,6 +811,8 @@ __device__ __forceinline__ void lin_scan_walk(const LinScan& A) {
       rg = L.gate<kBack>(it + 2, A.g_row);
     }
     S.take_v(sV);
+    int bad_from = kChunk;
+    bool bad = false;
     if constexpr (kOut) {
       S.state_part(smem + Lds::Q, g);
       if constexpr (kDots)
@@ -756,11 +821,14 @@ __device__ __forceinline__ void lin_scan_walk(const LinScan& A) {
         });
       barrier_lds();
       if (kDirect && it + 1 < nch) ask(it + 1);
+      if constexpr (MODE == kLinO) bad = S.clear_v(bad_from);
       S.pair_part(smem + Lds::P);
+      if (bad) S.taint_out(bad_from);
       S.store_out(c, n);
       if (kDots && w == W::kLight) S.end_dots(c, n, sR, nullptr, nullptr);
     }
     S.update(sK, g);
+    if (bad) S.taint_state(bad_from);
     if constexpr (MODE == kLinDQ) {
       if (S.anchor(c)) S.store_anchor(c);
     }

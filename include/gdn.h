@@ -365,6 +365,11 @@ size_t gdn_chunk_bwd_workspace_bytes(const gdn_shape_t* shape);
  *          -inf (the token starts from an empty state) is allowed.
  * A state is [n_seqs, n_heads, dv, dk] fp32.  Buffers are 16-byte aligned (g
  * and dg 4), row-major.
+ *
+ * An infinity or a NaN in q, k, v or g reaches the outputs and the state that
+ * the recurrence lets it reach, as a NaN, and no earlier token; in the
+ * backward it can reach the gradients of all tokens of its 64-token chunk.
+ * No other sequence is touched.
  */
 typedef struct {
     int32_t n_seqs;            /* N >= 1 */

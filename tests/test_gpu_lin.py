@@ -280,3 +280,33 @@ def test_step(N, H, Hk, dk, dv, dtype, gate):
     o2, S2 = api.lin_attn_fwd(x["q"], x["k"], x["v"], x["g"], x["cu"], initial_state=x["S0"])
     close(o2, ro, mo, "o " + tag(o))
     close(S2, rS, mS, "state fp32")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("name", ["q", "k", "v"])
+def test_non_finite_values_do_not_reach_earlier_tokens(dtype, name):
+    """An infinity or a NaN reaches what the recurrence says: from its token on, its value row (v), all rows (k),
+    or its token alone (q); everything else keeps its bits."""
+    lens = [150, 70, 40]
+    d = dev(make(lens, 2, 1 if name != "v" else 2, 64, 128, dtype, seed=12))
+    args = (d["g"], d["cu"])
+    o0, S0 = api.lin_attn_fwd(d["q"], d["k"], d["v"], *args, initial_state=d["S0"])
+    for t, col, x in ((37, 5, float("inf")), (63, 17, float("nan")), (149, 40, float("-inf")), (150, 3, float("nan")),
+                      (219, 63, float("inf"))):
+        n, end = (0, 150) if t < 150 else (1, 220)
+        b = d[name].clone()
+        b[t, 0, col] = x
+        o, S = api.lin_attn_fwd(*(b if m == name else d[m] for m in ("q", "k", "v")), *args, initial_state=d["S0"])
+        hit = torch.zeros_like(o0, dtype=torch.bool)
+        hit_S = torch.zeros_like(S0, dtype=torch.bool)
+        if name == "v":
+            hit[t:end, 0, col] = True
+            hit_S[n, 0, col] = True
+        elif name == "k":
+            hit[t:end] = True
+            hit_S[n, :, :, col] = True
+        else:
+            hit[t] = True
+        assert not torch.isfinite(o[hit]).any(), (t, col)
+        assert torch.equal(o[~hit], o0[~hit]), (t, col)
+        assert not torch.isfinite(S[hit_S]).any() and torch.equal(S[~hit_S], S0[~hit_S]), (t, col)
