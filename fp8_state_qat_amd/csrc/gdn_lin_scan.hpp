@@ -51,7 +51,14 @@
 // memory straight into LDS: Q and V are free after the state part, K has a
 // second tile, so the next chunk's rows are asked for in the middle of this
 // one and a chunk needs two barriers (a state pass one).  At 128 x 128 the
-// tiles take 80 KB: two workgroups a compute unit.
+// tiles take 80 KB: two workgroups a compute unit.  fp32 rows, which would not
+// fit twice, are fetched into registers a chunk ahead.
+//
+// Measured (MI355X, bf16, 16 heads of 128 x 128): 32768 tokens in one sequence,
+// state pass 65 us (268 MB; 62 us with its products taken out), output pass 146
+// us (537 MB; 110 without products, 131 with every load a cache hit: vector,
+// matrix and LDS work are each near half of its time).  Backward of 4 x 4096
+// tokens: state passes 76 us, dq 112 to 127, dk and dv 202 to 236 (cold and warm).
 #pragma once
 
 #include <type_traits>
