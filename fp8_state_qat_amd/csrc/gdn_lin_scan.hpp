@@ -299,6 +299,14 @@ __device__ __forceinline__ void lin_block_at(int blk, int& rt, int& kb) {   // i
 }
 __host__ __device__ constexpr int lin_tri(int a, int b) { return 4 * a - a * (a - 1) / 2 + b - a; }
 
+// wait_vmem for the rows asked for, but not for the four stores of a whole
+// chunk's outputs that followed them: vector memory operations of a wave
+// retire in order, so at most four outstanding ones are those stores.
+__device__ __forceinline__ void wait_rows() {
+  asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0F74);
+}
+
 // One workgroup's place in the batch, the same for all its waves.
 struct LinPlace {
   LinSeg sg;
@@ -598,13 +606,14 @@ struct LinWalk {
       for (int r = 0; r < 4; ++r) O[rt][r] *= s;
     }
   }
-  // DQ, DK: the wave's columns of r_i, c_j; e(row): its four columns of E.
+  // DQ, DK: the wave's columns of r_i, c_j; e(rt): this lane's four columns of
+  // E in row tile rt.
   template <class F>
   __device__ __forceinline__ void dots(int n, float* sR, F e) const {
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
       const int row = 16 * rt + ln;
-      const f32x4 ev = e(row);
+      const f32x4 ev = e(rt);
       float d = 0.0f;
 #pragma unroll
       for (int r = 0; r < 4; ++r) d = fmaf(O[rt][r], ev[r], d);
@@ -629,18 +638,20 @@ struct LinWalk {
         }
   }
   __device__ __forceinline__ void store_out(int c, int n) const {
-    const bool wide = sizeof(E) == 4 || A.out_f32;
+    const bool wide = sizeof(E) == 4 || (kDots && A.out_f32);
+    const int size = wide ? 4 : 2;
     // a chunk's rows lie within 2^31 bytes of its first: 32-bit offsets from there
-    char* base = (char*)A.out + (((int64_t)L.sg.t0 + kChunk * c) * A.os + (int64_t)L.vh * CV) * (wide ? 4 : 2);
+    char* base = (char*)A.out + (((int64_t)L.sg.t0 + kChunk * c) * A.os + (int64_t)L.vh * CV) * size;
+    uint32_t off = (uint32_t)((ln * A.os + 16 * w + 4 * gq) * size);
+    asm volatile("" : "+v"(off));            // one register, not eight kept through the walk
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
-      const int row = 16 * rt + ln;
-      if (row >= n) continue;
-      const uint32_t at = (uint32_t)(row * A.os + 16 * w + 4 * gq);
+      if (16 * rt + ln >= n) continue;
+      char* to = base + (int64_t)(16 * rt * A.os * size);
       if (wide)
-        *reinterpret_cast<f32x4*>(base + 4 * at) = O[rt];
+        *reinterpret_cast<f32x4*>(to + off) = O[rt];
       else
-        *reinterpret_cast<uint2*>(base + 2 * at) =
+        *reinterpret_cast<uint2*>(to + off) =
             make_uint2(pack_bf16x2(O[rt][0], O[rt][1]), pack_bf16x2(O[rt][2], O[rt][3]));
     }
   }
@@ -763,11 +774,17 @@ __device__ __forceinline__ void lin_scan_walk(const LinScan& A) {
   const E* pV = (const E*)A.V + t0 * A.vs + (int64_t)(L.vh / A.vd) * CV;
   const E* pQ = kOut ? (const E*)A.Q + t0 * A.qs + (int64_t)(L.vh / A.qd) * CK : nullptr;
   const E* pE = kDots ? (const E*)A.E + t0 * A.es + (int64_t)(L.vh / A.ed) * CV : nullptr;
-  // the rows of walk step it: K into its tile, V and Q into theirs
+  // the rows of walk step it: K into its tile, V and Q into theirs.  K's other
+  // tile is free a whole chunk ahead, and O asks for it once the gates are
+  // formed (DQ waits for its rows of E after that)
+  constexpr bool kEarly = MODE == kLinO;
+  auto ask_k = [&](int it) {
+    const int c = L.chunk<kBack>(it), n = L.rows(c);
+    RowsK::ask(lds0 + Lds::K + (it & 1) * W::TK::kBytes, pK + (int64_t)kChunk * c * A.ks, A.ks, n);
+  };
   auto ask = [&](int it) {
     const int c = L.chunk<kBack>(it), n = L.rows(c);
     const int64_t r0 = (int64_t)kChunk * c;
-    RowsK::ask(lds0 + Lds::K + (it & 1) * W::TK::kBytes, pK + r0 * A.ks, A.ks, n);
     RowsV::ask(lds0 + Lds::V + (kOut ? 0 : (it & 1) * W::TV::kBytes), pV + r0 * A.vs, A.vs, n);
     if constexpr (kOut) RowsK::ask(lds0 + Lds::Q, pQ + r0 * A.qs, A.qs, n);
   };
@@ -789,10 +806,15 @@ __device__ __forceinline__ void lin_scan_walk(const LinScan& A) {
     if constexpr (kOut) RowsK::fetch(xq, pQ + r0 * A.qs, A.qs, n);
   };
   if (nch > 0) {
-    if constexpr (kDirect) ask(0);
-    else fetch(0);
+    if constexpr (kDirect) {
+      ask_k(0);
+      ask(0);
+    } else {
+      fetch(0);
+    }
   }
   S.load_state();
+  if (kDirect) wait_vmem();                // the state is there: no wait for it inside the walk
 
 #pragma unroll 1
   for (int it = 0; it < nch; ++it) {
@@ -802,9 +824,14 @@ __device__ __forceinline__ void lin_scan_walk(const LinScan& A) {
     const char* sK = smem + Lds::K + (kDirect ? (it & 1) * W::TK::kBytes : 0);
     const char* sV = smem + Lds::V + (kDirect && !kOut ? (it & 1) * W::TV::kBytes : 0);
     if constexpr (kDirect) {
-      wait_vmem();
+      // output passes: the chunk before this one was whole, its four stores may go on
+      if (kOut && it > 0) wait_rows();
+      else wait_vmem();
       barrier_lds();
-      if (!kOut && it + 1 < nch) ask(it + 1);
+      if (!kOut && it + 1 < nch) {
+        ask_k(it + 1);
+        ask(it + 1);
+      }
     } else {
       RowsK::put(smem + Lds::K, xk);
       RowsV::put(smem + Lds::V, xv);
@@ -812,22 +839,34 @@ __device__ __forceinline__ void lin_scan_walk(const LinScan& A) {
       barrier_lds();
       if (it + 1 < nch) fetch(it + 1);
     }
+    // DQ: this lane's columns of E, on the way while the pairs are formed
+    using E4 = std::conditional_t<sizeof(E) == 2, uint2, f32x4>;
+    E4 er[kDots ? 4 : 1];
+    if constexpr (kDots) {
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) {
+        const int row = 16 * rt + S.ln;
+        er[rt] = *reinterpret_cast<const E4*>(pE + (r0 + (row < n ? row : n - 1)) * A.es + 16 * w + 4 * S.gq);
+      }
+    }
     if constexpr (kOut) W::pairs(w, W::NW, smem + Lds::Q, sK, sV, nullptr, g, n, smem + Lds::P, nullptr);
     if (w == W::kLight && it + 1 < nch) {
       Gsum += lin_gates<kRev>(sG[(it + 1) & 1], rg, L.rows(L.chunk<kBack>(it + 1)), MODE == kLinStF ? Gsum : 0.0);
       rg = L.gate<kBack>(it + 2, A.g_row);
     }
+    if (kDirect && kEarly && it + 1 < nch) ask_k(it + 1);
     S.take_v(sV);
     int bad_from = kChunk;
     bool bad = false;
     if constexpr (kOut) {
       S.state_part(smem + Lds::Q, g);
       if constexpr (kDots)
-        S.dots(n, sR, [&](int row) {
-          return ld4(pE + (r0 + (row < n ? row : n - 1)) * A.es + 16 * w + 4 * S.gq);
-        });
+        S.dots(n, sR, [&](int rt) { return ld4((const E*)&er[rt]); });
       barrier_lds();
-      if (kDirect && it + 1 < nch) ask(it + 1);
+      if (kDirect && it + 1 < nch) {
+        if constexpr (!kEarly) ask_k(it + 1);
+        ask(it + 1);
+      }
       if constexpr (MODE == kLinO) bad = S.clear_v(bad_from);
       S.pair_part(smem + Lds::P);
       if (bad) S.taint_out(bad_from);
@@ -929,7 +968,9 @@ void lin_rev_kernel(LinScan A, LinScan B) {
   };
   auto begin = [&](int it) {               // the chunk's tiles and gates are there
     if constexpr (kDirect) {
-      wait_vmem();
+      // from the third chunk on the one before was whole: its four stores may go on
+      if (it > 1) wait_rows();
+      else wait_vmem();
       barrier_lds();
     } else {
       const int c = L.chunk<true>(it), n = L.rows(c);
@@ -955,6 +996,7 @@ void lin_rev_kernel(LinScan A, LinScan B) {
     if (kDirect && nch > 0) ask(0);
     WK S(A, L, w);
     S.load_state();
+    if (kDirect) wait_vmem();
 #pragma unroll 1
     for (int it = 0; it < nch; ++it) {
       const int c = L.chunk<true>(it), n = L.rows(c);
@@ -966,7 +1008,7 @@ void lin_rev_kernel(LinScan A, LinScan B) {
       WV::pairs(w, WK::NW, smem + Lds::K, sQ, sO, nullptr, g, n, smem + Lds::PV, nullptr);
       S.take_v(sQ);
       S.state_part(smem + Lds::V, g);
-      S.dots(n, sR, [&](int row) { return WK::TV::row4(smem + Lds::K, row, 16 * w + 4 * S.gq); });
+      S.dots(n, sR, [&](int rt) { return WK::TV::row4(smem + Lds::K, 16 * rt + S.ln, 16 * w + 4 * S.gq); });
       asm volatile("" ::"v"(S.rdot));      // its load ends before the next chunk's are asked for
       middle(it);
       S.pair_part(smem + Lds::PK);
@@ -989,6 +1031,7 @@ void lin_rev_kernel(LinScan A, LinScan B) {
     if (kDirect && nch > 0) ask(0);
     WV S(B, L, wv);
     S.load_state();
+    if (kDirect) wait_vmem();
 #pragma unroll 1
     for (int it = 0; it < nch; ++it) {
       const int c = L.chunk<true>(it), n = L.rows(c);
