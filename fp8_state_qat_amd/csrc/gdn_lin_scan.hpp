@@ -439,13 +439,15 @@ struct LinWalk {
       rdot = l64 < n ? A.rdot[((int64_t)L.sg.t0 + kChunk * c + l64) * A.VH + L.vh] : 0.0f;
     if (!anchor(c)) return;
     const f32x4* d = dumped(c);
+    f32x4 s[RT];
+#pragma unroll
+    for (int tr = 0; tr < RT; ++tr) s[tr] = d[tr * NT];
+    __builtin_amdgcn_sched_barrier(0);       // all on the way before the first is waited for
     double y = 0.0;
 #pragma unroll
-    for (int tr = 0; tr < RT; ++tr) {
-      const f32x4 s = d[tr * NT];
+    for (int tr = 0; tr < RT; ++tr)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) y = fma((double)s[r], (double)X[tr][r], y);
-    }
+      for (int r = 0; r < 4; ++r) y = fma((double)s[tr][r], (double)X[tr][r], y);
     y = last_lane(wave_prefix_f64(y));
     if (l64 == 0) sY[w] = y;
   }
