@@ -284,8 +284,7 @@ __device__ __forceinline__ double lin_gates(LinGatesOf<kRev>& s, float g, int n,
 }
 
 
-// The six 16 x 32 blocks of P (row tile rt, k-block kb) inside the triangle,
-// and the ten 16 x 16 tiles (a, b >= a) of the reverse one.
+// The six 16 x 32 blocks of P (row tile rt, k-block kb) inside the triangle.
 template <bool kRev>
 __host__ __device__ constexpr bool lin_has(int rt, int kb) { return kRev ? 2 * kb + 1 >= rt : 2 * kb <= rt; }
 template <bool kRev>
@@ -297,7 +296,6 @@ __device__ __forceinline__ void lin_block_at(int blk, int& rt, int& kb) {   // i
   rt = kRev ? (blk < 4 ? blk >> 1 : blk - 2) : (blk < 2 ? blk : 1 + (blk >> 1));
   kb = kRev ? (blk < 4 ? blk & 1 : 1) : (blk < 2 ? 0 : blk & 1);
 }
-__host__ __device__ constexpr int lin_tri(int a, int b) { return 4 * a - a * (a - 1) / 2 + b - a; }
 
 // wait_vmem for the rows asked for, but not for the four stores of a whole
 // chunk's outputs that followed them: vector memory operations of a wave
@@ -432,11 +430,19 @@ struct LinWalk {
 #pragma unroll
     for (int tr = 0; tr < RT; ++tr) d[tr * NT] = X[tr];
   }
+  // A value for each token and head: a chunk's first, and this lane's from there
+  // (formed where it is used, not kept through the walk).
+  __device__ __forceinline__ int64_t row0(int c) const { return ((int64_t)L.sg.t0 + kChunk * c) * A.VH + L.vh; }
+  __device__ __forceinline__ uint32_t lane_row() const {
+    uint32_t i = (uint32_t)(l64 * A.VH);
+    asm volatile("" : "+v"(i));
+    return i;
+  }
   // DK: Y = <S, dS> at the chunk's end, anew from the stored state of its
   // group; and the light wave's r_i
   __device__ __forceinline__ void begin_dg(int c, int n, double* sY) {
     if (w == kLight)
-      rdot = l64 < n ? A.rdot[((int64_t)L.sg.t0 + kChunk * c + l64) * A.VH + L.vh] : 0.0f;
+      rdot = l64 < n ? (A.rdot + row0(c))[lane_row()] : 0.0f;
     if (!anchor(c)) return;
     const f32x4* d = dumped(c);
     f32x4 s[RT];
@@ -453,8 +459,8 @@ struct LinWalk {
   }
 
   // Pair products of the 16 x 32 blocks first, first + step, .., weighted, into
-  // sP.  sE: DK's tile of k; sM: its sums of M over the rows of a tile (ten of
-  // 16) and over the columns of a block (six of 16).
+  // sP.  sE: DK's tile of k; sM: its sums of M over the rows of a tile (16 at
+  // 64 a + 16 b) and over the columns of a block (16 at 256 + 64 kb + 16 a).
   static __device__ __forceinline__ void pairs(int first, int step, const char* sQ, const char* sK, const char* sV,
                                                const char* sE, const Gates& g, int n, char* sP, float* sM) {
     const int l64 = threadIdx.x & 63, ln = l64 & 15, gq = l64 >> 4;
@@ -498,7 +504,7 @@ struct LinWalk {
             const float m = ib > ia ? acc2[bb][r] * pw[4 * bb + r] : 0.0f;
             cm += m;
             const float rm = group_sum<16>(m);
-            if (b >= a && ln == 0) sM[16 * lin_tri(a, b) + 4 * gq + r] = rm;
+            if (ln == 0) sM[64 * a + 16 * b + 4 * gq + r] = rm;
           }
         }
       }
@@ -510,7 +516,7 @@ struct LinWalk {
       if constexpr (MODE == kLinDK) {
         cm += __shfl_xor(cm, 16, 64);
         cm += __shfl_xor(cm, 32, 64);
-        if (gq == 0) sM[160 + 16 * blk + ln] = cm;
+        if (gq == 0) sM[256 + 64 * kb + 16 * a + ln] = cm;
       }
     }
   }
@@ -662,30 +668,27 @@ struct LinWalk {
     float d = 0.0f;
 #pragma unroll
     for (int k = 0; k < NW; ++k) d += sR[kChunk * k + l64];
-    const int64_t at = ((int64_t)L.sg.t0 + kChunk * c + l64) * A.VH + L.vh;
     if constexpr (MODE == kLinDQ) {
-      if (l64 < n) A.rdot[at] = d;
+      if (l64 < n) (A.rdot + row0(c))[lane_row()] = d;
     } else if constexpr (MODE == kLinDK) {
       if (anchor(c)) {
         Y = sY[0];
 #pragma unroll
         for (int k = 1; k < NW; ++k) Y += sY[k];
       }
-      double rm = 0.0;                     // row sum of M, over the column blocks
+      // row sum of M, over the column blocks, and column sum, over the row
+      // blocks; what no block writes is 0
+      double rm = 0.0;
 #pragma unroll
-      for (int a = 0; a < 4; ++a)
-        if (a <= (l64 >> 4)) rm += (double)sM[16 * lin_tri(a, l64 >> 4) + (l64 & 15)];
-      double cm = 0.0;                     // column sum, over the row blocks
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-        if (lin_has<true>(l64 >> 4, kb)) cm += (double)sM[160 + 16 * lin_block<true>(l64 >> 4, kb) + (l64 & 15)];
+      for (int a = 0; a < 4; ++a) rm += (double)sM[64 * a + l64];
+      const double cm = (double)sM[256 + l64] + (double)sM[320 + l64];
       const double own = rm + (double)rdot - cm;
       const double head = wave_prefix_f64(own), pre = wave_prefix_f64((double)d);
       const double Xc = Y - last_lane(pre);
       const double dg = (last_lane(head) - head + own) + (pre - (double)d) + Xc;
       Y = Xc + last_lane(wave_prefix_f64((double)rdot));
       if (l64 < n) {
-        if (A.dg_tok != nullptr) A.dg_tok[at] = (float)dg;
+        if (A.dg_tok != nullptr) (A.dg_tok + row0(c))[lane_row()] = (float)dg;
         dg_sum += dg;
       }
     }
@@ -923,7 +926,8 @@ struct LinRevLds {
   static constexpr int G = PV + WV::kPBytes;
   static constexpr int R = G + 2 * (int)sizeof(LinGatesRev);
   static constexpr int M = R + WK::NW * kChunk * 4;
-  static constexpr int Y = M + (10 + 6) * 16 * 4;
+  static constexpr int kSums = 384;
+  static constexpr int Y = M + kSums * 4;
   static constexpr int kBytes = Y + WK::NW * 8;
 };
 
@@ -947,6 +951,7 @@ void lin_rev_kernel(LinScan A, LinScan B) {
   double* sY = reinterpret_cast<double*>(smem + Lds::Y);
   const uint32_t lds0 = lds_base_u32(smem);
 
+  for (int i = threadIdx.x; i < Lds::kSums; i += NT) sM[i] = 0.0f;
   LinPlace L;
   if (!L.find(A)) {
     // an unused slot's part of dg (a bad index array leaves it unread)
