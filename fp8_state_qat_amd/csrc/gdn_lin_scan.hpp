@@ -54,11 +54,18 @@
 // tiles take 80 KB: two workgroups a compute unit.  fp32 rows, which would not
 // fit twice, are fetched into registers a chunk ahead.
 //
-// Measured (MI355X, bf16, 16 heads of 128 x 128): 32768 tokens in one sequence,
-// state pass 65 us (268 MB; 62 us with its products taken out), output pass 146
-// us (537 MB; 110 without products, 131 with every load a cache hit: vector,
-// matrix and LDS work are each near half of its time).  Backward of 4 x 4096
-// tokens: state passes 76 us, dq 112 to 127, dk and dv 202 to 236 (cold and warm).
+// A wave's waits decide as much as its work: the compiler's own waits count
+// only its own loads and so drain the asked rows too.  Inside the walk there
+// are none between asking and using: the state is waited for before it, gates
+// and DQ's rows of E before the rows are asked for, and a chunk's output stores
+// stay in flight over its end (train batch 399 -> 371 us).
+//
+// Measured (MI355X, bf16, 16 heads of 128 x 128, cold to warm): 32768 tokens in
+// one sequence, state pass 62 to 68 us (268 MB; 62 with its products taken out),
+// output pass 133 to 150 (537 MB; 105 to 116 without products, 131 with every
+// load a cache hit; vector, matrix and LDS units are each busy 40 to 50% of the
+// time).  Backward of 4 x 4096 tokens: state passes 70 to 81, dq 97 to 123, dk
+// and dv 179 to 218.
 #pragma once
 
 #include <type_traits>
