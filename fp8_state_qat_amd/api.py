@@ -412,8 +412,9 @@ def _args(*specs):
 
 
 def _stream_at():
-    """torch's current stream as a plain integer."""
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    """torch's current stream as a plain integer (a checked device tensor has
+    initialised the device)."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _refuse():
