@@ -138,9 +138,9 @@ int lin_tile(int dv) { return dv % 128 == 0 ? 128 : 64; }
 // tokens: 239 with 256, 231 with 512).
 int64_t lin_units(const gdn_lin_t& s) { return s.io_dtype == GDN_F32 && s.dk == 128 ? 256 : 512; }
 // Forward calls of up to four chunks stay whole: one kernel instead of three
-// (130 tokens 12 us instead of 17, 192: 16 and 23, 256: 20 and 24; 384 tokens
-// the same either way).  The backward's chain a chunk is longer: 256 tokens
-// take 65 us whole and 53 in segments.
+// (130 tokens 12 us instead of 16.5, 192: 16.5 and 20, 256: 20 either way).
+// The backward's chain a chunk is longer: 256 tokens take 65 us whole and 38
+// in segments.
 constexpr int64_t kLinWhole = 256;
 int lin_seglen(const gdn_lin_t& s, bool bwd) {
   const int64_t VH = (int64_t)s.n_heads * (s.dv / lin_tile(s.dv));
