@@ -196,8 +196,7 @@ LinLayout lin_layout(const gdn_lin_t& s, void* ws, bool bwd) {
       L.segR = (float*)take(heads * state);
       L.decR = (float*)take(heads * 4);
     }
-    const size_t groups = (size_t)(s.total_tokens / (kAnchor * kChunk) + L.slots);
-    L.dump = (float*)take(groups * L.VH * state);
+    L.dump = (float*)take((size_t)(s.total_tokens / kChunk) * L.VH * state);
     L.rdot = (float*)take((size_t)s.total_tokens * L.VH * 4);
     if (s.gate_per_token && L.tiles > 1) L.dgt = (float*)take((size_t)s.total_tokens * L.VH * 4);
     if (!s.gate_per_token) L.dgp = (double*)take(heads * 8);
@@ -345,6 +344,8 @@ hipError_t launch_lin_bwd(const gdn_lin_t& s, const void* q, const void* k, cons
   K.seg = L.segR;
   K.first = d_final_state;
   K.dump = L.dump;
+  K.seg_in = L.segF;
+  K.first_in = initial_state;
   K.rdot = L.rdot;
   K.out = sum ? (void*)L.part_k : dk;
   K.os = qrow;

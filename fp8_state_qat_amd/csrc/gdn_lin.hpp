@@ -8,8 +8,6 @@ namespace gdn {
 // The passes of the scan (see gdn_lin_scan.hpp); kLinStR runs with kLinStF, kLinDV with kLinDK.
 enum LinMode : int { kLinO = 0, kLinStF = 1, kLinDQ = 2, kLinStR = 3, kLinDV = 4, kLinDK = 5 };
 
-constexpr int kAnchor = 4;  // chunks between two stored states of the backward
-
 struct LinScan {
   const void* Q;          // rows of the output side of a pair (null: state only)
   const void* K;          // rows contracted with Q and, transposed, with V into the state
@@ -23,7 +21,9 @@ struct LinScan {
   float* seg;             // [slot][VH][tw][dk]: state at the pass's start of a segment, or (state
                           // passes) the segment's own sum; null: one segment a sequence
   float* seg_decay;       // state passes: e^(sum of g) of each (slot, head)
-  float* dump;            // DQ writes, DK reads: raw accumulators every kAnchor chunks
+  float* dump;            // DQ writes, DK reads: raw accumulators after each chunk but a segment's last
+  const float* seg_in;    // DK: seg and first of the DQ pass
+  const float* first_in;
   float* rdot;            // [T][VH]: DQ writes, DK reads: q_i . (state part of dq_i)
   float* dg_tok;          // DK: [T][VH], or null
   double* dg_part;        // DK: [slot][VH] sums over the segment's tokens, or null

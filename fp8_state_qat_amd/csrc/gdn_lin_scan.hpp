@@ -19,10 +19,13 @@
 // in a chunk, with M_ij = D_ij (q_i.k_j)(do_i.v_j) for i > j, r_i = q_i.(state
 // part of dq_i), c_j = k_j.(state part of dk_j) and X = e^(G_C) <S, dS>,
 //     dg_t = sum_{i>=t} (sum_j M_ij + r_i) - sum_{j>=t} sum_i M_ij + sum_{j<t} c_j + X.
-// X = Y - sum_j c_j with Y = <S, dS> at the chunk's end; before it (the next
-// chunk of the reversed walk) Y is X + sum_i r_i.  That recursion is started
-// anew every kAnchor chunks from the product of the two states, the forward
-// one stored there by the dq pass: its rounding errors never run far.
+// X is formed from the two states in every chunk, the forward one stored by
+// the dq pass.  (X = <S', dS> - sum_j c_j with the state S' at the chunk's end
+// would let X be carried from chunk to chunk with few stored states, but what
+// is large or not finite in a chunk's k and v would reach the earlier chunks
+// through that difference: a row of v 1e5 times the others left errors of 2e-3
+// there instead of 2e-7.)  So errors of dg are relative to the largest sums of
+// its own chunk.
 //
 // Work split.  A workgroup owns one segment (a run of whole chunks of one
 // sequence) of one virtual head (a value head, or a 64- or 128-row tile of
@@ -304,12 +307,15 @@ __device__ __forceinline__ void lin_block_at(int blk, int& rt, int& kb) {   // i
   kb = kRev ? (blk < 4 ? blk & 1 : 1) : (blk < 2 ? 0 : blk & 1);
 }
 
-// wait_vmem for the rows asked for, but not for the four stores of a whole
-// chunk's outputs that followed them: vector memory operations of a wave
-// retire in order, so at most four outstanding ones are those stores.
+// wait_vmem for the rows asked for, but not for the kStores stores that every
+// wave issued after them (four of a whole chunk's outputs, and DQ's of the
+// state): vector memory operations of a wave retire in order, so at most
+// kStores outstanding ones are those stores.
+template <int kStores>
 __device__ __forceinline__ void wait_rows() {
-  asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0F74);
+  static_assert(kStores == 4 || kStores == 8 || kStores == 12, "the builtin's operand below holds up to 15");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kStores) : "memory");
+  __builtin_amdgcn_s_waitcnt(0x0F70 + kStores);
 }
 
 // One workgroup's place in the batch, the same for all its waves.
@@ -327,8 +333,9 @@ struct LinPlace {
     if (sg.bad) return false;
     sv = (int64_t)slot * A.VH + vh;
     if (sg.n < 0) return false;
-    // stored states: a segment's groups from t0 / (rows of a group) + slot on, which no two segments share
-    dump0 = ((int64_t)sg.t0 / (kAnchor * kChunk) + slot) * A.VH + vh;
+    // stored states: one after each chunk but a segment's last, from t0 / kChunk on, so that no two
+    // segments share one and all lie below T / kChunk
+    dump0 = (int64_t)sg.t0 / kChunk * A.VH + vh;
     nch = (sg.len + kChunk - 1) / kChunk;
     pg = A.g + sg.t0 * A.g_row + vh / A.tiles;
     return true;
@@ -381,11 +388,11 @@ struct LinWalk {
   f32x4 X[RT], O[4];
   Fr vf[2];                                // V^T fragments of this wave's columns
   float rdot;                              // DK, light wave: this lane's r_i
-  double Y, dg_sum;
+  double dg_sum;
 
   __device__ __forceinline__ LinWalk(const LinScan& a, const LinPlace& l, int wave)
       : A(a), L(l), w(wave), l64(threadIdx.x & 63), ln(threadIdx.x & 15), gq((threadIdx.x >> 4) & 3), rdot(0.0f),
-        Y(0.0), dg_sum(0.0) {}
+        dg_sum(0.0) {}
 
   __device__ __forceinline__ int64_t st_at(int tr, int r) const {
     const int row = 32 * (tr / 2) + 8 * gq + 4 * (tr & 1) + r, colx = 16 * w + ln;
@@ -428,11 +435,11 @@ struct LinWalk {
       }
     }
   }
-  __device__ __forceinline__ bool anchor(int c) const { return c % kAnchor == kAnchor - 1 || c == L.nch - 1; }
+  // DQ: the state after chunk c, which is not the segment's last, for DK
   __device__ __forceinline__ f32x4* dumped(int c) const {
-    return reinterpret_cast<f32x4*>(A.dump) + (L.dump0 + (c / kAnchor) * (int64_t)A.VH) * (CK * CV / 4) + 64 * w + l64;
+    return reinterpret_cast<f32x4*>(A.dump) + (L.dump0 + c * (int64_t)A.VH) * (CK * CV / 4) + 64 * w + l64;
   }
-  __device__ __forceinline__ void store_anchor(int c) const {
+  __device__ __forceinline__ void store_dump(int c) const {
     f32x4* d = dumped(c);
 #pragma unroll
     for (int tr = 0; tr < RT; ++tr) d[tr * NT] = X[tr];
@@ -445,22 +452,43 @@ struct LinWalk {
     asm volatile("" : "+v"(i));
     return i;
   }
-  // DK: Y = <S, dS> at the chunk's end, anew from the stored state of its
-  // group; and the light wave's r_i
+  // DK: this wave's part of <S, dS>, S the state entering the chunk: from the
+  // dq pass, or what that pass started the segment from; and the light wave's r_i
   __device__ __forceinline__ void begin_dg(int c, int n, double* sY) {
     if (w == kLight)
       rdot = l64 < n ? (A.rdot + row0(c))[lane_row()] : 0.0f;
-    if (!anchor(c)) return;
-    const f32x4* d = dumped(c);
-    f32x4 s[RT];
-#pragma unroll
-    for (int tr = 0; tr < RT; ++tr) s[tr] = d[tr * NT];
-    __builtin_amdgcn_sched_barrier(0);       // all on the way before the first is waited for
     double y = 0.0;
+    if (c > 0) {
+      const f32x4* d = dumped(c - 1);
+      f32x4 s[RT];
 #pragma unroll
-    for (int tr = 0; tr < RT; ++tr)
+      for (int tr = 0; tr < RT; ++tr) s[tr] = d[tr * NT];
+      __builtin_amdgcn_sched_barrier(0);     // all on the way before the first is waited for
 #pragma unroll
-      for (int r = 0; r < 4; ++r) y = fma((double)s[tr][r], (double)X[tr][r], y);
+      for (int tr = 0; tr < RT; ++tr)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y = fma((double)s[tr][r], (double)X[tr][r], y);
+    } else if (A.seg_in != nullptr || A.first_in != nullptr) {
+      const int64_t size = (int64_t)A.tw * A.dk;
+      const char* p = (const char*)(A.seg_in != nullptr ? A.seg_in + L.sv * size
+                                                        : A.first_in + ((int64_t)L.sg.n * A.VH + L.vh) * size);
+      uint32_t at = (uint32_t)st_at(0, 0) * 4;
+      asm volatile("" : "+v"(at));           // one register, not one for each row
+#pragma unroll
+      for (int t0 = 0; t0 < RT; t0 += 4) {
+        f32x4 s[4];
+#pragma unroll
+        for (int tr = 0; tr < 4; ++tr)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            s[tr][r] = *(const float*)(p + (32 * ((t0 + tr) / 2) + 4 * (tr & 1) + r) * CV * 4 + at);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int tr = 0; tr < 4; ++tr)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) y = fma((double)s[tr][r], (double)X[t0 + tr][r], y);
+      }
+    }
     y = last_lane(wave_prefix_f64(y));
     if (l64 == 0) sY[w] = y;
   }
@@ -671,18 +699,18 @@ struct LinWalk {
     }
   }
   // DQ's light wave: r_i; DK's: dg of the chunk's tokens.
-  __device__ __forceinline__ void end_dots(int c, int n, const float* sR, const float* sM, const double* sY) {
+  __device__ __forceinline__ void end_dots(int c, int n, const Gates& g, const float* sR, const float* sM,
+                                           const double* sY) {
     float d = 0.0f;
 #pragma unroll
     for (int k = 0; k < NW; ++k) d += sR[kChunk * k + l64];
     if constexpr (MODE == kLinDQ) {
       if (l64 < n) (A.rdot + row0(c))[lane_row()] = d;
     } else if constexpr (MODE == kLinDK) {
-      if (anchor(c)) {
-        Y = sY[0];
+      double Xc = sY[0];
 #pragma unroll
-        for (int k = 1; k < NW; ++k) Y += sY[k];
-      }
+      for (int k = 1; k < NW; ++k) Xc += sY[k];
+      Xc *= (double)lin_decay(g);
       // row sum of M, over the column blocks, and column sum, over the row
       // blocks; what no block writes is 0
       double rm = 0.0;
@@ -690,10 +718,10 @@ struct LinWalk {
       for (int a = 0; a < 4; ++a) rm += (double)sM[64 * a + l64];
       const double cm = (double)sM[256 + l64] + (double)sM[320 + l64];
       const double own = rm + (double)rdot - cm;
-      const double head = wave_prefix_f64(own), pre = wave_prefix_f64((double)d);
-      const double Xc = Y - last_lane(pre);
-      const double dg = (last_lane(head) - head + own) + (pre - (double)d) + Xc;
-      Y = Xc + last_lane(wave_prefix_f64((double)rdot));
+      const double head = wave_prefix_f64(own);
+      double pre = __shfl_up(wave_prefix_f64((double)d), 1, 64);   // without the token's own c
+      if (l64 == 0) pre = 0.0;
+      const double dg = (last_lane(head) - head + own) + pre + Xc;
       if (l64 < n) {
         if (A.dg_tok != nullptr) (A.dg_tok + row0(c))[lane_row()] = (float)dg;
         dg_sum += dg;
@@ -836,8 +864,8 @@ __device__ __forceinline__ void lin_scan_walk(const LinScan& A) {
     const char* sK = smem + Lds::K + (kDirect ? (it & 1) * W::TK::kBytes : 0);
     const char* sV = smem + Lds::V + (kDirect && !kOut ? (it & 1) * W::TV::kBytes : 0);
     if constexpr (kDirect) {
-      // output passes: the chunk before this one was whole, its four stores may go on
-      if (kOut && it > 0) wait_rows();
+      // output passes: the chunk before this one was whole, its stores may go on
+      if (kOut && it > 0) wait_rows<MODE == kLinDQ ? 4 + W::RT : 4>();
       else wait_vmem();
       barrier_lds();
       if (!kOut && it + 1 < nch) {
@@ -883,12 +911,12 @@ __device__ __forceinline__ void lin_scan_walk(const LinScan& A) {
       S.pair_part(smem + Lds::P);
       if (bad) S.taint_out(bad_from);
       S.store_out(c, n);
-      if (kDots && w == W::kLight) S.end_dots(c, n, sR, nullptr, nullptr);
+      if (kDots && w == W::kLight) S.end_dots(c, n, g, sR, nullptr, nullptr);
     }
     S.update(sK, g);
     if (bad) S.taint_state(bad_from);
     if constexpr (MODE == kLinDQ) {
-      if (S.anchor(c)) S.store_anchor(c);
+      if (it + 1 < nch) S.store_dump(c);
     }
     if constexpr (!kDirect) barrier_lds();
   }
@@ -983,7 +1011,7 @@ void lin_rev_kernel(LinScan A, LinScan B) {
   auto begin = [&](int it) {               // the chunk's tiles and gates are there
     if constexpr (kDirect) {
       // from the third chunk on the one before was whole: its four stores may go on
-      if (it > 1) wait_rows();
+      if (it > 1) wait_rows<4>();
       else wait_vmem();
       barrier_lds();
     } else {
@@ -1027,7 +1055,7 @@ void lin_rev_kernel(LinScan A, LinScan B) {
       middle(it);
       S.pair_part(smem + Lds::PK);
       S.store_out(c, n);
-      if (w == WK::kLight) S.end_dots(c, n, sR, sM, sY);
+      if (w == WK::kLight) S.end_dots(c, n, g, sR, sM, sY);
       S.update(sO, g);
       if constexpr (!kDirect) __syncthreads();
     }
