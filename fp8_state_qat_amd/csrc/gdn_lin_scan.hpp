@@ -387,12 +387,12 @@ struct LinWalk {
   // tile rt the row 16 rt + ln, columns 16 w + 4 gq + r
   f32x4 X[RT], O[4];
   Fr vf[2];                                // V^T fragments of this wave's columns
-  float rdot;                              // DK, light wave: this lane's r_i
+  float rdot, gate;                        // DK, light wave: this lane's r_i and log decay
   double dg_sum;
 
   __device__ __forceinline__ LinWalk(const LinScan& a, const LinPlace& l, int wave)
       : A(a), L(l), w(wave), l64(threadIdx.x & 63), ln(threadIdx.x & 15), gq((threadIdx.x >> 4) & 3), rdot(0.0f),
-        dg_sum(0.0) {}
+        gate(0.0f), dg_sum(0.0) {}
 
   __device__ __forceinline__ int64_t st_at(int tr, int r) const {
     const int row = 32 * (tr / 2) + 8 * gq + 4 * (tr & 1) + r, colx = 16 * w + ln;
@@ -453,10 +453,13 @@ struct LinWalk {
     return i;
   }
   // DK: this wave's part of <S, dS>, S the state entering the chunk: from the
-  // dq pass, or what that pass started the segment from; and the light wave's r_i
+  // dq pass, or what that pass started the segment from; and the light wave's
+  // r_i and log decays
   __device__ __forceinline__ void begin_dg(int c, int n, double* sY) {
-    if (w == kLight)
+    if (w == kLight) {
       rdot = l64 < n ? (A.rdot + row0(c))[lane_row()] : 0.0f;
+      gate = l64 < n ? L.pg[((int64_t)kChunk * c + l64) * A.g_row] : 0.0f;
+    }
     double y = 0.0;
     if (c > 0) {
       const f32x4* d = dumped(c - 1);
@@ -721,7 +724,9 @@ struct LinWalk {
       const double head = wave_prefix_f64(own);
       double pre = __shfl_up(wave_prefix_f64((double)d), 1, 64);   // without the token's own c
       if (l64 == 0) pre = 0.0;
-      const double dg = (last_lane(head) - head + own) + pre + Xc;
+      double dg = (last_lane(head) - head + own) + pre + Xc;
+      // a decay of 0 (-inf, a reset) leaves no product across its token: 0, not what the sums' rounding leaves
+      if (expf(gate) == 0.0f) dg *= 0.0;
       if (l64 < n) {
         if (A.dg_tok != nullptr) (A.dg_tok + row0(c))[lane_row()] = (float)dg;
         dg_sum += dg;
@@ -1051,7 +1056,7 @@ void lin_rev_kernel(LinScan A, LinScan B) {
       S.take_v(sQ);
       S.state_part(smem + Lds::V, g);
       S.dots(n, sR, [&](int rt) { return WK::TV::row4(smem + Lds::K, 16 * rt + S.ln, 16 * w + 4 * S.gq); });
-      asm volatile("" ::"v"(S.rdot));      // its load ends before the next chunk's are asked for
+      asm volatile("" ::"v"(S.rdot), "v"(S.gate));   // their loads end before the next chunk's are asked for
       middle(it);
       S.pair_part(smem + Lds::PK);
       S.store_out(c, n);

@@ -107,6 +107,21 @@ def test_strong_decays_are_judged_on_their_own(lens, dtype):
     check_dg(d)
 
 
+@pytest.mark.parametrize("lens", [[250, 90] + FILL, [250, 90]])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_resets_have_no_gradient(lens, dtype):
+    """The derivative of e^g at g = -inf is 0, as is that of a log decay whose e^g is 0 in fp32: exactly."""
+    d = make(lens, 4, 2, 64, 64, dtype, seed=25)
+    d["g"][::7, 2] = float("-inf")
+    d["g"][::5, 1] = -200.0
+    d["g"][:, 3] = float("-inf")
+    got = check_dg(d)
+    assert not got[::7, 2].any() and not got[::5, 1].any() and not got[:, 3].any() and got[:, 2].any()
+    d["g"] = torch.tensor([-0.1, float("-inf"), -0.05, -300.0])
+    got = check_dg(d)
+    assert not got[1] and not got[3] and got[0] and got[2]
+
+
 def reach(d, name, t, H, Hk, h):
     """Rows of (dq, dk, dv, dg) and heads, and of d_initial_state, that an infinity or a NaN in row t, head h of an
     input may reach: those of the recurrence, and the chunk of 64 tokens around t."""
