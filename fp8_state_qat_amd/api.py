@@ -568,6 +568,8 @@ def _addr(t):
 def _rows(t, name):
     if not isinstance(t, torch.Tensor) or t.dim() < 1 or t.shape[-1] < 1:
         raise ValueError(f"{name} must be a tensor [..., cols] with cols >= 1")
+    if t.shape[-1] >= 1 << 31:     # the library's 32-bit cols would wrap
+        raise ValueError(f"{name} must have fewer than 2^31 columns, got {t.shape[-1]}")
     return t.shape[-1], t.numel() // t.shape[-1]
 
 

@@ -153,6 +153,19 @@ def test_act_refusals():
         api.act_unpack(codes, torch.ones(R, 2))
 
 
+def test_columns_past_32_bits_are_refused():
+    """A column count that would wrap in the library's 32-bit field (2^32 + 64 as 64) is refused, not cut."""
+    wide = lambda dt, *s: torch.empty(*s, dtype=dt, device="meta")  # noqa: E731
+    for cols in (1 << 31, (1 << 32) + 64):
+        x, w = wide(BF, 1, cols), wide(torch.float32, cols)
+        codes, scales = wide(torch.float8_e4m3fn, 1, cols), wide(torch.float32, 1, -(-cols // 64))
+        for call in (lambda: api.act_pack(x), lambda: api.act_unpack(codes, scales),
+                     lambda: api.block_norm_fwd(x, w), lambda: api.block_norm_bwd(x, w, x),
+                     lambda: api.block_norm_bwd((codes, scales), w, x, io_dtype=BF)):
+            with pytest.raises(ValueError, match="columns"):
+                call()
+
+
 # ---------------------------------------------------------------- C ABI
 def _shape(**kw):
     return GdnLin(**dict(dict(n_seqs=2, n_heads=4, qk_heads=2, dk=64, dv=128, io_dtype=1, gate_per_token=1,
