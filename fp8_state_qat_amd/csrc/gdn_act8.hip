@@ -82,7 +82,7 @@ static bool act_vec(const void* p, const void* codes, int cols) {
 
 hipError_t launch_act_pack(const void* x, int dtype, uint8_t* codes, float* scales, int64_t rows, int cols,
                            hipStream_t stream) {
-  const int64_t groups = (cols + kGroupCols - 1) / kGroupCols, n = rows * groups;
+  const int64_t groups = ((int64_t)cols + kGroupCols - 1) / kGroupCols, n = rows * groups;
   auto go = [&](auto kern, auto* p) {
     hipLaunchKernelGGL(kern, dim3(act_blocks(n)), dim3(kThreads), 0, stream, p, codes, scales, (uint32_t)n,
                        (uint32_t)groups, cols);
@@ -100,7 +100,7 @@ hipError_t launch_act_pack(const void* x, int dtype, uint8_t* codes, float* scal
 
 hipError_t launch_act_unpack(const uint8_t* codes, const float* scales, void* x, int dtype, int64_t rows, int cols,
                              hipStream_t stream) {
-  const int64_t groups = (cols + kGroupCols - 1) / kGroupCols, n = rows * groups;
+  const int64_t groups = ((int64_t)cols + kGroupCols - 1) / kGroupCols, n = rows * groups;
   auto go = [&](auto kern, auto* p) {
     hipLaunchKernelGGL(kern, dim3(act_blocks(n)), dim3(kThreads), 0, stream, codes, scales, p, (uint32_t)n,
                        (uint32_t)groups, cols);

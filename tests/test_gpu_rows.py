@@ -214,3 +214,14 @@ def test_act_past_32_bits():
     want, sc = ref.pack(x[-3:])
     assert torch.equal(s[-3:].cpu().double(), sc) and torch.equal(values((codes[-3:], s[-3:])), want)
     assert torch.equal(api.act_unpack(codes, s)[-3:].cpu(), want.float().to(BF))
+
+
+@pytest.mark.parametrize("cols", [2 ** 31 - 8, 2 ** 31 - 1])
+def test_act_one_row_of_most_columns(cols):
+    x = torch.empty(1, cols, dtype=BF, device="cuda").normal_()
+    codes, s = api.act_pack(x)
+    tail = 2 ** 31 - 256
+    want, sc = ref.pack(x[:, tail:])
+    assert s.shape == (1, 2 ** 25) and torch.equal(s[:, -4:].cpu().double(), sc)
+    assert torch.equal(values((codes[:, tail:], s[:, -4:])), want)
+    assert torch.equal(api.act_unpack(codes, s)[:, tail:].cpu(), want.float().to(BF))
