@@ -70,10 +70,17 @@ __global__ __launch_bounds__(kThreads) void act_unpack_kernel(const uint8_t* __r
   }
 }
 
-// Threads of one launch: kUnroll groups of 8 lanes for each 8 threads; the
-// host has checked that the groups fit 31 bits.
-static unsigned act_blocks(int64_t n_groups) {
-  return (unsigned)((n_groups + kUnroll * (kThreads / 8) - 1) / (kUnroll * (kThreads / 8)));
+// Runs go(first row, groups, blocks) for as many launches as the rows need:
+// kUnroll groups of 8 lanes for each 8 threads.  The host has checked that the
+// groups fit 31 bits.
+template <class F>
+static void act_launches(int64_t rows, int64_t groups, F go) {
+  constexpr int64_t kPer = kUnroll * (kThreads / 8);
+  const int64_t most = max_blocks(kThreads) * kPer / groups;
+  for (int64_t r = 0; r < rows; r += most) {
+    const int64_t n = (rows - r < most ? rows - r : most) * groups;
+    go(r, (uint32_t)n, (unsigned)((n + kPer - 1) / kPer));
+  }
 }
 
 static bool act_vec(const void* p, const void* codes, int cols) {
@@ -82,10 +89,12 @@ static bool act_vec(const void* p, const void* codes, int cols) {
 
 hipError_t launch_act_pack(const void* x, int dtype, uint8_t* codes, float* scales, int64_t rows, int cols,
                            hipStream_t stream) {
-  const int64_t groups = ((int64_t)cols + kGroupCols - 1) / kGroupCols, n = rows * groups;
+  const int64_t groups = ((int64_t)cols + kGroupCols - 1) / kGroupCols;
   auto go = [&](auto kern, auto* p) {
-    hipLaunchKernelGGL(kern, dim3(act_blocks(n)), dim3(kThreads), 0, stream, p, codes, scales, (uint32_t)n,
-                       (uint32_t)groups, cols);
+    act_launches(rows, groups, [&](int64_t r, uint32_t n, unsigned blocks) {
+      hipLaunchKernelGGL(kern, dim3(blocks), dim3(kThreads), 0, stream, p + r * cols, codes + r * cols,
+                         scales + r * groups, n, (uint32_t)groups, cols);
+    });
   };
   const bool vec = act_vec(x, codes, cols);
   if (dtype == GDN_BF16) {
@@ -100,10 +109,12 @@ hipError_t launch_act_pack(const void* x, int dtype, uint8_t* codes, float* scal
 
 hipError_t launch_act_unpack(const uint8_t* codes, const float* scales, void* x, int dtype, int64_t rows, int cols,
                              hipStream_t stream) {
-  const int64_t groups = ((int64_t)cols + kGroupCols - 1) / kGroupCols, n = rows * groups;
+  const int64_t groups = ((int64_t)cols + kGroupCols - 1) / kGroupCols;
   auto go = [&](auto kern, auto* p) {
-    hipLaunchKernelGGL(kern, dim3(act_blocks(n)), dim3(kThreads), 0, stream, codes, scales, p, (uint32_t)n,
-                       (uint32_t)groups, cols);
+    act_launches(rows, groups, [&](int64_t r, uint32_t n, unsigned blocks) {
+      hipLaunchKernelGGL(kern, dim3(blocks), dim3(kThreads), 0, stream, codes + r * cols, scales + r * groups,
+                         p + r * cols, n, (uint32_t)groups, cols);
+    });
   };
   const bool vec = act_vec(x, codes, cols);
   if (dtype == GDN_BF16) {

@@ -22,6 +22,8 @@
 // walks rows blockIdx.x, + gridDim.x, ... with its threads on fixed columns,
 // keeps their partial sums in fp32 registers and writes one partial row; a
 // second kernel adds the partial rows in fp64, in a fixed order.
+#include <type_traits>
+
 #include "gdn_rows.hpp"
 
 namespace gdn {
@@ -362,11 +364,33 @@ static void norm_go(const NormArgs& A, const NormPlan& p, int64_t blocks, hipStr
 #undef GDN_NORM_KERNEL
 }
 
+// The forward's arguments from row r on.
+static NormArgs norm_from(NormArgs A, const gdn_norm_t& s, int64_t r) {
+  const int64_t n = r * s.cols, g = r * ((s.cols + kGroupCols - 1) / kGroupCols);
+  const int64_t io = s.io_dtype == GDN_F32 ? 4 : 2, xt = s.x_dtype == GDN_F32 ? 4 : 2;
+  auto at = [](auto*& p, int64_t bytes) {
+    if (p != nullptr) p = (std::remove_reference_t<decltype(p)>)((uintptr_t)p + bytes);
+  };
+  at(A.f, n * io);
+  at(A.z, n * io);
+  at(A.res, n * xt);
+  at(A.x, n * xt);
+  at(A.h, n * io);
+  at(A.f_codes, n);
+  at(A.z_codes, n);
+  at(A.f_scales, g * 4);
+  at(A.z_scales, g * 4);
+  A.rows = s.rows - r;
+  return A;
+}
+
 template <bool kBwd>
-static hipError_t norm_launch(const gdn_norm_t& s, const NormArgs& A, bool vec, bool ckpt, hipStream_t stream) {
+static hipError_t norm_launch(const gdn_norm_t& s, const NormArgs& all, bool vec, bool ckpt, hipStream_t stream) {
   const NormPlan p = norm_plan(s.cols, vec);
   const int64_t rows_of = norm_rows_of(p);
-  const int64_t blocks = kBwd ? norm_bwd_blocks(s, p) : (s.rows + rows_of - 1) / rows_of;
+  const int64_t most = max_blocks(p.tpr > kThreads ? p.tpr : kThreads);
+  NormArgs A = all;
+  int64_t blocks = kBwd ? norm_bwd_blocks(s, p) : (s.rows + rows_of - 1) / rows_of;
   auto typed = [&](auto tio, auto tx) {
     using TIO = decltype(tio);
     using TX = decltype(tx);
@@ -378,9 +402,21 @@ static hipError_t norm_launch(const gdn_norm_t& s, const NormArgs& A, bool vec, 
       else norm_go<TIO, TX, false, false, kBwd>(A, p, blocks, stream);
     }
   };
-  if (s.io_dtype == GDN_F32) typed(float(), float());
-  else if (s.x_dtype == GDN_F32) typed(uint16_t(), float());
-  else typed(uint16_t(), uint16_t());
+  auto launch = [&] {
+    if (s.io_dtype == GDN_F32) typed(float(), float());
+    else if (s.x_dtype == GDN_F32) typed(uint16_t(), float());
+    else typed(uint16_t(), uint16_t());
+  };
+  if (kBwd || blocks <= most) {
+    launch();
+    return hipGetLastError();
+  }
+  for (int64_t b = 0, all_blocks = blocks; b < all_blocks; b += most) {
+    blocks = all_blocks - b < most ? all_blocks - b : most;
+    A = norm_from(all, s, b * rows_of);
+    A.rows = A.rows < blocks * rows_of ? A.rows : blocks * rows_of;
+    launch();
+  }
   return hipGetLastError();
 }
 

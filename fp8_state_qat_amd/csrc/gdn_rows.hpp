@@ -10,6 +10,10 @@ namespace gdn {
 
 constexpr int kGroupCols = 64;  // columns that share one scale: the octets of 8 lanes
 
+// Workgroups of one launch at most: a launch takes fewer than 2^32 threads in
+// a dimension.  Larger calls go in several launches, rows after rows.
+constexpr int64_t max_blocks(int threads) { return (((int64_t)1 << 32) - 1) / threads; }
+
 // Eight consecutive columns of a row as fp32, n of them valid (the rest 0).
 // kVec: every row starts at a multiple of 16 bytes and cols % 8 == 0, so an
 // octet is whole or empty and moves in 16-byte accesses; else column by column.

@@ -225,3 +225,47 @@ def test_act_one_row_of_most_columns(cols):
     assert s.shape == (1, 2 ** 25) and torch.equal(s[:, -4:].cpu().double(), sc)
     assert torch.equal(values((codes[:, tail:], s[:, -4:])), want)
     assert torch.equal(api.act_unpack(codes, s)[:, tail:].cpu(), want.float().to(BF))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_act_more_groups_than_one_launch_takes(dtype):
+    """Four threads a group: from 2^30 groups on a launch would pass 2^32 threads."""
+    rows = 2 ** 30 + 70
+    x = torch.zeros(rows, 1, dtype=dtype, device="cuda")
+    at = torch.tensor([0, 5, 2 ** 30 - 65, 2 ** 30 - 64, 2 ** 30 - 63, 2 ** 30, rows - 1], device="cuda")
+    x[at, 0] = torch.randn(len(at), device="cuda").to(dtype)
+    codes, s = api.act_pack(x)
+    want, sc = ref.pack(x[at])
+    assert torch.equal(s[at].cpu().double(), sc) and torch.equal(values((codes[at], s[at])), want)
+    assert (s != 1).sum() == (sc != 1).sum()
+    back = api.act_unpack(codes, s, dtype=dtype)
+    assert torch.equal(back[at].cpu(), want.float().to(dtype)) and back.count_nonzero() == len(at)
+
+
+@pytest.mark.parametrize("rows,cols", [(2 ** 29 + 45, 8), (2 ** 23 + 3, 513)])
+def test_norm_more_rows_than_one_launch_takes(rows, cols):
+    """8 and 512 threads a row: the rows on both sides of 2^32 threads, residual, gate and checkpoints among them."""
+    f = torch.zeros(rows, cols, dtype=BF, device="cuda")
+    border = 2 ** 29 - 32 if cols == 8 else 2 ** 23 - 1
+    at = torch.tensor([0, border - 1, border, border + 1, rows - 1], device="cuda")
+    gen = torch.Generator().manual_seed(cols)
+    fv, zv = (torch.randn(len(at), cols, generator=gen).to(BF) for _ in range(2))
+    f[at] = fv.cuda()
+    w = 1 + 0.1 * torch.randn(cols, generator=gen)
+    x, h, (fc, fs), _ = api.block_norm_fwd(f, w.cuda(), residual=f, w_pre=w.cuda(), checkpoint=True)
+    d, w = fv.double(), w.double()
+    rx, rh = ref.norm(d, w, None, None, d, 1.0, w, 1e-6)
+    mag = (rx - d).abs() * 8 + d.abs()
+    close(x[at], rx, mag, "x")
+    close(h[at], rh, mag / torch.sqrt(rx.pow(2).mean(-1, keepdim=True) + 1e-6) * w.abs() + rh.abs(), "h")
+    want, sc = ref.pack(fv)
+    assert torch.equal(values((fc[at], fs[at])), want) and torch.equal(fs[at].cpu().double(), sc)
+    assert x.count_nonzero() == x[at].count_nonzero() and h.count_nonzero() == h[at].count_nonzero()
+    del x, h, fc, fs
+    f.zero_()
+    f[at] = zv.cuda()
+    x, _ = api.block_norm_fwd(f, w.float().cuda(), gate=f)
+    d = zv.double()
+    rx, _ = ref.norm(d, w, d, "silu", None, 1.0, None, 1e-6)
+    close(x[at], rx, rx.abs() * 8, "gated x")
+    assert x.count_nonzero() == x[at].count_nonzero()
