@@ -339,7 +339,10 @@ gdn_status_t gdn_chunk_bwd_dh(const gdn_shape_t* shape, const void* q, const voi
 
 namespace {
 
-gdn_status_t check_lin(const gdn_lin_t* s, bool step) {
+enum LinCall { kLinFwd, kLinBwd, kLinStep };
+
+gdn_status_t check_lin(const gdn_lin_t* s, LinCall call) {
+  const bool step = call == kLinStep;
   if (s == nullptr) return fail(GDN_ERR_INVALID_ARG, "shape is NULL");
   if (s->n_seqs < 1) return fail(GDN_ERR_INVALID_ARG, "n_seqs must be >= 1 (got %d)", s->n_seqs);
   if (s->n_heads < 1) return fail(GDN_ERR_INVALID_ARG, "n_heads must be >= 1 (got %d)", s->n_heads);
@@ -366,6 +369,8 @@ gdn_status_t check_lin(const gdn_lin_t* s, bool step) {
   const int64_t units = (int64_t)s->n_heads * (s->dv / 16) *
                         (step ? (int64_t)s->n_seqs : s->total_tokens / 64 + s->n_seqs);
   if (units >= (int64_t)1 << 31) return fail(GDN_ERR_UNSUPPORTED, "too many (segment, head, tile) units");
+  if (step ? !gdn::lin_step_fits(*s) : !gdn::lin_fits(*s, call == kLinBwd))
+    return fail(GDN_ERR_UNSUPPORTED, "a launch would pass 2^32 threads (n_seqs * n_heads * dv too large)");
   return GDN_OK;
 }
 
@@ -415,19 +420,19 @@ extern "C" {
 
 size_t gdn_lin_attn_fwd_workspace_bytes(const gdn_lin_t* shape) {
   g_err[0] = 0;
-  return check_lin(shape, false) == GDN_OK ? gdn::lin_fwd_workspace_bytes(*shape) : 0;
+  return check_lin(shape, kLinFwd) == GDN_OK ? gdn::lin_fwd_workspace_bytes(*shape) : 0;
 }
 
 size_t gdn_lin_attn_bwd_workspace_bytes(const gdn_lin_t* shape) {
   g_err[0] = 0;
-  return check_lin(shape, false) == GDN_OK ? gdn::lin_bwd_workspace_bytes(*shape) : 0;
+  return check_lin(shape, kLinBwd) == GDN_OK ? gdn::lin_bwd_workspace_bytes(*shape) : 0;
 }
 
 gdn_status_t gdn_lin_attn_fwd(const gdn_lin_t* shape, const void* q, const void* k, const void* v, const float* g,
                               const int32_t* cu_seqlens, const float* initial_state, void* o, float* final_state,
                               void* workspace, size_t workspace_bytes, void* stream) {
   g_err[0] = 0;
-  gdn_status_t st = check_lin(shape, false);
+  gdn_status_t st = check_lin(shape, kLinFwd);
   if (st != GDN_OK) return st;
   if (!cu_seqlens || !final_state)
     return fail(GDN_ERR_INVALID_ARG, "cu_seqlens and final_state must be non-NULL");
@@ -454,7 +459,7 @@ gdn_status_t gdn_lin_attn_bwd(const gdn_lin_t* shape, const void* q, const void*
                               const float* d_final_state, void* dq, void* dk, void* d_v, float* dg,
                               float* d_initial_state, void* workspace, size_t workspace_bytes, void* stream) {
   g_err[0] = 0;
-  gdn_status_t st = check_lin(shape, false);
+  gdn_status_t st = check_lin(shape, kLinBwd);
   if (st != GDN_OK) return st;
   if (!cu_seqlens || !d_initial_state)
     return fail(GDN_ERR_INVALID_ARG, "cu_seqlens and d_initial_state must be non-NULL");
@@ -480,7 +485,7 @@ gdn_status_t gdn_lin_attn_bwd(const gdn_lin_t* shape, const void* q, const void*
 gdn_status_t gdn_lin_attn_step(const gdn_lin_t* shape, const void* q, const void* k, const void* v, const float* g,
                                float* state, void* o, void* stream) {
   g_err[0] = 0;
-  gdn_status_t st = check_lin(shape, true);
+  gdn_status_t st = check_lin(shape, kLinStep);
   if (st != GDN_OK) return st;
   if (!q || !k || !v || !g || !state || !o)
     return fail(GDN_ERR_INVALID_ARG, "q, k, v, g, state and o must be non-NULL");

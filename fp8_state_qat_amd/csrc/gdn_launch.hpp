@@ -112,6 +112,9 @@ hipError_t launch_chunk_bwd_dh(const gdn_shape_t& s, const void* q, const void* 
 // Linear attention (gdn_lin_step.hip, gdn_lin.hip).
 hipError_t launch_lin_step(const gdn_lin_t& s, const void* q, const void* k, const void* v, const float* g,
                            float* state, void* o, hipStream_t stream);
+// Every launch of the call stays below 2^32 threads.
+bool lin_fits(const gdn_lin_t& s, bool bwd);
+bool lin_step_fits(const gdn_lin_t& s);
 size_t lin_fwd_workspace_bytes(const gdn_lin_t& s);
 hipError_t launch_lin_fwd(const gdn_lin_t& s, const void* q, const void* k, const void* v, const float* g,
                           const int32_t* cu_seqlens, const float* initial_state, void* o, float* final_state,

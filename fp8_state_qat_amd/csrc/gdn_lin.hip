@@ -250,6 +250,14 @@ void starts(const gdn_lin_t& s, const LinLayout& L, const LinStarts& F, const Li
 
 }  // namespace
 
+bool lin_fits(const gdn_lin_t& s, bool bwd) {
+  const LinLayout L = lin_layout(s, nullptr, bwd);
+  const int64_t scan = L.slots * L.VH * 4 * (bwd ? s.dk + L.tw : L.tw);
+  const int64_t sums = s.total_tokens * (L.R > 1 ? (int64_t)s.qk_heads * (s.dk / 4) : 0);
+  const int64_t dg = s.total_tokens * (L.tiles > 1 ? s.n_heads : 0);
+  const int64_t most = (int64_t)1 << 32;
+  return scan < most && (!bwd || (sums + kThreads < most && dg + kThreads < most));
+}
 size_t lin_fwd_workspace_bytes(const gdn_lin_t& s) { return lin_layout(s, nullptr, false).bytes; }
 size_t lin_bwd_workspace_bytes(const gdn_lin_t& s) { return lin_layout(s, nullptr, true).bytes; }
 

@@ -58,11 +58,17 @@ __global__ __launch_bounds__(kThreads) void lin_step_kernel(const T* __restrict_
 // Rows of a workgroup: 64 (32 KiB of state at dk = 128, eight 16-byte loads a
 // thread in flight) when that still gives the card a workgroup for every
 // compute unit, else 16, which spreads a small batch over four times as many.
+static bool lin_step_wide(const gdn_lin_t& s) { return (int64_t)s.n_seqs * s.n_heads * (s.dv / 64) >= 512; }
+
+bool lin_step_fits(const gdn_lin_t& s) {
+  return (int64_t)s.n_seqs * s.n_heads * (s.dv / (lin_step_wide(s) ? 64 : 16)) * kThreads < (int64_t)1 << 32;
+}
+
 hipError_t launch_lin_step(const gdn_lin_t& s, const void* q, const void* k, const void* v, const float* g,
                            float* state, void* o, hipStream_t stream) {
   const int64_t nh = (int64_t)s.n_seqs * s.n_heads;
   const int share = s.n_heads / s.qk_heads;
-  const bool wide = nh * (s.dv / 64) >= 512;
+  const bool wide = lin_step_wide(s);
   const int rows = wide ? 64 : 16;
   auto go = [&](auto kern, auto tag) {
     using T = decltype(tag);

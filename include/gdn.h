@@ -364,7 +364,9 @@ size_t gdn_chunk_bwd_workspace_bytes(const gdn_shape_t* shape);
  *          gate_per_token, else [n_heads], one decay a head for all tokens.
  *          -inf (the token starts from an empty state) is allowed.
  * A state is [n_seqs, n_heads, dv, dk] fp32.  Buffers are 16-byte aligned (g
- * and dg 4), row-major.
+ * and dg 4), row-major.  At most 65535 sequences (the step: any number), and
+ * refused with GDN_ERR_UNSUPPORTED where a launch would pass 2^32 threads: from
+ * n_seqs * n_heads * dv of about 2^29 (backward) or 2^30 on.
  *
  * An infinity or a NaN in q, k, v or g reaches the outputs and the state that
  * the recurrence lets it reach, as a NaN, and no earlier token; in the

@@ -205,6 +205,22 @@ def test_lin_rejects_bad_shapes(kw, status):
     assert _bwd(s, ws_bytes=1 << 40) == status and _lib.last_error()
 
 
+def test_lin_rejects_launches_past_32_bits_of_threads():
+    """A launch takes fewer than 2^32 threads: more (sequence, head) pairs are refused, not left to the launch."""
+    L = _lib.lib()
+    most = dict(n_seqs=32768, total_tokens=32768, dk=64, dv=64, gate_per_token=0)   # 4 threads for 64 + 64 columns
+    bwd = L.gdn_lin_attn_bwd_workspace_bytes
+    assert bwd(ctypes.byref(_shape(**most, n_heads=255, qk_heads=255))) > 0
+    s = _shape(**most, n_heads=256, qk_heads=256)
+    assert bwd(ctypes.byref(s)) == 0 and _bwd(s, ws_bytes=1 << 50) == 2 and "threads" in _lib.last_error()
+    fwd = L.gdn_lin_attn_fwd_workspace_bytes                                        # 4 threads for 64 columns
+    assert fwd(ctypes.byref(s)) > 0 and fwd(ctypes.byref(_shape(**most, n_heads=511, qk_heads=511))) > 0
+    s = _shape(**most, n_heads=512, qk_heads=512)
+    assert fwd(ctypes.byref(s)) == 0 and _fwd(s, ws_bytes=1 << 50) == 2 and "threads" in _lib.last_error()
+    step = _shape(n_seqs=1 << 20, total_tokens=1 << 20, n_heads=16, qk_heads=16, dv=64)   # 256 threads for 64 rows
+    assert L.gdn_lin_attn_step(ctypes.byref(step), *[P(FAKE)] * 7) == 2 and "threads" in _lib.last_error()
+
+
 def test_lin_rejects_null_misaligned_and_short_workspaces():
     s = _shape()
     for kw in (dict(q=0), dict(q=FAKE + 8), dict(ws=0), dict(ws=FAKE + 16), dict(ws_bytes=16)):
