@@ -269,3 +269,21 @@ def test_norm_more_rows_than_one_launch_takes(rows, cols):
     rx, _ = ref.norm(d, w, d, "silu", None, 1.0, None, 1e-6)
     close(x[at], rx, rx.abs() * 8, "gated x")
     assert x.count_nonzero() == x[at].count_nonzero()
+
+
+@pytest.mark.parametrize("rows,cols", [(2 ** 20 + 3, 1032), (2 ** 20 + 3, 513), (2 ** 22 + 77, 64)])
+def test_norm_weight_gradients_of_many_rows(rows, cols):
+    """Rows that are all alike, whose sums' roundings line up: the weights' gradients stay within 2^-18 of the sums
+    (at most 32 rows are added in fp32, 2^-19; a term's own rounding is 2^-19.3 as above)."""
+    gen = torch.Generator().manual_seed(rows + cols)
+    one, dx, dh = (torch.randn(1, cols, generator=gen).to(BF) for _ in range(3))
+    w = 1 + 0.1 * torch.randn(cols, generator=gen)
+    f, d_x, d_h = (t.cuda().expand(rows, cols).contiguous() for t in (one, dx, dh))
+    got = api.block_norm_bwd(f, w.cuda(), d_x, d_h=d_h, x=f, w_pre=w.cuda(), want_residual=False)
+    f, d_x, d_h, w = one.double(), dx.double(), dh.double(), w.double()
+    r = 1 / torch.sqrt(f.pow(2).mean() + 1e-6)
+    n, t = f * r, d_h * w
+    d = d_x + r * (t - n * (t * n).mean())
+    mag = (d_x.abs() + r * (t.abs() + n.abs() * (t * n).abs().mean())) * n.abs()
+    close(got[3], rows * (d * n)[0], rows * mag[0], "dw_post")
+    close(got[4], rows * (d_h * n)[0], rows * (d_h * n).abs()[0], "dw_pre")
