@@ -55,19 +55,41 @@ struct NormArgs {
   float res_scale, eps;
 };
 
-// The gate's value a(z) and its derivative.  e^-z is the hardware's 2^x of
-// -z log2(e), whose rounding leaves |z| 2^-24 of the value, and the quotient
-// its reciprocal (2^-23): the correctly rounded forms took half of the
-// kernels' instructions (per-head gated norms of 262144 x 128: 32 us, 6.2 TB/s,
-// for 39; a training step's norms of 16384 x 2048: 188 for 204).
+// The gate's value a(z) and, for the backward, its derivative, from e = e^-|z|,
+// which does not overflow: with r = 1 / (1 + e) the sigmoid p and 1 - p are r
+// and e r, in the order of z's sign.  fp32 rows take exp_down and the correctly
+// rounded quotient.  bf16 rows take the hardware's 2^x of |z| log2(e) and its
+// reciprocal, which leave 2^-20 + |z| 2^-24 of a value, far below the output's
+// 2^-9 (fp32's way takes half of the kernel's instructions); both flush
+// subnormal numbers, so they are kept 2^24 away from them.  The forward does
+// without the sign there, p = 1 / (1 + e^-z): heads of 262144 x 128 take 37.6
+// us so, 38.9 with it.
+template <typename T, bool kDer>
 __device__ __forceinline__ void gate_act(float z, int act, float& a, float& da) {
-  const float p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
+  constexpr float kLog2e = 1.4426950408889634f;
+  if constexpr (sizeof(T) == 2 && !kDer) {
+    const float e = __builtin_amdgcn_exp2f(fmaf(z, -kLog2e, -24.0f));
+    const float p = __builtin_amdgcn_rcpf(e + 0x1p-24f) * 0x1p-24f;
+    a = act == GDN_ACT_SIGMOID ? p : z * p;
+    return;
+  }
+  float r, er;
+  if constexpr (sizeof(T) == 4) {
+    const float e = exp_down(-fabsf(z));
+    r = 1.0f / (1.0f + e);
+    er = e * r;
+  } else {
+    const float e = __builtin_amdgcn_exp2f(fmaf(fabsf(z), -kLog2e, 24.0f));
+    r = __builtin_amdgcn_rcpf(fmaf(e, 0x1p-24f, 1.0f));
+    er = e * r * 0x1p-24f;
+  }
+  const float p = z < 0.0f ? er : r, q = z < 0.0f ? r : er;
   if (act == GDN_ACT_SIGMOID) {
     a = p;
-    da = p * (1.0f - p);
+    da = p * q;
   } else {
     a = z * p;
-    da = p * (1.0f + z * (1.0f - p));
+    da = p * (1.0f + z * q);
   }
 }
 
@@ -129,7 +151,7 @@ __global__ __launch_bounds__(norm_block<TPR>()) void block_norm_fwd_kernel(NormA
       float t = f[j][c] * r * w[c];
       if (A.z) {
         float a, da;
-        gate_act(y[j][c], A.act, a, da);
+        gate_act<TIO, false>(y[j][c], A.act, a, da);
         t *= a;
       }
       t *= A.res_scale;
@@ -239,7 +261,7 @@ __global__ __launch_bounds__(norm_block<TPR>()) void block_norm_bwd_kernel(NormA
       for (int c = 0; c < 8; ++c) {
         const float dy = A.res_scale * d[j][c], nn = f[j][c] * r;
         float a = 1.0f, da = 0.0f;
-        if (A.z) gate_act(z[j][c], A.act, a, da);
+        if (A.z) gate_act<TIO, true>(z[j][c], A.act, a, da);
         z[j][c] = dy * nn * wp[j][c] * da;
         const float u = dy * a;
         acc_p[j][c] = fmaf(u, nn, acc_p[j][c]);

@@ -287,3 +287,27 @@ def test_norm_weight_gradients_of_many_rows(rows, cols):
     mag = (d_x.abs() + r * (t.abs() + n.abs() * (t * n).abs().mean())) * n.abs()
     close(got[3], rows * (d * n)[0], rows * mag[0], "dw_post")
     close(got[4], rows * (d_h * n)[0], rows * (d_h * n).abs()[0], "dw_pre")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+def test_gate_far_from_zero(dtype, act):
+    """Gates of -103 to 103.  With f = w = 1 the outputs are the gate's value and, in d_gate, its derivative times n
+    = 1.  Either is a product of at most 12 fp32 roundings whatever z is (fp32: 2^-20 of it, of p (1 + |z| (1 - p))
+    for silu's derivative, whose sum cancels), and below 2^-126 a few subnormal steps times |z|; bf16's exponential
+    adds |z| 2^-23, then the output's rounding."""
+    z = torch.linspace(-103, 103, 64 * 64).view(64, 64).to(dtype)
+    f, w = torch.ones(64, 64, dtype=dtype), torch.ones(64)
+    x, _ = api.block_norm_fwd(f.cuda(), w.cuda(), gate=z.cuda(), act=act, eps=1e-30)
+    # dy = n = w = 1: the gradient of the gate is a'(z)
+    dz = api.block_norm_bwd(f.cuda(), w.cuda(), f.cuda(), gate=z.cuda(), act=act, eps=1e-30, want_residual=False)[1]
+    d = z.double()
+    p, q = torch.sigmoid(d), torch.sigmoid(-d)
+    pairs = ((x, p, p), (dz, p * q, p * q)) if act == "sigmoid" else \
+        ((x, d * p, (d * p).abs()), (dz, p * (1 + d * q), p * (1 + d.abs() * q)))
+    for got, want, mag in pairs:
+        tol = 2.0 ** -20 * mag + 2.0 ** -146 * (1 + d.abs())
+        if dtype == BF:
+            tol = tol + d.abs() * 2.0 ** -23 * mag + 2.0 ** -8 * want.abs() + 2.0 ** -133
+        bad = (got.double().cpu() - want).abs() > tol
+        assert not bad.any(), (int(bad.sum()), z[bad][:4].tolist(), got.cpu()[bad][:4].tolist(), want[bad][:4].tolist())
