@@ -57,7 +57,7 @@ struct NormArgs {
 
 // The gate's value a(z) and, for the backward, its derivative, from e = e^-|z|,
 // which does not overflow: with r = 1 / (1 + e) the sigmoid p and 1 - p are r
-// and e r, in the order of z's sign.  fp32 rows take exp_down and the correctly
+// and e r, in the order of z's sign.  fp32 rows take exp_full and the correctly
 // rounded quotient.  bf16 rows take the hardware's 2^x of |z| log2(e) and its
 // reciprocal, which leave 2^-20 + |z| 2^-24 of a value, far below the output's
 // 2^-9 (fp32's way takes half of the kernel's instructions); both flush
@@ -75,7 +75,7 @@ __device__ __forceinline__ void gate_act(float z, int act, float& a, float& da) 
   }
   float r, er;
   if constexpr (sizeof(T) == 4) {
-    const float e = exp_down(-fabsf(z));
+    const float e = exp_full(-fabsf(z));
     r = 1.0f / (1.0f + e);
     er = e * r;
   } else {

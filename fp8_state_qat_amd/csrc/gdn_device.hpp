@@ -361,4 +361,14 @@ __device__ __forceinline__ void mma_f32(f32x4& c, const float (&a)[8], const flo
   for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
 }
 
+// e^x, off by less than 2^-22 of itself whatever x (subnormal results by their
+// step): 2^n 2^a with n = round(x log2(e)) and a = x log2(e) - n from one fma,
+// the rest of log2(e) added.  (expf, compiled with contraction, takes that fma
+// and then subtracts the product's rounding again: |x| 2^-24.)
+__device__ __forceinline__ float exp_full(float x) {
+  const float n = rintf(__builtin_amdgcn_fmed3f(x, -150.0f, 90.0f) * 0x1.715476p+0f);
+  const float a = fmaf(x, 0x1.4ae0cp-26f, fmaf(x, 0x1.715476p+0f, -n));
+  return ldexpf(__builtin_amdgcn_exp2f(a), (int)n);
+}
+
 }  // namespace gdn

@@ -254,10 +254,28 @@ __device__ __forceinline__ double last_lane(double v) {
   const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
-__device__ __forceinline__ float lin_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// A sum of log decays in base 2 as its nearest whole number and the rest, and
+// 2^(n + f): decays are off by a few 2^-24 however strong they are.  (e^x as
+// 2^x of a rounded x log2(e), or by expf compiled with contraction, is off by
+// |x| 2^-24.)
+struct LinLog {
+  int n;
+  float f;
+};
+__device__ __forceinline__ LinLog lin_log(double x) {
+  const double n = x > -1e9 ? (x < 1e9 ? __builtin_rint(x) : 1e9) : -1e9;   // a NaN stays in the rest
+  return {(int)n, (float)(x - n)};
+}
+__device__ __forceinline__ float lin_pow(int n, float f) { return ldexpf(__builtin_amdgcn_exp2f(f), n); }
+__device__ __forceinline__ float lin_pow(double x) {
+  const LinLog s = lin_log(x);
+  return lin_pow(s.n, s.f);
+}
 
 struct LinGates {
-  float hi[kChunk], lo[kChunk];  // G_i = hi + lo
+  int n[kChunk];                 // G_i log2(e) = n + f
+  float f[kChunk];
   float in[kChunk];              // weight of X^T Q_a
   float out[kChunk];             // weight of K_b V_b^T in the state
 };
@@ -273,18 +291,18 @@ __device__ __forceinline__ float lin_decay(const LinGatesRev& g) { return g.deca
 
 // One wave: the chunk's gate vectors; rows from n on have no weight in the
 // state.  The sums run in fp64 (far tokens of a strongly decaying chunk differ
-// by large G); a log decay below -1e4 has the weight 0 and is held there, so
-// that -inf leaves no NaN.  later: log decays between the chunk and the end
-// that its state weights refer to.  Returns the chunk's sum.
+// by large G) and base 2; a log decay below -1e4 has the weight 0 and is held
+// there, so that -inf leaves no NaN.  later: log decays between the chunk and
+// the end that its state weights refer to.  Returns the chunk's sum.
 template <bool kRev>
 __device__ __forceinline__ double lin_gates(LinGatesOf<kRev>& s, float g, int n, double later = 0.0) {
   const int ln = threadIdx.x & 63;
-  const double G = wave_prefix_f64((double)(g < -1e4f ? -1e4f : g));
+  const double G = wave_prefix_f64((double)(g < -1e4f ? -1e4f : g) * 1.4426950408889634);
   const double C = last_lane(G);
-  const float hi = (float)G;
-  s.hi[ln] = hi;
-  s.lo[ln] = (float)(G - (double)hi);
-  const float a = expf(hi), b = expf((float)(C - G + later));
+  const LinLog own = lin_log(G);
+  s.n[ln] = own.n;
+  s.f[ln] = own.f;
+  const float a = lin_pow(own.n, own.f), b = lin_pow(C - G + later);
   s.in[ln] = kRev ? b : a;
   s.out[ln] = ln < n ? (kRev ? a : b) : 0.0f;
   if constexpr (kRev) {
@@ -506,7 +524,8 @@ struct LinWalk {
     for (int blk = first; blk < 6; blk += step) {
       int a, kb;
       lin_block_at<kRev>(blk, a, kb);
-      const float ah = g.hi[16 * a + ln], al = g.lo[16 * a + ln];
+      const int an = g.n[16 * a + ln];
+      const float af = g.f[16 * a + ln];
       // both tiles of the block, also where the triangle leaves one out (2 of 6)
       f32x4 acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
       f32x4 acc2[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
@@ -531,13 +550,14 @@ struct LinWalk {
 #pragma unroll
       for (int bb = 0; bb < 2; ++bb) {
         const int b = 2 * kb + bb;
-        const f32x4 bh = *reinterpret_cast<const f32x4*>(&g.hi[16 * b + 4 * gq]);
-        const f32x4 bl = *reinterpret_cast<const f32x4*>(&g.lo[16 * b + 4 * gq]);
+        const int4 b4 = *reinterpret_cast<const int4*>(&g.n[16 * b + 4 * gq]);
+        const int bn[4] = {b4.x, b4.y, b4.z, b4.w};
+        const f32x4 bf = *reinterpret_cast<const f32x4*>(&g.f[16 * b + 4 * gq]);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int ia = 16 * a + ln, ib = 16 * b + 4 * gq + r;
-          const float d = kRev ? (bh[r] - ah) + (bl[r] - al) : (ah - bh[r]) + (al - bl[r]);
-          pw[4 * bb + r] = (kRev ? ib >= ia && ib < n : ib <= ia) ? acc[bb][r] * lin_exp(d) : 0.0f;
+          const float d = kRev ? lin_pow(bn[r] - an, bf[r] - af) : lin_pow(an - bn[r], af - bf[r]);
+          pw[4 * bb + r] = (kRev ? ib >= ia && ib < n : ib <= ia) ? acc[bb][r] * d : 0.0f;
           if constexpr (MODE == kLinDK) {
             const float m = ib > ia ? acc2[bb][r] * pw[4 * bb + r] : 0.0f;
             cm += m;
@@ -726,7 +746,7 @@ struct LinWalk {
       if (l64 == 0) pre = 0.0;
       double dg = (last_lane(head) - head + own) + pre + Xc;
       // a decay of 0 (-inf, a reset) leaves no product across its token: 0, not what the sums' rounding leaves
-      if (expf(gate) == 0.0f) dg *= 0.0;
+      if (gate < -104.0f) dg *= 0.0;         // e^-104 rounds to 0
       if (l64 < n) {
         if (A.dg_tok != nullptr) (A.dg_tok + row0(c))[lane_row()] = (float)dg;
         dg_sum += dg;
@@ -926,7 +946,7 @@ __device__ __forceinline__ void lin_scan_walk(const LinScan& A) {
     if constexpr (!kDirect) barrier_lds();
   }
   S.store_state();
-  if (!kOut && w == W::kLight && S.l64 == 0) A.seg_decay[L.sv] = expf((float)Gsum);
+  if (!kOut && w == W::kLight && S.l64 == 0) A.seg_decay[L.sv] = lin_pow(Gsum);
 }
 
 template <class Eng, int CK, int CV, int MODE>

@@ -40,7 +40,7 @@ __global__ __launch_bounds__(kThreads) void lin_step_kernel(const T* __restrict_
   }
 #pragma unroll
   for (int p = 0; p < NP; ++p) vr[p] = io<T>::ld(v + nh * dv + kRows * vt + rr + RPP * p);
-  const float a = expf(g[n * g_row + h]);
+  const float a = exp_full(g[n * g_row + h]);
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     x[p].x = fmaf(x[p].x, a, vr[p] * kc[0]);

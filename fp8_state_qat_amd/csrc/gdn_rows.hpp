@@ -14,17 +14,6 @@ constexpr int kGroupCols = 64;  // columns that share one scale: the octets of 8
 // a dimension.  Larger calls go in several launches, rows after rows.
 constexpr int64_t max_blocks(int threads) { return (((int64_t)1 << 32) - 1) / threads; }
 
-// e^x for x <= 0, off by less than 2^-22 of itself whatever x (subnormal
-// results by their step): 2^n 2^a with n = round(x log2(e)) and a = x log2(e) -
-// n from one fma, the rest of log2(e) added.  (expf, compiled with contraction,
-// takes that fma and then subtracts the product's rounding again: |x| 2^-24.)
-__device__ __forceinline__ float exp_down(float x) {
-  x = x < -150.0f ? -150.0f : x;
-  const float n = rintf(x * 0x1.715476p+0f);
-  const float a = fmaf(x, 0x1.4ae0cp-26f, fmaf(x, 0x1.715476p+0f, -n));
-  return ldexpf(__builtin_amdgcn_exp2f(a), (int)n);
-}
-
 // Eight consecutive columns of a row as fp32, n of them valid (the rest 0).
 // kVec: every row starts at a multiple of 16 bytes and cols % 8 == 0, so an
 // octet is whole or empty and moves in 16-byte accesses; else column by column.

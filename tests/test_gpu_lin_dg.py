@@ -18,7 +18,7 @@ import torch
 
 import lin_ref as ref
 from fp8_state_qat_amd import api
-from test_gpu_lin import BF, F32, dev, make
+from test_gpu_lin import BF, F32, close, dev, make
 
 pytestmark = pytest.mark.gpu
 
@@ -120,6 +120,36 @@ def test_resets_have_no_gradient(lens, dtype):
     d["g"] = torch.tensor([-0.1, float("-inf"), -0.05, -300.0])
     got = check_dg(d)
     assert not got[1] and not got[3] and got[0] and got[2]
+
+
+@pytest.mark.parametrize("lens", [[150, 90] + FILL, [150, 90]])
+@pytest.mark.parametrize("gate", ["token", "head"])
+def test_strong_decays_keep_fp32(lens, gate):
+    """Outputs that only far tokens or the initial state reach, through decays of e^-15 to e^-60, keep fp32's
+    precision: 2^-19 of their magnitudes, as test_gpu_lin.py has it for every fp32 output."""
+    d = make(lens, 4, 4, 64, 64, F32, gate, seed=26)
+    d["g"] = 10 * d["g"] - 1.5
+    T = d["v"].shape[0]
+    far = torch.arange(T) % 24 == 23
+    far[:30] = False
+    d["k"][~far] = 0
+    d["do"][torch.arange(T) % 24 != 11] = 0
+    x = dev(d)
+    o, S = api.lin_attn_fwd(x["q"], x["k"], x["v"], x["g"], x["cu"], initial_state=x["S0"])
+    a = (d["q"], d["k"], d["v"], d["g"], d["cu"], d["S0"])
+    (ro, rS), (mo, mS) = ref.lin(*a), ref.lin_abs(*a)
+    close(o, ro, mo, "o fp32")
+    close(S, rS, mS, "state fp32")
+    want, mag, got = ref.lin(*a, d["do"], d["dS"]), ref.lin_abs(*a, d["do"], d["dS"]), grads(d)
+    for i, name in ((0, "dq"), (1, "dk"), (2, "dv"), (4, "d_initial_state")):
+        close(got[i], want[i], mag[i], f"{name} fp32")
+    # the step: one token whose state only decays
+    x["v"][:1] = 0
+    n, g = 1, torch.tensor([[-15.3, -33.7, -58.9, -71.3]])
+    S = x["S0"][:1].clone()
+    api.lin_attn_step(x["q"][:n], x["k"][:n], x["v"][:n], g.cuda(), S)
+    want = d["S0"][:1].double() * g.double().exp()[..., None, None]
+    close(S, want, want.abs(), "step's state fp32")
 
 
 def reach(d, name, t, H, Hk, h):
