@@ -635,6 +635,8 @@ def block_norm_bwd(f, w_post, d_x, *, d_h=None, x=None, w_pre=None, gate=None, a
     (needed with checkpoints and no d_h).
     Returns (d_f, d_gate, d_residual, d_w_post, d_w_pre), None where the
     forward had no such input (d_residual also without want_residual)."""
+    if not isinstance(f, tuple):
+        _rows(f, "f")
     if io_dtype is None:
         io_dtype = d_h.dtype if isinstance(d_h, torch.Tensor) else None if isinstance(f, tuple) else f.dtype
         if io_dtype is None:

@@ -136,6 +136,12 @@ def test_norm_bwd_refusals(over, what):
         api.block_norm_bwd(a.pop("f"), a.pop("w_post"), a.pop("d_x"), **a)
 
 
+@pytest.mark.parametrize("f", [None, [1.0], "f"])
+def test_norm_bwd_refuses_what_is_no_tensor(f):
+    with pytest.raises(ValueError, match="f must be a tensor"):
+        api.block_norm_bwd(f, torch.ones(C), torch.zeros(R, C, dtype=BF))
+
+
 def test_act_refusals():
     x = torch.zeros(R, C)
     codes = x.to(torch.float8_e4m3fn)
