@@ -199,3 +199,22 @@ def test_non_finite_values_stay_in_their_reach(lens, dtype, name):
             hit[n, heads] = True
         assert torch.equal(got[4][~hit], clean[4][~hit]), ("d_initial_state", name, t, x)
         assert not all(torch.isfinite(y).all() for y in got)
+
+
+def test_backward_offsets_past_32_bits():
+    """A long prompt ahead: rows whose byte and element offsets pass 2^32 and 2^31, also in the partial sums of dq and
+    dk over two value tiles and in the stored states, come out as alone."""
+    H, Hk, dk, dv, T, n = 16, 16, 64, 256, 540_000, 100
+    q, k = (torch.empty(T, Hk, dk, dtype=BF, device="cuda").normal_() / 8 for _ in range(2))
+    v, do = (torch.empty(T, H, dv, dtype=BF, device="cuda").normal_() for _ in range(2))
+    g = -0.1 * torch.rand(T, H, device="cuda")
+    got = api.lin_attn_bwd(q, k, v, g, torch.tensor([0, T - n, T], dtype=torch.int32, device="cuda"), do,
+                           check_status=True)
+    a = [x[T - n:].cpu() for x in (q, k, v, g)]
+    args = (*a, [0, n], None, do[T - n:].cpu(), None)
+    want, mag = ref.lin(*args), ref.lin_abs(*args)
+    for i, name in enumerate(("dq bf16", "dk bf16", "dv bf16")):
+        close(got[i][T - n:], want[i], mag[i], name)
+    close(got[4][1:], want[4], mag[4], "d_initial_state fp32")
+    err = (got[3][T - n:].double().cpu() - want[3]).abs()
+    assert not (err > 2.0 ** -16 * chunk_largest(mag[3], [0, n]) + 2.0 ** -24 * want[3].abs()).any()
