@@ -59,16 +59,17 @@
 //
 // A wave's waits decide as much as its work: the compiler's own waits count
 // only its own loads and so drain the asked rows too.  Inside the walk there
-// are none between asking and using: the state is waited for before it, gates
-// and DQ's rows of E before the rows are asked for, and a chunk's output stores
-// stay in flight over its end (train batch 399 -> 371 us).
+// are none between asking and using: the state is waited for before it, gates,
+// DQ's rows of E and DK's stored states before the rows are asked for, and a
+// chunk's stores stay in flight over its end (28 us of a training batch's 399).
 //
 // Measured (MI355X, bf16, 16 heads of 128 x 128, cold to warm): 32768 tokens in
 // one sequence, state pass 62 to 68 us (268 MB; 62 with its products taken out),
 // output pass 133 to 150 (537 MB; 105 to 116 without products, 131 with every
 // load a cache hit; vector, matrix and LDS units are each busy 40 to 50% of the
-// time).  Backward of 4 x 4096 tokens: state passes 70 to 81, dq 97 to 123, dk
-// and dv 179 to 218.
+// time).  Backward of 4 x 4096 tokens: state passes 66 to 80, dq 123 to 141,
+// dk and dv 189 to 236, of which about 20 and 15 the state of every chunk
+// takes, stored (268 MB) and read.
 #pragma once
 
 #include <type_traits>
@@ -453,14 +454,15 @@ struct LinWalk {
       }
     }
   }
-  // DQ: the state after chunk c, which is not the segment's last, for DK
+  // DQ: the state after chunk c, which is not the segment's last, for DK.  Past
+  // the caches both ways, which the rows fill (415 us for 424 at 128 x 192).
   __device__ __forceinline__ f32x4* dumped(int c) const {
     return reinterpret_cast<f32x4*>(A.dump) + (L.dump0 + c * (int64_t)A.VH) * (CK * CV / 4) + 64 * w + l64;
   }
   __device__ __forceinline__ void store_dump(int c) const {
     f32x4* d = dumped(c);
 #pragma unroll
-    for (int tr = 0; tr < RT; ++tr) d[tr * NT] = X[tr];
+    for (int tr = 0; tr < RT; ++tr) __builtin_nontemporal_store(X[tr], d + tr * NT);
   }
   // A value for each token and head: a chunk's first, and this lane's from there
   // (formed where it is used, not kept through the walk).
@@ -483,7 +485,7 @@ struct LinWalk {
       const f32x4* d = dumped(c - 1);
       f32x4 s[RT];
 #pragma unroll
-      for (int tr = 0; tr < RT; ++tr) s[tr] = d[tr * NT];
+      for (int tr = 0; tr < RT; ++tr) s[tr] = __builtin_nontemporal_load(d + tr * NT);
       __builtin_amdgcn_sched_barrier(0);     // all on the way before the first is waited for
 #pragma unroll
       for (int tr = 0; tr < RT; ++tr)
