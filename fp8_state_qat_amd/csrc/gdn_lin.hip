@@ -135,7 +135,11 @@ int lin_tile(int dv) { return dv % 128 == 0 ? 128 : 64; }
 // scan's workgroups fit a compute unit twice, with fp32 tiles of 128 key
 // channels once (8 heads of 128 x 128, 6000 fp32 tokens: 106 us forward and
 // 328 backward with 256 units, 119 and 374 with 512; 16 bf16 heads, 32k
-// tokens: 239 with 256, 231 with 512).
+// tokens: 239 with 256, 231 with 512).  In the backward the dq and state
+// passes fit twice and the reverse passes, but for bf16 heads of 64 x 64, once:
+// with 256 units and 512, 8 ragged bf16 heads of 64 x 128 take 102 and 99 us, 16
+// of 64 x 64 193 and 180, 8 of 128 x 192 508 and 426, but 16 of 128 x 128 400
+// and 421, and 8 fp32 heads of 64 x 128 183 and 198.
 int64_t lin_units(const gdn_lin_t& s) { return s.io_dtype == GDN_F32 && s.dk == 128 ? 256 : 512; }
 // Forward calls of up to four chunks stay whole: one kernel instead of three
 // (130 tokens 12 us instead of 16.5, 192: 16.5 and 20, 256: 20 either way).

@@ -69,7 +69,7 @@
 // load a cache hit; vector, matrix and LDS units are each busy 40 to 50% of the
 // time).  Backward of 4 x 4096 tokens: state passes 66 to 80, dq 123 to 141,
 // dk and dv 189 to 236, of which about 20 and 15 the state of every chunk
-// takes, stored (268 MB) and read.
+// takes, stored (235 MB) and read.
 #pragma once
 
 #include <type_traits>

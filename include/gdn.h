@@ -371,7 +371,12 @@ size_t gdn_chunk_bwd_workspace_bytes(const gdn_shape_t* shape);
  * An infinity or a NaN in q, k, v or g reaches the outputs and the state that
  * the recurrence lets it reach, as a NaN, and no earlier token; in the
  * backward it can reach the gradients of all tokens of its 64-token chunk.
- * No other sequence is touched.
+ * No other sequence is touched, but for the sum over all tokens that dg of a
+ * fixed decay is.
+ *
+ * fp32 results are off by about 2^-19 of the sum of their terms' magnitudes at
+ * most, dg by 2^-16 of the largest such sum in the token's chunk and head (its
+ * terms that do not lie across the token cancel).  dg is exactly 0 where e^g is.
  */
 typedef struct {
     int32_t n_seqs;            /* N >= 1 */
@@ -411,7 +416,8 @@ size_t gdn_lin_attn_fwd_workspace_bytes(const gdn_lin_t* shape);
  *                  heads that share a query/key head);  d_v as v
  *   dg             fp32, shape of g (summed over all tokens for [H])
  *   d_initial_state  a state (written also without an initial state)
- * cu_seqlens and the workspace as for gdn_lin_attn_fwd.
+ * cu_seqlens and the workspace as for gdn_lin_attn_fwd; the workspace holds
+ * the state entering every 64-token chunk, 4 dk dv bytes for each and head.
  */
 gdn_status_t gdn_lin_attn_bwd(const gdn_lin_t* shape, const void* q, const void* k, const void* v,
                               const float* g, const int32_t* cu_seqlens, const void* d_o,
