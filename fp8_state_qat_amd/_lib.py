@@ -34,6 +34,7 @@ NOALLOC_SCRATCH_BYTES = 64 << 20   # GDN_NOALLOC_SCRATCH_BYTES
 EXPORTS = ("gdn_chunk_fwd", "gdn_chunk_fwd_noalloc", "gdn_chunk_fwd_workspace_bytes", "gdn_workspace_status",
            "gdn_state_qdq",
            "gdn_state_qdq_int8", "gdn_decode_step", "gdn_chunk_bwd_dh", "gdn_chunk_bwd_workspace_bytes",
+           "gdn_chunk_grad", "gdn_chunk_grad_workspace_bytes",
            "gdn_lin_attn_fwd", "gdn_lin_attn_fwd_workspace_bytes", "gdn_lin_attn_bwd",
            "gdn_lin_attn_bwd_workspace_bytes", "gdn_lin_attn_step", "gdn_block_norm_fwd", "gdn_block_norm_bwd",
            "gdn_block_norm_bwd_workspace_bytes", "gdn_act_pack", "gdn_act_unpack",
@@ -136,6 +137,11 @@ def lib():
     L.gdn_chunk_bwd_dh.restype = ctypes.c_int
     L.gdn_chunk_bwd_workspace_bytes.argtypes = [ctypes.POINTER(GdnShape)]
     L.gdn_chunk_bwd_workspace_bytes.restype = ctypes.c_size_t
+    L.gdn_chunk_grad.argtypes = ([ctypes.POINTER(GdnShape)] + [_vp] * 9 + [ctypes.c_int64] + [_vp] * 9 +
+                                       [ctypes.c_size_t, _vp])
+    L.gdn_chunk_grad.restype = ctypes.c_int
+    L.gdn_chunk_grad_workspace_bytes.argtypes = [ctypes.POINTER(GdnShape), ctypes.c_int32]
+    L.gdn_chunk_grad_workspace_bytes.restype = ctypes.c_size_t
     L.gdn_state_qdq_int8.argtypes = [_vp, _vp, _vp, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _vp]
     L.gdn_state_qdq_int8.restype = ctypes.c_int
     L.gdn_decode_step.argtypes = [ctypes.POINTER(GdnShape), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,

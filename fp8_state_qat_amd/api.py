@@ -558,6 +558,81 @@ def lin_attn_step(q, k, v, g, state, *, o=None):
     return o
 
 
+# ---------------------------------------------------------------------------
+# All gradients of the chunked gated delta rule
+# ---------------------------------------------------------------------------
+def _grad_shape(N, H, dk, dv, T, io_dtype, qdq_flags):
+    return GdnShape(N, H, dk, dv, T, _DT[io_dtype], _DT[io_dtype], 0, int(qdq_flags), 0)
+
+
+def chunk_grad_workspace_bytes(N, H, dk, dv, T, io_dtype=torch.bfloat16, qdq_flags=0, states_given=False):
+    """Device workspace chunk_grad needs for this shape (bytes)."""
+    shape = _grad_shape(N, H, dk, dv, T, io_dtype, qdq_flags)
+    n = _lib.lib().gdn_chunk_grad_workspace_bytes(ctypes.byref(shape), 1 if states_given else 0)
+    if n == 0:
+        _refuse()
+    return n
+
+
+def chunk_grad(q, k, v, beta, g, cu_seqlens, d_o, *, seq_lens=None, initial_state=None, states=None,
+               d_final_state=None, qdq_flags=0, dq=None, dk=None, d_v=None, d_beta=None, dg=None,
+               d_initial_state=None, workspace=None, check_status=False):
+    """gdn_chunk_grad: every gradient of chunk_fwd over whole sequences for
+    L = sum o . d_o + <S_final, d_final_state>, identity straight-through at
+    the state's QDQ.  q, k: [T, H, dk]; v, d_o: [T, H, dv] (fp32 or bf16); beta,
+    g: [T, H] fp32; cu_seqlens, seq_lens, initial_state: as for chunk_fwd;
+    qdq_flags: the forward's (chunk_fwd's default is GDN_QDQ_CHUNK |
+    GDN_QDQ_WRITE).  states: the states after every chunk as the forward's
+    debug record bound_post has them ([n_bounds, H, dv, dk] fp32); None: they are
+    computed again.  check_status: read the workspace's status word after the
+    call (synchronizes; raises GdnError when the index arrays are out of
+    contract).
+    Returns (dq, dk, dv, dbeta, dg, d_initial_state): dq, dk, dv in the inputs'
+    dtype, the others fp32; rows of a segment past its length are 0."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError(f"k must be [T, H, dk], got {_what(k)}")
+    T, H, dk_ = k.shape
+    if k.dtype not in _DT:
+        raise ValueError("q, k, v must share one dtype: float32 or bfloat16")
+    if not isinstance(v, torch.Tensor) or v.dim() != 3 or v.shape[:2] != (T, H):
+        raise ValueError(f"v must be [{T}, {H}, dv], got {_what(v)}")
+    dv_ = v.shape[2]
+    N = _lin_seqs(cu_seqlens)
+    for name, t in (("q", q), ("beta", beta), ("g", g), ("d_o", d_o)):
+        if t is None:
+            raise ValueError(f"{name} is required")
+    f32, th, st = torch.float32, (T, H), (N, H, dv_, dk_)
+    if states is not None and (not isinstance(states, torch.Tensor) or states.dim() != 4 or
+                               states.shape[1:] != (H, dv_, dk_)):
+        raise ValueError(f"states must be [n_bounds, {H}, {dv_}, {dk_}], got {_what(states)}")
+    outs = [dq, dk, d_v, d_beta, dg, d_initial_state]
+    at = _args(("q", q, k.dtype, k.shape), ("k", k, None, None), ("v", v, k.dtype, None), ("beta", beta, f32, th),
+               ("g", g, f32, th), ("cu_seqlens", cu_seqlens, torch.int32, None),
+               ("seq_lens", seq_lens, torch.int32, (N,)), ("initial_state", initial_state, f32, st),
+               ("states", states, f32, None), ("d_o", d_o, k.dtype, v.shape),
+               ("d_final_state", d_final_state, f32, st), ("dq", dq, k.dtype, k.shape), ("dk", dk, k.dtype, k.shape),
+               ("d_v", d_v, k.dtype, v.shape), ("d_beta", d_beta, f32, th), ("dg", dg, f32, th),
+               ("d_initial_state", d_initial_state, f32, st))
+    for i, like in enumerate((q, k, v, beta, g)):
+        if outs[i] is None:
+            outs[i] = torch.empty_like(like)
+            at[11 + i] = outs[i].data_ptr()
+    if d_initial_state is None:
+        outs[5] = v.new_empty(st, dtype=f32)
+        at[16] = outs[5].data_ptr()
+    shape = ctypes.byref(_grad_shape(N, H, dk_, dv_, T, k.dtype, qdq_flags))
+    L = _lib.lib()
+    need = L.gdn_chunk_grad_workspace_bytes(shape, 0 if states is None else 1)
+    ws, ws_bytes, workspace = _scratch(workspace, need, k)
+    if states is not None and at[8] == 0:   # no entries, and so no memory: still given
+        at[8] = ws
+    at.insert(9, 0 if states is None else states.shape[0])
+    _lib.check(L.gdn_chunk_grad(shape, *at, ws, ws_bytes, _stream_at()))
+    if check_status:
+        workspace_status(workspace)
+    return tuple(outs)
+
+
 _ACT = {"silu": _lib.GDN_ACT_SILU, "sigmoid": _lib.GDN_ACT_SIGMOID}
 
 

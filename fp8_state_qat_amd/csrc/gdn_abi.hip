@@ -339,6 +339,74 @@ gdn_status_t gdn_chunk_bwd_dh(const gdn_shape_t* shape, const void* q, const voi
 
 namespace {
 
+gdn_status_t check_workspace(const void* workspace, size_t bytes, size_t need, uintptr_t align) {
+  if (workspace == nullptr || bytes < need)
+    return fail(GDN_ERR_INVALID_ARG, "workspace needs %zu bytes (got %zu%s)", need, bytes, workspace ? "" : ", NULL");
+  if (!aligned(workspace, align))
+    return fail(GDN_ERR_INVALID_ARG, "workspace must be %d-byte aligned", (int)align);
+  return GDN_OK;
+}
+
+gdn_status_t check_grad(const gdn_shape_t* s) {
+  gdn_status_t st = check_shape(s, false);
+  if (st != GDN_OK) return st;
+  if (s->gate_per_channel)
+    return fail(GDN_ERR_UNSUPPORTED, "gdn_chunk_grad takes one gate a head (gate_per_channel 0)");
+  if (s->qdq_flags & GDN_QDQ_W)
+    return fail(GDN_ERR_UNSUPPORTED, "gdn_chunk_grad of a forward with W QDQ is not built");
+  if (s->qdq_flags & GDN_QDQ_INT8) return fail(GDN_ERR_UNSUPPORTED, "GDN_QDQ_INT8 is a decode-step codec");
+  if (s->gate_grid_log2 != 0)
+    return fail(GDN_ERR_INVALID_ARG, "gdn_chunk_grad covers fully chunked sequences, which have no "
+                "recurrent writes: gate_grid_log2 must be 0");
+  if (s->total_tokens >= (int64_t)1 << 31) return fail(GDN_ERR_UNSUPPORTED, "total_tokens must be below 2^31");
+  if (!gdn::grad_fits(*s)) return fail(GDN_ERR_UNSUPPORTED, "a launch would pass 2^32 threads");
+  return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gdn_chunk_grad_workspace_bytes(const gdn_shape_t* shape, int32_t states_given) {
+  g_err[0] = 0;
+  return check_grad(shape) == GDN_OK ? gdn::grad_workspace_bytes(*shape, states_given != 0) : 0;
+}
+
+gdn_status_t gdn_chunk_grad(const gdn_shape_t* shape, const void* q, const void* k, const void* v, const float* beta,
+                            const float* g, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                            const float* initial_state, const float* states, int64_t n_states,
+                            const void* d_o, const float* d_final_state, void* dq, void* dk, void* d_v, float* d_beta, float* dg,
+                            float* d_initial_state, void* workspace, size_t workspace_bytes, void* stream) {
+  g_err[0] = 0;
+  gdn_status_t st = check_grad(shape);
+  if (st != GDN_OK) return st;
+  if (!cu_seqlens || !d_initial_state)
+    return fail(GDN_ERR_INVALID_ARG, "cu_seqlens and d_initial_state must be non-NULL");
+  if (shape->total_tokens > 0 &&
+      (!q || !k || !v || !beta || !g || !d_o || !dq || !dk || !d_v || !d_beta || !dg))
+    return fail(GDN_ERR_INVALID_ARG, "q, k, v, beta, g, d_o, dq, dk, d_v, d_beta and dg must be non-NULL");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(d_o, 16) || !aligned(dq, 16) ||
+      !aligned(dk, 16) || !aligned(d_v, 16) || !aligned(initial_state, 16) || !aligned(states, 16) ||
+      !aligned(d_final_state, 16) || !aligned(d_initial_state, 16) || !aligned(beta, 4) || !aligned(g, 4) ||
+      !aligned(d_beta, 4) || !aligned(dg, 4) || !aligned(cu_seqlens, 4) || !aligned(seq_lens, 4))
+    return fail(GDN_ERR_INVALID_ARG, "misaligned buffer (q, k, v, d_o, their gradients and states need 16 bytes)");
+  if (d_initial_state == initial_state || d_initial_state == d_final_state)
+    return fail(GDN_ERR_INVALID_ARG, "d_initial_state may not alias initial_state or d_final_state");
+  if (states != nullptr && n_states < 0) return fail(GDN_ERR_INVALID_ARG, "n_states must be >= 0");
+  st = check_workspace(workspace, workspace_bytes, gdn::grad_workspace_bytes(*shape, states != nullptr), 256);
+  if (st == GDN_OK) st = check_device();
+  if (st != GDN_OK) return st;
+  hipError_t e = gdn::launch_chunk_grad(*shape, q, k, v, beta, g, cu_seqlens, seq_lens, initial_state, states,
+                                        n_states, d_o, d_final_state, dq, dk, d_v, d_beta, dg, d_initial_state, workspace,
+                                        (hipStream_t)stream);
+  if (e != hipSuccess) return fail(GDN_ERR_DEVICE, "launch failed: %s", hipGetErrorString(e));
+  return GDN_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
 enum LinCall { kLinFwd, kLinBwd, kLinStep };
 
 gdn_status_t check_lin(const gdn_lin_t* s, LinCall call) {
@@ -371,14 +439,6 @@ gdn_status_t check_lin(const gdn_lin_t* s, LinCall call) {
   if (units >= (int64_t)1 << 31) return fail(GDN_ERR_UNSUPPORTED, "too many (segment, head, tile) units");
   if (step ? !gdn::lin_step_fits(*s) : !gdn::lin_fits(*s, call == kLinBwd))
     return fail(GDN_ERR_UNSUPPORTED, "a launch would pass 2^32 threads (n_seqs * n_heads * dv too large)");
-  return GDN_OK;
-}
-
-gdn_status_t check_workspace(const void* workspace, size_t bytes, size_t need, uintptr_t align) {
-  if (workspace == nullptr || bytes < need)
-    return fail(GDN_ERR_INVALID_ARG, "workspace needs %zu bytes (got %zu%s)", need, bytes, workspace ? "" : ", NULL");
-  if (!aligned(workspace, align))
-    return fail(GDN_ERR_INVALID_ARG, "workspace must be %d-byte aligned", (int)align);
   return GDN_OK;
 }
 

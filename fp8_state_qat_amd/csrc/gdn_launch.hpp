@@ -109,6 +109,16 @@ hipError_t launch_chunk_bwd_dh(const gdn_shape_t& s, const void* q, const void* 
                                const void* dout, const float* dfin, float* dh, float* dinit, float* dvals,
                                void* workspace, hipStream_t stream);
 
+// All gradients of the chunked forward (gdn_grad.hip).  Every launch of the
+// call stays below 2^32 threads where grad_fits.
+bool grad_fits(const gdn_shape_t& s);
+size_t grad_workspace_bytes(const gdn_shape_t& s, bool given);
+hipError_t launch_chunk_grad(const gdn_shape_t& s, const void* q, const void* k, const void* v, const float* beta,
+                             const float* g, const int32_t* cu_seqlens, const int32_t* seq_lens,
+                             const float* initial_state, const float* states, int64_t n_states, const void* d_o,
+                             const float* d_final_state, void* dq, void* dk, void* d_v, float* d_beta, float* dg,
+                             float* d_initial_state, void* workspace, hipStream_t stream);
+
 // Linear attention (gdn_lin_step.hip, gdn_lin.hip).
 hipError_t launch_lin_step(const gdn_lin_t& s, const void* q, const void* k, const void* v, const float* g,
                            float* state, void* o, hipStream_t stream);

@@ -353,6 +353,57 @@ gdn_status_t gdn_chunk_bwd_dh(const gdn_shape_t* shape,
 size_t gdn_chunk_bwd_workspace_bytes(const gdn_shape_t* shape);
 
 /*
+ * gdn_chunk_grad -- every gradient of the chunked forward over whole sequences
+ * (no prefix/suffix split), scalar gate, with identity straight-through
+ * gradients through the state's QDQ (#2497 "What does this PR do?"):
+ * L = sum_t o_t . d_o_t + <S_L, d_final_state> of each sequence, where a chunk
+ * starts from the state that the forward had at its boundary (after QDQ).
+ *   shape      as for gdn_chunk_fwd: fp32 or bf16 q, k, v (o_dtype is not used),
+ *              gate_per_channel 0, gate_grid_log2 0.  qdq_flags are those of the
+ *              forward (GDN_QDQ_WRITE changes no gradient: it touches the last
+ *              state only); GDN_QDQ_W and GDN_QDQ_INT8 are refused.
+ *   q, k, v, beta, g, cu_seqlens, seq_lens, initial_state   the forward's
+ *   states     the states after every chunk, after their QDQ, as the forward's
+ *              debug->bound_post has them ([n_bounds, H, dv, dk] fp32, chunk i of
+ *              sequence n at b = sum_{m<n} ceil(L_m / 64) + i); the last one of a
+ *              sequence is not read.  NULL: they are computed again (with
+ *              GDN_QDQ_CHUNK by the forward's own code, bit for bit its states).
+ *   n_states   entries of states (read only with states): fewer than the
+ *              sequences have chunks is found on the device like index arrays
+ *              out of contract
+ *   d_o        [total_tokens, H, dv] io_dtype
+ *   d_final_state  [N, H, dv, dk] fp32 or NULL (zero)
+ *   dq, dk, d_v    as q, k, v;  d_beta, dg  [total_tokens, H] fp32
+ *   d_initial_state  [N, H, dv, dk] fp32, written also without an initial
+ *              state; may not alias initial_state or d_final_state
+ *   workspace  gdn_chunk_grad_workspace_bytes(shape, states != NULL) bytes,
+ *              256-byte aligned; holds the call's status word on return
+ *              (gdn_workspace_status; index arrays out of contract: nothing is
+ *              written)
+ * Rows of a segment past L_n get zero gradients (what the inputs hold there is
+ * not read); rows outside every segment are not written.  dg is exactly 0 where
+ * e^g is.  Outputs may not overlap inputs.
+ *
+ * dq, dk, d_v and d_initial_state take terms of 16 or more significant bits
+ * (fp32 inputs: 24); d_beta and dg are sums of terms that can cancel, off by
+ * about 2^-16 (fp32 inputs: 2^-21) of the sum of their terms' magnitudes in the
+ * chunk at most.
+ */
+gdn_status_t gdn_chunk_grad(const gdn_shape_t* shape,
+                            const void* q, const void* k, const void* v,
+                            const float* beta, const float* g,
+                            const int32_t* cu_seqlens, const int32_t* seq_lens,
+                            const float* initial_state, const float* states, int64_t n_states,
+                            const void* d_o, const float* d_final_state,
+                            void* dq, void* dk, void* d_v, float* d_beta, float* dg,
+                            float* d_initial_state,
+                            void* workspace, size_t workspace_bytes, void* stream);
+/* Workspace bytes of gdn_chunk_grad: for each 64 tokens and head a record of
+ * 27 KiB and 4 dk dv bytes, twice that without given states; 0 for an invalid
+ * shape. */
+size_t gdn_chunk_grad_workspace_bytes(const gdn_shape_t* shape, int32_t states_given);
+
+/*
  * Linear attention with a decay for each head:
  *   S_t = e^{g_t} S_{t-1} + v_t k_t^T,   o_t = S_t q_t      (S: dv x dk, fp32)
  * over packed sequences, its gradients, and its single-token form.

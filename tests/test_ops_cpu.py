@@ -285,3 +285,108 @@ def test_act_rejects_null_and_misaligned():
         assert call(x=0) == 1 and call(x=FAKE + 1) == 1 and call(c=0) == 1 and call(s=FAKE + 2) == 1
         assert call(d=5) == 1 and call(rows=-1) == 1 and call(cols=0) == 1
         assert call(rows=1 << 31) == 2
+
+
+# ---------------------------------------------------------------- gradients of the gated delta rule
+def test_grad_reference_against_differences():
+    """Central differences of the 64-bit recurrence, a state replaced at a boundary held fixed: error h^2 f''' / 6 +
+    2^-53 |L| / h ~ 1e-9 at h = 1e-5."""
+    import grad_ref
+    gen = torch.Generator().manual_seed(0)
+
+    def rn(*s):
+        return torch.randn(*s, generator=gen).double()
+
+    L, H, dk, dv, cu, lens = 9, 2, 3, 4, [0, 0, 6, 9], [0, 5, 3]
+    a = [rn(L, H, dk), rn(L, H, dk), rn(L, H, dv), torch.sigmoid(rn(L, H)), -rn(L, H).abs()]
+    S0, do, dS = rn(3, H, dv, dk), rn(L, H, dv), rn(3, H, dv, dk)
+
+    def loss(q, k, v, b, g, S):
+        total = 0.0
+        for n in range(3):
+            r = slice(cu[n], cu[n] + lens[n])
+            o, _, S1 = grad_ref.forward(q[r], k[r], v[r], b[r], g[r], S[n])
+            total += float((o * do[r]).sum() + (S1 * dS[n]).sum())
+        return total
+
+    a.append(S0)
+    grads = grad_ref.grad(*a[:5], cu, do, lens, S0, dS)
+    for i, got in enumerate(grads):
+        flat = a[i].reshape(-1)
+        for j in range(0, flat.numel(), max(1, flat.numel() // 7)):
+            keep, h = float(flat[j]), 1e-5
+            flat[j] = keep + h
+            up = loss(*a)
+            flat[j] = keep - h
+            down = loss(*a)
+            flat[j] = keep
+            assert abs((up - down) / (2 * h) - float(got.reshape(-1)[j])) < 1e-7
+
+
+def _grad(**over):
+    a = dict(q=torch.zeros(T, H, DK, dtype=BF), k=torch.zeros(T, H, DK, dtype=BF), v=torch.zeros(T, H, DV, dtype=BF),
+             beta=torch.zeros(T, H), g=torch.zeros(T, H), cu=torch.tensor([0, 5, T], dtype=torch.int32),
+             d_o=torch.zeros(T, H, DV, dtype=BF))
+    a.update({k: over.pop(k) for k in list(over) if k in a})
+    return tuple(a.values()), over
+
+
+@pytest.mark.parametrize("over,what", [
+    (dict(q=None), "q is required"), (dict(q=torch.zeros(T, H, DK)), "q must be"), (dict(k=None), "k must be"),
+    (dict(k=torch.zeros(T, H, DK, dtype=torch.float16)), "dtype"), (dict(v=torch.zeros(T, H + 1, DV, dtype=BF)), "v"),
+    (dict(v=torch.zeros(T, H, DV)), "v must be"), (dict(beta=torch.zeros(T, H + 1)), "beta"),
+    (dict(g=torch.zeros(T, H, DK)), "g must"), (dict(d_o=None), "d_o"), (dict(d_o=torch.zeros(T, H, DV)), "d_o"),
+    (dict(cu=torch.tensor([0, 5, T])), "cu_seqlens"), (dict(seq_lens=torch.zeros(N + 1, dtype=torch.int32)), "seq_lens"),
+    (dict(initial_state=torch.zeros(N, H, DK, DV)), "initial_state"),
+    (dict(states=torch.zeros(3, H, DK, DV)), "states"), (dict(states=torch.zeros(3, H, DV, DK, dtype=BF)), "states"),
+    (dict(d_final_state=torch.zeros(N, H, DV)), "d_final_state"), (dict(dq=torch.zeros(T, H, DK)), "dq"),
+    (dict(dk=torch.zeros(T, H, DV, dtype=BF)), "dk"), (dict(d_v=torch.zeros(T, H, DV)), "d_v"),
+    (dict(d_beta=torch.zeros(T, H, dtype=BF)), "d_beta"), (dict(dg=torch.zeros(T)), "dg"),
+    (dict(d_initial_state=torch.zeros(N, H, DV, DK, dtype=BF)), "d_initial_state"),
+    (dict(q=torch.zeros(H, T, DK, dtype=BF).transpose(0, 1)), "contiguous"), ({}, "device tensor"),
+])
+def test_grad_refusals(over, what):
+    a, kw = _grad(**over)
+    with pytest.raises(ValueError, match=what):
+        api.chunk_grad(*a, **kw)
+
+
+def _grad_call(shape, ptr=FAKE, ws=FAKE * 16, ws_bytes=1 << 50, n_states=0, **over):
+    names = ("q", "k", "v", "beta", "g", "cu", "lens", "init", "states", "d_o", "d_fin", "dq", "dk", "d_v", "d_beta",
+             "dg", "d_init")
+    at = {n: ptr + 4096 * i for i, n in enumerate(names)}
+    at.update(over)
+    p = [P(at[n]) if at[n] else None for n in names]
+    return _lib.lib().gdn_chunk_grad(ctypes.byref(shape), *p[:9], n_states, *p[9:], P(ws) if ws else None, ws_bytes, None)
+
+
+def _grad_shape(**over):
+    a = dict(n_seqs=2, n_heads=4, dk=64, dv=64, total_tokens=100, io_dtype=1, o_dtype=1, gate_per_channel=0, qdq_flags=0,
+             gate_grid_log2=0)
+    a.update(over)
+    return _lib.GdnShape(**a)
+
+
+@pytest.mark.parametrize("shape,call,status,text", [
+    (dict(gate_per_channel=1), {}, 2, "one gate a head"), (dict(qdq_flags=4), {}, 2, "W QDQ"),
+    (dict(qdq_flags=8), {}, 2, "decode-step"), (dict(gate_grid_log2=3), {}, 1, "gate_grid_log2"),
+    (dict(dk=96), {}, 2, "dk"), (dict(dv=320), {}, 2, "dv"), (dict(n_seqs=0), {}, 1, "n_seqs"),
+    (dict(total_tokens=1 << 31), {}, 2, "total_tokens"), (dict(total_tokens=(1 << 31) - 1, n_heads=64), {}, 2, "threads"),
+    (dict(n_seqs=1 << 20, n_heads=16), {}, 2, "threads"),
+    ({}, dict(q=0), 1, "non-NULL"), ({}, dict(cu=0), 1, "non-NULL"), ({}, dict(d_init=0), 1, "non-NULL"),
+    ({}, dict(dg=0), 1, "non-NULL"), ({}, dict(k=FAKE + 8), 1, "misaligned"), ({}, dict(states=FAKE + 4), 1, "misaligned"),
+    ({}, dict(d_init=FAKE + 4096 * 7), 1, "alias"), ({}, dict(d_init=FAKE + 4096 * 10), 1, "alias"),
+    ({}, dict(n_states=-1), 1, "n_states"), ({}, dict(ws_bytes=1000), 1, "workspace needs"),
+    ({}, dict(ws=FAKE * 16 + 64), 1, "256-byte"), ({}, dict(ws=0), 1, "workspace needs"),
+])
+def test_grad_abi_refusals(shape, call, status, text):
+    assert _grad_call(_grad_shape(**shape), **call) == status
+    assert text in _lib.last_error()
+
+
+def test_grad_workspace_sizes():
+    L = _lib.lib()
+    sizes = [L.gdn_chunk_grad_workspace_bytes(ctypes.byref(_grad_shape(qdq_flags=f)), given)
+             for f, given in ((0, 1), (0, 0), (1, 1), (1, 0))]
+    assert 0 < sizes[0] == sizes[2] < sizes[1] < sizes[3]
+    assert L.gdn_chunk_grad_workspace_bytes(ctypes.byref(_grad_shape(dk=32)), 0) == 0
