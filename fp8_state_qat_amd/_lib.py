@@ -38,6 +38,7 @@ EXPORTS = ("gdn_chunk_fwd", "gdn_chunk_fwd_noalloc", "gdn_chunk_fwd_workspace_by
            "gdn_lin_attn_fwd", "gdn_lin_attn_fwd_workspace_bytes", "gdn_lin_attn_bwd",
            "gdn_lin_attn_bwd_workspace_bytes", "gdn_lin_attn_step", "gdn_block_norm_fwd", "gdn_block_norm_bwd",
            "gdn_block_norm_bwd_workspace_bytes", "gdn_act_pack", "gdn_act_unpack",
+           "gdn_distill_fwd", "gdn_distill_bwd", "gdn_distill_fwd_bwd",
            "gdn_status_string", "gdn_last_error")
 
 
@@ -103,6 +104,21 @@ class GdnNorm(ctypes.Structure):
     ]
 
 
+class GdnDistill(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("vocab", ctypes.c_int32),
+        ("topk", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("temperature", ctypes.c_float),
+        ("kd_weight", ctypes.c_float),
+        ("ce_weight", ctypes.c_float),
+        ("ignore_index", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("d_row_stride", ctypes.c_int64),
+    ]
+
+
 class GdnError(RuntimeError):
     def __init__(self, status: int, detail: str):
         self.status = status
@@ -163,6 +179,10 @@ def lib():
     for name, p in (("lin_attn_fwd", lin), ("lin_attn_bwd", lin), ("block_norm_bwd", norm)):
         f = getattr(L, f"gdn_{name}_workspace_bytes")
         f.argtypes, f.restype = [p], size
+    dis = ctypes.POINTER(GdnDistill)
+    for name, n in (("distill_fwd", 8), ("distill_bwd", 9), ("distill_fwd_bwd", 9)):
+        f = getattr(L, "gdn_" + name)
+        f.argtypes, f.restype = [dis] + [_vp] * n, ctypes.c_int
     L.gdn_status_string.argtypes = [ctypes.c_int]
     L.gdn_status_string.restype = ctypes.c_char_p
     L.gdn_last_error.argtypes = []

@@ -14,7 +14,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import GDN_BF16, GDN_F32, GDN_QDQ_CHUNK, GDN_QDQ_WRITE, GdnDebug, GdnLin, GdnNorm, GdnShape
+from ._lib import GDN_BF16, GDN_F32, GDN_QDQ_CHUNK, GDN_QDQ_WRITE, GdnDebug, GdnDistill, GdnLin, GdnNorm, GdnShape
 
 _DT = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
 
@@ -779,3 +779,102 @@ def act_unpack(codes, scales, *, dtype=torch.bfloat16):
     x = torch.empty_like(codes, dtype=dtype)
     _lib.check(_lib.lib().gdn_act_unpack(*at, x.data_ptr(), _DT[dtype], rows, cols, _stream_at()))
     return x
+
+
+# ---------------------------------------------------------------------------
+# Distillation from a teacher's top logits
+# ---------------------------------------------------------------------------
+def _matrix(t, name):
+    """Rows, columns and row stride of a matrix whose rows are contiguous (a
+    slice of a wider one will do)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[1] < 1:
+        raise ValueError(f"{name} must be a tensor [rows, vocab] with vocab >= 1, got {_what(t)}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    stride = t.stride(0) if rows > 1 else cols
+    if stride < cols:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    if cols >= 1 << 31:    # the library's 32-bit vocab would wrap
+        raise ValueError(f"{name} must have fewer than 2^31 columns, got {cols}")
+    return rows, cols, stride
+
+
+def _distill_args(logits, ids, top, teacher_lse, targets, temperature, kd_weight, ce_weight, ignore_index, out, *more):
+    """Checked shape, the addresses of ids, top, teacher_lse, targets and of
+    `more`, and the gradient's tensor (out, or one like the logits)."""
+    R, V, stride = _matrix(logits, "logits")
+    if logits.dtype not in _DT:
+        raise ValueError("logits must be float32 or bfloat16")
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or ids.shape[0] != R:
+        raise ValueError(f"ids must be [{R}, topk], got {_what(ids)}")
+    K = ids.shape[1]
+    if K >= 1 << 31:
+        raise ValueError(f"ids must have fewer than 2^31 columns, got {K}")
+    if top is None:
+        raise ValueError("top is required")
+    specs = [("ids", ids, torch.int32, None), ("top", top, torch.float32, (R, K)),
+             ("teacher_lse", teacher_lse, torch.float32, (R,)), ("targets", targets, torch.int64, (R,)), *more]
+    d_stride = 0
+    if out is not None:
+        if out is True:
+            out, d_stride = logits.new_empty(R, V), V
+        else:
+            d_stride = _matrix(out, "out")[2]
+            if out.dtype != logits.dtype or out.shape != logits.shape:
+                raise ValueError(f"out must be {logits.dtype} of shape {tuple(logits.shape)}, got {out.dtype} of "
+                                 f"shape {tuple(out.shape)}")
+    at = _args(("logits", logits[:1, :1], None, None), *specs,
+               ("out", None if out is None else out[:1, :1], None, None))
+    shape = GdnDistill(R, V, K, _DT[logits.dtype], float(temperature), float(kd_weight), float(ce_weight),
+                       int(ignore_index), stride, d_stride)
+    return ctypes.byref(shape), at[:-1], out
+
+
+def distill_fwd(logits, ids, top, *, teacher_lse=None, targets=None, temperature=1.0, kd_weight=1.0, ce_weight=0.0,
+                ignore_index=-100):
+    """gdn_distill_fwd: kd_weight * kd + ce_weight * ce of every row of logits
+    [rows, vocab] (fp32 or bf16; rows contiguous, any row stride).  kd: the
+    divergence of the student, softmax(logits / temperature), from the teacher's
+    kept logits top [rows, topk] fp32 at columns ids [rows, topk] int32 (negative:
+    not used), normalised over them, or with teacher_lse [rows] fp32 (logsumexp of
+    the teacher's whole row / temperature) with all other columns as one more
+    outcome.  ce: cross entropy against targets [rows] int64 (None: none); a row
+    whose target is ignore_index has no loss at all.
+    Returns (loss [rows], stats [rows, 4]) in fp32; stats is for distill_bwd."""
+    shape, at, _ = _distill_args(logits, ids, top, teacher_lse, targets, temperature, kd_weight, ce_weight,
+                                 ignore_index, None)
+    loss = top.new_empty(logits.shape[0])
+    stats = top.new_empty(logits.shape[0], 4)
+    _lib.check(_lib.lib().gdn_distill_fwd(shape, *at, loss.data_ptr(), stats.data_ptr(), _stream_at()))
+    return loss, stats
+
+
+def distill_bwd(logits, ids, top, stats, d_loss=None, *, teacher_lse=None, targets=None, temperature=1.0,
+                kd_weight=1.0, ce_weight=0.0, ignore_index=-100, out=None):
+    """gdn_distill_bwd: the gradient of distill_fwd's logits for d_loss [rows]
+    fp32 (None: 1).  stats: what distill_fwd returned; the other arguments are
+    its.  out: as the logits, and may be the logits themselves (they are
+    overwritten then).  Returns d_logits."""
+    R = logits.shape[0] if isinstance(logits, torch.Tensor) and logits.dim() else 0
+    if stats is None:
+        raise ValueError("stats is required")
+    shape, at, out = _distill_args(logits, ids, top, teacher_lse, targets, temperature, kd_weight, ce_weight,
+                                   ignore_index, True if out is None else out,
+                                   ("stats", stats, torch.float32, (R, 4)), ("d_loss", d_loss, torch.float32, (R,)))
+    _lib.check(_lib.lib().gdn_distill_bwd(shape, *at, out.data_ptr(), _stream_at()))
+    return out
+
+
+def distill_fwd_bwd(logits, ids, top, d_loss=None, *, teacher_lse=None, targets=None, temperature=1.0, kd_weight=1.0,
+                    ce_weight=0.0, ignore_index=-100, out=None):
+    """gdn_distill_fwd_bwd: distill_fwd's losses and, for d_loss [rows] fp32
+    (None: 1), the logits' gradient, reading the logits once.  out: as in
+    distill_bwd.  Returns (loss [rows] fp32, d_logits)."""
+    R = logits.shape[0] if isinstance(logits, torch.Tensor) and logits.dim() else 0
+    shape, at, out = _distill_args(logits, ids, top, teacher_lse, targets, temperature, kd_weight, ce_weight,
+                                   ignore_index, True if out is None else out,
+                                   ("d_loss", d_loss, torch.float32, (R,)))
+    loss = top.new_empty(R)
+    _lib.check(_lib.lib().gdn_distill_fwd_bwd(shape, *at, loss.data_ptr(), out.data_ptr(), _stream_at()))
+    return loss, out

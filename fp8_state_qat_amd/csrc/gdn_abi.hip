@@ -644,3 +644,88 @@ gdn_status_t gdn_act_unpack(const uint8_t* codes, const float* scales, void* x, 
 }
 
 }  // extern "C"
+
+namespace {
+
+gdn_status_t check_distill(const gdn_distill_t* s, bool grad, const void* logits, const int32_t* ids, const float* top,
+                           const float* teacher_lse, const int64_t* targets, const float* d_loss, const float* loss,
+                           const float* stats, const void* d_logits) {
+  if (s == nullptr) return fail(GDN_ERR_INVALID_ARG, "shape is NULL");
+  if (s->rows < 0) return fail(GDN_ERR_INVALID_ARG, "rows must be >= 0");
+  if (s->vocab < 1) return fail(GDN_ERR_INVALID_ARG, "vocab must be >= 1 (got %d)", s->vocab);
+  if (s->vocab > 1 << 20) return fail(GDN_ERR_UNSUPPORTED, "vocab above 2^20 is not supported (got %d)", s->vocab);
+  if (s->topk < 0) return fail(GDN_ERR_INVALID_ARG, "topk must be >= 0 (got %d)", s->topk);
+  if (s->topk > 256) return fail(GDN_ERR_UNSUPPORTED, "topk above 256 is not supported (got %d)", s->topk);
+  if (s->dtype != GDN_F32 && s->dtype != GDN_BF16)
+    return fail(GDN_ERR_INVALID_ARG, "dtype must be GDN_F32 or GDN_BF16");
+  if (!(s->temperature > 0.0f) || !(s->temperature < 1e30f))
+    return fail(GDN_ERR_INVALID_ARG, "temperature must be positive and finite");
+  if (s->row_stride < s->vocab || (grad && s->d_row_stride < s->vocab))
+    return fail(GDN_ERR_INVALID_ARG, "row strides must be at least vocab");
+  if (s->rows > 0 && (s->rows > ((int64_t)1 << 60) / s->row_stride ||
+                      (grad && s->rows > ((int64_t)1 << 60) / s->d_row_stride) || s->rows > (int64_t)1 << 50))
+    return fail(GDN_ERR_UNSUPPORTED, "rows times the row stride is too large");
+  if (s->rows > 0) {
+    if (!logits || (s->topk > 0 && (!ids || !top)))
+      return fail(GDN_ERR_INVALID_ARG, "logits, ids and top must be non-NULL");
+    if (grad && !d_logits) return fail(GDN_ERR_INVALID_ARG, "d_logits must be non-NULL");
+    if (!loss && !stats) return fail(GDN_ERR_INVALID_ARG, "loss and stats must be non-NULL");
+  }
+  const uintptr_t e = elem(s->dtype);
+  if (!aligned(logits, e) || !aligned(d_logits, e) || !aligned(ids, 4) || !aligned(top, 4) ||
+      !aligned(teacher_lse, 4) || !aligned(targets, 8) || !aligned(d_loss, 4) || !aligned(loss, 4) ||
+      !aligned(stats, 4))
+    return fail(GDN_ERR_INVALID_ARG, "misaligned buffer");
+  if (grad && s->rows > 0 && d_logits == logits && s->d_row_stride != s->row_stride)
+    return fail(GDN_ERR_INVALID_ARG, "d_logits in place of the logits needs their row stride");
+  return GDN_OK;
+}
+
+gdn_status_t run_distill(const gdn_distill_t* s, const void* logits, const int32_t* ids, const float* top,
+                         const float* teacher_lse, const int64_t* targets, const float* d_loss, float* loss,
+                         float* stats, void* d_logits, void* stream) {
+  gdn_status_t st = check_device();
+  if (st != GDN_OK || s->rows == 0) return st;
+  hipError_t e = gdn::launch_distill(*s, logits, ids, top, teacher_lse, targets, d_loss, loss, stats, d_logits,
+                                     (hipStream_t)stream);
+  if (e != hipSuccess) return fail(GDN_ERR_DEVICE, "launch failed: %s", hipGetErrorString(e));
+  return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status_t gdn_distill_fwd(const gdn_distill_t* shape, const void* logits, const int32_t* ids, const float* top,
+                             const float* teacher_lse, const int64_t* targets, float* loss, float* stats,
+                             void* stream) {
+  g_err[0] = 0;
+  gdn_status_t st = check_distill(shape, false, logits, ids, top, teacher_lse, targets, nullptr, loss, stats, nullptr);
+  if (st == GDN_OK && shape->rows > 0 && (!loss || !stats))
+    st = fail(GDN_ERR_INVALID_ARG, "loss and stats must be non-NULL");
+  if (st != GDN_OK) return st;
+  return run_distill(shape, logits, ids, top, teacher_lse, targets, nullptr, loss, stats, nullptr, stream);
+}
+
+gdn_status_t gdn_distill_bwd(const gdn_distill_t* shape, const void* logits, const int32_t* ids, const float* top,
+                             const float* teacher_lse, const int64_t* targets, const float* stats,
+                             const float* d_loss, void* d_logits, void* stream) {
+  g_err[0] = 0;
+  gdn_status_t st =
+      check_distill(shape, true, logits, ids, top, teacher_lse, targets, d_loss, nullptr, stats, d_logits);
+  if (st != GDN_OK) return st;
+  return run_distill(shape, logits, ids, top, teacher_lse, targets, d_loss, nullptr, const_cast<float*>(stats),
+                     d_logits, stream);
+}
+
+gdn_status_t gdn_distill_fwd_bwd(const gdn_distill_t* shape, const void* logits, const int32_t* ids, const float* top,
+                                 const float* teacher_lse, const int64_t* targets, const float* d_loss, float* loss,
+                                 void* d_logits, void* stream) {
+  g_err[0] = 0;
+  gdn_status_t st =
+      check_distill(shape, true, logits, ids, top, teacher_lse, targets, d_loss, loss, nullptr, d_logits);
+  if (st != GDN_OK) return st;
+  return run_distill(shape, logits, ids, top, teacher_lse, targets, d_loss, loss, nullptr, d_logits, stream);
+}
+
+}  // extern "C"

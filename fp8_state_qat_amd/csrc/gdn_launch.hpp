@@ -146,6 +146,12 @@ hipError_t launch_block_norm_bwd(const gdn_norm_t& s, const void* f, const float
                                  const void* d_x, const void* d_h, void* d_f, void* d_z, void* d_residual,
                                  float* dw_post, float* dw_pre, void* workspace, hipStream_t stream);
 
+// Distillation (gdn_distill.hip): losses (d_logits null), the gradient (loss
+// null), or both.
+hipError_t launch_distill(const gdn_distill_t& s, const void* logits, const int32_t* ids, const float* top,
+                          const float* teacher_lse, const int64_t* targets, const float* d_loss, float* loss,
+                          float* stats, void* d_logits, hipStream_t stream);
+
 // Activations as E4M3 codes (gdn_act8.hip).
 hipError_t launch_act_pack(const void* x, int dtype, uint8_t* codes, float* scales, int64_t rows, int cols,
                            hipStream_t stream);

@@ -550,6 +550,75 @@ gdn_status_t gdn_act_pack(const void* x, int32_t dtype, uint8_t* codes, float* s
 gdn_status_t gdn_act_unpack(const uint8_t* codes, const float* scales, void* x, int32_t dtype,
                             int64_t rows, int32_t cols, void* stream);
 
+/*
+ * Distillation from a teacher's top logits, with cross entropy (the loss of
+ * quantization-aware distillation, #2497 "What does this PR do?"), row by row.
+ * z: a row of logits; t_j, j < topk: the logits that were kept of the teacher's
+ * row, at columns ids_j; h: the temperature; q = softmax(z / h):
+ *   p_j = e^(t_j / h - c)
+ *   kd  = sum_j p_j (ln p_j - ln q_(ids_j))
+ *   ce  = logsumexp(z) - z_target
+ *   loss = kd_weight kd + ce_weight ce
+ * Without teacher_lse c is the logsumexp of the kept t / h, so that p sums to 1.
+ * With it (the logsumexp of t / h over the teacher's whole row) all columns that
+ * were not kept are one more outcome: kd += r (ln r - ln q_r), r = 1 - sum p (0
+ * where that is negative), q_r the sum of their q (no term where every column is
+ * kept).
+ *   - ids: a negative entry is not used; the same column may come twice (its p
+ *     add up); a row without any used entry has kd = 0.
+ *   - A row whose target is ignore_index has loss, statistics and gradient 0, and
+ *     its logits are not read for the gradient.
+ *   - A row with an id >= vocab, or with another target outside [0, vocab), gets
+ *     NaN everywhere.
+ *   - Logits of -inf (masked columns) are allowed: q = 0 there, the gradient too;
+ *     a kept or target column among them makes the loss +inf.  Other non-finite
+ *     logits make their row NaN.
+ * Sums and statistics in fp32 relative to the row's maximum, the teacher's p and
+ * the rest in fp64; a value of d_logits is rounded once.
+ */
+typedef struct {
+    int64_t rows;              /* >= 0 */
+    int32_t vocab;             /* 1 .. 2^20 */
+    int32_t topk;              /* 0 .. 256 */
+    int32_t dtype;             /* gdn_dtype_t of the logits and d_logits */
+    float temperature;         /* h > 0 */
+    float kd_weight, ce_weight;
+    int64_t ignore_index;
+    int64_t row_stride;        /* elements between rows of logits, >= vocab */
+    int64_t d_row_stride;      /* and of d_logits (not read by the forward) */
+} gdn_distill_t;
+
+/*
+ * gdn_distill_fwd
+ *   ids, top     [rows, topk] int32, fp32 (NULL with topk 0)
+ *   teacher_lse  [rows] fp32 or NULL
+ *   targets      [rows] int64 or NULL: no cross entropy (ce_weight is not read)
+ *   loss         [rows] fp32
+ *   stats        [rows, 4] fp32, for the backward: the logsumexp of z (0 without
+ *                targets), that of z / h, c, and that of z / h over the columns
+ *                that were not kept (0 without teacher_lse)
+ */
+gdn_status_t gdn_distill_fwd(const gdn_distill_t* shape, const void* logits, const int32_t* ids, const float* top,
+                             const float* teacher_lse, const int64_t* targets, float* loss, float* stats,
+                             void* stream);
+
+/*
+ * gdn_distill_bwd -- d_logits for the losses' gradients d_loss [rows] fp32 (NULL:
+ * 1); the other arguments are the forward's, stats what it wrote.  d_logits may be
+ * the logits themselves (same row stride), else they may not overlap.
+ */
+gdn_status_t gdn_distill_bwd(const gdn_distill_t* shape, const void* logits, const int32_t* ids, const float* top,
+                             const float* teacher_lse, const int64_t* targets, const float* stats,
+                             const float* d_loss, void* d_logits, void* stream);
+
+/*
+ * gdn_distill_fwd_bwd -- losses and d_logits in one call, where d_loss is known
+ * before the losses are (a mean's weights): the logits are read once.
+ */
+gdn_status_t gdn_distill_fwd_bwd(const gdn_distill_t* shape, const void* logits, const int32_t* ids, const float* top,
+                                 const float* teacher_lse, const int64_t* targets, const float* d_loss, float* loss,
+                                 void* d_logits, void* stream);
+
 /* Static description of a status code. */
 const char* gdn_status_string(gdn_status_t status);
 

@@ -390,3 +390,94 @@ def test_grad_workspace_sizes():
              for f, given in ((0, 1), (0, 0), (1, 1), (1, 0))]
     assert 0 < sizes[0] == sizes[2] < sizes[1] < sizes[3]
     assert L.gdn_chunk_grad_workspace_bytes(ctypes.byref(_grad_shape(dk=32)), 0) == 0
+
+
+# ---------------------------------------------------------------- distillation
+def test_distill_reference_against_differences():
+    """The definition's gradient by torch against central differences: error h^2 f''' / 6 + 2^-53 |L| / h ~ 1e-9."""
+    import distill_ref
+    gen = torch.Generator().manual_seed(0)
+    z = torch.randn(3, 9, generator=gen).double()
+    ids = torch.tensor([[1, 4, 4], [2, -1, 0], [8, 3, 5]])
+    top = torch.randn(3, 3, generator=gen)
+    targets = torch.tensor([4, -100, 0])
+    for lse in (None, torch.logsumexp(top.double() / 2, 1).float() + 0.5):
+        kw = dict(lse=lse, targets=targets, h=2.0, kd_weight=0.7, ce_weight=0.4)
+        _, _, dz = distill_ref.grads(z, ids, top, None, **kw)
+        assert (dz[1] == 0).all()
+        for j in range(27):
+            up, down = z.clone(), z.clone()
+            up.view(-1)[j] += 1e-5
+            down.view(-1)[j] -= 1e-5
+            slope = (distill_ref.losses(up, ids, top, **kw)[0].sum() -
+                     distill_ref.losses(down, ids, top, **kw)[0].sum()) / 2e-5
+            assert abs(float(slope) - float(dz.view(-1)[j])) < 1e-7
+
+
+DR, DV_, DK_ = 3, 20, 2
+
+
+def _distill(**over):
+    a = dict(z=torch.zeros(DR, DV_), ids=torch.zeros(DR, DK_, dtype=torch.int32), top=torch.zeros(DR, DK_))
+    a.update({k: over.pop(k) for k in list(over) if k in a})
+    return tuple(a.values()), over
+
+
+DISTILL_BAD = [
+    (dict(z=None), "logits"), (dict(z=torch.zeros(DR)), "logits"), (dict(z=torch.zeros(DR, DV_).half()), "float32"),
+    (dict(z=torch.zeros(DV_, DR).t()), "contiguous rows"), (dict(z=torch.zeros(DR, 0)), "vocab >= 1"),
+    (dict(z=torch.zeros(1, DV_).expand(DR, DV_)), "overlap"),
+    (dict(ids=torch.zeros(DR + 1, DK_, dtype=torch.int32)), "ids"), (dict(ids=torch.zeros(DR, DK_).long()), "ids"),
+    (dict(ids=None), "ids"), (dict(top=None), "top"), (dict(top=torch.zeros(DR, DK_ + 1)), "top"),
+    (dict(top=torch.zeros(DR, DK_).bfloat16()), "top"), (dict(teacher_lse=torch.zeros(DR, 1)), "teacher_lse"),
+    (dict(targets=torch.zeros(DR, dtype=torch.int32)), "targets"), ({}, "device tensor"),
+]
+
+
+@pytest.mark.parametrize("over,what", DISTILL_BAD)
+def test_distill_fwd_refusals(over, what):
+    a, kw = _distill(**over)
+    with pytest.raises(ValueError, match=what):
+        api.distill_fwd(*a, **kw)
+
+
+@pytest.mark.parametrize("over,what", DISTILL_BAD + [
+    (dict(d_loss=torch.zeros(DR + 1)), "d_loss"), (dict(out=torch.zeros(DR, DV_).bfloat16()), "out"),
+    (dict(out=torch.zeros(DR, DV_ + 1)), "out"), (dict(out=torch.zeros(DV_, DR).t()), "contiguous rows")])
+def test_distill_gradient_refusals(over, what):
+    a, kw = _distill(**over)
+    w = kw.pop("d_loss", torch.zeros(DR))
+    with pytest.raises(ValueError, match=what):
+        api.distill_fwd_bwd(*a, w, **kw)
+    with pytest.raises(ValueError, match=what):
+        api.distill_bwd(*a, torch.zeros(DR, 4), w, **kw)
+
+
+def test_distill_bwd_needs_stats():
+    a, _ = _distill()
+    with pytest.raises(ValueError, match="stats"):
+        api.distill_bwd(*a, None)
+    with pytest.raises(ValueError, match="stats"):
+        api.distill_bwd(*a, torch.zeros(DR, 3))
+
+
+@pytest.mark.parametrize("over,status,text", [
+    (dict(rows=-1), 1, "rows"), (dict(vocab=0), 1, "vocab"), (dict(vocab=(1 << 20) + 1, row_stride=1 << 21), 2, "vocab"),
+    (dict(topk=-1), 1, "topk"), (dict(topk=257), 2, "topk"), (dict(dtype=2), 1, "dtype"),
+    (dict(temperature=0.0), 1, "temperature"), (dict(temperature=float("nan")), 1, "temperature"),
+    (dict(temperature=float("inf")), 1, "temperature"), (dict(row_stride=19), 1, "strides"),
+    (dict(d_row_stride=19), 1, "strides"), (dict(rows=1 << 40, row_stride=1 << 30), 2, "too large"),
+    (dict(z=0), 1, "non-NULL"), (dict(ids=0), 1, "non-NULL"), (dict(top=0), 1, "non-NULL"), (dict(dz=0), 1, "d_logits"),
+    (dict(loss=0), 1, "non-NULL"), (dict(z=FAKE + 1), 1, "misaligned"), (dict(targets=FAKE + 4), 1, "misaligned"),
+    (dict(dz=FAKE, d_row_stride=24), 1, "row stride"),
+])
+def test_distill_abi_refusals(over, status, text):
+    at = dict(z=FAKE, ids=2 * FAKE, top=3 * FAKE, lse=4 * FAKE, targets=5 * FAKE, d_loss=6 * FAKE, loss=7 * FAKE,
+              dz=8 * FAKE)
+    at.update({k: over[k] for k in over if k in at})
+    s = dict(rows=3, vocab=20, topk=2, dtype=0, temperature=1.0, kd_weight=1.0, ce_weight=0.0, ignore_index=-100,
+             row_stride=20, d_row_stride=20)
+    s.update({k: over[k] for k in over if k in s})
+    p = [P(x) if x else None for x in at.values()]
+    assert _lib.lib().gdn_distill_fwd_bwd(ctypes.byref(_lib.GdnDistill(**s)), *p, None) == status
+    assert text in _lib.last_error()
