@@ -31,7 +31,6 @@ namespace gdn {
 namespace {
 
 constexpr int kMaxTop = 256, kMaxVocab = 1 << 20;
-constexpr double kLn2d = 0.6931471805599453;
 constexpr float kLog2ef = 1.4426950408889634f;
 
 struct DistillArgs {
@@ -70,6 +69,22 @@ struct Oct<uint16_t> {
     x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
     x[4] = bf16_lo(u.z); x[5] = bf16_hi(u.z); x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
   }
+  // columns of a set of bits to -inf
+  __device__ __forceinline__ void clear(uint32_t b) {
+    uint32_t* p[4] = {&u.x, &u.y, &u.z, &u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (b >> (2 * i) & 1) *p[i] = (*p[i] & 0xffff0000u) | 0xff80u;
+      if (b >> (2 * i + 1) & 1) *p[i] = (*p[i] & 0xffffu) | 0xff800000u;
+    }
+  }
+  // their largest value, up to the bits below an odd column's bf16 (it is a reference only)
+  __device__ __forceinline__ float largest() const {
+    const float a = fmaxf(fmaxf(bf16_lo(u.x), __uint_as_float(u.x)), fmaxf(bf16_lo(u.y), __uint_as_float(u.y)));
+    return fmaxf(fmaxf(a, fmaxf(bf16_lo(u.z), __uint_as_float(u.z))), fmaxf(bf16_lo(u.w), __uint_as_float(u.w)));
+  }
+  // unpacked anew from here on: the compiler would keep the values of an earlier get() instead, twice the registers
+  __device__ __forceinline__ void hide() { asm volatile("" : "+v"(u.x), "+v"(u.y), "+v"(u.z), "+v"(u.w)); }
 };
 template <>
 struct Oct<float> {
@@ -90,6 +105,16 @@ struct Oct<float> {
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
   }
+  __device__ __forceinline__ void clear(uint32_t m) {
+    float* p[8] = {&a.x, &a.y, &a.z, &a.w, &b.x, &b.y, &b.z, &b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (m >> i & 1) *p[i] = -INFINITY;
+  }
+  __device__ __forceinline__ float largest() const {
+    return fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)), fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
+  }
+  __device__ __forceinline__ void hide() {}
 };
 
 template <typename T>
@@ -102,37 +127,167 @@ __device__ __forceinline__ void st_some(T* p, int lo, int hi, const float (&x)[8
     }
 }
 
-// e^x by the hardware's 2^x; x <= a few, results below 2^-126 are 0.
-__device__ __forceinline__ float exp_hw(float x) { return __builtin_amdgcn_exp2f(x * kLog2ef); }
+// 2^x by the hardware; results below 2^-126 are 0.
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ double sum_f64(double x) { return last_lane(wave_prefix_f64(x)); }
 
-__device__ __forceinline__ double wave_max_f64(double x) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) x = fmax(x, __shfl_xor(x, o, 64));
-  return x;
-}
-__device__ __forceinline__ double wave_sum_f64(double x) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) x += __shfl_xor(x, o, 64);
-  return x;
-}
-
-// What a row's gradient is made of.
+// What a row's gradient is made of; exponentials in base 2.
 struct DistillRow {
-  float A, L;        // A e^(z / h - L) of every column ..
-  float B, lse;      // + B e^(z - lse)
-  float q, lse_h;    // kept columns beside a rest: q e^(z / h - lse_h) in place of the first
-  float a, b;        // factors of p and of [v = target]
+  float A, L;        // A 2^(z c / h - L) of every column (c = log2 e) ..
+  float B, lse;      // + B 2^(z c - lse); h = 2: + B (2^(z c / h - L))^2
+  float q, lse_h;    // kept columns beside a rest: q 2^(z c / h - lse_h) ..
+  float b, lse_b;    // .. + b 2^(z c - lse_b)
+  float a;           // factor of p
   int bad;
 };
 
+constexpr int kHash = 1024;
+
 struct DistillShared {
-  double p[kMaxTop], lt[kMaxTop];   // p_j and ln p_j (0 and 0 where unused)
-  int id[kMaxTop];                  // -1: unused
+  double p[kMaxTop];                // p_j, a column's whole at its first entry, else 0 (0: unused)
+  int id[kMaxTop];                  // -1: unused, or not the column's first entry
   float zj[kMaxTop];
   float zt;                         // the target's logit
+  int dup;
   float red[3][16];
   DistillRow row;
+  uint32_t hash[kHash];
 };
+
+// The kept entries of a row, one wave: p, the sums over them that the row's
+// values need, and the columns that come twice, found by a table of the ids (a
+// search through all pairs only where there are any).
+struct DistillKept {
+  double c, mass, rest;   // c, sum p, r
+  double kd;              // sum p_j (ln p_j - z_j / h)
+  double m, e1, eh;       // the columns' largest z_j, sums of e^(z_j - m), e^((z_j - m) / h)
+  int n;                  // columns
+  bool bad;
+};
+
+template <typename T>
+__device__ __forceinline__ DistillKept distill_kept(const DistillArgs& A, int64_t r, const T* z, DistillShared& sh,
+                                                    uint32_t* bits, int shift) {
+  constexpr int kPer = kMaxTop / 64;
+  const int lane = threadIdx.x & 63, K = A.K;
+  const bool tail = A.teacher_lse != nullptr;
+  const double h = (double)A.h;
+  DistillKept o;
+#pragma unroll
+  for (int i = 0; i < kHash / 256; ++i) reinterpret_cast<uint4*>(sh.hash)[lane + 64 * i] = make_uint4(0, 0, 0, 0);
+  int id[kPer];
+  float t[kPer], zj[kPer];
+  bool out = false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int j = lane + 64 * i;
+    id[i] = j < K ? A.ids[r * K + j] : -1;
+    out |= id[i] >= A.V;
+    if (id[i] >= A.V) id[i] = -1;
+    t[i] = id[i] >= 0 ? A.top[r * K + j] : -INFINITY;
+    zj[i] = id[i] >= 0 ? io<T>::ld(z + id[i]) : -INFINITY;
+  }
+  o.bad = __ballot(out) != 0;
+  bool dup = false;
+  float tm = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (64 * i >= K) break;
+    tm = fmaxf(tm, t[i]);
+    if (id[i] < 0) continue;
+    const uint32_t me = (uint32_t)id[i] + 1;
+    for (uint32_t at = (me * 2654435761u) >> 22;; at = (at + 1) & (kHash - 1)) {   // at most kMaxTop entries: ends
+      const uint32_t was = atomicCAS(&sh.hash[at], 0u, me);
+      dup |= was == me;
+      if (was == 0u || was == me) break;
+    }
+    if (bits != nullptr) {
+      const int b = id[i] + shift;
+      atomicOr(bits + (b >> 5), 1u << (b & 31));
+    }
+  }
+  if (tail) {
+    o.c = (double)A.teacher_lse[r];
+  } else {
+    const double m = (double)wave_max_dpp(tm);
+    double e = 0.0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (64 * i < K && t[i] > -INFINITY) e += exp(((double)t[i] - m) / h);
+    e = sum_f64(e);
+    o.c = e > 0.0 ? m / h + log(e) : -INFINITY;
+  }
+  double p[kPer], sp = 0.0, kd = 0.0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    p[i] = 0.0;
+    if (64 * i >= K) continue;
+    const double l = (double)t[i] / h - o.c;
+    if (t[i] > -INFINITY) p[i] = exp(l);
+    if (p[i] > 0.0) kd += p[i] * (l - (double)zj[i] / h);
+    sp += p[i];
+    sh.id[lane + 64 * i] = id[i];
+    sh.p[lane + 64 * i] = p[i];
+    sh.zj[lane + 64 * i] = zj[i];
+  }
+  o.mass = sum_f64(sp);
+  o.kd = sum_f64(kd);
+  if (__ballot(dup) != 0) {   // the first entry of a column takes the others' p
+    int keep[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      keep[i] = id[i];
+      if (id[i] < 0) continue;
+      const int j = lane + 64 * i;
+      p[i] = 0.0;
+      for (int e = 0; e < K; ++e)
+        if (sh.id[e] == id[i]) {
+          if (e < j) keep[i] = -1;
+          p[i] += sh.p[e];
+        }
+      if (keep[i] < 0) p[i] = 0.0;
+    }
+    __builtin_amdgcn_wave_barrier();   // every lane has read before the first writes: one wave, in order
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (64 * i < K) {
+        id[i] = keep[i];
+        sh.id[lane + 64 * i] = id[i];
+        sh.p[lane + 64 * i] = p[i];
+      }
+  }
+  o.rest = 0.0;
+  o.n = 0;
+  if (tail) {
+    float zm = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (id[i] >= 0) zm = fmaxf(zm, zj[i]);
+      o.n += __popcll(__ballot(id[i] >= 0));
+    }
+    o.m = (double)wave_max_dpp(zm);
+    double e1 = 0.0, eh = 0.0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (64 * i < K && id[i] >= 0 && o.m > -INFINITY) {
+        e1 += exp((double)zj[i] - o.m);
+        eh += exp(((double)zj[i] - o.m) / h);
+      }
+    o.e1 = sum_f64(e1);
+    o.eh = sum_f64(eh);
+    o.rest = o.n < A.V ? fmax(0.0, 1.0 - o.mass) : 0.0;   // no column is left: no rest
+  } else {
+    o.mass = o.c > -INFINITY ? 1.0 : 0.0;
+  }
+  return o;
+}
+
+// log(e^(m + ln s) + e^(n + ln t)) with s, t >= 0
+__device__ __forceinline__ double log_add(double m, double s, double n, double t) {
+  if (!(t > 0.0)) return s > 0.0 || s != s ? m + log(s) : -INFINITY;
+  const double x = s > 0.0 || s != s ? fmax(m, n) : n;
+  return x + log((s > 0.0 || s != s ? s * exp(m - x) : 0.0) + t * exp(n - x));
+}
 
 }  // namespace
 
@@ -151,15 +306,20 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
   const bool tail = A.teacher_lse != nullptr;
   const int64_t target = A.targets ? A.targets[r] : 0;
   const bool ignored = A.targets != nullptr && target == A.ignore;
-  const bool two = A.targets != nullptr && A.h != 1.0f;   // a second exponential
-  const float ih = 1.0f / A.h;
+  const bool two = A.targets != nullptr && A.h != 1.0f;   // a second exponential:
+  const bool square = A.h == 2.0f;                        // with h = 2 the first one's square
+  const float ch = (float)(1.4426950408889634 / (double)A.h);
 
-  // octet o: columns 8 o - shift .. + 7
+  // octet o: columns 8 o - shift .. + 7; whole ones from o0 to o1 - 1, at 16-byte addresses; the columns before and
+  // behind them are thread 0's and 1's edge octet, from column e0 with e_lo .. e_hi - 1 of it in the row
   constexpr int kPer = 16 / (int)sizeof(T);
   const int head = (kPer - (int)((uintptr_t)z / sizeof(T) % kPer)) % kPer;
   const int shift = (8 - head) % 8;
-  const int octs = (V + shift + 7) / 8;
-  const int tiles = (octs + TPB * U - 1) / (TPB * U);
+  const int o0 = shift > 0 ? 1 : 0, o1 = (V + shift) / 8;
+  const int tiles = max(1, (o1 - o0 + TPB * U - 1) / (TPB * U));
+  const int e_oct = tid == 0 ? 0 : o1, e0 = 8 * e_oct - shift;
+  const bool edge = tid == 0 ? shift > 0 : tid == 1 && (V + shift) % 8 != 0 && o1 >= o0;
+  const int e_lo = edge && tid == 0 ? shift : 0, e_hi = edge ? min(8, V - e0) : 0;
 
   if (ignored) {
     if (kStats && tid == 0) A.loss[r] = 0.0f;
@@ -167,239 +327,199 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
     if constexpr (kGrad) {
       const float zero[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
       const bool vec = (uintptr_t)(dz + head) % 16 == 0;
-      for (int o = tid; o < octs; o += TPB) {
-        const int v0 = 8 * o - shift;
-        if (vec && v0 >= 0 && v0 + 8 <= V) st_oct<T, true>(dz + v0, 8, zero);
-        else st_some(dz + v0, max(0, -v0), min(8, V - v0), zero);
+      for (int o = o0 + tid; o < o1; o += TPB) {
+        if (vec) st_oct<T, true>(dz + 8 * o - shift, 8, zero);
+        else st_some(dz + 8 * o - shift, 0, 8, zero);
       }
+      if (edge) st_some(dz + e0, e_lo, e_hi, zero);
     }
     return;
   }
 
-  Oct<T> x[U];
+  Oct<T> x[U], xe;
+  const T* zo = z + 8 * o0 - shift;   // octet o0
+  T* dzo = kGrad ? dz + 8 * o0 - shift : nullptr;
   auto load = [&](int tile) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int o = (tile * U + u) * TPB + tid, v0 = 8 * o - shift;
-      if (o >= octs) x[u].none();
-      else if (v0 >= 0 && v0 + 8 <= V) x[u].ld(z + v0);
-      else x[u].ld_some(z + v0, max(0, -v0), min(8, V - v0));
+      const uint32_t o = (uint32_t)((tile * U + u) * TPB + tid);
+      if ((int)o < o1 - o0) x[u].ld((const T*)((const char*)zo + o * (uint32_t)(8 * sizeof(T))));
+      else x[u].none();
     }
   };
   load(0);
+  xe.none();
+  if (edge) xe.ld_some(z + e0, e_lo, e_hi);
 
-  // the kept entries
-  if (tail && kStats) {
-    for (int i = tid; i < (octs + 3) / 4; i += TPB) reinterpret_cast<uint32_t*>(bits)[i] = 0u;
+  const bool mark = tail && kStats;
+  if (mark) {
+    for (int i = tid; i < (V + shift + 31) / 32; i += TPB) reinterpret_cast<uint32_t*>(bits)[i] = 0u;
     __syncthreads();
   }
-  double c = 0.0, mass = 0.0, rest = 0.0;   // wave 0's: c, sum p, r
-  bool bad = A.targets != nullptr && (target < 0 || target >= V);
+  DistillKept kp;   // wave 0's
   if (w == 0) {
-    if (lane == 0 && A.targets != nullptr && !bad) sh.zt = io<T>::ld(z + target);
-    double m = -INFINITY;
-    bool out = false;
-    for (int j = lane; j < K; j += 64) {
-      const int id = A.ids[r * K + j];
-      out |= id >= V;
-      const int use = id >= 0 && id < V ? id : -1;
-      const double t = use >= 0 ? (double)A.top[r * K + j] / (double)A.h : -INFINITY;
-      sh.id[j] = use;
-      sh.zj[j] = use >= 0 ? io<T>::ld(z + use) : -INFINITY;
-      sh.lt[j] = t;
-      m = fmax(m, t);
-      if (tail && kStats && use >= 0) {
-        const int at = use + shift;
-        atomicOr(reinterpret_cast<uint32_t*>(bits) + (at >> 5), 1u << (at & 31));
-      }
-    }
-    bad |= __ballot(out) != 0;
-    if (tail) {
-      c = (double)A.teacher_lse[r];
-    } else {
-      m = wave_max_f64(m);
-      double s = 0.0;
-      if (m > -INFINITY)
-        for (int j = lane; j < K; j += 64) s += exp(sh.lt[j] - m);
-      s = wave_sum_f64(s);
-      c = m > -INFINITY ? m + log(s) : -INFINITY;
-    }
-    double sum = 0.0;
-    for (int j = lane; j < K; j += 64) {
-      const double l = sh.lt[j] - c, p = sh.lt[j] > -INFINITY ? exp(l) : 0.0;
-      sh.p[j] = p;
-      sh.lt[j] = p > 0.0 ? l : 0.0;
-      sum += p;
-    }
-    mass = wave_sum_f64(sum);
-    if (tail) rest = fmax(0.0, 1.0 - mass);
-    else mass = c > -INFINITY ? 1.0 : 0.0;
+    kp = distill_kept<T>(A, r, z, sh, mark ? reinterpret_cast<uint32_t*>(bits) : nullptr, shift);
+    const bool aim = A.targets != nullptr && target >= 0 && target < V;
+    if (A.targets != nullptr && !aim) kp.bad = true;
+    if (lane == 0 && aim) sh.zt = io<T>::ld(z + target);
   }
-  __syncthreads();
+  if (mark) __syncthreads();
 
-  float mx = -INFINITY, s1 = 0.0f, sh_ = 0.0f;   // maximum, sums of e^(z - mx), e^((z - mx) / h)
+  // sums of 2^(z c / h - mh) and 2^(z c - m1), mh and m1 whole numbers near their largest arguments (so that what the
+  // fma rounds is the argument alone; h = 2: m1 is 2 mh); both are 0 where there is no value yet
+  float top = -INFINITY, mh = 0.0f, m1 = 0.0f, sum_h = 0.0f, sum_1 = 0.0f;
   if constexpr (kStats) {
     for (int tile = 0; tile < tiles; ++tile) {
       if (tile > 0) load(tile);
-      float m = mx;
-      uint32_t ex[U];
+      float m = top;
+      if (mark) {   // kept columns are not of the rest: -inf (their gradient is written by itself)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int o = (tile * U + u) * TPB + tid;
+          const uint32_t b = o < o1 - o0 ? bits[o0 + o] : 0u;
+          if (b != 0u) x[u].clear(b);
+        }
+        if (edge) xe.clear(bits[e_oct]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) m = fmaxf(m, x[u].largest());
+      if (tile == 0) m = fmaxf(m, xe.largest());
+      if (m > top) {
+        const float nh = rintf(m * ch), n1 = square ? 2.0f * nh : rintf(m * kLog2ef);
+        if (top > -INFINITY) {
+          sum_h *= exp2_hw(mh - nh);
+          sum_1 *= exp2_hw(m1 - n1);
+        }
+        top = m;
+        mh = nh;
+        m1 = n1;
+      }
+      auto add = [&](const Oct<T>& y) {
+        float v[8];
+        y.get(v);
+        if (!two) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum_h += exp2_hw(fmaf(v[i], ch, -mh));
+        } else if (square) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float e = exp2_hw(fmaf(v[i], ch, -mh));
+            sum_h += e;
+            sum_1 = fmaf(e, e, sum_1);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            sum_h += exp2_hw(fmaf(v[i], ch, -mh));
+            sum_1 += exp2_hw(fmaf(v[i], kLog2ef, -m1));
+          }
+        }
+      };
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int o = (tile * U + u) * TPB + tid;
-        ex[u] = tail && o < octs ? bits[o] : 0u;
-        float v[8];
-        x[u].get(v);
-        if (ex[u] != 0u) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = ex[u] >> i & 1 ? -INFINITY : v[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, v[i]);
+        x[u].hide();
+        add(x[u]);
+        __builtin_amdgcn_sched_barrier(0);   // octet by octet: mixed, they take twice the registers
       }
-      const float ref = m > -INFINITY ? m : 0.0f;
-      if (m > mx) {
-        s1 *= exp_hw(mx - ref);
-        sh_ *= exp_hw((mx - ref) * ih);
-        mx = m;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float v[8];
-        x[u].get(v);
-        if (ex[u] != 0u) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = ex[u] >> i & 1 ? -INFINITY : v[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sh_ += exp_hw((v[i] - ref) * ih);
-        if (two) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s1 += exp_hw(v[i] - ref);
-        }
-      }
+      if (tile == 0 && edge) add(xe);
     }
     // over the wave, then the workgroup
-    float m = mx;
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-    const float ref = m > -INFINITY ? m : 0.0f;
-    s1 *= exp_hw(mx - ref);
-    sh_ *= exp_hw((mx - ref) * ih);
+    const float m = wave_max_dpp(top);
+    const float nh = m > -INFINITY ? rintf(m * ch) : 0.0f;
+    const float n1 = square ? 2.0f * nh : m > -INFINITY ? rintf(m * kLog2ef) : 0.0f;
+    if (top > -INFINITY) {
+      sum_h *= exp2_hw(mh - nh);
+      sum_1 *= exp2_hw(m1 - n1);
+    }
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) {
-      s1 += __shfl_xor(s1, o, 64);
-      sh_ += __shfl_xor(sh_, o, 64);
+      sum_h += __shfl_xor(sum_h, o, 64);
+      sum_1 += __shfl_xor(sum_1, o, 64);
     }
     if (lane == 0) {
       sh.red[0][w] = m;
-      sh.red[1][w] = s1;
-      sh.red[2][w] = sh_;
+      sh.red[1][w] = sum_h;
+      sh.red[2][w] = sum_1;
     }
     __syncthreads();
   }
 
   // the row's few values: wave 0
   if (w == 0) {
-    const double h = (double)A.h;
-    double lse, lse_h, lse_r;   // of z, of z / h, of z / h over the rest
+    double lse = 0.0, lse_h, lse_r;   // of z, of z / h, of z / h over the rest
     if constexpr (kStats) {
       float m = -INFINITY;
 #pragma unroll
       for (int i = 0; i < NW; ++i) m = fmaxf(m, sh.red[0][i]);
-      double a1 = 0.0, ah = 0.0;
+      const float nh = m > -INFINITY ? rintf(m * ch) : 0.0f;
+      const float n1 = square ? 2.0f * nh : m > -INFINITY ? rintf(m * kLog2ef) : 0.0f;
+      double ah = 0.0, a1 = 0.0;
 #pragma unroll
       for (int i = 0; i < NW; ++i) {   // a wave without any value has sums of 0, or NaN
-        const float d = sh.red[0][i] > -INFINITY ? sh.red[0][i] - m : 0.0f;
-        a1 += (double)(sh.red[1][i] * exp_hw(d));
-        ah += (double)(sh.red[2][i] * exp_hw(d * ih));
+        const float mw = sh.red[0][i];
+        const float wh = mw > -INFINITY ? rintf(mw * ch) : nh;
+        const float w1 = square ? 2.0f * wh : mw > -INFINITY ? rintf(mw * kLog2ef) : n1;
+        ah += (double)(sh.red[1][i] * exp2_hw(wh - nh));
+        a1 += (double)(sh.red[2][i] * exp2_hw(w1 - n1));
       }
-      if (!two) a1 = ah;
-      lse_r = lse_h = ah > 0.0 || ah != ah ? (double)m / h + log(ah) : -INFINITY;
-      lse = a1 > 0.0 || a1 != a1 ? (double)m + log(a1) : -INFINITY;
+      // exponents are z fl(c / h): the same factor takes them back to z / h
+      const double bh = 1.0 / ((double)ch * (double)A.h), b1 = 1.0 / (double)kLog2ef;
+      const double mr = (double)nh * bh;
+      lse_r = ah > 0.0 || ah != ah ? mr + log(ah) : -INFINITY;
       if (tail) {
-        // the kept entries (each column once) join the rest
-        double mh = -INFINITY;
-        for (int j = lane; j < K; j += 64) mh = fmax(mh, (double)sh.zj[j]);
-        mh = fmax(wave_max_f64(mh), (double)m);
-        double e1 = 0.0, eh = 0.0;
-        int n = 0;
-        if (mh > -INFINITY) {
-          for (int j = lane; j < K; j += 64) {
-            const int id = sh.id[j];
-            bool first = id >= 0;
-            for (int i = 0; i < j; ++i) first &= sh.id[i] != id;
-            if (!first) continue;
-            ++n;
-            e1 += exp((double)sh.zj[j] - mh);
-            eh += exp(((double)sh.zj[j] - mh) / h);
-          }
-          e1 = wave_sum_f64(e1) + exp(lse - mh);
-          eh = wave_sum_f64(eh) + exp(lse_r - mh / h);
-          n = (int)wave_sum_f64((double)n);
-          lse = mh + log(e1);
-          lse_h = mh / h + log(eh);
-        }
-        if (n == V) rest = 0.0;   // no column is left
+        lse_h = log_add(mr, ah, kp.m / (double)A.h, kp.eh);
+        if (two) lse = log_add((double)n1 * b1, a1, kp.m, kp.e1);
+      } else {
+        lse_h = lse_r;
+        if (two) lse = a1 > 0.0 || a1 != a1 ? (double)n1 * b1 + log(a1) : -INFINITY;
       }
-      double kd = 0.0;
-      for (int j = lane; j < K; j += 64)
-        if (sh.p[j] > 0.0) kd += sh.p[j] * (sh.lt[j] - ((double)sh.zj[j] / h - lse_h));
-      kd = wave_sum_f64(kd);
-      if (rest > 0.0) kd += rest * (log(rest) - (lse_r - lse_h));
+      if (!two) lse = lse_h;
+      double kd = kp.kd + (kp.mass > 0.0 ? kp.mass * lse_h : 0.0);
+      if (tail && kp.rest > 0.0) kd += kp.rest * (log(kp.rest) - (lse_r - lse_h));
       double loss = (double)A.kd * kd;
-      if (A.targets != nullptr && !bad) loss += (double)A.ce * (lse - (double)sh.zt);
-      if (lane == 0) A.loss[r] = bad ? NAN : (float)loss;
+      if (A.targets != nullptr && !kp.bad) loss += (double)A.ce * (lse - (double)sh.zt);
+      if (lane == 0) A.loss[r] = kp.bad ? NAN : (float)loss;
       if constexpr (MODE == kDisFwd) {
         if (lane < 4) {
-          const double s = lane == 0 ? (A.targets ? lse : 0.0) : lane == 1 ? lse_h : lane == 2 ? c : tail ? lse_r : 0.0;
-          A.stats[4 * r + lane] = bad ? NAN : (float)s;
+          const double s = lane == 0 ? (A.targets ? lse : 0.0)
+                           : lane == 1 ? lse_h : lane == 2 ? kp.c : tail ? lse_r : 0.0;
+          A.stats[4 * r + lane] = kp.bad ? NAN : (float)s;
         }
       }
     } else {
       lse = (double)A.stats[4 * r];
       lse_h = (double)A.stats[4 * r + 1];
       lse_r = (double)A.stats[4 * r + 3];
-      if (tail) {
-        int n = 0;
-        if (K >= V) {   // every column may be kept
-          for (int j = lane; j < K; j += 64) {
-            bool first = sh.id[j] >= 0;
-            for (int i = 0; i < j; ++i) first &= sh.id[i] != sh.id[j];
-            n += first ? 1 : 0;
-          }
-          n = (int)wave_sum_f64((double)n);
-        }
-        if (n == V) rest = 0.0;
-      }
     }
     if constexpr (kGrad) {
+      constexpr double c = 1.4426950408889634;
       const double wt = A.d_loss ? (double)A.d_loss[r] : 1.0;
-      const double a = wt * (double)A.kd / h, b = A.targets ? wt * (double)A.ce : 0.0, m = mass + rest;
+      const double a = wt * (double)A.kd / (double)A.h, b = A.targets ? wt * (double)A.ce : 0.0;
+      const double m = kp.mass + kp.rest;
+      // of every column: ea e^(z / h - l) + b e^(z - lse)
+      double ea = a * m, l = lse_h;
+      if (tail) {
+        const bool any = lse_r > -INFINITY;
+        ea = any ? a * (m * exp(lse_r - lse_h) - kp.rest) : 0.0;
+        l = any ? lse_r : 0.0;
+      }
       DistillRow d;
       d.a = (float)a;
+      d.q = (float)(a * m);
+      d.lse_h = (float)(lse_h * c);
       d.b = (float)b;
-      d.lse_h = (float)lse_h;
-      d.lse = (float)lse;
+      d.lse_b = d.lse = b != 0.0 ? (float)(lse * c) : 0.0f;
+      d.A = (float)ea;
+      d.L = (float)(l * c);
       d.B = (float)b;
-      d.q = d.A = (float)(a * m);
-      d.L = d.lse_h;
-      if (tail) {
-        d.A = lse_r > -INFINITY ? (float)(a * (m * exp(lse_r - lse_h) - rest)) : 0.0f;
-        d.L = lse_r > -INFINITY ? (float)lse_r : 0.0f;
-      }
-      if (A.targets == nullptr) {
+      if (b != 0.0 && !two) {                  // one exponential for both
+        d.A = (float)(ea + b * exp(l - lse));
         d.B = 0.0f;
-        d.lse = 0.0f;
-      } else if (!two) {   // one exponential for both
-        if (!tail) {
-          d.A = (float)(a * m + b);
-        } else if (lse_r > -INFINITY) {
-          d.A = (float)(a * (m * exp(lse_r - lse_h) - rest) + b * exp(lse_r - lse));
-        }
-        d.B = 0.0f;
+      } else if (b != 0.0 && square) {
+        d.B = (float)(b * exp(2.0 * l - lse));
       }
-      d.bad = bad;
-      if (bad) d.A = NAN;
+      d.bad = kp.bad;
+      if (kp.bad) d.A = NAN;
       if (lane == 0) sh.row = d;
     }
   }
@@ -408,65 +528,89 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
     __syncthreads();
     const DistillRow d = sh.row;
     // wave 0: what the kept columns and the target get (from logits read before any store: dz may be z)
-    constexpr int kMine = (kMaxTop + 1 + 63) / 64;
-    int to[kMine];
-    float val[kMine];
+    constexpr int kMine = kMaxTop / 64;
+    int to[kMine + 1];
+    float val[kMine + 1];
     if (w == 0) {
-      const int n = K + (A.targets != nullptr ? 1 : 0);
+      auto column = [&](float zv) {
+        float g = d.A * exp2_hw(fmaf(zv, ch, -d.L));
+        if (d.B != 0.0f) {
+          const float e = square ? exp2_hw(fmaf(zv, ch, -d.L)) : 0.0f;
+          g += d.B * (square ? e * e : exp2_hw(fmaf(zv, kLog2ef, -d.lse)));
+        }
+        return g;
+      };
+      bool met = false;
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
         const int j = lane + 64 * i;
-        to[i] = -1;
-        if (j >= n || d.bad) continue;
-        const int id = j < K ? sh.id[j] : (int)target;
-        if (id < 0) continue;
-        bool first = true, kept = j < K;
-        double sum = 0.0;
-        for (int e = 0; e < K; ++e)
-          if (sh.id[e] == id) {
-            first &= e >= j;
-            kept = true;
-            sum += sh.p[e];
-          }
-        if (!first) continue;
-        const float zv = j < K ? sh.zj[j] : sh.zt;
+        to[i] = j < K && !d.bad ? sh.id[j] : -1;
+        if (to[i] < 0) continue;
+        const float zv = sh.zj[j];
         float g;
-        if (tail && kept) {
-          g = d.q * exp_hw(fmaf(zv, ih, -d.lse_h));
-          if (d.b != 0.0f) g += d.b * exp_hw(zv - d.lse);
+        if (tail) {
+          g = d.q * exp2_hw(fmaf(zv, ch, -d.lse_h));
+          if (d.b != 0.0f) g += d.b * exp2_hw(fmaf(zv, kLog2ef, -d.lse_b));
         } else {
-          g = d.A * exp_hw(fmaf(zv, ih, -d.L));
-          if (d.B != 0.0f) g += d.B * exp_hw(zv - d.lse);
+          g = column(zv);
         }
-        g -= d.a * (float)sum;
-        if (A.targets != nullptr && id == (int)target) g -= d.b;
-        to[i] = id;
+        g -= d.a * (float)sh.p[j];
+        if (A.targets != nullptr && to[i] == (int)target) {
+          g -= d.b;
+          met = true;
+        }
         val[i] = g;
+      }
+      to[kMine] = -1;
+      if (__ballot(met) == 0 && lane == 0 && A.targets != nullptr && !d.bad) {
+        to[kMine] = (int)target;
+        val[kMine] = column(sh.zt) - d.b;
       }
     }
     const bool vec = (uintptr_t)(dz + head) % 16 == 0;
+    auto grads = [&](const Oct<T>& y, float (&g)[8]) {
+      float v[8];
+      y.get(v);
+      if (d.B == 0.0f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = d.A * exp2_hw(fmaf(v[i], ch, -d.L));
+      } else if (square) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float e = exp2_hw(fmaf(v[i], ch, -d.L));
+          g[i] = e * fmaf(d.B, e, d.A);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          g[i] = fmaf(d.B, exp2_hw(fmaf(v[i], kLog2ef, -d.lse)), d.A * exp2_hw(fmaf(v[i], ch, -d.L)));
+      }
+    };
     for (int tile = 0; tile < tiles; ++tile) {
       if (tiles > 1 && (MODE == kDisBoth || tile > 0)) load(tile);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int o = (tile * U + u) * TPB + tid, v0 = 8 * o - shift;
-        if (o >= octs) continue;
-        float v[8], g[8];
-        x[u].get(v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = d.A * exp_hw(fmaf(v[i], ih, -d.L));
-        if (d.B != 0.0f) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) g[i] = fmaf(d.B, exp_hw(v[i] - d.lse), g[i]);
+        const uint32_t o = (uint32_t)((tile * U + u) * TPB + tid);
+        x[u].hide();
+        if ((int)o < o1 - o0) {
+          float g[8];
+          grads(x[u], g);
+          T* to_o = (T*)((char*)dzo + o * (uint32_t)(8 * sizeof(T)));
+          if (vec) st_oct<T, true>(to_o, 8, g);
+          else st_some(to_o, 0, 8, g);
         }
-        if (vec && v0 >= 0 && v0 + 8 <= V) st_oct<T, true>(dz + v0, 8, g);
-        else st_some(dz + v0, max(0, -v0), min(8, V - v0), g);
+        __builtin_amdgcn_sched_barrier(0);
       }
+    }
+    if (edge) {
+      float g[8];
+      grads(xe, g);
+      st_some(dz + e0, e_lo, e_hi, g);
     }
     __syncthreads();   // the kept columns' and the target's values replace the others
     if (w == 0) {
 #pragma unroll
-      for (int i = 0; i < kMine; ++i)
+      for (int i = 0; i <= kMine; ++i)
         if (to[i] >= 0) io<T>::st(dz + to[i], val[i]);
     }
   }
@@ -474,28 +618,32 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
 
 namespace {
 
-template <typename T, int TPB, int U>
-hipError_t launch_rows(const gdn_distill_t& s, DistillArgs a, int mode, hipStream_t stream) {
+template <typename T, int TPB, int U, int MODE>
+hipError_t launch_row(const gdn_distill_t& s, DistillArgs a, hipStream_t stream) {
   // the bitmap only where sums are formed beside a rest
   const size_t lds = sizeof(DistillShared) +
-                     (a.teacher_lse != nullptr && mode != kDisBwd ? ((size_t)(a.V + 14) / 8 + 3) / 4 * 4 : 0);
-  auto go = [&](auto kern, PerDeviceOnce& once) {
-    constexpr size_t most = sizeof(DistillShared) + ((size_t)kMaxVocab + 14) / 8 + 4;
-    static_assert(most <= 160 * 1024, "LDS budget exceeded");
-    hipError_t e = set_dyn_lds_once(once, (const void*)kern, most);
-    if (e != hipSuccess) return e;
-    for (int64_t r0 = 0; r0 < s.rows; r0 += max_blocks(TPB)) {
-      a.row0 = r0;
-      const int64_t n = s.rows - r0 < max_blocks(TPB) ? s.rows - r0 : max_blocks(TPB);
-      hipLaunchKernelGGL(kern, dim3((unsigned)n), dim3(TPB), lds, stream, a);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    return hipSuccess;
-  };
-  static PerDeviceOnce once[3];
-  if (mode == kDisFwd) return go(distill_kernel<T, TPB, U, kDisFwd>, once[0]);
-  if (mode == kDisBwd) return go(distill_kernel<T, TPB, U, kDisBwd>, once[1]);
-  return go(distill_kernel<T, TPB, U, kDisBoth>, once[2]);
+                     (a.teacher_lse != nullptr && MODE != kDisBwd ? ((size_t)(a.V + 14) / 8 + 3) / 4 * 4 : 0);
+  constexpr size_t most = sizeof(DistillShared) + ((size_t)kMaxVocab + 14) / 8 + 4;
+  static_assert(most <= 160 * 1024, "LDS budget exceeded");
+  auto kern = distill_kernel<T, TPB, U, MODE>;
+  static PerDeviceOnce once;
+  hipError_t e = set_dyn_lds_once(once, (const void*)kern, most);
+  if (e != hipSuccess) return e;
+  for (int64_t r0 = 0; r0 < s.rows; r0 += max_blocks(TPB)) {
+    a.row0 = r0;
+    const int64_t n = s.rows - r0 < max_blocks(TPB) ? s.rows - r0 : max_blocks(TPB);
+    hipLaunchKernelGGL(kern, dim3((unsigned)n), dim3(TPB), lds, stream, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <typename T, int TPB, int U>
+hipError_t launch_rows(const gdn_distill_t& s, const DistillArgs& a, int mode, hipStream_t stream) {
+  if (mode == kDisFwd) return launch_row<T, TPB, U, kDisFwd>(s, a, stream);
+  if (mode == kDisBwd) return launch_row<T, TPB, U, kDisBwd>(s, a, stream);
+  if constexpr (TPB < 1024) return launch_row<T, TPB, U, kDisBoth>(s, a, stream);
+  return hipErrorNotSupported;
 }
 
 }  // namespace
@@ -510,16 +658,25 @@ hipError_t launch_distill(const gdn_distill_t& s, const void* logits, const int3
   a.stride = s.row_stride; a.d_stride = s.d_row_stride; a.ignore = s.ignore_index;
   a.V = s.vocab; a.K = s.topk;
   a.h = s.temperature; a.kd = s.kd_weight; a.ce = s.ce_weight;
+  // Threads a row and octets a thread.  One direction: four octets on the way, many workgroups a compute unit.  Both:
+  // the row in registers, whatever of it fits.
   const int octs = s.vocab / 8 + 2;
   if (s.dtype == GDN_BF16) {
     if (octs <= 64 * 4) return launch_rows<uint16_t, 64, 4>(s, a, mode, stream);
     if (octs <= 256 * 4) return launch_rows<uint16_t, 256, 4>(s, a, mode, stream);
-    if (octs <= 256 * 16) return launch_rows<uint16_t, 256, 16>(s, a, mode, stream);
-    return launch_rows<uint16_t, 1024, 16>(s, a, mode, stream);
+    if (mode == kDisBoth)
+      return octs <= 256 * 16 ? launch_row<uint16_t, 256, 16, kDisBoth>(s, a, stream)
+                              : launch_row<uint16_t, 1024, 16, kDisBoth>(s, a, stream);
+    return octs <= 8192 ? launch_rows<uint16_t, 256, 4>(s, a, mode, stream)
+                        : launch_rows<uint16_t, 1024, 4>(s, a, mode, stream);
   }
   if (octs <= 64 * 4) return launch_rows<float, 64, 4>(s, a, mode, stream);
-  if (octs <= 256 * 8) return launch_rows<float, 256, 8>(s, a, mode, stream);
-  return launch_rows<float, 1024, 8>(s, a, mode, stream);
+  if (octs <= 256 * 4) return launch_rows<float, 256, 4>(s, a, mode, stream);
+  if (mode == kDisBoth)
+    return octs <= 256 * 8 ? launch_row<float, 256, 8, kDisBoth>(s, a, stream)
+                           : launch_row<float, 1024, 8, kDisBoth>(s, a, stream);
+  return octs <= 8192 ? launch_rows<float, 256, 4>(s, a, mode, stream)
+                      : launch_rows<float, 1024, 4>(s, a, mode, stream);
 }
 
 }  // namespace gdn

@@ -232,30 +232,6 @@ struct LinRows {
   }
 };
 
-// Inclusive prefix sum of fp64 over the lanes of a wave by DPP moves (the
-// steps of wave_prefix_sum), and a lane's value in every lane.
-template <int kCtrl, int kRowMask>
-__device__ __forceinline__ double dpp_add_f64(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, kCtrl, kRowMask, 0xF, false);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), kCtrl, kRowMask, 0xF, false);
-  return v + __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
-}
-__device__ __forceinline__ double wave_prefix_f64(double v) {
-  v = dpp_add_f64<0x111, 0xF>(v);
-  v = dpp_add_f64<0x112, 0xF>(v);
-  v = dpp_add_f64<0x114, 0xF>(v);
-  v = dpp_add_f64<0x118, 0xF>(v);
-  v = dpp_add_f64<0x142, 0xA>(v);
-  return dpp_add_f64<0x143, 0xC>(v);
-}
-__device__ __forceinline__ double last_lane(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
-  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
-}
-
 // A sum of log decays in base 2 as its nearest whole number and the rest, and
 // 2^(n + f): decays are off by a few 2^-24 however strong they are.  (e^x as
 // 2^x of a rounded x log2(e), or by expf compiled with contraction, is off by
