@@ -815,20 +815,20 @@ def _distill_args(logits, ids, top, teacher_lse, targets, temperature, kd_weight
         raise ValueError("top is required")
     specs = [("ids", ids, torch.int32, None), ("top", top, torch.float32, (R, K)),
              ("teacher_lse", teacher_lse, torch.float32, (R,)), ("targets", targets, torch.int64, (R,)), *more]
-    d_stride = 0
-    if out is not None:
-        if out is True:
-            out, d_stride = logits.new_empty(R, V), V
-        else:
-            d_stride = _matrix(out, "out")[2]
-            if out.dtype != logits.dtype or out.shape != logits.shape:
-                raise ValueError(f"out must be {logits.dtype} of shape {tuple(logits.shape)}, got {out.dtype} of "
-                                 f"shape {tuple(out.shape)}")
-    at = _args(("logits", logits[:1, :1], None, None), *specs,
-               ("out", None if out is None else out[:1, :1], None, None))
-    shape = GdnDistill(R, V, K, _DT[logits.dtype], float(temperature), float(kd_weight), float(ce_weight),
-                       int(ignore_index), stride, d_stride)
-    return ctypes.byref(shape), at[:-1], out
+    d_stride = V
+    if isinstance(out, torch.Tensor):
+        d_stride = _matrix(out, "out")[2]
+        if out.dtype is not logits.dtype or out.shape != logits.shape:
+            raise ValueError(f"out must be {logits.dtype} of shape {tuple(logits.shape)}, got {out.dtype} of "
+                             f"shape {tuple(out.shape)}")
+        specs.append(("out", out if out.is_contiguous() else out[:1, :1], None, None))
+    at = _args(("logits", logits if logits.is_contiguous() else logits[:1, :1], None, None), *specs)
+    if out is True:
+        out = logits.new_empty(R, V)
+    elif out is not None:
+        at.pop()
+    shape = GdnDistill(R, V, K, _DT[logits.dtype], temperature, kd_weight, ce_weight, ignore_index, stride, d_stride)
+    return ctypes.byref(shape), at, out
 
 
 def distill_fwd(logits, ids, top, *, teacher_lse=None, targets=None, temperature=1.0, kd_weight=1.0, ce_weight=0.0,
