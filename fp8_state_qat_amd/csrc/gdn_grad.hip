@@ -33,7 +33,7 @@ GradLayout grad_layout(const gdn_shape_t& s, bool given) {
   l.chunks = (s.total_tokens + kChunk - 1) / kChunk + s.n_seqs;
   l.items = l.chunks * s.n_heads;
   const size_t rec = s.io_dtype == GDN_BF16 ? GradRec<EngBF16>::kBytes : GradRec<EngF32>::kBytes;
-  const size_t states = (size_t)l.items * grad_state_bytes(s.dv, s.dk);
+  const size_t states = (size_t)l.items * s.dv * s.dk * 4;
   l.offs = kStatusBytes;
   l.rec = l.offs + pad256((size_t)(s.n_seqs + 2) * 4);
   l.R = l.rec + pad256((size_t)l.items * rec);
@@ -90,8 +90,8 @@ hipError_t launch_chunk_grad(const gdn_shape_t& s, const void* q, const void* k,
   a.n_kept = n_states;
   a.d_fin = d_final_state;
   a.rec = w + l.rec;
-  a.S = states == nullptr ? w + l.S : nullptr;
-  a.R = w + l.R;
+  a.S = states == nullptr ? reinterpret_cast<float*>(w + l.S) : nullptr;
+  a.R = reinterpret_cast<float*>(w + l.R);
   a.dq = dq; a.dk = dk; a.d_v = d_v;
   a.d_beta = d_beta; a.dg = dg; a.d_init = d_initial_state;
   a.N = s.n_seqs; a.H = s.n_heads; a.dv = s.dv;

@@ -43,8 +43,8 @@ struct GradArgs {
   int64_t n_kept;      // its entries
   const float* d_fin;  // gradient of the last states, or null
   char* rec;           // records (GradRec), one for each (chunk, head)
-  char* S;             // states entering every (chunk, head) (null with kept), see grad_state_bytes
-  char* R;             // gradients of the states after every (chunk, head)
+  float* S;            // states entering every (chunk, head), as kept (null with kept)
+  float* R;            // gradients of the states after every (chunk, head)
   void *dq, *dk, *d_v;
   float *d_beta, *dg, *d_init;
   int N, H, dv;
@@ -57,11 +57,12 @@ __host__ __device__ constexpr bool plane_pair(int i, int j, int planes) { return
 // Record of a (chunk, head): the lower-triangular M and P as their ten 16 x 16
 // blocks (row tile, column tile), each row-major, so that one copy gives rows
 // and, by transpose reads, columns; then the gates.  bf16 inputs: three bf16
-// planes of M, two of P; fp32 inputs: fp32.
+// planes (with two of P beta's and the gates' gradients were off by 4e-6, with
+// three by 5e-7); fp32 inputs: fp32.
 template <class Eng>
 struct GradRec {
   static constexpr bool kBF = Eng::kSplit;
-  static constexpr int kMPlanes = kBF ? 3 : 1, kPPlanes = kBF ? 2 : 1;
+  static constexpr int kMPlanes = kBF ? 3 : 1, kPPlanes = kMPlanes;
   static constexpr int kBlock = 256 * (int)sizeof(typename Eng::E);
   static constexpr int kPlane = 10 * kBlock;
   static constexpr int oP = kMPlanes * kPlane;
@@ -81,14 +82,9 @@ struct GradGates {
   int n[kChunk];       // G log2(e) = n + f
   float f[kChunk];
   float g[kChunk];     // the log-gates
-  float pad[kChunk];
+  float zero[kChunk];  // 1 where beta is 0, whose place 2^-60 takes in beta
 };
 static_assert(sizeof(GradGates) == 2048, "the record's gates");
-
-// Bytes of a stored state: bf16 inputs keep it as two bf16 planes [dv][dk], 16
-// significant bits, which is what the gradients' products take of it; fp32
-// inputs as fp32.
-__host__ __device__ constexpr int64_t grad_state_bytes(int dv, int dk) { return (int64_t)dv * dk * 4; }
 
 // True where the call computes nothing: index arrays out of contract, or
 // fewer states than chunks.
@@ -116,13 +112,21 @@ __device__ __forceinline__ GradPlace grad_place(const GradArgs& a, int j) {
   return p;
 }
 
+// Element (row, col) of a record's block, in units of four elements swizzled so
+// that reads of rows (16 of them, one unit a lane) and of columns meet no bank
+// twice.
+template <class Eng>
+__device__ __forceinline__ int tri_at(int row, int col) {
+  const int u = (col >> 2) ^ (Eng::kSplit ? (row >> 3) << 1 : row >> 2);
+  return 16 * row + 4 * u + (col & 3);
+}
 // Rows of a record's blocks as a fragment: row 16 ti + ln, columns kperm of
 // k-block kb; blocks above the diagonal are zero.
 template <class Eng>
 __device__ __forceinline__ typename Eng::Fr tri_rows(const char* plane, int ti, int kb, int ln, int gq) {
   using E = typename Eng::E;
   constexpr int kBlock = GradRec<Eng>::kBlock;
-  const char* p = plane + (16 * ln + 4 * gq) * sizeof(E);
+  const char* p = plane + tri_at<Eng>(ln, 4 * gq) * sizeof(E);
   const E* a = (const E*)(p + tri_block(ti, 2 * kb) * kBlock);
   if (2 * kb + 1 <= ti) return Eng::ld2(a, (const E*)(p + tri_block(ti, 2 * kb + 1) * kBlock));
   if constexpr (Eng::kSplit) {
@@ -140,14 +144,14 @@ __device__ __forceinline__ typename Eng::Fr tri_cols(const char* plane, int si, 
   constexpr int kBlock = GradRec<Eng>::kBlock;
   const bool first = 2 * kb >= si;
   if constexpr (Eng::kSplit) {
-    const char* p = plane + (16 * (4 * gq + (ln >> 2)) + 4 * (ln & 3)) * 2;
+    const char* p = plane + tri_at<Eng>(4 * gq + (ln >> 2), 4 * (ln & 3)) * 2;
     uint2 u = make_uint2(0, 0);
     if (first) u = lds_read_tr16(p + tri_block(2 * kb, si) * kBlock);
     const uint2 v = lds_read_tr16(p + tri_block(2 * kb + 1, si) * kBlock);
     return __builtin_bit_cast(bf16x8, make_uint4(u.x, u.y, v.x, v.y));
   } else {
     Frag8 r;
-    const E* p = (const E*)plane + 64 * gq + ln;
+    const E* p = (const E*)plane + tri_at<Eng>(4 * gq, ln);   // rows 4 gq + j share a swizzle
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       r.v[j] = first ? p[tri_block(2 * kb, si) * 256 + 16 * j] : 0.0f;

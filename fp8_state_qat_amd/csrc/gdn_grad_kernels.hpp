@@ -41,12 +41,13 @@ __device__ __forceinline__ void grad_gates(GradGates& s, float g, float beta, in
   const float eg = lin_pow(x.n, x.f), ec = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(eg), 63));
   s.eg[ln] = ln < nv ? eg : 0.0f;
   s.el[ln] = ln < nv ? lin_pow(C - G) : 0.0f;
-  s.beta[ln] = beta;
+  // beta's gradient is a quotient by it: 0 goes as 2^-60 (rows past the end stay 0)
+  s.beta[ln] = ln < nv && fabsf(beta) < 0x1p-60f ? copysignf(0x1p-60f, beta) : beta;
   s.ec[ln] = ec;
   s.n[ln] = x.n;
   s.f[ln] = x.f;
   s.g[ln] = g;
-  s.pad[ln] = 0.0f;
+  s.zero[ln] = beta == 0.0f ? 1.0f : 0.0f;
 }
 
 // Four values into bf16 planes (or fp32), plane i at p + i * stride.
@@ -128,7 +129,7 @@ __global__ __launch_bounds__(kThreads) void grad_prep_kernel(GradArgs a) {
       vp[i] = s <= r && r < nv ? d * cq[i] : 0.0f;   // rows past the chunk's end are zero
     }
     *reinterpret_cast<float4*>(sA + r * kL64 + 16 * S + 4 * gq) = make_float4(va[0], va[1], va[2], va[3]);
-    put4<Eng, Rec::kPPlanes>(rec + Rec::oP + tri_block(R, S) * Rec::kBlock + (16 * ln + 4 * gq) * (int)sizeof(E),
+    put4<Eng, Rec::kPPlanes>(rec + Rec::oP + tri_block(R, S) * Rec::kBlock + tri_at<Eng>(ln, 4 * gq) * (int)sizeof(E),
                              Rec::kPlane, vp);
   }
   __syncthreads();
@@ -138,7 +139,7 @@ __global__ __launch_bounds__(kThreads) void grad_prep_kernel(GradArgs a) {
     const int R = blk < 1 ? 0 : blk < 3 ? 1 : blk < 6 ? 2 : 3, S = blk - R * (R + 1) / 2;
     const float4 x = *reinterpret_cast<const float4*>(sX + (16 * R + r) * kL64 + 16 * S + c);
     const float x4[4] = {x.x, x.y, x.z, x.w};
-    put4<Eng, Rec::kMPlanes>(rec + blk * Rec::kBlock + (16 * r + c) * (int)sizeof(E), Rec::kPlane, x4);
+    put4<Eng, Rec::kMPlanes>(rec + blk * Rec::kBlock + tri_at<Eng>(r, c) * (int)sizeof(E), Rec::kPlane, x4);
   }
 }
 
@@ -212,25 +213,21 @@ struct GradWalk {
     if (w == 3) lds_load16(rec + Rec::oG, (uint32_t)(threadIdx.x & 63) * 16, buf + Ls::oG);
   }
 
-  // the state's planes of k-block p, its columns against 32 channels; the
-  // first two are what the gradients' kernel reads
+  // the state's planes of k-block p: 32 channels
   __device__ __forceinline__ void planes(int p, Fr (&f)[P]) const {
     const float x[8] = {X[2 * p][0], X[2 * p][1], X[2 * p][2], X[2 * p][3],
                         X[2 * p + 1][0], X[2 * p + 1][1], X[2 * p + 1][2], X[2 * p + 1][3]};
     split_planes<Eng, P>(x, f);
   }
-  __device__ __forceinline__ void dump(char* slot, int p, const Fr (&f)[P]) const {
-    const int el = (64 * vt + 16 * w + ln) * DK + 32 * p + 8 * gq;
-    if constexpr (Eng::kSplit) {
-      const int64_t plane = (int64_t)a.dv * DK * 2;
-      *reinterpret_cast<uint4*>(slot + 2 * el) = __builtin_bit_cast(uint4, f[0]);
-      *reinterpret_cast<uint4*>(slot + plane + 2 * el) = __builtin_bit_cast(uint4, f[1]);
-    } else {
-      Eng::st((E*)slot + el, f[0]);
-    }
+  // the state for the gradients' kernel (past the caches, the half lines of each store would go to memory by
+  // themselves: 835 MB for 530 in the training batch)
+  __device__ __forceinline__ void dump(float* slot, int p) const {
+#pragma unroll
+    for (int tr = 2 * p; tr < 2 * p + 2; ++tr)
+      *reinterpret_cast<f32x4*>(slot + at(tr)) = X[tr];
   }
   // acc = K X
-  __device__ __forceinline__ void against_k(const char* sK, char* slot, f32x4 (&acc)[4]) const {
+  __device__ __forceinline__ void against_k(const char* sK, float* slot, f32x4 (&acc)[4]) const {
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) acc[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -239,7 +236,7 @@ struct GradWalk {
 #pragma unroll
       for (int rt = 0; rt < 4; ++rt) kf[rt] = TK::template row8<Eng>(sK, 16 * rt + ln, 32 * p + 8 * gq);
       planes(p, xf);
-      dump(slot, p, xf);
+      dump(slot, p);
 #pragma unroll
       for (int i = 0; i < P; ++i)
 #pragma unroll
@@ -274,7 +271,7 @@ struct GradWalk {
     }
   }
 
-  __device__ __forceinline__ void forward(const char* buf, char* slot) {
+  __device__ __forceinline__ void forward(const char* buf, float* slot) {
     const char* sM = buf + Ls::oM;
     const GradGates& g = *reinterpret_cast<const GradGates*>(buf + Ls::oG);
     f32x4 acc[4];
@@ -319,7 +316,7 @@ struct GradWalk {
     update(buf, xf);
   }
 
-  __device__ __forceinline__ void backward(const char* buf, char* slot) {
+  __device__ __forceinline__ void backward(const char* buf, float* slot) {
     const char* sM = buf + Ls::oM;
     const char* sP = buf + Ls::oP;
     const GradGates& g = *reinterpret_cast<const GradGates*>(buf + Ls::oG);
@@ -418,7 +415,7 @@ struct GradWalk {
       wait_vmem();
       __syncthreads();   // the chunk's rows are there; the other buffer is free
       if (Ls::kBufs == 2 && it + 1 < nch) ask_chunk(it + 1);
-      char* slot = (kRev ? a.R : a.S) + ((int64_t)(chunk0 + chunk(it)) * a.H + h) * grad_state_bytes(a.dv, DK);
+      float* slot = (kRev ? a.R : a.S) + ((int64_t)(chunk0 + chunk(it)) * a.H + h) * a.dv * DK;
       if constexpr (kRev) backward(buf, slot);
       else forward(buf, slot);
       if (Ls::kBufs == 1 && it + 1 < nch) {
@@ -452,53 +449,313 @@ __global__ __launch_bounds__(kThreads, 1) void grad_scan_kernel(GradArgs a, int 
 }
 
 // ---------------------------------------------------------------------------
-// The gradients of a (chunk, head): eight waves, the value columns in tiles of
-// TV.  For a tile, waves 0 .. TV / 16 - 1 form E and the next TV / 16 form Y, 16
-// columns each, as the chains do; then all waves contract over the tile's
-// columns: rows of S and R against dO, Y, E (a wave: 32 channels, 64 / (8 /
-// (DK / 32)) tokens) and the triangle's pairs dO E^T, Y E^T (a wave: one or two
-// 16 x 16 tiles).  After the last tile the pairs become W, N and the sums that
-// beta's and the gates' gradients take.
+// The gradients of a (chunk, head), the value columns in tiles of TV = 16 G, by
+// 2 G waves.  First wave c < G does a forward chain's step for 16 columns, from S
+// as it is stored (fp32) and with the chains' precision: E, and o, the forward's
+// output; wave G + c the backward one's: Y.  What beta's and the gates' gradients
+// are made of falls off here, as sums over the columns: with p_r = dO_r.o_r -
+// Y_r.V_r,
+//     db_r = Y_r.E_r / b_r           dg_t = <dS, S> - sum_(r<t) p_r
+// (S_t = a_t S_(t-1) + b_t e_t k_t^T leaves <dS_t, S_t> = <dS_(t+1), S_(t+1)> +
+// p_t; dS is the gradient of S itself, the chunk before's R), so that errors of dg
+// are relative to the sums of its own chunk.  (beta = 0 goes as 2^-60: Y is a
+// multiple of it.)
+//
+// Then E and Y, and HV columns at a time S and R, go into LDS as two bf16 planes,
+// and all waves contract over them: S and R against dO, Y, E (a wave: 32 channels and
+// its share of the tokens), and the triangle's pairs dO E^T, Y E^T; last the
+// pairs become W and N, and W, N and their transposes meet K and Q.
+//
+// The split over the directions leaves a wave half of the registers that both
+// would take: sixteen waves a compute unit at 128 columns.
 // ---------------------------------------------------------------------------
-constexpr int kGradThreads = 512;
-
-template <class Eng, int DK>
+template <class Eng, int DK, int G>
 struct GradChunkLds {
   using E = typename Eng::E;
+  using Rec = GradRec<Eng>;
+  static constexpr int NW = 2 * G;
   static constexpr int SP = Eng::kSplit ? 2 : 1;                    // planes of S, R, E, Y, W, N
-  static constexpr int TV = Eng::kSplit || DK == 64 ? 64 : 32;      // value columns of a tile
+  static constexpr int TV = 16 * G, HV = Eng::kSplit && G == 4 ? 64 : 32;   // columns of a tile and of a step's
   static constexpr int kTile = kChunk * DK * (int)sizeof(E);
   static constexpr int kVTile = kChunk * TV * (int)sizeof(E);
-  static constexpr int kSTile = TV * DK * (int)sizeof(E);
-  static constexpr int kTri = GradRec<Eng>::kPlane;
+  static constexpr int kSTile = HV * DK * (int)sizeof(E);
+  static constexpr int kTri = Rec::kPlane;
   static constexpr int oQ = kTile;
   static constexpr int oO = 2 * kTile;
-  static constexpr int oE = oO + kVTile;                            // its first plane takes V's place
+  static constexpr int oG = oO + kVTile;
+  static constexpr int oSum = oG + (int)sizeof(GradGates);          // [3][G][64] floats, [G] doubles
+  static constexpr int base = oSum + 3 * G * kChunk * 4 + (G * 8 + 15) / 16 * 16;
+  // first: V, M, P, and E in fp32 from the forward waves to the backward ones
+  static constexpr int oV = base;
+  static constexpr int oM = oV + kVTile;
+  static constexpr int oP = oM + Rec::oP;
+  static constexpr int oX = oM + Rec::oG;
+  static constexpr int end1 = oX + G * 16 * 64 * 4;
+  // then: E and Y, S and R of a step's columns
+  static constexpr int oE = base;
   static constexpr int oY = oE + SP * kVTile;
   static constexpr int oS = oY + SP * kVTile;
   static constexpr int oR = oS + SP * kSTile;
-  static constexpr int oM = oR + SP * kSTile;
-  static constexpr int oP = oM + SP * kTri;
-  static constexpr int oG = oP + GradRec<Eng>::kPPlanes * kTri;
-  static constexpr int bytes = oG + (int)sizeof(GradGates);
-  // after the last tile: W and N in place of S and R, sums in place of dO
-  static constexpr int oW = oS;
+  static constexpr int end2 = oR + SP * kSTile;
+  // last: W, N
+  static constexpr int oW = base;
   static constexpr int oN = oW + SP * kTri;
-  static_assert(oN + SP * kTri <= oM, "W and N fit over S and R");
-  static constexpr int oSum = oO;
-  static_assert((3 * 4 + 3 * 4) * kChunk * 4 + 64 <= kVTile, "the sums fit over dO");
+  static constexpr int end3 = oN + SP * kTri;
+  static constexpr int bytes = end1 > end2 ? (end1 > end3 ? end1 : end3) : (end2 > end3 ? end2 : end3);
   static_assert(bytes <= 160 * 1024, "LDS budget exceeded");
+  static_assert(base % 16 == 0 && TV % HV == 0, "16-byte aligned, whole steps");
 };
 
-template <class Eng, int DK>
-__global__ __launch_bounds__(kGradThreads, 2) void grad_chunk_kernel(GradArgs a) {
+// The lane, as a value that the compiler does not know from before: addresses
+// formed from it are not those of an earlier part kept in registers.
+__device__ __forceinline__ int fresh_lane() {
+  int l = threadIdx.x;
+  asm volatile("" : "+v"(l));
+  return l & 63;
+}
+
+// The first part of a wave: its columns' state, E or Y, and sums.
+template <class Eng, int DK, int G>
+struct GradStep {
   using E = typename Eng::E;
   using Fr = typename Eng::Fr;
-  using Ls = GradChunkLds<Eng, DK>;
+  using Ls = GradChunkLds<Eng, DK, G>;
   using Rec = GradRec<Eng>;
-  constexpr int SP = Ls::SP, TV = Ls::TV, NKB = DK / 32;
   using TK = LinTile<E, DK>;
-  using TT = LinTile<E, TV>;
+  using TO = LinTile<E, Ls::TV>;
+  static constexpr int P = Rec::kMPlanes, NKB = DK / 32, NT = DK / 16;
+
+  char* smem;
+  int c, ln, gq;        // columns 16 c .. of the tile
+  f32x4 st[NT];         // S or R: tile tr holds channels dkmap(16 tr + 4 gq ..) of column 16 c + ln
+  f32x4 x[4];           // E or Y: tokens 16 rt + 4 gq + i of it
+
+  __device__ __forceinline__ const GradGates& gates() const {
+    return *reinterpret_cast<const GradGates*>(smem + Ls::oG);
+  }
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int tr = 0; tr < NT; ++tr) {
+      st[tr] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (p != nullptr)
+        st[tr] = *reinterpret_cast<const f32x4*>(p + (int64_t)(16 * c + ln) * DK + 8 * gq + 32 * (tr / 2) + 4 * (tr & 1));
+    }
+  }
+  // this lane's part of <state at p, st>
+  __device__ __forceinline__ float dot(const float* p) const {
+    float z = 0.0f;
+#pragma unroll
+    for (int tr = 0; tr < NT; ++tr) {
+      const f32x4 y = *reinterpret_cast<const f32x4*>(p + (int64_t)(16 * c + ln) * DK + 8 * gq + 32 * (tr / 2) + 4 * (tr & 1));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z = fmaf(st[tr][i], y[i], z);
+    }
+    return z;
+  }
+  // K (and Q) against the planes of the state
+  template <bool kQ>
+  __device__ __forceinline__ void against(f32x4 (&ck)[4], f32x4 (&cq)[4]) const {
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) {
+      ck[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if constexpr (kQ) cq[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+#pragma unroll
+    for (int p = 0; p < NKB; ++p) {
+      const float x8[8] = {st[2 * p][0], st[2 * p][1], st[2 * p][2], st[2 * p][3],
+                           st[2 * p + 1][0], st[2 * p + 1][1], st[2 * p + 1][2], st[2 * p + 1][3]};
+      Fr sf[P], f[4];
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) f[rt] = TK::template row8<Eng>(smem, 16 * rt + ln, 32 * p + 8 * gq);
+      split_planes<Eng, P>(x8, sf);
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) Eng::mma(ck[rt], f[rt], sf[i]);
+      if constexpr (kQ) {
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) f[rt] = TK::template row8<Eng>(smem + Ls::oQ, 16 * rt + ln, 32 * p + 8 * gq);
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+#pragma unroll
+          for (int rt = 0; rt < 4; ++rt) Eng::mma(cq[rt], f[rt], sf[i]);
+      }
+      __builtin_amdgcn_sched_barrier(0);   // reads in flight stay within the registers
+    }
+  }
+  __device__ __forceinline__ Fr column(int o, int kb) const {
+    return TO::template cols8<Eng, 4>(smem + o, kb, 16 * c, ln, gq);
+  }
+  // acc += A b for the record's lower-triangular A at o, or its transpose
+  template <bool kT, int PA>
+  __device__ __forceinline__ void tri(f32x4 (&acc)[4], int o, const Fr (&b)[2][P]) const {
+#pragma unroll
+    for (int i = 0; i < PA; ++i)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int rt = kT ? 0 : 2 * kb; rt < (kT ? 2 * kb + 2 : 4); ++rt) {
+          const char* p = smem + o + i * Rec::kPlane;
+          const Fr a = kT ? tri_cols<Eng>(p, rt, kb, ln, gq) : tri_rows<Eng>(p, rt, kb, ln, gq);
+#pragma unroll
+          for (int k = 0; plane_pair(i, k, P); ++k) Eng::mma(acc[rt], a, b[kb][k]);
+        }
+  }
+  static __device__ __forceinline__ void zero(f32x4 (&a)[4]) {
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) a[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  // sums over the columns of v (this lane's tokens) into LDS, [G][64]
+  __device__ __forceinline__ void sums(float* to, int rt, int i, float v) const {
+    v = group_sum<16>(v);
+    if (ln == 0) to[kChunk * c + 16 * rt + 4 * gq + i] = v;
+  }
+
+  // E = M (V - e^G K S^T) into x and, in fp32, for the backward wave; sums of dO.o
+  __device__ __forceinline__ void forward(float* sum_o) {
+    const GradGates& g = gates();
+    f32x4 ks[4], o[4];
+    against<true>(ks, o);
+    Fr f[2][P];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      float v[8];
+      frag_values(column(Ls::oV, kb), v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int rt = 2 * kb + (k >> 2), i = k & 3;
+        const float eg = g.eg[16 * rt + 4 * gq + i];
+        v[k] = fmaf(-eg, ks[rt][i], v[k]);
+        o[rt][i] *= eg;
+      }
+      split_planes<Eng, P>(v, f[kb]);
+    }
+    zero(x);
+    tri<false, P>(x, Ls::oM, f);
+    __builtin_amdgcn_sched_barrier(0);
+    float* ex = reinterpret_cast<float*>(smem + Ls::oX) + c * 1024;
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) reinterpret_cast<f32x4*>(ex)[64 * rt + 16 * gq + ln] = x[rt];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      float u[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int rt = 2 * kb + (k >> 2), i = k & 3;
+        u[k] = g.beta[16 * rt + 4 * gq + i] * x[rt][i];
+      }
+      split_planes<Eng, P>(u, f[kb]);
+    }
+    tri<false, Rec::kPPlanes>(o, Ls::oP, f);
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      float d[8];
+      frag_values(column(Ls::oO, kb), d);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sums(sum_o, 2 * kb + (k >> 2), k & 3, d[k] * o[2 * kb + (k >> 2)][k & 3]);
+    }
+  }
+  // Y = M^T b (P^T dO + e^(G_C - G) K R^T) into x; sums of Y.V
+  __device__ __forceinline__ void backward(float* sum_v) {
+    const GradGates& g = gates();
+    f32x4 kr[4], f1[4];
+    against<false>(kr, kr);
+    zero(f1);
+    Fr f[2][P];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      const Fr of = column(Ls::oO, kb);
+#pragma unroll
+      for (int i = 0; i < Rec::kPPlanes; ++i)
+#pragma unroll
+        for (int rt = 0; rt < 2 * kb + 2; ++rt)
+          Eng::mma(f1[rt], tri_cols<Eng>(smem + Ls::oP + i * Rec::kPlane, rt, kb, ln, gq), of);
+    }
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      float z[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int rt = 2 * kb + (k >> 2), i = k & 3, t = 16 * rt + 4 * gq + i;
+        z[k] = g.beta[t] * fmaf(g.el[t], kr[rt][i], f1[rt][i]);
+      }
+      split_planes<Eng, P>(z, f[kb]);
+    }
+    zero(x);
+    tri<true, P>(x, Ls::oM, f);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      float v[8];
+      frag_values(column(Ls::oV, kb), v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sums(sum_v, 2 * kb + (k >> 2), k & 3, v[k] * x[2 * kb + (k >> 2)][k & 3]);
+    }
+  }
+  // sums of Y.E, E from the forward wave
+  __device__ __forceinline__ void meet(float* sum_b) const {
+    const float* ex = reinterpret_cast<const float*>(smem + Ls::oX) + c * 1024;
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) {
+      const f32x4 e = reinterpret_cast<const f32x4*>(ex)[64 * rt + 16 * gq + ln];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sums(sum_b, rt, i, e[i] * x[rt][i]);
+    }
+  }
+  // the state's planes, row `row` of a step's tile
+  __device__ __forceinline__ void put_state(char* to, int row) const {
+#pragma unroll
+    for (int p = 0; p < NKB; ++p) {
+      const int col = 32 * p + 8 * gq;
+      const float x8[8] = {st[2 * p][0], st[2 * p][1], st[2 * p][2], st[2 * p][3],
+                           st[2 * p + 1][0], st[2 * p + 1][1], st[2 * p + 1][2], st[2 * p + 1][3]};
+      if constexpr (Eng::kSplit) {
+        Fr f[2];
+        Eng::split(x8, f[0], f[1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          Eng::st((E*)(to + i * Ls::kSTile + row * DK * 2 + 16 * lin_unit<TK::kUnits>(row, col / 8)), f[i]);
+      } else {
+        *(float4*)(to + row * DK * 4 + 16 * lin_unit<TK::kUnits>(row, col / 4)) = make_float4(x8[0], x8[1], x8[2], x8[3]);
+        *(float4*)(to + row * DK * 4 + 16 * lin_unit<TK::kUnits>(row, col / 4 + 1)) = make_float4(x8[4], x8[5], x8[6], x8[7]);
+      }
+    }
+  }
+  // x's planes, this lane's column of the token rows
+  __device__ __forceinline__ void put_x(char* to) const {
+    constexpr int kPer = 16 / (int)sizeof(E);
+    const int col = 16 * c + ln, in = (col % kPer) * (int)sizeof(E);
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        const int ra = 16 * rt + 4 * gq + i, rb = ra + 1;
+        char* a = to + ra * Ls::TV * (int)sizeof(E) + 16 * lin_unit<TO::kUnits>(ra, col / kPer) + in;
+        char* b = to + rb * Ls::TV * (int)sizeof(E) + 16 * lin_unit<TO::kUnits>(rb, col / kPer) + in;
+        if constexpr (Eng::kSplit) {
+          uint32_t hi, lo;
+          split_bf16x2(x[rt][i], x[rt][i + 1], hi, lo);
+          *(uint16_t*)a = (uint16_t)hi;
+          *(uint16_t*)b = (uint16_t)(hi >> 16);
+          *(uint16_t*)(a + Ls::kVTile) = (uint16_t)lo;
+          *(uint16_t*)(b + Ls::kVTile) = (uint16_t)(lo >> 16);
+        } else {
+          *(float*)a = x[rt][i];
+          *(float*)b = x[rt][i + 1];
+        }
+      }
+  }
+};
+
+template <class Eng, int DK, int G, bool kOne>
+__global__ __launch_bounds__(128 * G, G / 2) void grad_chunk_kernel(GradArgs a) {
+  using E = typename Eng::E;
+  using Fr = typename Eng::Fr;
+  using Ls = GradChunkLds<Eng, DK, G>;
+  using Rec = GradRec<Eng>;
+  constexpr int NW = Ls::NW, SP = Ls::SP, TV = Ls::TV, HV = Ls::HV, T = 64 * NW;
+  using TK = LinTile<E, DK>;
+  using TO = LinTile<E, TV>;
   extern __shared__ __align__(16) char smem[];
   if (grad_refused(a)) return;
   const int j = blockIdx.x / a.H, h = blockIdx.x % a.H;
@@ -506,430 +763,287 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_chunk_kernel(GradArgs a)
   const GradPlace pl = grad_place(a, j);
   const int nv = pl.nv, H = a.H, dv = a.dv;
   const uint32_t lds0 = lds_base_u32(smem);
-  const int tid = threadIdx.x, w = uniform(tid >> 6), l64 = tid & 63, ln = l64 & 15, gq = l64 >> 4;
+  const int tid = threadIdx.x, w = uniform(tid >> 6);
+  const bool rev = w >= G;
   const char* sK = smem;
   const char* sQ = smem + Ls::oQ;
-  char* sO = smem + Ls::oO;
-  char* sE = smem + Ls::oE;
-  char* sY = smem + Ls::oY;
-  char* sS = smem + Ls::oS;
-  char* sR = smem + Ls::oR;
-  const char* sM = smem + Ls::oM;
-  const char* sP = smem + Ls::oP;
+  const char* sO = smem + Ls::oO;
   const GradGates& g = *reinterpret_cast<const GradGates*>(smem + Ls::oG);
+  float* sum_o = reinterpret_cast<float*>(smem + Ls::oSum);         // [G][64] dO.o
+  float* sum_v = sum_o + G * kChunk;                                // Y.V
+  float* sum_b = sum_v + G * kChunk;                                // Y.E
+  double* sum_z = reinterpret_cast<double*>(sum_b + G * kChunk);    // [G] <dS, S>
 
   const int64_t row0 = (int64_t)pl.t0 * H + h;
-  const int64_t ch = (int64_t)j * H + h;
+  const int64_t ch = (int64_t)j * H + h, state = (int64_t)dv * DK;
+  const char* rec = a.rec + ch * Rec::kBytes;
   {
-    using RK = LinRows<E, DK, kGradThreads>;
+    using RK = LinRows<E, DK, T>;
     RK::ask(lds0, (const E*)a.k + row0 * DK, H * DK, nv);
     RK::ask(lds0 + Ls::oQ, (const E*)a.q + row0 * DK, H * DK, nv);
-    const char* rec = a.rec + ch * Rec::kBytes;
-    ask_bytes<8>(lds0 + Ls::oM, rec, SP * Ls::kTri);
-    ask_bytes<8>(lds0 + Ls::oP, rec + Rec::oP, Rec::kBytes - Rec::oP);   // P and the gates
+    ask_bytes<NW>(lds0 + Ls::oG, rec + Rec::oG, Rec::kGates);
   }
-  // the entering state: stored planes, or fp32 (kept, or the initial state)
-  const float* s32 = nullptr;
-  if (a.kept != nullptr) {
-    if (pl.c > 0) s32 = a.kept + (ch - H) * dv * DK;
-    else if (a.init != nullptr) s32 = a.init + ((int64_t)pl.n * H + h) * dv * DK;
-  }
-  const char* slotS = a.kept == nullptr ? a.S + ch * grad_state_bytes(dv, DK) : nullptr;
-  const char* slotR = a.R + ch * grad_state_bytes(dv, DK);
+  // the entering state (kept, the initial one, or the chain's), its gradient, and the leaving one's
+  const int64_t seq = ((int64_t)pl.n * H + h) * state;
+  const float* ps = a.kept == nullptr ? a.S + ch * state
+                    : pl.c > 0 ? a.kept + (ch - H) * state : a.init == nullptr ? nullptr : a.init + seq;
+  const float* pd = pl.c > 0 ? a.R + (ch - H) * state : a.d_init + seq;
+  const float* pr = a.R + ch * state;
 
   // this wave's share of the contractions: channels 32 wc .. 32 wc + 31, token tiles TPW tg ..
-  constexpr int CP = DK / 32, TG = 8 / CP, TPW = 4 / TG;
+  constexpr int CP = DK / 32, TG = NW / CP < 4 ? NW / CP : 4, TPW = 4 / TG;
+  constexpr bool kIdle = TG * CP < NW;   // more waves than shares (dk = 64 and 128 columns)
   const int wc = w % CP, tg = w / CP;
+  const bool share = !kIdle || tg < TG;
   f32x4 aq[TPW][2], ax[TPW][2], as[TPW][2];
+  // and of the triangle's ten tiles: w, w + NW, ..
+  constexpr int NTri = (10 + NW - 1) / NW;
+  f32x4 pe[NTri], ye[NTri];
+  auto clear = [&] {
 #pragma unroll
-  for (int t = 0; t < TPW; ++t)
+    for (int t = 0; t < TPW; ++t)
 #pragma unroll
-    for (int m = 0; m < 2; ++m) aq[t][m] = ax[t][m] = as[t][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  // and of the triangle's tiles: w, and 8 + w where there is one
-  const int n_tri = w < 2 ? 2 : 1;
-  f32x4 pe[2], ye[2];
+      for (int m = 0; m < 2; ++m) aq[t][m] = ax[t][m] = as[t][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int i = 0; i < 2; ++i) pe[i] = ye[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  auto tri_at = [](int job, int& T, int& S) {
-    T = job < 1 ? 0 : job < 3 ? 1 : job < 6 ? 2 : 3;
-    S = job - T * (T + 1) / 2;
+    for (int i = 0; i < NTri; ++i) pe[i] = ye[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  if constexpr (!kOne) clear();
+  auto tri_of = [](int job, int& Tt, int& St) {
+    Tt = job < 1 ? 0 : job < 3 ? 1 : job < 6 ? 2 : 3;
+    St = job - Tt * (Tt + 1) / 2;
   };
   double z = 0.0;
+  float keep_p = 0.0f, keep_b = 0.0f;   // sums of the earlier tiles (wave c: its columns'; lane: token)
 
-  for (int v0 = 0; v0 < dv; v0 += TV) {
-    if (v0 > 0) __syncthreads();   // the last tile is consumed
+  for (int v0 = 0; kOne ? v0 == 0 : v0 < dv; v0 += TV) {
+    f32x4 st[DK / 16];
+    const int c = rev ? w - G : w;
+    char* sE = smem + Ls::oE;
+    char* sY = smem + Ls::oY;
     {
-      using RV = LinRows<E, TV, kGradThreads>;
-      static_assert(TV == 64 || TV == 32, "tile rows");
-      RV::ask(lds0 + Ls::oE, (const E*)a.v + row0 * dv + v0, H * dv, nv);
-      RV::ask(lds0 + Ls::oO, (const E*)a.d_o + row0 * dv + v0, H * dv, nv);
-      // TV rows of a state plane
-      auto ask_state = [&](uint32_t to, const char* from) {
-        constexpr int kUnits = DK * (int)sizeof(E) / 16, kAll = TV * kUnits;
-        static_assert(kAll % kGradThreads == 0, "whole steps");
-#pragma unroll
-        for (int i = 0; i < kAll / kGradThreads; ++i) {
-          const int idx = tid + kGradThreads * i, row = idx / kUnits, u = lin_unit<kUnits>(row, idx % kUnits);
-          lds_load16(from, (uint32_t)(row * DK * (int)sizeof(E) + 16 * u), to + 16 * 64 * w + 16 * kGradThreads * i);
-        }
-      };
-      const int64_t plane = (int64_t)dv * DK * 2;
-#pragma unroll
-      for (int i = 0; i < SP; ++i) {
-        ask_state(lds0 + Ls::oR + i * Ls::kSTile, slotR + i * plane + (int64_t)v0 * DK * sizeof(E));
-        if (slotS != nullptr)
-          ask_state(lds0 + Ls::oS + i * Ls::kSTile, slotS + i * plane + (int64_t)v0 * DK * sizeof(E));
+      const int l64 = fresh_lane();
+      GradStep<Eng, DK, G> step;
+      step.smem = smem;
+      step.c = c;
+      step.ln = l64 & 15;
+      step.gq = l64 >> 4;
+      step.load(rev ? pr + (int64_t)v0 * DK : ps == nullptr ? nullptr : ps + (int64_t)v0 * DK);
+      if (v0 > 0) __syncthreads();   // the last tile is consumed
+      {
+        using RV = LinRows<E, TV, T>;
+        RV::ask(lds0 + Ls::oO, (const E*)a.d_o + row0 * dv + v0, H * dv, nv);
+        RV::ask(lds0 + Ls::oV, (const E*)a.v + row0 * dv + v0, H * dv, nv);
+        ask_bytes<NW>(lds0 + Ls::oM, rec, Rec::oG);
       }
-      if (slotS == nullptr) {
-        for (int i = tid; i < TV * DK / 8; i += kGradThreads) {
-          const int row = i / (DK / 8), c = 8 * (i % (DK / 8));
-          float x[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-          if (s32 != nullptr) {
-            const float4* p = reinterpret_cast<const float4*>(s32 + (int64_t)(v0 + row) * DK + c);
-            const float4 u = p[0], y = p[1];
-            x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w; x[4] = y.x; x[5] = y.y; x[6] = y.z; x[7] = y.w;
-          }
-          if constexpr (Eng::kSplit) {
-            Fr f[2];
-            split_planes<Eng, 2>(x, f);
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              Eng::st((E*)(sS + k * Ls::kSTile + row * DK * 2 + 16 * lin_unit<TK::kUnits>(row, c / 8)), f[k]);
-          } else {
-            float4* p0 = (float4*)(sS + row * DK * 4 + 16 * lin_unit<TK::kUnits>(row, c / 4));
-            float4* p1 = (float4*)(sS + row * DK * 4 + 16 * lin_unit<TK::kUnits>(row, c / 4 + 1));
-            *p0 = make_float4(x[0], x[1], x[2], x[3]);
-            *p1 = make_float4(x[4], x[5], x[6], x[7]);
-          }
+      if (!rev && ps != nullptr) z += (double)step.dot(pd + (int64_t)v0 * DK);
+      wait_vmem();
+      __syncthreads();
+      if (rev) step.backward(sum_v);
+      else step.forward(sum_o);
+      __syncthreads();   // E has come
+      if (rev) step.meet(sum_b);
+      __syncthreads();
+      if constexpr (!kOne) {
+        if (!rev && v0 + TV < dv) {   // the next tile's sums take the place
+          keep_p += sum_o[kChunk * w + l64] - sum_v[kChunk * w + l64];
+          keep_b += sum_b[kChunk * w + l64];
         }
       }
+      step.put_x(rev ? sY : sE);
+#pragma unroll
+      for (int tr = 0; tr < DK / 16; ++tr) st[tr] = step.st[tr];
     }
-    wait_vmem();
-    __syncthreads();
+    if constexpr (kOne) clear();   // not kept through the first part
 
-    if (w < 2 * (TV / 16)) {
-      const bool rev = w >= TV / 16;
-      const int cw = rev ? w - TV / 16 : w;         // columns 16 cw ..
-      const char* st = rev ? sR : sS;
-      f32x4 acc[4], r4[4];
 #pragma unroll
-      for (int rt = 0; rt < 4; ++rt) acc[rt] = r4[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int h0 = 0; h0 < TV; h0 += HV) {
+      const int l64 = fresh_lane(), ln = l64 & 15, gq = l64 >> 4;
+      char* sS = smem + Ls::oS;
+      char* sR = smem + Ls::oR;
+      if (h0 > 0) __syncthreads();   // the last columns are consumed
+      if (16 * c >= h0 && 16 * c < h0 + HV) {
+        GradStep<Eng, DK, G> step;
+        step.c = c;
+        step.ln = ln;
+        step.gq = gq;
 #pragma unroll
-      for (int p = 0; p < NKB; ++p) {
-        Fr kf[4];
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) kf[rt] = TK::template row8<Eng>(sK, 16 * rt + ln, 32 * p + 8 * gq);
-#pragma unroll
-        for (int i = 0; i < SP; ++i) {
-          const Fr sf = TK::template row8<Eng>(st + i * Ls::kSTile, 16 * cw + ln, 32 * p + 8 * gq);
-#pragma unroll
-          for (int rt = 0; rt < 4; ++rt) Eng::mma(acc[rt], kf[rt], sf);
-        }
+        for (int tr = 0; tr < DK / 16; ++tr) step.st[tr] = st[tr];
+        step.put_state(rev ? sR : sS, 16 * c - h0 + ln);
       }
-      Fr xf[2][SP];
-      const float* wt = rev ? g.el : g.eg;
-      Fr vf[2];
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) vf[kb] = TT::template cols8<Eng, 4>(rev ? sO : sE, kb, 16 * cw, ln, gq);
-      if (rev) {
-#pragma unroll
-        for (int i = 0; i < Rec::kPPlanes; ++i)
-#pragma unroll
-          for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int rt = 0; rt < 2 * kb + 2; ++rt)
-              Eng::mma(r4[rt], tri_cols<Eng>(sP + i * Rec::kPlane, rt, kb, ln, gq), vf[kb]);
-      }
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        float x[8];
-        frag_values(vf[kb], x);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int t = 32 * kb + 4 * gq + (k & 3) + 16 * (k >> 2);
-          const float s = acc[2 * kb + (k >> 2)][k & 3];
-          x[k] = rev ? g.beta[t] * fmaf(wt[t], s, r4[2 * kb + (k >> 2)][k & 3]) : fmaf(-wt[t], s, x[k]);
-        }
-        split_planes<Eng, SP>(x, xf[kb]);
-      }
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt) r4[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (rev) {
-#pragma unroll
-        for (int i = 0; i < SP; ++i)
-#pragma unroll
-          for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int rt = 0; rt < 2 * kb + 2; ++rt) {
-              const Fr mf = tri_cols<Eng>(sM + i * Ls::kTri, rt, kb, ln, gq);
-#pragma unroll
-              for (int k = 0; plane_pair(i, k, SP); ++k) Eng::mma(r4[rt], mf, xf[kb][k]);
-            }
-      } else {
-#pragma unroll
-        for (int i = 0; i < SP; ++i)
-#pragma unroll
-          for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int rt = 2 * kb; rt < 4; ++rt) {
-              const Fr mf = tri_rows<Eng>(sM + i * Ls::kTri, rt, kb, ln, gq);
-#pragma unroll
-              for (int k = 0; plane_pair(i, k, SP); ++k) Eng::mma(r4[rt], mf, xf[kb][k]);
-            }
-      }
-      // into the tile of E (over V, whose columns are this wave's too) or Y, row-major
-      char* to = rev ? sY : sE;
-      const int col = 16 * cw + ln;
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          const int ra = 16 * rt + 4 * gq + i, rb = ra + 1;
-          constexpr int kPer = 16 / (int)sizeof(E);
-          const int oa = ra * TV * (int)sizeof(E) + 16 * lin_unit<TT::kUnits>(ra, col / kPer) + (col % kPer) * (int)sizeof(E);
-          const int ob = rb * TV * (int)sizeof(E) + 16 * lin_unit<TT::kUnits>(rb, col / kPer) + (col % kPer) * (int)sizeof(E);
-          if constexpr (Eng::kSplit) {
-            uint32_t hi, lo;
-            split_bf16x2(r4[rt][i], r4[rt][i + 1], hi, lo);
-            *(uint16_t*)(to + oa) = (uint16_t)hi;
-            *(uint16_t*)(to + ob) = (uint16_t)(hi >> 16);
-            *(uint16_t*)(to + Ls::kVTile + oa) = (uint16_t)lo;
-            *(uint16_t*)(to + Ls::kVTile + ob) = (uint16_t)(lo >> 16);
-          } else {
-            *(float*)(to + oa) = r4[rt][i];
-            *(float*)(to + ob) = r4[rt][i + 1];
+      __syncthreads();
+
+      if (h0 == 0) {   // d_v: Y's first plane is Y rounded to bf16
+        for (int i = tid; i < kChunk * TO::kUnits; i += T) {
+          const int row = i / TO::kUnits, u = i % TO::kUnits;
+          if (row < nv) {
+            uint4 x = *reinterpret_cast<const uint4*>(sY + row * TV * (int)sizeof(E) + 16 * lin_unit<TO::kUnits>(row, u));
+            if (g.zero[row] != 0.0f) x = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>((E*)a.d_v + (row0 + (int64_t)row * H) * dv + v0 + u * (16 / (int)sizeof(E))) = x;
           }
         }
-    }
-    __syncthreads();
-
-    // d_v: Y's first plane is Y rounded to bf16
-    {
-      constexpr int kUnits = TT::kUnits;
-      for (int i = tid; i < kChunk * kUnits; i += kGradThreads) {
-        const int row = i / kUnits, u = i % kUnits;
-        if (row < nv)
-          *reinterpret_cast<uint4*>((E*)a.d_v + (row0 + (int64_t)row * H) * dv + v0 + u * (16 / (int)sizeof(E))) =
-              *reinterpret_cast<const uint4*>(sY + row * TV * (int)sizeof(E) + 16 * lin_unit<kUnits>(row, u));
+      }
+      // S against dO and Y, R against E (the barriers for the scheduler keep reads in flight within the registers)
+      if (share) {
+#pragma unroll
+        for (int kb = 0; kb < HV / 32; ++kb) {
+          auto column = [&](const char* p, Fr (&f)[2][SP]) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+              for (int i = 0; i < SP; ++i)
+                f[m][i] = TK::template cols8<Eng, 8>(p + i * Ls::kSTile, kb, 32 * wc + 4 * m, ln, gq);
+          };
+          const int hb = h0 / 32 + kb;
+          Fr sf[2][SP];
+          column(sS, sf);
+#pragma unroll
+          for (int t = 0; t < TPW; ++t) {
+            const int row = 16 * (TPW * tg + t) + ln;
+            const Fr of = row_kperm<Eng, TO>(sO, row, hb, gq);
+            Fr yf[SP];
+#pragma unroll
+            for (int i = 0; i < SP; ++i) yf[i] = row_kperm<Eng, TO>(sY + i * Ls::kVTile, row, hb, gq);
+#pragma unroll
+            for (int i = 0; i < SP; ++i)
+#pragma unroll
+              for (int m = 0; m < 2; ++m) Eng::mma(aq[t][m], sf[m][i], of);
+#pragma unroll
+            for (int i = 0; i < SP; ++i)
+#pragma unroll
+              for (int k = 0; plane_pair(i, k, SP); ++k)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) Eng::mma(ax[t][m], sf[m][i], yf[k]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          column(sR, sf);
+#pragma unroll
+          for (int t = 0; t < TPW; ++t) {
+            const int row = 16 * (TPW * tg + t) + ln;
+            Fr ef[SP];
+#pragma unroll
+            for (int i = 0; i < SP; ++i) ef[i] = row_kperm<Eng, TO>(sE + i * Ls::kVTile, row, hb, gq);
+#pragma unroll
+            for (int i = 0; i < SP; ++i)
+#pragma unroll
+              for (int k = 0; plane_pair(i, k, SP); ++k)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) Eng::mma(as[t][m], sf[m][i], ef[k]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      // the triangle: lane holds token t = 16 T + ln, s = 16 S + 4 gq + i
+#pragma unroll
+      for (int i = 0; i < NTri; ++i) {
+        if (w + NW * i >= 10) break;
+        int Tt, St;
+        tri_of(w + NW * i, Tt, St);
+#pragma unroll
+        for (int p = 0; p < HV / 32; ++p) {
+          const int col = h0 + 32 * p + 8 * gq;
+          const Fr of = TO::template row8<Eng>(sO, 16 * Tt + ln, col);
+          Fr ef[SP], yf[SP];
+#pragma unroll
+          for (int k = 0; k < SP; ++k) {
+            ef[k] = TO::template row8<Eng>(sE + k * Ls::kVTile, 16 * St + ln, col);
+            yf[k] = TO::template row8<Eng>(sY + k * Ls::kVTile, 16 * Tt + ln, col);
+          }
+#pragma unroll
+          for (int k = 0; k < SP; ++k) {
+            Eng::mma(pe[i], ef[k], of);
+#pragma unroll
+            for (int l = 0; plane_pair(k, l, SP); ++l) Eng::mma(ye[i], ef[k], yf[l]);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
-    // S and R against dO, Y and E
+  }
+  __syncthreads();   // the last columns are consumed
+
+  {
+    const int l64 = fresh_lane(), ln = l64 & 15, gq = l64 >> 4;
+    if (!rev) {
+      if constexpr (!kOne) {
+        sum_o[kChunk * w + l64] += keep_p;
+        sum_b[kChunk * w + l64] += keep_b;
+      }
+      z = last_lane(wave_prefix_f64(z));
+      if (l64 == 0) sum_z[w] = z;
+    }
+    // pairs
 #pragma unroll
-    for (int kb = 0; kb < TV / 32; ++kb) {
-      Fr sf[2][SP], rf[2][SP];
+    for (int i = 0; i < NTri; ++i) {
+      if (w + NW * i >= 10) break;
+      int Tt, St;
+      tri_of(w + NW * i, Tt, St);
+      const int t = 16 * Tt + ln, tn = g.n[t];
+      const float tf = g.f[t];
+      float wv[4], nn[4];
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int i = 0; i < SP; ++i) {
-          sf[m][i] = TK::template cols8<Eng, 8>(sS + i * Ls::kSTile, kb, 32 * wc + 4 * m, ln, gq);
-          rf[m][i] = TK::template cols8<Eng, 8>(sR + i * Ls::kSTile, kb, 32 * wc + 4 * m, ln, gq);
-        }
+      for (int k = 0; k < 4; ++k) {
+        const int s = 16 * St + 4 * gq + k;
+        const float d = s <= t && t < nv ? g.beta[s] * lin_pow(tn - g.n[s], tf - g.f[s]) : 0.0f;
+        wv[k] = d * pe[i][k];
+        nn[k] = s < t ? -d * ye[i][k] : 0.0f;
+      }
+      const int at = tri_block(Tt, St) * Rec::kBlock + tri_at<Eng>(ln, 4 * gq) * (int)sizeof(E);
+      put4<Eng, SP>(smem + Ls::oW + at, Ls::kTri, wv);
+      put4<Eng, SP>(smem + Ls::oN + at, Ls::kTri, nn);
+    }
+    if (share) {
 #pragma unroll
       for (int t = 0; t < TPW; ++t) {
-        const int row = 16 * (TPW * tg + t) + ln;
-        const Fr of = row_kperm<Eng, TT>(sO, row, kb, gq);
-        Fr yf[SP], ef[SP];
+        const int tok = 16 * (TPW * tg + t) + ln;
+        const float eg = g.eg[tok], bl = g.beta[tok] * g.el[tok];
 #pragma unroll
-        for (int i = 0; i < SP; ++i) {
-          yf[i] = row_kperm<Eng, TT>(sY + i * Ls::kVTile, row, kb, gq);
-          ef[i] = row_kperm<Eng, TT>(sE + i * Ls::kVTile, row, kb, gq);
-        }
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-#pragma unroll
-          for (int i = 0; i < SP; ++i) Eng::mma(aq[t][m], sf[m][i], of);
-#pragma unroll
-          for (int i = 0; i < SP; ++i)
-#pragma unroll
-            for (int k = 0; plane_pair(i, k, SP); ++k) {
-              Eng::mma(ax[t][m], sf[m][i], yf[k]);
-              Eng::mma(as[t][m], rf[m][i], ef[k]);
-            }
-        }
+          for (int r = 0; r < 4; ++r) {
+            aq[t][m][r] *= eg;
+            ax[t][m][r] = fmaf(bl, as[t][m][r], -eg * ax[t][m][r]);
+          }
       }
     }
-    // the triangle: lane holds token t = 16 T + ln, s = 16 S + 4 gq + i
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (i >= n_tri) break;
-      int T, S;
-      tri_at(i == 0 ? w : 8 + w, T, S);
-#pragma unroll
-      for (int p = 0; p < TV / 32; ++p) {
-        const Fr of = TT::template row8<Eng>(sO, 16 * T + ln, 32 * p + 8 * gq);
-        Fr ef[SP], yf[SP];
-#pragma unroll
-        for (int k = 0; k < SP; ++k) {
-          ef[k] = TT::template row8<Eng>(sE + k * Ls::kVTile, 16 * S + ln, 32 * p + 8 * gq);
-          yf[k] = TT::template row8<Eng>(sY + k * Ls::kVTile, 16 * T + ln, 32 * p + 8 * gq);
-        }
-#pragma unroll
-        for (int k = 0; k < SP; ++k) {
-          Eng::mma(pe[i], ef[k], of);
-#pragma unroll
-          for (int l = 0; plane_pair(k, l, SP); ++l) Eng::mma(ye[i], ef[k], yf[l]);
-        }
-      }
-    }
-    // <R, S>
-    for (int i = tid; i < TV * DK / 8; i += kGradThreads) {
-      float x[8], y[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = y[k] = 0.0f;
-#pragma unroll
-      for (int k = 0; k < SP; ++k) {
-        const int row = i / (DK / 8), c = 8 * (i % (DK / 8));
-        float p[8];
-        frag_values(TK::template row8<Eng>(sS + k * Ls::kSTile, row, c), p);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) x[q] += p[q];
-        frag_values(TK::template row8<Eng>(sR + k * Ls::kSTile, row, c), p);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) y[q] += p[q];
-      }
-      float d = 0.0f;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) d = fmaf(x[q], y[q], d);
-      z += (double)d;
-    }
-  }
-  __syncthreads();   // S, R, dO, E, Y are consumed
+    __syncthreads();
 
-  float* sum_q = reinterpret_cast<float*>(smem + Ls::oSum);   // [CP][64] q.dq, k.dk (entering), k.dk (leaving, without beta)
-  float* sum_x = sum_q + 4 * kChunk;
-  float* sum_s = sum_x + 4 * kChunk;
-  float* col_b = sum_s + 4 * kChunk;    // [4][64] by token tile: sums over t of P dO.E - B Y.E, t >= s
-  float* col_s = col_b + 4 * kChunk;    // the same for t > s
-  float* row_t = col_s + 4 * kChunk;    // [4][64] by s tile: sums over s of beta_s (..), s < t
-  double* sum_z = reinterpret_cast<double*>(row_t + 4 * kChunk);
-  z = last_lane(wave_prefix_f64(z));
-  if (l64 == 0) sum_z[w] = z;
-
-  // pairs
+    if (w == NW - 1) {
+      const int t = l64;
+      double p = 0.0, b = 0.0, zz = 0.0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (i >= n_tri) break;
-    int T, S;
-    tri_at(i == 0 ? w : 8 + w, T, S);
-    f32x4 ck = {0.0f, 0.0f, 0.0f, 0.0f}, cq = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int p = 0; p < NKB; ++p) {
-      const Fr kf = TK::template row8<Eng>(sK, 16 * S + ln, 32 * p + 8 * gq);
-      Eng::mma(ck, kf, TK::template row8<Eng>(sK, 16 * T + ln, 32 * p + 8 * gq));
-      Eng::mma(cq, kf, TK::template row8<Eng>(sQ, 16 * T + ln, 32 * p + 8 * gq));
-    }
-    const int t = 16 * T + ln, tn = g.n[t];
-    const float tf = g.f[t];
-    float wv[4], nvv[4], row = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int s = 16 * S + 4 * gq + k;
-      const bool low = s <= t && t < nv, strict = s < t && t < nv;
-      const float b = g.beta[s];
-      const float d = low ? lin_pow(tn - g.n[s], tf - g.f[s]) : 0.0f;
-      const float de = d * pe[i][k], dy = strict ? d * ye[i][k] : 0.0f;
-      wv[k] = b * de;
-      nvv[k] = -b * dy;
-      const float m1 = de * cq[k], m2 = dy * ck[k];
-      const float cs = strict ? m1 - m2 : 0.0f;
-      row = fmaf(b, cs, row);
-      const float all = group_sum<16>(m1 - m2), off = group_sum<16>(cs);
-      if (ln == 0) {
-        col_b[kChunk * T + s] = all;
-        col_s[kChunk * T + s] = off;
+      for (int i = 0; i < G; ++i) {
+        p += (double)sum_o[kChunk * i + t] - (double)sum_v[kChunk * i + t];
+        b += (double)sum_b[kChunk * i + t];
+        zz += sum_z[i];
+      }
+      double d = zz - (wave_prefix_f64(p) - p);
+      if (g.g[t] < -104.0f) d = 0.0;   // e^-104 rounds to 0: nothing lies across the token
+      if (t < nv) {
+        a.d_beta[row0 + (int64_t)t * H] = (float)(b / (double)g.beta[t]);
+        a.dg[row0 + (int64_t)t * H] = (float)d;
       }
     }
-    row += __shfl_xor(row, 16, 64);
-    row += __shfl_xor(row, 32, 64);
-    if (gq == 0) row_t[kChunk * S + t] = row;
-    const int at = tri_block(T, S) * Rec::kBlock + (16 * ln + 4 * gq) * (int)sizeof(E);
-    put4<Eng, SP>(smem + Ls::oW + at, Ls::kTri, wv);
-    put4<Eng, SP>(smem + Ls::oN + at, Ls::kTri, nvv);
+    if (!share) return;
   }
-  // state parts, their weights, and their products with q and k
-#pragma unroll
-  for (int t = 0; t < TPW; ++t) {
-    const int tok = 16 * (TPW * tg + t) + ln;
-    const float eg = g.eg[tok], el = g.el[tok], b = g.beta[tok];
-    float q[8], k[8];
-    frag_values(TK::template row8<Eng>(sQ, tok, 32 * wc + 8 * gq), q);
-    frag_values(TK::template row8<Eng>(sK, tok, 32 * wc + 8 * gq), k);
-    float dq = 0.0f, dx = 0.0f, ds = 0.0f;
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float q1 = eg * aq[t][m][r], x1 = -eg * ax[t][m][r], s1 = el * as[t][m][r];
-        dq = fmaf(q[4 * m + r], q1, dq);
-        dx = fmaf(k[4 * m + r], x1, dx);
-        ds = fmaf(k[4 * m + r], s1, ds);
-        aq[t][m][r] = q1;
-        ax[t][m][r] = fmaf(b, s1, x1);
-      }
-    dq += __shfl_xor(dq, 16, 64);
-    dq += __shfl_xor(dq, 32, 64);
-    dx += __shfl_xor(dx, 16, 64);
-    dx += __shfl_xor(dx, 32, 64);
-    ds += __shfl_xor(ds, 16, 64);
-    ds += __shfl_xor(ds, 32, 64);
-    if (gq == 0) {
-      sum_q[kChunk * wc + tok] = dq;
-      sum_x[kChunk * wc + tok] = dx;
-      sum_s[kChunk * wc + tok] = ds;
-    }
-  }
-  __syncthreads();
-
-  if (w == 0) {
-    const int t = l64;
-    double own = 0.0, out = 0.0, zz = 0.0;
-    float col = 0.0f, off = 0.0f;
-#pragma unroll
-    for (int i = 0; i < CP; ++i) {
-      own += (double)sum_q[kChunk * i + t] + (double)sum_x[kChunk * i + t];
-      out += (double)sum_s[kChunk * i + t];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i <= t >> 4) own += (double)row_t[kChunk * i + t];
-      if (i >= t >> 4) {
-        col += col_b[kChunk * i + t];
-        off += col_s[kChunk * i + t];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) zz += sum_z[i];
-    const double b = (double)g.beta[t];
-    own -= b * (double)off;
-    if (t >= nv) own = 0.0;
-    const double head = wave_prefix_f64(own);
-    double before = __shfl_up(wave_prefix_f64(b * out), 1, 64);   // without the token's own
-    if (t == 0) before = 0.0;
-    double d = (last_lane(head) - head + own) + before + zz * (double)g.ec[0];
-    if (g.g[t] < -104.0f) d = 0.0;   // e^-104 rounds to 0: nothing lies across the token
-    if (t < nv) {
-      a.d_beta[row0 + (int64_t)t * H] = col + (float)out;
-      a.dg[row0 + (int64_t)t * H] = (float)d;
-    }
-  }
-
   // dq += W K, dk += W^T Q + N K + N^T K; a lane: token 16 tile + ln, channels 32 wc + 8 gq ..
+  const int lz = fresh_lane(), lnz = lz & 15, gz = lz >> 4;
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb) {
     Fr kf[2], qf[2];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      kf[m] = TK::template cols8<Eng, 8>(sK, kb, 32 * wc + 4 * m, ln, gq);
-      qf[m] = TK::template cols8<Eng, 8>(sQ, kb, 32 * wc + 4 * m, ln, gq);
+      kf[m] = TK::template cols8<Eng, 8>(sK, kb, 32 * wc + 4 * m, lnz, gz);
+      qf[m] = TK::template cols8<Eng, 8>(sQ, kb, 32 * wc + 4 * m, lnz, gz);
     }
 #pragma unroll
     for (int t = 0; t < TPW; ++t) {
       const int tile = TPW * tg + t;
 #pragma unroll
       for (int i = 0; i < SP; ++i) {
+        const char* sW = smem + Ls::oW + i * Ls::kTri;
+        const char* sN = smem + Ls::oN + i * Ls::kTri;
         if (2 * kb <= tile) {
-          const Fr wf = tri_rows<Eng>(smem + Ls::oW + i * Ls::kTri, tile, kb, ln, gq);
-          const Fr nf = tri_rows<Eng>(smem + Ls::oN + i * Ls::kTri, tile, kb, ln, gq);
+          const Fr wf = tri_rows<Eng>(sW, tile, kb, lnz, gz), nf = tri_rows<Eng>(sN, tile, kb, lnz, gz);
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             Eng::mma(aq[t][m], kf[m], wf);
@@ -937,8 +1051,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_chunk_kernel(GradArgs a)
           }
         }
         if (2 * kb + 1 >= tile) {
-          const Fr wf = tri_cols<Eng>(smem + Ls::oW + i * Ls::kTri, tile, kb, ln, gq);
-          const Fr nf = tri_cols<Eng>(smem + Ls::oN + i * Ls::kTri, tile, kb, ln, gq);
+          const Fr wf = tri_cols<Eng>(sW, tile, kb, lnz, gz), nf = tri_cols<Eng>(sN, tile, kb, lnz, gz);
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             Eng::mma(ax[t][m], qf[m], wf);
@@ -946,13 +1059,14 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_chunk_kernel(GradArgs a)
           }
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 #pragma unroll
   for (int t = 0; t < TPW; ++t) {
-    const int tok = 16 * (TPW * tg + t) + ln;
+    const int tok = 16 * (TPW * tg + t) + lnz;
     if (tok >= nv) continue;
-    const int64_t at = (row0 + (int64_t)tok * H) * DK + 32 * wc + 8 * gq;
+    const int64_t at = (row0 + (int64_t)tok * H) * DK + 32 * wc + 8 * gz;
     const float q8[8] = {aq[t][0][0], aq[t][0][1], aq[t][0][2], aq[t][0][3],
                          aq[t][1][0], aq[t][1][1], aq[t][1][2], aq[t][1][3]};
     const float k8[8] = {ax[t][0][0], ax[t][0][1], ax[t][0][2], ax[t][0][3],
@@ -960,6 +1074,17 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_chunk_kernel(GradArgs a)
     Eng::st((E*)a.dq + at, Eng::round(q8));
     Eng::st((E*)a.dk + at, Eng::round(k8));
   }
+}
+
+template <class Eng, int DK, int G, bool kOne>
+hipError_t launch_grad_chunk(const GradArgs& a, int64_t items, hipStream_t stream) {
+  auto kern = grad_chunk_kernel<Eng, DK, G, kOne>;
+  constexpr size_t lds = GradChunkLds<Eng, DK, G>::bytes;
+  static PerDeviceOnce once;
+  hipError_t e = set_dyn_lds_once(once, (const void*)kern, lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3((unsigned)items), dim3(128 * G), lds, stream, a);
+  return hipGetLastError();
 }
 
 template <class Eng, int DK>
@@ -983,12 +1108,10 @@ hipError_t launch_grad(const gdn_shape_t& s, const GradArgs& a, int64_t items, h
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (items > 0) {
-    auto kern = grad_chunk_kernel<Eng, DK>;
-    constexpr size_t lds = GradChunkLds<Eng, DK>::bytes;
-    static PerDeviceOnce once;
-    if ((e = set_dyn_lds_once(once, (const void*)kern, lds)) != hipSuccess) return e;
-    hipLaunchKernelGGL(kern, dim3((unsigned)items), dim3(kGradThreads), lds, stream, a);
-    e = hipGetLastError();
+    // 128 value columns at once, where that is all of them; else (and fp32, whose tiles would not fit) 64 at a time
+    constexpr int kWide = Eng::kSplit ? 8 : 4;
+    if (s.dv == 16 * kWide) e = launch_grad_chunk<Eng, DK, kWide, true>(a, items, stream);
+    else e = launch_grad_chunk<Eng, DK, 4, false>(a, items, stream);
   } else {
     e = hipSuccess;
   }

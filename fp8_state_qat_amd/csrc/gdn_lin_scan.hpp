@@ -141,7 +141,8 @@ __device__ __forceinline__ LinSeg lin_find(const int32_t* __restrict__ cu, int N
 template <int U>
 __device__ __forceinline__ int lin_unit(int row, int u) {
   if constexpr (U >= 16) return u ^ (((row & 3) << 2) | ((row >> 2) & 3));
-  else return u ^ ((((row >> 1) & 1) << 2) | ((row >> 2) & 3));
+  else if constexpr (U >= 8) return u ^ ((((row >> 1) & 1) << 2) | ((row >> 2) & 3));
+  else return u ^ ((row >> 2) & 3);
 }
 
 __device__ __forceinline__ f32x4 ld4(const uint16_t* p) {
