@@ -4,7 +4,8 @@
 //
 // Workspace: the status word and the chunk offsets (as in gdn_chunk_fwd's),
 // one record for each (chunk, head), the gradients of the states after every
-// chunk, and without given states those entering it.  With the state's QDQ in
+// chunk, the tokens' errors and their gradients, and without given states those
+// entering every chunk.  With the state's QDQ in
 // the chunks and no given states, the forward runs again, its own code with
 // the boundary record, so that the gradients are taken at the very states it
 // had; its outputs, last states and workspace follow then.
@@ -15,7 +16,7 @@ namespace gdn {
 namespace {
 
 struct GradLayout {
-  size_t offs, rec, R, S, o, fin, fwd, bytes;
+  size_t offs, rec, R, E, Y, S, o, fin, fwd, bytes;
   int64_t chunks, items;
 };
 
@@ -37,7 +38,9 @@ GradLayout grad_layout(const gdn_shape_t& s, bool given) {
   l.offs = kStatusBytes;
   l.rec = l.offs + pad256((size_t)(s.n_seqs + 2) * 4);
   l.R = l.rec + pad256((size_t)l.items * rec);
-  l.S = l.R + states;
+  l.E = l.R + states;
+  l.Y = l.E + (size_t)l.items * s.dv * kChunk * 4;
+  l.S = l.Y + (size_t)l.items * s.dv * kChunk * 4;
   l.o = l.S + (given ? 0 : states);
   l.bytes = l.o;
   if (!given && (s.qdq_flags & GDN_QDQ_CHUNK)) {
@@ -92,6 +95,8 @@ hipError_t launch_chunk_grad(const gdn_shape_t& s, const void* q, const void* k,
   a.rec = w + l.rec;
   a.S = states == nullptr ? reinterpret_cast<float*>(w + l.S) : nullptr;
   a.R = reinterpret_cast<float*>(w + l.R);
+  a.E = reinterpret_cast<float*>(w + l.E);
+  a.Y = reinterpret_cast<float*>(w + l.Y);
   a.dq = dq; a.dk = dk; a.d_v = d_v;
   a.d_beta = d_beta; a.dg = dg; a.d_init = d_initial_state;
   a.N = s.n_seqs; a.H = s.n_heads; a.dv = s.dv;

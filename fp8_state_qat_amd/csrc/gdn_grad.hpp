@@ -45,6 +45,7 @@ struct GradArgs {
   char* rec;           // records (GradRec), one for each (chunk, head)
   float* S;            // states entering every (chunk, head), as kept (null with kept)
   float* R;            // gradients of the states after every (chunk, head)
+  float *E, *Y;        // [chunk][H][dv][64]: the tokens' errors, and their gradients (V's), transposed
   void *dq, *dk, *d_v;
   float *d_beta, *dg, *d_init;
   int N, H, dv;

@@ -188,17 +188,13 @@ struct GradWalk {
   __device__ __forceinline__ int at(int tr) const {
     return (64 * vt + 16 * w + ln) * DK + 32 * (tr / 2) + 8 * gq + 4 * (tr & 1);
   }
-  __device__ __forceinline__ void load(const float* p) {
+  // the state of entry i of p's
+  __device__ __forceinline__ void load(const float* p, int64_t i) {
 #pragma unroll
     for (int tr = 0; tr < NT; ++tr) {
       X[tr] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (p != nullptr) X[tr] = *reinterpret_cast<const f32x4*>(p + ((int64_t)n * a.H + h) * a.dv * DK + at(tr));
+      if (p != nullptr) X[tr] = *reinterpret_cast<const f32x4*>(p + (i * a.H + h) * a.dv * DK + at(tr));
     }
-  }
-  __device__ __forceinline__ void store(float* p) const {
-#pragma unroll
-    for (int tr = 0; tr < NT; ++tr)
-      *reinterpret_cast<f32x4*>(p + ((int64_t)n * a.H + h) * a.dv * DK + at(tr)) = X[tr];
   }
 
   __device__ __forceinline__ void ask(uint32_t buf, int j, int t0, int nv) const {
@@ -221,10 +217,16 @@ struct GradWalk {
   }
   // the state for the gradients' kernel (past the caches, the half lines of each store would go to memory by
   // themselves: 835 MB for 530 in the training batch)
-  __device__ __forceinline__ void dump(float* slot, int p) const {
+  __device__ __forceinline__ void dump(float* slot, int p0 = 0, int p1 = NKB) const {
 #pragma unroll
-    for (int tr = 2 * p; tr < 2 * p + 2; ++tr)
+    for (int tr = 2 * p0; tr < 2 * p1; ++tr)
       *reinterpret_cast<f32x4*>(slot + at(tr)) = X[tr];
+  }
+  // E or Y for the gradients' kernel, transposed: a token row for each value column
+  __device__ __forceinline__ void keep(float* to, const f32x4 (&x)[4]) const {
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt)
+      *reinterpret_cast<f32x4*>(to + (64 * vt + 16 * w + ln) * kChunk + 16 * rt + 4 * gq) = x[rt];
   }
   // acc = K X
   __device__ __forceinline__ void against_k(const char* sK, float* slot, f32x4 (&acc)[4]) const {
@@ -236,7 +238,7 @@ struct GradWalk {
 #pragma unroll
       for (int rt = 0; rt < 4; ++rt) kf[rt] = TK::template row8<Eng>(sK, 16 * rt + ln, 32 * p + 8 * gq);
       planes(p, xf);
-      dump(slot, p);
+      if (slot != nullptr) dump(slot, p, p + 1);
 #pragma unroll
       for (int i = 0; i < P; ++i)
 #pragma unroll
@@ -271,7 +273,8 @@ struct GradWalk {
     }
   }
 
-  __device__ __forceinline__ void forward(const char* buf, float* slot) {
+  // without a slot X is the state of this chunk alone
+  __device__ __forceinline__ void forward(const char* buf, float* slot, float* err) {
     const char* sM = buf + Ls::oM;
     const GradGates& g = *reinterpret_cast<const GradGates*>(buf + Ls::oG);
     f32x4 acc[4];
@@ -299,6 +302,8 @@ struct GradWalk {
 #pragma unroll
           for (int k = 0; plane_pair(i, k, P); ++k) Eng::mma(er[rt], mf, xf[kb][k]);
         }
+    keep(err, er);
+    if (slot == nullptr) return;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       float u[8], e[8];
@@ -316,7 +321,7 @@ struct GradWalk {
     update(buf, xf);
   }
 
-  __device__ __forceinline__ void backward(const char* buf, float* slot) {
+  __device__ __forceinline__ void backward(const char* buf, float* slot, float* dvs) {
     const char* sM = buf + Ls::oM;
     const char* sP = buf + Ls::oP;
     const GradGates& g = *reinterpret_cast<const GradGates*>(buf + Ls::oG);
@@ -357,6 +362,7 @@ struct GradWalk {
 #pragma unroll
           for (int k = 0; plane_pair(i, k, P); ++k) Eng::mma(y[rt], mf, zf[kb][k]);
         }
+    keep(dvs, y);
     const float ec = g.ec[0];
 #pragma unroll
     for (int tr = 0; tr < NT; ++tr)
@@ -403,7 +409,8 @@ struct GradWalk {
     const int L = a.seq_lens ? uniform(a.seq_lens[n]) : end - seg0;
     const int nch = (L + kChunk - 1) / kChunk, chunk0 = uniform(a.offs[n]);
     if (kRev && seg0 + L < end) clear_padding(seg0 + L, end);
-    load(kRev ? a.d_fin : a.init);
+    load(kRev ? a.d_fin : a.init, n);
+    const bool kept = !kRev && a.kept != nullptr;
     auto chunk = [&](int it) { return kRev ? nch - 1 - it : it; };
     auto ask_chunk = [&](int it) {
       const int c = chunk(it);
@@ -415,20 +422,25 @@ struct GradWalk {
       wait_vmem();
       __syncthreads();   // the chunk's rows are there; the other buffer is free
       if (Ls::kBufs == 2 && it + 1 < nch) ask_chunk(it + 1);
-      float* slot = (kRev ? a.R : a.S) + ((int64_t)(chunk0 + chunk(it)) * a.H + h) * a.dv * DK;
-      if constexpr (kRev) backward(buf, slot);
-      else forward(buf, slot);
+      const int64_t at = (int64_t)(chunk0 + chunk(it)) * a.H + h;
+      float* slot = (kRev ? a.R : a.S) + at * a.dv * DK;
+      if constexpr (kRev) {
+        backward(buf, slot, a.Y + at * a.dv * kChunk);
+      } else {
+        forward(buf, kept ? nullptr : slot, a.E + at * a.dv * kChunk);
+        if (kept) load(a.kept, chunk0 + it);
+      }
       if (Ls::kBufs == 1 && it + 1 < nch) {
         __syncthreads();
         ask_chunk(it + 1);
       }
     }
-    if constexpr (kRev) store(a.d_init);
+    if constexpr (kRev) dump(a.d_init + ((int64_t)n * a.H + h) * a.dv * DK);
   }
 };
 
-// Workgroups 0 .. n_rev - 1 walk backwards, the rest (none with kept states)
-// forwards.  Each direction's workgroups of an XCD (workgroup b runs on XCD b %
+// Workgroups 0 .. n_rev - 1 walk backwards, the rest forwards (with kept states
+// for E alone).  Each direction's workgroups of an XCD (workgroup b runs on XCD b %
 // 8) take neighbouring value tiles, which share K, Q and the records.
 template <class Eng, int DK>
 __global__ __launch_bounds__(kThreads, 1) void grad_scan_kernel(GradArgs a, int n_rev) {
@@ -449,62 +461,63 @@ __global__ __launch_bounds__(kThreads, 1) void grad_scan_kernel(GradArgs a, int 
 }
 
 // ---------------------------------------------------------------------------
-// The gradients of a (chunk, head), the value columns in tiles of TV = 16 G, by
-// 2 G waves.  First wave c < G does a forward chain's step for 16 columns, from S
-// as it is stored (fp32) and with the chains' precision: E, and o, the forward's
-// output; wave G + c the backward one's: Y.  What beta's and the gates' gradients
-// are made of falls off here, as sums over the columns: with p_r = dO_r.o_r -
-// Y_r.V_r,
+// The gradients of a (chunk, head) by four waves, 32 value columns at a time:
+// S and R against dO, Y and E, and the triangle's pairs dO E^T, Y E^T; last the
+// pairs become W and N, which meet K and Q with their transposes.  A wave has 32
+// channels of S and R, which come from memory as the A operands of its products
+// (a lane: two channels of eight columns), so that nothing but the tokens' rows
+// passes through LDS, and 2 workgroups a compute unit cover each other's waits.
+//
+// beta's and the gates' gradients are sums of the same products: with
+// p_r = dO_r.o_r - Y_r.V_r and O and V by their formulas,
 //     db_r = Y_r.E_r / b_r           dg_t = <dS, S> - sum_(r<t) p_r
+//     p_r = e^G q_r.(dO S)_r + sum_s W_rs q_r.k_s
+//           - e^G k_r.(Y S)_r + sum_s N_rs k_r.k_s - Y_r.E_r
+//     <dS, S> = e^(G_C) <R, S> + sum_r e^G (q_r.(dO S)_r - k_r.(Y S)_r)
 // (S_t = a_t S_(t-1) + b_t e_t k_t^T leaves <dS_t, S_t> = <dS_(t+1), S_(t+1)> +
-// p_t; dS is the gradient of S itself, the chunk before's R), so that errors of dg
-// are relative to the sums of its own chunk.  (beta = 0 goes as 2^-60: Y is a
-// multiple of it.)
-//
-// Then E and Y, and HV columns at a time S and R, go into LDS as two bf16 planes,
-// and all waves contract over them: S and R against dO, Y, E (a wave: 32 channels and
-// its share of the tokens), and the triangle's pairs dO E^T, Y E^T; last the
-// pairs become W and N, and W, N and their transposes meet K and Q.
-//
-// The split over the directions leaves a wave half of the registers that both
-// would take: sixteen waves a compute unit at 128 columns.
+// p_t), so that errors of dg are relative to the sums of its own chunk.  (beta = 0
+// goes as 2^-60: Y is a multiple of it.)  S, Y and E therefore have the planes of
+// the chains' products in these sums; what dq and dk alone are made of (R, W, N)
+// has two, sixteen bits against the eight that they are rounded to.
 // ---------------------------------------------------------------------------
-template <class Eng, int DK, int G>
+template <class Eng, int DK>
 struct GradChunkLds {
   using E = typename Eng::E;
-  using Rec = GradRec<Eng>;
-  static constexpr int NW = 2 * G;
-  static constexpr int SP = Eng::kSplit ? 2 : 1;                    // planes of S, R, E, Y, W, N
-  static constexpr int TV = 16 * G, HV = Eng::kSplit && G == 4 ? 64 : 32;   // columns of a tile and of a step's
+  static constexpr int HV = 32;                          // columns of a step
+  static constexpr int P = Eng::kSplit ? 3 : 1;          // planes of S, Y, E
+  static constexpr int P2 = Eng::kSplit ? 2 : 1;         // planes of R, W, N
   static constexpr int kTile = kChunk * DK * (int)sizeof(E);
-  static constexpr int kVTile = kChunk * TV * (int)sizeof(E);
-  static constexpr int kSTile = HV * DK * (int)sizeof(E);
-  static constexpr int kTri = Rec::kPlane;
+  static constexpr int kStep = kChunk * HV * (int)sizeof(E);
   static constexpr int oQ = kTile;
-  static constexpr int oO = 2 * kTile;
-  static constexpr int oG = oO + kVTile;
-  static constexpr int oSum = oG + (int)sizeof(GradGates);          // [3][G][64] floats, [G] doubles
-  static constexpr int base = oSum + 3 * G * kChunk * 4 + (G * 8 + 15) / 16 * 16;
-  // first: V, M, P, and E in fp32 from the forward waves to the backward ones
-  static constexpr int oV = base;
-  static constexpr int oM = oV + kVTile;
-  static constexpr int oP = oM + Rec::oP;
-  static constexpr int oX = oM + Rec::oG;
-  static constexpr int end1 = oX + G * 16 * 64 * 4;
-  // then: E and Y, S and R of a step's columns
-  static constexpr int oE = base;
-  static constexpr int oY = oE + SP * kVTile;
-  static constexpr int oS = oY + SP * kVTile;
-  static constexpr int oR = oS + SP * kSTile;
-  static constexpr int end2 = oR + SP * kSTile;
-  // last: W, N
-  static constexpr int oW = base;
-  static constexpr int oN = oW + SP * kTri;
-  static constexpr int end3 = oN + SP * kTri;
-  static constexpr int bytes = end1 > end2 ? (end1 > end3 ? end1 : end3) : (end2 > end3 ? end2 : end3);
-  static_assert(bytes <= 160 * 1024, "LDS budget exceeded");
-  static_assert(base % 16 == 0 && TV % HV == 0, "16-byte aligned, whole steps");
+  static constexpr int oG = 2 * kTile;
+  static constexpr int oYE = oG + (int)sizeof(GradGates);   // [4][64] Y.E
+  static constexpr int oQS = oYE + 4 * kChunk * 4;          // [4][64] q.(dO S)
+  static constexpr int oKS = oQS + 4 * kChunk * 4;          // [4][64] k.(Y S)
+  static constexpr int oT = oKS + 4 * kChunk * 4;           // [10][16] the pairs' part of p
+  static constexpr int oZ = oT + 10 * 16 * 4;               // [4] <R, S>
+  static constexpr int oO = oZ + 4 * 8;                     // dO, then planes of Y and of E, [column][token]
+  static constexpr int oY = oO + kStep;
+  static constexpr int oE = oY + P * kStep;
+  static constexpr int oW = oO;                             // last W and N
+  static constexpr int oN = oW + P2 * GradRec<Eng>::kPlane;
+  static constexpr int end1 = oE + P * kStep, end2 = oN + P2 * GradRec<Eng>::kPlane;
+  static constexpr int bytes = end1 > end2 ? end1 : end2;
+  static_assert(bytes <= 160 * 1024 && oO % 16 == 0, "LDS budget, 16-byte aligned");
 };
+
+// Eight values of a row fragment in the order kperm (or zeros) to memory.
+template <class Eng>
+__device__ __forceinline__ void put_dv(typename Eng::E* p, const typename Eng::Fr& f, bool zero) {
+  if constexpr (Eng::kSplit) {
+    uint4 u = __builtin_bit_cast(uint4, f);
+    if (zero) u = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint2*>(p) = make_uint2(u.x, u.y);
+    *reinterpret_cast<uint2*>(p + 16) = make_uint2(u.z, u.w);
+  } else {
+    *reinterpret_cast<float4*>(p) = zero ? float4{} : make_float4(f.v[0], f.v[1], f.v[2], f.v[3]);
+    *reinterpret_cast<float4*>(p + 16) = zero ? float4{} : make_float4(f.v[4], f.v[5], f.v[6], f.v[7]);
+  }
+}
 
 // The lane, as a value that the compiler does not know from before: addresses
 // formed from it are not those of an earlier part kept in registers.
@@ -514,248 +527,17 @@ __device__ __forceinline__ int fresh_lane() {
   return l & 63;
 }
 
-// The first part of a wave: its columns' state, E or Y, and sums.
-template <class Eng, int DK, int G>
-struct GradStep {
+template <class Eng, int DK>
+__global__ __launch_bounds__(kThreads, Eng::kSplit ? 2 : 1) void grad_chunk_kernel(GradArgs a) {
   using E = typename Eng::E;
   using Fr = typename Eng::Fr;
-  using Ls = GradChunkLds<Eng, DK, G>;
+  using Ls = GradChunkLds<Eng, DK>;
   using Rec = GradRec<Eng>;
+  constexpr int P = Ls::P, P2 = Ls::P2, HV = Ls::HV;
   using TK = LinTile<E, DK>;
-  using TO = LinTile<E, Ls::TV>;
-  static constexpr int P = Rec::kMPlanes, NKB = DK / 32, NT = DK / 16;
-
-  char* smem;
-  int c, ln, gq;        // columns 16 c .. of the tile
-  f32x4 st[NT];         // S or R: tile tr holds channels dkmap(16 tr + 4 gq ..) of column 16 c + ln
-  f32x4 x[4];           // E or Y: tokens 16 rt + 4 gq + i of it
-
-  __device__ __forceinline__ const GradGates& gates() const {
-    return *reinterpret_cast<const GradGates*>(smem + Ls::oG);
-  }
-  __device__ __forceinline__ void load(const float* p) {
-#pragma unroll
-    for (int tr = 0; tr < NT; ++tr) {
-      st[tr] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (p != nullptr)
-        st[tr] = *reinterpret_cast<const f32x4*>(p + (int64_t)(16 * c + ln) * DK + 8 * gq + 32 * (tr / 2) + 4 * (tr & 1));
-    }
-  }
-  // this lane's part of <state at p, st>
-  __device__ __forceinline__ float dot(const float* p) const {
-    float z = 0.0f;
-#pragma unroll
-    for (int tr = 0; tr < NT; ++tr) {
-      const f32x4 y = *reinterpret_cast<const f32x4*>(p + (int64_t)(16 * c + ln) * DK + 8 * gq + 32 * (tr / 2) + 4 * (tr & 1));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) z = fmaf(st[tr][i], y[i], z);
-    }
-    return z;
-  }
-  // K (and Q) against the planes of the state
-  template <bool kQ>
-  __device__ __forceinline__ void against(f32x4 (&ck)[4], f32x4 (&cq)[4]) const {
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt) {
-      ck[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if constexpr (kQ) cq[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-#pragma unroll
-    for (int p = 0; p < NKB; ++p) {
-      const float x8[8] = {st[2 * p][0], st[2 * p][1], st[2 * p][2], st[2 * p][3],
-                           st[2 * p + 1][0], st[2 * p + 1][1], st[2 * p + 1][2], st[2 * p + 1][3]};
-      Fr sf[P], f[4];
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt) f[rt] = TK::template row8<Eng>(smem, 16 * rt + ln, 32 * p + 8 * gq);
-      split_planes<Eng, P>(x8, sf);
-#pragma unroll
-      for (int i = 0; i < P; ++i)
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) Eng::mma(ck[rt], f[rt], sf[i]);
-      if constexpr (kQ) {
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) f[rt] = TK::template row8<Eng>(smem + Ls::oQ, 16 * rt + ln, 32 * p + 8 * gq);
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-#pragma unroll
-          for (int rt = 0; rt < 4; ++rt) Eng::mma(cq[rt], f[rt], sf[i]);
-      }
-      __builtin_amdgcn_sched_barrier(0);   // reads in flight stay within the registers
-    }
-  }
-  __device__ __forceinline__ Fr column(int o, int kb) const {
-    return TO::template cols8<Eng, 4>(smem + o, kb, 16 * c, ln, gq);
-  }
-  // acc += A b for the record's lower-triangular A at o, or its transpose
-  template <bool kT, int PA>
-  __device__ __forceinline__ void tri(f32x4 (&acc)[4], int o, const Fr (&b)[2][P]) const {
-#pragma unroll
-    for (int i = 0; i < PA; ++i)
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int rt = kT ? 0 : 2 * kb; rt < (kT ? 2 * kb + 2 : 4); ++rt) {
-          const char* p = smem + o + i * Rec::kPlane;
-          const Fr a = kT ? tri_cols<Eng>(p, rt, kb, ln, gq) : tri_rows<Eng>(p, rt, kb, ln, gq);
-#pragma unroll
-          for (int k = 0; plane_pair(i, k, P); ++k) Eng::mma(acc[rt], a, b[kb][k]);
-        }
-  }
-  static __device__ __forceinline__ void zero(f32x4 (&a)[4]) {
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt) a[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  }
-  // sums over the columns of v (this lane's tokens) into LDS, [G][64]
-  __device__ __forceinline__ void sums(float* to, int rt, int i, float v) const {
-    v = group_sum<16>(v);
-    if (ln == 0) to[kChunk * c + 16 * rt + 4 * gq + i] = v;
-  }
-
-  // E = M (V - e^G K S^T) into x and, in fp32, for the backward wave; sums of dO.o
-  __device__ __forceinline__ void forward(float* sum_o) {
-    const GradGates& g = gates();
-    f32x4 ks[4], o[4];
-    against<true>(ks, o);
-    Fr f[2][P];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      float v[8];
-      frag_values(column(Ls::oV, kb), v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int rt = 2 * kb + (k >> 2), i = k & 3;
-        const float eg = g.eg[16 * rt + 4 * gq + i];
-        v[k] = fmaf(-eg, ks[rt][i], v[k]);
-        o[rt][i] *= eg;
-      }
-      split_planes<Eng, P>(v, f[kb]);
-    }
-    zero(x);
-    tri<false, P>(x, Ls::oM, f);
-    __builtin_amdgcn_sched_barrier(0);
-    float* ex = reinterpret_cast<float*>(smem + Ls::oX) + c * 1024;
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt) reinterpret_cast<f32x4*>(ex)[64 * rt + 16 * gq + ln] = x[rt];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      float u[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int rt = 2 * kb + (k >> 2), i = k & 3;
-        u[k] = g.beta[16 * rt + 4 * gq + i] * x[rt][i];
-      }
-      split_planes<Eng, P>(u, f[kb]);
-    }
-    tri<false, Rec::kPPlanes>(o, Ls::oP, f);
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      float d[8];
-      frag_values(column(Ls::oO, kb), d);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) sums(sum_o, 2 * kb + (k >> 2), k & 3, d[k] * o[2 * kb + (k >> 2)][k & 3]);
-    }
-  }
-  // Y = M^T b (P^T dO + e^(G_C - G) K R^T) into x; sums of Y.V
-  __device__ __forceinline__ void backward(float* sum_v) {
-    const GradGates& g = gates();
-    f32x4 kr[4], f1[4];
-    against<false>(kr, kr);
-    zero(f1);
-    Fr f[2][P];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      const Fr of = column(Ls::oO, kb);
-#pragma unroll
-      for (int i = 0; i < Rec::kPPlanes; ++i)
-#pragma unroll
-        for (int rt = 0; rt < 2 * kb + 2; ++rt)
-          Eng::mma(f1[rt], tri_cols<Eng>(smem + Ls::oP + i * Rec::kPlane, rt, kb, ln, gq), of);
-    }
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      float z[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int rt = 2 * kb + (k >> 2), i = k & 3, t = 16 * rt + 4 * gq + i;
-        z[k] = g.beta[t] * fmaf(g.el[t], kr[rt][i], f1[rt][i]);
-      }
-      split_planes<Eng, P>(z, f[kb]);
-    }
-    zero(x);
-    tri<true, P>(x, Ls::oM, f);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      float v[8];
-      frag_values(column(Ls::oV, kb), v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) sums(sum_v, 2 * kb + (k >> 2), k & 3, v[k] * x[2 * kb + (k >> 2)][k & 3]);
-    }
-  }
-  // sums of Y.E, E from the forward wave
-  __device__ __forceinline__ void meet(float* sum_b) const {
-    const float* ex = reinterpret_cast<const float*>(smem + Ls::oX) + c * 1024;
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt) {
-      const f32x4 e = reinterpret_cast<const f32x4*>(ex)[64 * rt + 16 * gq + ln];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sums(sum_b, rt, i, e[i] * x[rt][i]);
-    }
-  }
-  // the state's planes, row `row` of a step's tile
-  __device__ __forceinline__ void put_state(char* to, int row) const {
-#pragma unroll
-    for (int p = 0; p < NKB; ++p) {
-      const int col = 32 * p + 8 * gq;
-      const float x8[8] = {st[2 * p][0], st[2 * p][1], st[2 * p][2], st[2 * p][3],
-                           st[2 * p + 1][0], st[2 * p + 1][1], st[2 * p + 1][2], st[2 * p + 1][3]};
-      if constexpr (Eng::kSplit) {
-        Fr f[2];
-        Eng::split(x8, f[0], f[1]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          Eng::st((E*)(to + i * Ls::kSTile + row * DK * 2 + 16 * lin_unit<TK::kUnits>(row, col / 8)), f[i]);
-      } else {
-        *(float4*)(to + row * DK * 4 + 16 * lin_unit<TK::kUnits>(row, col / 4)) = make_float4(x8[0], x8[1], x8[2], x8[3]);
-        *(float4*)(to + row * DK * 4 + 16 * lin_unit<TK::kUnits>(row, col / 4 + 1)) = make_float4(x8[4], x8[5], x8[6], x8[7]);
-      }
-    }
-  }
-  // x's planes, this lane's column of the token rows
-  __device__ __forceinline__ void put_x(char* to) const {
-    constexpr int kPer = 16 / (int)sizeof(E);
-    const int col = 16 * c + ln, in = (col % kPer) * (int)sizeof(E);
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        const int ra = 16 * rt + 4 * gq + i, rb = ra + 1;
-        char* a = to + ra * Ls::TV * (int)sizeof(E) + 16 * lin_unit<TO::kUnits>(ra, col / kPer) + in;
-        char* b = to + rb * Ls::TV * (int)sizeof(E) + 16 * lin_unit<TO::kUnits>(rb, col / kPer) + in;
-        if constexpr (Eng::kSplit) {
-          uint32_t hi, lo;
-          split_bf16x2(x[rt][i], x[rt][i + 1], hi, lo);
-          *(uint16_t*)a = (uint16_t)hi;
-          *(uint16_t*)b = (uint16_t)(hi >> 16);
-          *(uint16_t*)(a + Ls::kVTile) = (uint16_t)lo;
-          *(uint16_t*)(b + Ls::kVTile) = (uint16_t)(lo >> 16);
-        } else {
-          *(float*)a = x[rt][i];
-          *(float*)b = x[rt][i + 1];
-        }
-      }
-  }
-};
-
-template <class Eng, int DK, int G, bool kOne>
-__global__ __launch_bounds__(128 * G, G / 2) void grad_chunk_kernel(GradArgs a) {
-  using E = typename Eng::E;
-  using Fr = typename Eng::Fr;
-  using Ls = GradChunkLds<Eng, DK, G>;
-  using Rec = GradRec<Eng>;
-  constexpr int NW = Ls::NW, SP = Ls::SP, TV = Ls::TV, HV = Ls::HV, T = 64 * NW;
-  using TK = LinTile<E, DK>;
-  using TO = LinTile<E, TV>;
+  using TO = LinTile<E, HV>;
+  using TY = LinTile<E, kChunk>;
+  using RO = LinRows<E, HV, kThreads>;
   extern __shared__ __align__(16) char smem[];
   if (grad_refused(a)) return;
   const int j = blockIdx.x / a.H, h = blockIdx.x % a.H;
@@ -764,286 +546,305 @@ __global__ __launch_bounds__(128 * G, G / 2) void grad_chunk_kernel(GradArgs a) 
   const int nv = pl.nv, H = a.H, dv = a.dv;
   const uint32_t lds0 = lds_base_u32(smem);
   const int tid = threadIdx.x, w = uniform(tid >> 6);
-  const bool rev = w >= G;
   const char* sK = smem;
   const char* sQ = smem + Ls::oQ;
-  const char* sO = smem + Ls::oO;
   const GradGates& g = *reinterpret_cast<const GradGates*>(smem + Ls::oG);
-  float* sum_o = reinterpret_cast<float*>(smem + Ls::oSum);         // [G][64] dO.o
-  float* sum_v = sum_o + G * kChunk;                                // Y.V
-  float* sum_b = sum_v + G * kChunk;                                // Y.E
-  double* sum_z = reinterpret_cast<double*>(sum_b + G * kChunk);    // [G] <dS, S>
 
-  const int64_t row0 = (int64_t)pl.t0 * H + h;
-  const int64_t ch = (int64_t)j * H + h, state = (int64_t)dv * DK;
-  const char* rec = a.rec + ch * Rec::kBytes;
+  const int64_t row0 = (int64_t)pl.t0 * H + h, ch = (int64_t)j * H + h;
   {
-    using RK = LinRows<E, DK, T>;
+    using RK = LinRows<E, DK, kThreads>;
     RK::ask(lds0, (const E*)a.k + row0 * DK, H * DK, nv);
     RK::ask(lds0 + Ls::oQ, (const E*)a.q + row0 * DK, H * DK, nv);
-    ask_bytes<NW>(lds0 + Ls::oG, rec + Rec::oG, Rec::kGates);
+    ask_bytes<4>(lds0 + Ls::oG, a.rec + ch * Rec::kBytes + Rec::oG, Rec::kGates);
   }
-  // the entering state (kept, the initial one, or the chain's), its gradient, and the leaving one's
-  const int64_t seq = ((int64_t)pl.n * H + h) * state;
-  const float* ps = a.kept == nullptr ? a.S + ch * state
-                    : pl.c > 0 ? a.kept + (ch - H) * state : a.init == nullptr ? nullptr : a.init + seq;
-  const float* pd = pl.c > 0 ? a.R + (ch - H) * state : a.d_init + seq;
-  const float* pr = a.R + ch * state;
-
-  // this wave's share of the contractions: channels 32 wc .. 32 wc + 31, token tiles TPW tg ..
-  constexpr int CP = DK / 32, TG = NW / CP < 4 ? NW / CP : 4, TPW = 4 / TG;
-  constexpr bool kIdle = TG * CP < NW;   // more waves than shares (dk = 64 and 128 columns)
+  // this wave's share: channels 32 wc .. 32 wc + 31, token tiles TPW tg ..
+  constexpr int CP = DK / 32, TG = 4 / CP, TPW = 4 / TG;
   const int wc = w % CP, tg = w / CP;
-  const bool share = !kIdle || tg < TG;
-  f32x4 aq[TPW][2], ax[TPW][2], as[TPW][2];
-  // and of the triangle's ten tiles: w, w + NW, ..
-  constexpr int NTri = (10 + NW - 1) / NW;
-  f32x4 pe[NTri], ye[NTri];
-  auto clear = [&] {
+  // the entering state (kept, the initial one, or the chain's) and the leaving one's gradient
+  const int64_t state = (int64_t)dv * DK;
+  const float* ps = a.kept == nullptr ? a.S + ch * state
+                    : pl.c > 0 ? a.kept + (ch - H) * state
+                    : a.init == nullptr ? nullptr : a.init + ((int64_t)pl.n * H + h) * state;
+  const bool none = ps == nullptr;   // zeros
+  if (none) ps = a.R + ch * state;
+  const float* pr = a.R + ch * state;
+  const float* pe_ = a.E + ch * dv * kChunk;
+  const float* py_ = a.Y + ch * dv * kChunk;
+  const E* po = (const E*)a.d_o + row0 * dv;
+
+  // what the next step needs, on the way
+  f32x2 sx[8], rx[8];        // columns kperm, channels 32 wc + 2 ln ..
+  f32x4 ex[2], yx[2];        // column tid / 16 (+ 16), tokens 4 (tid % 16) ..
+  uint4 ox[RO::kPer];
+  auto fetch_state = [&](f32x2 (&x)[8], const float* p, int h0) {
+    const int l = fresh_lane(), at = 4 * (l >> 4) * DK + 2 * (l & 15);
+    const float* c = p + (h0 * DK + 32 * wc);
 #pragma unroll
-    for (int t = 0; t < TPW; ++t)
-#pragma unroll
-      for (int m = 0; m < 2; ++m) aq[t][m] = ax[t][m] = as[t][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < NTri; ++i) pe[i] = ye[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < 8; ++i)
+      x[i] = *reinterpret_cast<const f32x2*>(c + at + ((i & 3) + 16 * (i >> 2)) * DK);
   };
-  if constexpr (!kOne) clear();
+  auto fetch_rows = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      ex[i] = *reinterpret_cast<const f32x4*>(pe_ + (h0 * kChunk + 1024 * i) + 4 * tid);
+      yx[i] = *reinterpret_cast<const f32x4*>(py_ + (h0 * kChunk + 1024 * i) + 4 * tid);
+    }
+    RO::fetch(ox, po + h0, H * dv, nv);
+  };
+  auto put_rows = [&](char* to, const f32x4 (&x)[2]) {   // planes, [column][token]
+    const int l = w * 64 + fresh_lane();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int col = (l >> 4) + 16 * i, t0 = 4 * (l & 15);
+      constexpr int kPer = 16 / (int)sizeof(E);
+      const float x4[4] = {x[i][0], x[i][1], x[i][2], x[i][3]};
+      put4<Eng, P>(to + col * kChunk * (int)sizeof(E) + 16 * lin_unit<TY::kUnits>(col, t0 / kPer) +
+                       (t0 % kPer) * (int)sizeof(E),
+                   Ls::kStep, x4);
+    }
+  };
+
+  f32x4 aq[TPW][2], ax[TPW][2], as[TPW][2];
+#pragma unroll
+  for (int t = 0; t < TPW; ++t)
+#pragma unroll
+    for (int m = 0; m < 2; ++m) aq[t][m] = ax[t][m] = as[t][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  // and of the triangle's ten tiles: w, w + 4, ..
+  f32x4 pe[3], ye[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) pe[i] = ye[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   auto tri_of = [](int job, int& Tt, int& St) {
     Tt = job < 1 ? 0 : job < 3 ? 1 : job < 6 ? 2 : 3;
     St = job - Tt * (Tt + 1) / 2;
   };
   double z = 0.0;
-  float keep_p = 0.0f, keep_b = 0.0f;   // sums of the earlier tiles (wave c: its columns'; lane: token)
+  f32x4 dots = {0.0f, 0.0f, 0.0f, 0.0f};   // Y.E of tokens 4 (tid % 16) ..
 
-  for (int v0 = 0; kOne ? v0 == 0 : v0 < dv; v0 += TV) {
-    f32x4 st[DK / 16];
-    const int c = rev ? w - G : w;
-    char* sE = smem + Ls::oE;
-    char* sY = smem + Ls::oY;
-    {
-      const int l64 = fresh_lane();
-      GradStep<Eng, DK, G> step;
-      step.smem = smem;
-      step.c = c;
-      step.ln = l64 & 15;
-      step.gq = l64 >> 4;
-      step.load(rev ? pr + (int64_t)v0 * DK : ps == nullptr ? nullptr : ps + (int64_t)v0 * DK);
-      if (v0 > 0) __syncthreads();   // the last tile is consumed
-      {
-        using RV = LinRows<E, TV, T>;
-        RV::ask(lds0 + Ls::oO, (const E*)a.d_o + row0 * dv + v0, H * dv, nv);
-        RV::ask(lds0 + Ls::oV, (const E*)a.v + row0 * dv + v0, H * dv, nv);
-        ask_bytes<NW>(lds0 + Ls::oM, rec, Rec::oG);
-      }
-      if (!rev && ps != nullptr) z += (double)step.dot(pd + (int64_t)v0 * DK);
-      wait_vmem();
-      __syncthreads();
-      if (rev) step.backward(sum_v);
-      else step.forward(sum_o);
-      __syncthreads();   // E has come
-      if (rev) step.meet(sum_b);
-      __syncthreads();
-      if constexpr (!kOne) {
-        if (!rev && v0 + TV < dv) {   // the next tile's sums take the place
-          keep_p += sum_o[kChunk * w + l64] - sum_v[kChunk * w + l64];
-          keep_b += sum_b[kChunk * w + l64];
-        }
-      }
-      step.put_x(rev ? sY : sE);
+  fetch_rows(0);
+  fetch_state(sx, ps, 0);
+  fetch_state(rx, pr, 0);
+  for (int h0 = 0; h0 < dv; h0 += HV) {
+    const int hn = min(h0 + HV, dv - HV);   // the last step asks for itself again
+    if (h0 > 0) barrier_lds();              // the last columns are consumed
+    put_rows(smem + Ls::oY, yx);
+    put_rows(smem + Ls::oE, ex);
+    RO::put(smem + Ls::oO, ox);
+    if (none) {
 #pragma unroll
-      for (int tr = 0; tr < DK / 16; ++tr) st[tr] = step.st[tr];
+      for (int i = 0; i < 8; ++i) sx[i] = f32x2{0.0f, 0.0f};
     }
-    if constexpr (kOne) clear();   // not kept through the first part
+    float zs = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) dots[k] = fmaf(ex[i][k], yx[i][k], dots[k]);
+    Fr sf[2][P];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const float x8[8] = {sx[0][m], sx[1][m], sx[2][m], sx[3][m], sx[4][m], sx[5][m], sx[6][m], sx[7][m]};
+      split_planes<Eng, P>(x8, sf[m]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) zs = fmaf(sx[i][m], rx[i][m], zs);
+    }
+    z += (double)zs;
+    fetch_state(sx, ps, hn);
+    if (h0 == 0) wait_vmem();   // K, Q, gates
+    barrier_lds();
+    __builtin_amdgcn_sched_barrier(0);
 
+    // S against dO and Y
+    const int l = fresh_lane(), ln = l & 15, gq = l >> 4;
 #pragma unroll
-    for (int h0 = 0; h0 < TV; h0 += HV) {
-      const int l64 = fresh_lane(), ln = l64 & 15, gq = l64 >> 4;
-      char* sS = smem + Ls::oS;
-      char* sR = smem + Ls::oR;
-      if (h0 > 0) __syncthreads();   // the last columns are consumed
-      if (16 * c >= h0 && 16 * c < h0 + HV) {
-        GradStep<Eng, DK, G> step;
-        step.c = c;
-        step.ln = ln;
-        step.gq = gq;
+    for (int t = 0; t < TPW; ++t) {
+      const int tile = TPW * tg + t;
+      const Fr of = row_kperm<Eng, TO>(smem + Ls::oO, 16 * tile + ln, 0, gq);
+      Fr yf[P];
 #pragma unroll
-        for (int tr = 0; tr < DK / 16; ++tr) step.st[tr] = st[tr];
-        step.put_state(rev ? sR : sS, 16 * c - h0 + ln);
-      }
-      __syncthreads();
-
-      if (h0 == 0) {   // d_v: Y's first plane is Y rounded to bf16
-        for (int i = tid; i < kChunk * TO::kUnits; i += T) {
-          const int row = i / TO::kUnits, u = i % TO::kUnits;
-          if (row < nv) {
-            uint4 x = *reinterpret_cast<const uint4*>(sY + row * TV * (int)sizeof(E) + 16 * lin_unit<TO::kUnits>(row, u));
-            if (g.zero[row] != 0.0f) x = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>((E*)a.d_v + (row0 + (int64_t)row * H) * dv + v0 + u * (16 / (int)sizeof(E))) = x;
-          }
+      for (int i = 0; i < P; ++i)
+        yf[i] = TY::template cols8<Eng, 4>(smem + Ls::oY + i * Ls::kStep, 0, 16 * tile, ln, gq);
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          Eng::mma(aq[t][m], sf[m][i], of);
+          Eng::mma(ax[t][m], sf[m][0], yf[i]);
         }
+#pragma unroll
+      for (int i = 1; i < P; ++i)
+#pragma unroll
+        for (int k = 0; plane_pair(i, k, P); ++k)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) Eng::mma(ax[t][m], sf[m][i], yf[k]);
+      if (t == wc) {   // d_v: the first plane is Y rounded to bf16
+        const int tok = 16 * tile + ln;
+        if (tok < nv) put_dv<Eng>((E*)a.d_v + (row0 + (int64_t)tok * H) * dv + h0 + 4 * gq, yf[0], g.zero[tok] != 0.0f);
       }
-      // S against dO and Y, R against E (the barriers for the scheduler keep reads in flight within the registers)
-      if (share) {
+      __builtin_amdgcn_sched_barrier(0);   // reads in flight stay within the registers
+    }
+    fetch_rows(hn);
+    // R against E
+    Fr rf[2][P2];
 #pragma unroll
-        for (int kb = 0; kb < HV / 32; ++kb) {
-          auto column = [&](const char* p, Fr (&f)[2][SP]) {
+    for (int m = 0; m < 2; ++m) {
+      const float x8[8] = {rx[0][m], rx[1][m], rx[2][m], rx[3][m], rx[4][m], rx[5][m], rx[6][m], rx[7][m]};
+      split_planes<Eng, P2>(x8, rf[m]);
+    }
+    fetch_state(rx, pr, hn);
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+    for (int t = 0; t < TPW; ++t) {
+      Fr ef[P2];
 #pragma unroll
-              for (int i = 0; i < SP; ++i)
-                f[m][i] = TK::template cols8<Eng, 8>(p + i * Ls::kSTile, kb, 32 * wc + 4 * m, ln, gq);
-          };
-          const int hb = h0 / 32 + kb;
-          Fr sf[2][SP];
-          column(sS, sf);
+      for (int i = 0; i < P2; ++i)
+        ef[i] = TY::template cols8<Eng, 4>(smem + Ls::oE + i * Ls::kStep, 0, 16 * (TPW * tg + t), ln, gq);
 #pragma unroll
-          for (int t = 0; t < TPW; ++t) {
-            const int row = 16 * (TPW * tg + t) + ln;
-            const Fr of = row_kperm<Eng, TO>(sO, row, hb, gq);
-            Fr yf[SP];
+      for (int i = 0; i < P2; ++i)
 #pragma unroll
-            for (int i = 0; i < SP; ++i) yf[i] = row_kperm<Eng, TO>(sY + i * Ls::kVTile, row, hb, gq);
+        for (int k = 0; plane_pair(i, k, P2); ++k)
 #pragma unroll
-            for (int i = 0; i < SP; ++i)
+          for (int m = 0; m < 2; ++m) Eng::mma(as[t][m], rf[m][i], ef[k]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // the triangle: lane holds token t = 16 T + ln, s = 16 S + 4 gq + i
 #pragma unroll
-              for (int m = 0; m < 2; ++m) Eng::mma(aq[t][m], sf[m][i], of);
+    for (int i = 0; i < 3; ++i) {
+      if (w + 4 * i >= 10) break;
+      int Tt, St;
+      tri_of(w + 4 * i, Tt, St);
+      const Fr of = row_kperm<Eng, TO>(smem + Ls::oO, 16 * Tt + ln, 0, gq);
+      Fr ef[P], yf[P];
 #pragma unroll
-            for (int i = 0; i < SP; ++i)
-#pragma unroll
-              for (int k = 0; plane_pair(i, k, SP); ++k)
-#pragma unroll
-                for (int m = 0; m < 2; ++m) Eng::mma(ax[t][m], sf[m][i], yf[k]);
-          }
-          __builtin_amdgcn_sched_barrier(0);
-          column(sR, sf);
-#pragma unroll
-          for (int t = 0; t < TPW; ++t) {
-            const int row = 16 * (TPW * tg + t) + ln;
-            Fr ef[SP];
-#pragma unroll
-            for (int i = 0; i < SP; ++i) ef[i] = row_kperm<Eng, TO>(sE + i * Ls::kVTile, row, hb, gq);
-#pragma unroll
-            for (int i = 0; i < SP; ++i)
-#pragma unroll
-              for (int k = 0; plane_pair(i, k, SP); ++k)
-#pragma unroll
-                for (int m = 0; m < 2; ++m) Eng::mma(as[t][m], sf[m][i], ef[k]);
-          }
-          __builtin_amdgcn_sched_barrier(0);
-        }
+      for (int k = 0; k < P; ++k) {
+        ef[k] = TY::template cols8<Eng, 4>(smem + Ls::oE + k * Ls::kStep, 0, 16 * St, ln, gq);
+        yf[k] = TY::template cols8<Eng, 4>(smem + Ls::oY + k * Ls::kStep, 0, 16 * Tt, ln, gq);
       }
-      // the triangle: lane holds token t = 16 T + ln, s = 16 S + 4 gq + i
 #pragma unroll
-      for (int i = 0; i < NTri; ++i) {
-        if (w + NW * i >= 10) break;
-        int Tt, St;
-        tri_of(w + NW * i, Tt, St);
+      for (int k = 0; k < P; ++k) {
+        Eng::mma(pe[i], ef[k], of);
 #pragma unroll
-        for (int p = 0; p < HV / 32; ++p) {
-          const int col = h0 + 32 * p + 8 * gq;
-          const Fr of = TO::template row8<Eng>(sO, 16 * Tt + ln, col);
-          Fr ef[SP], yf[SP];
-#pragma unroll
-          for (int k = 0; k < SP; ++k) {
-            ef[k] = TO::template row8<Eng>(sE + k * Ls::kVTile, 16 * St + ln, col);
-            yf[k] = TO::template row8<Eng>(sY + k * Ls::kVTile, 16 * Tt + ln, col);
-          }
-#pragma unroll
-          for (int k = 0; k < SP; ++k) {
-            Eng::mma(pe[i], ef[k], of);
-#pragma unroll
-            for (int l = 0; plane_pair(k, l, SP); ++l) Eng::mma(ye[i], ef[k], yf[l]);
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);
+        for (int l = 0; plane_pair(k, l, P); ++l) Eng::mma(ye[i], ef[k], yf[l]);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
-  __syncthreads();   // the last columns are consumed
+  barrier_lds();   // the last columns are consumed
 
-  {
-    const int l64 = fresh_lane(), ln = l64 & 15, gq = l64 >> 4;
-    if (!rev) {
-      if constexpr (!kOne) {
-        sum_o[kChunk * w + l64] += keep_p;
-        sum_b[kChunk * w + l64] += keep_b;
+  const int l64 = fresh_lane(), ln = l64 & 15, gq = l64 >> 4;
+  auto over_quads = [](float v) {   // lanes ln, 16 + ln, 32 + ln, 48 + ln
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+  };
+  float* sYE = reinterpret_cast<float*>(smem + Ls::oYE);
+  float* sQS = reinterpret_cast<float*>(smem + Ls::oQS);
+  float* sKS = reinterpret_cast<float*>(smem + Ls::oKS);
+  float* sT = reinterpret_cast<float*>(smem + Ls::oT);
+  double* sZ = reinterpret_cast<double*>(smem + Ls::oZ);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) dots[k] = over_quads(dots[k]);
+  if (gq == 0) *reinterpret_cast<f32x4*>(sYE + kChunk * w + 4 * ln) = dots;
+  z = last_lane(wave_prefix_f64(z));
+  if (l64 == 0) sZ[w] = tg == 0 ? z : 0.0;
+#pragma unroll
+  for (int t = 0; t < TPW; ++t) {
+    const int tok = 16 * (TPW * tg + t) + ln;
+    float q8[8], k8[8], dq = 0.0f, dk = 0.0f;
+    frag_values(TK::template row8<Eng>(sQ, tok, 32 * wc + 8 * gq), q8);
+    frag_values(TK::template row8<Eng>(sK, tok, 32 * wc + 8 * gq), k8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        dq = fmaf(q8[2 * i + m], aq[t][m][i], dq);
+        dk = fmaf(k8[2 * i + m], ax[t][m][i], dk);
       }
-      z = last_lane(wave_prefix_f64(z));
-      if (l64 == 0) sum_z[w] = z;
+    dq = over_quads(dq);
+    dk = over_quads(dk);
+    if (gq == 0) {
+      sQS[kChunk * wc + tok] = dq;
+      sKS[kChunk * wc + tok] = dk;
     }
-    // pairs
+    // channels in the order of the products with K and Q
+    const float eg = g.eg[tok], bl = g.beta[tok] * g.el[tok];
+    f32x4 nq[2], nk[2];
 #pragma unroll
-    for (int i = 0; i < NTri; ++i) {
-      if (w + NW * i >= 10) break;
-      int Tt, St;
-      tri_of(w + NW * i, Tt, St);
-      const int t = 16 * Tt + ln, tn = g.n[t];
-      const float tf = g.f[t];
-      float wv[4], nn[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int s = 16 * St + 4 * gq + k;
-        const float d = s <= t && t < nv ? g.beta[s] * lin_pow(tn - g.n[s], tf - g.f[s]) : 0.0f;
-        wv[k] = d * pe[i][k];
-        nn[k] = s < t ? -d * ye[i][k] : 0.0f;
-      }
-      const int at = tri_block(Tt, St) * Rec::kBlock + tri_at<Eng>(ln, 4 * gq) * (int)sizeof(E);
-      put4<Eng, SP>(smem + Ls::oW + at, Ls::kTri, wv);
-      put4<Eng, SP>(smem + Ls::oN + at, Ls::kTri, nn);
+    for (int c = 0; c < 8; ++c) {
+      nq[c >> 2][c & 3] = eg * aq[t][c & 1][c >> 1];
+      nk[c >> 2][c & 3] = fmaf(bl, as[t][c & 1][c >> 1], -eg * ax[t][c & 1][c >> 1]);
     }
-    if (share) {
 #pragma unroll
-      for (int t = 0; t < TPW; ++t) {
-        const int tok = 16 * (TPW * tg + t) + ln;
-        const float eg = g.eg[tok], bl = g.beta[tok] * g.el[tok];
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            aq[t][m][r] *= eg;
-            ax[t][m][r] = fmaf(bl, as[t][m][r], -eg * ax[t][m][r]);
-          }
-      }
+    for (int m = 0; m < 2; ++m) {
+      aq[t][m] = nq[m];
+      ax[t][m] = nk[m];
     }
-    __syncthreads();
+  }
+  // pairs
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    if (w + 4 * i >= 10) break;
+    int Tt, St;
+    tri_of(w + 4 * i, Tt, St);
+    f32x4 cq = {0.0f, 0.0f, 0.0f, 0.0f}, ck = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int p = 0; p < DK / 32; ++p) {
+      const Fr kf = TK::template row8<Eng>(sK, 16 * St + ln, 32 * p + 8 * gq);
+      Eng::mma(ck, kf, TK::template row8<Eng>(sK, 16 * Tt + ln, 32 * p + 8 * gq));
+      Eng::mma(cq, kf, TK::template row8<Eng>(sQ, 16 * Tt + ln, 32 * p + 8 * gq));
+    }
+    const int t = 16 * Tt + ln, tn = g.n[t];
+    const float tf = g.f[t];
+    float wv[4], nn[4], p = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int s = 16 * St + 4 * gq + k;
+      const float d = s <= t && t < nv ? g.beta[s] * lin_pow(tn - g.n[s], tf - g.f[s]) : 0.0f;
+      wv[k] = d * pe[i][k];
+      nn[k] = s < t ? -d * ye[i][k] : 0.0f;
+      p = fmaf(wv[k], cq[k], fmaf(nn[k], ck[k], p));
+    }
+    p = over_quads(p);
+    if (gq == 0) sT[16 * (w + 4 * i) + ln] = p;
+    const int at = tri_block(Tt, St) * Rec::kBlock + tri_at<Eng>(ln, 4 * gq) * (int)sizeof(E);
+    put4<Eng, P2>(smem + Ls::oW + at, Rec::kPlane, wv);
+    put4<Eng, P2>(smem + Ls::oN + at, Rec::kPlane, nn);
+  }
+  barrier_lds();
 
-    if (w == NW - 1) {
-      const int t = l64;
-      double p = 0.0, b = 0.0, zz = 0.0;
+  if (w == 3) {
+    const int t = l64, Tt = t >> 4;
+    double ye_ = 0.0, e = 0.0, zz = 0.0, p = 0.0;
 #pragma unroll
-      for (int i = 0; i < G; ++i) {
-        p += (double)sum_o[kChunk * i + t] - (double)sum_v[kChunk * i + t];
-        b += (double)sum_b[kChunk * i + t];
-        zz += sum_z[i];
-      }
-      double d = zz - (wave_prefix_f64(p) - p);
-      if (g.g[t] < -104.0f) d = 0.0;   // e^-104 rounds to 0: nothing lies across the token
-      if (t < nv) {
-        a.d_beta[row0 + (int64_t)t * H] = (float)(b / (double)g.beta[t]);
-        a.dg[row0 + (int64_t)t * H] = (float)d;
-      }
+    for (int i = 0; i < 4; ++i) {
+      ye_ += (double)sYE[kChunk * i + t];
+      zz += sZ[i];
+      if (i < CP) e += (double)sQS[kChunk * i + t] - (double)sKS[kChunk * i + t];
+      if (i <= Tt) p += (double)sT[16 * tri_block(Tt, i) + (t & 15)];
     }
-    if (!share) return;
+    e *= (double)g.eg[t];
+    p += e - ye_;
+    double d = (double)g.ec[0] * zz + last_lane(wave_prefix_f64(e)) - (wave_prefix_f64(p) - p);
+    if (g.g[t] < -104.0f) d = 0.0;   // e^-104 rounds to 0: nothing lies across the token
+    if (t < nv) {
+      a.d_beta[row0 + (int64_t)t * H] = (float)(ye_ / (double)g.beta[t]);
+      a.dg[row0 + (int64_t)t * H] = (float)d;
+    }
   }
   // dq += W K, dk += W^T Q + N K + N^T K; a lane: token 16 tile + ln, channels 32 wc + 8 gq ..
-  const int lz = fresh_lane(), lnz = lz & 15, gz = lz >> 4;
 #pragma unroll
   for (int kb = 0; kb < 2; ++kb) {
     Fr kf[2], qf[2];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      kf[m] = TK::template cols8<Eng, 8>(sK, kb, 32 * wc + 4 * m, lnz, gz);
-      qf[m] = TK::template cols8<Eng, 8>(sQ, kb, 32 * wc + 4 * m, lnz, gz);
+      kf[m] = TK::template cols8<Eng, 8>(sK, kb, 32 * wc + 4 * m, ln, gq);
+      qf[m] = TK::template cols8<Eng, 8>(sQ, kb, 32 * wc + 4 * m, ln, gq);
     }
 #pragma unroll
     for (int t = 0; t < TPW; ++t) {
       const int tile = TPW * tg + t;
 #pragma unroll
-      for (int i = 0; i < SP; ++i) {
-        const char* sW = smem + Ls::oW + i * Ls::kTri;
-        const char* sN = smem + Ls::oN + i * Ls::kTri;
+      for (int i = 0; i < P2; ++i) {
+        const char* sW = smem + Ls::oW + i * Rec::kPlane;
+        const char* sN = smem + Ls::oN + i * Rec::kPlane;
         if (2 * kb <= tile) {
-          const Fr wf = tri_rows<Eng>(sW, tile, kb, lnz, gz), nf = tri_rows<Eng>(sN, tile, kb, lnz, gz);
+          const Fr wf = tri_rows<Eng>(sW, tile, kb, ln, gq), nf = tri_rows<Eng>(sN, tile, kb, ln, gq);
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             Eng::mma(aq[t][m], kf[m], wf);
@@ -1051,7 +852,7 @@ __global__ __launch_bounds__(128 * G, G / 2) void grad_chunk_kernel(GradArgs a) 
           }
         }
         if (2 * kb + 1 >= tile) {
-          const Fr wf = tri_cols<Eng>(sW, tile, kb, lnz, gz), nf = tri_cols<Eng>(sN, tile, kb, lnz, gz);
+          const Fr wf = tri_cols<Eng>(sW, tile, kb, ln, gq), nf = tri_cols<Eng>(sN, tile, kb, ln, gq);
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             Eng::mma(ax[t][m], qf[m], wf);
@@ -1059,14 +860,13 @@ __global__ __launch_bounds__(128 * G, G / 2) void grad_chunk_kernel(GradArgs a) 
           }
         }
       }
-      __builtin_amdgcn_sched_barrier(0);
     }
   }
 #pragma unroll
   for (int t = 0; t < TPW; ++t) {
-    const int tok = 16 * (TPW * tg + t) + lnz;
+    const int tok = 16 * (TPW * tg + t) + ln;
     if (tok >= nv) continue;
-    const int64_t at = (row0 + (int64_t)tok * H) * DK + 32 * wc + 8 * gz;
+    const int64_t at = (row0 + (int64_t)tok * H) * DK + 32 * wc + 8 * gq;
     const float q8[8] = {aq[t][0][0], aq[t][0][1], aq[t][0][2], aq[t][0][3],
                          aq[t][1][0], aq[t][1][1], aq[t][1][2], aq[t][1][3]};
     const float k8[8] = {ax[t][0][0], ax[t][0][1], ax[t][0][2], ax[t][0][3],
@@ -1074,17 +874,6 @@ __global__ __launch_bounds__(128 * G, G / 2) void grad_chunk_kernel(GradArgs a) 
     Eng::st((E*)a.dq + at, Eng::round(q8));
     Eng::st((E*)a.dk + at, Eng::round(k8));
   }
-}
-
-template <class Eng, int DK, int G, bool kOne>
-hipError_t launch_grad_chunk(const GradArgs& a, int64_t items, hipStream_t stream) {
-  auto kern = grad_chunk_kernel<Eng, DK, G, kOne>;
-  constexpr size_t lds = GradChunkLds<Eng, DK, G>::bytes;
-  static PerDeviceOnce once;
-  hipError_t e = set_dyn_lds_once(once, (const void*)kern, lds);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3((unsigned)items), dim3(128 * G), lds, stream, a);
-  return hipGetLastError();
 }
 
 template <class Eng, int DK>
@@ -1104,18 +893,18 @@ hipError_t launch_grad(const gdn_shape_t& s, const GradArgs& a, int64_t items, h
     static PerDeviceOnce once;
     if ((e = set_dyn_lds_once(once, (const void*)kern, lds)) != hipSuccess) return e;
     const int chains = s.n_seqs * s.n_heads * (s.dv / 64);
-    hipLaunchKernelGGL(kern, dim3((unsigned)(a.kept ? chains : 2 * chains)), dim3(kThreads), lds, stream, a, chains);
+    hipLaunchKernelGGL(kern, dim3((unsigned)(2 * chains)), dim3(kThreads), lds, stream, a, chains);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (items > 0) {
-    // 128 value columns at once, where that is all of them; else (and fp32, whose tiles would not fit) 64 at a time
-    constexpr int kWide = Eng::kSplit ? 8 : 4;
-    if (s.dv == 16 * kWide) e = launch_grad_chunk<Eng, DK, kWide, true>(a, items, stream);
-    else e = launch_grad_chunk<Eng, DK, 4, false>(a, items, stream);
-  } else {
-    e = hipSuccess;
+    auto kern = grad_chunk_kernel<Eng, DK>;
+    constexpr size_t lds = GradChunkLds<Eng, DK>::bytes;
+    static PerDeviceOnce once;
+    if ((e = set_dyn_lds_once(once, (const void*)kern, lds)) != hipSuccess) return e;
+    hipLaunchKernelGGL(kern, dim3((unsigned)items), dim3(kThreads), lds, stream, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  return e;
+  return hipSuccess;
 }
 
 }  // namespace gdn
