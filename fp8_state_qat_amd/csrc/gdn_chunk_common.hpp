@@ -74,6 +74,12 @@ __device__ __forceinline__ void wait_vmem() {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0), expcnt and lgkmcnt not waited
 }
+// The same for all but the N operations issued last (loads and stores complete
+// in order).
+template <int N>
+__device__ __forceinline__ void wait_vmem_but() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"i"(N) : "memory");
+}
 // Workgroup barrier that orders LDS accesses only: it does not wait for the
 // wave's direct LDS loads or global memory operations in flight.
 __device__ __forceinline__ void barrier_lds() {

@@ -165,7 +165,7 @@ struct GradScanLds {
   static constexpr int bytes = kBufs * buf;
 };
 
-template <class Eng, int DK, bool kRev>
+template <class Eng, int DK, bool kRev, bool kKept = false>
 struct GradWalk {
   using E = typename Eng::E;
   using Fr = typename Eng::Fr;
@@ -197,16 +197,46 @@ struct GradWalk {
     }
   }
 
-  __device__ __forceinline__ void ask(uint32_t buf, int j, int t0, int nv) const {
-    using RK = LinRows<E, DK, kThreads>;
-    using RV = LinRows<E, 64, kThreads>;
+  // What the next chunk needs, in kAsks steps: a step's load for each wave
+  // (records: wave w the KiB w, w + 4, ..; the gates beside M's last).
+  using RK = LinRows<E, DK, kThreads>;
+  using RV = LinRows<E, 64, kThreads>;
+  static constexpr int kRecKiB = (kRev ? Rec::oG : Rec::oP) / 1024;
+  static constexpr int kAsks = RK::kPer * (kRev ? 2 : 1) + RV::kPer + (kRecKiB + 4) / 4;
+  struct Next {
+    uint32_t buf;
+    const E *k, *q, *v;
+    const char* rec;
+    int nv;
+  };
+  __device__ __forceinline__ Next next(uint32_t buf, int j, int t0, int nv) const {
     const int64_t row0 = (int64_t)t0 * a.H + h;
-    RK::ask(buf, (const E*)a.k + row0 * DK, a.H * DK, nv);
-    if constexpr (kRev) RK::ask(buf + Ls::oQ, (const E*)a.q + row0 * DK, a.H * DK, nv);
-    RV::ask(buf + Ls::oV, (const E*)(kRev ? a.d_o : a.v) + row0 * a.dv + 64 * vt, a.H * a.dv, nv);
-    const char* rec = a.rec + ((int64_t)j * a.H + h) * Rec::kBytes;
-    ask_bytes<4>(buf + Ls::oM, rec, kRev ? Rec::oG : Rec::oP);
-    if (w == 3) lds_load16(rec + Rec::oG, (uint32_t)(threadIdx.x & 63) * 16, buf + Ls::oG);
+    return Next{buf, (const E*)a.k + row0 * DK, (const E*)a.q + row0 * DK,
+                (const E*)(kRev ? a.d_o : a.v) + row0 * a.dv + 64 * vt,
+                a.rec + ((int64_t)j * a.H + h) * Rec::kBytes, nv};
+  }
+  __device__ __forceinline__ void ask(const Next& x, int i) const {
+    if (i < RK::kPer) return RK::ask_step(i, x.buf, x.k, a.H * DK, x.nv);
+    i -= RK::kPer;
+    if (kRev) {
+      if (i < RK::kPer) return RK::ask_step(i, x.buf + Ls::oQ, x.q, a.H * DK, x.nv);
+      i -= RK::kPer;
+    }
+    if (i < RV::kPer) return RV::ask_step(i, x.buf + Ls::oV, x.v, a.H * a.dv, x.nv);
+    i -= RV::kPer;
+    const int kib = 4 * i + w;
+    if (4 * i + 3 > kRecKiB && kib > kRecKiB) return;
+    const bool gates = 4 * i + 3 >= kRecKiB && kib == kRecKiB;
+    lds_load16(x.rec + (gates ? Rec::oG : 1024 * kib), (uint32_t)(threadIdx.x & 63) * 16,
+               x.buf + (gates ? Ls::oG : Ls::oM + 1024 * kib));
+  }
+  // job i of n asks for its share
+  template <int N>
+  __device__ __forceinline__ void ask_share(const Next& x, int i) const {
+    if (Ls::kBufs == 1) return;
+#pragma unroll
+    for (int k = 0; k < kAsks; ++k)
+      if (k * N / kAsks == i) ask(x, k);
   }
 
   // the state's planes of k-block p: 32 channels
@@ -228,162 +258,238 @@ struct GradWalk {
     for (int rt = 0; rt < 4; ++rt)
       *reinterpret_cast<f32x4*>(to + (64 * vt + 16 * w + ln) * kChunk + 16 * rt + 4 * gq) = x[rt];
   }
-  // acc = K X
-  __device__ __forceinline__ void against_k(const char* sK, float* slot, f32x4 (&acc)[4]) const {
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt) acc[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int p = 0; p < NKB; ++p) {
-      Fr xf[P], kf[4];
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt) kf[rt] = TK::template row8<Eng>(sK, 16 * rt + ln, 32 * p + 8 * gq);
-      planes(p, xf);
-      if (slot != nullptr) dump(slot, p, p + 1);
-#pragma unroll
-      for (int i = 0; i < P; ++i)
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) Eng::mma(acc[rt], kf[rt], xf[i]);
-    }
-  }
-  // X += A^T B for a tile A of 64 rows, B in planes
-  __device__ __forceinline__ void update(const char* sA, const Fr (&b)[2][P]) {
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      constexpr int kStep = Eng::kSplit ? 4 : 2;   // row tiles whose products alternate
-#pragma unroll
-      for (int tr0 = 0; tr0 < NT; tr0 += kStep) {
-        Fr af[kStep];
-#pragma unroll
-        for (int i = 0; i < kStep; ++i)
-          af[i] = TK::template cols8<Eng, 8>(sA, kb, 32 * ((tr0 + i) / 2) + 4 * (i & 1), ln, gq);
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-#pragma unroll
-          for (int t = 0; t < kStep; ++t) Eng::mma(X[tr0 + t], af[t], b[kb][i]);
-      }
-    }
-  }
-  __device__ __forceinline__ void weights(const float* v, int kb, float (&x)[8]) const {
-    const f32x4 u = *reinterpret_cast<const f32x4*>(v + 32 * kb + 4 * gq);
-    const f32x4 y = *reinterpret_cast<const f32x4*>(v + 32 * kb + 16 + 4 * gq);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[j] = u[j];
-      x[4 + j] = y[j];
-    }
-  }
+  static constexpr int PP = Rec::kPPlanes;
+  static constexpr int kStep = Eng::kSplit ? 4 : 2, NU = 2 * NT / kStep;   // row tiles of a group of the update
+  using Frags = Fr[2 * 3 > kStep ? 2 * 3 : kStep];
 
-  // without a slot X is the state of this chunk alone
-  __device__ __forceinline__ void forward(const char* buf, float* slot, float* err) {
-    const char* sM = buf + Ls::oM;
-    const GradGates& g = *reinterpret_cast<const GradGates*>(buf + Ls::oG);
-    f32x4 acc[4];
-    against_k(buf, slot, acc);
-    Fr xf[2][P];
+  // N groups of products, each group's operands read while the one before runs:
+  // a wave is alone on its SIMD, nothing else covers the reads.  (The barriers
+  // hold the order against the compiler, which moves each read next to its use:
+  // FIGURE)
+  template <int N, class Load, class Work>
+  static __device__ __forceinline__ void pipeline(Load load, Work work) {
+    Frags f[2];
+    load(0, f[0]);
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      float v[8], e[8];
-      frag_values(TV::template cols8<Eng, 4>(buf + Ls::oV, kb, 16 * w, ln, gq), v);
-      weights(g.eg, kb, e);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = fmaf(-e[j], acc[2 * kb + (j >> 2)][j & 3], v[j]);
-      split_planes<Eng, P>(v, xf[kb]);
+    for (int i = 0; i < N; ++i) {
+      if (i + 1 < N) load(i + 1, f[(i + 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+      work(i, f[i & 1]);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    f32x4 er[4];
+  }
+  // K's rows, channels of k-block p
+  __device__ __forceinline__ void rows_k(const char* sK, int p, Frags& f) const {
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt) er[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int rt = 0; rt < 4; ++rt) f[rt] = TK::template row8<Eng>(sK, 16 * rt + ln, 32 * p + 8 * gq);
+  }
+  // the blocks of a plane of the record's matrix, or of its transpose
+  template <bool kT>
+  __device__ __forceinline__ void blocks(const char* p, Frags& f) const {
+    int n = 0;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int rt = kT ? 0 : 2 * kb; rt < (kT ? 2 * kb + 2 : 4); ++rt)
+        f[n++] = kT ? tri_cols<Eng>(p, rt, kb, ln, gq) : tri_rows<Eng>(p, rt, kb, ln, gq);
+  }
+  // acc += (plane i of A, or of A^T) b
+  template <bool kT, int PB>
+  static __device__ __forceinline__ void by_blocks(f32x4 (&acc)[4], const Frags& f, const Fr (&b)[2][PB], int i,
+                                                   int planes) {
+    int n = 0;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int rt = kT ? 0 : 2 * kb; rt < (kT ? 2 * kb + 2 : 4); ++rt, ++n)
+#pragma unroll
+        for (int k = 0; k < PB && plane_pair(i, k, planes); ++k) Eng::mma(acc[rt], f[n], b[kb][k]);
+  }
+  // group u of X += A^T b for a tile A of 64 rows
+  __device__ __forceinline__ void columns(const char* sA, int u, Frags& f) const {
+    const int kb = u / (NT / kStep), tr0 = u % (NT / kStep) * kStep;
+#pragma unroll
+    for (int i = 0; i < kStep; ++i)
+      f[i] = TK::template cols8<Eng, 8>(sA, kb, 32 * ((tr0 + i) / 2) + 4 * (i & 1), ln, gq);
+  }
+  __device__ __forceinline__ void update(int u, const Frags& f, const Fr (&b)[2][P]) {
+    const int kb = u / (NT / kStep), tr0 = u % (NT / kStep) * kStep;
 #pragma unroll
     for (int i = 0; i < P; ++i)
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int rt = 2 * kb; rt < 4; ++rt) {
-          const Fr mf = tri_rows<Eng>(sM + i * Rec::kPlane, rt, kb, ln, gq);
-#pragma unroll
-          for (int k = 0; plane_pair(i, k, P); ++k) Eng::mma(er[rt], mf, xf[kb][k]);
-        }
-    keep(err, er);
-    if (slot == nullptr) return;
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      float u[8], e[8];
-      weights(g.el, kb, u);
-      weights(g.beta, kb, e);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] = u[j] * e[j] * er[2 * kb + (j >> 2)][j & 3];
-      split_planes<Eng, P>(u, xf[kb]);
-    }
-    const float ec = g.ec[0];
+      for (int t = 0; t < kStep; ++t) Eng::mma(X[tr0 + t], f[t], b[kb][i]);
+  }
+  __device__ __forceinline__ void decay(float ec) {
 #pragma unroll
     for (int tr = 0; tr < NT; ++tr)
 #pragma unroll
       for (int r = 0; r < 4; ++r) X[tr][r] *= ec;
-    update(buf, xf);
+  }
+  static __device__ __forceinline__ void zero(f32x4 (&x)[4]) {
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) x[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  // value 8 kb + j: token 16 (2 kb + j / 4) + 4 gq + j % 4
+  __device__ __forceinline__ void weights(const float* v, float (&x)[16]) const {
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) {
+      const f32x4 u = *reinterpret_cast<const f32x4*>(v + 16 * rt + 4 * gq);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[4 * rt + j] = u[j];
+    }
   }
 
-  __device__ __forceinline__ void backward(const char* buf, float* slot, float* dvs) {
+  // kKept: X is the state of this chunk alone
+  __device__ __forceinline__ void forward(const char* buf, float* slot, float* err, const Next& then) {
     const char* sM = buf + Ls::oM;
-    const char* sP = buf + Ls::oP;
     const GradGates& g = *reinterpret_cast<const GradGates*>(buf + Ls::oG);
-    Fr of[2];
+    f32x4 acc[4], er[4];
+    zero(acc);
+    zero(er);
+    float eg[16], el[16], beta[16], ec = 0.0f;
+    Fr vf[2], xf[2][P], pl[2][P];
+    planes(0, pl[0]);
+    pipeline<NKB + P + (kKept ? 0 : NU)>(
+        [&](int i, Frags& f) {
+          if (i < NKB) rows_k(buf, i, f);
+          if (i == NKB - 1) {
+            weights(g.eg, eg);
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) of[kb] = TV::template cols8<Eng, 4>(buf + Ls::oV, kb, 16 * w, ln, gq);
-    f32x4 acc[4], fr[4];
-    against_k(buf, slot, acc);
+            for (int kb = 0; kb < 2; ++kb) vf[kb] = TV::template cols8<Eng, 4>(buf + Ls::oV, kb, 16 * w, ln, gq);
+          }
+          if (i >= NKB && i < NKB + P) blocks<false>(sM + (i - NKB) * Rec::kPlane, f);
+          if (i == NKB + P - 1) {
+            weights(g.el, el);
+            weights(g.beta, beta);
+            ec = g.ec[0];
+          }
+          if (i >= NKB + P) columns(buf, i - NKB - P, f);
+        },
+        [&](int i, const Frags& f) {
+          ask_share<NKB + P>(then, i);
+          if (i < NKB) {
+            if (i + 1 < NKB) planes(i + 1, pl[(i + 1) & 1]);
+            if constexpr (!kKept) dump(slot, i, i + 1);
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt) fr[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            for (int k = 0; k < P; ++k)
 #pragma unroll
-    for (int i = 0; i < Rec::kPPlanes; ++i)
+              for (int rt = 0; rt < 4; ++rt) Eng::mma(acc[rt], f[rt], pl[i & 1][k]);
+          } else if (i < NKB + P) {
+            if (i == NKB) {
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+              for (int kb = 0; kb < 2; ++kb) {
+                float v[8];
+                frag_values(vf[kb], v);
 #pragma unroll
-        for (int rt = 0; rt < 2 * kb + 2; ++rt)
-          Eng::mma(fr[rt], tri_cols<Eng>(sP + i * Rec::kPlane, rt, kb, ln, gq), of[kb]);
-    Fr zf[2][P];
+                for (int j = 0; j < 8; ++j) v[j] = fmaf(-eg[8 * kb + j], acc[2 * kb + (j >> 2)][j & 3], v[j]);
+                split_planes<Eng, P>(v, xf[kb]);
+              }
+            }
+            by_blocks<false>(er, f, xf, i - NKB, P);
+            if (!kKept && i == NKB + P - 1) decay(ec);
+          } else {
+            if (i == NKB + P) {
+              keep(err, er);
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      float e[8], b[8];
-      weights(g.el, kb, e);
-      weights(g.beta, kb, b);
+              for (int kb = 0; kb < 2; ++kb) {
+                float u[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) e[j] = b[j] * fmaf(e[j], acc[2 * kb + (j >> 2)][j & 3], fr[2 * kb + (j >> 2)][j & 3]);
-      split_planes<Eng, P>(e, zf[kb]);
-    }
-    f32x4 y[4];
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt) y[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int rt = 0; rt < 2 * kb + 2; ++rt) {
-          const Fr mf = tri_cols<Eng>(sM + i * Rec::kPlane, rt, kb, ln, gq);
-#pragma unroll
-          for (int k = 0; plane_pair(i, k, P); ++k) Eng::mma(y[rt], mf, zf[kb][k]);
-        }
-    keep(dvs, y);
-    const float ec = g.ec[0];
-#pragma unroll
-    for (int tr = 0; tr < NT; ++tr)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) X[tr][r] *= ec;
-    Fr qf[2][P];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      float o[8], e[8], u[8];
-      frag_values(of[kb], o);
-      weights(g.eg, kb, e);
+                for (int j = 0; j < 8; ++j)
+                  u[j] = el[8 * kb + j] * beta[8 * kb + j] * er[2 * kb + (j >> 2)][j & 3];
+                split_planes<Eng, P>(u, xf[kb]);
+              }
+            }
+            update(i - NKB - P, f, xf);
+          }
+        });
+    if constexpr (kKept) keep(err, er);
+  }
+
+  // The products with K (state) and P, half of the update by dO, Y, the other
+  // half, the update by Y: the updates by dO need nothing of the chain, and
+  // run beside the roundings to planes.
+  __device__ __forceinline__ void backward(const char* buf, float* slot, float* dvs, const Next& then) {
+    const GradGates& g = *reinterpret_cast<const GradGates*>(buf + Ls::oG);
+    constexpr int iP = NKB, iQ = iP + PP, iM = iQ + NU / 2, iR = iM + P, iK = iR + NU / 2, N = iK + NU;
+    f32x4 acc[4], fr[4], y[4];
+    zero(acc);
+    zero(fr);
+    zero(y);
+    float eg[16], el[16], beta[16], ec = 0.0f;
+    Fr of[2][1], qf[2][P], zf[2][P], pl[2][P];
+    planes(0, pl[0]);
+    auto z = [&](int kb) {
+      float e[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        o[j] *= e[j];
-        u[j] = -e[j] * y[2 * kb + (j >> 2)][j & 3];
+        const int rt = 2 * kb + (j >> 2);
+        e[j] = beta[8 * kb + j] * fmaf(el[8 * kb + j], acc[rt][j & 3], fr[rt][j & 3]);
       }
-      split_planes<Eng, P>(o, qf[kb]);
-      split_planes<Eng, P>(u, zf[kb]);
-    }
-    update(buf + Ls::oQ, qf);
-    update(buf, zf);
+      split_planes<Eng, P>(e, zf[kb]);
+    };
+    auto u = [&](int kb) {
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = -eg[8 * kb + j] * y[2 * kb + (j >> 2)][j & 3];
+      split_planes<Eng, P>(x, zf[kb]);
+    };
+    auto o = [&](int kb) {
+      float x[8];
+      frag_values(of[kb][0], x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] *= eg[8 * kb + j];
+      split_planes<Eng, P>(x, qf[kb]);
+    };
+    pipeline<N>(
+        [&](int i, Frags& f) {
+          if (i < iP) rows_k(buf, i, f);
+          if (i == iP - 1) {
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) of[kb][0] = TV::template cols8<Eng, 4>(buf + Ls::oV, kb, 16 * w, ln, gq);
+            weights(g.eg, eg);
+            ec = g.ec[0];
+          }
+          if (i >= iP && i < iQ) blocks<true>(buf + Ls::oP + (i - iP) * Rec::kPlane, f);
+          if (i == iQ - 1) {
+            weights(g.el, el);
+            weights(g.beta, beta);
+          }
+          if (i >= iQ && i < iM) columns(buf + Ls::oQ, i - iQ, f);
+          if (i >= iM && i < iR) blocks<true>(buf + Ls::oM + (i - iM) * Rec::kPlane, f);
+          if (i >= iR && i < iK) columns(buf + Ls::oQ, i - iR + NU / 2, f);
+          if (i >= iK) columns(buf, i - iK, f);
+        },
+        [&](int i, const Frags& f) {
+          ask_share<iR>(then, i);
+          if (i < iP) {
+            if (i + 1 < NKB) planes(i + 1, pl[(i + 1) & 1]);
+            dump(slot, i, i + 1);
+#pragma unroll
+            for (int k = 0; k < P; ++k)
+#pragma unroll
+              for (int rt = 0; rt < 4; ++rt) Eng::mma(acc[rt], f[rt], pl[i & 1][k]);
+          } else if (i < iQ) {
+            if (i == iP) o(0);
+            if (i == (PP > 1 ? iP + 1 : iP)) o(1);
+            if (i == iQ - 1) decay(ec);
+            by_blocks<true>(fr, f, of, i - iP, 8);
+          } else if (i < iM) {
+            if (i == iQ) z(1);
+            if (i == (NU > 2 ? iQ + 1 : iQ)) z(0);
+            update(i - iQ, f, qf);
+          } else if (i < iR) {
+            by_blocks<true>(y, f, zf, i - iM, P);
+          } else if (i < iK) {
+            if (i == iR) {
+              u(0);
+              keep(dvs, y);
+            }
+            if (i == (NU > 2 ? iR + 1 : iR)) u(1);
+            update(i - iR + NU / 2, f, qf);
+          } else {
+            update(i - iK, f, zf);
+          }
+        });
   }
 
   // Rows of a segment behind its sequence: zero gradients.
@@ -410,31 +516,40 @@ struct GradWalk {
     const int nch = (L + kChunk - 1) / kChunk, chunk0 = uniform(a.offs[n]);
     if (kRev && seg0 + L < end) clear_padding(seg0 + L, end);
     load(kRev ? a.d_fin : a.init, n);
-    const bool kept = !kRev && a.kept != nullptr;
     auto chunk = [&](int it) { return kRev ? nch - 1 - it : it; };
-    auto ask_chunk = [&](int it) {
+    auto at = [&](int it) {
       const int c = chunk(it);
-      ask(lds0 + (uint32_t)((it % Ls::kBufs) * Ls::buf), chunk0 + c, seg0 + c * kChunk, min(kChunk, L - c * kChunk));
+      return next(lds0 + (uint32_t)((it % Ls::kBufs) * Ls::buf), chunk0 + c, seg0 + c * kChunk, min(kChunk, L - c * kChunk));
     };
-    if (nch > 0) ask_chunk(0);
+    auto ask_all = [&](int it) {
+      const Next x = at(it);
+#pragma unroll
+      for (int k = 0; k < kAsks; ++k) ask(x, k);
+    };
+    if (nch > 0) ask_all(0);
     for (int it = 0; it < nch; ++it) {
       const char* buf = smem + (it % Ls::kBufs) * Ls::buf;
-      wait_vmem();
-      __syncthreads();   // the chunk's rows are there; the other buffer is free
-      if (Ls::kBufs == 2 && it + 1 < nch) ask_chunk(it + 1);
-      const int64_t at = (int64_t)(chunk0 + chunk(it)) * a.H + h;
-      float* slot = (kRev ? a.R : a.S) + at * a.dv * DK;
+      // the chunk's rows are there (asked for before the last chunk's four stores of E or Y, which may still be
+      // on the way); the other buffer is free
+      if (Ls::kBufs == 2 && it > 0 && !kKept) wait_vmem_but<4>();
+      else wait_vmem();
+      barrier_lds();
+      const int64_t slot = (int64_t)(chunk0 + chunk(it)) * a.H + h;
+      // the last chunk asks for its own rows again, into the other buffer
+      Next then = at(min(it + 1, nch - 1));
+      then.buf = lds0 + (uint32_t)(((it + 1) % Ls::kBufs) * Ls::buf);
       if constexpr (kRev) {
-        backward(buf, slot, a.Y + at * a.dv * kChunk);
+        backward(buf, a.R + slot * a.dv * DK, a.Y + slot * a.dv * kChunk, then);
       } else {
-        forward(buf, kept ? nullptr : slot, a.E + at * a.dv * kChunk);
-        if (kept) load(a.kept, chunk0 + it);
+        forward(buf, a.S + slot * a.dv * DK, a.E + slot * a.dv * kChunk, then);
+        if constexpr (kKept) load(a.kept, chunk0 + it);
       }
       if (Ls::kBufs == 1 && it + 1 < nch) {
-        __syncthreads();
-        ask_chunk(it + 1);
+        barrier_lds();
+        ask_all(it + 1);
       }
     }
+    wait_vmem();   // nothing is on the way into LDS when the wave ends
     if constexpr (kRev) dump(a.d_init + ((int64_t)n * a.H + h) * a.dv * DK);
   }
 };
@@ -453,6 +568,9 @@ __global__ __launch_bounds__(kThreads, 1) void grad_scan_kernel(GradArgs a, int 
   const int tiles = a.dv / 64, vt = item % tiles, nh = item / tiles;
   if (rev) {
     GradWalk<Eng, DK, true> walk(a, nh / a.H, nh % a.H, vt);
+    walk.run(smem);
+  } else if (a.kept != nullptr) {
+    GradWalk<Eng, DK, false, true> walk(a, nh / a.H, nh % a.H, vt);
     walk.run(smem);
   } else {
     GradWalk<Eng, DK, false> walk(a, nh / a.H, nh % a.H, vt);

@@ -205,14 +205,15 @@ struct LinRows {
   // Asked for and on the way (wait_vmem, then a barrier): rows from n on are
   // copies of the last valid one, which no result takes in.
   static __device__ __forceinline__ void ask(uint32_t lds, const E* p, int stride, int n) {
-    const uint32_t at = lds + 16 * 64 * (threadIdx.x >> 6);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int idx = (int)threadIdx.x + NT * i, row = idx / kUnits, u = lin_unit<kUnits>(row, idx % kUnits);
-      if (kAll % NT != 0 && uniform(idx) >= kAll) break;
-      const int r = row < n ? row : n - 1;
-      lds_load16(p, (uint32_t)(r * stride + u * (16 / (int)sizeof(E))) * (uint32_t)sizeof(E), at + 16 * NT * i);
-    }
+    for (int i = 0; i < kPer; ++i) ask_step(i, lds, p, stride, n);
+  }
+  static __device__ __forceinline__ void ask_step(int i, uint32_t lds, const E* p, int stride, int n) {
+    const int idx = (int)threadIdx.x + NT * i, row = idx / kUnits, u = lin_unit<kUnits>(row, idx % kUnits);
+    if (kAll % NT != 0 && uniform(idx) >= kAll) return;
+    const int r = row < n ? row : n - 1;
+    lds_load16(p, (uint32_t)(r * stride + u * (16 / (int)sizeof(E))) * (uint32_t)sizeof(E),
+               lds + 16 * 64 * (threadIdx.x >> 6) + 16 * NT * i);
   }
   // Through registers, in two halves; rows from n on are 0.
   static __device__ __forceinline__ void fetch(uint4 (&x)[kPer], const E* p, int stride, int n) {
