@@ -297,13 +297,14 @@ struct GradWalk {
   template <bool kT, int PB>
   static __device__ __forceinline__ void by_blocks(f32x4 (&acc)[4], const Frags& f, const Fr (&b)[2][PB], int i,
                                                    int planes) {
-    int n = 0;
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int k = 0; k < PB && plane_pair(i, k, planes); ++k) {
+      int n = 0;
 #pragma unroll
-      for (int rt = kT ? 0 : 2 * kb; rt < (kT ? 2 * kb + 2 : 4); ++rt, ++n)
+      for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int k = 0; k < PB && plane_pair(i, k, planes); ++k) Eng::mma(acc[rt], f[n], b[kb][k]);
+        for (int rt = kT ? 0 : 2 * kb; rt < (kT ? 2 * kb + 2 : 4); ++rt, ++n) Eng::mma(acc[rt], f[n], b[kb][k]);
+    }
   }
   // group u of X += A^T b for a tile A of 64 rows
   __device__ __forceinline__ void columns(const char* sA, int u, Frags& f) const {
@@ -613,8 +614,8 @@ struct GradChunkLds {
   static constexpr int oKS = oQS + 4 * kChunk * 4;          // [4][64] k.(Y S)
   static constexpr int oT = oKS + 4 * kChunk * 4;           // [10][16] the pairs' part of p
   static constexpr int oZ = oT + 10 * 16 * 4;               // [4] <R, S>
-  static constexpr int oO = oZ + 4 * 8;                     // dO, then planes of Y and of E, [column][token]
-  static constexpr int oY = oO + kStep;
+  static constexpr int oO = oZ + 4 * 8;                     // dO, twice, then planes of Y and of E, [column][token]
+  static constexpr int oY = oO + 2 * kStep;
   static constexpr int oE = oY + P * kStep;
   static constexpr int oW = oO;                             // last W and N
   static constexpr int oN = oW + P2 * GradRec<Eng>::kPlane;
@@ -677,7 +678,7 @@ __global__ __launch_bounds__(kThreads, Eng::kSplit ? 2 : 1) void grad_chunk_kern
   }
   // this wave's share: channels 32 wc .. 32 wc + 31, token tiles TPW tg ..
   constexpr int CP = DK / 32, TG = 4 / CP, TPW = 4 / TG;
-  const int wc = w % CP, tg = w / CP;
+  const int wc = w % CP, tg = TG == 1 ? 0 : w / CP;
   // the entering state (kept, the initial one, or the chain's) and the leaving one's gradient
   const int64_t state = (int64_t)dv * DK;
   const float* ps = a.kept == nullptr ? a.S + ch * state
@@ -693,21 +694,19 @@ __global__ __launch_bounds__(kThreads, Eng::kSplit ? 2 : 1) void grad_chunk_kern
   // what the next step needs, on the way
   f32x2 sx[8], rx[8];        // columns kperm, channels 32 wc + 2 ln ..
   f32x4 ex[2], yx[2];        // column tid / 16 (+ 16), tokens 4 (tid % 16) ..
-  uint4 ox[RO::kPer];
-  auto fetch_state = [&](f32x2 (&x)[8], const float* p, int h0) {
-    const int l = fresh_lane(), at = 4 * (l >> 4) * DK + 2 * (l & 15);
+  auto fetch_state = [&](f32x2 (&x)[8], const float* p, int h0, int lanes) {
+    const int l = fresh_lane(), at = (4 * (l >> 4) * DK + 2 * (l & 15)) & lanes;
     const float* c = p + (h0 * DK + 32 * wc);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       x[i] = *reinterpret_cast<const f32x2*>(c + at + ((i & 3) + 16 * (i >> 2)) * DK);
   };
-  auto fetch_rows = [&](int h0) {
+  auto fetch_rows = [&](int h0, int lanes) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      ex[i] = *reinterpret_cast<const f32x4*>(pe_ + (h0 * kChunk + 1024 * i) + 4 * tid);
-      yx[i] = *reinterpret_cast<const f32x4*>(py_ + (h0 * kChunk + 1024 * i) + 4 * tid);
+      ex[i] = *reinterpret_cast<const f32x4*>(pe_ + (h0 * kChunk + 1024 * i) + (4 * tid & lanes));
+      yx[i] = *reinterpret_cast<const f32x4*>(py_ + (h0 * kChunk + 1024 * i) + (4 * tid & lanes));
     }
-    RO::fetch(ox, po + h0, H * dv, nv);
   };
   auto put_rows = [&](char* to, const f32x4 (&x)[2]) {   // planes, [column][token]
     const int l = w * 64 + fresh_lane();
@@ -738,15 +737,17 @@ __global__ __launch_bounds__(kThreads, Eng::kSplit ? 2 : 1) void grad_chunk_kern
   double z = 0.0;
   f32x4 dots = {0.0f, 0.0f, 0.0f, 0.0f};   // Y.E of tokens 4 (tid % 16) ..
 
-  fetch_rows(0);
-  fetch_state(sx, ps, 0);
-  fetch_state(rx, pr, 0);
+  RO::ask(lds0 + Ls::oO, po, H * dv, nv);
+  fetch_rows(0, ~0);
+  fetch_state(sx, ps, 0, ~0);
+  fetch_state(rx, pr, 0, ~0);
+  __builtin_amdgcn_sched_barrier(0);
   for (int h0 = 0; h0 < dv; h0 += HV) {
-    const int hn = min(h0 + HV, dv - HV);   // the last step asks for itself again
+    // the last step has no next one: each of its loads is of one place (a branch cost 48 registers' spills)
+    const int hn = min(h0 + HV, dv - HV), lanes = h0 + HV < dv ? ~0 : 0;
     if (h0 > 0) barrier_lds();              // the last columns are consumed
     put_rows(smem + Ls::oY, yx);
     put_rows(smem + Ls::oE, ex);
-    RO::put(smem + Ls::oO, ox);
     if (none) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) sx[i] = f32x2{0.0f, 0.0f};
@@ -765,17 +766,19 @@ __global__ __launch_bounds__(kThreads, Eng::kSplit ? 2 : 1) void grad_chunk_kern
       for (int i = 0; i < 8; ++i) zs = fmaf(sx[i][m], rx[i][m], zs);
     }
     z += (double)zs;
-    fetch_state(sx, ps, hn);
-    if (h0 == 0) wait_vmem();   // K, Q, gates
+    // dO, and first K, Q and the gates; R's eight loads came last
+    wait_vmem_but<8>();
     barrier_lds();
+    fetch_state(sx, ps, hn, lanes);
     __builtin_amdgcn_sched_barrier(0);
 
     // S against dO and Y
+    const char* sO = smem + Ls::oO + (h0 / HV & 1) * Ls::kStep;
     const int l = fresh_lane(), ln = l & 15, gq = l >> 4;
 #pragma unroll
     for (int t = 0; t < TPW; ++t) {
       const int tile = TPW * tg + t;
-      const Fr of = row_kperm<Eng, TO>(smem + Ls::oO, 16 * tile + ln, 0, gq);
+      const Fr of = row_kperm<Eng, TO>(sO, 16 * tile + ln, 0, gq);
       Fr yf[P];
 #pragma unroll
       for (int i = 0; i < P; ++i)
@@ -793,13 +796,15 @@ __global__ __launch_bounds__(kThreads, Eng::kSplit ? 2 : 1) void grad_chunk_kern
         for (int k = 0; plane_pair(i, k, P); ++k)
 #pragma unroll
           for (int m = 0; m < 2; ++m) Eng::mma(ax[t][m], sf[m][i], yf[k]);
-      if (t == wc) {   // d_v: the first plane is Y rounded to bf16
-        const int tok = 16 * tile + ln;
-        if (tok < nv) put_dv<Eng>((E*)a.d_v + (row0 + (int64_t)tok * H) * dv + h0 + 4 * gq, yf[0], g.zero[tok] != 0.0f);
-      }
       __builtin_amdgcn_sched_barrier(0);   // reads in flight stay within the registers
     }
-    fetch_rows(hn);
+    if (lanes) RO::ask(lds0 + Ls::oO + (h0 / HV + 1 & 1) * Ls::kStep, po + hn, H * dv, nv);
+    fetch_rows(hn, lanes);
+    // d_v, 16 tokens a wave: the first plane is Y rounded to bf16
+    const Fr yw = TY::template cols8<Eng, 4>(smem + Ls::oY, 0, 16 * w, ln, gq);
+    if (16 * w + ln < nv)
+      put_dv<Eng>((E*)a.d_v + row0 * dv + h0 + (uint32_t)((16 * w + ln) * H * dv + 4 * gq), yw,
+                  g.zero[16 * w + ln] != 0.0f);
     // R against E
     Fr rf[2][P2];
 #pragma unroll
@@ -807,7 +812,7 @@ __global__ __launch_bounds__(kThreads, Eng::kSplit ? 2 : 1) void grad_chunk_kern
       const float x8[8] = {rx[0][m], rx[1][m], rx[2][m], rx[3][m], rx[4][m], rx[5][m], rx[6][m], rx[7][m]};
       split_planes<Eng, P2>(x8, rf[m]);
     }
-    fetch_state(rx, pr, hn);
+    fetch_state(rx, pr, hn, lanes);
 #pragma unroll
     for (int t = 0; t < TPW; ++t) {
       Fr ef[P2];
@@ -828,7 +833,7 @@ __global__ __launch_bounds__(kThreads, Eng::kSplit ? 2 : 1) void grad_chunk_kern
       if (w + 4 * i >= 10) break;
       int Tt, St;
       tri_of(w + 4 * i, Tt, St);
-      const Fr of = row_kperm<Eng, TO>(smem + Ls::oO, 16 * Tt + ln, 0, gq);
+      const Fr of = row_kperm<Eng, TO>(sO, 16 * Tt + ln, 0, gq);
       Fr ef[P], yf[P];
 #pragma unroll
       for (int k = 0; k < P; ++k) {
@@ -848,8 +853,10 @@ __global__ __launch_bounds__(kThreads, Eng::kSplit ? 2 : 1) void grad_chunk_kern
 
   const int l64 = fresh_lane(), ln = l64 & 15, gq = l64 >> 4;
   auto over_quads = [](float v) {   // lanes ln, 16 + ln, 32 + ln, 48 + ln
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
+    const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+    const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(y[0]) + __uint_as_float(y[1]);
   };
   float* sYE = reinterpret_cast<float*>(smem + Ls::oYE);
   float* sQS = reinterpret_cast<float*>(smem + Ls::oQS);
