@@ -953,7 +953,7 @@ static hipError_t launch_sched(const gdn_shape_t& s, const ChunkArgs& a, hipStre
 }
 
 // Compute units of the current device (0 when it cannot be read).
-static int device_cu_count() {
+int device_cu_count() {
   static int cached[64] = {0};
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0) return 0;

@@ -56,7 +56,7 @@ GradLayout grad_layout(const gdn_shape_t& s, bool given) {
 bool grad_fits(const gdn_shape_t& s) {
   const int64_t chunks = (s.total_tokens + kChunk - 1) / kChunk + s.n_seqs;
   return chunks * s.n_heads < ((int64_t)1 << 32) / 512 &&
-         (int64_t)s.n_seqs * s.n_heads * (s.dv / 64) < ((int64_t)1 << 32) / (2 * kThreads);
+         (int64_t)s.n_seqs * s.n_heads * (s.dv / 64) < ((int64_t)1 << 32) / (4 * kThreads);   // two directions, 512 threads
 }
 
 size_t grad_workspace_bytes(const gdn_shape_t& s, bool given) { return grad_layout(s, given).bytes; }

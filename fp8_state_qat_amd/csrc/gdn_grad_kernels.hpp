@@ -144,49 +144,65 @@ __global__ __launch_bounds__(kThreads) void grad_prep_kernel(GradArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// The chains.  A workgroup of four waves walks one sequence and head for 64
-// value columns, forwards (S) or backwards (R); wave w holds columns 16 w ..
-// 16 w + 15 of the transposed state in accumulators (rows: key channels as
-// dkmap orders them), which are the B operand of K S^T as they stand; X, E,
-// U follow the same way, from registers to registers.
+// The chains.  A workgroup of 2 CG waves walks one sequence and head for 16 CG
+// value columns, forwards (S) or backwards (R).  A pair of waves holds 16 columns
+// of the transposed state in accumulators, wave HS of it half HS of the key
+// channels (rows, as dkmap orders them), which are the B operand of K S^T as they
+// stand.  A chunk's chain of products is long and each depends on the one before:
+// two waves on a SIMD run beside each other where one waits, and each does half of
+// every product.  K S^T is a sum over the channels: the waves swap halves of their
+// sums, and wave HS goes on with tokens 32 HS .. 32 HS + 31, whose half of the
+// triangular product it also forms (half kb of the operand is known to the wave
+// kb; the other needs it where the triangle does); the halves of its result are
+// swapped again for the state's update.
 // ---------------------------------------------------------------------------
-template <class Eng, int DK>
+template <class Eng, int DK, int CG>
 struct GradScanLds {
   using E = typename Eng::E;
   static constexpr int kTile = kChunk * DK * (int)sizeof(E);
-  static constexpr int kVTile = kChunk * 64 * (int)sizeof(E);
+  static constexpr int kVTile = kChunk * 16 * CG * (int)sizeof(E);
   static constexpr int oQ = kTile;                                 // backwards only
   static constexpr int oV = 2 * kTile;                             // V, or dO
   static constexpr int oM = oV + kVTile;
   static constexpr int oP = oM + GradRec<Eng>::oP;
   static constexpr int oG = oM + GradRec<Eng>::oG;
   static constexpr int buf = oG + 1024;
-  static constexpr int kBufs = 2 * buf <= 160 * 1024 ? 2 : 1;
-  static constexpr int bytes = kBufs * buf;
+  // what the waves of a pair swap: 2 KiB of sums for either, later planes in
+  // their place; the other planes in the place of P, which is consumed by then
+  // (forwards it is not there at all)
+  static constexpr int kSwap = 4096, kPlanes = (Eng::kSplit ? 3 : 1) * 64 * 8 * (int)sizeof(E);
+  static_assert(kPlanes <= kSwap && CG * kPlanes <= GradRec<Eng>::oG - GradRec<Eng>::oP, "the swaps' places");
+  static constexpr int kBufs = 2 * buf + CG * kSwap <= 160 * 1024 ? 2 : 1;
+  static constexpr int oSwap = kBufs * buf;
+  static constexpr int bytes = oSwap + CG * kSwap;
+  static_assert(bytes <= 160 * 1024, "LDS budget exceeded");
 };
 
-template <class Eng, int DK, bool kRev, bool kKept = false>
+template <class Eng, int DK, int CG, int HS, bool kRev, bool kKept = false>
 struct GradWalk {
   using E = typename Eng::E;
   using Fr = typename Eng::Fr;
   using TK = LinTile<E, DK>;
-  using TV = LinTile<E, 64>;
-  using Ls = GradScanLds<Eng, DK>;
+  using TV = LinTile<E, 16 * CG>;
+  using Ls = GradScanLds<Eng, DK, CG>;
   using Rec = GradRec<Eng>;
-  static constexpr int NT = DK / 16, NKB = DK / 32;
+  static constexpr int kT = 128 * CG, kW = 2 * CG;      // threads, waves
+  static constexpr int NT = DK / 32, NKB = DK / 64;     // of this wave's channels
   static constexpr int P = Eng::kSplit ? 3 : 1;   // planes of what the states are formed from
 
   const GradArgs& a;
   const int n, h, vt, w, ln, gq;
+  char* const smem;
   f32x4 X[NT];
 
-  __device__ __forceinline__ GradWalk(const GradArgs& args, int seq, int head, int tile)
+  __device__ __forceinline__ GradWalk(const GradArgs& args, int seq, int head, int tile, char* lds)
       : a(args), n(seq), h(head), vt(tile), w(uniform(threadIdx.x >> 6)), ln(threadIdx.x & 15),
-        gq((threadIdx.x >> 4) & 3) {}
+        gq((threadIdx.x >> 4) & 3), smem(lds) {}
 
+  __device__ __forceinline__ int col0() const { return 16 * (w % CG); }   // of the tile
   // element of a [dv][dk] state that X[tr][0] of this lane is
   __device__ __forceinline__ int at(int tr) const {
-    return (64 * vt + 16 * w + ln) * DK + 32 * (tr / 2) + 8 * gq + 4 * (tr & 1);
+    return (16 * CG * vt + col0() + ln) * DK + DK / 2 * HS + 32 * (tr / 2) + 8 * gq + 4 * (tr & 1);
   }
   // the state of entry i of p's
   __device__ __forceinline__ void load(const float* p, int64_t i) {
@@ -198,37 +214,49 @@ struct GradWalk {
   }
 
   // What the next chunk needs, in kAsks steps: a step's load for each wave
-  // (records: wave w the KiB w, w + 4, ..; the gates beside M's last).
-  using RK = LinRows<E, DK, kThreads>;
-  using RV = LinRows<E, 64, kThreads>;
+  // (records: wave w the KiB w, w + kW, ..; the gates beside the last).
+  using RK = LinRows<E, DK, kT>;
+  using RV = LinRows<E, 16 * CG, kT>;
   static constexpr int kRecKiB = (kRev ? Rec::oG : Rec::oP) / 1024;
-  static constexpr int kAsks = RK::kPer * (kRev ? 2 : 1) + RV::kPer + (kRecKiB + 4) / 4;
+  static constexpr int kAsks = RK::kPer * (kRev ? 2 : 1) + RV::kPer + (kRecKiB + kW) / kW;
   struct Next {
-    uint32_t buf;
+    uint32_t buf;   // of this wave: + 1024 w
     const E *k, *q, *v;
     const char* rec;
-    int nv;
   };
-  __device__ __forceinline__ Next next(uint32_t buf, int j, int t0, int nv) const {
+  uint32_t ko[RK::kPer], vo[RV::kPer];   // this lane's bytes from them, for chunks of `rows` rows
+  int rows = -1;
+  __device__ __forceinline__ Next next(uint32_t buf, int j, int t0, int nv) {
+    if (nv != rows) {   // rows from nv on are copies of the last valid one, which no result takes in
+      rows = nv;
+#pragma unroll
+      for (int i = 0; i < RK::kPer; ++i) ko[i] = RK::offset(i, a.H * DK, nv);
+#pragma unroll
+      for (int i = 0; i < RV::kPer; ++i) vo[i] = RV::offset(i, a.H * a.dv, nv);
+    }
     const int64_t row0 = (int64_t)t0 * a.H + h;
-    return Next{buf, (const E*)a.k + row0 * DK, (const E*)a.q + row0 * DK,
-                (const E*)(kRev ? a.d_o : a.v) + row0 * a.dv + 64 * vt,
-                a.rec + ((int64_t)j * a.H + h) * Rec::kBytes, nv};
+    return Next{buf + 1024 * w, (const E*)a.k + row0 * DK, (const E*)a.q + row0 * DK,
+                (const E*)(kRev ? a.d_o : a.v) + row0 * a.dv + 16 * CG * vt,
+                a.rec + ((int64_t)j * a.H + h) * Rec::kBytes + 1024 * w};
   }
   __device__ __forceinline__ void ask(const Next& x, int i) const {
-    if (i < RK::kPer) return RK::ask_step(i, x.buf, x.k, a.H * DK, x.nv);
+    if (i < RK::kPer) return lds_load16(x.k, ko[i], x.buf + 16 * kT * i);
     i -= RK::kPer;
     if (kRev) {
-      if (i < RK::kPer) return RK::ask_step(i, x.buf + Ls::oQ, x.q, a.H * DK, x.nv);
+      if (i < RK::kPer) return lds_load16(x.q, ko[i], x.buf + Ls::oQ + 16 * kT * i);
       i -= RK::kPer;
     }
-    if (i < RV::kPer) return RV::ask_step(i, x.buf + Ls::oV, x.v, a.H * a.dv, x.nv);
+    if (i < RV::kPer) {
+      if (RV::kAll % kT == 0 || 64 * w + kT * i < RV::kAll) lds_load16(x.v, vo[i], x.buf + Ls::oV + 16 * kT * i);
+      return;
+    }
     i -= RV::kPer;
-    const int kib = 4 * i + w;
-    if (4 * i + 3 > kRecKiB && kib > kRecKiB) return;
-    const bool gates = 4 * i + 3 >= kRecKiB && kib == kRecKiB;
-    lds_load16(x.rec + (gates ? Rec::oG : 1024 * kib), (uint32_t)(threadIdx.x & 63) * 16,
-               x.buf + (gates ? Ls::oG : Ls::oM + 1024 * kib));
+    const uint32_t lane16 = (uint32_t)(16 * (16 * gq + ln));
+    if (kW * (i + 1) <= kRecKiB || kW * i + w < kRecKiB) {
+      lds_load16(x.rec + 1024 * kW * i, lane16, x.buf + Ls::oM + 1024 * kW * i);
+    } else if (kW * i + w == kRecKiB) {
+      lds_load16(x.rec - 1024 * w + Rec::oG, lane16, x.buf - 1024 * w + Ls::oG);
+    }
   }
   // job i of n asks for its share
   template <int N>
@@ -252,20 +280,20 @@ struct GradWalk {
     for (int tr = 2 * p0; tr < 2 * p1; ++tr)
       *reinterpret_cast<f32x4*>(slot + at(tr)) = X[tr];
   }
-  // E or Y for the gradients' kernel, transposed: a token row for each value column
-  __device__ __forceinline__ void keep(float* to, const f32x4 (&x)[4]) const {
+  // this wave's tokens of E or Y for the gradients' kernel, transposed: a token row for each value column
+  __device__ __forceinline__ void keep(float* to, const f32x4 (&x)[2]) const {
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt)
-      *reinterpret_cast<f32x4*>(to + (64 * vt + 16 * w + ln) * kChunk + 16 * rt + 4 * gq) = x[rt];
+    for (int r = 0; r < 2; ++r)
+      *reinterpret_cast<f32x4*>(to + (16 * CG * vt + col0() + ln) * kChunk + 32 * HS + 16 * r + 4 * gq) = x[r];
   }
   static constexpr int PP = Rec::kPPlanes;
-  static constexpr int kStep = Eng::kSplit ? 4 : 2, NU = 2 * NT / kStep;   // row tiles of a group of the update
-  using Frags = Fr[2 * 3 > kStep ? 2 * 3 : kStep];
+  static constexpr int kMax = Eng::kSplit ? 4 : 2, kStep = NT < kMax ? NT : kMax;   // row tiles of a group of the update
+  static constexpr int NU = 2 * NT / kStep;
+  using Frags = Fr[6];
 
-  // N groups of products, each group's operands read while the one before runs:
-  // a wave is alone on its SIMD, nothing else covers the reads.  (The barriers
-  // hold the order against the compiler, which moves each read next to its use:
-  // FIGURE)
+  // N groups of products, each group's operands read while the one before runs
+  // (the barriers hold the order against the compiler, which moves each read next
+  // to its use).
   template <int N, class Load, class Work>
   static __device__ __forceinline__ void pipeline(Load load, Work work) {
     Frags f[2];
@@ -278,40 +306,50 @@ struct GradWalk {
       __builtin_amdgcn_sched_barrier(0);
     }
   }
-  // K's rows, channels of k-block p
+  // K's rows, channels of this wave's k-block p
   __device__ __forceinline__ void rows_k(const char* sK, int p, Frags& f) const {
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt) f[rt] = TK::template row8<Eng>(sK, 16 * rt + ln, 32 * p + 8 * gq);
+    for (int rt = 0; rt < 4; ++rt) f[rt] = TK::template row8<Eng>(sK, 16 * rt + ln, DK / 2 * HS + 32 * p + 8 * gq);
   }
-  // the blocks of a plane of the record's matrix, or of its transpose
-  template <bool kT>
-  __device__ __forceinline__ void blocks(const char* p, Frags& f) const {
+  // P^T's blocks (a plane): row tile rt, k-blocks from rt / 2 on
+  __device__ __forceinline__ void blocks_p(const char* p, Frags& f) const {
     int n = 0;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-      for (int rt = kT ? 0 : 2 * kb; rt < (kT ? 2 * kb + 2 : 4); ++rt)
-        f[n++] = kT ? tri_cols<Eng>(p, rt, kb, ln, gq) : tri_rows<Eng>(p, rt, kb, ln, gq);
+      for (int rt = 0; rt < 2 * kb + 2; ++rt) f[n++] = tri_cols<Eng>(p, rt, kb, ln, gq);
   }
-  // acc += (plane i of A, or of A^T) b
-  template <bool kT, int PB>
-  static __device__ __forceinline__ void by_blocks(f32x4 (&acc)[4], const Frags& f, const Fr (&b)[2][PB], int i,
-                                                   int planes) {
+  __device__ __forceinline__ void by_p(f32x4 (&acc)[4], const Frags& f, const Fr (&b)[2]) const {
+    int n = 0;
 #pragma unroll
-    for (int k = 0; k < PB && plane_pair(i, k, planes); ++k) {
-      int n = 0;
+    for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+      for (int rt = 0; rt < 2 * kb + 2; ++rt) Eng::mma(acc[rt], f[n++], b[kb]);
+  }
+  // M's blocks (or M^T's) of this wave's tokens: k-blocks up to HS (from HS on)
+  static constexpr int kb0 = kRev ? HS : 0, kb1 = kRev ? 2 : HS + 1;
+  __device__ __forceinline__ void blocks_m(const char* p, Frags& f) const {
 #pragma unroll
-        for (int rt = kT ? 0 : 2 * kb; rt < (kT ? 2 * kb + 2 : 4); ++rt, ++n) Eng::mma(acc[rt], f[n], b[kb][k]);
-    }
+    for (int kb = kb0; kb < kb1; ++kb)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        f[2 * (kb - kb0) + r] = kRev ? tri_cols<Eng>(p, 2 * HS + r, kb, ln, gq) : tri_rows<Eng>(p, 2 * HS + r, kb, ln, gq);
+  }
+  // acc += (plane i) b
+  __device__ __forceinline__ void by_m(f32x4 (&acc)[2], const Frags& f, const Fr (&b)[2][P], int i) const {
+#pragma unroll
+    for (int k = 0; plane_pair(i, k, P); ++k)
+#pragma unroll
+      for (int kb = kb0; kb < kb1; ++kb)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) Eng::mma(acc[r], f[2 * (kb - kb0) + r], b[kb][k]);
   }
   // group u of X += A^T b for a tile A of 64 rows
   __device__ __forceinline__ void columns(const char* sA, int u, Frags& f) const {
     const int kb = u / (NT / kStep), tr0 = u % (NT / kStep) * kStep;
 #pragma unroll
     for (int i = 0; i < kStep; ++i)
-      f[i] = TK::template cols8<Eng, 8>(sA, kb, 32 * ((tr0 + i) / 2) + 4 * (i & 1), ln, gq);
+      f[i] = TK::template cols8<Eng, 8>(sA, kb, DK / 2 * HS + 32 * ((tr0 + i) / 2) + 4 * (i & 1), ln, gq);
   }
   __device__ __forceinline__ void update(int u, const Frags& f, const Fr (&b)[2][P]) {
     const int kb = u / (NT / kStep), tr0 = u % (NT / kStep) * kStep;
@@ -326,117 +364,147 @@ struct GradWalk {
 #pragma unroll
       for (int r = 0; r < 4; ++r) X[tr][r] *= ec;
   }
-  static __device__ __forceinline__ void zero(f32x4 (&x)[4]) {
+  template <int N>
+  static __device__ __forceinline__ void zero(f32x4 (&x)[N]) {
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt) x[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int rt = 0; rt < N; ++rt) x[rt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  // value 8 kb + j: token 16 (2 kb + j / 4) + 4 gq + j % 4
-  __device__ __forceinline__ void weights(const float* v, float (&x)[16]) const {
+  // of tokens 16 rt + 4 gq + j, rt from r0 on
+  template <int N>
+  __device__ __forceinline__ void weights(const float* v, int r0, float (&x)[N]) const {
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt) {
-      const f32x4 u = *reinterpret_cast<const f32x4*>(v + 16 * rt + 4 * gq);
+    for (int r = 0; r < N / 4; ++r) {
+      const f32x4 u = *reinterpret_cast<const f32x4*>(v + 16 * (r0 + r) + 4 * gq);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[4 * rt + j] = u[j];
+      for (int j = 0; j < 4; ++j) x[4 * r + j] = u[j];
     }
+  }
+
+  // The pair's swaps.  The receiver is the wave whose half of the triangular
+  // product needs the other's (the sender's) half of the operand.
+  static constexpr bool kReceiver = kRev == (HS == 0);
+  __device__ __forceinline__ char* swap() const { return smem + Ls::oSwap + (w % CG) * Ls::kSwap; }
+  __device__ __forceinline__ int lane() const { return 16 * gq + ln; }
+  __device__ __forceinline__ void give_sums(const f32x4 (&x)[4]) const {   // the other's tokens
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      reinterpret_cast<f32x4*>(swap() + 2048 * (1 - HS))[64 * r + lane()] = x[2 * (1 - HS) + r];
+  }
+  __device__ __forceinline__ f32x4 other_sums(int r) const {
+    return reinterpret_cast<const f32x4*>(swap() + 2048 * HS)[64 * r + lane()];
+  }
+  static __device__ __forceinline__ void put_planes(char* p, int lane, const Fr (&f)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) Eng::st((E*)p + 8 * (64 * i + lane), f[i]);
+  }
+  static __device__ __forceinline__ void get_planes(const char* p, int lane, Fr (&f)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) f[i] = Eng::ld((const E*)p + 8 * (64 * i + lane));
+  }
+  __device__ __forceinline__ char* swap_p(const char* buf) const {
+    return const_cast<char*>(buf) + Ls::oP + (w % CG) * Ls::kPlanes;
+  }
+  __device__ __forceinline__ void give_half(const char* buf, const Fr (&f)[P]) const {
+    if constexpr (!kReceiver) put_planes(swap_p(buf), lane(), f);
+  }
+  __device__ __forceinline__ void other_half(const char* buf, Fr (&f)[P]) const {
+    if constexpr (kReceiver) get_planes(swap_p(buf), lane(), f);
+  }
+  __device__ __forceinline__ void give_update(const char* buf, const Fr (&f)[P]) const {
+    put_planes(kReceiver ? swap_p(buf) : swap(), lane(), f);
+  }
+  __device__ __forceinline__ void other_update(const char* buf, Fr (&f)[P]) const {
+    get_planes(kReceiver ? swap() : swap_p(buf), lane(), f);
   }
 
   // kKept: X is the state of this chunk alone
   __device__ __forceinline__ void forward(const char* buf, float* slot, float* err, const Next& then) {
     const char* sM = buf + Ls::oM;
     const GradGates& g = *reinterpret_cast<const GradGates*>(buf + Ls::oG);
-    f32x4 acc[4], er[4];
+    constexpr int iM = NKB, iK = iM + P, N = kKept ? iK : iK + NU;
+    f32x4 acc[4], er[2];
     zero(acc);
     zero(er);
-    float eg[16], el[16], beta[16], ec = 0.0f;
-    Fr vf[2], xf[2][P], pl[2][P];
+    float eg[8], el[8], beta[8], ec = 0.0f;
+    Fr vf, xf[2][P], pl[2][P];
     planes(0, pl[0]);
-    pipeline<NKB + P + (kKept ? 0 : NU)>(
+    pipeline<N>(
         [&](int i, Frags& f) {
-          if (i < NKB) rows_k(buf, i, f);
-          if (i == NKB - 1) {
-            weights(g.eg, eg);
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) vf[kb] = TV::template cols8<Eng, 4>(buf + Ls::oV, kb, 16 * w, ln, gq);
-          }
-          if (i >= NKB && i < NKB + P) blocks<false>(sM + (i - NKB) * Rec::kPlane, f);
-          if (i == NKB + P - 1) {
-            weights(g.el, el);
-            weights(g.beta, beta);
+          if (i < iM) rows_k(buf, i, f);
+          if (i == iM - 1) {
+            weights(g.eg, 2 * HS, eg);
+            vf = TV::template cols8<Eng, 4>(buf + Ls::oV, HS, col0(), ln, gq);
             ec = g.ec[0];
           }
-          if (i >= NKB + P) columns(buf, i - NKB - P, f);
+          if (i >= iM && i < iK) blocks_m(sM + (i - iM) * Rec::kPlane, f);
+          if (i == iK - 1) {
+            weights(g.el, 2 * HS, el);
+            weights(g.beta, 2 * HS, beta);
+          }
+          if (i >= iK) columns(buf, i - iK, f);
         },
         [&](int i, const Frags& f) {
-          ask_share<NKB + P>(then, i);
-          if (i < NKB) {
+          ask_share<iK>(then, i);
+          if (i < iM) {
             if (i + 1 < NKB) planes(i + 1, pl[(i + 1) & 1]);
             if constexpr (!kKept) dump(slot, i, i + 1);
 #pragma unroll
             for (int k = 0; k < P; ++k)
 #pragma unroll
               for (int rt = 0; rt < 4; ++rt) Eng::mma(acc[rt], f[rt], pl[i & 1][k]);
-          } else if (i < NKB + P) {
-            if (i == NKB) {
+          } else if (i < iK) {
+            if (i == iM) {
+              give_sums(acc);
+              if constexpr (!kKept) decay(ec);
+              barrier_lds();
+              float v[8];
+              frag_values(vf, v);
 #pragma unroll
-              for (int kb = 0; kb < 2; ++kb) {
-                float v[8];
-                frag_values(vf[kb], v);
+              for (int r = 0; r < 2; ++r) {
+                const f32x4 y = other_sums(r);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = fmaf(-eg[8 * kb + j], acc[2 * kb + (j >> 2)][j & 3], v[j]);
-                split_planes<Eng, P>(v, xf[kb]);
+                for (int j = 0; j < 4; ++j) v[4 * r + j] = fmaf(-eg[4 * r + j], acc[2 * HS + r][j] + y[j], v[4 * r + j]);
               }
+              split_planes<Eng, P>(v, xf[HS]);
+              give_half(buf, xf[HS]);
+              barrier_lds();
+              other_half(buf, xf[1 - HS]);
             }
-            by_blocks<false>(er, f, xf, i - NKB, P);
-            if (!kKept && i == NKB + P - 1) decay(ec);
+            by_m(er, f, xf, i - iM);
           } else {
-            if (i == NKB + P) {
+            if (i == iK) {
               keep(err, er);
+              float u[8];
 #pragma unroll
-              for (int kb = 0; kb < 2; ++kb) {
-                float u[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  u[j] = el[8 * kb + j] * beta[8 * kb + j] * er[2 * kb + (j >> 2)][j & 3];
-                split_planes<Eng, P>(u, xf[kb]);
-              }
+              for (int j = 0; j < 8; ++j) u[j] = el[j] * beta[j] * er[j >> 2][j & 3];
+              split_planes<Eng, P>(u, xf[HS]);
+              give_update(buf, xf[HS]);
+              barrier_lds();
+              other_update(buf, xf[1 - HS]);
             }
-            update(i - NKB - P, f, xf);
+            update(i - iK, f, xf);
           }
         });
     if constexpr (kKept) keep(err, er);
   }
 
-  // The products with K (state) and P, half of the update by dO, Y, the other
-  // half, the update by Y: the updates by dO need nothing of the chain, and
-  // run beside the roundings to planes.
+  // The products with K (state) and P (the first wave one plane, the second the
+  // others: it has less of M), the update by dO, which needs nothing of the chain,
+  // in two parts beside the swaps, Y, the update by Y.
   __device__ __forceinline__ void backward(const char* buf, float* slot, float* dvs, const Next& then) {
     const GradGates& g = *reinterpret_cast<const GradGates*>(buf + Ls::oG);
-    constexpr int iP = NKB, iQ = iP + PP, iM = iQ + NU / 2, iR = iM + P, iK = iR + NU / 2, N = iK + NU;
-    f32x4 acc[4], fr[4], y[4];
+    constexpr int p0 = HS == 0 ? PP - 1 : 0, NP = PP == 1 ? (HS == 0 ? 0 : 1) : HS == 0 ? 1 : PP - 1;
+    constexpr int iP = NKB, iQ = iP + NP, iR = iQ + NU / 2, iM = iR + NU / 2, iK = iM + P, N = iK + NU;
+    f32x4 acc[4], fr[4], y[2];
     zero(acc);
     zero(fr);
     zero(y);
-    float eg[16], el[16], beta[16], ec = 0.0f;
-    Fr of[2][1], qf[2][P], zf[2][P], pl[2][P];
+    float eg[16], el[16], beta[8], ec = 0.0f;
+    Fr of[2], qf[2][P], zf[2][P], pl[2][P];
     planes(0, pl[0]);
-    auto z = [&](int kb) {
-      float e[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int rt = 2 * kb + (j >> 2);
-        e[j] = beta[8 * kb + j] * fmaf(el[8 * kb + j], acc[rt][j & 3], fr[rt][j & 3]);
-      }
-      split_planes<Eng, P>(e, zf[kb]);
-    };
-    auto u = [&](int kb) {
-      float x[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = -eg[8 * kb + j] * y[2 * kb + (j >> 2)][j & 3];
-      split_planes<Eng, P>(x, zf[kb]);
-    };
     auto o = [&](int kb) {
       float x[8];
-      frag_values(of[kb][0], x);
+      frag_values(of[kb], x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] *= eg[8 * kb + j];
       split_planes<Eng, P>(x, qf[kb]);
@@ -446,22 +514,21 @@ struct GradWalk {
           if (i < iP) rows_k(buf, i, f);
           if (i == iP - 1) {
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) of[kb][0] = TV::template cols8<Eng, 4>(buf + Ls::oV, kb, 16 * w, ln, gq);
-            weights(g.eg, eg);
+            for (int kb = 0; kb < 2; ++kb) of[kb] = TV::template cols8<Eng, 4>(buf + Ls::oV, kb, col0(), ln, gq);
+            weights(g.eg, 0, eg);
             ec = g.ec[0];
           }
-          if (i >= iP && i < iQ) blocks<true>(buf + Ls::oP + (i - iP) * Rec::kPlane, f);
+          if (i >= iP && i < iQ) blocks_p(buf + Ls::oP + (p0 + i - iP) * Rec::kPlane, f);
           if (i == iQ - 1) {
-            weights(g.el, el);
-            weights(g.beta, beta);
+            weights(g.el, 0, el);
+            weights(g.beta, 2 * HS, beta);
           }
           if (i >= iQ && i < iM) columns(buf + Ls::oQ, i - iQ, f);
-          if (i >= iM && i < iR) blocks<true>(buf + Ls::oM + (i - iM) * Rec::kPlane, f);
-          if (i >= iR && i < iK) columns(buf + Ls::oQ, i - iR + NU / 2, f);
+          if (i >= iM && i < iK) blocks_m(buf + Ls::oM + (i - iM) * Rec::kPlane, f);
           if (i >= iK) columns(buf, i - iK, f);
         },
         [&](int i, const Frags& f) {
-          ask_share<iR>(then, i);
+          ask_share<iK>(then, i);
           if (i < iP) {
             if (i + 1 < NKB) planes(i + 1, pl[(i + 1) & 1]);
             dump(slot, i, i + 1);
@@ -470,24 +537,48 @@ struct GradWalk {
 #pragma unroll
               for (int rt = 0; rt < 4; ++rt) Eng::mma(acc[rt], f[rt], pl[i & 1][k]);
           } else if (i < iQ) {
-            if (i == iP) o(0);
-            if (i == (PP > 1 ? iP + 1 : iP)) o(1);
-            if (i == iQ - 1) decay(ec);
-            by_blocks<true>(fr, f, of, i - iP, 8);
+            by_p(fr, f, of);
           } else if (i < iM) {
-            if (i == iQ) z(1);
-            if (i == (NU > 2 ? iQ + 1 : iQ)) z(0);
-            update(i - iQ, f, qf);
-          } else if (i < iR) {
-            by_blocks<true>(y, f, zf, i - iM, P);
-          } else if (i < iK) {
-            if (i == iR) {
-              u(0);
-              keep(dvs, y);
+            if (i == iQ) {
+#pragma unroll
+              for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[rt][j] = fmaf(el[4 * rt + j], acc[rt][j], fr[rt][j]);
+              give_sums(acc);
+              decay(ec);
+              o(0);
+              o(1);
             }
-            if (i == (NU > 2 ? iR + 1 : iR)) u(1);
-            update(i - iR + NU / 2, f, qf);
+            if (i == iR) {
+              barrier_lds();
+              float x[8];
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const f32x4 t = other_sums(r);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[4 * r + j] = beta[4 * r + j] * (acc[2 * HS + r][j] + t[j]);
+              }
+              split_planes<Eng, P>(x, zf[HS]);
+              give_half(buf, zf[HS]);
+            }
+            update(i - iQ, f, qf);
+          } else if (i < iK) {
+            if (i == iM) {
+              barrier_lds();
+              other_half(buf, zf[1 - HS]);
+            }
+            by_m(y, f, zf, i - iM);
           } else {
+            if (i == iK) {
+              keep(dvs, y);
+              float x[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) x[j] = -eg[8 * HS + j] * y[j >> 2][j & 3];
+              split_planes<Eng, P>(x, zf[HS]);
+              give_update(buf, zf[HS]);
+              barrier_lds();
+              other_update(buf, zf[1 - HS]);
+            }
             update(i - iK, f, zf);
           }
         });
@@ -495,22 +586,23 @@ struct GradWalk {
 
   // Rows of a segment behind its sequence: zero gradients.
   __device__ __forceinline__ void clear_padding(int t0, int t1) const {
+    constexpr int kC = 16 * CG;
     const int64_t from = (int64_t)t0 * a.H + h;
-    for (int i = threadIdx.x; i < (t1 - t0) * 64; i += kThreads)
-      ((E*)a.d_v)[(from + (int64_t)(i >> 6) * a.H) * a.dv + 64 * vt + (i & 63)] = 0;
+    for (int i = threadIdx.x; i < (t1 - t0) * kC; i += kT)
+      ((E*)a.d_v)[(from + (int64_t)(i / kC) * a.H) * a.dv + kC * vt + i % kC] = 0;
     if (vt != 0) return;
-    for (int i = threadIdx.x; i < (t1 - t0) * DK; i += kThreads) {
+    for (int i = threadIdx.x; i < (t1 - t0) * DK; i += kT) {
       const int64_t e = (from + (int64_t)(i / DK) * a.H) * DK + i % DK;
       ((E*)a.dq)[e] = 0;
       ((E*)a.dk)[e] = 0;
     }
-    for (int i = threadIdx.x; i < t1 - t0; i += kThreads) {
+    for (int i = threadIdx.x; i < t1 - t0; i += kT) {
       a.d_beta[from + (int64_t)i * a.H] = 0.0f;
       a.dg[from + (int64_t)i * a.H] = 0.0f;
     }
   }
 
-  __device__ __forceinline__ void run(char* smem) {
+  __device__ __forceinline__ void run() {
     const uint32_t lds0 = lds_base_u32(smem);
     const int seg0 = uniform(a.cu[n]), end = uniform(a.cu[n + 1]);
     const int L = a.seq_lens ? uniform(a.seq_lens[n]) : end - seg0;
@@ -530,15 +622,15 @@ struct GradWalk {
     if (nch > 0) ask_all(0);
     for (int it = 0; it < nch; ++it) {
       const char* buf = smem + (it % Ls::kBufs) * Ls::buf;
-      // the chunk's rows are there (asked for before the last chunk's four stores of E or Y, which may still be
-      // on the way); the other buffer is free
-      if (Ls::kBufs == 2 && it > 0 && !kKept) wait_vmem_but<4>();
+      // the chunk's rows are there (asked for before the last chunk's two stores of E or Y, which may still be
+      // on the way); the other buffer and the swaps' places are free
+      if (Ls::kBufs == 2 && it > 0 && !kKept) wait_vmem_but<2>();
       else wait_vmem();
       barrier_lds();
       const int64_t slot = (int64_t)(chunk0 + chunk(it)) * a.H + h;
       // the last chunk asks for its own rows again, into the other buffer
       Next then = at(min(it + 1, nch - 1));
-      then.buf = lds0 + (uint32_t)(((it + 1) % Ls::kBufs) * Ls::buf);
+      then.buf = lds0 + (uint32_t)(((it + 1) % Ls::kBufs) * Ls::buf + 1024 * w);
       if constexpr (kRev) {
         backward(buf, a.R + slot * a.dv * DK, a.Y + slot * a.dv * kChunk, then);
       } else {
@@ -557,25 +649,27 @@ struct GradWalk {
 
 // Workgroups 0 .. n_rev - 1 walk backwards, the rest forwards (with kept states
 // for E alone).  Each direction's workgroups of an XCD (workgroup b runs on XCD b %
-// 8) take neighbouring value tiles, which share K, Q and the records.
-template <class Eng, int DK>
-__global__ __launch_bounds__(kThreads, 1) void grad_scan_kernel(GradArgs a, int n_rev) {
+// 8) take neighbouring value tiles, which share K, Q and the records.  Waves w and
+// w + CG are a pair, on one SIMD.
+template <class Eng, int DK, int CG>
+__global__ __launch_bounds__(128 * CG, CG / 2) void grad_scan_kernel(GradArgs a, int n_rev) {
   extern __shared__ __align__(16) char smem[];
   if (grad_refused(a)) return;
   const bool rev = (int)blockIdx.x < n_rev;
   const int nb = rev ? n_rev : (int)gridDim.x - n_rev, b = rev ? (int)blockIdx.x : (int)blockIdx.x - n_rev;
   const int xq = nb / 8, xr = nb % 8, xc = b % 8;
   const int item = xc * xq + min(xc, xr) + b / 8;
-  const int tiles = a.dv / 64, vt = item % tiles, nh = item / tiles;
+  const int tiles = a.dv / (16 * CG), vt = item % tiles, nh = item / tiles, n = nh / a.H, h = nh % a.H;
+  const bool second = uniform(threadIdx.x >> 6) >= CG;
   if (rev) {
-    GradWalk<Eng, DK, true> walk(a, nh / a.H, nh % a.H, vt);
-    walk.run(smem);
+    if (!second) GradWalk<Eng, DK, CG, 0, true>(a, n, h, vt, smem).run();
+    else GradWalk<Eng, DK, CG, 1, true>(a, n, h, vt, smem).run();
   } else if (a.kept != nullptr) {
-    GradWalk<Eng, DK, false, true> walk(a, nh / a.H, nh % a.H, vt);
-    walk.run(smem);
+    if (!second) GradWalk<Eng, DK, CG, 0, false, true>(a, n, h, vt, smem).run();
+    else GradWalk<Eng, DK, CG, 1, false, true>(a, n, h, vt, smem).run();
   } else {
-    GradWalk<Eng, DK, false> walk(a, nh / a.H, nh % a.H, vt);
-    walk.run(smem);
+    if (!second) GradWalk<Eng, DK, CG, 0, false>(a, n, h, vt, smem).run();
+    else GradWalk<Eng, DK, CG, 1, false>(a, n, h, vt, smem).run();
   }
 }
 
@@ -1001,6 +1095,18 @@ __global__ __launch_bounds__(kThreads, Eng::kSplit ? 2 : 1) void grad_chunk_kern
   }
 }
 
+template <class Eng, int DK, int CG>
+hipError_t launch_grad_scan(const gdn_shape_t& s, const GradArgs& a, hipStream_t stream) {
+  auto kern = grad_scan_kernel<Eng, DK, CG>;
+  constexpr size_t lds = GradScanLds<Eng, DK, CG>::bytes;
+  static PerDeviceOnce once;
+  hipError_t e = set_dyn_lds_once(once, (const void*)kern, lds);
+  if (e != hipSuccess) return e;
+  const int chains = s.n_seqs * s.n_heads * (s.dv / (16 * CG));
+  hipLaunchKernelGGL(kern, dim3((unsigned)(2 * chains)), dim3(128 * CG), lds, stream, a, chains);
+  return hipGetLastError();
+}
+
 template <class Eng, int DK>
 hipError_t launch_grad(const gdn_shape_t& s, const GradArgs& a, int64_t items, hipStream_t stream) {
   hipError_t e;
@@ -1012,15 +1118,12 @@ hipError_t launch_grad(const gdn_shape_t& s, const GradArgs& a, int64_t items, h
     hipLaunchKernelGGL(kern, dim3((unsigned)items), dim3(kThreads), lds, stream, a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  {
-    auto kern = grad_scan_kernel<Eng, DK>;
-    constexpr size_t lds = GradScanLds<Eng, DK>::bytes;
-    static PerDeviceOnce once;
-    if ((e = set_dyn_lds_once(once, (const void*)kern, lds)) != hipSuccess) return e;
-    const int chains = s.n_seqs * s.n_heads * (s.dv / 64);
-    hipLaunchKernelGGL(kern, dim3((unsigned)(2 * chains)), dim3(kThreads), lds, stream, a, chains);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
+  // 32 value columns a workgroup where a compute unit each is there for all of them, both ways: a chunk's step is
+  // shorter (one sequence of 8192 tokens, 16 heads, 128 x 128: 408 us for 518), but two on a compute unit do not
+  // fit (the training batch, twice as many as compute units: 487 us for 385)
+  const bool few = (int64_t)s.n_seqs * s.n_heads * (s.dv / 32) * 2 <= device_cu_count();
+  if ((e = few ? launch_grad_scan<Eng, DK, 2>(s, a, stream) : launch_grad_scan<Eng, DK, 4>(s, a, stream)) != hipSuccess)
+    return e;
   if (items > 0) {
     auto kern = grad_chunk_kernel<Eng, DK>;
     constexpr size_t lds = GradChunkLds<Eng, DK>::bytes;

@@ -28,6 +28,9 @@ inline hipError_t set_dyn_lds_once(PerDeviceOnce& once, const void* kern, size_t
   return e;  // concurrent first calls on one device both set it: harmless
 }
 
+// Compute units of the current device (0 when it cannot be read).
+int device_cu_count();
+
 hipError_t launch_state_qdq(const float* in, float* out, float* scales, int64_t n_tiles, int dk,
                             hipStream_t stream);
 

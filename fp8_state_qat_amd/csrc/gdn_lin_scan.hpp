@@ -209,11 +209,13 @@ struct LinRows {
     for (int i = 0; i < kPer; ++i) ask_step(i, lds, p, stride, n);
   }
   static __device__ __forceinline__ void ask_step(int i, uint32_t lds, const E* p, int stride, int n) {
+    if (kAll % NT != 0 && uniform((int)threadIdx.x + NT * i) >= kAll) return;
+    lds_load16(p, offset(i, stride, n), lds + 16 * 64 * (threadIdx.x >> 6) + 16 * NT * i);
+  }
+  static __device__ __forceinline__ uint32_t offset(int i, int stride, int n) {   // bytes
     const int idx = (int)threadIdx.x + NT * i, row = idx / kUnits, u = lin_unit<kUnits>(row, idx % kUnits);
-    if (kAll % NT != 0 && uniform(idx) >= kAll) return;
     const int r = row < n ? row : n - 1;
-    lds_load16(p, (uint32_t)(r * stride + u * (16 / (int)sizeof(E))) * (uint32_t)sizeof(E),
-               lds + 16 * 64 * (threadIdx.x >> 6) + 16 * NT * i);
+    return (uint32_t)(r * stride + u * (16 / (int)sizeof(E))) * (uint32_t)sizeof(E);
   }
   // Through registers, in two halves; rows from n on are 0.
   static __device__ __forceinline__ void fetch(uint4 (&x)[kPer], const E* p, int stride, int n) {
