@@ -275,9 +275,9 @@ struct GradWalk {
   }
   // the state for the gradients' kernel (past the caches, the half lines of each store would go to memory by
   // themselves: 835 MB for 530 in the training batch)
-  __device__ __forceinline__ void dump(float* slot, int p0 = 0, int p1 = NKB) const {
+  __device__ __forceinline__ void dump(float* slot) const {
 #pragma unroll
-    for (int tr = 2 * p0; tr < 2 * p1; ++tr)
+    for (int tr = 0; tr < NT; ++tr)
       *reinterpret_cast<f32x4*>(slot + at(tr)) = X[tr];
   }
   // this wave's tokens of E or Y for the gradients' kernel, transposed: a token row for each value column
@@ -417,8 +417,8 @@ struct GradWalk {
     get_planes(kReceiver ? swap() : swap_p(buf), lane(), f);
   }
 
-  // kKept: X is the state of this chunk alone
-  __device__ __forceinline__ void forward(const char* buf, float* slot, float* err, const Next& then) {
+  // kKept: X is the state of this chunk alone, the next one's entry j
+  __device__ __forceinline__ void forward(const char* buf, float* err, const Next& then, int64_t j) {
     const char* sM = buf + Ls::oM;
     const GradGates& g = *reinterpret_cast<const GradGates*>(buf + Ls::oG);
     constexpr int iM = NKB, iK = iM + P, N = kKept ? iK : iK + NU;
@@ -447,7 +447,6 @@ struct GradWalk {
           ask_share<iK>(then, i);
           if (i < iM) {
             if (i + 1 < NKB) planes(i + 1, pl[(i + 1) & 1]);
-            if constexpr (!kKept) dump(slot, i, i + 1);
 #pragma unroll
             for (int k = 0; k < P; ++k)
 #pragma unroll
@@ -455,7 +454,8 @@ struct GradWalk {
           } else if (i < iK) {
             if (i == iM) {
               give_sums(acc);
-              if constexpr (!kKept) decay(ec);
+              if constexpr (kKept) load(a.kept, j);
+              else decay(ec);
               barrier_lds();
               float v[8];
               frag_values(vf, v);
@@ -491,7 +491,7 @@ struct GradWalk {
   // The products with K (state) and P (the first wave one plane, the second the
   // others: it has less of M), the update by dO, which needs nothing of the chain,
   // in two parts beside the swaps, Y, the update by Y.
-  __device__ __forceinline__ void backward(const char* buf, float* slot, float* dvs, const Next& then) {
+  __device__ __forceinline__ void backward(const char* buf, float* dvs, const Next& then) {
     const GradGates& g = *reinterpret_cast<const GradGates*>(buf + Ls::oG);
     constexpr int p0 = HS == 0 ? PP - 1 : 0, NP = PP == 1 ? (HS == 0 ? 0 : 1) : HS == 0 ? 1 : PP - 1;
     constexpr int iP = NKB, iQ = iP + NP, iR = iQ + NU / 2, iM = iR + NU / 2, iK = iM + P, N = iK + NU;
@@ -531,7 +531,6 @@ struct GradWalk {
           ask_share<iK>(then, i);
           if (i < iP) {
             if (i + 1 < NKB) planes(i + 1, pl[(i + 1) & 1]);
-            dump(slot, i, i + 1);
 #pragma unroll
             for (int k = 0; k < P; ++k)
 #pragma unroll
@@ -619,24 +618,22 @@ struct GradWalk {
 #pragma unroll
       for (int k = 0; k < kAsks; ++k) ask(x, k);
     };
+    auto slot = [&](int it) { return (int64_t)(chunk0 + chunk(it)) * a.H + h; };
     if (nch > 0) ask_all(0);
+    if (!kKept && nch > 0) dump((kRev ? a.R : a.S) + slot(0) * a.dv * DK);
     for (int it = 0; it < nch; ++it) {
       const char* buf = smem + (it % Ls::kBufs) * Ls::buf;
-      // the chunk's rows are there (asked for before the last chunk's two stores of E or Y, which may still be
-      // on the way); the other buffer and the swaps' places are free
-      if (Ls::kBufs == 2 && it > 0 && !kKept) wait_vmem_but<2>();
+      // the chunk's rows are there (asked for before the last chunk's stores, which have this one's time: 359 us for
+      // 385 with them first, in the training batch); the other buffer and the swaps' places are free
+      if (Ls::kBufs == 2 && it > 0 && !kKept) wait_vmem_but<NT + 2>();
       else wait_vmem();
       barrier_lds();
-      const int64_t slot = (int64_t)(chunk0 + chunk(it)) * a.H + h;
       // the last chunk asks for its own rows again, into the other buffer
       Next then = at(min(it + 1, nch - 1));
       then.buf = lds0 + (uint32_t)(((it + 1) % Ls::kBufs) * Ls::buf + 1024 * w);
-      if constexpr (kRev) {
-        backward(buf, a.R + slot * a.dv * DK, a.Y + slot * a.dv * kChunk, then);
-      } else {
-        forward(buf, a.S + slot * a.dv * DK, a.E + slot * a.dv * kChunk, then);
-        if constexpr (kKept) load(a.kept, chunk0 + it);
-      }
+      if constexpr (kRev) backward(buf, a.Y + slot(it) * a.dv * kChunk, then);
+      else forward(buf, a.E + slot(it) * a.dv * kChunk, then, chunk0 + it);
+      if (!kKept && it + 1 < nch) dump((kRev ? a.R : a.S) + slot(it + 1) * a.dv * DK);
       if (Ls::kBufs == 1 && it + 1 < nch) {
         barrier_lds();
         ask_all(it + 1);
@@ -1119,8 +1116,8 @@ hipError_t launch_grad(const gdn_shape_t& s, const GradArgs& a, int64_t items, h
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   // 32 value columns a workgroup where a compute unit each is there for all of them, both ways: a chunk's step is
-  // shorter (one sequence of 8192 tokens, 16 heads, 128 x 128: 408 us for 518), but two on a compute unit do not
-  // fit (the training batch, twice as many as compute units: 487 us for 385)
+  // shorter (one sequence of 8192 tokens, 16 heads, 128 x 128: 381 us for about 490), but two on a compute unit do not
+  // fit (the training batch, twice as many as compute units: 490 us for 359)
   const bool few = (int64_t)s.n_seqs * s.n_heads * (s.dv / 32) * 2 <= device_cu_count();
   if ((e = few ? launch_grad_scan<Eng, DK, 2>(s, a, stream) : launch_grad_scan<Eng, DK, 4>(s, a, stream)) != hipSuccess)
     return e;
