@@ -23,9 +23,9 @@
 // it shows in the S that the chunks start from.
 //
 // Three launches (gdn_grad.hip): records of every (chunk, head) in parallel
-// (M, P, gates); the chains S and R, one workgroup for each (sequence, head,
-// 64 value columns) and direction, which need nothing of each other and run
-// side by side; the gradients of every (chunk, head) in parallel.
+// (M, P, gates); the chains, forwards (S; it leaves S and E of every chunk) and
+// backwards (R; R and Y), which need nothing of each other and run side by side;
+// the gradients of every (chunk, head) in parallel, from S, R, E and Y.
 #pragma once
 
 #include "gdn_lin_scan.hpp"

@@ -19,7 +19,8 @@ __device__ __forceinline__ typename Eng::Fr row_kperm(const char* t, int row, in
 }
 
 // ---------------------------------------------------------------------------
-// Records.  One workgroup of four waves for each (chunk, head).
+// Records.  One workgroup of four waves for each (chunk, head).  Bounded by
+// memory: 16384 tokens, 16 heads of 128 read 0.14 GB and write 0.13 in 66 us.
 // ---------------------------------------------------------------------------
 template <class Eng, int DK>
 struct GradPrepLds {
@@ -154,7 +155,19 @@ __global__ __launch_bounds__(kThreads) void grad_prep_kernel(GradArgs a) {
 // sums, and wave HS goes on with tokens 32 HS .. 32 HS + 31, whose half of the
 // triangular product it also forms (half kb of the operand is known to the wave
 // kb; the other needs it where the triangle does); the halves of its result are
-// swapped again for the state's update.
+// swapped again for the state's update.  (One wave with all channels: a chunk in
+// 9.4 thousand cycles, 7.4 thousand so.)
+//
+// States, E and Y have 24 bits in every product: operands formed on the way are
+// three bf16 planes, K, Q, V and dO enter as they are.  With two planes beta's and
+// the gates' gradients were off by 3e-6 to 5e-6.
+//
+// Memory and the chain bound it: 4 x 4096 tokens, 16 heads, 128 x 128 in bf16 take
+// 358 us for 0.53 GB read and 0.81 written (3.7 TB/s of the copy's 5.0), matrix
+// units busy 24% of the time, backwards alone 324 us, forwards 278; one sequence
+// of 8192 tokens 378 us, 7.1 thousand cycles a chunk.  What did not help: loads of
+// the next chunk through registers (417 us for 385), at the start or the end of a
+// chunk alone (423, 413), 32 columns a wave (409).
 // ---------------------------------------------------------------------------
 template <class Eng, int DK, int CG>
 struct GradScanLds {
@@ -689,6 +702,11 @@ __global__ __launch_bounds__(128 * CG, CG / 2) void grad_scan_kernel(GradArgs a,
 // goes as 2^-60: Y is a multiple of it.)  S, Y and E therefore have the planes of
 // the chains' products in these sums; what dq and dk alone are made of (R, W, N)
 // has two, sixteen bits against the eight that they are rounded to.
+//
+// Memory bounds it: 4 x 4096 tokens, 16 heads, 128 x 128 in bf16 take 294 us for
+// 1.05 GB read and 0.24 written (4.4 TB/s of the copy's 5.0), at 1.85 GHz.  (Before,
+// each chunk's E and Y were formed again here by sixteen waves and all of S, R, E, Y
+// went through LDS: 555 us, most of it in one workgroup a compute unit's waits.)
 // ---------------------------------------------------------------------------
 template <class Eng, int DK>
 struct GradChunkLds {
@@ -1116,8 +1134,8 @@ hipError_t launch_grad(const gdn_shape_t& s, const GradArgs& a, int64_t items, h
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   // 32 value columns a workgroup where a compute unit each is there for all of them, both ways: a chunk's step is
-  // shorter (one sequence of 8192 tokens, 16 heads, 128 x 128: 381 us for about 490), but two on a compute unit do not
-  // fit (the training batch, twice as many as compute units: 490 us for 359)
+  // shorter (one sequence of 8192 tokens, 16 heads, 128 x 128: 378 us for 531), but two on a compute unit do not
+  // fit (the training batch, twice as many as compute units: 429 us for 358)
   const bool few = (int64_t)s.n_seqs * s.n_heads * (s.dv / 32) * 2 <= device_cu_count();
   if ((e = few ? launch_grad_scan<Eng, DK, 2>(s, a, stream) : launch_grad_scan<Eng, DK, 4>(s, a, stream)) != hipSuccess)
     return e;

@@ -384,10 +384,10 @@ size_t gdn_chunk_bwd_workspace_bytes(const gdn_shape_t* shape);
  * not read); rows outside every segment are not written.  dg is exactly 0 where
  * e^g is.  Outputs may not overlap inputs.
  *
- * dq, dk, d_v and d_initial_state take terms of 16 or more significant bits
- * (fp32 inputs: 24); d_beta and dg are sums of terms that can cancel, off by
- * about 2^-16 (fp32 inputs: 2^-21) of the sum of their terms' magnitudes in the
- * chunk at most.
+ * The states, their gradients, d_v before its rounding, d_beta and dg take terms
+ * of 24 significant bits, dq and dk of bf16 inputs terms of 16 or more; d_beta and
+ * dg are sums of terms that can cancel, off by about 2^-19 of the sum of their
+ * terms' magnitudes in the chunk at most.
  */
 gdn_status_t gdn_chunk_grad(const gdn_shape_t* shape,
                             const void* q, const void* k, const void* v,
@@ -399,8 +399,8 @@ gdn_status_t gdn_chunk_grad(const gdn_shape_t* shape,
                             float* d_initial_state,
                             void* workspace, size_t workspace_bytes, void* stream);
 /* Workspace bytes of gdn_chunk_grad: for each 64 tokens and head a record of
- * 27 KiB and 4 dk dv bytes, twice that without given states; 0 for an invalid
- * shape. */
+ * 32 KiB (fp32 inputs: 22), 512 dv bytes, and 4 dk dv bytes, twice those without
+ * given states; 0 for an invalid shape. */
 size_t gdn_chunk_grad_workspace_bytes(const gdn_shape_t* shape, int32_t states_given);
 
 /*
