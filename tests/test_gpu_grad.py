@@ -149,6 +149,25 @@ def test_given_states(dk, dv, dtype):
     close(run(d, states.cuda()), want(d, states), bounds(d, states), dtype)
 
 
+@pytest.mark.parametrize("dk,dv,dtype,given", [(64, 64, BF, False), (128, 128, BF, False), (128, 64, BF, True),
+                                               (64, 128, F32, False), (128, 64, F32, True)])
+def test_many_sequences(dk, dv, dtype, given):
+    """More chains than compute units, whose workgroups are wider: the bits that a sequence gives alone."""
+    seg = [(7 * i * i + 1) % 131 for i in range(40)]
+    d = make(seg, 4, dk, dv, dtype, seed=11)
+    nb = n_bounds(d)
+    states = torch.randn(sum(nb), 4, dv, dk, generator=torch.Generator().manual_seed(12)) if given else None
+    got = run(d, None if states is None else states.cuda())
+    close(got, want(d, states), bounds(d, states), dtype)
+    for n in (0, 3, 39):
+        r, at = slice(int(d["cu"][n]), int(d["cu"][n + 1])), sum(nb[:n])
+        one = {m: None if x is None else x[n:n + 1] if m in ("S0", "dS") else x[r] for m, x in d.items() if m != "cu"}
+        one["cu"] = torch.tensor([0, seg[n]], dtype=torch.int32)
+        alone = run(one, None if states is None else states[at:at + nb[n]].cuda())
+        for name, x, y in zip(NAMES, got, alone):
+            assert torch.equal(x[n:n + 1] if name == "dS0" else x[r], y), (n, name)
+
+
 @pytest.mark.parametrize("dk,dtype", [(64, BF), (128, BF), (64, F32), (128, F32)])
 @pytest.mark.parametrize("flags", [GDN_QDQ_CHUNK, GDN_QDQ_CHUNK | GDN_QDQ_WRITE])
 def test_quantized_forward(dk, dtype, flags):
