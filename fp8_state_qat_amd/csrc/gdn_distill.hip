@@ -90,9 +90,10 @@ template <>
 struct Oct<float> {
   float4 a, b;
   __device__ __forceinline__ void none() { a = b = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
-  __device__ __forceinline__ void ld(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
+  __device__ __forceinline__ void ld(const float* p) { ld(p, p + 4); }
+  __device__ __forceinline__ void ld(const float* p, const float* q) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(q);
   }
   __device__ __forceinline__ void ld_some(const float* p, int lo, int hi) {
     float x[8];
@@ -119,14 +120,14 @@ struct Oct<float> {
 
 // A whole octet, past the caches: the gradient is not read here again (16384 x
 // 32000: 441 us for 468).
-__device__ __forceinline__ void st_row(uint16_t* p, const float (&x)[8]) {
+__device__ __forceinline__ void st_row(uint16_t* p, uint16_t*, const float (&x)[8]) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   const u32x4 u = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
   __builtin_nontemporal_store(u, reinterpret_cast<u32x4*>(p));
 }
-__device__ __forceinline__ void st_row(float* p, const float (&x)[8]) {
+__device__ __forceinline__ void st_row(float* p, float* q, const float (&x)[8]) {   // in halves
   st_stream(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
-  st_stream(reinterpret_cast<float4*>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
+  st_stream(reinterpret_cast<float4*>(q), make_float4(x[4], x[5], x[6], x[7]));
 }
 template <typename T>
 __device__ __forceinline__ void st_some(T* p, int lo, int hi, const float (&x)[8]) {
@@ -350,10 +351,20 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
   Oct<T> x[U], xe;
   const T* zo = z + 8 * o0 - shift;   // octet o0
   T* dzo = kGrad ? dz + 8 * o0 - shift : nullptr;
+  // fp32: a whole wave's octets as two runs of 1 KiB, 16 bytes a lane, so that each access fills its lines (gradient
+  // of 1000 x 50001 by 256 threads a row, not in a cache: 83 us for 92)
+  auto runs = [&](uint32_t o) { return sizeof(T) == 4 && (int)(o - lane) + 64 <= o1 - o0; };
+  auto run_at = [&](uint32_t o) { return (o - lane) * 32u + 16u * lane; };   // the first's bytes from octet o0
   auto load = [&](int tile) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint32_t o = (uint32_t)((tile * U + u) * TPB + tid);
+      if constexpr (sizeof(T) == 4) {
+        if (runs(o)) {
+          x[u].ld((const T*)((const char*)zo + run_at(o)), (const T*)((const char*)zo + run_at(o) + 1024));
+          continue;
+        }
+      }
       if ((int)o < o1 - o0) x[u].ld((const T*)((const char*)zo + o * (uint32_t)(8 * sizeof(T))));
       else x[u].none();
     }
@@ -387,7 +398,13 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int o = (tile * U + u) * TPB + tid;
-          const uint32_t b = o < o1 - o0 ? bits[o0 + o] : 0u;
+          uint32_t b = 0u;
+          if (runs(o)) {
+            const uint8_t* half = bits + o0 + (o - lane) + lane / 2;
+            b = (half[0] >> 4 * (lane & 1) & 15u) | (half[32] >> 4 * (lane & 1) & 15u) << 4;
+          } else if (o < o1 - o0) {
+            b = bits[o0 + o];
+          }
           if (b != 0u) x[u].clear(b);
         }
         if (edge) xe.clear(bits[e_oct]);
@@ -609,8 +626,13 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
           float g[8];
           grads(x[u], g);
           T* to_o = (T*)((char*)dzo + o * (uint32_t)(8 * sizeof(T)));
-          if (vec) st_row(to_o, g);
-          else st_some(to_o, 0, 8, g);
+          T* to_q = to_o + 4;
+          if (runs(o)) {
+            to_o = (T*)((char*)dzo + run_at(o));
+            to_q = to_o + 256;
+          }
+          if (vec) st_row(to_o, to_q, g);
+          else st_some(to_o, 0, 4, g), st_some(to_q - 4, 4, 8, g);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -673,7 +695,7 @@ hipError_t launch_distill(const gdn_distill_t& s, const void* logits, const int3
   // 32000 bf16: 209 us; 16 octets took 256 registers and 670 us).  Both: as much of the row in registers as leaves two
   // workgroups a compute unit, the rest read again from the last-level cache (4096 x 131072 bf16: 442 us with 512
   // threads and half a row, 612 with 1024 and all of it, 484 with 256 and a quarter).  The gradient alone, bf16: 417 us
-  // with 16 octets, 441 with four (16384 x 32000); fp32: 75 us with four, 79 with eight (1000 x 50001).
+  // with 16 octets, 441 with four (16384 x 32000); fp32: as below.
   const int octs = s.vocab / 8 + 2;
   if (s.dtype == GDN_BF16) {
     if (octs <= 64 * 4) return launch_rows<uint16_t, 64, 4>(s, a, mode, stream);
@@ -690,7 +712,11 @@ hipError_t launch_distill(const gdn_distill_t& s, const void* logits, const int3
   if (mode == kDisFwd)
     return octs <= 8192 ? launch_row<float, 256, 4, kDisFwd>(s, a, stream)
                         : launch_row<float, 1024, 4, kDisFwd>(s, a, stream);
-  if (mode == kDisBwd) return launch_row<float, 256, 4, kDisBwd>(s, a, stream);
+  // the gradient alone: a row in the fewest turns once it fills most of 1024 threads (4000 x 32000: 174 us for 199
+  // with 256 threads, 1000 x 50001 77 for 83; 1000 x 20011 would take 36.5 for 34.8)
+  if (mode == kDisBwd)
+    return octs < 3584 ? launch_row<float, 256, 4, kDisBwd>(s, a, stream)
+                       : launch_row<float, 1024, 4, kDisBwd>(s, a, stream);
   return octs <= 256 * 8 ? launch_row<float, 256, 8, kDisBoth>(s, a, stream)
                          : launch_row<float, 512, 8, kDisBoth>(s, a, stream);
 }

@@ -156,6 +156,30 @@ def test_slices_of_wider_rows(dtype, off, wide):
     assert torch.isnan(box[:, :off]).all() and torch.isnan(box[:, off + 120:]).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [2101, 28700])
+@pytest.mark.parametrize("off,to", [(1, 1), (2, 3), (3, 0)])
+def test_slices_of_long_rows(dtype, V, off, to):
+    """The same of rows that whole waves go through; with other addresses of the gradient than of the logits."""
+    d = make(3, V, 17, dtype, True, True, 2.0, seed=off)
+    box = torch.full((3, V + 9), float("nan"), dtype=dtype, device="cuda")
+    z = box[:, off:off + V]
+    z.copy_(d["z"])
+    ids, top, w = (d[n].cuda() for n in ("ids", "top", "d_loss"))
+    rl, _, dz = want(d)
+    loss, stats = api.distill_fwd(z, ids, top, **kwargs(d))
+    check_loss(loss, rl, d)
+    for what in ("backward", "both"):
+        out_box = torch.full((3, V + 9), 9.0, dtype=dtype, device="cuda")
+        out = out_box[:, to:to + V]
+        if what == "backward":
+            api.distill_bwd(z, ids, top, stats, w, out=out, **kwargs(d))
+        else:
+            check_loss(api.distill_fwd_bwd(z, ids, top, w, out=out, **kwargs(d))[0], rl, d)
+        check_grad(out, dz, d, what)
+        assert (out_box[:, :to] == 9.0).all() and (out_box[:, to + V:] == 9.0).all()
+
+
 @pytest.mark.parametrize("tail", [False, True])
 def test_the_same_column_twice_and_every_column(tail):
     d = make(3, 40, 40, F32, tail, True, 1.0, seed=3)
