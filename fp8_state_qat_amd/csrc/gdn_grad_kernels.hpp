@@ -230,6 +230,7 @@ struct GradWalk {
   // (records: wave w the KiB w, w + kW, ..; the gates beside the last).
   using RK = LinRows<E, DK, kT>;
   using RV = LinRows<E, 16 * CG, kT>;
+  static_assert(RK::kAll % kT == 0 && RV::kAll % kT == 0, "every thread has its share of the rows");
   static constexpr int kRecKiB = (kRev ? Rec::oG : Rec::oP) / 1024;
   static constexpr int kAsks = RK::kPer * (kRev ? 2 : 1) + RV::kPer + (kRecKiB + kW) / kW;
   struct Next {
@@ -259,10 +260,7 @@ struct GradWalk {
       if (i < RK::kPer) return lds_load16(x.q, ko[i], x.buf + Ls::oQ + 16 * kT * i);
       i -= RK::kPer;
     }
-    if (i < RV::kPer) {
-      if (RV::kAll % kT == 0 || 64 * w + kT * i < RV::kAll) lds_load16(x.v, vo[i], x.buf + Ls::oV + 16 * kT * i);
-      return;
-    }
+    if (i < RV::kPer) return lds_load16(x.v, vo[i], x.buf + Ls::oV + 16 * kT * i);
     i -= RV::kPer;
     const uint32_t lane16 = (uint32_t)(16 * (16 * gq + ln));
     if (kW * (i + 1) <= kRecKiB || kW * i + w < kRecKiB) {
