@@ -382,7 +382,8 @@ size_t gdn_chunk_bwd_workspace_bytes(const gdn_shape_t* shape);
  *              written)
  * Rows of a segment past L_n get zero gradients (what the inputs hold there is
  * not read); rows outside every segment are not written.  dg is exactly 0 where
- * e^g is.  Outputs may not overlap inputs.
+ * e^g is.  An infinity or a NaN reaches gradients of its own sequence and head
+ * only.  Outputs may not overlap inputs.
  *
  * The states, their gradients, d_v before its rounding, d_beta and dg take terms
  * of 24 significant bits, dq and dk of bf16 inputs terms of 16 or more; d_beta and

@@ -280,6 +280,23 @@ def test_captured_and_replayed(flags):
             assert torch.equal(a, b), (i, name)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("what", ["q", "k", "v", "d_o"])
+def test_what_is_not_finite_stays_in_its_sequence_and_head(what, dtype):
+    d = make([70, 130, 40], 2, 64, 128, dtype, [70, 129, 40], seed=21)
+    plain = run(d)
+    d[what] = d[what].clone()
+    d[what][70 + 100, 1, 5] = float("inf")
+    got = run(d)
+    assert not torch.isfinite(got[0][70:199, 1].float()).all() or not torch.isfinite(got[1][70:199, 1].float()).all()
+    for name, x, y in zip(NAMES, got, plain):
+        if name == "dS0":
+            assert torch.equal(x[[0, 2]], y[[0, 2]]) and torch.equal(x[1, 0], y[1, 0]), name
+        else:
+            assert torch.equal(x[:70], y[:70]) and torch.equal(x[199:], y[199:]), name
+            assert torch.equal(x[70:199, 0], y[70:199, 0]), name
+
+
 @pytest.mark.parametrize("bad", [[0, 50, 40], [0, 64, 200], [-1, 64, 100]])
 def test_bad_index_arrays_write_nothing(bad):
     d = make([64, 36], 1, 64, 64, BF, seed=13)
