@@ -78,10 +78,11 @@ struct Oct<uint16_t> {
       if (b >> (2 * i + 1) & 1) *p[i] = (*p[i] & 0xffffu) | 0xff800000u;
     }
   }
-  // their largest value, up to the bits below an odd column's bf16 (it is a reference only)
+  // their largest value, exactly: an odd column with its neighbour's bits below it would be a NaN for +inf, and off by
+  // more than exponentials bear from |z / h| = 1e4 on
   __device__ __forceinline__ float largest() const {
-    const float a = fmaxf(fmaxf(bf16_lo(u.x), __uint_as_float(u.x)), fmaxf(bf16_lo(u.y), __uint_as_float(u.y)));
-    return fmaxf(fmaxf(a, fmaxf(bf16_lo(u.z), __uint_as_float(u.z))), fmaxf(bf16_lo(u.w), __uint_as_float(u.w)));
+    const float a = fmaxf(fmaxf(bf16_lo(u.x), bf16_hi(u.x)), fmaxf(bf16_lo(u.y), bf16_hi(u.y)));
+    return fmaxf(fmaxf(a, fmaxf(bf16_lo(u.z), bf16_hi(u.z))), fmaxf(bf16_lo(u.w), bf16_hi(u.w)));
   }
   // unpacked anew from here on: the compiler would keep the values of an earlier get() instead, twice the registers
   __device__ __forceinline__ void hide() { asm volatile("" : "+v"(u.x), "+v"(u.y), "+v"(u.z), "+v"(u.w)); }

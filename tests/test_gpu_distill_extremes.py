@@ -1,0 +1,146 @@
+"""Distillation on the GPU at the ends of its range: masked vocabularies, far logits, values that are not finite.
+
+The reference forms everything from differences of a row's logits in 64 bits, so that it holds for logits of any size.
+Tolerances.  A logsumexp's sum is within 2^-15 of itself (derived in test_gpu_distill.py; an argument (v - max) c / h
+has two roundings more, |x| 2^-23 for |x| < 17 where e^x counts), and the rest of a row's values is formed in fp64: a
+loss is within (kd_weight + ce_weight) 2^-14 + 2^-23 of itself.  A probability is within 2^-15 for the sum and |y| 1.5 *
+2^-23 < 2^-16 for its argument y > -87 of itself, so a gradient's value within 2^-14 of its terms' magnitudes, with
+bf16 2^-8 of itself more.
+"""
+import math
+
+import pytest
+import torch
+
+from fp8_state_qat_amd import api
+
+pytestmark = pytest.mark.gpu
+BF, F32, F64 = torch.bfloat16, torch.float32, torch.float64
+INF, NAN = float("inf"), float("nan")
+
+
+def lse(y):
+    m = y.max().detach()
+    return m + (y - m).exp().sum().log() if m > -INF else m
+
+
+def reference(d):
+    """(loss [R], dz [R, V], magnitudes of the gradient's terms [R, V]) in double."""
+    h, wk, wc = (float(torch.tensor(d["kw"][n], dtype=F32)) for n in ("temperature", "kd_weight", "ce_weight"))  # as passed
+    z0 = d["z"].to(F64)
+    R, V = z0.shape
+    loss, dz, mag = torch.zeros(R, dtype=F64), torch.zeros(R, V, dtype=F64), torch.zeros(R, V, dtype=F64)
+    for r in range(R):
+        z = z0[r].clone().requires_grad_()
+        top = z.max().detach()
+        y = (z - top) / h
+        on = d["ids"][r] >= 0
+        ids, t = d["ids"][r][on].long(), d["top"][r][on].to(F64) / h
+        c = lse(t) if d["lse"] is None else d["lse"][r].to(F64)
+        p = (t - c).exp()
+        total = lse(y)
+        kd = (p * (t - c - (y[ids] - total))).sum() if len(ids) else torch.zeros((), dtype=F64)
+        a, b = abs(float(d["d_loss"][r])) * wk / h, abs(float(d["d_loss"][r])) * wc
+        mag[r] = a * (y - total).exp().detach()
+        mag[r].index_add_(0, ids, a * p)
+        if d["lse"] is not None:
+            off = torch.ones(V, dtype=torch.bool)
+            off[ids] = False
+            rest = max(0.0, 1.0 - float(p.sum()))
+            if off.any() and rest > 0:
+                last = lse(y[off])
+                kd = kd + rest * (math.log(rest) - (last - total))
+                mag[r][off] += a * rest * (y[off] - y[off].max()).exp().detach() / (y[off] - y[off].max()).exp().sum().item()
+        out = wk * kd
+        if d["targets"] is not None:
+            k = int(d["targets"][r])
+            x = z - top
+            out = out + wc * (lse(x) - x[k])
+            mag[r] += b * torch.softmax(x, 0).detach()
+            mag[r, k] += b
+        loss[r] = out.detach()
+        dz[r], = torch.autograd.grad(out * float(d["d_loss"][r]), z)
+    return loss, dz, mag
+
+
+def make(z, ids, dtype, tail, ce=True, h=1.0, seed=0):
+    """The teacher's logits: 3 of every row, spread by chance; targets among the kept."""
+    gen = torch.Generator().manual_seed(seed)
+    R, K = ids.shape
+    d = dict(z=z.to(dtype), ids=ids.int(), top=2 * torch.randn(R, K, generator=gen))
+    d["lse"] = (torch.logsumexp(d["top"].double() / h, 1) + 0.4).float() if tail else None
+    d["targets"] = ids[:, 0].long() if ce else None
+    d["d_loss"] = torch.rand(R, generator=gen) + 0.25
+    d["kw"] = dict(temperature=h, kd_weight=0.75, ce_weight=0.25 if ce else 0.0)
+    return d
+
+
+def run(d):
+    """(losses of both calls, gradients of both)."""
+    x = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in d.items()}
+    kw = dict(teacher_lse=x["lse"], targets=x["targets"], **d["kw"])
+    a = x["z"], x["ids"], x["top"]
+    loss, stats = api.distill_fwd(*a, **kw)
+    back = api.distill_bwd(*a, stats, x["d_loss"], **kw)
+    both, grad = api.distill_fwd_bwd(*a, x["d_loss"], **kw)
+    for out in (x["z"].clone(), x["z"].clone()):      # in place
+        api.distill_bwd(out, x["ids"], x["top"], stats, x["d_loss"], out=out, **kw)
+        assert torch.equal(out, back) or not torch.isfinite(back).all()
+    return (loss.cpu(), both.cpu()), (back.cpu(), grad.cpu()), stats.cpu()
+
+
+def check(d, far=0.0):
+    """far: the logsumexps' magnitude, of which a probability may be off by 2^-22 times itself more."""
+    loss, dz, mag = reference(d)
+    losses, grads, stats = run(d)
+    wanted = loss.float()
+    tol = (d["kw"]["kd_weight"] + d["kw"]["ce_weight"]) * 2.0 ** -14 + 2.0 ** -23 * loss.abs()
+    for got in losses:
+        ok = (got == wanted) | ((got.double() - loss).abs() <= tol)
+        assert ok.all(), (got, wanted)
+    for name, g in zip(("backward", "both"), grads):
+        err = (g.double() - dz).abs()
+        bound = (2.0 ** -14 + 2.0 ** -22 * far) * mag + (2.0 ** -8 * dz.abs() if g.dtype == BF else 0) + 1e-36
+        bad = ~(err <= bound)
+        assert not bad.any(), f"{name}: {bad.nonzero()[:5].tolist()}, worst {float((err / bound).max()):.3g}"
+    return losses, grads, stats
+
+
+def random_ids(R, V, K, lo=0):
+    gen = torch.Generator().manual_seed(V)
+    return torch.stack([lo + torch.randperm(V - lo, generator=gen)[:K] for _ in range(R)])
+
+
+# ---------------------------------------------------------------- far logits
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("V,h", [(301, 1.0), (700, 2.0), (5003, 1.0), (40000, 0.5)])
+def test_far_logits_beside_each_other(dtype, tail, V, h):
+    """Logits whose neighbours differ in size and sign; the largest in even and in odd columns."""
+    z = torch.randn(6, V, generator=torch.Generator().manual_seed(V))
+    z[0, 0::2], z[0, 1::2] = -30000.0, -20000.0
+    z[1, 1::2], z[1, 0::2] = -30000.0, -20000.0
+    z[2, 101] = z[3, 100] = 20000.0
+    z[4] *= 9000.0
+    z[5, 0::2] -= 25000.0
+    check(make(z, random_ids(6, V, 3), dtype, tail, h=h), far=45000.0 / min(h, 1.0))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [40, 5003])
+@pytest.mark.parametrize("value", [INF, NAN])
+def test_a_logit_that_is_not_finite_makes_its_row_nan(dtype, V, value):
+    z = torch.randn(4, V, generator=torch.Generator().manual_seed(V))
+    z[1, 6] = z[2, 7] = value
+    for h in (1.0, 2.0):
+        alone(make(z, random_ids(4, V, 3, lo=9), dtype, False, h=h), (0, 3))
+
+
+def alone(d, good):
+    losses, grads, _ = run(d)
+    r = torch.zeros(len(d["z"]), dtype=torch.bool)
+    r[list(good)] = True
+    for x in losses:
+        assert torch.isfinite(x[r]).all() and torch.isnan(x[~r]).all(), x
+    for g in grads:
+        assert torch.isfinite(g[r]).all() and torch.isnan(g[~r]).all(), torch.isnan(g).sum(1)
