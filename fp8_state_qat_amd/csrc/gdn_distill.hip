@@ -388,9 +388,11 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
   }
   if (mark) __syncthreads();
 
-  // sums of 2^(z c / h - mh) and 2^(z c - m1), mh and m1 whole numbers near their largest arguments (so that what the
-  // fma rounds is the argument alone; h = 2: m1 is 2 mh); both are 0 where there is no value yet
-  float top = -INFINITY, mh = 0.0f, m1 = 0.0f, sum_h = 0.0f, sum_1 = 0.0f;
+  // sums of 2^((z - top) c / h) and 2^((z - top) c), top the largest value so far: exactly subtracted before it is
+  // scaled, so that no argument is above 0, however large the logits (a thread whose columns are all masked by the
+  // type's lowest value sums theirs, until a real one leaves 0 of the sum).  Both are 0 where there is no value yet
+  float top = -INFINITY, sum_h = 0.0f, sum_1 = 0.0f;
+  auto reference = [](float m) { return m > -INFINITY ? m : 0.0f; };
   if constexpr (kStats) {
     for (int tile = 0; tile < tiles; ++tile) {
       if (tile > 0) load(tile);
@@ -413,34 +415,30 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
 #pragma unroll
       for (int u = 0; u < U; ++u) m = fmaxf(m, x[u].largest());
       if (tile == 0) m = fmaxf(m, xe.largest());
-      if (m > top) {
-        const float nh = rintf(m * ch), n1 = square ? 2.0f * nh : rintf(m * kLog2ef);
-        if (top > -INFINITY) {
-          sum_h *= exp2_hw(mh - nh);
-          sum_1 *= exp2_hw(m1 - n1);
-        }
+      if (m > top) {   // a sum over no value is 0, or NaN
+        sum_h *= exp2_hw((top - m) * ch);
+        sum_1 *= exp2_hw((top - m) * kLog2ef);
         top = m;
-        mh = nh;
-        m1 = n1;
       }
+      const float to = reference(top);
       auto add = [&](const Oct<T>& y) {
         float v[8];
         y.get(v);
         if (!two) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum_h += exp2_hw(fmaf(v[i], ch, -mh));
+          for (int i = 0; i < 8; ++i) sum_h += exp2_hw((v[i] - to) * ch);
         } else if (square) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float e = exp2_hw(fmaf(v[i], ch, -mh));
+            const float e = exp2_hw((v[i] - to) * ch);
             sum_h += e;
             sum_1 = fmaf(e, e, sum_1);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            sum_h += exp2_hw(fmaf(v[i], ch, -mh));
-            sum_1 += exp2_hw(fmaf(v[i], kLog2ef, -m1));
+            sum_h += exp2_hw((v[i] - to) * ch);
+            sum_1 += exp2_hw((v[i] - to) * kLog2ef);
           }
         }
       };
@@ -454,12 +452,8 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
     }
     // over the wave, then the workgroup
     const float m = wave_max_dpp(top);
-    const float nh = m > -INFINITY ? rintf(m * ch) : 0.0f;
-    const float n1 = square ? 2.0f * nh : m > -INFINITY ? rintf(m * kLog2ef) : 0.0f;
-    if (top > -INFINITY) {
-      sum_h *= exp2_hw(mh - nh);
-      sum_1 *= exp2_hw(m1 - n1);
-    }
+    sum_h *= exp2_hw((top - reference(m)) * ch);
+    sum_1 *= exp2_hw((top - reference(m)) * kLog2ef);
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) {
       sum_h += __shfl_xor(sum_h, o, 64);
@@ -480,27 +474,22 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
       float m = -INFINITY;
 #pragma unroll
       for (int i = 0; i < NW; ++i) m = fmaxf(m, sh.red[0][i]);
-      const float nh = m > -INFINITY ? rintf(m * ch) : 0.0f;
-      const float n1 = square ? 2.0f * nh : m > -INFINITY ? rintf(m * kLog2ef) : 0.0f;
+      m = reference(m);
       double ah = 0.0, a1 = 0.0;
 #pragma unroll
       for (int i = 0; i < NW; ++i) {   // a wave without any value has sums of 0, or NaN
-        const float mw = sh.red[0][i];
-        const float wh = mw > -INFINITY ? rintf(mw * ch) : nh;
-        const float w1 = square ? 2.0f * wh : mw > -INFINITY ? rintf(mw * kLog2ef) : n1;
-        ah += (double)(sh.red[1][i] * exp2_hw(wh - nh));
-        a1 += (double)(sh.red[2][i] * exp2_hw(w1 - n1));
+        const float below = sh.red[0][i] - m;
+        ah += (double)(sh.red[1][i] * exp2_hw(below * ch));
+        a1 += (double)(sh.red[2][i] * exp2_hw(below * kLog2ef));
       }
-      // exponents are z fl(c / h): the same factor takes them back to z / h
-      const double bh = 1.0 / ((double)ch * (double)A.h), b1 = 1.0 / (double)kLog2ef;
-      const double mr = (double)nh * bh;
+      const double m1 = (double)m, mr = m1 / (double)A.h;
       lse_r = ah > 0.0 || ah != ah ? mr + log(ah) : -INFINITY;
       if (tail) {
         lse_h = log_add(mr, ah, kp.m / (double)A.h, kp.eh);
-        if (two) lse = log_add((double)n1 * b1, a1, kp.m, kp.e1);
+        if (two) lse = log_add(m1, a1, kp.m, kp.e1);
       } else {
         lse_h = lse_r;
-        if (two) lse = a1 > 0.0 || a1 != a1 ? (double)n1 * b1 + log(a1) : -INFINITY;
+        if (two) lse = a1 > 0.0 || a1 != a1 ? m1 + log(a1) : -INFINITY;
       }
       if (!two) lse = lse_h;
       double kd = kp.kd + (kp.mass > 0.0 ? kp.mass * lse_h : 0.0);

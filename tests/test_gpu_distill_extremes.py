@@ -144,3 +144,30 @@ def alone(d, good):
         assert torch.isfinite(x[r]).all() and torch.isnan(x[~r]).all(), x
     for g in grads:
         assert torch.isfinite(g[r]).all() and torch.isnan(g[~r]).all(), torch.isnan(g).sum(1)
+
+
+# ---------------------------------------------------------------- masks of finite values
+def masked(V, values, kept):
+    """A row for each value and mask: a run of columns to the end, an octet and a run, all but a few columns."""
+    z = torch.randn(3 * len(values), V, generator=torch.Generator().manual_seed(V))
+    for i, m in enumerate(values):
+        z[3 * i, V // 3:] = m
+        z[3 * i + 1, 8:16] = z[3 * i + 1, 24:V // 2] = m
+        z[3 * i + 2, :kept] = z[3 * i + 2, kept + 12:] = m
+    return z
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("h", [0.7, 1.0, 2.0, 3.0])
+@pytest.mark.parametrize("V", [60, 511, 700, 9001, 66000, 140003])
+def test_masked_by_finite_values(dtype, tail, h, V):
+    """Ranges of columns at the type's lowest value and others that stand for it."""
+    values = [torch.finfo(dtype).min, -1e30, -1e10, -1e9]
+    kept = 24 if V == 60 else V // 2 - 6
+    z = masked(V, values, kept)
+    R = len(z)
+    ids = torch.stack([torch.tensor([0, 1, 17]) if r % 3 < 2 else torch.tensor([kept, kept + 5, kept + 9])
+                       for r in range(R)])
+    losses, grads, stats = check(make(z, ids, dtype, tail, h=h))
+    assert torch.isfinite(stats).all()
