@@ -279,12 +279,13 @@ __device__ __forceinline__ DistillKept distill_kept(const DistillArgs& A, int64_
       o.n += __popcll(__ballot(id[i] >= 0));
     }
     o.m = (double)wave_max_dpp(zm);
+    const double m = o.m > -INFINITY ? o.m : 0.0;   // no value: sums of 0, or of a NaN
     double e1 = 0.0, eh = 0.0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (64 * i < K && id[i] >= 0 && o.m > -INFINITY) {
-        e1 += exp((double)zj[i] - o.m);
-        eh += exp(((double)zj[i] - o.m) / h);
+      if (64 * i < K && id[i] >= 0) {
+        e1 += exp((double)zj[i] - m);
+        eh += exp(((double)zj[i] - m) / h);
       }
     o.e1 = sum_f64(e1);
     o.eh = sum_f64(eh);
@@ -295,9 +296,9 @@ __device__ __forceinline__ DistillKept distill_kept(const DistillArgs& A, int64_
   return o;
 }
 
-// log(e^(m + ln s) + e^(n + ln t)) with s, t >= 0
+// log(e^(m + ln s) + e^(n + ln t)) with s, t >= 0 or NaN
 __device__ __forceinline__ double log_add(double m, double s, double n, double t) {
-  if (!(t > 0.0)) return s > 0.0 || s != s ? m + log(s) : -INFINITY;
+  if (t == 0.0) return s > 0.0 || s != s ? m + log(s) : -INFINITY;
   const double x = s > 0.0 || s != s ? fmax(m, n) : n;
   return x + log((s > 0.0 || s != s ? s * exp(m - x) : 0.0) + t * exp(n - x));
 }
@@ -517,7 +518,7 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
       // of every column: ea e^(z / h - l) + b e^(z - lse)
       double ea = a * m, l = lse_h;
       if (tail) {
-        const bool any = lse_r > -INFINITY;
+        const bool any = lse_r != -INFINITY;   // a NaN is a value
         ea = any ? a * (m * exp(lse_r - lse_h) - kp.rest) : 0.0;
         l = any ? lse_r : 0.0;
       }

@@ -171,3 +171,19 @@ def test_masked_by_finite_values(dtype, tail, h, V):
                        for r in range(R)])
     losses, grads, stats = check(make(z, ids, dtype, tail, h=h))
     assert torch.isfinite(stats).all()
+
+
+# ---------------------------------------------------------------- values that are not finite, beside a rest
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("ce", [False, True])
+@pytest.mark.parametrize("h", [1.0, 2.0, 3.0])
+@pytest.mark.parametrize("value", [INF, NAN])
+def test_a_logit_that_is_not_finite_beside_a_rest(dtype, ce, h, value):
+    """In a kept column, in all of them, in the target's, in others."""
+    V = 700
+    z = torch.randn(6, V, generator=torch.Generator().manual_seed(3))
+    ids = random_ids(6, V, 3, lo=20)
+    z[1, ids[1, 1]] = value
+    z[2, ids[2]] = value
+    z[3, 6] = z[4, 7] = value
+    alone(make(z, ids, dtype, True, ce, h), (0, 5))
