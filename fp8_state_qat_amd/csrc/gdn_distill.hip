@@ -515,11 +515,12 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
       const double wt = A.d_loss ? (double)A.d_loss[r] : 1.0;
       const double a = wt * (double)A.kd / (double)A.h, b = A.targets ? wt * (double)A.ce : 0.0;
       const double m = kp.mass + kp.rest;
-      // of every column: ea e^(z / h - l) + b e^(z - lse)
-      double ea = a * m, l = lse_h;
+      // of every column: ea e^(z / h - l) + eb e^(z - lse)
+      double ea = a * m, eb = b, l = lse_h;
       if (tail) {
         const bool any = lse_r != -INFINITY;   // a NaN is a value
         ea = any ? a * (m * exp(lse_r - lse_h) - kp.rest) : 0.0;
+        eb = any ? b : 0.0;   // none but -inf: no column takes them, and e^(l - lse) may be infinite
         l = any ? lse_r : 0.0;
       }
       DistillRow d;
@@ -530,12 +531,12 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
       d.lse_b = d.lse = b != 0.0 ? (float)(lse * c) : 0.0f;
       d.A = (float)ea;
       d.L = (float)(l * c);
-      d.B = (float)b;
-      if (b != 0.0 && !two) {                  // one exponential for both
-        d.A = (float)(ea + b * exp(l - lse));
+      d.B = (float)eb;
+      if (eb != 0.0 && !two) {                 // one exponential for both
+        d.A = (float)(ea + eb * exp(l - lse));
         d.B = 0.0f;
-      } else if (b != 0.0 && square) {
-        d.B = (float)(b * exp(2.0 * l - lse));
+      } else if (eb != 0.0 && square) {
+        d.B = (float)(eb * exp(2.0 * l - lse));
       }
       d.bad = kp.bad;
       if (kp.bad) d.A = NAN;

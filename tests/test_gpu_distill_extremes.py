@@ -187,3 +187,21 @@ def test_a_logit_that_is_not_finite_beside_a_rest(dtype, ce, h, value):
     z[2, ids[2]] = value
     z[3, 6] = z[4, 7] = value
     alone(make(z, ids, dtype, True, ce, h), (0, 5))
+
+
+# ---------------------------------------------------------------- a rest without any value
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("h", [1.0, 2.0, 3.0])
+@pytest.mark.parametrize("level", [-100.0, -600.0, 100.0])
+def test_every_column_that_is_not_kept_is_masked(dtype, h, level):
+    """By -inf: their gradient is 0.  What of p is kept sums to 1, so that no mass is left for the rest."""
+    V = 700
+    z = torch.full((4, V), -INF)
+    ids = random_ids(4, V, 3)
+    for r in range(4):
+        z[r, ids[r]] = level + torch.randn(3, generator=torch.Generator().manual_seed(r))
+    d = make(z, ids, dtype, True, h=h)
+    d["lse"] = (torch.logsumexp(d["top"].double() / h, 1) - 0.01).float()
+    _, grads, _ = check(d)
+    for g in grads:
+        assert (g[torch.isinf(d["z"])] == 0).all()
