@@ -17,7 +17,11 @@
 // The rest's sum is formed without the kept entries, as the difference of the
 // whole sum and theirs would cancel: a bitmap of I in LDS, a byte for each eight
 // columns.  All sums relative to their maximum; the few values of a row beyond
-// its sums (p, c, r, the loss) in fp64, as 1 - sum p cancels.
+// its sums (p, c, r, the loss) in fp64, as 1 - sum p cancels, and from differences
+// of logits only: a logsumexp is kept as a logit x and the rest of it, for next to
+// logits of 1e16 and more nothing is left of it in one number.  The backward reads
+// it as one fp32 number, off by 2^-24 of it and every probability by as much of
+// itself times it: rows where that passes 2^-15 are summed again.
 //
 // Memory bound: a row belongs to one workgroup, thread i of TPB to the octets of
 // eight columns i, i + TPB, ..; U octets a thread are asked for at once and
@@ -46,6 +50,7 @@ struct DistillArgs {
   int64_t row0, stride, d_stride, ignore;
   int V, K;
   float h, kd, ce;
+  double ih;                  // 1 / h
 };
 
 enum DistillMode { kDisFwd = 0, kDisBwd = 1, kDisBoth = 2 };
@@ -144,15 +149,34 @@ __device__ __forceinline__ void st_some(T* p, int lo, int hi, const float (&x)[8
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ double sum_f64(double x) { return last_lane(wave_prefix_f64(x)); }
 
+constexpr float kFar = 1024.0f;   // logsumexps above it are not taken from fp32 statistics
+
 // What a row's gradient is made of; exponentials in base 2.
 struct DistillRow {
-  float A, L;        // A 2^(z c / h - L) of every column (c = log2 e) ..
-  float B, lse;      // + B 2^(z c - lse); h = 2: + B (2^(z c / h - L))^2
-  float q, lse_h;    // kept columns beside a rest: q 2^(z c / h - lse_h) ..
-  float b, lse_b;    // .. + b 2^(z c - lse_b)
-  float a;           // factor of p
+  float A, x;        // A 2^((z - x) c / h) of every column (c = log2 e) ..
+  float B, x1;       // + B 2^((z - x1) c); h = 2: + B (2^((z - x) c / h))^2
+  float q, xh;       // kept columns beside a rest: q 2^((z - xh) c / h) ..
+  float b;           // .. + b 2^((z - x1) c)
+  float a, t;        // factors of p and of the target
   int bad;
 };
+
+// A logsumexp of z / h: x / h + s.
+struct DistillLse {
+  double x, s;
+  // from an fp32 number of at most kFar
+  __device__ __forceinline__ void read(float l, double h, double ih) {
+    x = (double)(float)((double)l * h);
+    s = (double)l - x * ih;
+  }
+};
+// A lane's value in every lane: wave 0 forms its few logarithms and exponentials one to a lane.
+__device__ __forceinline__ double of_lane(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
 
 constexpr int kHash = 1024;
 
@@ -172,8 +196,9 @@ struct DistillShared {
 // search through all pairs only where there are any).
 struct DistillKept {
   double c, mass, rest;   // c, sum p, r
-  double kd;              // sum p_j (ln p_j - z_j / h)
-  double m, e1, eh;       // the columns' largest z_j, sums of e^(z_j - m), e^((z_j - m) / h)
+  double m;               // the largest z_j (0: none is above -inf)
+  double kd;              // sum p_j (ln p_j - (z_j - m) / h)
+  double e1, eh;          // of the columns, sums of e^(z_j - m), e^((z_j - m) / h)
   int n;                  // columns
   bool bad;
 };
@@ -184,7 +209,7 @@ __device__ __forceinline__ DistillKept distill_kept(const DistillArgs& A, int64_
   constexpr int kPer = kMaxTop / 64;
   const int lane = threadIdx.x & 63, K = A.K;
   const bool tail = A.teacher_lse != nullptr;
-  const double h = (double)A.h;
+  const double ih = A.ih;
   DistillKept o;
 #pragma unroll
   for (int i = 0; i < kHash / 256; ++i) reinterpret_cast<uint4*>(sh.hash)[lane + 64 * i] = make_uint4(0, 0, 0, 0);
@@ -226,18 +251,23 @@ __device__ __forceinline__ DistillKept distill_kept(const DistillArgs& A, int64_
     double e = 0.0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (64 * i < K && t[i] > -INFINITY) e += exp(((double)t[i] - m) / h);
+      if (64 * i < K && t[i] > -INFINITY) e += exp(((double)t[i] - m) * ih);
     e = sum_f64(e);
-    o.c = e > 0.0 ? m / h + log(e) : -INFINITY;
+    o.c = e > 0.0 ? m * ih + log(e) : -INFINITY;
   }
+  float zm = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) zm = fmaxf(zm, zj[i]);
+  zm = wave_max_dpp(zm);
+  o.m = zm > -INFINITY ? (double)zm : 0.0;
   double p[kPer], sp = 0.0, kd = 0.0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     p[i] = 0.0;
     if (64 * i >= K) continue;
-    const double l = (double)t[i] / h - o.c;
+    const double l = (double)t[i] * ih - o.c;
     if (t[i] > -INFINITY) p[i] = exp(l);
-    if (p[i] > 0.0) kd += p[i] * (l - (double)zj[i] / h);
+    if (p[i] > 0.0) kd += p[i] * (l - ((double)zj[i] - o.m) * ih);
     sp += p[i];
     sh.id[lane + 64 * i] = id[i];
     sh.p[lane + 64 * i] = p[i];
@@ -272,21 +302,15 @@ __device__ __forceinline__ DistillKept distill_kept(const DistillArgs& A, int64_
   o.rest = 0.0;
   o.n = 0;
   if (tail) {
-    float zm = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (id[i] >= 0) zm = fmaxf(zm, zj[i]);
-      o.n += __popcll(__ballot(id[i] >= 0));
-    }
-    o.m = (double)wave_max_dpp(zm);
-    const double m = o.m > -INFINITY ? o.m : 0.0;   // no value: sums of 0, or of a NaN
     double e1 = 0.0, eh = 0.0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
+    for (int i = 0; i < kPer; ++i) {
+      o.n += __popcll(__ballot(id[i] >= 0));
       if (64 * i < K && id[i] >= 0) {
-        e1 += exp((double)zj[i] - m);
-        eh += exp(((double)zj[i] - m) / h);
+        e1 += exp((double)zj[i] - o.m);
+        eh += exp(((double)zj[i] - o.m) * ih);
       }
+    }
     o.e1 = sum_f64(e1);
     o.eh = sum_f64(eh);
     o.rest = o.n < A.V ? fmax(0.0, 1.0 - o.mass) : 0.0;   // no column is left: no rest
@@ -294,13 +318,6 @@ __device__ __forceinline__ DistillKept distill_kept(const DistillArgs& A, int64_
     o.mass = o.c > -INFINITY ? 1.0 : 0.0;
   }
   return o;
-}
-
-// log(e^(m + ln s) + e^(n + ln t)) with s, t >= 0 or NaN
-__device__ __forceinline__ double log_add(double m, double s, double n, double t) {
-  if (t == 0.0) return s > 0.0 || s != s ? m + log(s) : -INFINITY;
-  const double x = s > 0.0 || s != s ? fmax(m, n) : n;
-  return x + log((s > 0.0 || s != s ? s * exp(m - x) : 0.0) + t * exp(n - x));
 }
 
 }  // namespace
@@ -322,7 +339,7 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
   const bool ignored = A.targets != nullptr && target == A.ignore;
   const bool two = A.targets != nullptr && A.h != 1.0f;   // a second exponential:
   const bool square = A.h == 2.0f;                        // with h = 2 the first one's square
-  const float ch = (float)(1.4426950408889634 / (double)A.h);
+  const float ch = (float)(1.4426950408889634 * A.ih);
 
   // octet o: columns 8 o - shift .. + 7; whole ones from o0 to o1 - 1, at 16-byte addresses; the columns before and
   // behind them are thread 0's and 1's edge octet, from column e0 with e_lo .. e_hi - 1 of it in the row
@@ -394,6 +411,12 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
   // type's lowest value sums theirs, until a real one leaves 0 of the sum).  Both are 0 where there is no value yet
   float top = -INFINITY, sum_h = 0.0f, sum_1 = 0.0f;
   auto reference = [](float m) { return m > -INFINITY ? m : 0.0f; };
+  auto raise = [&](float m) {   // a sum over no value is 0, or NaN
+    sum_h *= exp2_hw((top - m) * ch);
+    sum_1 *= exp2_hw((top - m) * kLog2ef);
+    top = m;
+  };
+  bool again = kStats;
   if constexpr (kStats) {
     for (int tile = 0; tile < tiles; ++tile) {
       if (tile > 0) load(tile);
@@ -416,11 +439,7 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
 #pragma unroll
       for (int u = 0; u < U; ++u) m = fmaxf(m, x[u].largest());
       if (tile == 0) m = fmaxf(m, xe.largest());
-      if (m > top) {   // a sum over no value is 0, or NaN
-        sum_h *= exp2_hw((top - m) * ch);
-        sum_1 *= exp2_hw((top - m) * kLog2ef);
-        top = m;
-      }
+      if (m > top) raise(m);
       const float to = reference(top);
       auto add = [&](const Oct<T>& y) {
         float v[8];
@@ -451,10 +470,32 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
       }
       if (tile == 0 && edge) add(xe);
     }
-    // over the wave, then the workgroup
+  } else {
+    const float* s = A.stats + 4 * r;
+    again = fabsf(s[1]) > kFar || (A.targets != nullptr && fabsf(s[0]) > kFar) || (tail && fabsf(s[3]) > kFar);
+    if (again) {
+      __syncthreads();   // the table of the kept columns
+      auto kept = [&](int i) {
+        const uint32_t me = (uint32_t)i + 1;
+        for (uint32_t at = (me * 2654435761u) >> 22;; at = (at + 1) & (kHash - 1)) {   // at most kMaxTop entries: ends
+          const uint32_t was = sh.hash[at];
+          if (was == me || was == 0u) return was == me;
+        }
+      };
+#pragma unroll 1
+      for (int i = tid; i < V; i += TPB) {
+        if (tail && kept(i)) continue;
+        const float v = io<T>::ld(z + i);
+        if (v > top) raise(v);
+        const float to = reference(top);
+        sum_h += exp2_hw((v - to) * ch);
+        sum_1 += exp2_hw((v - to) * kLog2ef);
+      }
+    }
+  }
+  if (again) {   // over the wave, then the workgroup
     const float m = wave_max_dpp(top);
-    sum_h *= exp2_hw((top - reference(m)) * ch);
-    sum_1 *= exp2_hw((top - reference(m)) * kLog2ef);
+    raise(reference(m));
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) {
       sum_h += __shfl_xor(sum_h, o, 64);
@@ -470,11 +511,13 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
 
   // the row's few values: wave 0
   if (w == 0) {
-    double lse = 0.0, lse_h, lse_r;   // of z, of z / h, of z / h over the rest
-    if constexpr (kStats) {
+    const double ih = A.ih;
+    DistillLse all, one, rest;   // of z / h, of z, of z / h over the rest (s = -inf: no value)
+    if (again) {
       float m = -INFINITY;
 #pragma unroll
       for (int i = 0; i < NW; ++i) m = fmaxf(m, sh.red[0][i]);
+      const bool none = !(m > -INFINITY);
       m = reference(m);
       double ah = 0.0, a1 = 0.0;
 #pragma unroll
@@ -483,60 +526,71 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
         ah += (double)(sh.red[1][i] * exp2_hw(below * ch));
         a1 += (double)(sh.red[2][i] * exp2_hw(below * kLog2ef));
       }
-      const double m1 = (double)m, mr = m1 / (double)A.h;
-      lse_r = ah > 0.0 || ah != ah ? mr + log(ah) : -INFINITY;
-      if (tail) {
-        lse_h = log_add(mr, ah, kp.m / (double)A.h, kp.eh);
-        if (two) lse = log_add(m1, a1, kp.m, kp.e1);
-      } else {
-        lse_h = lse_r;
-        if (two) lse = a1 > 0.0 || a1 != a1 ? m1 + log(a1) : -INFINITY;
+      rest.x = all.x = (double)m;
+      double sh_ = ah, s1 = a1;
+      if (tail && kp.n > 0) {   // and the kept columns', relative to the larger maximum
+        const double x = none ? kp.m : kp.eh == 0.0 ? rest.x : fmax(rest.x, kp.m);
+        const double e = exp(lane == 0 ? (rest.x - x) * ih : lane == 1 ? (kp.m - x) * ih : lane == 2 ? rest.x - x : kp.m - x);
+        auto moved = [](double s, double by) { return s == 0.0 ? 0.0 : s * by; };
+        all.x = x;
+        sh_ = moved(ah, of_lane(e, 0)) + moved(kp.eh, of_lane(e, 1));
+        s1 = moved(a1, of_lane(e, 2)) + moved(kp.e1, of_lane(e, 3));
       }
-      if (!two) lse = lse_h;
-      double kd = kp.kd + (kp.mass > 0.0 ? kp.mass * lse_h : 0.0);
-      if (tail && kp.rest > 0.0) kd += kp.rest * (log(kp.rest) - (lse_r - lse_h));
-      double loss = (double)A.kd * kd;
-      if (A.targets != nullptr && !kp.bad) loss += (double)A.ce * (lse - (double)sh.zt);
-      if (lane == 0) A.loss[r] = kp.bad ? NAN : (float)loss;
-      if constexpr (MODE == kDisFwd) {
-        if (lane < 4) {
-          const double s = lane == 0 ? (A.targets ? lse : 0.0)
-                           : lane == 1 ? lse_h : lane == 2 ? kp.c : tail ? lse_r : 0.0;
-          A.stats[4 * r + lane] = kp.bad ? NAN : (float)s;
+      const double l = log(lane == 0 ? ah : lane == 1 ? sh_ : lane == 2 ? s1 : kp.rest);
+      rest.s = of_lane(l, 0);
+      all.s = of_lane(l, 1);
+      one.x = all.x;
+      one.s = two ? of_lane(l, 2) : all.s;
+      if constexpr (kStats) {
+        double kd = kp.kd + (kp.mass > 0.0 ? kp.mass * ((all.x - kp.m) * ih + all.s) : 0.0);
+        if (tail && kp.rest > 0.0)
+          kd += kp.rest * (of_lane(l, 3) - ((rest.x - all.x) * ih + (rest.s - all.s)));
+        double loss = (double)A.kd * kd;
+        if (A.targets != nullptr && !kp.bad) loss += (double)A.ce * ((one.x - (double)sh.zt) + one.s);
+        if (lane == 0) A.loss[r] = kp.bad ? NAN : (float)loss;
+        if constexpr (MODE == kDisFwd) {
+          if (lane < 4) {
+            const double s = lane == 0 ? (A.targets ? one.x + one.s : 0.0)
+                             : lane == 1 ? all.x * ih + all.s : lane == 2 ? kp.c : tail ? rest.x * ih + rest.s : 0.0;
+            A.stats[4 * r + lane] = kp.bad ? NAN : (float)s;
+          }
         }
       }
     } else {
-      lse = (double)A.stats[4 * r];
-      lse_h = (double)A.stats[4 * r + 1];
-      lse_r = (double)A.stats[4 * r + 3];
+      one.read(A.stats[4 * r], 1.0, 1.0);
+      all.read(A.stats[4 * r + 1], (double)A.h, ih);
+      rest.read(A.stats[4 * r + 3], (double)A.h, ih);
     }
     if constexpr (kGrad) {
-      constexpr double c = 1.4426950408889634;
       const double wt = A.d_loss ? (double)A.d_loss[r] : 1.0;
-      const double a = wt * (double)A.kd / (double)A.h, b = A.targets ? wt * (double)A.ce : 0.0;
+      const double a = wt * (double)A.kd * ih, b = A.targets ? wt * (double)A.ce : 0.0;
       const double m = kp.mass + kp.rest;
-      // of every column: ea e^(z / h - l) + eb e^(z - lse)
-      double ea = a * m, eb = b, l = lse_h;
+      // of every column: ea e^(z / h - l) + eb e^(z - one), l the rest's logsumexp where there is one
+      const DistillLse l = tail ? rest : all;
+      const double e = exp(lane == 0 ? -all.s : lane == 1 ? -l.s : lane == 2 ? -one.s : lane == 3 ? (l.x - one.x) - one.s
+                                     : (rest.x - all.x) * ih + (rest.s - all.s));
+      // (without any value there is none to take f e^inf)
+      auto times = [&](double f, int i) { return f == 0.0 && of_lane(e, i) == INFINITY ? 0.0 : f * of_lane(e, i); };
+      double ea = a * m, eb = b;
       if (tail) {
-        const bool any = lse_r != -INFINITY;   // a NaN is a value
-        ea = any ? a * (m * exp(lse_r - lse_h) - kp.rest) : 0.0;
-        eb = any ? b : 0.0;   // none but -inf: no column takes them, and e^(l - lse) may be infinite
-        l = any ? lse_r : 0.0;
+        const bool any = rest.s != -INFINITY;   // a NaN is a value
+        ea = any ? a * (m * of_lane(e, 4) - kp.rest) : 0.0;
+        eb = any ? b : 0.0;   // none but -inf: no column takes them, and e^(l - one) may be infinite
       }
       DistillRow d;
       d.a = (float)a;
-      d.q = (float)(a * m);
-      d.lse_h = (float)(lse_h * c);
-      d.b = (float)b;
-      d.lse_b = d.lse = b != 0.0 ? (float)(lse * c) : 0.0f;
-      d.A = (float)ea;
-      d.L = (float)(l * c);
-      d.B = (float)eb;
-      if (eb != 0.0 && !two) {                 // one exponential for both
-        d.A = (float)(ea + eb * exp(l - lse));
-        d.B = 0.0f;
-      } else if (eb != 0.0 && square) {
-        d.B = (float)(eb * exp(2.0 * l - lse));
+      d.t = (float)b;
+      d.xh = (float)all.x;
+      d.q = (float)times(a * m, 0);
+      d.x1 = (float)one.x;
+      d.b = (float)times(b, 2);
+      d.x = (float)l.x;
+      d.A = (float)times(ea, 1);
+      d.B = (float)times(eb, 2);
+      if (eb != 0.0 && (!two || square)) {   // one exponential for both
+        const double be = eb * of_lane(e, 3);
+        d.B = two ? (float)be : 0.0f;
+        if (!two) d.A = (float)(times(ea, 1) + be);
       }
       d.bad = kp.bad;
       if (kp.bad) d.A = NAN;
@@ -553,11 +607,9 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
     float val[kMine + 1];
     if (w == 0) {
       auto column = [&](float zv) {
-        float g = d.A * exp2_hw(fmaf(zv, ch, -d.L));
-        if (d.B != 0.0f) {
-          const float e = square ? exp2_hw(fmaf(zv, ch, -d.L)) : 0.0f;
-          g += d.B * (square ? e * e : exp2_hw(fmaf(zv, kLog2ef, -d.lse)));
-        }
+        const float e = exp2_hw((zv - d.x) * ch);
+        float g = d.A * e;
+        if (d.B != 0.0f) g += d.B * (square ? e * e : exp2_hw((zv - d.x1) * kLog2ef));
         return g;
       };
       bool met = false;
@@ -569,14 +621,14 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
         const float zv = sh.zj[j];
         float g;
         if (tail) {
-          g = d.q * exp2_hw(fmaf(zv, ch, -d.lse_h));
-          if (d.b != 0.0f) g += d.b * exp2_hw(fmaf(zv, kLog2ef, -d.lse_b));
+          g = d.q * exp2_hw((zv - d.xh) * ch);
+          if (d.b != 0.0f) g += d.b * exp2_hw((zv - d.x1) * kLog2ef);
         } else {
           g = column(zv);
         }
         g -= d.a * (float)sh.p[j];
         if (A.targets != nullptr && to[i] == (int)target) {
-          g -= d.b;
+          g -= d.t;
           met = true;
         }
         val[i] = g;
@@ -584,7 +636,7 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
       to[kMine] = -1;
       if (__ballot(met) == 0 && lane == 0 && A.targets != nullptr && !d.bad) {
         to[kMine] = (int)target;
-        val[kMine] = column(sh.zt) - d.b;
+        val[kMine] = column(sh.zt) - d.t;
       }
     }
     const bool vec = (uintptr_t)(dz + head) % 16 == 0;
@@ -593,17 +645,17 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
       y.get(v);
       if (d.B == 0.0f) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = d.A * exp2_hw(fmaf(v[i], ch, -d.L));
+        for (int i = 0; i < 8; ++i) g[i] = d.A * exp2_hw((v[i] - d.x) * ch);
       } else if (square) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float e = exp2_hw(fmaf(v[i], ch, -d.L));
+          const float e = exp2_hw((v[i] - d.x) * ch);
           g[i] = e * fmaf(d.B, e, d.A);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          g[i] = fmaf(d.B, exp2_hw(fmaf(v[i], kLog2ef, -d.lse)), d.A * exp2_hw(fmaf(v[i], ch, -d.L)));
+          g[i] = fmaf(d.B, exp2_hw((v[i] - d.x1) * kLog2ef), d.A * exp2_hw((v[i] - d.x) * ch));
       }
     };
     // the last tile first where both passes run: it is still in registers
@@ -682,7 +734,7 @@ hipError_t launch_distill(const gdn_distill_t& s, const void* logits, const int3
   a.d_loss = d_loss; a.loss = loss; a.stats = stats; a.dz = d_logits;
   a.stride = s.row_stride; a.d_stride = s.d_row_stride; a.ignore = s.ignore_index;
   a.V = s.vocab; a.K = s.topk;
-  a.h = s.temperature; a.kd = s.kd_weight; a.ce = s.ce_weight;
+  a.h = s.temperature; a.ih = 1.0 / (double)s.temperature; a.kd = s.kd_weight; a.ce = s.ce_weight;
   // Threads a row and octets a thread.  The losses: four octets on the way, many workgroups a compute unit (16384 x
   // 32000 bf16: 209 us; 16 octets took 256 registers and 670 us).  Both: as much of the row in registers as leaves two
   // workgroups a compute unit, the rest read again from the last-level cache (4096 x 131072 bf16: 442 us with 512

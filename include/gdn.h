@@ -574,8 +574,9 @@ gdn_status_t gdn_act_unpack(const uint8_t* codes, const float* scales, void* x, 
  *   - Logits of -inf (masked columns) are allowed: q = 0 there, the gradient too;
  *     a kept or target column among them makes the loss +inf.  Other non-finite
  *     logits make their row NaN.
- * Sums and statistics in fp32 relative to the row's maximum, the teacher's p and
- * the rest in fp64; a value of d_logits is rounded once.
+ * Sums in fp32 relative to the row's maximum, the teacher's p and what follows from
+ * the sums in fp64, from differences of logits; a value of d_logits is rounded once.
+ * Rows are as exact far from 0 as near it.
  */
 typedef struct {
     int64_t rows;              /* >= 0 */
@@ -606,7 +607,9 @@ gdn_status_t gdn_distill_fwd(const gdn_distill_t* shape, const void* logits, con
 /*
  * gdn_distill_bwd -- d_logits for the losses' gradients d_loss [rows] fp32 (NULL:
  * 1); the other arguments are the forward's, stats what it wrote.  d_logits may be
- * the logits themselves (same row stride), else they may not overlap.
+ * the logits themselves (same row stride), else they may not overlap.  A row whose
+ * statistics pass 1024 in magnitude, where 24 bits of them would show in its
+ * gradient, is summed again (and read twice).
  */
 gdn_status_t gdn_distill_bwd(const gdn_distill_t* shape, const void* logits, const int32_t* ids, const float* top,
                              const float* teacher_lse, const int64_t* targets, const float* stats,

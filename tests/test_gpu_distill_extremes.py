@@ -205,3 +205,38 @@ def test_every_column_that_is_not_kept_is_masked(dtype, h, level):
     _, grads, _ = check(d)
     for g in grads:
         assert (g[torch.isinf(d["z"])] == 0).all()
+
+
+# ---------------------------------------------------------------- rows whose logits are all far
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("V,h", [(301, 1.0), (700, 2.0), (5003, 0.7), (40000, 3.0)])
+def test_far_rows(dtype, tail, V, h):
+    """A row is as exact far from 0 as near it, also by the backward alone, whose statistics have 24 bits."""
+    gen = torch.Generator().manual_seed(V)
+    step = 128.0 if dtype == BF else 1.0
+    z = torch.stack([at + step * torch.randn(V, generator=gen).round() for at in (2e4, -2e4, 500.0, -1500.0)])
+    check(make(z, random_ids(4, V, 3), dtype, tail, h=h))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("V,h", [(60, 1.0), (700, 2.0), (700, 0.7), (9001, 1.0), (40000, 3.0)])
+def test_rows_whose_mask_leaves_nothing(dtype, tail, V, h):
+    """Every column at one far value: all are alike."""
+    low = torch.finfo(dtype).min
+    z = torch.stack([torch.full((V,), x) for x in (low, -1e30, -1e9, -3000.0, 1e20, -low)])
+    check(make(z, random_ids(6, V, 3), dtype, tail, h=h))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("h", [0.7, 1.0, 2.0, 3.0])
+@pytest.mark.parametrize("V", [60, 700, 9001])
+def test_a_rest_whose_mask_leaves_nothing(dtype, h, V):
+    """All but the kept columns at one far value: the rest's part of the gradient is spread over them alike."""
+    low = torch.finfo(dtype).min
+    ids = random_ids(4, V, 3)
+    z = torch.stack([torch.full((V,), x) for x in (low, -1e30, -1e9, -3000.0)])
+    for r in range(4):
+        z[r, ids[r]] = torch.randn(3, generator=torch.Generator().manual_seed(r))
+    check(make(z, ids, dtype, True, h=h))
