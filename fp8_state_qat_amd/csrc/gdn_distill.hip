@@ -215,7 +215,7 @@ __device__ __forceinline__ DistillKept distill_kept(const DistillArgs& A, int64_
   for (int i = 0; i < kHash / 256; ++i) reinterpret_cast<uint4*>(sh.hash)[lane + 64 * i] = make_uint4(0, 0, 0, 0);
   int id[kPer];
   float t[kPer], zj[kPer];
-  bool out = false;
+  bool out = false, used = false;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int j = lane + 64 * i;
@@ -223,8 +223,11 @@ __device__ __forceinline__ DistillKept distill_kept(const DistillArgs& A, int64_
     out |= id[i] >= A.V;
     if (id[i] >= A.V) id[i] = -1;
     t[i] = id[i] >= 0 ? A.top[r * K + j] : -INFINITY;
+    out |= !(t[i] < INFINITY);   // a NaN or +inf of the teacher's
+    used |= id[i] >= 0;
     zj[i] = id[i] >= 0 ? io<T>::ld(z + id[i]) : -INFINITY;
   }
+  if (tail) out |= used && !(fabsf(A.teacher_lse[r]) < INFINITY);
   o.bad = __ballot(out) != 0;
   bool dup = false;
   float tm = -INFINITY;

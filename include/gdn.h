@@ -569,8 +569,9 @@ gdn_status_t gdn_act_unpack(const uint8_t* codes, const float* scales, void* x, 
  *     add up); a row without any used entry has kd = 0.
  *   - A row whose target is ignore_index has loss, statistics and gradient 0, and
  *     its logits are not read for the gradient.
- *   - A row with an id >= vocab, or with another target outside [0, vocab), gets
- *     NaN everywhere.
+ *   - A row with an id >= vocab, with another target outside [0, vocab), or, where
+ *     an entry is used, with a kept logit of NaN or +inf or a teacher_lse that is
+ *     not finite, gets NaN everywhere.
  *   - Logits of -inf (masked columns) are allowed: q = 0 there, the gradient too;
  *     a kept or target column among them makes the loss +inf.  Other non-finite
  *     logits make their row NaN.

@@ -240,3 +240,28 @@ def test_a_rest_whose_mask_leaves_nothing(dtype, h, V):
     for r in range(4):
         z[r, ids[r]] = torch.randn(3, generator=torch.Generator().manual_seed(r))
     check(make(z, ids, dtype, True, h=h))
+
+
+# ---------------------------------------------------------------- the teacher's values
+@pytest.mark.parametrize("tail", [False, True])
+def test_a_teacher_that_is_not_finite_makes_its_row_nan(tail):
+    """NaN and +inf among the kept logits or as their logsumexp; entries that are not used are not looked at."""
+    V = 300
+    z, ids = torch.randn(9, V, generator=torch.Generator().manual_seed(1)), random_ids(9, V, 3)
+    d = make(z, ids, F32, tail)
+    clean = run(d)
+    d["top"][1, 0], d["top"][2, 2] = NAN, INF
+    d["top"][3] = NAN
+    d["ids"][5, 1] = -1
+    plain = run(d)
+    d["top"][5, 1] = NAN
+    bad = [1, 2, 3]
+    if tail:
+        d["lse"][6], d["lse"][7], d["lse"][8] = NAN, INF, -INF
+        bad += [6, 7, 8]
+    good = [r for r in range(9) if r not in bad]
+    alone(d, good)
+    got = run(d)
+    for x, y, p in zip((*got[0], *got[1]), (*clean[0], *clean[1]), (*plain[0], *plain[1])):
+        keep = [r for r in good if r != 5]
+        assert torch.equal(x[keep], y[keep]) and torch.equal(x[5], p[5])
