@@ -658,8 +658,8 @@ gdn_status_t check_distill(const gdn_distill_t* s, bool grad, const void* logits
   if (s->topk > 256) return fail(GDN_ERR_UNSUPPORTED, "topk above 256 is not supported (got %d)", s->topk);
   if (s->dtype != GDN_F32 && s->dtype != GDN_BF16)
     return fail(GDN_ERR_INVALID_ARG, "dtype must be GDN_F32 or GDN_BF16");
-  if (!(s->temperature > 0.0f) || !(s->temperature < 1e30f))
-    return fail(GDN_ERR_INVALID_ARG, "temperature must be positive and finite");
+  if (!(s->temperature >= 1e-30f) || !(s->temperature < 1e30f))   // their inverses are factors in fp32
+    return fail(GDN_ERR_INVALID_ARG, "temperature must be at least 1e-30 and below 1e30");
   if (s->row_stride < s->vocab || (grad && s->d_row_stride < s->vocab))
     return fail(GDN_ERR_INVALID_ARG, "row strides must be at least vocab");
   if (s->rows > 0 && (s->rows > ((int64_t)1 << 60) / s->row_stride ||

@@ -584,7 +584,7 @@ typedef struct {
     int32_t vocab;             /* 1 .. 2^20 */
     int32_t topk;              /* 0 .. 256 */
     int32_t dtype;             /* gdn_dtype_t of the logits and d_logits */
-    float temperature;         /* h > 0 */
+    float temperature;         /* h, 1e-30 .. 1e30 */
     float kd_weight, ce_weight;
     int64_t ignore_index;
     int64_t row_stride;        /* elements between rows of logits, >= vocab */
