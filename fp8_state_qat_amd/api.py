@@ -800,10 +800,15 @@ def _matrix(t, name):
     return rows, cols, stride
 
 
+_NEW = object()   # a gradient's tensor that is allocated here
+
+
 def _distill_args(logits, ids, top, teacher_lse, targets, temperature, kd_weight, ce_weight, ignore_index, out, *more):
     """Checked shape, the addresses of ids, top, teacher_lse, targets and of
-    `more`, and the gradient's tensor (out, or one like the logits)."""
+    `more`, and the gradient's tensor (out, one like the logits, or none)."""
     R, V, stride = _matrix(logits, "logits")
+    if out is not None and out is not _NEW and not isinstance(out, torch.Tensor):
+        raise ValueError("out must be a torch tensor")
     if logits.dtype not in _DT:
         raise ValueError("logits must be float32 or bfloat16")
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or ids.shape[0] != R:
@@ -823,7 +828,7 @@ def _distill_args(logits, ids, top, teacher_lse, targets, temperature, kd_weight
                              f"shape {tuple(out.shape)}")
         specs.append(("out", out if out.is_contiguous() else out[:1, :1], None, None))
     at = _args(("logits", logits if logits.is_contiguous() else logits[:1, :1], None, None), *specs)
-    if out is True:
+    if out is _NEW:
         out = logits.new_empty(R, V)
     elif out is not None:
         at.pop()
@@ -860,7 +865,7 @@ def distill_bwd(logits, ids, top, stats, d_loss=None, *, teacher_lse=None, targe
     if stats is None:
         raise ValueError("stats is required")
     shape, at, out = _distill_args(logits, ids, top, teacher_lse, targets, temperature, kd_weight, ce_weight,
-                                   ignore_index, True if out is None else out,
+                                   ignore_index, _NEW if out is None else out,
                                    ("stats", stats, torch.float32, (R, 4)), ("d_loss", d_loss, torch.float32, (R,)))
     _lib.check(_lib.lib().gdn_distill_bwd(shape, *at, out.data_ptr(), _stream_at()))
     return out
@@ -873,7 +878,7 @@ def distill_fwd_bwd(logits, ids, top, d_loss=None, *, teacher_lse=None, targets=
     distill_bwd.  Returns (loss [rows] fp32, d_logits)."""
     R = logits.shape[0] if isinstance(logits, torch.Tensor) and logits.dim() else 0
     shape, at, out = _distill_args(logits, ids, top, teacher_lse, targets, temperature, kd_weight, ce_weight,
-                                   ignore_index, True if out is None else out,
+                                   ignore_index, _NEW if out is None else out,
                                    ("d_loss", d_loss, torch.float32, (R,)))
     loss = top.new_empty(R)
     _lib.check(_lib.lib().gdn_distill_fwd_bwd(shape, *at, loss.data_ptr(), out.data_ptr(), _stream_at()))

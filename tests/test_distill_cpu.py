@@ -2,8 +2,9 @@
 import ctypes
 
 import pytest
+import torch
 
-from fp8_state_qat_amd import _lib
+from fp8_state_qat_amd import _lib, api
 
 P, FAKE = ctypes.c_void_p, 1 << 20
 
@@ -17,3 +18,12 @@ def test_temperatures_whose_inverse_leaves_fp32_are_refused(temperature):
     assert L.gdn_distill_fwd_bwd(ctypes.byref(s), *at, None) == 1 and "temperature" in _lib.last_error()
     assert L.gdn_distill_bwd(ctypes.byref(s), *at, None) == 1 and "temperature" in _lib.last_error()
     assert L.gdn_distill_fwd(ctypes.byref(s), *at[:7], None) == 1 and "temperature" in _lib.last_error()
+
+
+@pytest.mark.parametrize("out", [True, False, 3, "x", [[0.0]]])
+def test_an_out_that_is_no_tensor_is_refused(out):
+    a = torch.zeros(3, 20), torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, 2)
+    with pytest.raises(ValueError, match="out must be a torch tensor"):
+        api.distill_fwd_bwd(*a, out=out)
+    with pytest.raises(ValueError, match="out must be a torch tensor"):
+        api.distill_bwd(*a, torch.zeros(3, 4), out=out)
