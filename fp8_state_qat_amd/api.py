@@ -51,6 +51,16 @@ def _on_device(**tensors):
             dev = t.device
         elif t.device != dev:
             raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+    if dev is not None:
+        _current(dev.index)
+
+
+def _current(dev):
+    """The kernels run on the current device and its stream: tensors of another
+    one are refused."""
+    now = torch._C._cuda_getDevice()
+    if dev != now:
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{now}")
 
 
 def _stream():
@@ -381,7 +391,8 @@ def decode_step(q, k, v, beta, g, state, *, qdq=True, o=None, o_dtype=None, stat
 def _args(*specs):
     """Checks of (name, tensor or None, dtype or None, shape or None), in
     order: type, dtype, shape and contiguity of every tensor first, then that
-    all live on one device.  Returns their addresses (None for no tensor)."""
+    all live on the current device.  Returns their addresses (None for no
+    tensor)."""
     at = []
     dev, host, other = -1, None, None
     for name, t, dtype, shape in specs:
@@ -408,6 +419,8 @@ def _args(*specs):
         raise ValueError(f"{host} must be a device tensor")
     if other is not None:
         raise ValueError(f"{other[0]} is on cuda:{other[1]}, the other tensors on cuda:{dev}")
+    if dev >= 0:
+        _current(dev)
     return at
 
 
