@@ -594,21 +594,23 @@ struct GradWalk {
         });
   }
 
-  // Rows of a segment behind its sequence: zero gradients.
+  // Rows of a segment behind its sequence: zero gradients.  Counted in 64 bits: a
+  // segment may have 2^31 rows.
   __device__ __forceinline__ void clear_padding(int t0, int t1) const {
-    constexpr int kC = 16 * CG;
-    const int64_t from = (int64_t)t0 * a.H + h;
-    for (int i = threadIdx.x; i < (t1 - t0) * kC; i += kT)
-      ((E*)a.d_v)[(from + (int64_t)(i / kC) * a.H) * a.dv + kC * vt + i % kC] = 0;
+    constexpr int kC = 16 * CG, kPer = 16 / (int)sizeof(E);   // columns, of 16 bytes
+    const int64_t rows = t1 - t0, from = (int64_t)t0 * a.H + h;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (int64_t i = threadIdx.x; i < rows * (kC / kPer); i += kT)
+      *reinterpret_cast<uint4*>((E*)a.d_v + (from + i / (kC / kPer) * a.H) * a.dv + kC * vt + i % (kC / kPer) * kPer) = zero;
     if (vt != 0) return;
-    for (int i = threadIdx.x; i < (t1 - t0) * DK; i += kT) {
-      const int64_t e = (from + (int64_t)(i / DK) * a.H) * DK + i % DK;
-      ((E*)a.dq)[e] = 0;
-      ((E*)a.dk)[e] = 0;
+    for (int64_t i = threadIdx.x; i < rows * (DK / kPer); i += kT) {
+      const int64_t e = (from + i / (DK / kPer) * a.H) * DK + i % (DK / kPer) * kPer;
+      *reinterpret_cast<uint4*>((E*)a.dq + e) = zero;
+      *reinterpret_cast<uint4*>((E*)a.dk + e) = zero;
     }
-    for (int i = threadIdx.x; i < t1 - t0; i += kT) {
-      a.d_beta[from + (int64_t)i * a.H] = 0.0f;
-      a.dg[from + (int64_t)i * a.H] = 0.0f;
+    for (int64_t i = threadIdx.x; i < rows; i += kT) {
+      a.d_beta[from + i * a.H] = 0.0f;
+      a.dg[from + i * a.H] = 0.0f;
     }
   }
 

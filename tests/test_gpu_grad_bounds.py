@@ -1,0 +1,29 @@
+"""Gradients of the gated delta rule on the GPU at the borders that the calls document."""
+import pytest
+import torch
+
+from fp8_state_qat_amd import GdnError, api
+from fp8_state_qat_amd._lib import GDN_QDQ_CHUNK
+from test_gpu_grad import BF, F32, NAMES, bounds, close, dev, make, n_bounds, run, want
+
+pytestmark = pytest.mark.gpu
+
+
+def test_padding_of_more_than_2_24_rows_gets_zeros():
+    """Rows whose elements pass 2^31 in one segment."""
+    T, L, dk, dv = (1 << 24) + 70, 65, 128, 64
+    d = make([L], 1, dk, dv, BF, [L], False, False, seed=31)
+    x = {m: torch.zeros((T, *d[m].shape[1:]), dtype=d[m].dtype, device="cuda") for m in ("q", "k", "v", "beta", "g", "d_o")}
+    for m, t in x.items():
+        t[:L] = d[m].cuda()
+    outs = {n: torch.full_like(x[m], 7.0) for n, m in (("dq", "q"), ("dk", "k"), ("d_v", "v"), ("d_beta", "beta"), ("dg", "g"))}
+    cu, lens = (torch.tensor(t, dtype=torch.int32, device="cuda") for t in ([0, T], [L]))
+    got = api.chunk_grad(x["q"], x["k"], x["v"], x["beta"], x["g"], cu, x["d_o"], seq_lens=lens, check_status=True, **outs)
+    alone = run(d)
+    for name, a, b in zip(NAMES, got, alone):
+        if name == "dS0":
+            assert torch.equal(a, b)
+            continue
+        assert torch.equal(a[:L], b), name
+        for i in range(L, T, 1 << 21):
+            assert (a[i:i + (1 << 21)] == 0).all(), (name, i)
