@@ -428,7 +428,7 @@ struct GradWalk {
     get_planes(kReceiver ? swap() : swap_p(buf), lane(), f);
   }
 
-  // kKept: X is the state of this chunk alone, the next one's entry j
+  // kKept: X is the state of this chunk alone, the next one's entry j (none: -1)
   __device__ __forceinline__ void forward(const char* buf, float* err, const Next& then, int64_t j) {
     const char* sM = buf + Ls::oM;
     const GradGates& g = *reinterpret_cast<const GradGates*>(buf + Ls::oG);
@@ -465,8 +465,8 @@ struct GradWalk {
           } else if (i < iK) {
             if (i == iM) {
               give_sums(acc);
-              if constexpr (kKept) load(a.kept, j);
-              else decay(ec);
+              if constexpr (!kKept) decay(ec);
+              else if (j >= 0) load(a.kept, j);
               barrier_lds();
               float v[8];
               frag_values(vf, v);
@@ -645,7 +645,7 @@ struct GradWalk {
       Next then = at(min(it + 1, nch - 1));
       then.buf = lds0 + (uint32_t)(((it + 1) % Ls::kBufs) * Ls::buf + 1024 * w);
       if constexpr (kRev) backward(buf, a.Y + slot(it) * a.dv * kChunk, then);
-      else forward(buf, a.E + slot(it) * a.dv * kChunk, then, chunk0 + it);
+      else forward(buf, a.E + slot(it) * a.dv * kChunk, then, it + 1 < nch ? chunk0 + it : -1);
       if (!kKept && it + 1 < nch) dump((kRev ? a.R : a.S) + slot(it + 1) * a.dv * DK);
       if (Ls::kBufs == 1 && it + 1 < nch) {
         barrier_lds();

@@ -27,3 +27,15 @@ def test_padding_of_more_than_2_24_rows_gets_zeros():
         assert torch.equal(a[:L], b), name
         for i in range(L, T, 1 << 21):
             assert (a[i:i + (1 << 21)] == 0).all(), (name, i)
+
+
+@pytest.mark.parametrize("dk,dtype", [(64, BF), (128, BF), (128, F32)])
+def test_the_last_given_state_of_a_sequence_reaches_nothing(dk, dtype):
+    d = make([70, 0, 200, 64], 2, dk, 64, dtype, [70, 0, 190, 64], seed=32)
+    nb = n_bounds(d)
+    states = torch.randn(sum(nb), 2, 64, dk, generator=torch.Generator().manual_seed(33))
+    plain = run(d, states.cuda())
+    for n in (0, 2, 3):
+        states[sum(nb[:n + 1]) - 1] = float("nan")
+    for name, a, b in zip(NAMES, run(d, states.cuda()), plain):
+        assert torch.equal(a, b), name
