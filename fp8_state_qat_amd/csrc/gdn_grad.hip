@@ -5,10 +5,11 @@
 // Workspace: the status word and the chunk offsets (as in gdn_chunk_fwd's),
 // one record for each (chunk, head), the gradients of the states after every
 // chunk, the tokens' errors and their gradients, and without given states those
-// entering every chunk.  With the state's QDQ in
-// the chunks and no given states, the forward runs again, its own code with
-// the boundary record, so that the gradients are taken at the very states it
-// had; its outputs, last states and workspace follow then.
+// entering every chunk.  With the state's QDQ in the chunks and no given states,
+// the forward runs again, its own code with the boundary record, so that the
+// gradients are taken at the very states it had.  Its workspace is then the first
+// part, with the status word and the offsets that the whole call uses (what it
+// finds on the device is the call's), and its outputs and last states the last.
 #include "gdn_grad.hpp"
 
 namespace gdn {
@@ -16,8 +17,9 @@ namespace gdn {
 namespace {
 
 struct GradLayout {
-  size_t offs, rec, R, E, Y, S, o, fin, fwd, bytes;
+  size_t rec, R, E, Y, S, o, fin, bytes;
   int64_t chunks, items;
+  bool again;   // the forward runs again
 };
 
 size_t pad256(size_t x) { return (x + 255) / 256 * 256; }
@@ -35,18 +37,17 @@ GradLayout grad_layout(const gdn_shape_t& s, bool given) {
   l.items = l.chunks * s.n_heads;
   const size_t rec = s.io_dtype == GDN_BF16 ? GradRec<EngBF16>::kBytes : GradRec<EngF32>::kBytes;
   const size_t states = (size_t)l.items * s.dv * s.dk * 4;
-  l.offs = kStatusBytes;
-  l.rec = l.offs + pad256((size_t)(s.n_seqs + 2) * 4);
+  l.again = !given && (s.qdq_flags & GDN_QDQ_CHUNK);
+  l.rec = l.again ? pad256(prep_workspace_bytes(again(s))) : kStatusBytes + pad256((size_t)(s.n_seqs + 2) * 4);
   l.R = l.rec + pad256((size_t)l.items * rec);
   l.E = l.R + states;
   l.Y = l.E + (size_t)l.items * s.dv * kChunk * 4;
   l.S = l.Y + (size_t)l.items * s.dv * kChunk * 4;
   l.o = l.S + (given ? 0 : states);
   l.bytes = l.o;
-  if (!given && (s.qdq_flags & GDN_QDQ_CHUNK)) {
+  if (l.again) {
     l.fin = l.o + pad256((size_t)s.total_tokens * s.n_heads * s.dv * (s.io_dtype == GDN_BF16 ? 2 : 4));
-    l.fwd = l.fin + pad256((size_t)s.n_seqs * s.n_heads * s.dv * s.dk * 4);
-    l.bytes = l.fwd + prep_workspace_bytes(again(s));
+    l.bytes = l.fin + pad256((size_t)s.n_seqs * s.n_heads * s.dv * s.dk * 4);
   }
   return l;
 }
@@ -70,20 +71,21 @@ hipError_t launch_chunk_grad(const gdn_shape_t& s, const void* q, const void* k,
   char* w = reinterpret_cast<char*>(workspace);
   PrepLayout L{};
   L.status = reinterpret_cast<int32_t*>(w);
-  L.offs = reinterpret_cast<int32_t*>(w + l.offs);
+  L.offs = reinterpret_cast<int32_t*>(w + kStatusBytes);
   L.items = l.items;
-  hipError_t e = launch_prep(s, q, k, beta, g, cu_seqlens, seq_lens, nullptr, L, false, nullptr, nullptr, stream);
-  if (e != hipSuccess) return e;
-  if (states == nullptr && (s.qdq_flags & GDN_QDQ_CHUNK)) {
+  hipError_t e;
+  if (l.again) {
     gdn_debug_t d{};
     d.bound_offsets = L.offs;
     d.bound_post = reinterpret_cast<float*>(w + l.S);
     e = launch_chunk_fwd(again(s), q, k, v, beta, g, cu_seqlens, seq_lens, nullptr, initial_state, w + l.o,
-                         reinterpret_cast<float*>(w + l.fin), w + l.fwd, &d, stream);
-    if (e != hipSuccess) return e;
+                         reinterpret_cast<float*>(w + l.fin), w, &d, stream);
     states = d.bound_post;
     n_states = l.chunks;
+  } else {
+    e = launch_prep(s, q, k, beta, g, cu_seqlens, seq_lens, nullptr, L, false, nullptr, nullptr, stream);
   }
+  if (e != hipSuccess) return e;
   GradArgs a{};
   a.q = q; a.k = k; a.v = v; a.d_o = d_o;
   a.beta = beta; a.g = g;

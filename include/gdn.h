@@ -379,7 +379,7 @@ size_t gdn_chunk_bwd_workspace_bytes(const gdn_shape_t* shape);
  *   workspace  gdn_chunk_grad_workspace_bytes(shape, states != NULL) bytes,
  *              256-byte aligned; holds the call's status word on return
  *              (gdn_workspace_status; index arrays out of contract: nothing is
- *              written)
+ *              written; with states computed again also that of the forward)
  * Rows of a segment past L_n get zero gradients (what the inputs hold there is
  * not read); rows outside every segment are not written.  dg is exactly 0 where
  * e^g is.  An infinity or a NaN reaches gradients of its own sequence and head
@@ -401,7 +401,8 @@ gdn_status_t gdn_chunk_grad(const gdn_shape_t* shape,
                             void* workspace, size_t workspace_bytes, void* stream);
 /* Workspace bytes of gdn_chunk_grad: for each 64 tokens and head a record of
  * 32 KiB (fp32 inputs: 22), 512 dv bytes, and 4 dk dv bytes, twice those without
- * given states; 0 for an invalid shape. */
+ * given states; with GDN_QDQ_CHUNK and none given gdn_chunk_fwd's workspace, o and
+ * final_state too.  0 for an invalid shape. */
 size_t gdn_chunk_grad_workspace_bytes(const gdn_shape_t* shape, int32_t states_given);
 
 /*

@@ -39,3 +39,28 @@ def test_the_last_given_state_of_a_sequence_reaches_nothing(dk, dtype):
         states[sum(nb[:n + 1]) - 1] = float("nan")
     for name, a, b in zip(NAMES, run(d, states.cuda()), plain):
         assert torch.equal(a, b), name
+
+
+@pytest.mark.parametrize("dk,dtype", [(64, BF), (128, BF), (64, F32), (128, F32)])
+def test_the_forward_run_again_shares_the_call_s_status(dk, dtype):
+    """Index arrays out of contract write nothing and are reported; the same workspace serves the next call; no tokens."""
+    d = make([130, 64], 2, dk, 64, dtype, seed=34)
+    x = dev(d)
+    plain = run(d, qdq_flags=GDN_QDQ_CHUNK)
+    ws = torch.empty(api.chunk_grad_workspace_bytes(2, 2, dk, 64, 194, dtype, GDN_QDQ_CHUNK), dtype=torch.uint8,
+                     device="cuda")
+    outs = dict(dq=x["q"], dk=x["k"], d_v=x["v"], d_beta=x["beta"], dg=x["g"], d_initial_state=x["S0"])
+    outs = {m: torch.full_like(t, 3.0) for m, t in outs.items()}
+    for bad in ([0, 130, 100], [0, 64, 500], [-1, 64, 100]):
+        cu = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        with pytest.raises(GdnError, match="out of contract"):
+            api.chunk_grad(x["q"], x["k"], x["v"], x["beta"], x["g"], cu, x["d_o"], initial_state=x["S0"],
+                           qdq_flags=GDN_QDQ_CHUNK, workspace=ws, check_status=True, **outs)
+        for m, t in outs.items():
+            assert (t == 3.0).all(), m
+    got = run(d, qdq_flags=GDN_QDQ_CHUNK, workspace=ws)
+    for name, a, b in zip(NAMES, got, plain):
+        assert torch.equal(a, b), name
+    e = make([0, 0], 2, dk, 64, dtype, seed=35)
+    got = run(e, qdq_flags=GDN_QDQ_CHUNK)
+    assert got[0].shape == (0, 2, dk) and torch.equal(got[5], e["dS"].cuda())
