@@ -185,11 +185,11 @@ struct DistillShared {
   int id[kMaxTop];                  // -1: unused, or not the column's first entry
   float zj[kMaxTop];
   float zt;                         // the target's logit
-  int dup;
   float red[3][16];
   DistillRow row;
-  uint32_t hash[kHash];
+  alignas(16) uint32_t hash[kHash];   // id + 1, 0: free
 };
+static_assert(sizeof(DistillShared) % 16 == 0, "the bitmap behind it");
 
 // The kept entries of a row, one wave: p, the sums over them that the row's
 // values need, and the columns that come twice, found by a table of the ids (a
