@@ -64,3 +64,19 @@ def test_the_forward_run_again_shares_the_call_s_status(dk, dtype):
     e = make([0, 0], 2, dk, 64, dtype, seed=35)
     got = run(e, qdq_flags=GDN_QDQ_CHUNK)
     assert got[0].shape == (0, 2, dk) and torch.equal(got[5], e["dS"].cuda())
+
+
+# Norms of errors.  States, their gradients, d_v before its rounding, d_beta and dg take terms of 24 bits and sums in
+# fp32: a product of at most 64 tokens and 128 channels is off by sqrt(192) 2^-24 of its terms' norm, for errors of
+# random signs, and a path from the inputs to an output has at most five such products: sqrt(5 * 192) 2^-24 < 2^-19.
+# (Terms of 16 bits would be off by 2^-17 / sqrt(3) each.)  With fp32 inputs the other gradients are as exact.
+@pytest.mark.parametrize("dk,dv,dtype,given", [(64, 64, BF, False), (128, 128, BF, False), (64, 128, BF, True),
+                                               (128, 192, BF, True), (64, 64, F32, False), (128, 128, F32, True)])
+def test_terms_of_24_bits(dk, dv, dtype, given):
+    d = make([700, 130], 2, dk, dv, dtype, seed=36)
+    states = torch.randn(sum(n_bounds(d)), 2, dv, dk, generator=torch.Generator().manual_seed(37)) if given else None
+    got, wanted = run(d, None if states is None else states.cuda()), want(d, states)
+    for name, g, w in zip(NAMES, got, wanted):
+        if g.dtype == F32:
+            err = float((g.double().cpu() - w).norm() / w.norm())
+            assert err < 2.0 ** -19, (name, err)
