@@ -385,10 +385,9 @@ size_t gdn_chunk_bwd_workspace_bytes(const gdn_shape_t* shape);
  * e^g is.  An infinity or a NaN reaches gradients of its own sequence and head
  * only.  Outputs may not overlap inputs.
  *
- * The states, their gradients, d_v before its rounding, d_beta and dg take terms
- * of 24 significant bits, dq and dk of bf16 inputs terms of 16 or more; d_beta and
- * dg are sums of terms that can cancel, off by about 2^-19 of the sum of their
- * terms' magnitudes in the chunk at most.
+ * The states, their gradients and every output before its rounding take terms of
+ * 24 significant bits; d_beta and dg are sums of terms that can cancel, off by about
+ * 2^-19 of the sum of their terms' magnitudes in the chunk at most.
  */
 gdn_status_t gdn_chunk_grad(const gdn_shape_t* shape,
                             const void* q, const void* k, const void* v,

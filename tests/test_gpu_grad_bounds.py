@@ -80,3 +80,18 @@ def test_terms_of_24_bits(dk, dv, dtype, given):
         if g.dtype == F32:
             err = float((g.double().cpu() - w).norm() / w.norm())
             assert err < 2.0 ** -19, (name, err)
+
+
+# A bf16 value of a sum that is off by e is off from the rounded sum's border by more than half a step only where the
+# sum lies within e of it, which has a chance of 2 e over the step, 2^-8 of the value: with e = 2^-19 (above) the excess
+# over half a step is in norm 2^-19 sqrt(2 * 2^-19 / 2^-8) = 2^-24 of the values', held to 4 times that.  (Terms of 16
+# bits: sqrt(5) 2^-17, an excess of 2^-20.)
+@pytest.mark.parametrize("dk,dv,given", [(64, 64, False), (128, 128, False), (64, 128, True), (128, 192, True)])
+def test_bf16_gradients_are_sums_of_24_bits_rounded_once(dk, dv, given):
+    d = make([700, 130], 2, dk, dv, BF, seed=38)
+    states = torch.randn(sum(n_bounds(d)), 2, dv, dk, generator=torch.Generator().manual_seed(39)) if given else None
+    got, wanted = run(d, None if states is None else states.cuda()), want(d, states)
+    for name, g, w in zip(NAMES[:3], got, wanted):
+        half = torch.ldexp(torch.ones_like(w), torch.frexp(w).exponent - 9)   # of a value's step, 2^-7 of its power of 2
+        excess = ((g.double().cpu() - w).abs() - half).clamp(min=0)
+        assert float(excess.norm() / w.norm()) < 2.0 ** -22, (name, float(excess.norm() / w.norm()))
