@@ -739,17 +739,20 @@ hipError_t launch_distill(const gdn_distill_t& s, const void* logits, const int3
   a.V = s.vocab; a.K = s.topk;
   a.h = s.temperature; a.ih = 1.0 / (double)s.temperature; a.kd = s.kd_weight; a.ce = s.ce_weight;
   // Threads a row and octets a thread.  The losses: four octets on the way, many workgroups a compute unit (16384 x
-  // 32000 bf16: 209 us; 16 octets took 256 registers and 670 us).  Both: as much of the row in registers as leaves two
-  // workgroups a compute unit, the rest read again from the last-level cache (4096 x 131072 bf16: 442 us with 512
+  // 32000 bf16: 192 us; 16 octets took 256 registers and 670 us), and 1024 threads for a long row where each has a
+  // compute unit to itself (256 x 131072: bf16 19 us for 35 with 256 threads, fp32 25.4 for 26.5; 1024 x 131072 would
+  // take 65 for 51 and 97 for 89, 4096 rows in bf16 283 for 193).  Both: as much of the row in registers as leaves two
+  // workgroups a compute unit, the rest read again from the last-level cache (4096 x 131072 bf16: 438 us with 512
   // threads and half a row, 612 with 1024 and all of it, 484 with 256 and a quarter).  The gradient alone, bf16: 417 us
   // with 16 octets, 441 with four (16384 x 32000); fp32: as below.
   const int octs = s.vocab / 8 + 2;
+  const bool alone = octs > 8192 && s.rows <= device_cu_count();
   if (s.dtype == GDN_BF16) {
     if (octs <= 64 * 4) return launch_rows<uint16_t, 64, 4>(s, a, mode, stream);
     if (octs <= 256 * 4) return launch_rows<uint16_t, 256, 4>(s, a, mode, stream);
     if (mode == kDisFwd)
-      return octs <= 8192 ? launch_row<uint16_t, 256, 4, kDisFwd>(s, a, stream)
-                          : launch_row<uint16_t, 1024, 4, kDisFwd>(s, a, stream);
+      return alone ? launch_row<uint16_t, 1024, 4, kDisFwd>(s, a, stream)
+                   : launch_row<uint16_t, 256, 4, kDisFwd>(s, a, stream);
     if (mode == kDisBwd) return launch_row<uint16_t, 256, 16, kDisBwd>(s, a, stream);
     return octs <= 256 * 16 ? launch_row<uint16_t, 256, 16, kDisBoth>(s, a, stream)
                             : launch_row<uint16_t, 512, 16, kDisBoth>(s, a, stream);
@@ -757,13 +760,14 @@ hipError_t launch_distill(const gdn_distill_t& s, const void* logits, const int3
   if (octs <= 64 * 4) return launch_rows<float, 64, 4>(s, a, mode, stream);
   if (octs <= 256 * 4) return launch_rows<float, 256, 4>(s, a, mode, stream);
   if (mode == kDisFwd)
-    return octs <= 8192 ? launch_row<float, 256, 4, kDisFwd>(s, a, stream)
-                        : launch_row<float, 1024, 4, kDisFwd>(s, a, stream);
+    return alone ? launch_row<float, 1024, 4, kDisFwd>(s, a, stream) : launch_row<float, 256, 4, kDisFwd>(s, a, stream);
   // the gradient alone: a row in the fewest turns once it fills most of 1024 threads (4000 x 32000: 174 us for 199
   // with 256 threads, 1000 x 50001 77 for 83; 1000 x 20011 would take 36.5 for 34.8)
   if (mode == kDisBwd)
     return octs < 3584 ? launch_row<float, 256, 4, kDisBwd>(s, a, stream)
                        : launch_row<float, 1024, 4, kDisBwd>(s, a, stream);
+  // both, fp32: 256 threads while they hold the row (4000 x 16000: 90 us for 105 with 512), else 512 (2000 x 50001: 163
+  // us; 256 threads 182, 256 and 1024 threads of four octets 193)
   return octs <= 256 * 8 ? launch_row<float, 256, 8, kDisBoth>(s, a, stream)
                          : launch_row<float, 512, 8, kDisBoth>(s, a, stream);
 }

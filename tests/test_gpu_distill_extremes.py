@@ -265,3 +265,20 @@ def test_a_teacher_that_is_not_finite_makes_its_row_nan(tail):
     for x, y, p in zip((*got[0], *got[1]), (*clean[0], *clean[1]), (*plain[0], *plain[1])):
         keep = [r for r in good if r != 5]
         assert torch.equal(x[keep], y[keep]) and torch.equal(x[5], p[5])
+
+
+# ---------------------------------------------------------------- many rows
+@pytest.mark.parametrize("dtype,V,h", [(BF, 131075, 2.0), (F32, 70001, 1.0)])
+def test_many_rows_of_a_wide_vocabulary(dtype, V, h):
+    """More rows than compute units, whose long rows go by fewer threads each; masked columns among them."""
+    z = torch.randn(4, V, generator=torch.Generator().manual_seed(V))
+    ids = random_ids(4, V, 3)
+    z[1, :V // 2] = torch.finfo(dtype).min
+    z[1, ids[1]] = 1.0
+    d = make(z, ids, dtype, True, h=h)
+    loss, _, _ = reference(d)
+    x = {n: d[n].cuda().repeat(100, *[1] * (d[n].dim() - 1)) for n in ("z", "ids", "top", "lse", "targets")}
+    got, stats = api.distill_fwd(x["z"], x["ids"], x["top"], teacher_lse=x["lse"], targets=x["targets"], **d["kw"])
+    got, stats = got.view(100, 4).cpu(), stats.view(100, 4, 4).cpu()
+    assert (got == got[0]).all() and (stats == stats[0]).all() and torch.isfinite(stats).all()
+    assert ((got[0].double() - loss).abs() <= 2.0 ** -14 + 2.0 ** -23 * loss.abs()).all()
