@@ -1055,7 +1055,7 @@ __global__ __launch_bounds__(kThreads, Eng::kSplit ? 2 : 1) void grad_chunk_kern
     e *= (double)g.eg[t];
     p += e - ye_;
     double d = (double)g.ec[0] * zz + last_lane(wave_prefix_f64(e)) - (wave_prefix_f64(p) - p);
-    if (g.g[t] < -104.0f) d = 0.0;   // e^-104 rounds to 0: nothing lies across the token
+    if (g.g[t] < -103.97208f) d = 0.0;   // e^g rounds to 0 (below 2^-150): nothing lies across the token
     if (t < nv) {
       a.d_beta[row0 + (int64_t)t * H] = (float)(ye_ / (double)g.beta[t]);
       a.dg[row0 + (int64_t)t * H] = (float)d;

@@ -382,7 +382,8 @@ size_t gdn_chunk_bwd_workspace_bytes(const gdn_shape_t* shape);
  *              written; with states computed again also that of the forward)
  * Rows of a segment past L_n get zero gradients (what the inputs hold there is
  * not read); rows outside every segment are not written.  dg is exactly 0 where
- * e^g is.  An infinity or a NaN reaches gradients of its own sequence and head
+ * e^g is in fp32.  A beta below 2^-60 in magnitude counts as that (d_v is 0 where it
+ * is 0, d_beta what it would be).  An infinity or a NaN reaches gradients of its own sequence and head
  * only.  Outputs may not overlap inputs.
  *
  * The states, their gradients and every output before its rounding take terms of

@@ -95,3 +95,14 @@ def test_bf16_gradients_are_sums_of_24_bits_rounded_once(dk, dv, given):
         half = torch.ldexp(torch.ones_like(w), torch.frexp(w).exponent - 9)   # of a value's step, 2^-7 of its power of 2
         excess = ((g.double().cpu() - w).abs() - half).clamp(min=0)
         assert float(excess.norm() / w.norm()) < 2.0 ** -22, (name, float(excess.norm() / w.norm()))
+
+
+@pytest.mark.parametrize("dk,dtype", [(64, BF), (128, F32)])
+def test_dg_is_0_where_a_decay_is_0_in_fp32(dk, dtype):
+    """e^g is 0 below 2^-150: g <= -103.97208, and 2^-149 from the next value on."""
+    d = make([130], 2, dk, 64, dtype, seed=40)
+    d["g"][7], d["g"][70], d["g"][71], d["g"][100] = -103.98, -103.99, -104.5, -103.97209
+    assert float(torch.tensor(-103.97209).exp()) == 0
+    got = run(d)[4]
+    assert (got[[7, 70, 71, 100]] == 0).all(), got[[7, 70, 71, 100]]
+    assert (got[[6, 8, 69, 72]] != 0).all()
