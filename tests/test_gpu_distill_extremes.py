@@ -282,3 +282,48 @@ def test_many_rows_of_a_wide_vocabulary(dtype, V, h):
     got, stats = got.view(100, 4).cpu(), stats.view(100, 4, 4).cpu()
     assert (got == got[0]).all() and (stats == stats[0]).all() and torch.isfinite(stats).all()
     assert ((got[0].double() - loss).abs() <= 2.0 ** -14 + 2.0 ** -23 * loss.abs()).all()
+
+
+# ---------------------------------------------------------------- the largest sizes
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("off", [0, 1])
+def test_the_largest_vocabulary(dtype, tail, off):
+    """2^20 columns, the row at any address, 256 kept of which some come twice."""
+    V, K = 1 << 20, 256
+    z = torch.randn(1, V, generator=torch.Generator().manual_seed(5))
+    ids = random_ids(1, V, K)
+    ids[0, 100:110], ids[0, 3] = ids[0, 50], V - 1
+    d = make(z, ids, dtype, tail, h=2.0)
+    loss, dz, mag = reference(d)
+    box = torch.zeros(V + 8, dtype=dtype, device="cuda")
+    x = box[off:off + V].view(1, V)
+    x.copy_(d["z"])
+    kw = dict(teacher_lse=None if d["lse"] is None else d["lse"].cuda(), targets=d["targets"].cuda(), **d["kw"])
+    a = x, d["ids"].cuda(), d["top"].cuda()
+    got, stats = api.distill_fwd(*a, **kw)
+    w = d["d_loss"].cuda()
+    both, g = api.distill_fwd_bwd(*a, w, **kw)
+    back = api.distill_bwd(*a, stats, w, out=x, **kw)
+    for v in (got, both):
+        assert ((v.double().cpu() - loss).abs() <= 2.0 ** -14 + 2.0 ** -23 * loss.abs()).all()
+    for v in (g, back):
+        tol = 2.0 ** -14 * mag + (2.0 ** -8 * dz.abs() if dtype == BF else 0) + 1e-36
+        assert ((v.double().cpu() - dz).abs() <= tol).all()
+    assert (box[:off] == 0).all() and (box[off + V:] == 0).all()
+
+
+def test_more_rows_than_a_launch_has():
+    """2^26 rows of two columns: the rows of the second launch come out as alone."""
+    R = (1 << 26) + 70
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    z = torch.randn(R, 2, generator=gen, device="cuda")
+    ids = torch.randint(2, (R, 1), generator=gen, device="cuda").int()
+    top, targets = torch.randn(R, 1, generator=gen, device="cuda"), torch.randint(2, (R,), generator=gen, device="cuda")
+    loss, g = api.distill_fwd_bwd(z, ids, top, targets=targets, ce_weight=0.5)
+    end = [t[-100:].contiguous() for t in (z, ids, top)]
+    l1, g1 = api.distill_fwd_bwd(*end, targets=targets[-100:].contiguous(), ce_weight=0.5)
+    assert torch.equal(loss[-100:], l1) and torch.equal(g[-100:], g1)
+    want = -torch.log_softmax(z[::4096].double(), 1)
+    want = want.gather(1, ids[::4096].long()) + 0.5 * want.gather(1, targets[::4096, None])
+    assert ((loss[::4096, None].double() - want).abs() <= 2.0 ** -14 + 2.0 ** -23 * want.abs()).all()
