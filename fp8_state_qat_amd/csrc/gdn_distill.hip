@@ -161,13 +161,14 @@ struct DistillRow {
   int bad;
 };
 
-// A logsumexp of z / h: x / h + s.
+// A logsumexp of z / h: x / h + s; f = e^-s (large, not infinite, where there is no value).
 struct DistillLse {
-  double x, s;
-  // from an fp32 number of at most kFar
+  double x, s, f;
+  // from an fp32 number of at most kFar: |s| <= 2^-14, so f has an error of 2^-44
   __device__ __forceinline__ void read(float l, double h, double ih) {
     x = (double)(float)((double)l * h);
     s = (double)l - x * ih;
+    f = fma(s, fma(s, 0.5, -1.0), 1.0);
   }
 };
 // A lane's value in every lane: wave 0 forms its few logarithms and exponentials one to a lane.
@@ -198,7 +199,7 @@ struct DistillKept {
   double c, mass, rest;   // c, sum p, r
   double m;               // the largest z_j (0: none is above -inf)
   double kd;              // sum p_j (ln p_j - (z_j - m) / h)
-  double e1, eh;          // of the columns, sums of e^(z_j - m), e^((z_j - m) / h)
+  double e1, eh;          // of the columns, sums of e^(z_j - m), e^((z_j - m) / h) (distill_sums)
   int n;                  // columns
   bool bad;
 };
@@ -215,7 +216,7 @@ __device__ __forceinline__ DistillKept distill_kept(const DistillArgs& A, int64_
   for (int i = 0; i < kHash / 256; ++i) reinterpret_cast<uint4*>(sh.hash)[lane + 64 * i] = make_uint4(0, 0, 0, 0);
   int id[kPer];
   float t[kPer], zj[kPer];
-  bool out = false, used = false;
+  bool out = false;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int j = lane + 64 * i;
@@ -223,12 +224,8 @@ __device__ __forceinline__ DistillKept distill_kept(const DistillArgs& A, int64_
     out |= id[i] >= A.V;
     if (id[i] >= A.V) id[i] = -1;
     t[i] = id[i] >= 0 ? A.top[r * K + j] : -INFINITY;
-    out |= !(t[i] < INFINITY);   // a NaN or +inf of the teacher's
-    used |= id[i] >= 0;
     zj[i] = id[i] >= 0 ? io<T>::ld(z + id[i]) : -INFINITY;
   }
-  if (tail) out |= used && !(fabsf(A.teacher_lse[r]) < INFINITY);
-  o.bad = __ballot(out) != 0;
   bool dup = false;
   float tm = -INFINITY;
 #pragma unroll
@@ -268,6 +265,7 @@ __device__ __forceinline__ DistillKept distill_kept(const DistillArgs& A, int64_
   for (int i = 0; i < kPer; ++i) {
     p[i] = 0.0;
     if (64 * i >= K) continue;
+    out |= id[i] >= 0 && !(t[i] < INFINITY && (!tail || fabs(o.c) < INFINITY));   // not finite, of the teacher's
     const double l = (double)t[i] * ih - o.c;
     if (t[i] > -INFINITY) p[i] = exp(l);
     if (p[i] > 0.0) kd += p[i] * (l - ((double)zj[i] - o.m) * ih);
@@ -276,6 +274,7 @@ __device__ __forceinline__ DistillKept distill_kept(const DistillArgs& A, int64_
     sh.p[lane + 64 * i] = p[i];
     sh.zj[lane + 64 * i] = zj[i];
   }
+  o.bad = __ballot(out) != 0;
   o.mass = sum_f64(sp);
   o.kd = sum_f64(kd);
   if (__ballot(dup) != 0) {   // the first entry of a column takes the others' p
@@ -305,22 +304,28 @@ __device__ __forceinline__ DistillKept distill_kept(const DistillArgs& A, int64_
   o.rest = 0.0;
   o.n = 0;
   if (tail) {
-    double e1 = 0.0, eh = 0.0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      o.n += __popcll(__ballot(id[i] >= 0));
-      if (64 * i < K && id[i] >= 0) {
-        e1 += exp((double)zj[i] - o.m);
-        eh += exp(((double)zj[i] - o.m) * ih);
-      }
-    }
-    o.e1 = sum_f64(e1);
-    o.eh = sum_f64(eh);
+    for (int i = 0; i < kPer; ++i) o.n += __popcll(__ballot(id[i] >= 0));
     o.rest = o.n < A.V ? fmax(0.0, 1.0 - o.mass) : 0.0;   // no column is left: no rest
   } else {
     o.mass = o.c > -INFINITY ? 1.0 : 0.0;
   }
   return o;
+}
+
+// The sums over the kept columns, where they are beside a rest.
+__device__ __forceinline__ void distill_sums(DistillKept& o, const DistillShared& sh, int K, double ih) {
+  double e1 = 0.0, eh = 0.0;
+#pragma unroll
+  for (int i = 0; i < kMaxTop / 64; ++i) {
+    const int j = (int)(threadIdx.x & 63) + 64 * i;
+    if (64 * i < K && sh.id[j] >= 0) {
+      e1 += exp((double)sh.zj[j] - o.m);
+      eh += exp(((double)sh.zj[j] - o.m) * ih);
+    }
+  }
+  o.e1 = sum_f64(e1);
+  o.eh = sum_f64(eh);
 }
 
 }  // namespace
@@ -403,6 +408,7 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
   DistillKept kp;   // wave 0's
   if (w == 0) {
     kp = distill_kept<T>(A, r, z, sh, mark ? reinterpret_cast<uint32_t*>(bits) : nullptr, shift);
+    if (mark) distill_sums(kp, sh, K, A.ih);
     const bool aim = A.targets != nullptr && target >= 0 && target < V;
     if (A.targets != nullptr && !aim) kp.bad = true;
     if (lane == 0 && aim) sh.zt = io<T>::ld(z + target);
@@ -531,6 +537,7 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
       }
       rest.x = all.x = (double)m;
       double sh_ = ah, s1 = a1;
+      if (!kStats && tail) distill_sums(kp, sh, K, ih);
       if (tail && kp.n > 0) {   // and the kept columns', relative to the larger maximum
         const double x = none ? kp.m : kp.eh == 0.0 ? rest.x : fmax(rest.x, kp.m);
         const double e = exp(lane == 0 ? (rest.x - x) * ih : lane == 1 ? (kp.m - x) * ih : lane == 2 ? rest.x - x : kp.m - x);
@@ -544,6 +551,13 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
       all.s = of_lane(l, 1);
       one.x = all.x;
       one.s = two ? of_lane(l, 2) : all.s;
+      if constexpr (kGrad) {
+        const double s = lane == 0 ? all.s : lane == 1 ? rest.s : one.s;
+        const double f = exp(s < -700.0 ? 700.0 : -s);
+        all.f = of_lane(f, 0);
+        rest.f = of_lane(f, 1);
+        one.f = of_lane(f, 2);
+      }
       if constexpr (kStats) {
         double kd = kp.kd + (kp.mass > 0.0 ? kp.mass * ((all.x - kp.m) * ih + all.s) : 0.0);
         if (tail && kp.rest > 0.0)
@@ -570,30 +584,27 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
       const double m = kp.mass + kp.rest;
       // of every column: ea e^(z / h - l) + eb e^(z - one), l the rest's logsumexp where there is one
       const DistillLse l = tail ? rest : all;
-      const double e = exp(lane == 0 ? -all.s : lane == 1 ? -l.s : lane == 2 ? -one.s : lane == 3 ? (l.x - one.x) - one.s
-                                     : (rest.x - all.x) * ih + (rest.s - all.s));
-      // (without any value there is none to take f e^inf)
-      auto times = [&](double f, int i) { return f == 0.0 && of_lane(e, i) == INFINITY ? 0.0 : f * of_lane(e, i); };
+      const double e = exp(lane == 0 ? (rest.x - all.x) * ih + (rest.s - all.s) : (l.x - one.x) - one.s);
       double ea = a * m, eb = b;
       if (tail) {
         const bool any = rest.s != -INFINITY;   // a NaN is a value
-        ea = any ? a * (m * of_lane(e, 4) - kp.rest) : 0.0;
+        ea = any ? a * (m * of_lane(e, 0) - kp.rest) : 0.0;
         eb = any ? b : 0.0;   // none but -inf: no column takes them, and e^(l - one) may be infinite
       }
       DistillRow d;
       d.a = (float)a;
       d.t = (float)b;
       d.xh = (float)all.x;
-      d.q = (float)times(a * m, 0);
+      d.q = (float)(a * m * all.f);
       d.x1 = (float)one.x;
-      d.b = (float)times(b, 2);
+      d.b = (float)(b * one.f);
       d.x = (float)l.x;
-      d.A = (float)times(ea, 1);
-      d.B = (float)times(eb, 2);
+      d.A = (float)(ea * l.f);
+      d.B = (float)(eb * one.f);
       if (eb != 0.0 && (!two || square)) {   // one exponential for both
-        const double be = eb * of_lane(e, 3);
+        const double be = eb * of_lane(e, 1);
         d.B = two ? (float)be : 0.0f;
-        if (!two) d.A = (float)(times(ea, 1) + be);
+        if (!two) d.A = (float)(ea * l.f + be);
       }
       d.bad = kp.bad;
       if (kp.bad) d.A = NAN;
