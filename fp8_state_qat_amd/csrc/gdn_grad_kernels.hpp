@@ -691,23 +691,27 @@ __global__ __launch_bounds__(128 * CG, CG / 2) void grad_scan_kernel(GradArgs a,
 // (a lane: two channels of eight columns), so that nothing but the tokens' rows
 // passes through LDS, and 2 workgroups a compute unit cover each other's waits.
 //
-// beta's and the gates' gradients are sums of the same products: with
-// p_r = dO_r.o_r - Y_r.V_r and O and V by their formulas,
-//     db_r = Y_r.E_r / b_r           dg_t = <dS, S> - sum_(r<t) p_r
-//     p_r = e^G q_r.(dO S)_r + sum_s W_rs q_r.k_s
-//           - e^G k_r.(Y S)_r + sum_s N_rs k_r.k_s - Y_r.E_r
-//     <dS, S> = e^(G_C) <R, S> + sum_r e^G (q_r.(dO S)_r - k_r.(Y S)_r)
-// (S_t = a_t S_(t-1) + b_t e_t k_t^T leaves <dS_t, S_t> = <dS_(t+1), S_(t+1)> +
-// p_t), so that errors of dg are relative to the sums of its own chunk.  (beta = 0
-// goes as 2^-60: Y is a multiple of it.)  S, Y and E therefore have the planes of
-// the chains' products in these sums, and what dq and dk alone are made of (R, W,
-// N) too: with two planes, sixteen bits, these differed from the same sums in fp32
-// by 1e-4 in norm, in values next to a border of bf16, for 1.7% of the time.
+// beta's and the gates' gradients are sums of the same products: with the pairs
+// B_rs = W_rs q_r.k_s + N_rs k_r.k_s (s < r),
+//     db_r = Y_r.E_r / b_r
+//     dg_t = e^(G_C) <R, S> + sum_(r>=t) (own_r + sum_s B_rs - sum_u B_ur)
+//                           + sum_(s<t) b_s e^(G_C - G_s) k_s.(E R)_s
+//     own_r = e^G (q_r.(dO S)_r - k_r.(Y S)_r)
+// The sums over tokens and pairs are fp64, a pair the same fp32 number in its row
+// and in its column: what does not lie across token t cancels to 2^-53, and dg keeps
+// 20 bits and more also where a token forgets nearly all.  (By <dS, S> less the sum
+// of dO_r.o_r - Y_r.V_r over the earlier tokens, which needs no k.(E R), errors were
+// those of the whole chunk's sums, two to three times as large.)  beta = 0 goes as
+// 2^-60: Y is a multiple of it.  All operands have the planes of the chains'
+// products: with two planes, sixteen bits, of what dq and dk alone are made of (R,
+// W, N) these differed from sums in fp32 by 1e-4 in norm, in values next to a border
+// of bf16, for 1.7% of the time.
 //
-// Memory bounds it: 4 x 4096 tokens, 16 heads, 128 x 128 in bf16 take 294 us for
-// 1.05 GB read and 0.24 written (4.4 TB/s of the copy's 5.0), at 1.85 GHz.  (Before,
-// each chunk's E and Y were formed again here by sixteen waves and all of S, R, E, Y
-// went through LDS: 555 us, most of it in one workgroup a compute unit's waits.)
+// Memory bounds it: 4 x 4096 tokens, 16 heads, 128 x 128 in bf16 take 305 us for
+// 1.05 GB read and 0.24 written (4.2 TB/s of the copy's 5.0), at 1.85 GHz, matrix
+// units busy a third of the time.  (Before, each chunk's E and Y were formed again
+// here by sixteen waves and all of S, R, E, Y went through LDS: 555 us, most of it
+// in one workgroup a compute unit's waits.)
 // ---------------------------------------------------------------------------
 template <class Eng, int DK>
 struct GradChunkLds {
@@ -721,14 +725,16 @@ struct GradChunkLds {
   static constexpr int oYE = oG + (int)sizeof(GradGates);   // [4][64] Y.E
   static constexpr int oQS = oYE + 4 * kChunk * 4;          // [4][64] q.(dO S)
   static constexpr int oKS = oQS + 4 * kChunk * 4;          // [4][64] k.(Y S)
-  static constexpr int oT = oKS + 4 * kChunk * 4;           // [10][16] the pairs' part of p
-  static constexpr int oZ = oT + 10 * 16 * 4;               // [4] <R, S>
+  static constexpr int oKR = oKS + 4 * kChunk * 4;          // [4][64] k.(E R)
+  static constexpr int oT = oKR + 4 * kChunk * 4;           // [64] the pairs' rows less their columns, fp64
+  static constexpr int oZ = oT + kChunk * 8;                // [4] <R, S>
   static constexpr int oO = oZ + 4 * 8;                     // dO, twice, then planes of Y and of E, [column][token]
   static constexpr int oY = oO + 2 * kStep;
   static constexpr int oE = oY + P * kStep;
   static constexpr int oW = oO;                             // last W and N
   static constexpr int oN = oW + P * GradRec<Eng>::kPlane;
-  static constexpr int end1 = oE + P * kStep, end2 = oN + P * GradRec<Eng>::kPlane;
+  static constexpr int oB = oN + P * GradRec<Eng>::kPlane;  // and the pairs' parts of the log-gates' gradients
+  static constexpr int end1 = oE + P * kStep, end2 = oB + 10 * 256 * 4;
   static constexpr int bytes = end1 > end2 ? end1 : end2;
   static_assert(bytes <= 160 * 1024 && oO % 16 == 0, "LDS budget, 16-byte aligned");
 };
@@ -970,7 +976,9 @@ __global__ __launch_bounds__(kThreads, Eng::kSplit ? 2 : 1) void grad_chunk_kern
   float* sYE = reinterpret_cast<float*>(smem + Ls::oYE);
   float* sQS = reinterpret_cast<float*>(smem + Ls::oQS);
   float* sKS = reinterpret_cast<float*>(smem + Ls::oKS);
-  float* sT = reinterpret_cast<float*>(smem + Ls::oT);
+  float* sKR = reinterpret_cast<float*>(smem + Ls::oKR);
+  double* sT = reinterpret_cast<double*>(smem + Ls::oT);
+  float* sB = reinterpret_cast<float*>(smem + Ls::oB);
   double* sZ = reinterpret_cast<double*>(smem + Ls::oZ);
 #pragma unroll
   for (int k = 0; k < 4; ++k) dots[k] = over_quads(dots[k]);
@@ -980,7 +988,7 @@ __global__ __launch_bounds__(kThreads, Eng::kSplit ? 2 : 1) void grad_chunk_kern
 #pragma unroll
   for (int t = 0; t < TPW; ++t) {
     const int tok = 16 * (TPW * tg + t) + ln;
-    float q8[8], k8[8], dq = 0.0f, dk = 0.0f;
+    float q8[8], k8[8], dq = 0.0f, dk = 0.0f, dr = 0.0f;
     frag_values(TK::template row8<Eng>(sQ, tok, 32 * wc + 8 * gq), q8);
     frag_values(TK::template row8<Eng>(sK, tok, 32 * wc + 8 * gq), k8);
 #pragma unroll
@@ -989,12 +997,15 @@ __global__ __launch_bounds__(kThreads, Eng::kSplit ? 2 : 1) void grad_chunk_kern
       for (int m = 0; m < 2; ++m) {
         dq = fmaf(q8[2 * i + m], aq[t][m][i], dq);
         dk = fmaf(k8[2 * i + m], ax[t][m][i], dk);
+        dr = fmaf(k8[2 * i + m], as[t][m][i], dr);
       }
     dq = over_quads(dq);
     dk = over_quads(dk);
+    dr = over_quads(dr);
     if (gq == 0) {
       sQS[kChunk * wc + tok] = dq;
       sKS[kChunk * wc + tok] = dk;
+      sKR[kChunk * wc + tok] = dr;
     }
     // channels in the order of the products with K and Q
     const float eg = g.eg[tok], bl = g.beta[tok] * g.el[tok];
@@ -1025,36 +1036,57 @@ __global__ __launch_bounds__(kThreads, Eng::kSplit ? 2 : 1) void grad_chunk_kern
     }
     const int t = 16 * Tt + ln, tn = g.n[t];
     const float tf = g.f[t];
-    float wv[4], nn[4], p = 0.0f;
+    float wv[4], nn[4], b[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int s = 16 * St + 4 * gq + k;
       const float d = s <= t && t < nv ? g.beta[s] * lin_pow(tn - g.n[s], tf - g.f[s]) : 0.0f;
       wv[k] = d * pe[i][k];
       nn[k] = s < t ? -d * ye[i][k] : 0.0f;
-      p = fmaf(wv[k], cq[k], fmaf(nn[k], ck[k], p));
+      b[k] = s < t ? fmaf(wv[k], cq[k], nn[k] * ck[k]) : 0.0f;
     }
-    p = over_quads(p);
-    if (gq == 0) sT[16 * (w + 4 * i) + ln] = p;
+    *reinterpret_cast<float4*>(sB + 256 * (w + 4 * i) + 16 * ln + 4 * gq) = make_float4(b[0], b[1], b[2], b[3]);
     const int at = tri_block(Tt, St) * Rec::kBlock + tri_at<Eng>(ln, 4 * gq) * (int)sizeof(E);
     put4<Eng, P>(smem + Ls::oW + at, Rec::kPlane, wv);
     put4<Eng, P>(smem + Ls::oN + at, Rec::kPlane, nn);
   }
   barrier_lds();
+  {   // rows less columns of the pairs' parts, four lanes a token of this wave's sixteen
+    const int tk = l64 >> 2, part = l64 & 3;
+    double own = 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i <= w) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(sB + 256 * tri_block(w, i) + 16 * tk + 4 * part);
+        own += ((double)x[0] + (double)x[1]) + ((double)x[2] + (double)x[3]);
+      }
+      if (i >= w) {
+        const float* x = sB + 256 * tri_block(i, w) + 64 * part + tk;
+        own -= ((double)x[0] + (double)x[16]) + ((double)x[32] + (double)x[48]);
+      }
+    }
+    own = dpp_add_f64<0xB1, 0xF>(own);   // lanes 1 0 3 2
+    own = dpp_add_f64<0x4E, 0xF>(own);   // lanes 2 3 0 1
+    if (part == 0) sT[16 * w + tk] = own;
+  }
+  barrier_lds();
 
   if (w == 3) {
-    const int t = l64, Tt = t >> 4;
-    double ye_ = 0.0, e = 0.0, zz = 0.0, p = 0.0;
+    const int t = l64;
+    double ye_ = 0.0, own = 0.0, out = 0.0, zz = 0.0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       ye_ += (double)sYE[kChunk * i + t];
       zz += sZ[i];
-      if (i < CP) e += (double)sQS[kChunk * i + t] - (double)sKS[kChunk * i + t];
-      if (i <= Tt) p += (double)sT[16 * tri_block(Tt, i) + (t & 15)];
+      if (i < CP) {
+        own += (double)sQS[kChunk * i + t] - (double)sKS[kChunk * i + t];
+        out += (double)sKR[kChunk * i + t];
+      }
     }
-    e *= (double)g.eg[t];
-    p += e - ye_;
-    double d = (double)g.ec[0] * zz + last_lane(wave_prefix_f64(e)) - (wave_prefix_f64(p) - p);
+    own = fma(own, (double)g.eg[t], sT[t]);
+    out *= (double)g.beta[t] * (double)g.el[t];
+    const double later = wave_prefix_f64(own);
+    double d = (double)g.ec[0] * zz + (last_lane(later) - later + own) + (wave_prefix_f64(out) - out);
     if (g.g[t] < -103.97208f) d = 0.0;   // e^g rounds to 0 (below 2^-150): nothing lies across the token
     if (t < nv) {
       a.d_beta[row0 + (int64_t)t * H] = (float)(ye_ / (double)g.beta[t]);

@@ -388,7 +388,7 @@ size_t gdn_chunk_bwd_workspace_bytes(const gdn_shape_t* shape);
  *
  * The states, their gradients and every output before its rounding take terms of
  * 24 significant bits; d_beta and dg are sums of terms that can cancel, off by about
- * 2^-19 of the sum of their terms' magnitudes in the chunk at most.
+ * 2^-19 of their terms' magnitudes at most (dg_t: of what lies across token t).
  */
 gdn_status_t gdn_chunk_grad(const gdn_shape_t* shape,
                             const void* q, const void* k, const void* v,

@@ -106,3 +106,27 @@ def test_dg_is_0_where_a_decay_is_0_in_fp32(dk, dtype):
     got = run(d)[4]
     assert (got[[7, 70, 71, 100]] == 0).all(), got[[7, 70, 71, 100]]
     assert (got[[6, 8, 69, 72]] != 0).all()
+
+
+# Every term across a token that keeps e^-20 of the state has that factor; it is off by 2^-20 of itself at most (three
+# operands of 24 bits, sums in fp32 of at most 128 terms of random signs, decays to a few 2^-24), and what is not across
+# the token cancels in 64 bits: of a chunk's sums of at most 2^7, 2^-46, against e^-20 = 2^-28.9: 2^-17.  Held to 2^-15.
+@pytest.mark.parametrize("dk,dtype,given", [(64, BF, False), (128, BF, True), (64, F32, True), (128, F32, False)])
+def test_dg_of_tokens_that_forget_nearly_all(dk, dtype, given):
+    d = make([200, 64], 2, dk, 64, dtype, seed=41)
+    at = [0, 5, 70, 127, 128, 199, 220]
+    d["g"][at] = -20.0
+    states = torch.randn(sum(n_bounds(d)), 2, 64, dk, generator=torch.Generator().manual_seed(42)) if given else None
+    got, wanted = run(d, None if states is None else states.cuda())[4].cpu().double(), want(d, states)[4]
+    err = (got - wanted)[at].norm() / wanted[at].norm()
+    assert err < 2.0 ** -15, (float(err), got[at], wanted[at])
+
+
+# In norm: a rounding is off by 2^-24 / sqrt(3) in the mean of squares, at a mean mantissa of 1.4 by 2^-25.3; a sum of n
+# terms of random signs rounds partial sums of n / 2 of them in the mean; dg is made of three products of 64 tokens and
+# 128 channels (S, R, and theirs), its own sums are fp64: sqrt(3 * 96) 2^-25.3 = 2^-21.2.
+@pytest.mark.parametrize("seg,dk,dv,dtype", [([632], 64, 64, F32), ([700], 64, 128, BF), ([300, 333], 128, 64, BF)])
+def test_dg_is_as_exact_as_its_terms(seg, dk, dv, dtype):
+    d = make(seg, 4, dk, dv, dtype, init=False, fin=False, seed=43)
+    err = (run(d)[4].cpu().double() - want(d)[4]).norm() / want(d)[4].norm()
+    assert err < 2.0 ** -21, float(err)
