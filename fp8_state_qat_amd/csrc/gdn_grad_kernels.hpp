@@ -867,7 +867,6 @@ __global__ __launch_bounds__(kThreads, Eng::kSplit ? 2 : 1) void grad_chunk_kern
 #pragma unroll
       for (int i = 0; i < 8; ++i) sx[i] = f32x2{0.0f, 0.0f};
     }
-    float zs = 0.0f;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -877,10 +876,9 @@ __global__ __launch_bounds__(kThreads, Eng::kSplit ? 2 : 1) void grad_chunk_kern
     for (int m = 0; m < 2; ++m) {
       const float x8[8] = {sx[0][m], sx[1][m], sx[2][m], sx[3][m], sx[4][m], sx[5][m], sx[6][m], sx[7][m]};
       split_planes<Eng, P>(x8, sf[m]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) zs = fmaf(sx[i][m], rx[i][m], zs);
     }
-    z += (double)zs;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z += (double)fmaf(sx[i][1], rx[i][1], sx[i][0] * rx[i][0]);
     // dO, and first K, Q and the gates; R's eight loads came last
     wait_vmem_but<8>();
     barrier_lds();
