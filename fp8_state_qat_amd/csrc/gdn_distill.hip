@@ -481,7 +481,9 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
     }
   } else {
     const float* s = A.stats + 4 * r;
-    again = fabsf(s[1]) > kFar || (A.targets != nullptr && fabsf(s[0]) > kFar) || (tail && fabsf(s[3]) > kFar);
+    const bool none = s[3] == -INFINITY && A.h >= 1.0f;   // of the rest (h < 1: or a logsumexp below fp32's)
+    again = fabsf(s[1]) > kFar || (A.targets != nullptr && fabsf(s[0]) > kFar) ||
+            (tail && !none && fabsf(s[3]) > kFar);
     if (again) {
       __syncthreads();   // the table of the kept columns
       auto kept = [&](int i) {
@@ -577,6 +579,7 @@ __global__ __launch_bounds__(TPB) void distill_kernel(DistillArgs A) {
       one.read(A.stats[4 * r], 1.0, 1.0);
       all.read(A.stats[4 * r + 1], (double)A.h, ih);
       rest.read(A.stats[4 * r + 3], (double)A.h, ih);
+      if (A.stats[4 * r + 3] == -INFINITY) rest = DistillLse{0.0, -INFINITY, 1.0};   // no value of the rest
     }
     if constexpr (kGrad) {
       const double wt = A.d_loss ? (double)A.d_loss[r] : 1.0;
