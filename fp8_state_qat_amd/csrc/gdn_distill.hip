@@ -244,16 +244,19 @@ __device__ __forceinline__ DistillKept distill_kept(const DistillArgs& A, int64_
       atomicOr(bits + (b >> 5), 1u << (b & 31));
     }
   }
+  double m = 0.0;   // ln p_j = (t_j - m) / h - le (in one number c next to t / h of 1e12 nothing is left of le)
+  double le;
   if (tail) {
-    o.c = (double)A.teacher_lse[r];
+    o.c = le = (double)A.teacher_lse[r];
   } else {
-    const double m = (double)wave_max_dpp(tm);
+    m = (double)wave_max_dpp(tm);
     double e = 0.0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (64 * i < K && t[i] > -INFINITY) e += exp(((double)t[i] - m) * ih);
     e = sum_f64(e);
-    o.c = e > 0.0 ? m * ih + log(e) : -INFINITY;
+    le = log(e);
+    o.c = e > 0.0 ? m * ih + le : -INFINITY;
   }
   float zm = -INFINITY;
 #pragma unroll
@@ -266,7 +269,7 @@ __device__ __forceinline__ DistillKept distill_kept(const DistillArgs& A, int64_
     p[i] = 0.0;
     if (64 * i >= K) continue;
     out |= id[i] >= 0 && !(t[i] < INFINITY && (!tail || fabs(o.c) < INFINITY));   // not finite, of the teacher's
-    const double l = (double)t[i] * ih - o.c;
+    const double l = ((double)t[i] - m) * ih - le;
     if (t[i] > -INFINITY) p[i] = exp(l);
     if (p[i] > 0.0) kd += p[i] * (l - ((double)zj[i] - o.m) * ih);
     sp += p[i];

@@ -327,3 +327,19 @@ def test_more_rows_than_a_launch_has():
     want = -torch.log_softmax(z[::4096].double(), 1)
     want = want.gather(1, ids[::4096].long()) + 0.5 * want.gather(1, targets[::4096, None])
     assert ((loss[::4096, None].double() - want).abs() <= 2.0 ** -14 + 2.0 ** -23 * want.abs()).all()
+
+
+# ---------------------------------------------------------------- the ends of the temperature
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("tail,h", [(False, 1e-29), (False, 1e-12), (False, 1e-3), (False, 1e3), (False, 1e12),
+                                    (False, 9e29), (True, 1e-3), (True, 1e3), (True, 1e12), (True, 9e29)])
+def test_cold_and_hot(dtype, tail, h):
+    """From one-hot distributions to uniform ones.  (Not a given logsumexp of cold ones: it is fp32, and at 1e12 half a
+    step of it is 2^15, so that the p that it stands for are e^(2^15).)"""
+    z = torch.randn(4, 700, generator=torch.Generator().manual_seed(9))
+    d = make(z, random_ids(4, 700, 3), dtype, tail, h=h)
+    d["top"] = d["top"] + torch.tensor([0.0, 5.0, -3.0])
+    if tail:   # the logsumexp of the kept, which have nearly all of the mass
+        d["lse"] = (torch.logsumexp(d["top"].double() / float(torch.tensor(h)), 1) + 2.0 ** -6).float()
+        d["lse"] = torch.maximum(d["lse"], (d["top"].amax(1).double() / float(torch.tensor(h))).float())
+    check(d)
