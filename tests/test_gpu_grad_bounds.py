@@ -130,3 +130,26 @@ def test_dg_is_as_exact_as_its_terms(seg, dk, dv, dtype):
     d = make(seg, 4, dk, dv, dtype, init=False, fin=False, seed=43)
     err = (run(d)[4].cpu().double() - want(d)[4]).norm() / want(d)[4].norm()
     assert err < 2.0 ** -21, float(err)
+
+
+@pytest.mark.parametrize("dk,dtype,given", [(64, BF, False), (128, BF, True), (64, F32, True), (128, F32, False)])
+def test_resets(dk, dtype, given):
+    """Log-gates of -inf: alone, at a chunk's first and last token, several in a row, at a sequence's first."""
+    d = make([200, 70], 2, dk, 64, dtype, seed=44)
+    at = [0, 7, 63, 64, 100, 101, 102, 199, 200]
+    d["g"][at] = -float("inf")
+    d["g"][150, 0] = -float("inf")
+    states = torch.randn(sum(n_bounds(d)), 2, 64, dk, generator=torch.Generator().manual_seed(45)) if given else None
+    got, wanted = run(d, None if states is None else states.cuda()), want(d, states)
+    close(got, wanted, bounds(d, states), dtype)
+    assert (got[4][at] == 0).all() and got[4][150, 0] == 0
+    assert (got[5][:, :] == 0).all()     # nothing reaches the initial states
+
+
+def test_thousands_of_short_sequences():
+    """Sequences of 0 to 3 tokens, more than one scan's workgroup counts at a time."""
+    gen = torch.Generator().manual_seed(46)
+    seg = torch.randint(0, 4, (3000,), generator=gen).tolist()
+    d = make(seg, 1, 64, 64, BF, seed=47)
+    got, wanted = run(d), want(d)
+    close(got, wanted, bounds(d), BF)
