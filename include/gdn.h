@@ -362,7 +362,9 @@ size_t gdn_chunk_bwd_workspace_bytes(const gdn_shape_t* shape);
  *              gate_per_channel 0, gate_grid_log2 0.  qdq_flags are those of the
  *              forward (GDN_QDQ_WRITE changes no gradient: it touches the last
  *              state only); GDN_QDQ_W and GDN_QDQ_INT8 are refused.
- *   q, k, v, beta, g, cu_seqlens, seq_lens, initial_state   the forward's
+ *   q, k, v, beta, g, cu_seqlens, seq_lens, initial_state   the forward's; g may be
+ *              -inf (the token forgets everything) but where the forward's own code
+ *              runs again (below), which takes finite gates: -1e5 forgets as much
  *   states     the states after every chunk, after their QDQ, as the forward's
  *              debug->bound_post has them ([n_bounds, H, dv, dk] fp32, chunk i of
  *              sequence n at b = sum_{m<n} ceil(L_m / 64) + i); the last one of a
